@@ -11,6 +11,8 @@ fallback: if the shared library is missing, every call raises.
     gemm_bf16_f32acc_epilogue(...)                    the same with bf16 A and B
     gemm_tc(A, B, C, ...)                             the same for fp16/bf16 A, B and fp32/fp16/bf16 C
     gemm_tc_batched(A, B, C, ..., b_trans=False)      a strided batch of those (3-D tensors), op(B) = B or B^T
+    fp8_quantize(X, Q, S, layout="rows")              X held in 8 bits with an FP32 scale for each block of 128
+    gemm_fp8(A, SA, B, SB, C, ..., b_trans=True)      the product of two matrices held that way
 
 Tensors are torch CUDA tensors on the current device; A and B may be 2-D
 views with a leading dimension larger than their width (unit column stride).
@@ -38,6 +40,11 @@ GEMM_ACT_GELU_TANH = 3
 GEMM_DTYPE_F32 = 0
 GEMM_DTYPE_F16 = 1
 GEMM_DTYPE_BF16 = 2
+GEMM_DTYPE_E4M3 = 3
+GEMM_DTYPE_E5M2 = 4
+GEMM_FP8_ROWS = 0
+GEMM_FP8_COLS = 1
+GEMM_FP8_BLOCKS = 2
 GEMM_PATH_F32 = 0
 GEMM_PATH_TC = 1
 
@@ -52,6 +59,7 @@ class TuneEntry(ctypes.Structure):
 
 EXPORTED_SYMBOLS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_f16_f32acc_epilogue", "gemm_bf16_f32acc_epilogue",
                     "gemm_tc_f32acc_epilogue", "gemm_tc_strided_batched", "gemm_f16_f32acc_epilogue_noalloc",
+                    "gemm_fp8_quantize_block128", "gemm_fp8_block128",
                     "gemm_tune_set", "gemm_tune_get",
                     "gemm_status_string", "gemm_last_cuda_error", "gemm_check", "gemm_watchdog_selftest",
                     "gemm_last_plan", "gemm_last_launch_count", "gemm_tc_rate_probe",
@@ -109,6 +117,13 @@ def lib():
                                                   c_int, c_void_p]
             L.gemm_f16_f32acc_epilogue_noalloc.restype = c_int
             L.gemm_f16_f32acc_epilogue_noalloc.argtypes = L.gemm_f16_f32acc_epilogue.argtypes
+            L.gemm_fp8_quantize_block128.restype = c_int
+            L.gemm_fp8_quantize_block128.argtypes = [c_int, c_int, c_void_p, c_int, c_ll, c_void_p, c_int, c_ll,
+                                                     c_void_p, c_ll, c_int, c_void_p]
+            L.gemm_fp8_block128.restype = c_int
+            L.gemm_fp8_block128.argtypes = [c_int, c_int, c_int, c_float, c_void_p, c_int, c_ll, c_void_p, c_ll,
+                                            c_void_p, c_int, c_ll, c_void_p, c_ll, c_int, c_int, c_float, c_void_p,
+                                            c_int, c_ll, c_void_p, c_int, c_void_p]
             L.gemm_tune_set.restype = c_int
             L.gemm_tune_set.argtypes = [ctypes.POINTER(TuneEntry), c_int]
             L.gemm_tune_get.restype = c_int
@@ -388,6 +403,117 @@ def gemm_tc_batched(A, B, C, alpha: float = 1.0, beta: float = 0.0, bias=None, a
                                        ctypes.c_void_p(bias_ptr or None), int(act), _stream_handle(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_tc_strided_batched")
+
+
+_FP8_LAYOUTS = {"rows": GEMM_FP8_ROWS, "cols": GEMM_FP8_COLS, "blocks": GEMM_FP8_BLOCKS}
+_types_cache = None
+
+
+def _type_codes():
+    """torch dtype -> gemm_dtype code."""
+    global _types_cache
+    if _types_cache is None:
+        import torch
+        _types_cache = {torch.float32: GEMM_DTYPE_F32, torch.float16: GEMM_DTYPE_F16, torch.bfloat16: GEMM_DTYPE_BF16,
+                        torch.float8_e4m3fn: GEMM_DTYPE_E4M3, torch.float8_e5m2: GEMM_DTYPE_E5M2}
+    return _types_cache
+
+
+def _typed_mat(t, name, codes):
+    """(pointer, row stride, type code) of a 2-D CUDA tensor of one of the types `codes`."""
+    code = _type_codes().get(getattr(t, "dtype", None), -1)
+    if code not in codes:
+        raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in codes)}")
+    ptr, ld = _mat(t, name, t.dtype)
+    return ptr, ld, code
+
+
+_TYPE_NAMES = ("float32", "float16", "bfloat16", "float8_e4m3fn", "float8_e5m2")
+_FLOATS = (GEMM_DTYPE_F32, GEMM_DTYPE_F16, GEMM_DTYPE_BF16)
+_FP8S = (GEMM_DTYPE_E4M3, GEMM_DTYPE_E5M2)
+
+
+def _fp8_shapes(rows, cols, layout):
+    """Shapes of Q and S of a rows x cols matrix."""
+    if layout not in _FP8_LAYOUTS:
+        raise ValueError(f"layout must be one of {tuple(_FP8_LAYOUTS)}, got {layout!r}")
+    if layout == "rows":
+        return (rows, cols), (-(-cols // 128), rows)
+    if layout == "cols":
+        return (cols, rows), (-(-rows // 128), cols)
+    return (rows, cols), (-(-rows // 128), -(-cols // 128))
+
+
+def fp8_empty(rows: int, cols: int, layout: str = "rows", dtype=None, device="cuda"):
+    """Uninitialised (Q, S) for fp8_quantize of a rows x cols matrix, with row
+    strides that gemm_fp8 takes (Q: a multiple of 16, S: a multiple of 4)."""
+    import torch
+    dtype = torch.float8_e4m3fn if dtype is None else dtype
+    (qr, qc), (sr, sc) = _fp8_shapes(rows, cols, layout)
+    Q = torch.empty(qr, (qc + 15) // 16 * 16, dtype=dtype, device=device)[:, :qc]
+    S = torch.empty(sr, (sc + 3) // 4 * 4, dtype=torch.float32, device=device)[:, :sc]
+    return Q, S
+
+
+def fp8_quantize(X, Q, S, layout: str = "rows", *, stream=None) -> None:
+    """X (rows x cols; fp32, fp16 or bf16) to 8 bits with one FP32 scale for each block of 128.
+
+    layout "rows":   blocks of 128 along a row; Q is rows x cols, S is (ceil(cols/128), rows).
+    layout "cols":   blocks of 128 along a column; Q is the transpose, cols x rows, S is (ceil(rows/128), cols).
+    layout "blocks": blocks of 128 x 128; Q is rows x cols, S is (ceil(rows/128), ceil(cols/128)).
+    Q is float8_e4m3fn or float8_e5m2.  fp8_empty() makes a fitting pair.
+    """
+    x_ptr, ldx, x_type = _typed_mat(X, "X", _FLOATS)
+    q_ptr, ldq, q_type = _typed_mat(Q, "Q", _FP8S)
+    s_ptr, lds, _ = _typed_mat(S, "S", (GEMM_DTYPE_F32,))
+    rows, cols = X.shape
+    q_shape, s_shape = _fp8_shapes(rows, cols, layout)
+    if Q.shape != q_shape or S.shape != s_shape:
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} Q{tuple(Q.shape)} S{tuple(S.shape)} for layout {layout!r}")
+    st = lib().gemm_fp8_quantize_block128(rows, cols, x_ptr, x_type, ldx, q_ptr, q_type, ldq, s_ptr, lds,
+                                          _FP8_LAYOUTS[layout], _stream_handle(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp8_quantize_block128")
+
+
+def gemm_fp8(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=None, act: int = 0, *,
+             b_trans: bool = True, b_scales: str = "blocks", stream=None) -> None:
+    """C = act(alpha * A @ op(B) + beta * C + bias) of matrices held in 8 bits (see fp8_quantize).
+
+    A: (M, K) with SA in layout "rows".  C: (M, N) fp32, fp16 or bf16; bias: fp32 or None.
+    b_trans=True:  B is (N, K), op(B) = B^T, with scales in layout b_scales, "blocks" or "rows".
+    b_trans=False: B is (K, N), op(B) = B, with scales in layout "blocks".
+    So y = x W^T takes x in "rows" and W in "blocks"; dx = dy W takes dy in "rows" and the same
+    W with b_trans=False; dW = dy^T x takes both quantized with layout "cols" and b_scales="rows".
+    """
+    a_ptr, lda, a_type = _typed_mat(A, "A", _FP8S)
+    b_ptr, ldb, b_type = _typed_mat(B, "B", _FP8S)
+    c_ptr, ldc, c_type = _typed_mat(C, "C", _FLOATS)
+    sa_ptr, ldsa, _ = _typed_mat(SA, "SA", (GEMM_DTYPE_F32,))
+    sb_ptr, ldsb, _ = _typed_mat(SB, "SB", (GEMM_DTYPE_F32,))
+    M, K = A.shape
+    N, K2 = B.shape if b_trans else B.shape[::-1]
+    if K2 != K or C.shape != (M, N):
+        raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    if b_scales != "blocks" and (b_scales != "rows" or not b_trans):
+        raise ValueError(f"b_scales must be 'blocks', or 'rows' with b_trans=True, got {b_scales!r}")
+    if SA.shape != _fp8_shapes(M, K, "rows")[1] or SB.shape != _fp8_shapes(*B.shape, b_scales)[1]:
+        raise ValueError(f"scales do not fit: SA{tuple(SA.shape)} SB{tuple(SB.shape)} for A{tuple(A.shape)} B{tuple(B.shape)}")
+    bias_ptr = None
+    if bias is not None:
+        bias_ptr = _vector(bias, "bias", N)
+    st = lib().gemm_fp8_block128(M, N, K, alpha, a_ptr, a_type, lda, sa_ptr, ldsa, b_ptr, b_type, ldb, sb_ptr, ldsb,
+                                 1 if b_trans else 0, _FP8_LAYOUTS[b_scales], beta, c_ptr, c_type, ldc, bias_ptr, act,
+                                 _stream_handle(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp8_block128")
+
+
+def _vector(t, name, n):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA float32 tensor of length {n}")
+    return t.data_ptr()
 
 
 def tune_set(entries) -> None:

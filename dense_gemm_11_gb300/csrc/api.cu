@@ -1,6 +1,7 @@
 // api.cu -- the C ABI of libgemm11.so: argument checks, degenerate shapes,
 // dispatch to the FP32 / FP16 paths, status codes, the per-(device, stream)
 // split-K scratch and the device watchdog word.
+#include <algorithm>
 #include <atomic>
 #include <cstdint>
 #include <cstdio>
@@ -10,6 +11,7 @@
 #include <utility>
 
 #include "../../include/gemm11.h"
+#include "fp8.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -414,6 +416,14 @@ int gemm_f32_3xtf32(int M, int N, int K, float alpha, const float *A, int lda, c
 namespace {
 
 bool valid_act(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_GELU_TANH; }
+bool valid_fp8(int type) { return type == GEMM_DTYPE_E4M3 || type == GEMM_DTYPE_E5M2; }
+
+// A call with an empty result.
+int noop() {
+    t_last_plan = "noop_empty";
+    t_last_launches = 0;
+    return GEMM_OK;
+}
 
 // The tensor-core entry points (FP16 or BF16 operands, FP32 accumulate,
 // FP32/FP16/BF16 output, fused epilogue, optional strided batch and
@@ -547,6 +557,96 @@ int gemm_f16_f32acc_epilogue_noalloc(int M, int N, int K, float alpha, const voi
         if (e == cudaSuccess && reject == 1) return GEMM_ERR_UNSUPPORTED;
         if (e == cudaSuccess && reject == 2) return GEMM_ERR_SCRATCH_LIMIT;
     }
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int x_type, long long ldx, void *Q, int q_type,
+                               long long ldq, float *S, long long lds, int layout, void *stream) {
+    if (rows < 0 || cols < 0 || layout < GEMM_FP8_ROWS || layout > GEMM_FP8_BLOCKS) return GEMM_ERR_INVALID_ARG;
+    if (x_type != GEMM_DTYPE_F32 && x_type != GEMM_DTYPE_F16 && x_type != GEMM_DTYPE_BF16) return GEMM_ERR_INVALID_ARG;
+    if (!valid_fp8(q_type)) return GEMM_ERR_INVALID_ARG;
+    const long long q_cols = layout == GEMM_FP8_COLS ? rows : cols;
+    const long long s_cols = layout == GEMM_FP8_ROWS ? rows : layout == GEMM_FP8_COLS ? cols : (cols + 127LL) / 128;
+    if (ldx < std::max(1, cols) || ldq < std::max(1LL, q_cols) || lds < std::max(1LL, s_cols)) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return noop();
+    if (!X || !Q || !S) return GEMM_ERR_INVALID_ARG;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    Fp8Quant q;
+    q.rows = rows;
+    q.cols = cols;
+    q.X = X;
+    q.x_type = x_type;
+    q.ldx = ldx;
+    q.Q = Q;
+    q.q_type = q_type;
+    q.ldq = ldq;
+    q.S = S;
+    q.lds = lds;
+    q.layout = layout;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_fp8_quantize(q, s, &info);
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_type, long long lda, const float *SA,
+                      long long ldsa, const void *B, int b_type, long long ldb, const float *SB, long long ldsb,
+                      int b_trans, int b_layout, float beta, void *C, int c_type, long long ldc, const float *bias,
+                      int act, void *stream) {
+    if (M < 0 || N < 0 || K < 0 || !valid_act(act) || !valid_fp8(a_type) || !valid_fp8(b_type)) return GEMM_ERR_INVALID_ARG;
+    if (c_type != GEMM_DTYPE_F32 && c_type != GEMM_DTYPE_F16 && c_type != GEMM_DTYPE_BF16) return GEMM_ERR_INVALID_ARG;
+    if (b_trans != 0 && b_trans != 1) return GEMM_ERR_INVALID_ARG;
+    if (b_layout != GEMM_FP8_BLOCKS && !(b_layout == GEMM_FP8_ROWS && b_trans)) return GEMM_ERR_INVALID_ARG;
+    const long long kb = (K + 127LL) / 128, nb = (N + 127LL) / 128;
+    const bool b_rows = b_layout == GEMM_FP8_ROWS;
+    if (lda < std::max(1, K) || ldb < std::max(1, b_trans ? K : N) || ldc < std::max(1, N) || ldsa < std::max(1, M) ||
+        ldsb < std::max<long long>(1, b_rows ? N : b_trans ? kb : nb))
+        return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return noop();
+    if (!C) return GEMM_ERR_INVALID_ARG;
+    const bool product = K > 0 && alpha != 0.f;
+    if (product) {
+        if (!A || !SA || !B || !SB) return GEMM_ERR_INVALID_ARG;
+        auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+        const bool ok = al16(A) && al16(B) && al16(SA) && (M == 1 || lda % 16 == 0) &&
+                        ((b_trans ? N : K) == 1 || ldb % 16 == 0) && (kb == 1 || ldsa % 4 == 0) &&
+                        (!b_rows || (al16(SB) && (kb == 1 || ldsb % 4 == 0)));
+        if (!ok) return GEMM_ERR_UNSUPPORTED;
+    }
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    Fp8Gemm g;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.alpha = alpha;
+    g.A = A;
+    g.a_type = a_type;
+    g.lda = lda;
+    g.SA = SA;
+    g.ldsa = ldsa;
+    g.B = B;
+    g.b_type = b_type;
+    g.ldb = ldb;
+    g.SB = SB;
+    g.ldsb = ldsb;
+    g.b_trans = b_trans;
+    g.b_rows = b_rows;
+    g.beta = beta;
+    g.C = C;
+    g.c_type = c_type;
+    g.ldc = ldc;
+    g.bias = bias;
+    g.act = act;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = product ? run_fp8_gemm(g, s, &info) : run_fp8_scale_c(g, s, &info);
+    if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return fail_cuda(e);
     return finish_call(info, s);
 }

@@ -1,0 +1,69 @@
+// fp8.cuh -- device helpers of the 8-bit block-scaled product: the
+// tcgen05.mma of kind::f8f6f4 (e4m3 / e5m2 operands, FP32 accumulator).
+#pragma once
+
+#include "ptx.cuh"
+
+namespace gemm11 {
+
+// D(tmem) (+)= A(smem desc) x B(smem desc), 8-bit operands, K = 32 per
+// instruction (32 bytes of each K-major row).
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The pair form: issued by one thread of the even CTA, as umma_f16_pair.
+__device__ __forceinline__ void umma_f8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4: operand formats E4M3 = 0, E5M2 = 1
+// (they may differ), FP32 accumulator, a_mn / b_mn = operand stored MN-major.
+constexpr uint32_t umma_idesc_f8(int M, int N, int a_e5m2, int b_e5m2, int a_mn, int b_mn) {
+    return (1u << 4)                                     // D format: F32
+           | (static_cast<uint32_t>(a_e5m2) << 7)        // A format
+           | (static_cast<uint32_t>(b_e5m2) << 10)       // B format
+           | (static_cast<uint32_t>(a_mn) << 15)         // A major
+           | (static_cast<uint32_t>(b_mn) << 16)         // B major
+           | (static_cast<uint32_t>(N >> 3) << 17)       // N >> 3
+           | (static_cast<uint32_t>(M >> 4) << 24);      // M >> 4
+}
+
+// act(alpha * v + beta * cold + b) for four values, the activation's branch
+// taken once for all four so that their chains interleave.
+__device__ __forceinline__ void epilogue4(float (&v)[4], float alpha, float beta, const float (&cold)[4],
+                                          const float (&b)[4], int act) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] *= alpha;
+        if (beta != 0.f) v[i] = fmaf(beta, cold[i], v[i]);
+        v[i] += b[i];
+    }
+    if (act == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = gelu_erf(v[i]);
+    } else if (act == 3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = gelu_tanh(v[i]);
+    } else if (act == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = fmaxf(v[i], 0.f);
+    }
+}
+
+}  // namespace gemm11

@@ -1,0 +1,71 @@
+// fp8.h -- host-side interfaces of the 8-bit block-scaled operators (the
+// quantizer, the product and the few-token mixture-of-experts layer), shared
+// by their translation units and api.cu (not installed, not part of the C ABI).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "internal.h"
+
+namespace gemm11 {
+
+constexpr int kScaleBlock = 128;  // elements that share one scale along the contraction
+// 8-bit types, the codes of the C ABI's gemm_dtype.
+constexpr int kTypeE4M3 = 3;
+constexpr int kTypeE5M2 = 4;
+
+// Tensor map of a row-major matrix of `outer` rows of `inner` elements, rows
+// row_bytes apart; false when the encoder is missing or refuses.
+bool encode_matrix_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
+                       uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+
+// ---- quantizer (fp8_quant.cu) ----
+struct Fp8Quant {
+    int rows = 0, cols = 0;
+    const void *X = nullptr;
+    int x_type = 0;
+    long long ldx = 0;
+    void *Q = nullptr;
+    int q_type = kTypeE4M3;
+    long long ldq = 0;
+    float *S = nullptr;
+    long long lds = 0;
+    int layout = 0;  // the codes of gemm_fp8_layout
+};
+cudaError_t run_fp8_quantize(const Fp8Quant &q, cudaStream_t stream, CallInfo *info);
+
+// ---- product (fp8_gemm.cu) ----
+// C = act(alpha * sum over k blocks of sa sb (A_kb op(B)_kb) + beta * C + bias).
+// A: M x K, its scales SA[kb * ldsa + m].  B: N x K (b_trans) or K x N; its
+// scales one for each 128 x 128 block of B as stored, SB[row / 128 * ldsb +
+// col / 128], or (b_rows, N x K only) SB[kb * ldsb + n].
+struct Fp8Gemm {
+    int M = 0, N = 0, K = 0;
+    float alpha = 1.f, beta = 0.f;
+    const void *A = nullptr;
+    int a_type = kTypeE4M3;
+    long long lda = 0;
+    const float *SA = nullptr;
+    long long ldsa = 0;
+    const void *B = nullptr;
+    int b_type = kTypeE4M3;
+    long long ldb = 0;
+    const float *SB = nullptr;
+    long long ldsb = 0;
+    int b_trans = 1;
+    int b_rows = 0;
+    void *C = nullptr;
+    int c_type = 0;
+    long long ldc = 0;
+    const float *bias = nullptr;
+    int act = 0;
+};
+// K > 0 and alpha != 0.
+cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
+// The same with no product (K == 0 or alpha == 0): C = act(beta * C + bias).
+cudaError_t run_fp8_scale_c(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
+
+}  // namespace gemm11

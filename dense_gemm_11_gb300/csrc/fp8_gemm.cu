@@ -1,0 +1,458 @@
+// fp8_gemm.cu -- the product of two matrices held in 8 bits with one FP32
+// scale for each 128 of the contraction:
+//
+//   C[m, n] = act(alpha * sum_kb sa[kb, m] sb[kb, n] D_kb[m, n] + beta C + bias[n]),
+//   D_kb[m, n] = sum over the 128 k of block kb of A[m, k] op(B)[k, n].
+//
+// D_kb has no scales in it, so the tensor core forms it (tcgen05.mma of
+// kind::f8f6f4, FP32 accumulator in tensor memory) and the epilogue warps
+// multiply it by sa sb and add it to running sums in FP32 registers.  That
+// also keeps the tensor core's sums, which truncate, 128 long.  Two
+// accumulators in tensor memory alternate: while the warps take one block's
+// sums out, the tensor core forms the next.
+//
+// Tiles are computed transposed, C^T = op(B)^T A^T: 128 columns n of C on the
+// MMA's row side (tensor-memory lanes), BN rows m on its column side, so that
+// a few rows of A cost no more than BN >= M columns of accumulator and a warp
+// stores 32 consecutive elements of a row of C.
+//
+// Roles of a CTA: warp 0 issues the TMA loads (operand tiles with the 128-byte
+// swizzle, and the BN scales of A for the block), warp 1 the MMAs, the others
+// are the epilogue.  Too few tiles for the SMs: the k blocks of a tile are
+// shared out over the CTAs of a cluster, whose partial sums are added in rank
+// order through distributed shared memory.  Every wait is bounded.
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "fp8.cuh"
+#include "fp8.h"
+
+namespace gemm11 {
+namespace {
+
+constexpr int kPR = 128;                 // columns n of a tile: the MMA's row side
+constexpr int kPBytes = kPR * kScaleBlock;  // 16 KB of op(B) for one k block
+
+struct Fp8Args {
+    int M, N, K, kb_total;
+    float alpha, beta;
+    const float *SB;
+    long long sb_n, sb_kb;  // scale of B: SB[n index * sb_n + kb * sb_kb], n index = n or n / 128
+    int b_rows;
+    const float *bias;
+    int act;
+    void *C;
+    long long ldc;
+    int c_type;
+    int c_vec;  // rows of C take aligned stores of 4 elements
+    int tiles_m, splits;
+    int p_mn;   // op(B)'s tile is MN-major (B stored K x N)
+    uint32_t idesc;
+    unsigned *err;
+    unsigned long long wait_ns;
+    size_t c_extent;  // checked by GEMM11_DEBUG builds
+};
+
+constexpr int tmem_cols_fp8(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512; }
+
+template <int BN, int STAGES>
+struct Fp8Cfg {
+    static constexpr int kEpi = BN <= 64 ? 4 : 8;  // epilogue warps
+    static constexpr int kThreads = 64 + 32 * kEpi;
+    static constexpr int kCols = BN / (kEpi / 4);  // accumulator columns of a warp
+    static constexpr int kQBytes = BN * kScaleBlock;
+    static constexpr int kStageBytes = kPBytes + kQBytes;
+    // Scales of A, one slot for each k block in flight.  The producer refills
+    // block i's slot only after the MMA of block i - STAGES is complete, which
+    // was issued after the epilogue had released block i - STAGES - 2, so
+    // STAGES + 2 slots are never overwritten while in use.
+    static constexpr int kSlots = STAGES + 2;
+    static constexpr int kSlotFloats = BN < 32 ? 32 : BN;  // TMA writes start on 128 bytes
+    static constexpr int kSmemBytes = 1024 + STAGES * kStageBytes + kSlots * kSlotFloats * 4 + (2 * STAGES + 5) * 8 + 16;
+    static constexpr int kTmemCols = tmem_cols_fp8(2 * BN);
+    static_assert(BN % 16 == 0 && BN >= 16 && BN <= 128, "MMA N, two accumulators");
+    static_assert(STAGES * kStageBytes >= kPR * BN * 4, "the partial tile fits in the operand ring");
+};
+
+__device__ __forceinline__ void fp8_timeout(volatile int *abort_flag, unsigned *err) {
+    *abort_flag = 1;
+    atomicOr(err, kWatchdogTimeout);
+}
+
+// Four consecutive columns n.. of row m of C from their sums.
+__device__ __forceinline__ void store4(const Fp8Args &p, int m, int n, float (&v)[4]) {
+    const size_t ci = static_cast<size_t>(m) * static_cast<size_t>(p.ldc) + n;
+    float cold[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool in = n + i < p.N;
+        cold[i] = (p.beta != 0.f && in) ? load_out(p.C, ci + i, p.c_type) : 0.f;
+        b[i] = (p.bias && in) ? __ldg(p.bias + n + i) : 0.f;
+    }
+    epilogue4(v, p.alpha, p.beta, cold, b, p.act);
+    if (!debug_in_bounds(p.c_extent == 0 || ci + min(3, p.N - 1 - n) < p.c_extent, p.err)) return;
+    if (p.c_vec && n + 4 <= p.N) {
+        if (p.c_type == kOutF32)
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.C) + ci) = make_float4(v[0], v[1], v[2], v[3]);
+        else
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.C) + ci) =
+                make_uint2(pack2_out16(v[0], v[1], p.c_type), pack2_out16(v[2], v[3], p.c_type));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < p.N) store_out(p.C, ci + i, p.c_type, v[i]);
+    }
+}
+
+template <int BN, int STAGES>
+__global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
+    fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
+                    const __grid_constant__ CUtensorMap tm_sq, const Fp8Args p) {
+    using Cfg = Fp8Cfg<BN, STAGES>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sP = smem;
+    uint8_t *sQ = smem + STAGES * kPBytes;
+    float *sS = reinterpret_cast<float *>(sQ + STAGES * Cfg::kQBytes);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sS + Cfg::kSlots * Cfg::kSlotFloats);
+    uint64_t *empty = full + STAGES;
+    uint64_t *tfull = empty + STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], Cfg::kEpi);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tm_p);
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_sq);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_holder, Cfg::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // The M tiles of one 128-column panel of op(B) run next to each other.
+    const int tile = blockIdx.x / p.splits, split = blockIdx.x % p.splits;
+    const int n0 = (tile / p.tiles_m) * kPR, m0 = (tile % p.tiles_m) * BN;
+    const int kb0 = static_cast<int>(static_cast<long long>(p.kb_total) * split / p.splits);
+    const int kb1 = static_cast<int>(static_cast<long long>(p.kb_total) * (split + 1) / p.splits);
+    const int q = warp & 3;                               // tensor-memory lane quarter
+    const int col0 = ((warp - 2) >> 2) * Cfg::kCols;      // first accumulator column (epilogue warps)
+    const int n = n0 + q * 32 + lane;
+    float acc[Cfg::kCols];
+    uint32_t armed = 0, armed_parity = 0;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ TMA producer
+        int stage = 0, slot = 0;
+        uint32_t phase = 0;
+        for (int kb = kb0; kb < kb1 && !*abort_flag; ++kb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
+                fp8_timeout(abort_flag, p.err);
+                break;
+            }
+            mbar_arrive_expect_tx(&full[stage], Cfg::kStageBytes + BN * 4);
+            const int k0 = kb * kScaleBlock;
+            if (p.p_mn)
+                tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, n0, k0);
+            else
+                tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, k0, n0);
+            tma_load_2d(&tm_q, &full[stage], sQ + stage * Cfg::kQBytes, k0, m0);
+            tma_load_2d(&tm_sq, &full[stage], sS + slot * Cfg::kSlotFloats, m0, kb);
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            if (kDebugBuild && !mbar_wait(&empty[stage], phase, p.wait_ns)) {  // one stage in flight
+                fp8_timeout(abort_flag, p.err);
+                break;
+            }
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            if (++slot == Cfg::kSlots) slot = 0;
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ------------------------------------------------ MMA issuer
+        // K-major: 128-byte rows, 8-row groups 1024 bytes apart, 32 k = 32
+        // bytes along the row.  MN-major: 128 n bytes for each k, 8-k groups
+        // 1024 bytes apart, 32 k = 4 groups.
+        const uint64_t p_desc0 = umma_desc_sw128(smem_u32(sP), 16, 1024);
+        const uint64_t q_desc0 = umma_desc_sw128(smem_u32(sQ), 16, 1024);
+        const uint32_t p_step = p.p_mn ? 4096u >> 4 : 32u >> 4;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int i = 0; i < kb1 - kb0; ++i) {
+            const int buf = i & 1;
+            if (!mbar_wait(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) || !mbar_wait(&full[stage], phase, p.wait_ns)) {
+                fp8_timeout(abort_flag, p.err);
+                break;
+            }
+            tc_fence_after();
+            const uint64_t pd = p_desc0 + static_cast<uint64_t>(stage * (kPBytes >> 4));
+            const uint64_t qd = q_desc0 + static_cast<uint64_t>(stage * (Cfg::kQBytes >> 4));
+#pragma unroll
+            for (int kk = 0; kk < kScaleBlock / 32; ++kk)
+                umma_f8(tmem_base + buf * BN, pd + p_step * kk, qd + 2u * kk, p.idesc, kk > 0 ? 1u : 0u);
+            umma_commit(&empty[stage]);
+            umma_commit(&tfull[buf]);
+            if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ epilogue: scale and add
+#pragma unroll
+        for (int j = 0; j < Cfg::kCols; ++j) acc[j] = 0.f;
+        const int nn = p.b_rows ? min(n, p.N - 1) : n0 / kScaleBlock;
+        const float *sb = p.SB + nn * p.sb_n;
+        float s_next = kb0 < kb1 ? __ldg(sb + kb0 * p.sb_kb) : 0.f;
+        int slot = 0;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const int i = kb - kb0, buf = i & 1;
+            const float s = s_next;
+            if (kb + 1 < kb1) s_next = __ldg(sb + (kb + 1) * p.sb_kb);
+            if (!mbar_wait(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
+                fp8_timeout(abort_flag, p.err);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + col0;
+            const float4 *sa = reinterpret_cast<const float4 *>(sS + slot * Cfg::kSlotFloats + col0);
+#pragma unroll
+            for (int c = 0; c < Cfg::kCols / 16; ++c) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(t + c * 16, r);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 f = sa[c * 4 + j];
+                    acc[c * 16 + 4 * j] = fmaf(s * f.x, __uint_as_float(r[4 * j]), acc[c * 16 + 4 * j]);
+                    acc[c * 16 + 4 * j + 1] = fmaf(s * f.y, __uint_as_float(r[4 * j + 1]), acc[c * 16 + 4 * j + 1]);
+                    acc[c * 16 + 4 * j + 2] = fmaf(s * f.z, __uint_as_float(r[4 * j + 2]), acc[c * 16 + 4 * j + 2]);
+                    acc[c * 16 + 4 * j + 3] = fmaf(s * f.w, __uint_as_float(r[4 * j + 3]), acc[c * 16 + 4 * j + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[buf]);
+            if (++slot == Cfg::kSlots) slot = 0;
+        }
+        if (p.splits == 1 && !*abort_flag && n < p.N) {
+            const float b_n = p.bias ? __ldg(p.bias + n) : 0.f;
+            const float b4[4] = {b_n, b_n, b_n, b_n};
+#pragma unroll
+            for (int j = 0; j < Cfg::kCols; j += 4) {
+                if (m0 + col0 + j >= p.M) break;
+                float w[4], cold[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int m = m0 + col0 + j + k;
+                    w[k] = acc[j + k];
+                    cold[k] = (p.beta != 0.f && m < p.M) ? load_out(p.C, static_cast<size_t>(m) * p.ldc + n, p.c_type) : 0.f;
+                }
+                epilogue4(w, p.alpha, p.beta, cold, b4, p.act);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const size_t ci = static_cast<size_t>(m0 + col0 + j + k) * p.ldc + n;
+                    if (m0 + col0 + j + k < p.M && debug_in_bounds(p.c_extent == 0 || ci < p.c_extent, p.err))
+                        store_out(p.C, ci, p.c_type, w[k]);
+                }
+            }
+        }
+    }
+
+    // ---------------------------------------------------- drain: copies and MMAs of this CTA
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < STAGES; ++s)
+            if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u)) fp8_timeout(abort_flag, p.err);
+    }
+    if (warp == 1 && lane == 0) {
+        umma_commit(mma_done);
+        if (!mbar_wait(mma_done, 0)) fp8_timeout(abort_flag, p.err);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem_base, Cfg::kTmemCols);
+    }
+    if (p.splits == 1) return;
+
+    // ---------------------------------------------------- cluster split: add the partial tiles
+    // The operand ring is idle now; each CTA's partial goes over it, row m of
+    // C at m * 128 floats, and the CTAs take groups of four columns in turn.
+    float *part = reinterpret_cast<float *>(smem);
+    const int rows = min(BN, p.M - m0);
+    if (warp >= 2) {
+#pragma unroll
+        for (int j = 0; j < Cfg::kCols; ++j)
+            if (col0 + j < rows) part[(col0 + j) * kPR + q * 32 + lane] = acc[j];
+    }
+    cluster_sync();
+    const uint32_t part_addr = smem_u32(part);
+    if (!*abort_flag) {
+        for (int i = split * Cfg::kThreads + threadIdx.x; i < rows * (kPR / 4); i += p.splits * Cfg::kThreads) {
+            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int r = 0; r < p.splits; ++r) {
+                const float4 w = ld_shared_cluster_v4(mapa_shared(part_addr + i * 16, r));
+                v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+            }
+            const int nn = n0 + (i % (kPR / 4)) * 4;
+            if (nn < p.N) store4(p, m0 + i / (kPR / 4), nn, v);
+        }
+    }
+    __syncwarp();
+    cluster_sync();  // a CTA's partial stays until every CTA has read it
+}
+
+// C = act(beta * C + bias), where there is no product.
+__global__ void __launch_bounds__(256) fp8_scale_c_kernel(const Fp8Args p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long groups = (p.N + 3) / 4, total = groups * p.M;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        store4(p, static_cast<int>(i / groups), static_cast<int>(i % groups) * 4, v);
+    }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
+Fp8Args fp8_args(const Fp8Gemm &g) {
+    Fp8Args a = {};
+    a.M = g.M;
+    a.N = g.N;
+    a.K = g.K;
+    a.kb_total = (g.K + kScaleBlock - 1) / kScaleBlock;
+    a.alpha = g.alpha;
+    a.beta = g.beta;
+    a.SB = g.SB;
+    a.b_rows = g.b_rows;
+    a.sb_n = g.b_rows ? 1 : (g.b_trans ? g.ldsb : 1);
+    a.sb_kb = g.b_rows ? g.ldsb : (g.b_trans ? 1 : g.ldsb);
+    a.bias = g.bias;
+    a.act = g.act;
+    a.C = g.C;
+    a.ldc = g.ldc;
+    a.c_type = g.c_type;
+    const int cb = g.c_type == kOutF32 ? 4 : 2;
+    a.c_vec = reinterpret_cast<uintptr_t>(g.C) % (4 * cb) == 0 && (g.M == 1 || g.ldc % 4 == 0);
+    a.p_mn = g.b_trans ? 0 : 1;
+    a.err = watchdog_word();
+    a.wait_ns = kWaitLimitNs;
+    a.splits = 1;
+    if (kDebugBuild) a.c_extent = static_cast<size_t>(g.M - 1) * static_cast<size_t>(g.ldc) + g.N;
+    return a;
+}
+
+template <int BN, int STAGES>
+cudaError_t launch_fp8_tile(const Fp8Gemm &g, Fp8Args a, cudaStream_t stream) {
+    using Cfg = Fp8Cfg<BN, STAGES>;
+    auto kern = fp8_tile_kernel<BN, STAGES>;
+    static unsigned long long smem_set = 0;
+    cudaError_t e = ensure_dynamic_smem(kern, Cfg::kSmemBytes, smem_set);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tp, tq, ts;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const bool ok =
+        (g.b_trans ? encode_matrix_map(&tp, u8, g.B, g.K, g.N, g.ldb, kScaleBlock, kPR, sw)
+                   : encode_matrix_map(&tp, u8, g.B, g.N, g.K, g.ldb, kPR, kScaleBlock, sw)) &&
+        encode_matrix_map(&tq, u8, g.A, g.K, g.M, g.lda, kScaleBlock, BN, sw) &&
+        encode_matrix_map(&ts, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.SA, g.M, a.kb_total, g.ldsa * 4, BN, 1,
+                          CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (!ok) return cudaErrorNotSupported;
+    a.idesc = umma_idesc_f8(kPR, BN, g.b_type == kTypeE5M2, g.a_type == kTypeE5M2, a.p_mn, 0);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(a.splits);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((g.N + kPR - 1) / kPR) * a.tiles_m * a.splits);
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.splits > 1 ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, tp, tq, ts, a);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+}  // namespace
+
+bool encode_matrix_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
+                       uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {(row_bytes + 15) / 16 * 16};  // a single row has no stride of its own
+    cuuint32_t box[2] = {box_inner, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) {
+    Fp8Args a = fp8_args(g);
+    const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;
+    a.tiles_m = (g.M + bn - 1) / bn;
+    const long long tiles = static_cast<long long>((g.N + kPR - 1) / kPR) * a.tiles_m;
+    const int sms = device_sm_count();
+    if (tiles * 2 <= sms) a.splits = static_cast<int>(std::min<long long>({8, sms / tiles, std::max(1, a.kb_total / 2)}));
+    info->launches = 1;
+    switch (bn) {
+        case 16: info->plan = "fp8_tile_n16"; return launch_fp8_tile<16, 10>(g, a, stream);
+        case 32: info->plan = "fp8_tile_n32"; return launch_fp8_tile<32, 9>(g, a, stream);
+        case 64: info->plan = "fp8_tile_n64"; return launch_fp8_tile<64, 8>(g, a, stream);
+        default: info->plan = "fp8_tile_n128"; return launch_fp8_tile<128, 6>(g, a, stream);
+    }
+}
+
+cudaError_t run_fp8_scale_c(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) {
+    const Fp8Args a = fp8_args(g);
+    const long long groups = static_cast<long long>((g.N + 3) / 4) * g.M;
+    const unsigned grid = static_cast<unsigned>(std::min<long long>((groups + 255) / 256, 8LL * device_sm_count()));
+    info->plan = "fp8_scale_c";
+    info->launches = 1;
+    return launch_kernel(fp8_scale_c_kernel, dim3(grid), dim3(256), 0, stream, a);
+}
+
+}  // namespace gemm11

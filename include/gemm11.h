@@ -89,7 +89,9 @@ typedef enum {
 typedef enum {
     GEMM_DTYPE_F32 = 0,  /* IEEE binary32 */
     GEMM_DTYPE_F16 = 1,  /* IEEE binary16 (__half) */
-    GEMM_DTYPE_BF16 = 2  /* bfloat16 (__nv_bfloat16): binary32 with the low 16 bits dropped */
+    GEMM_DTYPE_BF16 = 2, /* bfloat16 (__nv_bfloat16): binary32 with the low 16 bits dropped */
+    GEMM_DTYPE_E4M3 = 3, /* 8 bits, 4 exponent, 3 mantissa, no infinity, largest value 448 (fp8 entry points only) */
+    GEMM_DTYPE_E5M2 = 4  /* 8 bits, 5 exponent, 2 mantissa, largest value 57344 (fp8 entry points only) */
 } gemm_dtype;
 
 /*
@@ -252,6 +254,79 @@ GEMM11_API int gemm_tc_strided_batched(int batch, int M, int N, int K, float alp
  */
 GEMM11_API int gemm_f16_f32acc_epilogue_noalloc(int M, int N, int K, float alpha, const void *A, const void *B,
                                                 float beta, float *C, const float *bias, int act, void *stream);
+
+/*
+ * Matrices held in 8 bits with one FP32 scale for each block of 128.
+ *
+ * A value is q * s: q an 8-bit float, s the scale of its block.  The blocks
+ * run along the dimension that a product sums over, so that the product can
+ * form each block's sum of q's on the tensor cores and apply the scales to it:
+ *   GEMM_FP8_ROWS    a block is 128 consecutive elements of a row.  Q is
+ *                    rows x cols; element (r, c) has the scale
+ *                    S[(c / 128) * lds + r] -- the scales of one block column
+ *                    lie next to each other, as a product reads them.
+ *   GEMM_FP8_COLS    a block is 128 consecutive elements of a column, and Q is
+ *                    the transpose, cols x rows: Q[c * ldq + r] with the scale
+ *                    S[(r / 128) * lds + c].  (The same as GEMM_FP8_ROWS of the
+ *                    transposed matrix: an operand of a product that sums over
+ *                    its rows, such as the gradient of a layer's weights.)
+ *   GEMM_FP8_BLOCKS  a block is 128 x 128: Q is rows x cols with the scale
+ *                    S[(r / 128) * lds + c / 128].  Serves products along
+ *                    either dimension (a layer's weights: forward, and
+ *                    gradient of the input).
+ * The last block of a row or column may be shorter.
+ */
+typedef enum {
+    GEMM_FP8_ROWS = 0,
+    GEMM_FP8_COLS = 1,
+    GEMM_FP8_BLOCKS = 2
+} gemm_fp8_layout;
+
+/*
+ * gemm_fp8_quantize_block128 -- X (rows x cols, row-major, ldx elements a row,
+ * FP32, FP16 or BF16) to 8 bits (q_type GEMM_DTYPE_E4M3 or GEMM_DTYPE_E5M2)
+ * with scales, in one of the layouts above.  For each block, with
+ * F = 448 (e4m3) or 57344 (e5m2):
+ *   a = max(max |x|, 2^-117),   s = a / F,   q = round8(x * (F / a)),
+ * every operation in FP32 rounded to nearest, round8 to nearest even.  A NaN
+ * becomes a NaN code and does not count in the maximum; an infinity makes the
+ * scale of its block infinite, so every value of the block reads back as NaN
+ * or infinity.
+ * Any alignment and leading dimensions are accepted (16-byte aligned rows of X
+ * and 8-byte aligned rows of Q take wider loads and stores).  Returns
+ * GEMM_ERR_INVALID_ARG for a negative size, a short leading dimension, an
+ * unknown type or layout, or a NULL pointer with a non-empty extent.
+ */
+GEMM11_API int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int x_type, long long ldx, void *Q,
+                                          int q_type, long long ldq, float *S, long long lds, int layout,
+                                          void *stream);
+
+/*
+ * gemm_fp8_block128 -- the product of two matrices held as above:
+ *   C = round_c( act( alpha * sum_k A[i, k] op(B)[k, j] + beta * C[i, j] + bias[j] ) )
+ * with A[i, k] = Qa[i * lda + k] * SA[(k / 128) * ldsa + i] (GEMM_FP8_ROWS) and
+ *   b_trans = 1  B stored N x K, op(B) = B^T; b_layout GEMM_FP8_BLOCKS
+ *                (SB[(j / 128) * ldsb + k / 128]: a layer's forward product) or
+ *                GEMM_FP8_ROWS (SB[(k / 128) * ldsb + j]: the gradient of its
+ *                weights, both operands quantized along the tokens);
+ *   b_trans = 0  B stored K x N, op(B) = B; b_layout GEMM_FP8_BLOCKS only
+ *                (SB[(k / 128) * ldsb + j / 128]: the gradient of its input,
+ *                with the weights as the forward product holds them).
+ * a_type and b_type are GEMM_DTYPE_E4M3 or GEMM_DTYPE_E5M2 and may differ;
+ * c_type is FP32, FP16 or BF16.  The q's of one block are multiplied and
+ * summed on the tensor cores (exact products, FP32 sums 128 long); scales,
+ * the sum over blocks and the epilogue are FP32 with round-to-nearest.
+ * alpha, beta, bias, act, round_c and the degenerate shapes are those of
+ * gemm_tc_f32acc_epilogue.  C may have any alignment and any ldc >= N.
+ * The tensor-memory-access path needs A, B and SA 16-byte aligned, lda and ldb
+ * multiples of 16 (bytes), ldsa a multiple of 4, and for GEMM_FP8_ROWS of B
+ * the same of SB and ldsb (leading dimensions of a single row excepted);
+ * anything else returns GEMM_ERR_UNSUPPORTED.  M, N and K are unrestricted.
+ */
+GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_type, long long lda,
+                                 const float *SA, long long ldsa, const void *B, int b_type, long long ldb,
+                                 const float *SB, long long ldsb, int b_trans, int b_layout, float beta, void *C,
+                                 int c_type, long long ldc, const float *bias, int act, void *stream);
 
 /*
  * Tuned plans.  The planners pick a kernel family, tile width and split-K

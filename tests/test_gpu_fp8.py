@@ -1,0 +1,310 @@
+"""The quantizer to 8 bits with block-128 scales and the product of matrices held that way.
+
+Bounds.  The quantizer's formula is a chain of correctly rounded FP32
+operations, so its outputs are compared bit for bit.  The product: the q's
+multiply exactly; the tensor core sums 128 of them in FP32 in four steps whose
+alignment may drop up to 2^-24 of the largest term for each of the 33 addends
+of a step, 4 * 33 * 2^-24 = 7.9e-6 of sum |a||b| at the very most; the two
+scale products and the sum over at most 90 blocks round to nearest, each at
+2^-24 of a partial sum no larger than S: together at most 1e-5 S + 5e-6 S at
+90 blocks, and the shapes here have at most 32.  So 1e-5 S, the framework's
+bound for FP32 products, plus one rounding of a 16-bit result.
+"""
+import numpy as np
+import pytest
+import torch
+
+import dense_gemm_11_gb300 as g
+import fp8_ref as ref
+from conftest import gpu_available
+from helpers import TOL_F32, assert_within
+
+pytestmark = [pytest.mark.gpu, pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
+E4, E5 = torch.float8_e4m3fn, torch.float8_e5m2
+OUT = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+
+
+def rand(rows, cols, seed, dtype=torch.float32, scale=1.0):
+    x = torch.from_numpy(np.random.default_rng(seed).standard_normal((rows, cols)) * scale).to(dtype)
+    return x.cuda()
+
+
+def quantized(x, layout, dtype=E4):
+    Q, S = g.fp8_empty(*x.shape, layout, dtype)
+    g.fp8_quantize(x, Q, S, layout)
+    return Q, S
+
+
+def assert_quantized(x, Q, S, layout):
+    assert g.check() == g.GEMM_OK
+    q, s = ref.quantize(x.float().cpu().numpy(), Q.dtype, layout)
+    assert np.array_equal(S.double().cpu().numpy(), s, equal_nan=True)
+    assert np.array_equal(Q.float().double().cpu().numpy(), q, equal_nan=True)
+
+
+@pytest.mark.parametrize("layout", ["rows", "cols", "blocks"])
+@pytest.mark.parametrize("xt", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (16, 4096), (127, 129), (129, 200), (300, 1000), (33, 65), (257, 640)])
+def test_quantize(layout, xt, rows, cols):
+    x = rand(rows, cols, rows + cols, xt)
+    for dtype in (E4, E5):
+        assert_quantized(x, *quantized(x, layout, dtype), layout)
+
+
+@pytest.mark.parametrize("layout", ["rows", "cols", "blocks"])
+def test_quantize_strided_and_unaligned(layout):
+    """Rows that start anywhere, on either side."""
+    base = rand(150, 411, 3, torch.bfloat16)
+    for off, cols in ((1, 300), (8, 256), (3, 77)):
+        x = base[:, off:off + cols]
+        qr, qc = (cols, 150) if layout == "cols" else (150, cols)
+        room = torch.zeros(qr, qc + 13, dtype=torch.uint8, device="cuda")
+        Q = room.view(E4)[:, 5:5 + qc]
+        S = torch.zeros(g._fp8_shapes(150, cols, layout)[1], device="cuda")
+        g.fp8_quantize(x, Q, S, layout)
+        assert_quantized(x, Q, S, layout)
+        assert not room[:, :5].any() and not room[:, 5 + qc:].any()
+
+
+@pytest.mark.parametrize("layout", ["rows", "cols", "blocks"])
+def test_quantize_special_values(layout):
+    x = rand(256, 256, 5)
+    x[:128, :128] = 0.0                     # a block of zeros
+    x[3, 200], x[200, 3] = float("nan"), float("-inf")
+    x[130, 130:256] *= 2.0 ** -130          # subnormal values beside ordinary ones
+    x[255, 255] = 3.0e38
+    for dtype in (E4, E5):
+        Q, S = quantized(x, layout, dtype)
+        assert_quantized(x, Q, S, layout)
+    tiny = torch.full((4, 256), 1e-44, device="cuda")
+    assert_quantized(tiny, *quantized(tiny, layout), layout)
+
+
+def test_quantize_empty():
+    for r, c in ((0, 5), (5, 0)):
+        for layout in ("rows", "cols", "blocks"):
+            g.fp8_quantize(torch.empty(r, c, device="cuda"), *g.fp8_empty(r, c, layout), layout)
+            assert g.last_launch_count() == 0
+
+
+def operands(M, N, K, way, a_type=E4, b_type=E4, seed=0):
+    """(A, SA, B, SB, keyword arguments) of one direction of a linear layer."""
+    if way == "wgrad":
+        A, SA = quantized(rand(K, M, seed), "cols", a_type)
+        B, SB = quantized(rand(K, N, seed + 1), "cols", b_type)
+        return A, SA, B, SB, {"b_trans": True, "b_scales": "rows"}
+    A, SA = quantized(rand(M, K, seed), "rows", a_type)
+    t = way == "forward"
+    B, SB = quantized(rand(*((N, K) if t else (K, N)), seed + 1, scale=K ** -0.5), "blocks", b_type)
+    return A, SA, B, SB, {"b_trans": t, "b_scales": "blocks"}
+
+
+def check_product(M, N, K, way, ct=torch.float32, seed=0, types=(E4, E4), alpha=1.0, beta=0.0, bias=False, act=0, ld_pad=0):
+    A, SA, B, SB, kw = operands(M, N, K, way, *types, seed)
+    room = rand(M, N + ld_pad, seed + 2, ct) if beta else torch.full((M, N + ld_pad), float("nan"), dtype=ct, device="cuda")
+    before, C = room.clone(), room[:, :N]
+    b = rand(1, N, seed + 3)[0] if bias else None
+    want, S = ref.product(A, SA, B, SB, kw["b_trans"], kw["b_scales"], alpha, beta, before[:, :N], b, act)
+    g.gemm_fp8(A, SA, B, SB, C, alpha, beta, b, act, **kw)
+    assert g.check() == g.GEMM_OK
+    assert_within(C.double().cpu().numpy(), want.cpu().numpy(), S.cpu().numpy(), TOL_F32, f"{way} {M}x{N}x{K} {g.last_plan()}",
+                  out=OUT[ct], bias=None if b is None else b.cpu().numpy())
+    if ld_pad:
+        assert torch.equal(room[:, N:].view(torch.uint8), before[:, N:].view(torch.uint8))
+
+
+SHAPES = [(1, 1, 1), (1, 128, 128), (1, 4096, 512), (2, 130, 127), (16, 640, 300), (17, 257, 129), (33, 96, 1000), (64, 1024, 2048),
+          (65, 200, 256), (128, 128, 4096), (129, 384, 640), (200, 1111, 130), (300, 256, 255), (513, 700, 384), (1000, 3000, 777)]
+
+
+@pytest.mark.parametrize("way", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(way, M, N, K):
+    check_product(M, N, K, way, seed=M + N + K)
+
+
+@pytest.mark.parametrize("way", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("types", [(E5, E4), (E4, E5), (E5, E5)])
+def test_product_types(way, types):
+    for M, N, K in ((9, 300, 400), (260, 300, 400)):
+        check_product(M, N, K, way, types=types)
+
+
+@pytest.mark.parametrize("ct", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("act", [0, 1, 2, 3])
+@pytest.mark.parametrize("M,N,K", [(7, 300, 500), (140, 260, 256), (300, 520, 130)])
+def test_product_epilogue(ct, act, M, N, K):
+    check_product(M, N, K, "forward", ct, alpha=0.7, beta=0.0, bias=True, act=act)
+    check_product(M, N, K, "dgrad", ct, alpha=-1.3, beta=0.5, bias=True, act=act, ld_pad=3)
+
+
+def test_product_into_odd_columns():
+    """C whose rows start anywhere."""
+    for M in (5, 150, 300):
+        A, SA, B, SB, kw = operands(M, 203, 256, "forward")
+        room = torch.zeros(M, 211, dtype=torch.bfloat16, device="cuda")
+        C = room[:, 3:206]
+        g.gemm_fp8(A, SA, B, SB, C)
+        want, S = ref.product(A, SA, B, SB, True, "blocks")
+        assert_within(C.double().cpu().numpy(), want.cpu().numpy(), S.cpu().numpy(), TOL_F32, out="bf16")
+        assert not room[:, :3].any() and not room[:, 206:].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(4, 256, 4096), (256, 256, 4096), (1000, 512, 2048)])
+def test_product_of_small_integers_is_exact(M, N, K):
+    """With scales of one every sum is an integer below 2^24."""
+    rng = np.random.default_rng(M)
+    a = torch.from_numpy(rng.integers(-4, 5, (M, K)).astype(np.float32)).cuda()
+    b = torch.from_numpy(rng.integers(-4, 5, (N, K)).astype(np.float32)).cuda()
+    SA, SB = torch.ones(K // 128, M, device="cuda"), torch.ones(N // 128, K // 128, device="cuda")
+    C = torch.empty(M, N, device="cuda")
+    g.gemm_fp8(a.to(E4), SA, b.to(E4), SB, C)
+    assert torch.equal(C.double(), a.double() @ b.double().t())
+
+
+def test_product_scales_of_very_different_size():
+    """Each block's scale reaches its own sums and no others."""
+    A, SA, B, SB, kw = operands(150, 400, 1024, "forward")
+    for t in (SA, SB):
+        t.copy_(torch.from_numpy(2.0 ** np.random.default_rng(1).integers(-20, 20, t.shape)).float())
+    for m in (5, 150):
+        C = torch.empty(m, 400, device="cuda")
+        g.gemm_fp8(A[:m], SA[:, :m], B, SB, C)
+        want, S = ref.product(A[:m], SA[:, :m], B, SB, True, "blocks")
+        assert_within(C.double().cpu().numpy(), want.cpu().numpy(), S.cpu().numpy(), TOL_F32)
+
+
+def test_product_keeps_nan_in_its_row():
+    for M in (4, 200, 400):
+        x = rand(M, 512, 1)
+        x[2, 77] = float("nan")
+        A, SA = quantized(x, "rows")
+        B, SB = quantized(rand(300, 512, 2), "blocks")
+        C = torch.empty(M, 300, device="cuda")
+        g.gemm_fp8(A, SA, B, SB, C)
+        bad = torch.isnan(C).all(dim=1)
+        assert bad[2] and int(bad.sum()) == 1 and int(torch.isnan(C).any(dim=1).sum()) == 1
+
+
+def test_no_product():
+    """alpha = 0 or K = 0 leave act(beta C + bias); a C that is not read may hold NaN."""
+    A, SA, B, SB, kw = operands(40, 130, 256, "forward")
+    bias = rand(1, 130, 9)[0]
+    C = torch.full((40, 133), float("nan"), device="cuda")[:, :130]
+    g.gemm_fp8(A, SA, B, SB, C, alpha=0.0, bias=bias, act=2)
+    assert torch.equal(C, bias.clamp(min=0).expand(40, 130))
+    g.gemm_fp8(A[:, :0], SA[:0], B[:, :0], SB[:, :0], C, beta=2.0)
+    assert torch.equal(C, 2 * bias.clamp(min=0).expand(40, 130))
+    g.gemm_fp8(A[:0], SA[:, :0], B, SB, C[:0])
+    assert g.last_launch_count() == 0
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (40, 512, 4096), (300, 640, 1000), (129, 4096, 512)])
+def test_repeats_are_bitwise_equal(M, N, K):
+    A, SA, B, SB, kw = operands(M, N, K, "forward")
+    outs = []
+    for _ in range(3):
+        C = torch.empty(M, N, device="cuda")
+        g.gemm_fp8(A, SA, B, SB, C)
+        outs.append(C)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+
+
+def test_two_streams():
+    jobs = [(operands(M, N, K, "forward", seed=M), torch.empty(M, N, device="cuda")) for M, N, K in ((16, 4096, 2048), (300, 1024, 1024))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for (args, C), st in zip(jobs, streams):
+            g.gemm_fp8(*args[:4], C, stream=st)
+    torch.cuda.synchronize()
+    for (args, C), _ in zip(jobs, streams):
+        want, S = ref.product(*args[:4], True, "blocks")
+        assert_within(C.double().cpu().numpy(), want.cpu().numpy(), S.cpu().numpy(), TOL_F32)
+
+
+def test_captured_chain():
+    """Quantizer and product in a CUDA graph, replayed on other inputs."""
+    x = rand(24, 512, 1, torch.bfloat16)
+    B, SB = quantized(rand(384, 512, 2), "blocks")
+    A, SA = g.fp8_empty(24, 512, "rows")
+    C = torch.empty(24, 384, device="cuda")
+
+    def chain():
+        g.fp8_quantize(x, A, SA, "rows")
+        g.gemm_fp8(A, SA, B, SB, C)
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for seed in (5, 6):
+        x.copy_(rand(24, 512, seed, torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, S = ref.product(A, SA, B, SB, True, "blocks")
+        assert_quantized(x, A, SA, "rows")
+        assert_within(C.double().cpu().numpy(), want.cpu().numpy(), S.cpu().numpy(), TOL_F32)
+
+
+def test_gradients_against_formula_and_differences():
+    """f(x, W) = sum(dy * (x W^T)) on the values that the 8-bit operands hold: dx and dW from the two backward products."""
+    T, I, O = 150, 260, 330
+    x, W, dy = rand(T, I, 1), rand(O, I, 2, scale=I ** -0.5), rand(T, O, 3)
+    Wq, dyq = quantized(W, "blocks"), quantized(dy, "rows", E5)
+    dx = torch.empty(T, I, device="cuda")
+    g.gemm_fp8(*dyq, *Wq, dx, b_trans=False)
+    w64, dy64, x64 = ref.dequantize(*Wq, "blocks"), ref.dequantize(*dyq, "rows"), x.double()
+    S = (dy64.abs() @ w64.abs()).cpu().numpy()
+    assert_within(dx.double().cpu().numpy(), (dy64 @ w64).cpu().numpy(), S, TOL_F32, "dx")
+    f = lambda x_, w_, d_: float((d_ * (x_ @ w_.t())).sum())  # noqa: E731
+    for t, i in ((0, 0), (77, 200), (149, 259)):
+        e = torch.zeros_like(x64)
+        e[t, i] = 0.5
+        diff = f(x64 + e, w64, dy64) - f(x64 - e, w64, dy64)  # linear in x: exact up to rounding in 64 bits
+        assert abs(float(dx[t, i]) - diff) <= TOL_F32 * S[t, i] + 1e-9
+    dyc, xc = quantized(dy, "cols", E5), quantized(x, "cols")
+    dW = torch.empty(O, I, device="cuda")
+    g.gemm_fp8(*dyc, *xc, dW, b_scales="rows")
+    dy64, x64 = ref.dequantize(*dyc, "rows").t(), ref.dequantize(*xc, "rows").t()
+    S = (dy64.abs().t() @ x64.abs()).cpu().numpy()
+    assert_within(dW.double().cpu().numpy(), (dy64.t() @ x64).cpu().numpy(), S, TOL_F32, "dW")
+    for o, i in ((0, 0), (200, 100), (329, 259)):
+        e = torch.zeros_like(w64)
+        e[o, i] = 0.5
+        diff = f(x64, w64 + e, dy64) - f(x64, w64 - e, dy64)
+        assert abs(float(dW[o, i]) - diff) <= TOL_F32 * S[o, i] + 1e-9
+
+
+def test_refusals():
+    A, SA, B, SB, kw = operands(20, 256, 256, "forward")
+    C = torch.empty(20, 256, device="cuda")
+    x = rand(20, 256, 1)
+    with pytest.raises(TypeError):
+        g.fp8_quantize(x.double(), A, SA)
+    with pytest.raises(TypeError):
+        g.fp8_quantize(x, A.float(), SA)
+    with pytest.raises(TypeError):
+        g.fp8_quantize(x.cpu(), A, SA)
+    with pytest.raises(ValueError):
+        g.fp8_quantize(x, A, SA, "columns")
+    with pytest.raises(ValueError):
+        g.fp8_quantize(x, A, SA, "cols")
+    with pytest.raises(ValueError):
+        g.fp8_quantize(x.t(), *g.fp8_empty(256, 20))
+    with pytest.raises(ValueError):
+        g.gemm_fp8(A, SA, B, SB, C[:, :255])
+    with pytest.raises(ValueError):
+        g.gemm_fp8(A, SA[:, :19], B, SB, C)
+    with pytest.raises(ValueError):
+        g.gemm_fp8(A, SA, B, SB, C, b_trans=False, b_scales="rows")
+    with pytest.raises(TypeError):
+        g.gemm_fp8(A, SA, B, SB, C, bias=torch.zeros(255, device="cuda"))
+    with pytest.raises(g.GemmError) as e:
+        g.gemm_fp8(A, SA, B, SB, C, act=4)
+    assert e.value.status == g.GEMM_ERR_INVALID_ARG
+    odd = torch.empty(20, 257, dtype=torch.uint8, device="cuda").view(E4)[:, :256]
+    with pytest.raises(g.GemmError) as e:
+        g.gemm_fp8(odd, SA, B, SB, C)
+    assert e.value.status == g.GEMM_ERR_UNSUPPORTED
