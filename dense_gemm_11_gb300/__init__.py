@@ -13,6 +13,7 @@ fallback: if the shared library is missing, every call raises.
     gemm_tc_batched(A, B, C, ..., b_trans=False)      a strided batch of those (3-D tensors), op(B) = B or B^T
     fp8_quantize(X, Q, S, layout="rows")              X held in 8 bits with an FP32 scale for each block of 128
     gemm_fp8(A, SA, B, SB, C, ..., b_trans=True)      the product of two matrices held that way
+    moe_few_tokens(X, router, gate, up, down, Y, k)   a mixture-of-experts layer for a few tokens, one launch
 
 Tensors are torch CUDA tensors on the current device; A and B may be 2-D
 views with a leading dimension larger than their width (unit column stride).
@@ -37,6 +38,7 @@ GEMM_ACT_NONE = 0
 GEMM_ACT_GELU = 1
 GEMM_ACT_RELU = 2
 GEMM_ACT_GELU_TANH = 3
+GEMM_ACT_SILU = 4
 GEMM_DTYPE_F32 = 0
 GEMM_DTYPE_F16 = 1
 GEMM_DTYPE_BF16 = 2
@@ -59,7 +61,7 @@ class TuneEntry(ctypes.Structure):
 
 EXPORTED_SYMBOLS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_f16_f32acc_epilogue", "gemm_bf16_f32acc_epilogue",
                     "gemm_tc_f32acc_epilogue", "gemm_tc_strided_batched", "gemm_f16_f32acc_epilogue_noalloc",
-                    "gemm_fp8_quantize_block128", "gemm_fp8_block128",
+                    "gemm_fp8_quantize_block128", "gemm_fp8_block128", "gemm_moe_few_tokens",
                     "gemm_tune_set", "gemm_tune_get",
                     "gemm_status_string", "gemm_last_cuda_error", "gemm_check", "gemm_watchdog_selftest",
                     "gemm_last_plan", "gemm_last_launch_count", "gemm_tc_rate_probe",
@@ -124,6 +126,10 @@ def lib():
             L.gemm_fp8_block128.argtypes = [c_int, c_int, c_int, c_float, c_void_p, c_int, c_ll, c_void_p, c_ll,
                                             c_void_p, c_int, c_ll, c_void_p, c_ll, c_int, c_int, c_float, c_void_p,
                                             c_int, c_ll, c_void_p, c_int, c_void_p]
+            L.gemm_moe_few_tokens.restype = c_int
+            L.gemm_moe_few_tokens.argtypes = [c_int, c_int, c_int, c_int, c_int, c_void_p, c_int, c_ll, c_void_p, c_int,
+                                              c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int,
+                                              c_int, c_void_p, c_int, c_ll, c_void_p, c_void_p, c_void_p]
             L.gemm_tune_set.restype = c_int
             L.gemm_tune_set.argtypes = [ctypes.POINTER(TuneEntry), c_int]
             L.gemm_tune_get.restype = c_int
@@ -507,6 +513,68 @@ def gemm_fp8(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=None, 
                                  _stream_handle(stream))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_block128")
+
+
+def moe_few_tokens(X, router, gate, up, down, Y, top_k: int, *, scales=None, act: int = GEMM_ACT_SILU,
+                   renormalize: bool = True, ids=None, weights=None, stream=None) -> None:
+    """Y = sum_j w_j down[e_j] @ (act(gate[e_j] @ x) * (up[e_j] @ x)) for every row x of X, in one launch.
+
+    X: (T, H) fp16 or bf16.  router: (E, H), X's type or fp32.  gate, up: (E, I, H), down: (E, H, I), contiguous,
+    X's type, or float8_e4m3fn with scales = (s_gate, s_up, s_down), one fp32 scale for each 128 x 128 block
+    ((E, ceil(I/128), ceil(H/128)) and (E, ceil(H/128), ceil(I/128)); fp8_quantize with layout "blocks", expert by
+    expert).  up=None: no gating, h = act(gate @ x).  Y: (T, H) fp32, fp16 or bf16.
+    The e_j are the top_k largest logits of router @ x (ties: the lower index); w_j their softmax probabilities,
+    divided by their sum with renormalize=True.  ids (int32) and weights (fp32), both (T, top_k) and contiguous,
+    receive them if given.  Limits: T <= 128, E <= 512, top_k <= 16, T * top_k <= 1024, H and I multiples of 16.
+    """
+    import torch
+    codes = _type_codes()
+    x_ptr, ldx, x_type = _typed_mat(X, "X", (GEMM_DTYPE_F16, GEMM_DTYPE_BF16))
+    y_ptr, ldy, y_type = _typed_mat(Y, "Y", _FLOATS)
+    r_ptr, ldr, r_type = _typed_mat(router, "router", _FLOATS)
+    T, H = X.shape
+    E = router.shape[0]
+    w_type = codes.get(getattr(gate, "dtype", None), -1)
+    if w_type != x_type and w_type != GEMM_DTYPE_E4M3:
+        raise TypeError("gate, up and down must have X's type or be float8_e4m3fn")
+    if r_type not in (x_type, GEMM_DTYPE_F32):
+        raise TypeError("router must have X's type or be float32")
+    I = gate.shape[1] if gate.dim() == 3 else -1
+    for t, name, shape in ((gate, "gate", (E, I, H)), (up, "up", (E, I, H)), (down, "down", (E, H, I))):
+        if t is None and name == "up":
+            continue
+        if not t.is_cuda or t.dtype != gate.dtype:
+            raise TypeError(f"{name} must be a CUDA {gate.dtype} tensor")
+        if t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous and {shape}, got {tuple(t.shape)}")
+    if Y.shape != X.shape or router.shape[1] != H or (E > 1 and ldr != H):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} router{tuple(router.shape)} Y{tuple(Y.shape)} (router contiguous)")
+    s_ptr = [None, None, None]
+    if w_type == GEMM_DTYPE_E4M3:
+        if scales is None or len(scales) != 3:
+            raise ValueError("8-bit weights need scales = (s_gate, s_up, s_down)")
+        hb, ib = (H + 127) // 128, (I + 127) // 128
+        for i, (t, shape) in enumerate(zip(scales, ((E, ib, hb), (E, ib, hb), (E, hb, ib)))):
+            if i == 1 and up is None:
+                continue
+            if not t.is_cuda or t.dtype != torch.float32:
+                raise TypeError("scales must be CUDA float32 tensors")
+            if t.shape != shape or not t.is_contiguous():
+                raise ValueError(f"scales[{i}] must be contiguous and {shape}, got {tuple(t.shape)}")
+            s_ptr[i] = t.data_ptr()
+    elif scales is not None:
+        raise ValueError("scales are for 8-bit weights only")
+    out = [None, None]
+    for i, (t, name, dt) in enumerate(((ids, "ids", torch.int32), (weights, "weights", torch.float32))):
+        if t is not None:
+            if not t.is_cuda or t.dtype != dt or t.shape != (T, top_k) or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous CUDA {dt} tensor of shape {(T, top_k)}")
+            out[i] = t.data_ptr()
+    st = lib().gemm_moe_few_tokens(T, E, top_k, H, I, x_ptr, x_type, ldx, r_ptr, r_type, gate.data_ptr(),
+                                   None if up is None else up.data_ptr(), down.data_ptr(), w_type, *s_ptr, act,
+                                   1 if renormalize else 0, y_ptr, y_type, ldy, *out, _stream_handle(stream))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_moe_few_tokens")
 
 
 def _vector(t, name, n):

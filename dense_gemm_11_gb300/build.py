@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(BUILD_DIR, "libgemm11.so")
 DEBUG_BUILD_DIR = os.path.join(HERE, "_build_debug")
 DEBUG_LIB_PATH = os.path.join(DEBUG_BUILD_DIR, "libgemm11_debug.so")
-SOURCES = ["api.cu", "sgemm.cu", "hgemm.cu", "probe.cu", "fp8_quant.cu", "fp8_gemm.cu"]
+SOURCES = ["api.cu", "sgemm.cu", "hgemm.cu", "probe.cu", "fp8_quant.cu", "fp8_gemm.cu", "moe.cu"]
 HEADERS = ["internal.h", "ptx.cuh", "fp8.h", "fp8.cuh", os.path.join("..", "..", "include", "gemm11.h")]
 
 NVCC_FLAGS = [

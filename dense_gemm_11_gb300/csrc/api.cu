@@ -84,6 +84,7 @@ struct ScratchEntry {
     size_t ncounters = 0;
     float *operands = nullptr;
     size_t operand_floats = 0;
+    bool captured = false;  // a CUDA graph holds the addresses of partials and counters
 };
 std::mutex g_scratch_mu;
 std::map<std::pair<int, uintptr_t>, ScratchEntry> g_scratch;
@@ -156,36 +157,77 @@ unsigned *watchdog_word() {
     return s ? s->watchdog : nullptr;
 }
 
+namespace {
+
+// While `stream` is being captured nothing may wait for it, and allocations
+// need the relaxed capture mode; the new buffer is cleared (bytes > 0) on a
+// stream of its own, outside the graph.
+cudaError_t scratch_alloc_capturing(void **user, size_t bytes, size_t clear) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
+    if (e != cudaSuccess) return e;
+    cudaStream_t side = nullptr;
+    e = scratch_alloc(user, bytes);
+    if (e == cudaSuccess && clear) {
+        e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
+        if (e == cudaSuccess) e = cudaMemsetAsync(*user, 0, clear, side);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(side);
+        if (side) cudaStreamDestroy(side);
+    }
+    (void)cudaThreadExchangeStreamCaptureMode(&mode);
+    return e;
+}
+
+bool is_capturing(cudaStream_t stream) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
+        (void)cudaGetLastError();  // the legacy stream while another one is captured
+        return false;
+    }
+    return st == cudaStreamCaptureStatusActive;
+}
+
+}  // namespace
+
 cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out) {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
+    const bool capturing = is_capturing(stream);
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     ScratchEntry &e = g_scratch[{dev, reinterpret_cast<uintptr_t>(stream)}];
+    // A buffer whose address a graph has keeps living: growing leaves it.
+    const bool keep_old = e.captured || capturing;
     if (e.partial_floats < partial_floats) {
         // Work already queued on this stream may still use the old buffer.
-        cudaError_t r = cudaStreamSynchronize(stream);
+        cudaError_t r = keep_old ? cudaSuccess : cudaStreamSynchronize(stream);
         if (r != cudaSuccess) return r;
-        scratch_free(e.partials);
+        if (!keep_old) scratch_free(e.partials);
         e.partials = nullptr;
         e.partial_floats = 0;
         size_t want = partial_floats + partial_floats / 4;
-        r = scratch_alloc(reinterpret_cast<void **>(&e.partials), want * sizeof(float));
+        void **at = reinterpret_cast<void **>(&e.partials);
+        r = capturing ? scratch_alloc_capturing(at, want * sizeof(float), 0) : scratch_alloc(at, want * sizeof(float));
         if (r != cudaSuccess) return r;
         e.partial_floats = want;
     }
     if (e.ncounters < ncounters) {
-        cudaError_t r = cudaStreamSynchronize(stream);
+        cudaError_t r = keep_old ? cudaSuccess : cudaStreamSynchronize(stream);
         if (r != cudaSuccess) return r;
-        scratch_free(e.counters);
+        if (!keep_old) scratch_free(e.counters);
         e.counters = nullptr;
         e.ncounters = 0;
         size_t want = ncounters < 1024 ? 1024 : ncounters + ncounters / 4;
-        r = scratch_alloc(reinterpret_cast<void **>(&e.counters), want * sizeof(unsigned));
-        if (r != cudaSuccess) return r;
-        r = cudaMemset(e.counters, 0, want * sizeof(unsigned));
+        void **at = reinterpret_cast<void **>(&e.counters);
+        if (capturing) {
+            r = scratch_alloc_capturing(at, want * sizeof(unsigned), want * sizeof(unsigned));
+        } else {
+            r = scratch_alloc(at, want * sizeof(unsigned));
+            if (r == cudaSuccess) r = cudaMemset(e.counters, 0, want * sizeof(unsigned));
+        }
         if (r != cudaSuccess) return r;
         e.ncounters = want;
     }
+    e.captured = e.captured || capturing;
     out->partials = e.partials;
     out->counters = e.counters;
     return cudaSuccess;
@@ -647,6 +689,63 @@ int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_typ
     CallInfo info;
     const cudaError_t e = product ? run_fp8_gemm(g, s, &info) : run_fp8_scale_c(g, s, &info);
     if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, int x_type, long long ldx,
+                        const void *router, int router_type, const void *gate, const void *up, const void *down,
+                        int w_type, const float *s_gate, const float *s_up, const float *s_down, int act,
+                        int renormalize, void *Y, int y_type, long long ldy, int *ids, float *weights, void *stream) {
+    static_assert(kActSilu == GEMM_ACT_SILU, "activation codes");
+    if (T < 0 || E < 0 || H < 0 || I < 0 || (renormalize != 0 && renormalize != 1)) return GEMM_ERR_INVALID_ARG;
+    if (!valid_act(act) && act != GEMM_ACT_SILU) return GEMM_ERR_INVALID_ARG;
+    if (x_type != GEMM_DTYPE_F16 && x_type != GEMM_DTYPE_BF16) return GEMM_ERR_INVALID_ARG;
+    if (router_type != GEMM_DTYPE_F32 && router_type != x_type) return GEMM_ERR_INVALID_ARG;
+    if (w_type != x_type && w_type != GEMM_DTYPE_E4M3) return GEMM_ERR_INVALID_ARG;
+    if (y_type != GEMM_DTYPE_F32 && y_type != GEMM_DTYPE_F16 && y_type != GEMM_DTYPE_BF16) return GEMM_ERR_INVALID_ARG;
+    if (ldx < std::max(1, H) || ldy < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return noop();
+    if (E < 1 || I < 1 || top_k < 1 || top_k > E) return GEMM_ERR_INVALID_ARG;
+    if (!X || !router || !gate || !down || !Y) return GEMM_ERR_INVALID_ARG;
+    const bool fp8 = w_type == GEMM_DTYPE_E4M3;
+    if (fp8 && (!s_gate || !s_down || (up && !s_up))) return GEMM_ERR_INVALID_ARG;
+    auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+    const bool ok = top_k <= kMoeMaxTopK && E <= kMoeMaxExperts && T <= kMoeMaxTokens && T * top_k <= kMoeMaxSlots &&
+                    H % 16 == 0 && I % 16 == 0 && al16(X) && al16(router) && al16(gate) && al16(up) && al16(down) &&
+                    (T == 1 || ldx % 8 == 0);
+    if (!ok) return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    Moe m;
+    m.T = T;
+    m.E = E;
+    m.top_k = top_k;
+    m.H = H;
+    m.I = I;
+    m.X = X;
+    m.x_type = x_type;
+    m.ldx = ldx;
+    m.router = router;
+    m.router_type = router_type;
+    m.gate = gate;
+    m.up = up;
+    m.down = down;
+    m.w_type = w_type;
+    m.s_gate = s_gate;
+    m.s_up = s_up;
+    m.s_down = s_down;
+    m.Y = Y;
+    m.y_type = y_type;
+    m.ldy = ldy;
+    m.act = act;
+    m.renorm = renormalize;
+    m.ids = ids;
+    m.weights = weights;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_moe(m, s, &info);
     if (e != cudaSuccess) return fail_cuda(e);
     return finish_call(info, s);
 }

@@ -68,4 +68,26 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
 // The same with no product (K == 0 or alpha == 0): C = act(beta * C + bias).
 cudaError_t run_fp8_scale_c(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
 
+// ---- mixture of experts for a few tokens (moe.cu) ----
+constexpr int kMoeMaxTokens = 128, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxSlots = 1024;
+constexpr int kActSilu = 4;  // the C ABI's GEMM_ACT_SILU
+struct Moe {
+    int T = 0, E = 0, top_k = 0, H = 0, I = 0;
+    const void *X = nullptr;  // T x H
+    int x_type = 0;
+    long long ldx = 0;
+    const void *router = nullptr;  // E x H
+    int router_type = 0;
+    const void *gate = nullptr, *up = nullptr, *down = nullptr;  // E x I x H, E x I x H (or NULL), E x H x I
+    int w_type = 0;
+    const float *s_gate = nullptr, *s_up = nullptr, *s_down = nullptr;  // 128 x 128 scales of 8-bit weights
+    void *Y = nullptr;  // T x H
+    int y_type = 0;
+    long long ldy = 0;
+    int act = 0, renorm = 0;
+    int *ids = nullptr;  // T x top_k, or NULL
+    float *weights = nullptr;
+};
+cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info);
+
 }  // namespace gemm11

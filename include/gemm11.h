@@ -82,7 +82,8 @@ typedef enum {
     GEMM_ACT_NONE = 0,      /* identity */
     GEMM_ACT_GELU = 1,      /* exact GELU: x * Phi(x) = 0.5 * x * (1 + erf(x / sqrt(2))) */
     GEMM_ACT_RELU = 2,      /* max(x, 0) */
-    GEMM_ACT_GELU_TANH = 3  /* 0.5 * x * (1 + tanh(sqrt(2/pi) * (x + 0.044715 * x^3))) */
+    GEMM_ACT_GELU_TANH = 3, /* 0.5 * x * (1 + tanh(sqrt(2/pi) * (x + 0.044715 * x^3))) */
+    GEMM_ACT_SILU = 4       /* x / (1 + exp(-x)) (gemm_moe_few_tokens only) */
 } gemm_act;
 
 /* Element types of the tensor-core entry point gemm_tc_f32acc_epilogue. */
@@ -327,6 +328,43 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
                                  const float *SA, long long ldsa, const void *B, int b_type, long long ldb,
                                  const float *SB, long long ldsb, int b_trans, int b_layout, float beta, void *C,
                                  int c_type, long long ldc, const float *bias, int act, void *stream);
+
+/*
+ * gemm_moe_few_tokens -- a whole mixture-of-experts feed-forward layer for a
+ * few tokens (a decode step), one kernel launch.  For each row x of X (T x H):
+ *   logits = Wr x,  p = softmax(logits),  e_1 .. e_k the top_k experts with the
+ *   largest logits (equal logits: the lower index first),
+ *   w_j = p[e_j], or p[e_j] / sum_i p[e_i] with renormalize = 1,
+ *   h_j = act(Wgate[e_j] x) * (Wup[e_j] x), or act(Wgate[e_j] x) without Wup,
+ *   y   = round_y( sum_j w_j Wdown[e_j] h_j ).
+ *   X       T x H, FP16 or BF16 (x_type), ldx elements a row.
+ *   router  E x H contiguous, FP32 or x_type.
+ *   gate, up  E x I x H contiguous, down E x H x I contiguous, all of w_type:
+ *           x_type, or GEMM_DTYPE_E4M3 with one FP32 scale for each 128 x 128
+ *           block of every expert's matrix (GEMM_FP8_BLOCKS; s_gate and s_up
+ *           E x ceil(I/128) x ceil(H/128), s_down E x ceil(H/128) x ceil(I/128)).
+ *           up (and s_up) may be NULL: a layer without a gate.
+ *   Y       T x H, FP32, FP16 or BF16 (y_type), ldy elements a row.
+ *   act     any gemm_act.
+ *   ids     T x top_k int, weights T x top_k float: the choice and the w_j in
+ *           the order of the logits; either may be NULL.
+ * Sums, the softmax and the logits are FP32; h is rounded once, to TF32.  A
+ * token with a NaN logit gets NaN weights, and so a NaN row.
+ * Limits: 1 <= top_k <= min(E, 16), E <= 512, T <= 128, T * top_k <= 1024;
+ * H and I multiples of 16; X, router, gate, up and down 16-byte aligned and
+ * ldx a multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
+ * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
+ * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive
+ * otherwise.  Scratch: T E + T top_k (H + I) floats of library-owned device
+ * memory per stream.  A call under stream capture may allocate it, and a graph
+ * keeps the scratch it was captured with: replays of it must not overlap on
+ * the GPU with each other or with calls on the stream that it was captured on.
+ */
+GEMM11_API int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, int x_type, long long ldx,
+                                   const void *router, int router_type, const void *gate, const void *up,
+                                   const void *down, int w_type, const float *s_gate, const float *s_up,
+                                   const float *s_down, int act, int renormalize, void *Y, int y_type, long long ldy,
+                                   int *ids, float *weights, void *stream);
 
 /*
  * Tuned plans.  The planners pick a kernel family, tile width and split-K

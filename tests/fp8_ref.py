@@ -69,3 +69,33 @@ def product(A, SA, B, SB, b_trans, b_scales, alpha=1.0, beta=0.0, C=None, bias=N
     if bias is not None:
         v = v + bias.double()
     return act64(v, act), S
+
+
+def moe(X, router, gate, up, down, top_k, scales=None, act=4, renormalize=True):
+    """(y, ids, weights, per-element error scale of y) in float64."""
+    x = X.double().cpu()
+    E = router.shape[0]
+    logits = x @ router.double().cpu().t()
+    T = x.shape[0]
+    order = np.lexsort((np.broadcast_to(np.arange(E), (T, E)), -logits.numpy()), axis=1)[:, :top_k]
+    ids = torch.from_numpy(np.ascontiguousarray(order))
+    p = torch.softmax(logits, dim=1)
+    w = p.gather(1, ids)
+    if renormalize:
+        w = w / w.sum(dim=1, keepdim=True)
+
+    def matrix(m, i, e):
+        return m[e].double().cpu() if scales is None else dequantize(m[e], scales[i][e], "blocks").cpu()
+
+    y, S = torch.zeros_like(x), torch.zeros_like(x)
+    for e in range(E):
+        t, j = (ids == e).nonzero(as_tuple=True)
+        if not len(t):
+            continue
+        h = act64(x[t] @ matrix(gate, 0, e).t(), act)
+        if up is not None:
+            h = h * (x[t] @ matrix(up, 1, e).t())
+        d = matrix(down, 2, e)
+        y.index_add_(0, t, (h @ d.t()) * w[t, j][:, None])
+        S.index_add_(0, t, (h.abs() @ d.abs().t()) * w[t, j][:, None])
+    return y, ids, w, S

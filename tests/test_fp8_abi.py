@@ -64,3 +64,32 @@ def test_fp8_empty_strides():
         Q, S = g.fp8_empty(130, 257, layout, device="cpu")
         assert (Q.shape, S.shape) == tuple(map(torch.Size, g._fp8_shapes(130, 257, layout)))
         assert Q.stride(0) % 16 == 0 and S.stride(0) % 4 == 0 and Q.dtype == torch.float8_e4m3fn
+
+
+MOE = dict(T=4, E=8, top_k=2, H=256, I=128, X=FAKE, x_type=g.GEMM_DTYPE_BF16, ldx=256, router=FAKE, router_type=g.GEMM_DTYPE_BF16,
+           gate=FAKE, up=FAKE, down=FAKE, w_type=E4, s_gate=FAKE, s_up=FAKE, s_down=FAKE, act=g.GEMM_ACT_SILU, renormalize=1,
+           Y=FAKE, y_type=g.GEMM_DTYPE_BF16, ldy=256, ids=None, weights=None, stream=None)
+
+
+@pytest.mark.parametrize("change", [
+    dict(T=-1), dict(E=-1), dict(E=0), dict(H=-1), dict(I=-1), dict(I=0), dict(top_k=0), dict(top_k=9), dict(x_type=0), dict(x_type=E4),
+    dict(router_type=g.GEMM_DTYPE_F16), dict(w_type=g.GEMM_DTYPE_F16), dict(w_type=E5), dict(y_type=E4), dict(act=5), dict(act=-1),
+    dict(renormalize=2), dict(ldx=255), dict(ldy=255), dict(X=None), dict(router=None), dict(gate=None), dict(down=None),
+    dict(Y=None), dict(s_gate=None), dict(s_up=None), dict(s_down=None),
+])
+def test_moe_rejects(L, change):
+    assert L.gemm_moe_few_tokens(*{**MOE, **change}.values()) == g.GEMM_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("change", [
+    dict(T=129), dict(E=513), dict(E=32, top_k=17), dict(T=128, top_k=16, E=64), dict(H=264, ldx=264, ldy=264), dict(I=120),
+    dict(X=FAKE + 2), dict(router=FAKE + 2), dict(gate=FAKE + 1), dict(up=FAKE + 1), dict(down=FAKE + 8), dict(ldx=257),
+])
+def test_moe_does_not_support(L, change):
+    assert L.gemm_moe_few_tokens(*{**MOE, **change}.values()) == g.GEMM_ERR_UNSUPPORTED
+
+
+def test_moe_empty(L):
+    for change in (dict(T=0), dict(H=0)):
+        assert L.gemm_moe_few_tokens(*{**MOE, **dict(X=None, Y=None), **change}.values()) == g.GEMM_OK
+        assert g.last_launch_count() == 0
