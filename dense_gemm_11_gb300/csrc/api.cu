@@ -713,7 +713,7 @@ int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, in
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool ok = top_k <= kMoeMaxTopK && E <= kMoeMaxExperts && T <= kMoeMaxTokens && T * top_k <= kMoeMaxSlots &&
                     H % 16 == 0 && I % 16 == 0 && al16(X) && al16(router) && al16(gate) && al16(up) && al16(down) &&
-                    (T == 1 || ldx % 8 == 0);
+                    (T == 1 || ldx % 8 == 0) && static_cast<long long>(E) * std::max(H, I) < (1LL << 31);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
@@ -746,6 +746,7 @@ int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     CallInfo info;
     const cudaError_t e = run_moe(m, s, &info);
+    if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
     if (e != cudaSuccess) return fail_cuda(e);
     return finish_call(info, s);
 }

@@ -21,6 +21,10 @@ constexpr int kTypeE5M2 = 4;
 // row_bytes apart; false when the encoder is missing or refuses.
 bool encode_matrix_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
+// The same with a third dimension (rows row_bytes, its steps step_bytes apart)
+// and the 128-byte swizzle.
+bool encode_box_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows, uint64_t steps,
+                    uint64_t row_bytes, uint64_t step_bytes, uint32_t box_inner, uint32_t box_rows, uint32_t box_steps);
 
 // ---- quantizer (fp8_quant.cu) ----
 struct Fp8Quant {

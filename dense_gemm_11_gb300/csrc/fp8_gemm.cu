@@ -430,6 +430,18 @@ bool encode_matrix_map(CUtensorMap *map, CUtensorMapDataType dt, const void *bas
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_box_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t rows, uint64_t steps,
+                    uint64_t row_bytes, uint64_t step_bytes, uint32_t box_inner, uint32_t box_rows, uint32_t box_steps) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {inner, rows, steps};
+    cuuint64_t strides[2] = {row_bytes, step_bytes};
+    cuuint32_t box[3] = {box_inner, box_rows, box_steps};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, dt, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) {
     Fp8Args a = fp8_args(g);
     const int bn = g.M <= 16 ? 16 : g.M <= 32 ? 32 : g.M <= 64 ? 64 : 128;

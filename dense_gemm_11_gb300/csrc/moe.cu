@@ -9,24 +9,27 @@
 // read once and used for one to a few products each, so the layer takes as
 // long as those bytes do.  The kernel is persistent (one CTA per SM, launched
 // cooperatively) and built as one stream of weight bytes:
-//   * work is cut into units of 16 matrix rows (8 gate rows with the 8 up rows
-//     they meet, or 16 rows of the down projection) for one expert and up to
-//     8 NT of its tokens.  Units are small so that they spread evenly;
-//   * a producer warp copies each unit's rows and its tokens' activations in
-//     chunks (1 KB of every row) into a ring of stages with bulk copies.  It
-//     runs ahead of the arithmetic across units, and into the down projection
-//     while the other CTAs still finish the first half;
-//   * eight warps share a chunk's k; each multiplies its 16 x (K / 8) slice by
-//     the tokens with mma.sync and the eight partial tiles are added in warp
-//     order in shared memory.  The matrix instruction is the warp-level one:
-//     a unit has 1 to 8 NT columns of 128-column tcgen05 tiles and is bound by
-//     memory, and fragments come straight from the row-major chunk (the k of a
-//     fragment may be any permutation that both operands share, so that a
-//     thread's k's are 8 neighbours, one 16-byte load).
-// Between the phases (router, first half, down projection) CTAs meet at two
-// grid barriers; the last unit of a row group to finish adds the experts'
-// contributions of its 16 columns in slot order, so results do not depend on
-// timing.  Every wait is bounded.
+//   * work is cut into units of 16 WR matrix rows (gate rows with the up rows
+//     they meet, or rows of the down projection) for one expert and up to 8 NT
+//     of its tokens.  A unit goes through its k in stages of 16 KB of weights:
+//     16 WR rows x 8 / WR boxes of 128 bytes, one TMA copy (two with a gate);
+//   * a producer warp fills a ring of stages.  It runs ahead of the arithmetic
+//     across units, and into the down projection while the other CTAs still
+//     finish the first half;
+//   * eight warps take a stage's WR row groups x 8 / WR boxes, one each, and
+//     multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
+//     share rows add their sums in warp order in shared memory at the unit's
+//     end.  The matrix instruction is the warp-level one: a unit has 1 to 8 NT
+//     columns of a 128-column tcgen05 tile and is bound by memory, and
+//     fragments come straight from the row-major rows (the k of a fragment may
+//     be any permutation that both operands share, so that a thread's k's are
+//     neighbours, one 16-byte load).
+// Few row groups (WR = 1) make many small units, which spread evenly over the
+// SMs; many (WR = 8) read a token's activations once for 128 rows and leave no
+// sums to add.  The host takes the largest WR whose units still spread well.
+// Between the phases (router, first half, down projection, sum over a token's
+// experts) CTAs meet at grid barriers; every sum has a fixed order, so results
+// do not depend on timing.  Every wait is bounded.
 //
 // Numbers: weights and tokens of the same 16-bit type multiply exactly in
 // mma.sync's native type; 8-bit weights and the down projection use TF32,
@@ -35,6 +38,8 @@
 // either bits or range).
 #include <algorithm>
 #include <cstdint>
+
+#include <cmath>
 
 #include <cuda_fp8.h>
 
@@ -46,8 +51,8 @@ namespace {
 
 constexpr int kWarps = 8;                       // consumer warps
 constexpr int kMoeThreads = 32 * (kWarps + 1);  // and the producer warp
-constexpr int kRows = 16;                       // matrix rows of a unit
-constexpr int kMaxStages = 16;
+constexpr int kStageWeights = 16384;            // bytes of weights in a stage
+constexpr int kMaxStages = 12;
 
 struct MoeArgs {
     int T, E, top_k, H, I;
@@ -62,10 +67,13 @@ struct MoeArgs {
     int y_type, act, renorm;
     int *ids;
     float *weights;
-    float *logits, *hidden, *part;  // scratch: T x E, slots x I, slots x H
-    unsigned *counters;             // 0..2: barriers and exit; 4..: row groups of the down projection
+    float *logits, *hidden, *part;  // scratch: T x E, slots x I, k_splits x slots x H
+    unsigned *counters;             // three barriers and the exit
     unsigned *err;
-    int stages, stage_bytes, tok_rows;
+    int wr1, wr2;    // row groups (of 16 rows) of a unit in the first half and in the down projection
+    int k_splits;    // units of the down projection that share a row group's k
+    int flat_h, flat_i;  // rows of H (I) elements are whole 128-byte boxes: one copy takes a stage's boxes
+    int stages, stage_bytes;
 };
 
 // Shared-memory tables of the routing, the same in every CTA.
@@ -137,11 +145,21 @@ __device__ __forceinline__ float moe_act(int act, float v) {
 
 // Eight neighbouring values of a row as floats.
 __device__ __forceinline__ void widen8(const uint4 &w, int type, float (&v)[8]) { unpack8_out16(w, type, v); }
-__device__ __forceinline__ void widen8_e4m3(const uint2 &w, float (&v)[8]) {
+__device__ __forceinline__ void widen4(uint32_t lo, uint32_t hi, int type, float (&v)[4]) {
+    if (type == kOutF16) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    } else {
+        v[0] = __uint_as_float(lo << 16), v[1] = __uint_as_float(lo & 0xFFFF0000u);
+        v[2] = __uint_as_float(hi << 16), v[3] = __uint_as_float(hi & 0xFFFF0000u);
+    }
+}
+// N e4m3 values, four in a word, as floats.
+template <int N>
+__device__ __forceinline__ void widen_e4m3(const uint32_t *w, float *v) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t u = i < 2 ? w.x : w.y;
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(u >> (16 * (i & 1))), __NV_E4M3);
+    for (int i = 0; i < N / 2; ++i) {
+        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
         const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
@@ -292,138 +310,146 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
 
 // ---------------------------------------------------------------- units
 struct Unit {
-    int expert, rg, pair, start, count;
+    int expert, row, start, count;  // first matrix row (of the expert), first slot in `order`, tokens
+    int ch0, ch1, split;            // stages
 };
 // Unit u of the first half: the token groups of an expert next to each other
 // for the same rows, so that they share the rows' bytes in L2.
-__device__ __forceinline__ Unit first_unit(const Routing &r, int u, int row_groups) {
+__device__ __forceinline__ Unit first_unit(const Routing &r, int u, int row_groups, int rows, int stages) {
     Unit n;
     const int p0 = u / row_groups, first = r.pair_first[p0], groups = r.pair_groups[p0];
     const int i = u - first * row_groups;
-    n.rg = i / groups;
-    n.pair = first + i % groups;
-    n.expert = r.pair_expert[n.pair];
-    n.start = r.pair_start[n.pair];
-    n.count = r.pair_count[n.pair];
+    const int pair = first + i % groups;
+    n.row = i / groups * rows;
+    n.expert = r.pair_expert[pair];
+    n.start = r.pair_start[pair];
+    n.count = r.pair_count[pair];
+    n.ch0 = 0;
+    n.ch1 = stages;
+    n.split = 0;
     return n;
 }
 // Unit u of the down projection: row group by row group.
-__device__ __forceinline__ Unit down_unit(const Routing &r, int u) {
+__device__ __forceinline__ Unit down_unit(const Routing &r, int u, int rows, int stages, int splits) {
     Unit n;
-    n.rg = u / r.pairs;
-    n.pair = u % r.pairs;
-    n.expert = r.pair_expert[n.pair];
-    n.start = r.pair_start[n.pair];
-    n.count = r.pair_count[n.pair];
+    n.split = u % splits;
+    u /= splits;
+    const int pair = u % r.pairs;
+    n.row = u / r.pairs * rows;
+    n.expert = r.pair_expert[pair];
+    n.start = r.pair_start[pair];
+    n.count = r.pair_count[pair];
+    n.ch0 = stages * n.split / splits;
+    n.ch1 = stages * (n.split + 1) / splits;
     return n;
 }
 
 template <bool FP8>
 struct MoeCfg {
     static constexpr int kWBytes = FP8 ? 1 : 2;
-    static constexpr int kKC = 1024 / kWBytes;         // k of a chunk
-    static constexpr int kKW = kKC / kWarps;           // of one warp: 128 (one scale block) or 64
-    // Row strides in shared memory that keep the fragment loads free of bank
-    // conflicts: a quarter warp reads 2 rows x 64 bytes (16-bit weights and
-    // tokens) or 4 x 16 bytes of 2 rows (FP32 activations), half a warp 4 rows
-    // x 32 bytes (8-bit weights).
-    static constexpr int kWStride = 1024 + (FP8 ? 32 : 64);
-    static constexpr int kXStride = kKC * 2 + 64;
-    static constexpr int kHStride = kKC * 4 + 16;
+    static constexpr int kBoxK = 128 / kWBytes;  // k of a box: 128 (one scale block) or 64
     static constexpr int kScaleBytes = FP8 ? 2 * kWarps * 4 : 0;
-    static constexpr int kActOffset = kRows * kWStride + kScaleBytes;
+    static constexpr int kActOffset = kStageWeights + kScaleBytes;
+    // Row strides of the activations: 4 neighbouring 16-byte pieces of 2
+    // tokens (a quarter warp's load) fall on different banks.
+    static constexpr int kXPad = FP8 ? 32 : 16, kHPad = FP8 ? 64 : 32;
+    static constexpr int act_stride(int wr, bool first) {
+        return 8 / wr * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
+    }
 };
 
-// The 16 rows x this warp's k of one chunk times the tokens, added to acc.
-// FIRST: tokens are X rows of 16 bits, else FP32 h rows.  valid: k's of the
-// chunk that exist.
+// This warp's 16 rows x one box of k times the tokens, added to acc.  Thread
+// (g, t) has rows g and g + 8 (w0, w1: their 128 bytes, 16-byte chunk c at
+// c ^ g by the copy's swizzle) at the k of chunks 2 t + s, and token 8 n + g at
+// the same k.  FIRST: tokens are X rows of 16 bits, else FP32 h rows, of
+// `valid` k's.  Where a chunk is two or four pieces of activations, the threads
+// take them in an order turned by t (no bank conflicts), and their weights with
+// them.
 template <int XT, bool FP8, int NT, bool FIRST>
-__device__ __forceinline__ void multiply_chunk(const uint8_t *stage, int valid, int count, float (&acc)[NT][4]) {
+__device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *act, int stride, int valid,
+                                             int count, float (&c)[NT][4]) {
     using Cfg = MoeCfg<FP8>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int k_warp = warp * Cfg::kKW;
-    if (k_warp >= valid) return;
-    float sum[NT][4];
-    float(&c)[NT][4] = FP8 ? sum : acc;
-    if (FP8) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    constexpr int kChunkK = 16 / Cfg::kWBytes;           // k of a 16-byte chunk: 16 or 8
+    constexpr int kPieceK = FIRST ? 8 : 4;               // k of a 16-byte piece of activations
+    constexpr int kPieces = kChunkK / kPieceK;           // 1, 2 or 4
+    constexpr int kActBytes = FIRST ? 2 : 4;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
-    }
-#pragma unroll
-    for (int s = 0; s < Cfg::kKW / 32; ++s) {
-        const int k = k_warp + s * 32 + t * 8;
-        const bool in = k < valid;
-        const uint8_t *w0 = stage + g * Cfg::kWStride + k * Cfg::kWBytes, *w1 = w0 + 8 * Cfg::kWStride;
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        if constexpr (!FP8 && FIRST) {
-            const uint4 a = in ? *reinterpret_cast<const uint4 *>(w0) : zero;
-            const uint4 b = in ? *reinterpret_cast<const uint4 *>(w1) : zero;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n * 8 >= count) break;
-                const uint4 x = in && n * 8 + g < count ? *reinterpret_cast<const uint4 *>(stage + Cfg::kActOffset + (n * 8 + g) * Cfg::kXStride + k * 2) : zero;
-                mma_16bit<XT>(c[n], a.x, b.x, a.y, b.y, x.x, x.y);
-                mma_16bit<XT>(c[n], a.z, b.z, a.w, b.w, x.z, x.w);
-            }
-        } else {
-            float wa[8], wb[8];
-            if constexpr (FP8) {
-                const uint2 z2 = make_uint2(0, 0);
-                widen8_e4m3(in ? *reinterpret_cast<const uint2 *>(w0) : z2, wa);
-                widen8_e4m3(in ? *reinterpret_cast<const uint2 *>(w1) : z2, wb);
-            } else {
-                widen8(in ? *reinterpret_cast<const uint4 *>(w0) : zero, XT, wa);
-                widen8(in ? *reinterpret_cast<const uint4 *>(w1) : zero, XT, wb);
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if (n * 8 >= count) break;
-                const bool tok = in && n * 8 + g < count;
-                float x[8];
-                if constexpr (FIRST) {
-                    widen8(tok ? *reinterpret_cast<const uint4 *>(stage + Cfg::kActOffset + (n * 8 + g) * Cfg::kXStride + k * 2) : zero, XT, x);
-                } else {
-                    const float4 *h = reinterpret_cast<const float4 *>(stage + Cfg::kActOffset + (n * 8 + g) * Cfg::kHStride + k * 4);
-                    const float4 z4 = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4 h0 = tok ? h[0] : z4, h1 = tok ? h[1] : z4;
-                    x[0] = h0.x, x[1] = h0.y, x[2] = h0.z, x[3] = h0.w, x[4] = h1.x, x[5] = h1.y, x[6] = h1.z, x[7] = h1.w;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a[4] = {wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1]};
-                    mma_tf32(c[n], a, x[2 * i], x[2 * i + 1]);
-                }
-            }
+    for (int s = 0; s < 2; ++s) {
+        const int chunk = 2 * t + s;
+        uint4 a = *reinterpret_cast<const uint4 *>(w0 + ((chunk ^ g) << 4));
+        uint4 b = *reinterpret_cast<const uint4 *>(w1 + ((chunk ^ g) << 4));
+        const int turn = kPieces == 4 ? t : kPieces == 2 ? t >> 1 : 0;
+        if constexpr (kPieces == 2) {
+            if (turn) a = make_uint4(a.z, a.w, a.x, a.y), b = make_uint4(b.z, b.w, b.x, b.y);
         }
-    }
-    if (FP8) {
-        const float *sc = reinterpret_cast<const float *>(stage + kRows * Cfg::kWStride);
-        const float s0 = sc[warp], s1 = sc[kWarps + warp];
+        if constexpr (kPieces == 4) {
+            if (turn & 1) a = make_uint4(a.y, a.x, a.w, a.z), b = make_uint4(b.y, b.x, b.w, b.z);
+            if (turn & 2) a = make_uint4(a.z, a.w, a.x, a.y), b = make_uint4(b.z, b.w, b.x, b.y);
+        }
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            acc[n][0] = fmaf(s0, sum[n][0], acc[n][0]);
-            acc[n][1] = fmaf(s0, sum[n][1], acc[n][1]);
-            acc[n][2] = fmaf(s1, sum[n][2], acc[n][2]);
-            acc[n][3] = fmaf(s1, sum[n][3], acc[n][3]);
+        for (int j = 0; j < kPieces; ++j) {
+            const int k = chunk * kChunkK + (j ^ turn) * kPieceK;
+            uint4 x[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                x[n] = k < valid && n * 8 + g < count ? *reinterpret_cast<const uint4 *>(act + (n * 8 + g) * stride + k * kActBytes) : zero;
+            if constexpr (!FP8 && FIRST) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma_16bit<XT>(c[n], aw[0], bw[0], aw[1], bw[1], x[n].x, x[n].y);
+                    mma_16bit<XT>(c[n], aw[2], bw[2], aw[3], bw[3], x[n].z, x[n].w);
+                }
+            } else {
+                float wa[kPieceK], wb[kPieceK];
+                if constexpr (FP8 && FIRST) {
+                    widen_e4m3<8>(&aw[2 * j], wa);
+                    widen_e4m3<8>(&bw[2 * j], wb);
+                } else if constexpr (FP8) {
+                    widen_e4m3<4>(&aw[j], wa);
+                    widen_e4m3<4>(&bw[j], wb);
+                } else {
+                    widen4(aw[2 * j], aw[2 * j + 1], XT, wa);
+                    widen4(bw[2 * j], bw[2 * j + 1], XT, wb);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float xf[8];
+                    if constexpr (FIRST)
+                        widen8(x[n], XT, xf);
+                    else
+                        xf[0] = __uint_as_float(x[n].x), xf[1] = __uint_as_float(x[n].y), xf[2] = __uint_as_float(x[n].z),
+                        xf[3] = __uint_as_float(x[n].w);
+#pragma unroll
+                    for (int i = 0; i < kPieceK / 2; ++i) {
+                        const float f[4] = {wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1]};
+                        mma_tf32(c[n], f, xf[2 * i], xf[2 * i + 1]);
+                    }
+                }
+            }
         }
     }
 }
 
-template <int XT, bool FP8, int NT, bool GATED>
-__global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeArgs p) {
+template <int XT, bool FP8, int NT>
+__global__ void __launch_bounds__(kMoeThreads, 1)
+    moe_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
+               const __grid_constant__ CUtensorMap tm_down, const MoeArgs p) {
     using Cfg = MoeCfg<FP8>;
-    extern __shared__ __align__(128) uint8_t ring[];
+    extern __shared__ uint8_t ring_raw[];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Routing r;
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ float red[2][kWarps][NT][4][32];
     __shared__ volatile int abort_flag;
-    __shared__ int last;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kUnitRows1 = GATED ? 8 : 16;  // rows of h of a unit
-    const int rg1 = p.I / kUnitRows1, rg2 = p.H / kRows;
-    const int nch1 = (p.H + Cfg::kKC - 1) / Cfg::kKC, nch2 = (p.I + Cfg::kKC - 1) / Cfg::kKC;
+    const bool gated = p.up != nullptr;
+    const int rows1 = (gated ? 8 : 16) * p.wr1, rows2 = 16 * p.wr2;  // rows of h and of y of a unit
+    const int rg1 = (p.I + rows1 - 1) / rows1, rg2 = (p.H + rows2 - 1) / rows2;
+    const int kc1 = 8 / p.wr1 * Cfg::kBoxK, kc2 = 8 / p.wr2 * Cfg::kBoxK;  // k of a stage
+    const int nch1 = (p.H + kc1 - 1) / kc1, nch2 = (p.I + kc2 - 1) / kc2;
 
     auto give_up = [&] {
         abort_flag = 1;
@@ -436,6 +462,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeArgs p) {
         }
         abort_flag = 0;
         fence_mbarrier_init();
+        tma_prefetch_desc(&tm_gate);
+        tma_prefetch_desc(&tm_up);
+        tma_prefetch_desc(&tm_down);
     }
     __syncthreads();
 
@@ -458,82 +487,82 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeArgs p) {
     }
     fence_proxy_async_smem();  // the ring held the keys
     __syncthreads();
-    const int units1 = r.pairs * rg1, units2 = r.pairs * rg2;
+    const int units1 = r.pairs * rg1, units2 = r.pairs * rg2 * p.k_splits;
     if (blockIdx.x == 0)
         for (int s = threadIdx.x; s < p.T * p.top_k && r.pairs; s += kMoeThreads) {
             if (p.ids) p.ids[s] = r.expert[s];
             if (p.weights) p.weights[s] = r.weight[s];
         }
     // CTAs that had one unit less in the first half begin the second.
-    const int shift = (blockIdx.x + gridDim.x - units1 % gridDim.x) % gridDim.x;
+    const int grid = gridDim.x;
+    const int shift = (static_cast<int>(blockIdx.x) + grid - units1 % grid) % grid;
 
     if (warp == kWarps) {
         // ------------------------------------------------ producer
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
-        const long long hi_bytes = static_cast<long long>(p.H) * Cfg::kWBytes, i_bytes = static_cast<long long>(p.I) * Cfg::kWBytes;
-        // Takes a free stage and starts the copies of a chunk's weight rows.
-        auto load_rows = [&](bool first, const Unit &n, int ch) {
+        // Takes a free stage and starts the copies of its weights.
+        auto load_weights = [&](bool first, const Unit &n, int ch) {
             if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u))) {
                 if (lane == 0) give_up();
                 ok = false;
                 return;
             }
             uint8_t *dst = ring + static_cast<size_t>(stage) * p.stage_bytes;
-            const int k0 = ch * Cfg::kKC, k = min(Cfg::kKC, (first ? p.H : p.I) - k0);
-            if (lane == 0)
-                mbar_arrive_expect_tx(&full[stage], kRows * k * Cfg::kWBytes + n.count * k * (first ? 2 : 4));
-            __syncwarp();
-            if (lane < kRows) {
-                const uint8_t *base;
-                long long row;
-                if (first) {
-                    const bool is_up = GATED && lane >= 8;
-                    base = static_cast<const uint8_t *>(is_up ? p.up : p.gate);
-                    row = static_cast<long long>(n.expert) * p.I + n.rg * kUnitRows1 + (GATED ? lane & 7 : lane);
-                    base += row * hi_bytes;
-                } else {
-                    row = static_cast<long long>(n.expert) * p.H + n.rg * kRows + lane;
-                    base = static_cast<const uint8_t *>(p.down) + row * i_bytes;
+            const int kc = first ? kc1 : kc2, width = first ? p.H : p.I, wr = first ? p.wr1 : p.wr2;
+            const int k0 = ch * kc, k = min(kc, width - k0), boxes = 8 / wr;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&full[stage], kStageWeights + n.count * k * (first ? 2 : 4));
+                const bool flat = first ? p.flat_h : p.flat_i;
+                const int y = n.expert * (first ? p.I : p.H) + n.row;
+                const int half = first && gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
+                const int box_bytes = (half ? half : kStageWeights) / boxes;
+                const CUtensorMap *m = first ? &tm_gate : &tm_down;
+                for (int b = 0; b < (flat ? 1 : boxes); ++b) {
+                    const int x = flat ? 0 : k0 + b * Cfg::kBoxK, z = flat ? ch * boxes : 0;
+                    tma_load_3d(m, &full[stage], dst + b * box_bytes, x, y, z);
+                    if (half) tma_load_3d(&tm_up, &full[stage], dst + half + b * box_bytes, x, y, z);
                 }
-                bulk_load(dst + lane * Cfg::kWStride, base + static_cast<long long>(k0) * Cfg::kWBytes, k * Cfg::kWBytes, &full[stage]);
             }
+            __syncwarp();
             if constexpr (FP8) {
-                // scales of the chunk's 8 k blocks, for rows 0..7 and rows 8..15
-                const int kbs = ((first ? p.H : p.I) + kScaleBlock - 1) / kScaleBlock;
-                const int nbs = ((first ? p.I : p.H) + kScaleBlock - 1) / kScaleBlock;
-                const int kb = ch * kWarps + (lane & 7);
+                // scales of each warp's box, for its rows g and g + 8
+                const int kbs = (width + kScaleBlock - 1) / kScaleBlock, rows = first ? p.I : p.H;
+                const int w = lane & 7, kb = ch * boxes + w / wr, wrow = w % wr;
                 if (lane < 2 * kWarps && kb < kbs) {
-                    const int row = first ? n.rg * kUnitRows1 + (GATED ? 0 : lane & 8) : n.rg * kRows + (lane & 8);
-                    const float *s = first ? (GATED && lane >= 8 ? p.s_up : p.s_gate) : p.s_down;
-                    cp_async_4(dst + kRows * Cfg::kWStride + lane * 4,
-                               s + (static_cast<long long>(n.expert) * nbs + row / kScaleBlock) * kbs + kb, 4);
+                    const bool is_up = first && gated && lane >= kWarps;
+                    const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + (lane & 8)));
+                    const float *s = first ? (is_up ? p.s_up : p.s_gate) : p.s_down;
+                    const long long nbs = (rows + kScaleBlock - 1) / kScaleBlock;
+                    cp_async_4(dst + kStageWeights + lane * 4, s + (n.expert * nbs + row / kScaleBlock) * kbs + kb, 4);
                 }
                 cp_async_arrive(&full[stage]);
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         };
-        // The activations of the same chunk.
+        // The activations of the same k.
         auto load_tokens = [&](bool first, const Unit &n, int ch, int at) {
             uint8_t *dst = ring + static_cast<size_t>(at) * p.stage_bytes + Cfg::kActOffset;
-            const int k0 = ch * Cfg::kKC, k = min(Cfg::kKC, (first ? p.H : p.I) - k0);
-            for (int i = lane; i < n.count; i += 32) {
-                const int slot = r.order[n.start + i];
+            const int kc = first ? kc1 : kc2, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
+            if (lane < n.count) {
+                const int slot = r.order[n.start + lane];
                 if (first)
-                    bulk_load(dst + i * Cfg::kXStride, static_cast<const uint16_t *>(p.X) + (slot / p.top_k) * p.ldx + k0, k * 2, &full[at]);
+                    bulk_load(dst + lane * Cfg::act_stride(p.wr1, true),
+                              static_cast<const uint16_t *>(p.X) + (slot / p.top_k) * p.ldx + k0, k * 2, &full[at]);
                 else
-                    bulk_load(dst + i * Cfg::kHStride, p.hidden + static_cast<long long>(slot) * p.I + k0, k * 4, &full[at]);
+                    bulk_load(dst + lane * Cfg::act_stride(p.wr2, false), p.hidden + static_cast<long long>(slot) * p.I + k0, k * 4,
+                              &full[at]);
             }
         };
         auto next = [&] {
             if (++stage == p.stages) stage = 0, phase ^= 1u;
         };
-        for (int u = blockIdx.x; ok && u < units1; u += gridDim.x) {
-            const Unit n = first_unit(r, u, rg1);
+        for (int u = blockIdx.x; ok && u < units1; u += grid) {
+            const Unit n = first_unit(r, u, rg1, rows1, nch1);
             for (int ch = 0; ch < nch1; ++ch) {
-                load_rows(true, n, ch);
+                load_weights(true, n, ch);
                 if (!ok) break;
                 load_tokens(true, n, ch, stage);
                 next();
@@ -541,28 +570,34 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeArgs p) {
         }
         // Down projection: fill the ring with weights, wait for every CTA's h,
         // then hand the h rows of those stages in and go on.
-        const int mine2 = shift < units2 ? (units2 - shift + static_cast<int>(gridDim.x) - 1) / gridDim.x : 0;
-        const int total = mine2 * nch2, ahead = min(total, p.stages), stage0 = stage;
-        for (int i = 0; ok && i < ahead; ++i) {
-            load_rows(false, down_unit(r, shift + (i / nch2) * gridDim.x), i % nch2);
-            if (ok) next();
+        const int stage0 = stage;
+        int ahead = 0;
+        for (int u = shift; ok && u < units2 && ahead < p.stages; u += grid) {
+            const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
+            for (int ch = n.ch0; ok && ch < n.ch1 && ahead < p.stages; ++ch) {
+                load_weights(false, n, ch);
+                if (ok) next(), ++ahead;
+            }
         }
-        if (ok && total > 0) {
-            if (!__all_sync(0xffffffffu, wait_count(&p.counters[1], gridDim.x))) {
+        if (ok && ahead > 0) {
+            if (!__all_sync(0xffffffffu, wait_count(&p.counters[1], grid))) {
                 if (lane == 0) give_up();
                 ok = false;
             }
             fence_proxy_async_all();
         }
-        for (int i = 0; ok && i < total; ++i) {
-            const Unit n = down_unit(r, shift + (i / nch2) * gridDim.x);
-            if (i < ahead) {
-                load_tokens(false, n, i % nch2, (stage0 + i) % p.stages);
-            } else {
-                load_rows(false, n, i % nch2);
-                if (!ok) break;
-                load_tokens(false, n, i % nch2, stage);
-                next();
+        int i = 0;
+        for (int u = shift; ok && u < units2; u += grid) {
+            const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
+            for (int ch = n.ch0; ok && ch < n.ch1; ++ch, ++i) {
+                if (i < ahead) {
+                    load_tokens(false, n, ch, (stage0 + i) % p.stages);
+                } else {
+                    load_weights(false, n, ch);
+                    if (!ok) break;
+                    load_tokens(false, n, ch, stage);
+                    next();
+                }
             }
         }
         __syncwarp();
@@ -576,106 +611,183 @@ __global__ void __launch_bounds__(kMoeThreads, 1) moe_kernel(const MoeArgs p) {
         // ------------------------------------------------ arithmetic
         int stage = 0, buf = 0;
         uint32_t phase = 0;
-        auto take = [&] {  // after a time-out everything runs through without waiting
-            if (!abort_flag && !mbar_wait(&full[stage], phase)) give_up();
-        };
-        auto release = [&] {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[stage]);
-            if (++stage == p.stages) stage = 0, phase ^= 1u;
-        };
-        auto put = [&](const float (&acc)[NT][4]) {
+        const int g = lane >> 2;
+        // One unit's sums for this warp's row group and box column.
+        auto unit_sums = [&](auto first_c, const Unit &n, float(&acc)[NT][4]) {
+            constexpr bool kFirst = decltype(first_c)::value;
+            const int wr = kFirst ? p.wr1 : p.wr2, boxes = 8 / wr, my_row = warp % wr, my_box = warp / wr;
+            const bool halves = kFirst && gated;
+            const int w_off = halves ? (my_box * wr + my_row) * 1024 : (my_box * wr + my_row) * 2048;
+            const int row8 = halves ? kStageWeights / 2 : 1024;
+            const int stride = Cfg::act_stride(wr, kFirst), width = kFirst ? p.H : p.I;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int ch = n.ch0; ch < n.ch1; ++ch) {
+                // after a time-out everything runs through without waiting
+                if (!abort_flag && !mbar_wait(&full[stage], phase)) give_up();
+                const uint8_t *st = ring + static_cast<size_t>(stage) * p.stage_bytes;
+                const int k0 = (ch * boxes + my_box) * Cfg::kBoxK;
+                if (k0 < width) {
+                    const uint8_t *w0 = st + w_off + g * 128;
+                    const uint8_t *act = st + Cfg::kActOffset + my_box * Cfg::kBoxK * (kFirst ? 2 : 4);
+                    if constexpr (FP8) {
+                        float sum[NT][4] = {};
+                        multiply_box<XT, FP8, NT, kFirst>(w0, w0 + row8, act, stride, width - k0, n.count, sum);
+                        const float *sc = reinterpret_cast<const float *>(st + kStageWeights);
+                        const float s0 = sc[warp], s1 = sc[kWarps + warp];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) red[buf][warp][n][i][lane] = acc[n][i];
-        };
-        auto total = [&](int n, int i, int l) {
-            float s = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[buf][w][n][i][l];
-            return s;
-        };
-        for (int u = blockIdx.x; u < units1; u += gridDim.x) {
-            const Unit n = first_unit(r, u, rg1);
-            float acc[NT][4] = {};
-            for (int ch = 0; ch < nch1; ++ch) {
-                take();
-                multiply_chunk<XT, FP8, NT, true>(ring + static_cast<size_t>(stage) * p.stage_bytes, p.H - ch * Cfg::kKC, n.count, acc);
-                release();
-            }
-            put(acc);
-            consumer_sync();
-            // fragment element i of lane l: row l / 4 + 8 (i / 2), token 2 (l % 4) + i % 2
-            for (int x = threadIdx.x; x < NT * (GATED ? 64 : 128); x += 32 * kWarps) {
-                const int i = GATED ? x & 1 : x & 3, l = (x >> (GATED ? 1 : 2)) & 31, nt = x / (GATED ? 64 : 128);
-                const int tok = nt * 8 + 2 * (l & 3) + (i & 1);
-                if (tok < n.count) {
-                    float h = moe_act(p.act, total(nt, i, l));
-                    if (GATED) h *= total(nt, i + 2, l);
-                    const int row = n.rg * kUnitRows1 + (l >> 2) + (GATED ? 0 : 8 * (i >> 1));
-                    p.hidden[static_cast<long long>(r.order[n.start + tok]) * p.I + row] = tf32_round(h);
+                        for (int i = 0; i < NT; ++i) {
+                            acc[i][0] = fmaf(s0, sum[i][0], acc[i][0]);
+                            acc[i][1] = fmaf(s0, sum[i][1], acc[i][1]);
+                            acc[i][2] = fmaf(s1, sum[i][2], acc[i][2]);
+                            acc[i][3] = fmaf(s1, sum[i][3], acc[i][3]);
+                        }
+                    } else {
+                        multiply_box<XT, FP8, NT, kFirst>(w0, w0 + row8, act, stride, width - k0, n.count, acc);
+                    }
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
             }
-            buf ^= 1;
+            // Warps of the same rows: the first one adds the others' sums.
+            if (boxes > 1) {
+                if (my_box > 0) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) red[buf][warp][i][j][lane] = acc[i][j];
+                }
+                consumer_sync();
+                if (my_box == 0) {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            for (int b = 1; b < boxes; ++b) acc[i][j] += red[buf][b * wr + my_row][i][j][lane];
+                }
+                buf ^= 1;
+            }
+            return my_box == 0;
+        };
+        // Element i of a fragment: row g + 8 (i / 2), token 2 (lane % 4) + i % 2.
+        float acc[NT][4];
+        for (int u = blockIdx.x; u < units1; u += grid) {
+            const Unit n = first_unit(r, u, rg1, rows1, nch1);
+            if (!unit_sums(std::true_type{}, n, acc)) continue;
+            const int row = n.row + (warp % p.wr1) * (gated ? 8 : 16) + g;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = nt * 8 + 2 * (lane & 3) + (i & 1);
+                    if (tok >= n.count || (gated && i >= 2)) continue;
+                    const int at = row + (gated ? 0 : 8 * (i >> 1));
+                    float h = moe_act(p.act, acc[nt][i]);
+                    if (gated) h *= acc[nt][(i + 2) & 3];
+                    if (at < p.I) p.hidden[static_cast<long long>(r.order[n.start + tok]) * p.I + at] = tf32_round(h);
+                }
         }
         fence_proxy_async_all();  // h is read by bulk copies
         __threadfence();
         consumer_sync();
         if (threadIdx.x == 0) atomicAdd(&p.counters[1], 1u);
-        for (int u = shift; u < units2; u += gridDim.x) {
-            const Unit n = down_unit(r, u);
-            float acc[NT][4] = {};
-            for (int ch = 0; ch < nch2; ++ch) {
-                take();
-                multiply_chunk<XT, FP8, NT, false>(ring + static_cast<size_t>(stage) * p.stage_bytes, p.I - ch * Cfg::kKC, n.count, acc);
-                release();
-            }
-            put(acc);
-            consumer_sync();
-            for (int x = threadIdx.x; x < NT * 128; x += 32 * kWarps) {
-                const int i = x & 3, l = (x >> 2) & 31, nt = x >> 7;
-                const int tok = nt * 8 + 2 * (l & 3) + (i & 1);
-                if (tok < n.count)
-                    p.part[static_cast<long long>(r.order[n.start + tok]) * p.H + n.rg * kRows + (l >> 2) + 8 * (i >> 1)] = total(nt, i, l);
-            }
-            buf ^= 1;
-            __threadfence();
-            consumer_sync();
-            if (threadIdx.x == 0) last = atomicAdd(&p.counters[4 + n.rg], 1u) == static_cast<unsigned>(r.pairs - 1);
-            consumer_sync();
-            if (last) {
-                __threadfence();
-                if (threadIdx.x == 0) p.counters[4 + n.rg] = 0u;
-                if (!abort_flag)
-                    for (int x = threadIdx.x; x < p.T * kRows; x += 32 * kWarps) {
-                        const int t = x / kRows, c = n.rg * kRows + x % kRows;
-                        float y = 0.f;
-                        for (int j = 0; j < p.top_k; ++j) {
-                            const int slot = t * p.top_k + j;
-                            y = fmaf(r.weight[slot], __ldcg(p.part + static_cast<long long>(slot) * p.H + c), y);
-                        }
-                        store_out(p.Y, static_cast<size_t>(t) * p.ldy + c, p.y_type, y);
+        const long long slots = static_cast<long long>(p.T) * p.top_k;
+        for (int u = shift; u < units2; u += grid) {
+            const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
+            if (!unit_sums(std::false_type{}, n, acc)) continue;
+            const int row = n.row + (warp % p.wr2) * 16 + g;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = nt * 8 + 2 * (lane & 3) + (i & 1), at = row + 8 * (i >> 1);
+                    if (tok < n.count && at < p.H) p.part[(n.split * slots + r.order[n.start + tok]) * p.H + at] = acc[nt][i];
+                }
+        }
+        // ------------------------------------------------ sum over a token's experts
+        __threadfence();
+        consumer_sync();
+        if (threadIdx.x == 0) {
+            atomicAdd(&p.counters[2], 1u);
+            if (!wait_count(&p.counters[2], grid)) give_up();
+        }
+        consumer_sync();
+        if (!abort_flag) {
+            const int groups = p.H / 4;
+            for (int x = blockIdx.x * 32 * kWarps + threadIdx.x; x < p.T * groups; x += grid * 32 * kWarps) {
+                const int t = x / groups, c = x % groups * 4;
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < p.top_k; ++j) {
+                    const long long slot = static_cast<long long>(t) * p.top_k + j;
+                    float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + slot * p.H + c));
+                    for (int s = 1; s < p.k_splits; ++s) {
+                        const float4 w = __ldcg(reinterpret_cast<const float4 *>(p.part + (s * slots + slot) * p.H + c));
+                        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                     }
+                    const float f = r.weight[slot];
+                    y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) store_out(p.Y, static_cast<size_t>(t) * p.ldy + c + i, p.y_type, y[i]);
             }
         }
     }
     __syncthreads();
     // The last CTA to leave clears the barriers for the next call.
-    if (threadIdx.x == 0 && atomicAdd(&p.counters[2], 1u) == gridDim.x - 1) p.counters[0] = p.counters[1] = p.counters[2] = 0u;
+    if (threadIdx.x == 0 && atomicAdd(&p.counters[3], 1u) == gridDim.x - 1)
+        p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = 0u;
 }
 
-template <int XT, bool FP8, int NT, bool GATED>
-cudaError_t launch_moe(MoeArgs a, cudaStream_t stream) {
+// Tensor map of E matrices of `rows` rows of `width` elements.  flat: a box is
+// `boxes` 128-byte pieces of `box_rows` rows (dimensions: piece, row, piece
+// number); else one piece, and the row's ragged end reads as zeros.
+bool encode_expert_map(CUtensorMap *map, const void *base, int elem_bytes, CUtensorMapDataType dt, uint64_t all_rows,
+                       uint64_t width, bool flat, uint32_t box_rows, uint32_t boxes) {
+    const uint64_t piece = 128 / elem_bytes;
+    return flat ? encode_box_map(map, dt, base, piece, all_rows, width / piece, width * elem_bytes, 128, piece, box_rows, boxes)
+                : encode_box_map(map, dt, base, width, all_rows, 1, width * elem_bytes, width * elem_bytes, piece, box_rows, 1);
+}
+
+// Row groups of a unit: the most (8, 4, 2, 1) whose units (groups_of_one of
+// them with one row group) keep the SMs busy to 90 % in whole rounds, but at
+// least as many as hold a stage's activations (act_bytes with one row group)
+// within twice its weights, so that the ring keeps enough stages.
+int pick_row_groups(double groups_of_one, int sms, int act_bytes) {
+    int least = 1;
+    while (least < 8 && act_bytes / least > 2 * kStageWeights) least *= 2;
+    for (int wr = 8; wr > least; wr /= 2) {
+        const double units = groups_of_one / wr;
+        if (units >= 0.9 * std::ceil(units / sms) * sms) return wr;
+    }
+    return least;
+}
+
+template <int XT, bool FP8, int NT>
+cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stream) {
     using Cfg = MoeCfg<FP8>;
-    auto kern = moe_kernel<XT, FP8, NT, GATED>;
-    a.tok_rows = std::min(a.T, 8 * NT);
-    // a stage holds the rows and either kind of activations
-    const int act_bytes = a.tok_rows * std::max(Cfg::kXStride, Cfg::kHStride);
-    a.stage_bytes = (Cfg::kActOffset + act_bytes + 127) / 128 * 128;
-    constexpr int kRing = 227 * 1024 - 1024 - static_cast<int>(sizeof(Routing) + 2 * kWarps * NT * 4 * 32 * 4 + 16 * kMaxStages + 64);
-    static_assert(kRing >= kWarps * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
-    a.stages = std::min(kMaxStages, kRing / a.stage_bytes);
+    auto kern = moe_kernel<XT, FP8, NT>;
+    const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * 8 * Cfg::kBoxK * 2;  // of X rows; h rows twice that
+    a.wr1 = pick_row_groups(active * m.I / (m.up ? 8 : 16), sms, act);
+    a.wr2 = pick_row_groups(active * m.H / 16, sms, 2 * act);
+    // a stage holds the weights, their scales and either kind of activations
+    const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.wr1, true), Cfg::act_stride(a.wr2, false));
+    a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
+    constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * kWarps * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
+    static_assert(kRing >= 1024 + kWarps * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
+    a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);
+    if (a.stages < 2) return cudaErrorInvalidConfiguration;
+    const int wb = Cfg::kWBytes;
+    const auto dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    a.flat_h = m.H * wb % 128 == 0;
+    a.flat_i = m.I * wb % 128 == 0;
+    CUtensorMap tg, tu, td;
+    const uint64_t rows_i = static_cast<uint64_t>(m.E) * m.I, rows_h = static_cast<uint64_t>(m.E) * m.H;
+    const uint32_t box1 = (m.up ? 8 : 16) * a.wr1;
+    if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, box1, 8 / a.wr1) ||
+        !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, box1, 8 / a.wr1) ||
+        !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, 16 * a.wr2, 8 / a.wr2))
+        return cudaErrorNotSupported;
     static unsigned long long smem_set = 0;
     cudaError_t e = ensure_dynamic_smem(kern, kRing, smem_set);
     if (e != cudaSuccess) return e;
@@ -689,13 +801,15 @@ cudaError_t launch_moe(MoeArgs a, cudaStream_t stream) {
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a);
+    e = cudaLaunchKernelEx(&cfg, kern, tg, tu, td, a);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
 template <int XT, bool FP8>
-cudaError_t launch_moe_types(const MoeArgs &a, cudaStream_t stream) {
-    return a.up ? launch_moe<XT, FP8, 1, true>(a, stream) : launch_moe<XT, FP8, 1, false>(a, stream);
+cudaError_t launch_moe_tokens(const Moe &m, const MoeArgs &a, double active, double tokens, cudaStream_t stream) {
+    if (tokens <= 6.0) return launch_moe<XT, FP8, 1>(m, a, active, stream);
+    if (tokens <= 12.0) return launch_moe<XT, FP8, 2>(m, a, active, stream);
+    return launch_moe<XT, FP8, 4>(m, a, active, stream);
 }
 
 }  // namespace
@@ -725,10 +839,13 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     a.ids = m.ids;
     a.weights = m.weights;
     a.err = watchdog_word();
-    const size_t slots = static_cast<size_t>(m.T) * m.top_k;
-    const size_t n_logits = (static_cast<size_t>(m.T) * m.E + 63) / 64 * 64, n_hidden = slots * m.I, n_part = slots * m.H;
+    // Experts with any token if the router chose evenly, and tokens of one.
+    const double slots = static_cast<double>(m.T) * m.top_k;
+    const double active = m.E * (1.0 - std::pow(1.0 - static_cast<double>(m.top_k) / m.E, m.T)), tokens = slots / active;
+    a.k_splits = 1;
+    const size_t n_logits = (static_cast<size_t>(m.T) * m.E + 63) / 64 * 64, n_hidden = static_cast<size_t>(slots) * m.I;
     Scratch s;
-    cudaError_t e = acquire_scratch(stream, n_logits + n_hidden + n_part, 4 + m.H / kRows, &s);
+    const cudaError_t e = acquire_scratch(stream, n_logits + n_hidden + static_cast<size_t>(slots) * m.H * a.k_splits, 4, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
     a.hidden = s.partials + n_logits;
@@ -738,8 +855,8 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     info->plan = "moe_few_tokens";
     const bool fp8 = m.w_type == kTypeE4M3;
     if (m.x_type == kOutF16)
-        return fp8 ? launch_moe_types<kOutF16, true>(a, stream) : launch_moe_types<kOutF16, false>(a, stream);
-    return fp8 ? launch_moe_types<kOutBF16, true>(a, stream) : launch_moe_types<kOutBF16, false>(a, stream);
+        return fp8 ? launch_moe_tokens<kOutF16, true>(m, a, active, tokens, stream) : launch_moe_tokens<kOutF16, false>(m, a, active, tokens, stream);
+    return fp8 ? launch_moe_tokens<kOutBF16, true>(m, a, active, tokens, stream) : launch_moe_tokens<kOutBF16, false>(m, a, active, tokens, stream);
 }
 
 }  // namespace gemm11
