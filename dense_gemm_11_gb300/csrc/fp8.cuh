@@ -6,6 +6,15 @@
 
 namespace gemm11 {
 
+// mbar_wait that reads the clock only once a wait has lasted: the try itself
+// suspends for a while, so that most waits end within the first few.
+__device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity, unsigned long long limit_ns = kWaitLimitNs) {
+    const uint32_t a = smem_u32(bar);
+    for (int i = 0; i < 16; ++i)
+        if (mbar_try_wait(a, parity)) return true;
+    return mbar_wait(bar, parity, limit_ns);
+}
+
 // D(tmem) (+)= A(smem desc) x B(smem desc), 8-bit operands, K = 32 per
 // instruction (32 bytes of each K-major row).
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

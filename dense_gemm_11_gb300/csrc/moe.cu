@@ -43,8 +43,8 @@
 
 #include <cuda_fp8.h>
 
+#include "fp8.cuh"
 #include "fp8.h"
-#include "ptx.cuh"
 
 namespace gemm11 {
 namespace {
@@ -70,7 +70,7 @@ struct MoeArgs {
     float *logits, *hidden, *part;  // scratch: T x E, slots x I, k_splits x slots x H
     unsigned *counters;             // three barriers and the exit
     unsigned *err;
-    int wr1, wr2;    // row groups (of 16 rows) of a unit in the first half and in the down projection
+    int lw1, lw2;    // log2 of WR, the row groups (of 16 rows) of a unit, in the first half and in the down projection
     int k_splits;    // units of the down projection that share a row group's k
     int flat_h, flat_i;  // rows of H (I) elements are whole 128-byte boxes: one copy takes a stage's boxes
     int stages, stage_bytes;
@@ -353,8 +353,8 @@ struct MoeCfg {
     // Row strides of the activations: 4 neighbouring 16-byte pieces of 2
     // tokens (a quarter warp's load) fall on different banks.
     static constexpr int kXPad = FP8 ? 32 : 16, kHPad = FP8 ? 64 : 32;
-    static constexpr int act_stride(int wr, bool first) {
-        return 8 / wr * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
+    __host__ __device__ static constexpr int act_stride(int lw, bool first) {
+        return (8 >> lw) * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
     }
 };
 
@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     __shared__ volatile int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool gated = p.up != nullptr;
-    const int rows1 = (gated ? 8 : 16) * p.wr1, rows2 = 16 * p.wr2;  // rows of h and of y of a unit
+    const int rows1 = (gated ? 8 : 16) << p.lw1, rows2 = 16 << p.lw2;  // rows of h and of y of a unit
     const int rg1 = (p.I + rows1 - 1) / rows1, rg2 = (p.H + rows2 - 1) / rows2;
-    const int kc1 = 8 / p.wr1 * Cfg::kBoxK, kc2 = 8 / p.wr2 * Cfg::kBoxK;  // k of a stage
+    const int kc1 = (8 >> p.lw1) * Cfg::kBoxK, kc2 = (8 >> p.lw2) * Cfg::kBoxK;  // k of a stage
     const int nch1 = (p.H + kc1 - 1) / kc1, nch2 = (p.I + kc2 - 1) / kc2;
 
     auto give_up = [&] {
@@ -502,69 +502,86 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
+        // What this lane copies for a unit, worked out once for its stages:
+        // a token's row (lane < count), and with 8-bit weights the scales of
+        // warp lane % 8's box, for its rows g (lane < 8) or g + 8.
+        int y = 0, count = 0;
+        const uint8_t *token = nullptr;
+        const float *scale = nullptr;
+        auto begin_unit = [&](bool first, const Unit &n) {
+            const int rows = first ? p.I : p.H, width = first ? p.H : p.I, lw = first ? p.lw1 : p.lw2;
+            y = n.expert * rows + n.row;
+            count = n.count;
+            if (lane < count) {
+                const int slot = r.order[n.start + lane];
+                token = first ? static_cast<const uint8_t *>(p.X) + 2 * (slot / p.top_k * p.ldx)
+                              : reinterpret_cast<const uint8_t *>(p.hidden + static_cast<long long>(slot) * p.I);
+            }
+            if constexpr (FP8) {
+                const int wrow = lane & ((1 << lw) - 1), box = (lane & 7) >> lw;
+                const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + (lane & 8)));
+                const long long kbs = (width + kScaleBlock - 1) / kScaleBlock, nbs = (rows + kScaleBlock - 1) / kScaleBlock;
+                const float *base = !first ? p.s_down : gated && lane >= kWarps ? p.s_up : p.s_gate;
+                scale = base + (n.expert * nbs + row / kScaleBlock) * kbs + box;
+            }
+        };
         // Takes a free stage and starts the copies of its weights.
-        auto load_weights = [&](bool first, const Unit &n, int ch) {
-            if (!__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1u))) {
+        auto load_weights = [&](bool first, int ch) {
+            if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u))) {
                 if (lane == 0) give_up();
                 ok = false;
                 return;
             }
-            uint8_t *dst = ring + static_cast<size_t>(stage) * p.stage_bytes;
-            const int kc = first ? kc1 : kc2, width = first ? p.H : p.I, wr = first ? p.wr1 : p.wr2;
-            const int k0 = ch * kc, k = min(kc, width - k0), boxes = 8 / wr;
+            uint8_t *dst = ring + stage * p.stage_bytes;
+            const int lw = first ? p.lw1 : p.lw2, boxes = 8 >> lw, width = first ? p.H : p.I;
+            const int k0 = ch * boxes * Cfg::kBoxK, k = min(boxes * Cfg::kBoxK, width - k0);
             if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], kStageWeights + n.count * k * (first ? 2 : 4));
-                const bool flat = first ? p.flat_h : p.flat_i;
-                const int y = n.expert * (first ? p.I : p.H) + n.row;
-                const int half = first && gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
-                const int box_bytes = (half ? half : kStageWeights) / boxes;
-                const CUtensorMap *m = first ? &tm_gate : &tm_down;
-                for (int b = 0; b < (flat ? 1 : boxes); ++b) {
-                    const int x = flat ? 0 : k0 + b * Cfg::kBoxK, z = flat ? ch * boxes : 0;
-                    tma_load_3d(m, &full[stage], dst + b * box_bytes, x, y, z);
-                    if (half) tma_load_3d(&tm_up, &full[stage], dst + half + b * box_bytes, x, y, z);
+                mbar_arrive_expect_tx(&full[stage], kStageWeights + count * k * (first ? 2 : 4));
+                if (first) {
+                    const int half = gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
+                    if (p.flat_h) {
+                        tma_load_3d(&tm_gate, &full[stage], dst, 0, y, ch * boxes);
+                        if (half) tma_load_3d(&tm_up, &full[stage], dst + half, 0, y, ch * boxes);
+                    } else {
+                        for (int b = 0; b < boxes; ++b) {
+                            const int at = b * ((half ? 1024 : 2048) << lw);
+                            tma_load_3d(&tm_gate, &full[stage], dst + at, k0 + b * Cfg::kBoxK, y, 0);
+                            if (half) tma_load_3d(&tm_up, &full[stage], dst + half + at, k0 + b * Cfg::kBoxK, y, 0);
+                        }
+                    }
+                } else if (p.flat_i) {
+                    tma_load_3d(&tm_down, &full[stage], dst, 0, y, ch * boxes);
+                } else {
+                    for (int b = 0; b < boxes; ++b)
+                        tma_load_3d(&tm_down, &full[stage], dst + b * (2048 << lw), k0 + b * Cfg::kBoxK, y, 0);
                 }
             }
             __syncwarp();
             if constexpr (FP8) {
-                // scales of each warp's box, for its rows g and g + 8
-                const int kbs = (width + kScaleBlock - 1) / kScaleBlock, rows = first ? p.I : p.H;
-                const int w = lane & 7, kb = ch * boxes + w / wr, wrow = w % wr;
-                if (lane < 2 * kWarps && kb < kbs) {
-                    const bool is_up = first && gated && lane >= kWarps;
-                    const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + (lane & 8)));
-                    const float *s = first ? (is_up ? p.s_up : p.s_gate) : p.s_down;
-                    const long long nbs = (rows + kScaleBlock - 1) / kScaleBlock;
-                    cp_async_4(dst + kStageWeights + lane * 4, s + (n.expert * nbs + row / kScaleBlock) * kbs + kb, 4);
-                }
+                if (lane < 2 * kWarps && k0 + ((lane & 7) >> lw) * Cfg::kBoxK < width)
+                    cp_async_4(dst + kStageWeights + lane * 4, scale + ch * boxes, 4);
                 cp_async_arrive(&full[stage]);
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
         };
         // The activations of the same k.
-        auto load_tokens = [&](bool first, const Unit &n, int ch, int at) {
-            uint8_t *dst = ring + static_cast<size_t>(at) * p.stage_bytes + Cfg::kActOffset;
-            const int kc = first ? kc1 : kc2, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
-            if (lane < n.count) {
-                const int slot = r.order[n.start + lane];
-                if (first)
-                    bulk_load(dst + lane * Cfg::act_stride(p.wr1, true),
-                              static_cast<const uint16_t *>(p.X) + (slot / p.top_k) * p.ldx + k0, k * 2, &full[at]);
-                else
-                    bulk_load(dst + lane * Cfg::act_stride(p.wr2, false), p.hidden + static_cast<long long>(slot) * p.I + k0, k * 4,
-                              &full[at]);
-            }
+        auto load_tokens = [&](bool first, int ch, int at) {
+            const int lw = first ? p.lw1 : p.lw2, kc = (8 >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
+            const int bytes = first ? 2 : 4;
+            if (lane < count)
+                bulk_load(ring + at * p.stage_bytes + Cfg::kActOffset + lane * Cfg::act_stride(lw, first), token + k0 * bytes, k * bytes,
+                          &full[at]);
         };
         auto next = [&] {
             if (++stage == p.stages) stage = 0, phase ^= 1u;
         };
         for (int u = blockIdx.x; ok && u < units1; u += grid) {
-            const Unit n = first_unit(r, u, rg1, rows1, nch1);
+            begin_unit(true, first_unit(r, u, rg1, rows1, nch1));
             for (int ch = 0; ch < nch1; ++ch) {
-                load_weights(true, n, ch);
+                load_weights(true, ch);
                 if (!ok) break;
-                load_tokens(true, n, ch, stage);
+                load_tokens(true, ch, stage);
                 next();
             }
         }
@@ -574,8 +591,9 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         int ahead = 0;
         for (int u = shift; ok && u < units2 && ahead < p.stages; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
+            begin_unit(false, n);
             for (int ch = n.ch0; ok && ch < n.ch1 && ahead < p.stages; ++ch) {
-                load_weights(false, n, ch);
+                load_weights(false, ch);
                 if (ok) next(), ++ahead;
             }
         }
@@ -589,13 +607,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         int i = 0;
         for (int u = shift; ok && u < units2; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
+            begin_unit(false, n);
             for (int ch = n.ch0; ok && ch < n.ch1; ++ch, ++i) {
                 if (i < ahead) {
-                    load_tokens(false, n, ch, (stage0 + i) % p.stages);
+                    load_tokens(false, ch, (stage0 + i) % p.stages);
                 } else {
-                    load_weights(false, n, ch);
+                    load_weights(false, ch);
                     if (!ok) break;
-                    load_tokens(false, n, ch, stage);
+                    load_tokens(false, ch, stage);
                     next();
                 }
             }
@@ -615,17 +634,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         // One unit's sums for this warp's row group and box column.
         auto unit_sums = [&](auto first_c, const Unit &n, float(&acc)[NT][4]) {
             constexpr bool kFirst = decltype(first_c)::value;
-            const int wr = kFirst ? p.wr1 : p.wr2, boxes = 8 / wr, my_row = warp % wr, my_box = warp / wr;
+            const int lw = kFirst ? p.lw1 : p.lw2, boxes = 8 >> lw, my_row = warp & ((1 << lw) - 1), my_box = warp >> lw;
             const bool halves = kFirst && gated;
-            const int w_off = halves ? (my_box * wr + my_row) * 1024 : (my_box * wr + my_row) * 2048;
+            const int w_off = warp * (halves ? 1024 : 2048);
             const int row8 = halves ? kStageWeights / 2 : 1024;
-            const int stride = Cfg::act_stride(wr, kFirst), width = kFirst ? p.H : p.I;
+            const int stride = Cfg::act_stride(lw, kFirst), width = kFirst ? p.H : p.I;
 #pragma unroll
             for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
             for (int ch = n.ch0; ch < n.ch1; ++ch) {
                 // after a time-out everything runs through without waiting
-                if (!abort_flag && !mbar_wait(&full[stage], phase)) give_up();
-                const uint8_t *st = ring + static_cast<size_t>(stage) * p.stage_bytes;
+                if (!abort_flag && !mbar_wait_patient(&full[stage], phase)) give_up();
+                const uint8_t *st = ring + stage * p.stage_bytes;
                 const int k0 = (ch * boxes + my_box) * Cfg::kBoxK;
                 if (k0 < width) {
                     const uint8_t *w0 = st + w_off + g * 128;
@@ -664,7 +683,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            for (int b = 1; b < boxes; ++b) acc[i][j] += red[buf][b * wr + my_row][i][j][lane];
+                            for (int b = 1; b < boxes; ++b) acc[i][j] += red[buf][(b << lw) + my_row][i][j][lane];
                 }
                 buf ^= 1;
             }
@@ -675,7 +694,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int u = blockIdx.x; u < units1; u += grid) {
             const Unit n = first_unit(r, u, rg1, rows1, nch1);
             if (!unit_sums(std::true_type{}, n, acc)) continue;
-            const int row = n.row + (warp % p.wr1) * (gated ? 8 : 16) + g;
+            const int row = n.row + (warp & ((1 << p.lw1) - 1)) * (gated ? 8 : 16) + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -696,7 +715,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         for (int u = shift; u < units2; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
             if (!unit_sums(std::false_type{}, n, acc)) continue;
-            const int row = n.row + (warp % p.wr2) * 16 + g;
+            const int row = n.row + (warp & ((1 << p.lw2) - 1)) * 16 + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -749,16 +768,17 @@ bool encode_expert_map(CUtensorMap *map, const void *base, int elem_bytes, CUten
                 : encode_box_map(map, dt, base, width, all_rows, 1, width * elem_bytes, width * elem_bytes, piece, box_rows, 1);
 }
 
-// Row groups of a unit: the most (8, 4, 2, 1) whose units (groups_of_one of
-// them with one row group) keep the SMs busy to 90 % in whole rounds, but at
-// least as many as hold a stage's activations (act_bytes with one row group)
-// within twice its weights, so that the ring keeps enough stages.
+// log2 of WR, the row groups of a unit: the most (8, 4, 2, 1) whose units
+// (groups_of_one of them with one row group) keep the SMs busy to 90 % in
+// whole rounds, but at least as many as hold a stage's activations (act_bytes
+// with one row group) within twice its weights, so that the ring keeps enough
+// stages.
 int pick_row_groups(double groups_of_one, int sms, int act_bytes) {
-    int least = 1;
-    while (least < 8 && act_bytes / least > 2 * kStageWeights) least *= 2;
-    for (int wr = 8; wr > least; wr /= 2) {
-        const double units = groups_of_one / wr;
-        if (units >= 0.9 * std::ceil(units / sms) * sms) return wr;
+    int least = 0;
+    while (least < 3 && (act_bytes >> least) > 2 * kStageWeights) ++least;
+    for (int lw = 3; lw > least; --lw) {
+        const double units = groups_of_one / (1 << lw);
+        if (units >= 0.9 * std::ceil(units / sms) * sms) return lw;
     }
     return least;
 }
@@ -768,10 +788,10 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     using Cfg = MoeCfg<FP8>;
     auto kern = moe_kernel<XT, FP8, NT>;
     const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * 8 * Cfg::kBoxK * 2;  // of X rows; h rows twice that
-    a.wr1 = pick_row_groups(active * m.I / (m.up ? 8 : 16), sms, act);
-    a.wr2 = pick_row_groups(active * m.H / 16, sms, 2 * act);
+    a.lw1 = pick_row_groups(active * m.I / (m.up ? 8 : 16), sms, act);
+    a.lw2 = pick_row_groups(active * m.H / 16, sms, 2 * act);
     // a stage holds the weights, their scales and either kind of activations
-    const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.wr1, true), Cfg::act_stride(a.wr2, false));
+    const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.lw1, true), Cfg::act_stride(a.lw2, false));
     a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
     constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * kWarps * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
     static_assert(kRing >= 1024 + kWarps * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
@@ -783,10 +803,10 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     a.flat_i = m.I * wb % 128 == 0;
     CUtensorMap tg, tu, td;
     const uint64_t rows_i = static_cast<uint64_t>(m.E) * m.I, rows_h = static_cast<uint64_t>(m.E) * m.H;
-    const uint32_t box1 = (m.up ? 8 : 16) * a.wr1;
-    if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, box1, 8 / a.wr1) ||
-        !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, box1, 8 / a.wr1) ||
-        !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, 16 * a.wr2, 8 / a.wr2))
+    const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = 8 >> a.lw1, rows2 = 16 << a.lw2, boxes2 = 8 >> a.lw2;
+    if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
+        !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
+        !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, rows2, boxes2))
         return cudaErrorNotSupported;
     static unsigned long long smem_set = 0;
     cudaError_t e = ensure_dynamic_smem(kern, kRing, smem_set);
