@@ -11,12 +11,14 @@
 // cooperatively) and built as one stream of weight bytes:
 //   * work is cut into units of 16 WR matrix rows (gate rows with the up rows
 //     they meet, or rows of the down projection) for one expert and up to 8 NT
-//     of its tokens.  A unit goes through its k in stages of 16 KB of weights:
-//     16 WR rows x 8 / WR boxes of 128 bytes, one TMA copy (two with a gate);
+//     of its tokens.  A unit goes through its k in stages of 32 KB of weights:
+//     16 WR rows x 16 / WR boxes of 128 bytes, one TMA copy (two with a gate).
+//     Issuing a copy costs the producer about 100 cycles, so stages are large:
+//     with 16 KB it, not memory, set the pace (130 us against ??? at 1 token)
 //   * a producer warp fills a ring of stages.  It runs ahead of the arithmetic
 //     across units, and into the down projection while the other CTAs still
 //     finish the first half;
-//   * eight warps take a stage's WR row groups x 8 / WR boxes, one each, and
+//   * eight warps take a stage's WR row groups x 16 / WR boxes, two each, and
 //     multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
 //     share rows add their sums in warp order in shared memory at the unit's
 //     end.  The matrix instruction is the warp-level one: a unit has 1 to 8 NT
@@ -51,8 +53,11 @@ namespace {
 
 constexpr int kWarps = 8;                       // consumer warps
 constexpr int kMoeThreads = 32 * (kWarps + 1);  // and the producer warp
-constexpr int kStageWeights = 16384;            // bytes of weights in a stage
+constexpr int kStageWeights = 32768;            // bytes of weights in a stage
+constexpr int kBoxes = 2;                       // 16 rows x 128 bytes boxes of a warp in a stage
 constexpr int kMaxStages = 12;
+constexpr int kMaxSplits = 4;                   // units that share a row group's k in the down projection
+constexpr int kChoiceKeys = 16384;              // logits looked at together
 
 struct MoeArgs {
     int T, E, top_k, H, I;
@@ -88,7 +93,7 @@ struct Routing {
 };
 
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
@@ -98,13 +103,13 @@ template <int XT>
 __device__ __forceinline__ void mma_16bit(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
     if constexpr (XT == kOutBF16)
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
     else
-        asm volatile(
+        asm(
             "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
             "{%0, %1, %2, %3};"
             : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -167,50 +172,68 @@ __device__ __forceinline__ void widen_e4m3(const uint32_t *w, float *v) {
 }
 
 // ---------------------------------------------------------------- routing
-// Logits of expert e for 8 tokens at a time, one (expert, token group) a CTA;
-// the consumer warps share H.
+// Sum of w x over `threads` threads' share of H for one expert and 8 tokens.
 template <int XT>
-__device__ void router_logits(const MoeArgs &p, float *red) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = (p.T + 7) / 8;
-    for (int u = blockIdx.x; u < p.E * groups; u += gridDim.x) {
-        const int e = u / groups, t0 = (u % groups) * 8;
-        float acc[8];
+__device__ __forceinline__ void router_dot(const MoeArgs &p, int e, int t0, int thread, int threads, float (&acc)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-        for (int k = threadIdx.x * 8; k < p.H; k += 32 * kWarps * 8) {
-            float w[8];
-            const long long at = static_cast<long long>(e) * p.H + k;
-            if (p.router_f32) {
-                const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.router) + at);
-                const float4 a = __ldg(r), b = __ldg(r + 1);
-                w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-            } else {
-                widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.router) + at)), XT, w);
-            }
+    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+    for (int k = thread * 8; k < p.H; k += threads * 8) {
+        float w[8];
+        uint4 x[8];
+        const long long at = static_cast<long long>(e) * p.H + k;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (t0 + i >= p.T) break;
-                float x[8];
-                widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + (t0 + i) * p.ldx + k)), XT, x);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i] = fmaf(w[j], x[j], acc[i]);
-            }
+        for (int i = 0; i < 8; ++i)
+            x[i] = t0 + i < p.T ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + (t0 + i) * p.ldx + k))
+                                : make_uint4(0, 0, 0, 0);
+        if (p.router_f32) {
+            const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.router) + at);
+            const float4 a = __ldg(r), b = __ldg(r + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        } else {
+            widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.router) + at)), XT, w);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+            float f[8];
+            widen8(x[i], XT, f);
 #pragma unroll
-            for (int d = 16; d >= 1; d >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
-            if (lane == 0) red[warp * 8 + i] = acc[i];
+            for (int j = 0; j < 8; ++j) acc[i] = fmaf(w[j], f[j], acc[i]);
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
+}
+
+// All logits, in units of one expert and 8 tokens: a CTA takes a unit while
+// there are no more units than CTAs (its warps share H), else each warp does.
+template <int XT>
+__device__ void router_logits(const MoeArgs &p, float *red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int groups = (p.T + 7) / 8, units = p.E * groups;
+    float acc[8];
+    if (units > static_cast<int>(gridDim.x)) {
+        for (int u = warp * gridDim.x + blockIdx.x; u < units; u += gridDim.x * kWarps) {
+            const int e = u / groups, t0 = (u % groups) * 8;
+            router_dot<XT>(p, e, t0, lane, 32, acc);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (lane == i && t0 + i < p.T) p.logits[(t0 + i) * p.E + e] = acc[i];
+        }
+    } else if (static_cast<int>(blockIdx.x) < units) {
+        const int e = blockIdx.x / groups, t0 = (blockIdx.x % groups) * 8;
+        router_dot<XT>(p, e, t0, threadIdx.x, 32 * kWarps, acc);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane == i) red[warp * 8 + i] = acc[i];
         consumer_sync();
         if (threadIdx.x < 8 && t0 + threadIdx.x < p.T) {
-            float s = 0.f;
+            float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) s += red[w * 8 + threadIdx.x];
-            p.logits[static_cast<long long>(t0 + threadIdx.x) * p.E + e] = s;
+            for (int w = 0; w < kWarps; ++w) v += red[w * 8 + threadIdx.x];
+            p.logits[(t0 + threadIdx.x) * p.E + e] = v;
         }
-        consumer_sync();
     }
 }
 
@@ -222,89 +245,87 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-// One warp, one token: softmax and its top_k largest, by repeated maximum
-// (keys in shared memory, taken ones set to 0).
+__device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+
+// One warp, one token: softmax and its top_k largest, by repeated maximum over
+// the logits' keys (shared memory; taken ones are set to 0).
 __device__ void choose_experts(const MoeArgs &p, int t, uint32_t *keys, Routing &r) {
     const int lane = threadIdx.x & 31;
-    const float *logits = p.logits + static_cast<long long>(t) * p.E;
-    for (int e = lane; e < p.E; e += 32) keys[e] = logit_key(__ldcg(logits + e));
-    float top = 0.f, chosen = 0.f;
-    float mine[(kMoeMaxTopK + 31) / 32];
-    mine[0] = 0.f;
+    float top = 0.f, chosen = 0.f, sum = 0.f, mine = 0.f;
     for (int j = 0; j < p.top_k; ++j) {
         uint32_t best = 0;
         int at = 0;
-        for (int e = lane; e < p.E; e += 32)
-            if (keys[e] > best) best = keys[e], at = e;
+        for (int e = lane; e < p.E; e += 32) {
+            const uint32_t k = keys[e];
+            if (k > best) best = k, at = e;
+        }
         const uint32_t m = __reduce_max_sync(0xffffffffu, best);
         const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(at) : 0xFFFFFFFFu));
-        const float l = __ldcg(logits + e);
-        if (j == 0) top = l;
+        const float l = key_logit(m);
+        if (j == 0) {
+            top = l;
+            if (!p.renorm)
+                for (int i = lane; i < p.E; i += 32) sum += expf(key_logit(keys[i]) - top);
+        }
         const float v = expf(l - top);
         chosen += v;
-        if (lane == j) mine[0] = v;
+        if (lane == j) mine = v;
         if (lane == 0) r.expert[t * p.top_k + j] = static_cast<uint16_t>(e);
         if (lane == (e & 31)) keys[e] = 0;
-        __syncwarp();
     }
-    float sum = chosen;
-    if (!p.renorm) {
-        sum = 0.f;
-        for (int e = lane; e < p.E; e += 32) sum += expf(__ldcg(logits + e) - top);
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    }
-    if (lane < p.top_k) r.weight[t * p.top_k + lane] = mine[0] / sum;
-    __syncwarp();
+    for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane < p.top_k) r.weight[t * p.top_k + lane] = mine / (p.renorm ? chosen : sum);
 }
 
-// One warp: slots grouped by expert (a counting sort that keeps their order),
-// and the (expert, token group) pairs that the units go over.
+// Slots grouped by expert, in ascending order, and the (expert, token group)
+// pairs that the units go over.  The warps deal the experts out and find an
+// expert's slots by ballots.
 __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
-    const int lane = threadIdx.x & 31, slots = p.T * p.top_k;
-    for (int e = lane; e <= p.E; e += 32) r.offset[e] = 0;
-    __syncwarp();
-    for (int s = lane; s < slots; s += 32) atomicAdd(&r.offset[r.expert[s]], 1);
-    __syncwarp();
-    int before = 0, pairs_before = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-        const int e = e0 + lane;
-        const int n = e < p.E ? r.offset[e] : 0;
-        const int np = (n + group - 1) / group;
-        int sum = n, psum = np;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int a = __shfl_up_sync(0xffffffffu, sum, d), b = __shfl_up_sync(0xffffffffu, psum, d);
-            if (lane >= d) sum += a, psum += b;
-        }
-        if (e < p.E) {
-            const int first = pairs_before + psum - np, start = before + sum - n;
-            r.offset[e] = start;
-            for (int i = 0; i < np; ++i) {
-                r.pair_expert[first + i] = static_cast<uint16_t>(e);
-                r.pair_first[first + i] = static_cast<uint16_t>(first);
-                r.pair_groups[first + i] = static_cast<uint8_t>(np);
-                r.pair_start[first + i] = static_cast<uint16_t>(start + i * group);
-                r.pair_count[first + i] = static_cast<uint8_t>(min(group, n - i * group));
-            }
-        }
-        before += __shfl_sync(0xffffffffu, sum, 31);
-        pairs_before += __shfl_sync(0xffffffffu, psum, 31);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = p.T * p.top_k;
+    for (int e = warp; e < p.E; e += kWarps) {
+        int n = 0;
+        for (int s0 = 0; s0 < slots; s0 += 32)
+            n += __popc(__ballot_sync(0xffffffffu, s0 + lane < slots && r.expert[s0 + lane] == e));
+        if (lane == 0) r.offset[e] = n;
     }
-    if (lane == 0) r.pairs = pairs_before;
-    __syncwarp();
-    for (int s0 = 0; s0 < slots; s0 += 32) {
-        const int s = s0 + lane;
-        const int e = s < slots ? r.expert[s] : -1 - lane;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        const int base = s < slots ? r.offset[e] : 0;
-        __syncwarp();
-        if (s < slots) {
-            r.order[base + rank] = static_cast<uint16_t>(s);
-            if (rank == 0) r.offset[e] = base + __popc(same);
+    consumer_sync();
+    if (warp == 0) {
+        int before = 0, pairs_before = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int n = e < p.E ? r.offset[e] : 0;
+            const int np = (n + group - 1) / group;
+            int sum = n, psum = np;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int a = __shfl_up_sync(0xffffffffu, sum, d), b = __shfl_up_sync(0xffffffffu, psum, d);
+                if (lane >= d) sum += a, psum += b;
+            }
+            if (e < p.E) {
+                const int first = pairs_before + psum - np, start = before + sum - n;
+                r.offset[e] = start;
+                for (int i = 0; i < np; ++i) {
+                    r.pair_expert[first + i] = static_cast<uint16_t>(e);
+                    r.pair_first[first + i] = static_cast<uint16_t>(first);
+                    r.pair_groups[first + i] = static_cast<uint8_t>(np);
+                    r.pair_start[first + i] = static_cast<uint16_t>(start + i * group);
+                    r.pair_count[first + i] = static_cast<uint8_t>(min(group, n - i * group));
+                }
+            }
+            before += __shfl_sync(0xffffffffu, sum, 31);
+            pairs_before += __shfl_sync(0xffffffffu, psum, 31);
         }
-        __syncwarp();
+        if (lane == 0) r.pairs = pairs_before;
+    }
+    consumer_sync();
+    for (int e = warp; e < p.E; e += kWarps) {
+        int at = r.offset[e];
+        for (int s0 = 0; s0 < slots; s0 += 32) {
+            const unsigned same = __ballot_sync(0xffffffffu, s0 + lane < slots && r.expert[s0 + lane] == e);
+            if (same & (1u << lane)) r.order[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(s0 + lane);
+            at += __popc(same);
+        }
     }
 }
 
@@ -348,13 +369,13 @@ template <bool FP8>
 struct MoeCfg {
     static constexpr int kWBytes = FP8 ? 1 : 2;
     static constexpr int kBoxK = 128 / kWBytes;  // k of a box: 128 (one scale block) or 64
-    static constexpr int kScaleBytes = FP8 ? 2 * kWarps * 4 : 0;
+    static constexpr int kScaleBytes = FP8 ? kBoxes * 2 * kWarps * 4 : 0;
     static constexpr int kActOffset = kStageWeights + kScaleBytes;
     // Row strides of the activations: 4 neighbouring 16-byte pieces of 2
     // tokens (a quarter warp's load) fall on different banks.
     static constexpr int kXPad = FP8 ? 32 : 16, kHPad = FP8 ? 64 : 32;
     __host__ __device__ static constexpr int act_stride(int lw, bool first) {
-        return (8 >> lw) * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
+        return (kBoxes * kWarps >> lw) * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
     }
 };
 
@@ -448,7 +469,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const bool gated = p.up != nullptr;
     const int rows1 = (gated ? 8 : 16) << p.lw1, rows2 = 16 << p.lw2;  // rows of h and of y of a unit
     const int rg1 = (p.I + rows1 - 1) / rows1, rg2 = (p.H + rows2 - 1) / rows2;
-    const int kc1 = (8 >> p.lw1) * Cfg::kBoxK, kc2 = (8 >> p.lw2) * Cfg::kBoxK;  // k of a stage
+    const int kc1 = (kBoxes * kWarps >> p.lw1) * Cfg::kBoxK, kc2 = (kBoxes * kWarps >> p.lw2) * Cfg::kBoxK;  // k of a stage
     const int nch1 = (p.H + kc1 - 1) / kc1, nch2 = (p.I + kc2 - 1) / kc2;
 
     auto give_up = [&] {
@@ -478,11 +499,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             if (!wait_count(&p.counters[0], gridDim.x)) give_up();
         }
         consumer_sync();
-        if (!abort_flag)
-            for (int t = warp; t < p.T; t += kWarps)
-                choose_experts(p, t, reinterpret_cast<uint32_t *>(ring) + warp * kMoeMaxExperts, r);
-        consumer_sync();
-        if (warp == 0 && !abort_flag) group_slots(p, r, 8 * NT);
+        // every CTA makes the same choice, as many tokens at a time as fit
+        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
+        const int at_once = min(p.T, kChoiceKeys / p.E);
+        for (int t0 = 0; t0 < p.T; t0 += at_once) {
+            const int n = min(at_once, p.T - t0) * p.E;
+            for (int i = threadIdx.x; i < n; i += 32 * kWarps) keys[i] = logit_key(__ldcg(p.logits + t0 * p.E + i));
+            consumer_sync();
+            for (int t = t0 + warp; t < min(p.T, t0 + at_once); t += kWarps) choose_experts(p, t, keys + (t - t0) * p.E, r);
+            consumer_sync();
+        }
+        group_slots(p, r, 8 * NT);
         if (threadIdx.x == 0 && abort_flag) r.pairs = 0;
     }
     fence_proxy_async_smem();  // the ring held the keys
@@ -503,8 +530,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
         // What this lane copies for a unit, worked out once for its stages:
-        // a token's row (lane < count), and with 8-bit weights the scales of
-        // warp lane % 8's box, for its rows g (lane < 8) or g + 8.
+        // a token's row (lane < count), and with 8-bit weights one scale of
+        // the stage: box lane / 16 of warp lane % 8, its rows g or g + 8.
         int y = 0, count = 0;
         const uint8_t *token = nullptr;
         const float *scale = nullptr;
@@ -518,10 +545,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                               : reinterpret_cast<const uint8_t *>(p.hidden + static_cast<long long>(slot) * p.I);
             }
             if constexpr (FP8) {
-                const int wrow = lane & ((1 << lw) - 1), box = (lane & 7) >> lw;
+                const int wrow = lane & ((1 << lw) - 1), box = ((lane >> 4) * kWarps + (lane & 7)) >> lw;
                 const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + (lane & 8)));
                 const long long kbs = (width + kScaleBlock - 1) / kScaleBlock, nbs = (rows + kScaleBlock - 1) / kScaleBlock;
-                const float *base = !first ? p.s_down : gated && lane >= kWarps ? p.s_up : p.s_gate;
+                const float *base = !first ? p.s_down : gated && (lane & 8) ? p.s_up : p.s_gate;
                 scale = base + (n.expert * nbs + row / kScaleBlock) * kbs + box;
             }
         };
@@ -533,7 +560,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 return;
             }
             uint8_t *dst = ring + stage * p.stage_bytes;
-            const int lw = first ? p.lw1 : p.lw2, boxes = 8 >> lw, width = first ? p.H : p.I;
+            const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes * kWarps >> lw, width = first ? p.H : p.I;
             const int k0 = ch * boxes * Cfg::kBoxK, k = min(boxes * Cfg::kBoxK, width - k0);
             if (lane == 0) {
                 mbar_arrive_expect_tx(&full[stage], kStageWeights + count * k * (first ? 2 : 4));
@@ -558,7 +585,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             }
             __syncwarp();
             if constexpr (FP8) {
-                if (lane < 2 * kWarps && k0 + ((lane & 7) >> lw) * Cfg::kBoxK < width)
+                if (k0 + (((lane >> 4) * kWarps + (lane & 7)) >> lw) * Cfg::kBoxK < width)
                     cp_async_4(dst + kStageWeights + lane * 4, scale + ch * boxes, 4);
                 cp_async_arrive(&full[stage]);
             }
@@ -567,7 +594,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         };
         // The activations of the same k.
         auto load_tokens = [&](bool first, int ch, int at) {
-            const int lw = first ? p.lw1 : p.lw2, kc = (8 >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
+            const int lw = first ? p.lw1 : p.lw2, kc = (kBoxes * kWarps >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
             const int bytes = first ? 2 : 4;
             if (lane < count)
                 bulk_load(ring + at * p.stage_bytes + Cfg::kActOffset + lane * Cfg::act_stride(lw, first), token + k0 * bytes, k * bytes,
@@ -634,43 +661,60 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         // One unit's sums for this warp's row group and box column.
         auto unit_sums = [&](auto first_c, const Unit &n, float(&acc)[NT][4]) {
             constexpr bool kFirst = decltype(first_c)::value;
-            const int lw = kFirst ? p.lw1 : p.lw2, boxes = 8 >> lw, my_row = warp & ((1 << lw) - 1), my_box = warp >> lw;
+            // The warp has box columns my_box and my_box + sharers.
+            const int lw = kFirst ? p.lw1 : p.lw2, sharers = kWarps >> lw, my_row = warp & ((1 << lw) - 1), my_box = warp >> lw;
             const bool halves = kFirst && gated;
-            const int w_off = warp * (halves ? 1024 : 2048);
-            const int row8 = halves ? kStageWeights / 2 : 1024;
+            const int w_box = halves ? 1024 : 2048, row8 = halves ? kStageWeights / 2 : 1024;
             const int stride = Cfg::act_stride(lw, kFirst), width = kFirst ? p.H : p.I;
+            float part[kBoxes][NT][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            for (int b = 0; b < kBoxes; ++b)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) part[b][i][0] = part[b][i][1] = part[b][i][2] = part[b][i][3] = 0.f;
             for (int ch = n.ch0; ch < n.ch1; ++ch) {
                 // after a time-out everything runs through without waiting
                 if (!abort_flag && !mbar_wait_patient(&full[stage], phase)) give_up();
                 const uint8_t *st = ring + stage * p.stage_bytes;
-                const int k0 = (ch * boxes + my_box) * Cfg::kBoxK;
-                if (k0 < width) {
-                    const uint8_t *w0 = st + w_off + g * 128;
-                    const uint8_t *act = st + Cfg::kActOffset + my_box * Cfg::kBoxK * (kFirst ? 2 : 4);
-                    if constexpr (FP8) {
-                        float sum[NT][4] = {};
-                        multiply_box<XT, FP8, NT, kFirst>(w0, w0 + row8, act, stride, width - k0, n.count, sum);
-                        const float *sc = reinterpret_cast<const float *>(st + kStageWeights);
-                        const float s0 = sc[warp], s1 = sc[kWarps + warp];
+                const uint8_t *w0 = st + warp * w_box + g * 128, *act = st + Cfg::kActOffset + my_box * Cfg::kBoxK * (kFirst ? 2 : 4);
+                const int valid = width - (ch * kBoxes * sharers + my_box) * Cfg::kBoxK;
+                if constexpr (FP8) {
+                    const float *sc = reinterpret_cast<const float *>(st + kStageWeights) + warp;
+                    float sum[kBoxes][NT][4] = {};
+#pragma unroll
+                    for (int b = 0; b < kBoxes; ++b)
+                        multiply_box<XT, FP8, NT, kFirst>(w0 + b * kWarps * w_box, w0 + b * kWarps * w_box + row8,
+                                                          act + b * sharers * Cfg::kBoxK * (kFirst ? 2 : 4), stride,
+                                                          valid - b * sharers * Cfg::kBoxK, n.count, sum[b]);
+#pragma unroll
+                    for (int b = 0; b < kBoxes; ++b) {
+                        // a box past the end has no scale: its sums are zeros
+                        const bool in = valid > b * sharers * Cfg::kBoxK;
+                        const float s0 = in ? sc[b * 2 * kWarps] : 0.f, s1 = in ? sc[b * 2 * kWarps + kWarps] : 0.f;
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            acc[i][0] = fmaf(s0, sum[i][0], acc[i][0]);
-                            acc[i][1] = fmaf(s0, sum[i][1], acc[i][1]);
-                            acc[i][2] = fmaf(s1, sum[i][2], acc[i][2]);
-                            acc[i][3] = fmaf(s1, sum[i][3], acc[i][3]);
+                            part[b][i][0] = fmaf(s0, sum[b][i][0], part[b][i][0]);
+                            part[b][i][1] = fmaf(s0, sum[b][i][1], part[b][i][1]);
+                            part[b][i][2] = fmaf(s1, sum[b][i][2], part[b][i][2]);
+                            part[b][i][3] = fmaf(s1, sum[b][i][3], part[b][i][3]);
                         }
-                    } else {
-                        multiply_box<XT, FP8, NT, kFirst>(w0, w0 + row8, act, stride, width - k0, n.count, acc);
                     }
+                } else {
+#pragma unroll
+                    for (int b = 0; b < kBoxes; ++b)
+                        multiply_box<XT, FP8, NT, kFirst>(w0 + b * kWarps * w_box, w0 + b * kWarps * w_box + row8,
+                                                          act + b * sharers * Cfg::kBoxK * (kFirst ? 2 : 4), stride,
+                                                          valid - b * sharers * Cfg::kBoxK, n.count, part[b]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
                 if (++stage == p.stages) stage = 0, phase ^= 1u;
             }
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = part[0][i][j] + part[1][i][j];
             // Warps of the same rows: the first one adds the others' sums.
-            if (boxes > 1) {
+            if (sharers > 1) {
                 if (my_box > 0) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
@@ -683,7 +727,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                     for (int i = 0; i < NT; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            for (int b = 1; b < boxes; ++b) acc[i][j] += red[buf][(b << lw) + my_row][i][j][lane];
+                            for (int b = 1; b < sharers; ++b) acc[i][j] += red[buf][(b << lw) + my_row][i][j][lane];
                 }
                 buf ^= 1;
             }
@@ -768,42 +812,55 @@ bool encode_expert_map(CUtensorMap *map, const void *base, int elem_bytes, CUten
                 : encode_box_map(map, dt, base, width, all_rows, 1, width * elem_bytes, width * elem_bytes, piece, box_rows, 1);
 }
 
-// log2 of WR, the row groups of a unit: the most (8, 4, 2, 1) whose units
-// (groups_of_one of them with one row group) keep the SMs busy to 90 % in
-// whole rounds, but at least as many as hold a stage's activations (act_bytes
-// with one row group) within twice its weights, so that the ring keeps enough
-// stages.
-int pick_row_groups(double groups_of_one, int sms, int act_bytes) {
+// How a phase is cut into units: log2 of WR, and of the down projection also
+// how many units share a row group's k.  `groups` row groups of 16 (one of each
+// expert that is used), `k` long; `act_bytes` of activations in a stage with
+// WR = 1.  Preferred is the largest WR, then the fewest splits, whose units
+// fill whole rounds over the SMs to 94 %; failing that, what fills them best.
+// WR is at least what keeps a stage's activations within its weights (the ring
+// would hold too few stages) and a stage's k below the whole length.
+struct Cut {
+    int lw = 0, splits = 1;
+};
+Cut pick_cut(double groups, int k, int box_k, int act_bytes, int max_splits, int sms) {
     int least = 0;
-    while (least < 3 && (act_bytes >> least) > 2 * kStageWeights) ++least;
-    for (int lw = 3; lw > least; --lw) {
-        const double units = groups_of_one / (1 << lw);
-        if (units >= 0.9 * std::ceil(units / sms) * sms) return lw;
-    }
-    return least;
+    while (least < 3 && ((act_bytes >> least) > kStageWeights || (kBoxes * kWarps >> least) * box_k >= 2 * k)) ++least;
+    Cut best;
+    double best_fill = -1.0;
+    for (int lw = 3; lw >= least; --lw)
+        for (int splits = 1; splits <= max_splits; splits *= 2) {
+            if (splits > 1 && (kBoxes * kWarps >> lw) * box_k * splits * 2 > k) break;  // two stages at least
+            const double units = std::max(1.0, groups / (1 << lw) * splits);
+            const double fill = units / (std::ceil(units / sms - 1e-9) * sms);
+            if (fill > best_fill + 1e-9) best_fill = fill, best.lw = lw, best.splits = splits;
+            if (fill >= 0.94) return best;
+        }
+    return best;
 }
 
 template <int XT, bool FP8, int NT>
 cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stream) {
     using Cfg = MoeCfg<FP8>;
     auto kern = moe_kernel<XT, FP8, NT>;
-    const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * 8 * Cfg::kBoxK * 2;  // of X rows; h rows twice that
-    a.lw1 = pick_row_groups(active * m.I / (m.up ? 8 : 16), sms, act);
-    a.lw2 = pick_row_groups(active * m.H / 16, sms, 2 * act);
+    const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * kBoxes * kWarps * Cfg::kBoxK * 2;  // of X rows; h rows twice that
+    const Cut c1 = pick_cut(active * m.I / (m.up ? 8 : 16), m.H, Cfg::kBoxK, act, 1, sms);
+    const Cut c2 = pick_cut(active * m.H / 16, m.I, Cfg::kBoxK, 2 * act, kMaxSplits, sms);
+    a.lw1 = c1.lw;
+    a.lw2 = c2.lw;
+    a.k_splits = c2.splits;
     // a stage holds the weights, their scales and either kind of activations
     const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.lw1, true), Cfg::act_stride(a.lw2, false));
     a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
     constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * kWarps * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
-    static_assert(kRing >= 1024 + kWarps * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
-    a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);
-    if (a.stages < 2) return cudaErrorInvalidConfiguration;
+    static_assert(kRing >= 1024 + kChoiceKeys * 4 && kChoiceKeys >= kMoeMaxExperts, "the ring holds the keys of the choice");
+    a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);  // two at least: 2 x (32 + 32) KB and paddings
     const int wb = Cfg::kWBytes;
     const auto dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     a.flat_h = m.H * wb % 128 == 0;
     a.flat_i = m.I * wb % 128 == 0;
     CUtensorMap tg, tu, td;
     const uint64_t rows_i = static_cast<uint64_t>(m.E) * m.I, rows_h = static_cast<uint64_t>(m.E) * m.H;
-    const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = 8 >> a.lw1, rows2 = 16 << a.lw2, boxes2 = 8 >> a.lw2;
+    const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = kBoxes * kWarps >> a.lw1, rows2 = 16 << a.lw2, boxes2 = kBoxes * kWarps >> a.lw2;
     if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
         !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
         !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, rows2, boxes2))
@@ -862,10 +919,9 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     // Experts with any token if the router chose evenly, and tokens of one.
     const double slots = static_cast<double>(m.T) * m.top_k;
     const double active = m.E * (1.0 - std::pow(1.0 - static_cast<double>(m.top_k) / m.E, m.T)), tokens = slots / active;
-    a.k_splits = 1;
     const size_t n_logits = (static_cast<size_t>(m.T) * m.E + 63) / 64 * 64, n_hidden = static_cast<size_t>(slots) * m.I;
     Scratch s;
-    const cudaError_t e = acquire_scratch(stream, n_logits + n_hidden + static_cast<size_t>(slots) * m.H * a.k_splits, 4, &s);
+    const cudaError_t e = acquire_scratch(stream, n_logits + n_hidden + static_cast<size_t>(slots) * m.H * kMaxSplits, 4, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
     a.hidden = s.partials + n_logits;

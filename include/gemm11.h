@@ -355,7 +355,7 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  * ldx a multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
  * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
  * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive
- * otherwise.  Scratch: T E + T top_k (H + I) floats of library-owned device
+ * otherwise.  Scratch: T E + T top_k (4 H + I) floats of library-owned device
  * memory per stream.  A call under stream capture may allocate it, and a graph
  * keeps the scratch it was captured with: replays of it must not overlap on
  * the GPU with each other or with calls on the stream that it was captured on.
