@@ -18,8 +18,8 @@
 //   * a producer warp fills a ring of stages.  It runs ahead of the arithmetic
 //     across units, and into the down projection while the other CTAs still
 //     finish the first half;
-//   * eight warps take a stage's WR row groups x 16 / WR boxes, two each, and
-//     multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
+//   * the other warps take a stage's WR row groups x 16 / WR boxes, one or two
+//     each, and multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
 //     share rows add their sums in warp order in shared memory at the unit's
 //     end.  The matrix instruction is the warp-level one: a unit has 1 to 8 NT
 //     columns of a 128-column tcgen05 tile and is bound by memory, and
@@ -33,11 +33,20 @@
 // experts) CTAs meet at grid barriers; every sum has a fixed order, so results
 // do not depend on timing.  Every wait is bounded.
 //
-// Numbers: weights and tokens of the same 16-bit type multiply exactly in
-// mma.sync's native type; 8-bit weights and the down projection use TF32,
-// which holds every 16- and 8-bit value exactly.  Sums are FP32.  h is rounded
-// once, to TF32 (11 significant bits, FP32's range: a 16-bit type would lose
-// either bits or range).
+// Numbers.  Every product is a 16-bit x 16-bit mma.sync with FP32 sums; what
+// the activations are held in depends on the weights:
+//   BF16 weights   X as it is; h as the sum of two BF16 numbers (16 significant
+//                  bits, FP32's range), two products each;
+//   FP16 weights   X as it is; h in FP16 after scaling a token's h by the power
+//                  of two that brings its largest element to [2^14, 2^15): 11
+//                  bits down to 2^-28 of the largest, nothing overflows.  h is
+//                  written in FP32 first and converted, with its maximum known,
+//                  between two grid barriers, while the ring fills with weights;
+//   e4m3 weights   widened to FP16 (exact), one conversion for two elements
+//                  (TF32 products took two more each, and twice the matrix
+//                  instructions: 3.2 TB/s against 4.x); h as for FP16, and a
+//                  BF16 X too (8 bits: exact down to 2^-31 of the largest).
+// The e4m3 scale of a 128 x 128 block multiplies that block's FP32 sum.
 #include <algorithm>
 #include <cstdint>
 
@@ -51,10 +60,8 @@
 namespace gemm11 {
 namespace {
 
-constexpr int kWarps = 8;                       // consumer warps
-constexpr int kMoeThreads = 32 * (kWarps + 1);  // and the producer warp
 constexpr int kStageWeights = 32768;            // bytes of weights in a stage
-constexpr int kBoxes = 2;                       // 16 rows x 128 bytes boxes of a warp in a stage
+constexpr int kBoxes = 16;                      // of 16 rows x 128 bytes in a stage
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 4;                   // units that share a row group's k in the down projection
 constexpr int kChoiceKeys = 16384;              // logits looked at together
@@ -72,8 +79,14 @@ struct MoeArgs {
     int y_type, act, renorm;
     int *ids;
     float *weights;
-    float *logits, *hidden, *part;  // scratch: T x E, slots x I, k_splits x slots x H
-    unsigned *counters;             // three barriers and the exit
+    // Scratch: T x E logits; h in FP32 (slots x I), or two BF16 parts in
+    // alternate runs of 64; h and X in FP16, scaled; the largest |h| of a slot,
+    // and the scale of a token; k_splits x slots x H partial results.
+    float *logits, *hidden, *part;
+    __half *hidden16, *x16;
+    unsigned *h_max;
+    float *x_scale;
+    unsigned *counters;  // four barriers and the exit
     unsigned *err;
     int lw1, lw2;    // log2 of WR, the row groups (of 16 rows) of a unit, in the first half and in the down projection
     int k_splits;    // units of the down projection that share a row group's k
@@ -84,6 +97,7 @@ struct MoeArgs {
 // Shared-memory tables of the routing, the same in every CTA.
 struct Routing {
     float weight[kMoeMaxSlots];
+    float x_scale[kMoeMaxTokens];   // what a token's sums are multiplied by
     uint16_t expert[kMoeMaxSlots];  // of slot t * top_k + j
     uint16_t order[kMoeMaxSlots];   // slots, grouped by expert, ascending
     uint16_t pair_expert[kMoeMaxSlots], pair_first[kMoeMaxSlots], pair_start[kMoeMaxSlots];
@@ -92,13 +106,6 @@ struct Routing {
     int pairs;
 };
 
-__device__ __forceinline__ void mma_tf32(float (&c)[4], const float (&a)[4], float b0, float b1) {
-    asm(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2])), "r"(__float_as_uint(a[3])),
-          "r"(__float_as_uint(b0)), "r"(__float_as_uint(b1)));
-}
 template <int XT>
 __device__ __forceinline__ void mma_16bit(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -128,7 +135,10 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
-__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int WARPS>
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory");
+}
 __device__ __forceinline__ unsigned load_acquire(const unsigned *p) {
     unsigned v;
     asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
@@ -150,26 +160,28 @@ __device__ __forceinline__ float moe_act(int act, float v) {
 
 // Eight neighbouring values of a row as floats.
 __device__ __forceinline__ void widen8(const uint4 &w, int type, float (&v)[8]) { unpack8_out16(w, type, v); }
-__device__ __forceinline__ void widen4(uint32_t lo, uint32_t hi, int type, float (&v)[4]) {
-    if (type == kOutF16) {
-        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo)), b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-        v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
-    } else {
-        v[0] = __uint_as_float(lo << 16), v[1] = __uint_as_float(lo & 0xFFFF0000u);
-        v[2] = __uint_as_float(hi << 16), v[3] = __uint_as_float(hi & 0xFFFF0000u);
-    }
+// Four e4m3 values of a word as two FP16 pairs.
+__device__ __forceinline__ void widen_e4m3(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xFFFFu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    lo = *reinterpret_cast<const uint32_t *>(&a);
+    hi = *reinterpret_cast<const uint32_t *>(&b);
 }
-// N e4m3 values, four in a word, as floats.
-template <int N>
-__device__ __forceinline__ void widen_e4m3(const uint32_t *w, float *v) {
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[i / 2] >> (16 * (i & 1))), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
+// Four 8 x 16-byte matrices, whose rows' addresses the lanes give in turn:
+// word i of thread (g, t) is bytes [4 t, 4 t + 4) of row g of matrix i.
+__device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
+// 2^e that brings a largest magnitude into [2^14, 2^15), and 2^-e.  Normal
+// numbers both (a maximum below 2^-112 stays smaller); 1 for zero.
+__device__ __forceinline__ int fit_exponent(float largest) {
+    const int field = static_cast<int>(__float_as_uint(largest) >> 23) & 0xFF;
+    return largest == 0.f ? 0 : min(126, 14 + 127 - field);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }
 
 // ---------------------------------------------------------------- routing
 // Sum of w x over `threads` threads' share of H for one expert and 8 tokens.
@@ -208,7 +220,7 @@ __device__ __forceinline__ void router_dot(const MoeArgs &p, int e, int t0, int 
 
 // All logits, in units of one expert and 8 tokens: a CTA takes a unit while
 // there are no more units than CTAs (its warps share H), else each warp does.
-template <int XT>
+template <int XT, int kWarps>
 __device__ void router_logits(const MoeArgs &p, float *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int groups = (p.T + 7) / 8, units = p.E * groups;
@@ -227,7 +239,7 @@ __device__ void router_logits(const MoeArgs &p, float *red) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (lane == i) red[warp * 8 + i] = acc[i];
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (threadIdx.x < 8 && t0 + threadIdx.x < p.T) {
             float v = 0.f;
 #pragma unroll
@@ -235,6 +247,37 @@ __device__ void router_logits(const MoeArgs &p, float *red) {
             p.logits[(t0 + threadIdx.x) * p.E + e] = v;
         }
     }
+}
+
+// One token's X in FP16, scaled, by a whole CTA.
+template <int XT, int kWarps>
+__device__ void scale_token(const MoeArgs &p, int t, float *red) {
+    const uint16_t *x = static_cast<const uint16_t *>(p.X) + t * p.ldx;
+    float m = 0.f;
+    for (int k = threadIdx.x * 8; k < p.H; k += 32 * kWarps * 8) {
+        float v[8];
+        widen8(__ldg(reinterpret_cast<const uint4 *>(x + k)), XT, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(v[i]) < INFINITY) m = fmaxf(m, fabsf(v[i]));
+    }
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+    consumer_sync<kWarps>();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red[w]);
+    consumer_sync<kWarps>();
+    const int e = fit_exponent(m);
+    const float f = pow2(e);
+    for (int k = threadIdx.x * 8; k < p.H; k += 32 * kWarps * 8) {
+        float v[8];
+        widen8(__ldg(reinterpret_cast<const uint4 *>(x + k)), XT, v);
+        *reinterpret_cast<uint4 *>(p.x16 + static_cast<long long>(t) * p.H + k) =
+            make_uint4(pack2_out16(v[0] * f, v[1] * f, kOutF16), pack2_out16(v[2] * f, v[3] * f, kOutF16),
+                       pack2_out16(v[4] * f, v[5] * f, kOutF16), pack2_out16(v[6] * f, v[7] * f, kOutF16));
+    }
+    if (threadIdx.x == 0) p.x_scale[t] = pow2(-e);
 }
 
 // Order-preserving key of a logit: -0 equals +0, NaN comes first; 0 is below
@@ -281,6 +324,7 @@ __device__ void choose_experts(const MoeArgs &p, int t, uint32_t *keys, Routing 
 // Slots grouped by expert, in ascending order, and the (expert, token group)
 // pairs that the units go over.  The warps deal the experts out and find an
 // expert's slots by ballots.
+template <int kWarps>
 __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = p.T * p.top_k;
     for (int e = warp; e < p.E; e += kWarps) {
@@ -289,7 +333,7 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
             n += __popc(__ballot_sync(0xffffffffu, s0 + lane < slots && r.expert[s0 + lane] == e));
         if (lane == 0) r.offset[e] = n;
     }
-    consumer_sync();
+    consumer_sync<kWarps>();
     if (warp == 0) {
         int before = 0, pairs_before = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
@@ -318,7 +362,7 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
         }
         if (lane == 0) r.pairs = pairs_before;
     }
-    consumer_sync();
+    consumer_sync<kWarps>();
     for (int e = warp; e < p.E; e += kWarps) {
         int at = r.offset[e];
         for (int s0 = 0; s0 < slots; s0 += 32) {
@@ -330,6 +374,9 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
 }
 
 // ---------------------------------------------------------------- units
+// Bytes of a slot's h as two BF16 parts.
+__host__ __device__ constexpr long long parts_bytes(int I) { return (I + 63ll) / 64 * 256; }
+
 struct Unit {
     int expert, row, start, count;  // first matrix row (of the expert), first slot in `order`, tokens
     int ch0, ch1, split;            // stages
@@ -365,100 +412,85 @@ __device__ __forceinline__ Unit down_unit(const Routing &r, int u, int rows, int
     return n;
 }
 
-template <bool FP8>
+template <int XT, bool FP8>
 struct MoeCfg {
     static constexpr int kWBytes = FP8 ? 1 : 2;
     static constexpr int kBoxK = 128 / kWBytes;  // k of a box: 128 (one scale block) or 64
-    static constexpr int kScaleBytes = FP8 ? kBoxes * 2 * kWarps * 4 : 0;
+    static constexpr bool kTwoParts = !FP8 && XT == kOutBF16;  // h as two BF16 numbers
+    static constexpr bool kScaledX = FP8 && XT == kOutBF16;    // X as scaled FP16
+    static constexpr int kMma = FP8 ? kOutF16 : XT;
+    static constexpr int kXBytes = 2, kHBytes = kTwoParts ? 4 : 2;
+    static constexpr int kScaleBytes = FP8 ? kBoxes * 2 * 4 : 0;
     static constexpr int kActOffset = kStageWeights + kScaleBytes;
-    // Row strides of the activations: 4 neighbouring 16-byte pieces of 2
-    // tokens (a quarter warp's load) fall on different banks.
-    static constexpr int kXPad = FP8 ? 32 : 16, kHPad = FP8 ? 64 : 32;
+    // Row strides of the activations: the 8 threads of a quarter warp (16 of
+    // half a warp with 8-byte loads) fall on different banks.
+    static constexpr int kPad = FP8 ? 32 : 16;
     __host__ __device__ static constexpr int act_stride(int lw, bool first) {
-        return (kBoxes * kWarps >> lw) * kBoxK * (first ? 2 : 4) + (first ? kXPad : kHPad);
+        return (kBoxes >> lw) * kBoxK * (first ? kXBytes : kHBytes) + kPad;
     }
 };
 
-// This warp's 16 rows x one box of k times the tokens, added to acc.  Thread
-// (g, t) has rows g and g + 8 (w0, w1: their 128 bytes, 16-byte chunk c at
-// c ^ g by the copy's swizzle) at the k of chunks 2 t + s, and token 8 n + g at
-// the same k.  FIRST: tokens are X rows of 16 bits, else FP32 h rows, of
-// `valid` k's.  Where a chunk is two or four pieces of activations, the threads
-// take them in an order turned by t (no bank conflicts), and their weights with
-// them.
-template <int XT, bool FP8, int NT, bool FIRST>
-__device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *act, int stride, int valid,
-                                             int count, float (&c)[NT][4]) {
-    using Cfg = MoeCfg<FP8>;
+// This warp's 16 rows x one box of k times the tokens, added to c.  Thread
+// (g, t) holds rows g and g + 8, token 8 n + g and the same k's of both; w0 and
+// w1 are the first of each 8 rows (16-byte chunk c of row g at c ^ g, by the
+// copy's swizzle), act[n] its token's k's of this box.  PARTS: the second BF16
+// parts follow the first after 128 bytes.  TAIL: only `valid` k's exist; the
+// weights past them are zeros, the activations are left over from other stages.
+template <int XT, bool FP8, int NT, bool PARTS, bool TAIL>
+__device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *const (&act)[NT], int valid,
+                                             float (&c)[NT][4]) {
+    using Cfg = MoeCfg<XT, FP8>;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    constexpr int kChunkK = 16 / Cfg::kWBytes;           // k of a 16-byte chunk: 16 or 8
-    constexpr int kPieceK = FIRST ? 8 : 4;               // k of a 16-byte piece of activations
-    constexpr int kPieces = kChunkK / kPieceK;           // 1, 2 or 4
-    constexpr int kActBytes = FIRST ? 2 : 4;
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if constexpr (FP8) {
+        // Lanes 0-7 and 8-15 give the two groups' rows of one chunk, 16-31 of the next.
+        const uint32_t row = smem_u32((lane & 8) ? w1 : w0) + (lane & 7) * 128;
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        const int chunk = 2 * t + s;
-        uint4 a = *reinterpret_cast<const uint4 *>(w0 + ((chunk ^ g) << 4));
-        uint4 b = *reinterpret_cast<const uint4 *>(w1 + ((chunk ^ g) << 4));
-        const int turn = kPieces == 4 ? t : kPieces == 2 ? t >> 1 : 0;
-        if constexpr (kPieces == 2) {
-            if (turn) a = make_uint4(a.z, a.w, a.x, a.y), b = make_uint4(b.z, b.w, b.x, b.y);
-        }
-        if constexpr (kPieces == 4) {
-            if (turn & 1) a = make_uint4(a.y, a.x, a.w, a.z), b = make_uint4(b.y, b.x, b.w, b.z);
-            if (turn & 2) a = make_uint4(a.z, a.w, a.x, a.y), b = make_uint4(b.z, b.w, b.x, b.y);
-        }
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        for (int ch = 0; ch < 8; ch += 2) {
+            uint32_t w[4];
+            load_matrices(row + (((ch + (lane >> 4)) ^ (lane & 7)) << 4), w);
 #pragma unroll
-        for (int j = 0; j < kPieces; ++j) {
-            const int k = chunk * kChunkK + (j ^ turn) * kPieceK;
-            uint4 x[NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                x[n] = k < valid && n * 8 + g < count ? *reinterpret_cast<const uint4 *>(act + (n * 8 + g) * stride + k * kActBytes) : zero;
-            if constexpr (!FP8 && FIRST) {
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a0, a1, a2, a3;
+                widen_e4m3(w[2 * h], a0, a2);
+                widen_e4m3(w[2 * h + 1], a1, a3);
+                const int k = (ch + h) * 16 + t * 4;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    mma_16bit<XT>(c[n], aw[0], bw[0], aw[1], bw[1], x[n].x, x[n].y);
-                    mma_16bit<XT>(c[n], aw[2], bw[2], aw[3], bw[3], x[n].z, x[n].w);
-                }
-            } else {
-                float wa[kPieceK], wb[kPieceK];
-                if constexpr (FP8 && FIRST) {
-                    widen_e4m3<8>(&aw[2 * j], wa);
-                    widen_e4m3<8>(&bw[2 * j], wb);
-                } else if constexpr (FP8) {
-                    widen_e4m3<4>(&aw[j], wa);
-                    widen_e4m3<4>(&bw[j], wb);
-                } else {
-                    widen4(aw[2 * j], aw[2 * j + 1], XT, wa);
-                    widen4(bw[2 * j], bw[2 * j + 1], XT, wb);
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float xf[8];
-                    if constexpr (FIRST)
-                        widen8(x[n], XT, xf);
-                    else
-                        xf[0] = __uint_as_float(x[n].x), xf[1] = __uint_as_float(x[n].y), xf[2] = __uint_as_float(x[n].z),
-                        xf[3] = __uint_as_float(x[n].w);
-#pragma unroll
-                    for (int i = 0; i < kPieceK / 2; ++i) {
-                        const float f[4] = {wa[2 * i], wb[2 * i], wa[2 * i + 1], wb[2 * i + 1]};
-                        mma_tf32(c[n], f, xf[2 * i], xf[2 * i + 1]);
-                    }
+                    uint2 x = *reinterpret_cast<const uint2 *>(act[n] + k * 2);
+                    if (TAIL && k >= valid) x = make_uint2(0, 0);
+                    mma_16bit<Cfg::kMma>(c[n], a0, a1, a2, a3, x.x, x.y);
                 }
             }
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int chunk = 2 * t + s;
+            const uint4 a = *reinterpret_cast<const uint4 *>(w0 + g * 128 + ((chunk ^ g) << 4));
+            const uint4 b = *reinterpret_cast<const uint4 *>(w1 + g * 128 + ((chunk ^ g) << 4));
+#pragma unroll
+            for (int part = 0; part < (PARTS ? 2 : 1); ++part)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    uint4 x = *reinterpret_cast<const uint4 *>(act[n] + part * 128 + chunk * 16);
+                    if (TAIL && chunk * 8 >= valid) x = make_uint4(0, 0, 0, 0);
+                    mma_16bit<Cfg::kMma>(c[n], a.x, b.x, a.y, b.y, x.x, x.y);
+                    mma_16bit<Cfg::kMma>(c[n], a.z, b.z, a.w, b.w, x.z, x.w);
+                }
         }
     }
 }
 
+// Consumer warps: sixteen with one box each while their registers last (16
+// tokens), else eight with two boxes.
+constexpr int moe_warps(int nt) { return nt <= 2 ? 16 : 8; }
+
 template <int XT, bool FP8, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 1)
+__global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
     moe_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
                const __grid_constant__ CUtensorMap tm_down, const MoeArgs p) {
-    using Cfg = MoeCfg<FP8>;
+    using Cfg = MoeCfg<XT, FP8>;
+    constexpr int kWarps = moe_warps(NT), kMine = kBoxes / kWarps;  // boxes of a warp in a stage
     extern __shared__ uint8_t ring_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Routing r;
@@ -469,7 +501,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     const bool gated = p.up != nullptr;
     const int rows1 = (gated ? 8 : 16) << p.lw1, rows2 = 16 << p.lw2;  // rows of h and of y of a unit
     const int rg1 = (p.I + rows1 - 1) / rows1, rg2 = (p.H + rows2 - 1) / rows2;
-    const int kc1 = (kBoxes * kWarps >> p.lw1) * Cfg::kBoxK, kc2 = (kBoxes * kWarps >> p.lw2) * Cfg::kBoxK;  // k of a stage
+    const int kc1 = (kBoxes >> p.lw1) * Cfg::kBoxK, kc2 = (kBoxes >> p.lw2) * Cfg::kBoxK;  // k of a stage
     const int nch1 = (p.H + kc1 - 1) / kc1, nch2 = (p.I + kc2 - 1) / kc2;
 
     auto give_up = [&] {
@@ -491,32 +523,39 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 
     // ---------------------------------------------------- router
     if (warp < kWarps) {
-        router_logits<XT>(p, &red[0][0][0][0][0]);
+        if (blockIdx.x == 0)
+            for (int i = threadIdx.x; i < p.T * p.top_k; i += 32 * kWarps) p.h_max[i] = 0u;
+        if constexpr (Cfg::kScaledX) {
+            for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) scale_token<XT, kWarps>(p, t, &red[0][0][0][0][0]);
+            fence_proxy_async_all();  // x16 is read by bulk copies
+        }
+        router_logits<XT, kWarps>(p, &red[0][0][0][0][0]);
         __threadfence();
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (threadIdx.x == 0) {
             atomicAdd(&p.counters[0], 1u);
             if (!wait_count(&p.counters[0], gridDim.x)) give_up();
         }
-        consumer_sync();
+        consumer_sync<kWarps>();
         // every CTA makes the same choice, as many tokens at a time as fit
         uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
         const int at_once = min(p.T, kChoiceKeys / p.E);
         for (int t0 = 0; t0 < p.T; t0 += at_once) {
             const int n = min(at_once, p.T - t0) * p.E;
             for (int i = threadIdx.x; i < n; i += 32 * kWarps) keys[i] = logit_key(__ldcg(p.logits + t0 * p.E + i));
-            consumer_sync();
+            consumer_sync<kWarps>();
             for (int t = t0 + warp; t < min(p.T, t0 + at_once); t += kWarps) choose_experts(p, t, keys + (t - t0) * p.E, r);
-            consumer_sync();
+            consumer_sync<kWarps>();
         }
-        group_slots(p, r, 8 * NT);
+        group_slots<kWarps>(p, r, 8 * NT);
         if (threadIdx.x == 0 && abort_flag) r.pairs = 0;
+        for (int t = threadIdx.x; t < p.T; t += 32 * kWarps) r.x_scale[t] = Cfg::kScaledX ? __ldcg(p.x_scale + t) : 1.f;
     }
-    fence_proxy_async_smem();  // the ring held the keys
+    fence_proxy_async_all();  // the ring held the keys; x16 of other CTAs is read by bulk copies
     __syncthreads();
     const int units1 = r.pairs * rg1, units2 = r.pairs * rg2 * p.k_splits;
     if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s < p.T * p.top_k && r.pairs; s += kMoeThreads) {
+        for (int s = threadIdx.x; s < p.T * p.top_k && r.pairs; s += 32 * (kWarps + 1)) {
             if (p.ids) p.ids[s] = r.expert[s];
             if (p.weights) p.weights[s] = r.weight[s];
         }
@@ -531,7 +570,11 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         bool ok = true;
         // What this lane copies for a unit, worked out once for its stages:
         // a token's row (lane < count), and with 8-bit weights one scale of
-        // the stage: box lane / 16 of warp lane % 8, its rows g or g + 8.
+        // the stage: of box lane % 16, its rows g or g + 8.
+        // Bytes of a token's k elements (two parts come in whole runs of 64).
+        auto act_bytes = [](bool first, int k) {
+            return first ? k * Cfg::kXBytes : Cfg::kTwoParts ? (k + 63) / 64 * 256 : k * Cfg::kHBytes;
+        };
         int y = 0, count = 0;
         const uint8_t *token = nullptr;
         const float *scale = nullptr;
@@ -541,14 +584,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             count = n.count;
             if (lane < count) {
                 const int slot = r.order[n.start + lane];
-                token = first ? static_cast<const uint8_t *>(p.X) + 2 * (slot / p.top_k * p.ldx)
-                              : reinterpret_cast<const uint8_t *>(p.hidden + static_cast<long long>(slot) * p.I);
+                const int t = slot / p.top_k;
+                if (first)
+                    token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
+                                          : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
+                else
+                    token = Cfg::kTwoParts ? reinterpret_cast<const uint8_t *>(p.hidden) + slot * parts_bytes(p.I)
+                                           : reinterpret_cast<const uint8_t *>(p.hidden16 + static_cast<long long>(slot) * p.I);
             }
             if constexpr (FP8) {
-                const int wrow = lane & ((1 << lw) - 1), box = ((lane >> 4) * kWarps + (lane & 7)) >> lw;
-                const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + (lane & 8)));
+                const int wrow = lane & ((1 << lw) - 1), box = (lane & 15) >> lw, upper = lane >> 4;
+                const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + upper * 8));
                 const long long kbs = (width + kScaleBlock - 1) / kScaleBlock, nbs = (rows + kScaleBlock - 1) / kScaleBlock;
-                const float *base = !first ? p.s_down : gated && (lane & 8) ? p.s_up : p.s_gate;
+                const float *base = !first ? p.s_down : gated && upper ? p.s_up : p.s_gate;
                 scale = base + (n.expert * nbs + row / kScaleBlock) * kbs + box;
             }
         };
@@ -560,10 +608,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                 return;
             }
             uint8_t *dst = ring + stage * p.stage_bytes;
-            const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes * kWarps >> lw, width = first ? p.H : p.I;
+            const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes >> lw, width = first ? p.H : p.I;
             const int k0 = ch * boxes * Cfg::kBoxK, k = min(boxes * Cfg::kBoxK, width - k0);
             if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], kStageWeights + count * k * (first ? 2 : 4));
+                mbar_arrive_expect_tx(&full[stage], kStageWeights + count * act_bytes(first, k));
                 if (first) {
                     const int half = gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
                     if (p.flat_h) {
@@ -585,7 +633,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             }
             __syncwarp();
             if constexpr (FP8) {
-                if (k0 + (((lane >> 4) * kWarps + (lane & 7)) >> lw) * Cfg::kBoxK < width)
+                if (k0 + ((lane & 15) >> lw) * Cfg::kBoxK < width)
                     cp_async_4(dst + kStageWeights + lane * 4, scale + ch * boxes, 4);
                 cp_async_arrive(&full[stage]);
             }
@@ -594,11 +642,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         };
         // The activations of the same k.
         auto load_tokens = [&](bool first, int ch, int at) {
-            const int lw = first ? p.lw1 : p.lw2, kc = (kBoxes * kWarps >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
-            const int bytes = first ? 2 : 4;
+            const int lw = first ? p.lw1 : p.lw2, kc = (kBoxes >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
             if (lane < count)
-                bulk_load(ring + at * p.stage_bytes + Cfg::kActOffset + lane * Cfg::act_stride(lw, first), token + k0 * bytes, k * bytes,
-                          &full[at]);
+                bulk_load(ring + at * p.stage_bytes + Cfg::kActOffset + lane * Cfg::act_stride(lw, first),
+                          token + k0 * (first ? Cfg::kXBytes : Cfg::kHBytes), act_bytes(first, k), &full[at]);
         };
         auto next = [&] {
             if (++stage == p.stages) stage = 0, phase ^= 1u;
@@ -625,7 +672,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
             }
         }
         if (ok && ahead > 0) {
-            if (!__all_sync(0xffffffffu, wait_count(&p.counters[1], grid))) {
+            if (!__all_sync(0xffffffffu, wait_count(&p.counters[Cfg::kTwoParts ? 1 : 2], grid))) {
                 if (lane == 0) give_up();
                 ok = false;
             }
@@ -661,49 +708,52 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         // One unit's sums for this warp's row group and box column.
         auto unit_sums = [&](auto first_c, const Unit &n, float(&acc)[NT][4]) {
             constexpr bool kFirst = decltype(first_c)::value;
-            // The warp has box columns my_box and my_box + sharers.
+            // The warp has box columns my_box, my_box + sharers, ..
             const int lw = kFirst ? p.lw1 : p.lw2, sharers = kWarps >> lw, my_row = warp & ((1 << lw) - 1), my_box = warp >> lw;
             const bool halves = kFirst && gated;
             const int w_box = halves ? 1024 : 2048, row8 = halves ? kStageWeights / 2 : 1024;
-            const int stride = Cfg::act_stride(lw, kFirst), width = kFirst ? p.H : p.I;
-            float part[kBoxes][NT][4];
+            const int width = kFirst ? p.H : p.I;
+            constexpr bool kParts = !kFirst && Cfg::kTwoParts;
+            constexpr int kBoxBytes = Cfg::kBoxK * (kFirst ? Cfg::kXBytes : Cfg::kHBytes);  // of a token's k's of a box
+            // Token of this thread in each group of 8 (past the last: the last one, whose sums nobody takes).
+            int token_at[NT];
 #pragma unroll
-            for (int b = 0; b < kBoxes; ++b)
+            for (int i = 0; i < NT; ++i)
+                token_at[i] = Cfg::kActOffset + my_box * kBoxBytes + min(i * 8 + g, n.count - 1) * Cfg::act_stride(lw, kFirst);
+            float part[kMine][NT][4];
+#pragma unroll
+            for (int b = 0; b < kMine; ++b)
 #pragma unroll
                 for (int i = 0; i < NT; ++i) part[b][i][0] = part[b][i][1] = part[b][i][2] = part[b][i][3] = 0.f;
             for (int ch = n.ch0; ch < n.ch1; ++ch) {
                 // after a time-out everything runs through without waiting
                 if (!abort_flag && !mbar_wait_patient(&full[stage], phase)) give_up();
-                const uint8_t *st = ring + stage * p.stage_bytes;
-                const uint8_t *w0 = st + warp * w_box + g * 128, *act = st + Cfg::kActOffset + my_box * Cfg::kBoxK * (kFirst ? 2 : 4);
-                const int valid = width - (ch * kBoxes * sharers + my_box) * Cfg::kBoxK;
-                if constexpr (FP8) {
-                    const float *sc = reinterpret_cast<const float *>(st + kStageWeights) + warp;
-                    float sum[kBoxes][NT][4] = {};
+                const uint8_t *st = ring + stage * p.stage_bytes, *w0 = st + warp * w_box;
 #pragma unroll
-                    for (int b = 0; b < kBoxes; ++b)
-                        multiply_box<XT, FP8, NT, kFirst>(w0 + b * kWarps * w_box, w0 + b * kWarps * w_box + row8,
-                                                          act + b * sharers * Cfg::kBoxK * (kFirst ? 2 : 4), stride,
-                                                          valid - b * sharers * Cfg::kBoxK, n.count, sum[b]);
+                for (int b = 0; b < kMine; ++b) {
+                    const int valid = width - (ch * kMine * sharers + b * sharers + my_box) * Cfg::kBoxK;
+                    if (valid <= 0) continue;
+                    const uint8_t *act[NT];
 #pragma unroll
-                    for (int b = 0; b < kBoxes; ++b) {
-                        // a box past the end has no scale: its sums are zeros
-                        const bool in = valid > b * sharers * Cfg::kBoxK;
-                        const float s0 = in ? sc[b * 2 * kWarps] : 0.f, s1 = in ? sc[b * 2 * kWarps + kWarps] : 0.f;
+                    for (int i = 0; i < NT; ++i) act[i] = st + token_at[i] + b * sharers * kBoxBytes;
+                    const uint8_t *w = w0 + b * kWarps * w_box;
+                    float sum[NT][4] = {};
+                    float(&to)[NT][4] = FP8 ? sum : part[b];
+                    if (valid >= Cfg::kBoxK)
+                        multiply_box<XT, FP8, NT, kParts, false>(w, w + row8, act, valid, to);
+                    else
+                        multiply_box<XT, FP8, NT, kParts, true>(w, w + row8, act, valid, to);
+                    if constexpr (FP8) {
+                        const float *sc = reinterpret_cast<const float *>(st + kStageWeights) + warp + b * kWarps;
+                        const float s0 = sc[0], s1 = sc[kBoxes];
 #pragma unroll
                         for (int i = 0; i < NT; ++i) {
-                            part[b][i][0] = fmaf(s0, sum[b][i][0], part[b][i][0]);
-                            part[b][i][1] = fmaf(s0, sum[b][i][1], part[b][i][1]);
-                            part[b][i][2] = fmaf(s1, sum[b][i][2], part[b][i][2]);
-                            part[b][i][3] = fmaf(s1, sum[b][i][3], part[b][i][3]);
+                            part[b][i][0] = fmaf(s0, sum[i][0], part[b][i][0]);
+                            part[b][i][1] = fmaf(s0, sum[i][1], part[b][i][1]);
+                            part[b][i][2] = fmaf(s1, sum[i][2], part[b][i][2]);
+                            part[b][i][3] = fmaf(s1, sum[i][3], part[b][i][3]);
                         }
                     }
-                } else {
-#pragma unroll
-                    for (int b = 0; b < kBoxes; ++b)
-                        multiply_box<XT, FP8, NT, kFirst>(w0 + b * kWarps * w_box, w0 + b * kWarps * w_box + row8,
-                                                          act + b * sharers * Cfg::kBoxK * (kFirst ? 2 : 4), stride,
-                                                          valid - b * sharers * Cfg::kBoxK, n.count, part[b]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
@@ -712,7 +762,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = part[0][i][j] + part[1][i][j];
+                for (int j = 0; j < 4; ++j) acc[i][j] = kMine == 2 ? part[0][i][j] + part[kMine - 1][i][j] : part[0][i][j];
             // Warps of the same rows: the first one adds the others' sums.
             if (sharers > 1) {
                 if (my_box > 0) {
@@ -721,7 +771,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) red[buf][warp][i][j][lane] = acc[i][j];
                 }
-                consumer_sync();
+                consumer_sync<kWarps>();
                 if (my_box == 0) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i)
@@ -742,19 +792,60 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int tok = nt * 8 + 2 * (lane & 3) + (i & 1);
-                    if (tok >= n.count || (gated && i >= 2)) continue;
-                    const int at = row + (gated ? 0 : 8 * (i >> 1));
-                    float h = moe_act(p.act, acc[nt][i]);
-                    if (gated) h *= acc[nt][(i + 2) & 3];
-                    if (at < p.I) p.hidden[static_cast<long long>(r.order[n.start + tok]) * p.I + at] = tf32_round(h);
+                for (int j = 0; j < 2; ++j) {
+                    const int tok = nt * 8 + 2 * (lane & 3) + j;
+                    const bool in = tok < n.count;
+                    const int slot = in ? r.order[n.start + tok] : 0;
+                    const float xs = Cfg::kScaledX ? r.x_scale[slot / p.top_k] : 1.f;
+                    float largest = 0.f;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (gated && half) break;
+                        const int at = row + 8 * half;
+                        float h = moe_act(p.act, acc[nt][j + 2 * half] * xs);
+                        if (gated) h *= acc[nt][j + 2] * xs;
+                        if (!in || at >= p.I) continue;
+                        if constexpr (Cfg::kTwoParts) {
+                            __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(p.hidden) + slot * parts_bytes(p.I)) +
+                                                at / 64 * 128 + at % 64;
+                            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                            const float rest = h - __bfloat162float(hi);
+                            to[0] = hi;
+                            to[64] = __float2bfloat16_rn(fabsf(h) < INFINITY ? rest : 0.f);  // inf - inf is no remainder
+                        } else {
+                            p.hidden[static_cast<long long>(slot) * p.I + at] = h;
+                            if (fabsf(h) < INFINITY) largest = fmaxf(largest, fabsf(h));
+                        }
+                    }
+                    if constexpr (!Cfg::kTwoParts) {
+#pragma unroll
+                        for (int d = 16; d >= 4; d >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
+                        if (in && lane < 4) atomicMax(p.h_max + slot, __float_as_uint(largest));
+                    }
                 }
         }
-        fence_proxy_async_all();  // h is read by bulk copies
+        if constexpr (Cfg::kTwoParts) fence_proxy_async_all();  // h is read by bulk copies
         __threadfence();
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (threadIdx.x == 0) atomicAdd(&p.counters[1], 1u);
+        if constexpr (!Cfg::kTwoParts) {
+            // h to FP16, now that every slot's largest element is known
+            if (threadIdx.x == 0 && !wait_count(&p.counters[1], grid)) give_up();
+            consumer_sync<kWarps>();
+            const int per = p.I / 8, all = p.T * p.top_k * per;
+            for (int x = blockIdx.x * 32 * kWarps + threadIdx.x; x < all; x += grid * 32 * kWarps) {
+                const float f = pow2(fit_exponent(__uint_as_float(__ldcg(p.h_max + x / per))));
+                const float4 *h = reinterpret_cast<const float4 *>(p.hidden) + 2ll * x;
+                const float4 a = __ldcg(h), b = __ldcg(h + 1);
+                reinterpret_cast<uint4 *>(p.hidden16)[x] =
+                    make_uint4(pack2_out16(a.x * f, a.y * f, kOutF16), pack2_out16(a.z * f, a.w * f, kOutF16),
+                               pack2_out16(b.x * f, b.y * f, kOutF16), pack2_out16(b.z * f, b.w * f, kOutF16));
+            }
+            fence_proxy_async_all();  // read by bulk copies
+            __threadfence();
+            consumer_sync<kWarps>();
+            if (threadIdx.x == 0) atomicAdd(&p.counters[2], 1u);
+        }
         const long long slots = static_cast<long long>(p.T) * p.top_k;
         for (int u = shift; u < units2; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
@@ -770,12 +861,12 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
         }
         // ------------------------------------------------ sum over a token's experts
         __threadfence();
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (threadIdx.x == 0) {
-            atomicAdd(&p.counters[2], 1u);
-            if (!wait_count(&p.counters[2], grid)) give_up();
+            atomicAdd(&p.counters[3], 1u);
+            if (!wait_count(&p.counters[3], grid)) give_up();
         }
-        consumer_sync();
+        consumer_sync<kWarps>();
         if (!abort_flag) {
             const int groups = p.H / 4;
             for (int x = blockIdx.x * 32 * kWarps + threadIdx.x; x < p.T * groups; x += grid * 32 * kWarps) {
@@ -788,7 +879,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
                         const float4 w = __ldcg(reinterpret_cast<const float4 *>(p.part + (s * slots + slot) * p.H + c));
                         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                     }
-                    const float f = r.weight[slot];
+                    float f = r.weight[slot];
+                    if (!Cfg::kTwoParts) f *= pow2(-fit_exponent(__uint_as_float(__ldcg(p.h_max + slot))));
                     y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
                 }
 #pragma unroll
@@ -798,8 +890,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1)
     }
     __syncthreads();
     // The last CTA to leave clears the barriers for the next call.
-    if (threadIdx.x == 0 && atomicAdd(&p.counters[3], 1u) == gridDim.x - 1)
-        p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = 0u;
+    if (threadIdx.x == 0 && atomicAdd(&p.counters[4], 1u) == gridDim.x - 1)
+        p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = p.counters[4] = 0u;
 }
 
 // Tensor map of E matrices of `rows` rows of `width` elements.  flat: a box is
@@ -816,7 +908,7 @@ bool encode_expert_map(CUtensorMap *map, const void *base, int elem_bytes, CUten
 // how many units share a row group's k.  `groups` row groups of 16 (one of each
 // expert that is used), `k` long; `act_bytes` of activations in a stage with
 // WR = 1.  Preferred is the largest WR, then the fewest splits, whose units
-// fill whole rounds over the SMs to 94 %; failing that, what fills them best.
+// fill whole rounds over the SMs to 90 %; failing that, what fills them best.
 // WR is at least what keeps a stage's activations within its weights (the ring
 // would hold too few stages) and a stage's k below the whole length.
 struct Cut {
@@ -824,34 +916,34 @@ struct Cut {
 };
 Cut pick_cut(double groups, int k, int box_k, int act_bytes, int max_splits, int sms) {
     int least = 0;
-    while (least < 3 && ((act_bytes >> least) > kStageWeights || (kBoxes * kWarps >> least) * box_k >= 2 * k)) ++least;
+    while (least < 3 && ((act_bytes >> least) > kStageWeights || (kBoxes >> least) * box_k >= 2 * k)) ++least;
     Cut best;
     double best_fill = -1.0;
     for (int lw = 3; lw >= least; --lw)
         for (int splits = 1; splits <= max_splits; splits *= 2) {
-            if (splits > 1 && (kBoxes * kWarps >> lw) * box_k * splits * 2 > k) break;  // two stages at least
+            if (splits > 1 && (kBoxes >> lw) * box_k * splits * 2 > k) break;  // two stages at least
             const double units = std::max(1.0, groups / (1 << lw) * splits);
             const double fill = units / (std::ceil(units / sms - 1e-9) * sms);
             if (fill > best_fill + 1e-9) best_fill = fill, best.lw = lw, best.splits = splits;
-            if (fill >= 0.94) return best;
+            if (fill >= 0.9) return best;
         }
     return best;
 }
 
 template <int XT, bool FP8, int NT>
 cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stream) {
-    using Cfg = MoeCfg<FP8>;
+    using Cfg = MoeCfg<XT, FP8>;
     auto kern = moe_kernel<XT, FP8, NT>;
-    const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * kBoxes * kWarps * Cfg::kBoxK * 2;  // of X rows; h rows twice that
-    const Cut c1 = pick_cut(active * m.I / (m.up ? 8 : 16), m.H, Cfg::kBoxK, act, 1, sms);
-    const Cut c2 = pick_cut(active * m.H / 16, m.I, Cfg::kBoxK, 2 * act, kMaxSplits, sms);
+    const int sms = device_sm_count(), act = std::min(m.T, 8 * NT) * kBoxes * Cfg::kBoxK;  // elements of a stage with WR = 1
+    const Cut c1 = pick_cut(active * m.I / (m.up ? 8 : 16), m.H, Cfg::kBoxK, act * Cfg::kXBytes, 1, sms);
+    const Cut c2 = pick_cut(active * m.H / 16, m.I, Cfg::kBoxK, act * Cfg::kHBytes, kMaxSplits, sms);
     a.lw1 = c1.lw;
     a.lw2 = c2.lw;
     a.k_splits = c2.splits;
     // a stage holds the weights, their scales and either kind of activations
     const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.lw1, true), Cfg::act_stride(a.lw2, false));
     a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
-    constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * kWarps * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
+    constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * moe_warps(NT) * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
     static_assert(kRing >= 1024 + kChoiceKeys * 4 && kChoiceKeys >= kMoeMaxExperts, "the ring holds the keys of the choice");
     a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);  // two at least: 2 x (32 + 32) KB and paddings
     const int wb = Cfg::kWBytes;
@@ -860,7 +952,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     a.flat_i = m.I * wb % 128 == 0;
     CUtensorMap tg, tu, td;
     const uint64_t rows_i = static_cast<uint64_t>(m.E) * m.I, rows_h = static_cast<uint64_t>(m.E) * m.H;
-    const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = kBoxes * kWarps >> a.lw1, rows2 = 16 << a.lw2, boxes2 = kBoxes * kWarps >> a.lw2;
+    const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = kBoxes >> a.lw1, rows2 = 16 << a.lw2, boxes2 = kBoxes >> a.lw2;
     if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
         !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
         !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, rows2, boxes2))
@@ -873,7 +965,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     attr.val.cooperative = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(device_sm_count());
-    cfg.blockDim = dim3(kMoeThreads);
+    cfg.blockDim = dim3(32 * (moe_warps(NT) + 1));
     cfg.dynamicSmemBytes = kRing;
     cfg.stream = stream;
     cfg.attrs = &attr;
@@ -919,13 +1011,22 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     // Experts with any token if the router chose evenly, and tokens of one.
     const double slots = static_cast<double>(m.T) * m.top_k;
     const double active = m.E * (1.0 - std::pow(1.0 - static_cast<double>(m.top_k) / m.E, m.T)), tokens = slots / active;
-    const size_t n_logits = (static_cast<size_t>(m.T) * m.E + 63) / 64 * 64, n_hidden = static_cast<size_t>(slots) * m.I;
+    // Scratch, in floats, each part on 256 bytes.
+    auto up64 = [](size_t n) { return (n + 63) / 64 * 64; };
+    const size_t n_slots = static_cast<size_t>(m.T) * m.top_k;
+    const size_t n_logits = up64(static_cast<size_t>(m.T) * m.E), n_hidden = up64(n_slots * parts_bytes(m.I) / 4);
+    const size_t n_h16 = up64(n_slots * m.I / 2), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
     Scratch s;
-    const cudaError_t e = acquire_scratch(stream, n_logits + n_hidden + static_cast<size_t>(slots) * m.H * kMaxSplits, 4, &s);
+    const cudaError_t e =
+        acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
-    a.hidden = s.partials + n_logits;
-    a.part = a.hidden + n_hidden;
+    a.hidden = a.logits + n_logits;
+    a.hidden16 = reinterpret_cast<__half *>(a.hidden + n_hidden);
+    a.x16 = reinterpret_cast<__half *>(a.hidden + n_hidden + n_h16);
+    a.h_max = reinterpret_cast<unsigned *>(a.hidden + n_hidden + n_h16 + n_x16);
+    a.x_scale = a.hidden + n_hidden + n_h16 + n_x16 + n_max;
+    a.part = a.x_scale + up64(m.T);
     a.counters = s.counters;
     info->launches = 1;
     info->plan = "moe_few_tokens";
