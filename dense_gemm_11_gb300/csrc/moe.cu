@@ -40,8 +40,10 @@
 //   FP16 weights   X as it is; h in FP16 after scaling a token's h by the power
 //                  of two that brings its largest element to [2^14, 2^15): 11
 //                  bits down to 2^-28 of the largest, nothing overflows.  h is
-//                  written in FP32 first and converted, with its maximum known,
-//                  between two grid barriers, while the ring fills with weights;
+//                  written in FP32 and in FP16 as it is; where some slot's
+//                  maximum turns out to be outside [2^-4, 65504] (as it is, h
+//                  keeps 2^-21 of the maximum or better inside) all are fitted
+//                  between two grid barriers (3 us), else nothing is;
 //   e4m3 weights   widened to FP16 (exact), one conversion for two elements
 //                  (TF32 products took two more each, and twice the matrix
 //                  instructions: 3.2 TB/s against 4.x); h as for FP16, and a
@@ -83,7 +85,7 @@ struct MoeArgs {
     // alternate runs of 64; h and X in FP16, scaled; the largest |h| of a slot,
     // and the scale of a token; k_splits x slots x H partial results.
     float *logits, *hidden, *part;
-    __half *hidden16, *x16;
+    __half *hidden16, *x16;  // hidden16: h as it is, or fitted
     unsigned *h_max;
     float *x_scale;
     unsigned *counters;  // four barriers and the exit
@@ -98,7 +100,7 @@ struct MoeArgs {
 struct Routing {
     float weight[kMoeMaxSlots];
     float x_scale[kMoeMaxTokens];   // what a token's sums are multiplied by
-    uint16_t expert[kMoeMaxSlots];  // of slot t * top_k + j
+    alignas(4) uint16_t expert[kMoeMaxSlots];  // of slot t * top_k + j
     uint16_t order[kMoeMaxSlots];   // slots, grouped by expert, ascending
     uint16_t pair_expert[kMoeMaxSlots], pair_first[kMoeMaxSlots], pair_start[kMoeMaxSlots];
     uint8_t pair_groups[kMoeMaxSlots], pair_count[kMoeMaxSlots];
@@ -184,66 +186,82 @@ __device__ __forceinline__ int fit_exponent(float largest) {
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<unsigned>(127 + e) << 23); }
 
 // ---------------------------------------------------------------- routing
-// Sum of w x over `threads` threads' share of H for one expert and 8 tokens.
+constexpr int kRouterTokens = 4;  // of one unit
+
+// Sum of w x over `threads` threads' share of H for one expert and 4 tokens,
+// two steps' loads in flight.
 template <int XT>
-__device__ __forceinline__ void router_dot(const MoeArgs &p, int e, int t0, int thread, int threads, float (&acc)[8]) {
+__device__ __forceinline__ void router_dot(const MoeArgs &p, int e, int t0, int thread, int threads, float (&acc)[kRouterTokens]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    for (int k = thread * 8; k < p.H; k += threads * 8) {
-        float w[8];
-        uint4 x[8];
-        const long long at = static_cast<long long>(e) * p.H + k;
+    for (int i = 0; i < kRouterTokens; ++i) acc[i] = 0.f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const int step = threads * 8;
+    for (int k0 = thread * 8; k0 < p.H; k0 += 2 * step) {
+        uint4 x[2][kRouterTokens], w16[2];
+        float w[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            x[i] = t0 + i < p.T ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + (t0 + i) * p.ldx + k))
-                                : make_uint4(0, 0, 0, 0);
-        if (p.router_f32) {
-            const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.router) + at);
-            const float4 a = __ldg(r), b = __ldg(r + 1);
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-        } else {
-            widen8(__ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.router) + at)), XT, w);
+        for (int u = 0; u < 2; ++u) {
+            const int k = k0 + u * step;
+            const bool in = k < p.H;
+            const long long at = static_cast<long long>(e) * p.H + k;
+            if (p.router_f32) {
+                const float4 *r = reinterpret_cast<const float4 *>(static_cast<const float *>(p.router) + at);
+                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                const float4 a = in ? __ldg(r) : z, b = in ? __ldg(r + 1) : z;
+                w[u][0] = a.x, w[u][1] = a.y, w[u][2] = a.z, w[u][3] = a.w, w[u][4] = b.x, w[u][5] = b.y, w[u][6] = b.z, w[u][7] = b.w;
+            } else {
+                w16[u] = in ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.router) + at)) : zero;
+            }
+#pragma unroll
+            for (int i = 0; i < kRouterTokens; ++i)
+                x[u][i] = in && t0 + i < p.T
+                              ? __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + (t0 + i) * p.ldx + k))
+                              : zero;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float f[8];
-            widen8(x[i], XT, f);
+        for (int u = 0; u < 2; ++u) {
+            if (!p.router_f32) widen8(w16[u], XT, w[u]);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) acc[i] = fmaf(w[j], f[j], acc[i]);
+            for (int i = 0; i < kRouterTokens; ++i) {
+                float f[8];
+                widen8(x[u][i], XT, f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i] = fmaf(w[u][j], f[j], acc[i]);
+            }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < kRouterTokens; ++i)
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
 }
 
-// All logits, in units of one expert and 8 tokens: a CTA takes a unit while
+// All logits, in units of one expert and 4 tokens: a CTA takes a unit while
 // there are no more units than CTAs (its warps share H), else each warp does.
 template <int XT, int kWarps>
 __device__ void router_logits(const MoeArgs &p, float *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int groups = (p.T + 7) / 8, units = p.E * groups;
-    float acc[8];
+    const int groups = (p.T + kRouterTokens - 1) / kRouterTokens, units = p.E * groups;
+    float acc[kRouterTokens];
     if (units > static_cast<int>(gridDim.x)) {
         for (int u = warp * gridDim.x + blockIdx.x; u < units; u += gridDim.x * kWarps) {
-            const int e = u / groups, t0 = (u % groups) * 8;
+            const int e = u / groups, t0 = (u % groups) * kRouterTokens;
             router_dot<XT>(p, e, t0, lane, 32, acc);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kRouterTokens; ++i)
                 if (lane == i && t0 + i < p.T) p.logits[(t0 + i) * p.E + e] = acc[i];
         }
     } else if (static_cast<int>(blockIdx.x) < units) {
-        const int e = blockIdx.x / groups, t0 = (blockIdx.x % groups) * 8;
+        const int e = blockIdx.x / groups, t0 = (blockIdx.x % groups) * kRouterTokens;
         router_dot<XT>(p, e, t0, threadIdx.x, 32 * kWarps, acc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (lane == i) red[warp * 8 + i] = acc[i];
+        for (int i = 0; i < kRouterTokens; ++i)
+            if (lane == i) red[warp * kRouterTokens + i] = acc[i];
         consumer_sync<kWarps>();
-        if (threadIdx.x < 8 && t0 + threadIdx.x < p.T) {
+        if (threadIdx.x < kRouterTokens && t0 + threadIdx.x < p.T) {
             float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) v += red[w * 8 + threadIdx.x];
+            for (int w = 0; w < kWarps; ++w) v += red[w * kRouterTokens + threadIdx.x];
             p.logits[(t0 + threadIdx.x) * p.E + e] = v;
         }
     }
@@ -291,48 +309,50 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
 // One warp, one token: softmax and its top_k largest, by repeated maximum over
-// the logits' keys (shared memory; taken ones are set to 0).
+// the logits' keys (shared memory; taken ones are set to 0).  Lane j keeps the
+// j-th choice.
 __device__ void choose_experts(const MoeArgs &p, int t, uint32_t *keys, Routing &r) {
     const int lane = threadIdx.x & 31;
-    float top = 0.f, chosen = 0.f, sum = 0.f, mine = 0.f;
+    uint32_t mine = 0, first = 0;
+    int my_expert = 0;
+    float sum = 0.f;
     for (int j = 0; j < p.top_k; ++j) {
         uint32_t best = 0;
         int at = 0;
+#pragma unroll 2
         for (int e = lane; e < p.E; e += 32) {
             const uint32_t k = keys[e];
             if (k > best) best = k, at = e;
         }
         const uint32_t m = __reduce_max_sync(0xffffffffu, best);
         const int e = static_cast<int>(__reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(at) : 0xFFFFFFFFu));
-        const float l = key_logit(m);
         if (j == 0) {
-            top = l;
+            first = m;
             if (!p.renorm)
-                for (int i = lane; i < p.E; i += 32) sum += expf(key_logit(keys[i]) - top);
+                for (int i = lane; i < p.E; i += 32) sum += expf(key_logit(keys[i]) - key_logit(m));
         }
-        const float v = expf(l - top);
-        chosen += v;
-        if (lane == j) mine = v;
-        if (lane == 0) r.expert[t * p.top_k + j] = static_cast<uint16_t>(e);
+        if (lane == j) mine = m, my_expert = e;
         if (lane == (e & 31)) keys[e] = 0;
     }
+    const float v = lane < p.top_k ? expf(key_logit(mine) - key_logit(first)) : 0.f;
+    if (p.renorm) sum = v;
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane < p.top_k) r.weight[t * p.top_k + lane] = mine / (p.renorm ? chosen : sum);
+    if (lane < p.top_k) {
+        r.weight[t * p.top_k + lane] = v / sum;
+        r.expert[t * p.top_k + lane] = static_cast<uint16_t>(my_expert);
+    }
 }
 
 // Slots grouped by expert, in ascending order, and the (expert, token group)
-// pairs that the units go over.  The warps deal the experts out and find an
-// expert's slots by ballots.
+// pairs that the units go over.  A slot's place in its expert's list is the
+// number of earlier slots with the same expert.
 template <int kWarps>
 __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = p.T * p.top_k;
-    for (int e = warp; e < p.E; e += kWarps) {
-        int n = 0;
-        for (int s0 = 0; s0 < slots; s0 += 32)
-            n += __popc(__ballot_sync(0xffffffffu, s0 + lane < slots && r.expert[s0 + lane] == e));
-        if (lane == 0) r.offset[e] = n;
-    }
+    for (int e = threadIdx.x; e < p.E; e += 32 * kWarps) r.offset[e] = 0;
+    consumer_sync<kWarps>();
+    for (int s = threadIdx.x; s < slots; s += 32 * kWarps) atomicAdd(&r.offset[r.expert[s]], 1);
     consumer_sync<kWarps>();
     if (warp == 0) {
         int before = 0, pairs_before = 0;
@@ -363,14 +383,27 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
         if (lane == 0) r.pairs = pairs_before;
     }
     consumer_sync<kWarps>();
-    for (int e = warp; e < p.E; e += kWarps) {
-        int at = r.offset[e];
-        for (int s0 = 0; s0 < slots; s0 += 32) {
-            const unsigned same = __ballot_sync(0xffffffffu, s0 + lane < slots && r.expert[s0 + lane] == e);
-            if (same & (1u << lane)) r.order[at + __popc(same & ((1u << lane) - 1u))] = static_cast<uint16_t>(s0 + lane);
-            at += __popc(same);
-        }
+    const uint32_t *two = reinterpret_cast<const uint32_t *>(r.expert);  // two slots' experts
+    for (int s = threadIdx.x; s < slots; s += 32 * kWarps) {
+        const uint32_t e = r.expert[s];
+        const uint32_t both = e | (e << 16);
+        int rank = 0;
+#pragma unroll 4
+        for (int i = 0; i < s / 2; ++i) rank += __popc(__vcmpeq2(two[i], both) & 0x00010001u);
+        if ((s & 1) && r.expert[s - 1] == e) ++rank;
+        r.order[r.offset[e] + rank] = static_cast<uint16_t>(s);
     }
+}
+
+// Whether every slot's largest |h| is inside FP16's comfortable range.  Each
+// warp looks for itself (after the first half's barrier).
+__device__ __forceinline__ bool slots_fit(const MoeArgs &p) {
+    bool fits = true;
+    for (int i = threadIdx.x & 31; i < p.T * p.top_k; i += 32) {
+        const float m = __uint_as_float(__ldcg(p.h_max + i));
+        fits = fits && (m == 0.f || (m >= 0.0625f && m <= 65504.f));
+    }
+    return __all_sync(0xffffffffu, fits);
 }
 
 // ---------------------------------------------------------------- units
@@ -433,10 +466,11 @@ struct MoeCfg {
 // This warp's 16 rows x one box of k times the tokens, added to c.  Thread
 // (g, t) holds rows g and g + 8, token 8 n + g and the same k's of both; w0 and
 // w1 are the first of each 8 rows (16-byte chunk c of row g at c ^ g, by the
-// copy's swizzle), act[n] its token's k's of this box.  PARTS: the second BF16
+// copy's swizzle), act[n] its token's k's of this box; USED of the NT groups of
+// 8 tokens exist.  PARTS: the second BF16
 // parts follow the first after 128 bytes.  TAIL: only `valid` k's exist; the
 // weights past them are zeros, the activations are left over from other stages.
-template <int XT, bool FP8, int NT, bool PARTS, bool TAIL>
+template <int XT, bool FP8, int NT, int USED, bool PARTS, bool TAIL>
 __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *const (&act)[NT], int valid,
                                              float (&c)[NT][4]) {
     using Cfg = MoeCfg<XT, FP8>;
@@ -455,7 +489,7 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
                 widen_e4m3(w[2 * h + 1], a1, a3);
                 const int k = (ch + h) * 16 + t * 4;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < USED; ++n) {
                     uint2 x = *reinterpret_cast<const uint2 *>(act[n] + k * 2);
                     if (TAIL && k >= valid) x = make_uint2(0, 0);
                     mma_16bit<Cfg::kMma>(c[n], a0, a1, a2, a3, x.x, x.y);
@@ -471,7 +505,7 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
 #pragma unroll
             for (int part = 0; part < (PARTS ? 2 : 1); ++part)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                for (int n = 0; n < USED; ++n) {
                     uint4 x = *reinterpret_cast<const uint4 *>(act[n] + part * 128 + chunk * 16);
                     if (TAIL && chunk * 8 >= valid) x = make_uint4(0, 0, 0, 0);
                     mma_16bit<Cfg::kMma>(c[n], a.x, b.x, a.y, b.y, x.x, x.y);
@@ -562,6 +596,7 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
     // CTAs that had one unit less in the first half begin the second.
     const int grid = gridDim.x;
     const int shift = (static_cast<int>(blockIdx.x) + grid - units1 % grid) % grid;
+    bool h_fits = true;  // h is used as the first half wrote it
 
     if (warp == kWarps) {
         // ------------------------------------------------ producer
@@ -672,10 +707,9 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
             }
         }
         if (ok && ahead > 0) {
-            if (!__all_sync(0xffffffffu, wait_count(&p.counters[Cfg::kTwoParts ? 1 : 2], grid))) {
-                if (lane == 0) give_up();
-                ok = false;
-            }
+            ok = __all_sync(0xffffffffu, wait_count(&p.counters[1], grid));
+            if (ok && !Cfg::kTwoParts && !slots_fit(p)) ok = __all_sync(0xffffffffu, wait_count(&p.counters[2], grid));
+            if (!ok && lane == 0) give_up();
             fence_proxy_async_all();
         }
         int i = 0;
@@ -739,10 +773,12 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
                     const uint8_t *w = w0 + b * kWarps * w_box;
                     float sum[NT][4] = {};
                     float(&to)[NT][4] = FP8 ? sum : part[b];
-                    if (valid >= Cfg::kBoxK)
-                        multiply_box<XT, FP8, NT, kParts, false>(w, w + row8, act, valid, to);
+                    if (valid < Cfg::kBoxK)
+                        multiply_box<XT, FP8, NT, NT, kParts, true>(w, w + row8, act, valid, to);
+                    else if (NT > 1 && n.count <= 8)
+                        multiply_box<XT, FP8, NT, 1, kParts, false>(w, w + row8, act, valid, to);
                     else
-                        multiply_box<XT, FP8, NT, kParts, true>(w, w + row8, act, valid, to);
+                        multiply_box<XT, FP8, NT, NT, kParts, false>(w, w + row8, act, valid, to);
                     if constexpr (FP8) {
                         const float *sc = reinterpret_cast<const float *>(st + kStageWeights) + warp + b * kWarps;
                         const float s0 = sc[0], s1 = sc[kBoxes];
@@ -813,7 +849,9 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
                             to[0] = hi;
                             to[64] = __float2bfloat16_rn(fabsf(h) < INFINITY ? rest : 0.f);  // inf - inf is no remainder
                         } else {
-                            p.hidden[static_cast<long long>(slot) * p.I + at] = h;
+                            const long long to = static_cast<long long>(slot) * p.I + at;
+                            p.hidden[to] = h;
+                            p.hidden16[to] = __float2half_rn(h);
                             if (fabsf(h) < INFINITY) largest = fmaxf(largest, fabsf(h));
                         }
                     }
@@ -824,7 +862,7 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
                     }
                 }
         }
-        if constexpr (Cfg::kTwoParts) fence_proxy_async_all();  // h is read by bulk copies
+        fence_proxy_async_all();  // h is read by bulk copies
         __threadfence();
         consumer_sync<kWarps>();
         if (threadIdx.x == 0) atomicAdd(&p.counters[1], 1u);
@@ -832,6 +870,9 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
             // h to FP16, now that every slot's largest element is known
             if (threadIdx.x == 0 && !wait_count(&p.counters[1], grid)) give_up();
             consumer_sync<kWarps>();
+            h_fits = slots_fit(p);
+        }
+        if (!h_fits) {
             const int per = p.I / 8, all = p.T * p.top_k * per;
             for (int x = blockIdx.x * 32 * kWarps + threadIdx.x; x < all; x += grid * 32 * kWarps) {
                 const float f = pow2(fit_exponent(__uint_as_float(__ldcg(p.h_max + x / per))));
@@ -880,7 +921,7 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
                         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
                     }
                     float f = r.weight[slot];
-                    if (!Cfg::kTwoParts) f *= pow2(-fit_exponent(__uint_as_float(__ldcg(p.h_max + slot))));
+                    if (!h_fits) f *= pow2(-fit_exponent(__uint_as_float(__ldcg(p.h_max + slot))));
                     y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
                 }
 #pragma unroll
