@@ -15,9 +15,11 @@
 //     16 WR rows x 16 / WR boxes of 128 bytes, one TMA copy (two with a gate).
 //     Issuing a copy costs the producer about 100 cycles, so stages are large:
 //     with 16 KB it, not memory, set the pace (130 us against ??? at 1 token)
-//   * a producer warp fills a ring of stages.  It runs ahead of the arithmetic
-//     across units, and into the down projection while the other CTAs still
-//     finish the first half;
+//   * one warp fills a ring of stages with weights.  It runs ahead of the
+//     arithmetic across units, and into the down projection while other CTAs
+//     still finish the first half.  One or two more bring the tokens' rows of
+//     the same k, a copy each (by the weights' warp, 6 of them a stage held the
+//     weights back: 136 us against ?? at 64 tokens, 64 experts);
 //   * the other warps take a stage's WR row groups x 16 / WR boxes, one or two
 //     each, and multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
 //     share rows add their sums in warp order in shared memory at the unit's
@@ -66,7 +68,7 @@ constexpr int kStageWeights = 32768;            // bytes of weights in a stage
 constexpr int kBoxes = 16;                      // of 16 rows x 128 bytes in a stage
 constexpr int kMaxStages = 12;
 constexpr int kMaxSplits = 4;                   // units that share a row group's k in the down projection
-constexpr int kChoiceKeys = 16384;              // logits looked at together
+constexpr int kTokensOfTheirOwn = 32;           // from so many on a CTA routes a token by itself
 
 struct MoeArgs {
     int T, E, top_k, H, I;
@@ -88,6 +90,8 @@ struct MoeArgs {
     __half *hidden16, *x16;  // hidden16: h as it is, or fitted
     unsigned *h_max;
     float *x_scale;
+    uint16_t *chosen;  // T x top_k, and their weights
+    float *chosen_weight;
     unsigned *counters;  // four barriers and the exit
     unsigned *err;
     int lw1, lw2;    // log2 of WR, the row groups (of 16 rows) of a unit, in the first half and in the down projection
@@ -100,7 +104,7 @@ struct MoeArgs {
 struct Routing {
     float weight[kMoeMaxSlots];
     float x_scale[kMoeMaxTokens];   // what a token's sums are multiplied by
-    alignas(4) uint16_t expert[kMoeMaxSlots];  // of slot t * top_k + j
+    uint16_t expert[kMoeMaxSlots];  // of slot t * top_k + j
     uint16_t order[kMoeMaxSlots];   // slots, grouped by expert, ascending
     uint16_t pair_expert[kMoeMaxSlots], pair_first[kMoeMaxSlots], pair_start[kMoeMaxSlots];
     uint8_t pair_groups[kMoeMaxSlots], pair_count[kMoeMaxSlots];
@@ -267,6 +271,60 @@ __device__ void router_logits(const MoeArgs &p, float *red) {
     }
 }
 
+// Order-preserving key of a logit: -0 equals +0, NaN comes first; 0 is below
+// every key.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+    if (v != v) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
+
+// The keys of one token's logits, by a whole CTA: a warp takes 4 experts at a
+// time.
+template <int XT, int kWarps>
+__device__ void router_token(const MoeArgs &p, int t, uint32_t *keys) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint16_t *x = static_cast<const uint16_t *>(p.X) + t * p.ldx;
+    const int esize = p.router_f32 ? 4 : 2;
+    for (int e0 = warp * 4; e0 < p.E; e0 += kWarps * 4) {
+        float acc[4] = {};
+#pragma unroll 2
+        for (int k = lane * 8; k < p.H; k += 256) {
+            float f[8];
+            widen8(__ldg(reinterpret_cast<const uint4 *>(x + k)), XT, f);
+            uint4 w[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int e = min(e0 + i, p.E - 1);
+                const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.router) + (static_cast<long long>(e) * p.H + k) * esize);
+                w[i][0] = __ldg(r);
+                if (p.router_f32) w[i][1] = __ldg(r + 1);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float v[8];
+                if (p.router_f32) {
+                    v[0] = __uint_as_float(w[i][0].x), v[1] = __uint_as_float(w[i][0].y), v[2] = __uint_as_float(w[i][0].z);
+                    v[3] = __uint_as_float(w[i][0].w), v[4] = __uint_as_float(w[i][1].x), v[5] = __uint_as_float(w[i][1].y);
+                    v[6] = __uint_as_float(w[i][1].z), v[7] = __uint_as_float(w[i][1].w);
+                } else {
+                    widen8(w[i][0], XT, v);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) acc[i] = fmaf(v[j], f[j], acc[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], d);
+            if (lane == i && e0 + i < p.E) keys[e0 + i] = logit_key(acc[i]);
+        }
+    }
+}
+
 // One token's X in FP16, scaled, by a whole CTA.
 template <int XT, int kWarps>
 __device__ void scale_token(const MoeArgs &p, int t, float *red) {
@@ -298,20 +356,10 @@ __device__ void scale_token(const MoeArgs &p, int t, float *red) {
     if (threadIdx.x == 0) p.x_scale[t] = pow2(-e);
 }
 
-// Order-preserving key of a logit: -0 equals +0, NaN comes first; 0 is below
-// every key.
-__device__ __forceinline__ uint32_t logit_key(float v) {
-    if (v != v) return 0xFFFFFFFFu;
-    const uint32_t b = __float_as_uint(v + 0.f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
-
 // One warp, one token: softmax and its top_k largest, by repeated maximum over
 // the logits' keys (shared memory; taken ones are set to 0).  Lane j keeps the
 // j-th choice.
-__device__ void choose_experts(const MoeArgs &p, int t, uint32_t *keys, Routing &r) {
+__device__ void choose_experts(const MoeArgs &p, uint32_t *keys, uint16_t *experts, float *weights) {
     const int lane = threadIdx.x & 31;
     uint32_t mine = 0, first = 0;
     int my_expert = 0;
@@ -339,35 +387,44 @@ __device__ void choose_experts(const MoeArgs &p, int t, uint32_t *keys, Routing 
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
     if (lane < p.top_k) {
-        r.weight[t * p.top_k + lane] = v / sum;
-        r.expert[t * p.top_k + lane] = static_cast<uint16_t>(my_expert);
+        weights[lane] = v / sum;
+        experts[lane] = static_cast<uint16_t>(my_expert);
     }
 }
 
 // Slots grouped by expert, in ascending order, and the (expert, token group)
-// pairs that the units go over.  A slot's place in its expert's list is the
-// number of earlier slots with the same expert.
+// pairs that the units go over.  A token has an expert once at most, so an
+// expert's slots are a mask over the tokens (4 words each, in `mask`), and a
+// slot's place among them the bits below its own.
 template <int kWarps>
-__device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
+__device__ void group_slots(const MoeArgs &p, Routing &r, uint32_t *mask, int group) {
+    static_assert(kMoeMaxTokens == 128, "four words of a mask");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slots = p.T * p.top_k;
-    for (int e = threadIdx.x; e < p.E; e += 32 * kWarps) r.offset[e] = 0;
+    for (int i = threadIdx.x; i < p.E * 4; i += 32 * kWarps) mask[i] = 0;
     consumer_sync<kWarps>();
-    for (int s = threadIdx.x; s < slots; s += 32 * kWarps) atomicAdd(&r.offset[r.expert[s]], 1);
+    for (int s = threadIdx.x; s < slots; s += 32 * kWarps) {
+        const int t = s / p.top_k;
+        atomicOr(&mask[r.expert[s] * 4 + (t >> 5)], 1u << (t & 31));
+    }
     consumer_sync<kWarps>();
     if (warp == 0) {
         int before = 0, pairs_before = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
-            const int n = e < p.E ? r.offset[e] : 0;
+            int n = 0;
+            if (e < p.E) {
+                const uint4 m = *reinterpret_cast<const uint4 *>(mask + e * 4);
+                n = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
+            }
             const int np = (n + group - 1) / group;
-            int sum = n, psum = np;
+            int sum = n | (np << 16);  // both sums at once
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
-                const int a = __shfl_up_sync(0xffffffffu, sum, d), b = __shfl_up_sync(0xffffffffu, psum, d);
-                if (lane >= d) sum += a, psum += b;
+                const int a = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += a;
             }
             if (e < p.E) {
-                const int first = pairs_before + psum - np, start = before + sum - n;
+                const int first = pairs_before + (sum >> 16) - np, start = before + (sum & 0xFFFF) - n;
                 r.offset[e] = start;
                 for (int i = 0; i < np; ++i) {
                     r.pair_expert[first + i] = static_cast<uint16_t>(e);
@@ -377,20 +434,17 @@ __device__ void group_slots(const MoeArgs &p, Routing &r, int group) {
                     r.pair_count[first + i] = static_cast<uint8_t>(min(group, n - i * group));
                 }
             }
-            before += __shfl_sync(0xffffffffu, sum, 31);
-            pairs_before += __shfl_sync(0xffffffffu, psum, 31);
+            const int all = __shfl_sync(0xffffffffu, sum, 31);
+            before += all & 0xFFFF;
+            pairs_before += all >> 16;
         }
         if (lane == 0) r.pairs = pairs_before;
     }
     consumer_sync<kWarps>();
-    const uint32_t *two = reinterpret_cast<const uint32_t *>(r.expert);  // two slots' experts
     for (int s = threadIdx.x; s < slots; s += 32 * kWarps) {
-        const uint32_t e = r.expert[s];
-        const uint32_t both = e | (e << 16);
-        int rank = 0;
-#pragma unroll 4
-        for (int i = 0; i < s / 2; ++i) rank += __popc(__vcmpeq2(two[i], both) & 0x00010001u);
-        if ((s & 1) && r.expert[s - 1] == e) ++rank;
+        const int e = r.expert[s], t = s / p.top_k;
+        int rank = __popc(mask[e * 4 + (t >> 5)] & ((1u << (t & 31)) - 1u));
+        for (int i = 0; i < (t >> 5); ++i) rank += __popc(mask[e * 4 + i]);
         r.order[r.offset[e] + rank] = static_cast<uint16_t>(s);
     }
 }
@@ -518,13 +572,16 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
 // Consumer warps: sixteen with one box each while their registers last (16
 // tokens), else eight with two boxes.
 constexpr int moe_warps(int nt) { return nt <= 2 ? 16 : 8; }
+constexpr int moe_token_warps(int nt) { return nt == 1 ? 1 : 2; }
+constexpr int moe_threads(int nt) { return 32 * (moe_warps(nt) + 1 + moe_token_warps(nt)); }
 
 template <int XT, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
+__global__ void __launch_bounds__(moe_threads(NT), 1)
     moe_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
                const __grid_constant__ CUtensorMap tm_down, const MoeArgs p) {
     using Cfg = MoeCfg<XT, FP8>;
     constexpr int kWarps = moe_warps(NT), kMine = kBoxes / kWarps;  // boxes of a warp in a stage
+    constexpr int kTokenWarps = moe_token_warps(NT), kThreads = moe_threads(NT);
     extern __shared__ uint8_t ring_raw[];
     uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(ring_raw) + 1023) & ~uintptr_t(1023));
     __shared__ Routing r;
@@ -544,7 +601,7 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], FP8 ? 33 : 1);
+            mbar_init(&full[s], (FP8 ? 33 : 1) + kTokenWarps);
             mbar_init(&empty[s], kWarps);
         }
         abort_flag = 0;
@@ -563,7 +620,22 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
             for (int t = gridDim.x - 1 - blockIdx.x; t < p.T; t += gridDim.x) scale_token<XT, kWarps>(p, t, &red[0][0][0][0][0]);
             fence_proxy_async_all();  // x16 is read by bulk copies
         }
-        router_logits<XT, kWarps>(p, &red[0][0][0][0][0]);
+        // Few tokens: the logits are dealt out over the CTAs, and after the
+        // barrier every CTA makes the same choice.  Many: a CTA takes a token,
+        // logits and choice, and the barrier is for the choices.
+        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
+        const bool by_token = p.T >= kTokensOfTheirOwn;
+        const int slots = p.T * p.top_k;
+        if (by_token) {
+            for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
+                router_token<XT, kWarps>(p, t, keys);
+                consumer_sync<kWarps>();
+                if (warp == 0) choose_experts(p, keys, p.chosen + t * p.top_k, p.chosen_weight + t * p.top_k);
+                consumer_sync<kWarps>();
+            }
+        } else {
+            router_logits<XT, kWarps>(p, &red[0][0][0][0][0]);
+        }
         __threadfence();
         consumer_sync<kWarps>();
         if (threadIdx.x == 0) {
@@ -571,17 +643,19 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
             if (!wait_count(&p.counters[0], gridDim.x)) give_up();
         }
         consumer_sync<kWarps>();
-        // every CTA makes the same choice, as many tokens at a time as fit
-        uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
-        const int at_once = min(p.T, kChoiceKeys / p.E);
-        for (int t0 = 0; t0 < p.T; t0 += at_once) {
-            const int n = min(at_once, p.T - t0) * p.E;
-            for (int i = threadIdx.x; i < n; i += 32 * kWarps) keys[i] = logit_key(__ldcg(p.logits + t0 * p.E + i));
+        if (by_token) {
+            for (int i = threadIdx.x; i < slots; i += 32 * kWarps) {
+                r.expert[i] = __ldcg(p.chosen + i);
+                if (abort_flag) r.expert[i] = 0;  // never written
+                r.weight[i] = __ldcg(p.chosen_weight + i);
+            }
+        } else {
+            for (int i = threadIdx.x; i < p.T * p.E; i += 32 * kWarps) keys[i] = logit_key(__ldcg(p.logits + i));
             consumer_sync<kWarps>();
-            for (int t = t0 + warp; t < min(p.T, t0 + at_once); t += kWarps) choose_experts(p, t, keys + (t - t0) * p.E, r);
-            consumer_sync<kWarps>();
+            for (int t = warp; t < p.T; t += kWarps) choose_experts(p, keys + t * p.E, r.expert + t * p.top_k, r.weight + t * p.top_k);
         }
-        group_slots<kWarps>(p, r, 8 * NT);
+        consumer_sync<kWarps>();
+        group_slots<kWarps>(p, r, keys, 8 * NT);
         if (threadIdx.x == 0 && abort_flag) r.pairs = 0;
         for (int t = threadIdx.x; t < p.T; t += 32 * kWarps) r.x_scale[t] = Cfg::kScaledX ? __ldcg(p.x_scale + t) : 1.f;
     }
@@ -589,7 +663,7 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
     __syncthreads();
     const int units1 = r.pairs * rg1, units2 = r.pairs * rg2 * p.k_splits;
     if (blockIdx.x == 0)
-        for (int s = threadIdx.x; s < p.T * p.top_k && r.pairs; s += 32 * (kWarps + 1)) {
+        for (int s = threadIdx.x; s < p.T * p.top_k && r.pairs; s += kThreads) {
             if (p.ids) p.ids[s] = r.expert[s];
             if (p.weights) p.weights[s] = r.weight[s];
         }
@@ -599,34 +673,15 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
     bool h_fits = true;  // h is used as the first half wrote it
 
     if (warp == kWarps) {
-        // ------------------------------------------------ producer
+        // ------------------------------------------------ weights
         int stage = 0;
         uint32_t phase = 0, armed = 0, armed_parity = 0;
         bool ok = true;
-        // What this lane copies for a unit, worked out once for its stages:
-        // a token's row (lane < count), and with 8-bit weights one scale of
-        // the stage: of box lane % 16, its rows g or g + 8.
-        // Bytes of a token's k elements (two parts come in whole runs of 64).
-        auto act_bytes = [](bool first, int k) {
-            return first ? k * Cfg::kXBytes : Cfg::kTwoParts ? (k + 63) / 64 * 256 : k * Cfg::kHBytes;
-        };
-        int y = 0, count = 0;
-        const uint8_t *token = nullptr;
-        const float *scale = nullptr;
+        int y = 0;                     // matrix row of the unit
+        const float *scale = nullptr;  // 8-bit weights: this lane's scale of a stage, of box lane % 16, its rows g or g + 8
         auto begin_unit = [&](bool first, const Unit &n) {
             const int rows = first ? p.I : p.H, width = first ? p.H : p.I, lw = first ? p.lw1 : p.lw2;
             y = n.expert * rows + n.row;
-            count = n.count;
-            if (lane < count) {
-                const int slot = r.order[n.start + lane];
-                const int t = slot / p.top_k;
-                if (first)
-                    token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
-                                          : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
-                else
-                    token = Cfg::kTwoParts ? reinterpret_cast<const uint8_t *>(p.hidden) + slot * parts_bytes(p.I)
-                                           : reinterpret_cast<const uint8_t *>(p.hidden16 + static_cast<long long>(slot) * p.I);
-            }
             if constexpr (FP8) {
                 const int wrow = lane & ((1 << lw) - 1), box = (lane & 15) >> lw, upper = lane >> 4;
                 const int row = min(rows - 1, n.row + (first && gated ? wrow * 8 : wrow * 16 + upper * 8));
@@ -635,18 +690,16 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
                 scale = base + (n.expert * nbs + row / kScaleBlock) * kbs + box;
             }
         };
-        // Takes a free stage and starts the copies of its weights.
-        auto load_weights = [&](bool first, int ch) {
+        auto load_stage = [&](bool first, int ch) {
             if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u))) {
                 if (lane == 0) give_up();
                 ok = false;
                 return;
             }
             uint8_t *dst = ring + stage * p.stage_bytes;
-            const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes >> lw, width = first ? p.H : p.I;
-            const int k0 = ch * boxes * Cfg::kBoxK, k = min(boxes * Cfg::kBoxK, width - k0);
+            const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes >> lw, width = first ? p.H : p.I, k0 = ch * boxes * Cfg::kBoxK;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], kStageWeights + count * act_bytes(first, k));
+                mbar_arrive_expect_tx(&full[stage], kStageWeights);
                 if (first) {
                     const int half = gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
                     if (p.flat_h) {
@@ -668,72 +721,74 @@ __global__ void __launch_bounds__(32 * (moe_warps(NT) + 1), 1)
             }
             __syncwarp();
             if constexpr (FP8) {
-                if (k0 + ((lane & 15) >> lw) * Cfg::kBoxK < width)
-                    cp_async_4(dst + kStageWeights + lane * 4, scale + ch * boxes, 4);
+                if (k0 + ((lane & 15) >> lw) * Cfg::kBoxK < width) cp_async_4(dst + kStageWeights + lane * 4, scale + ch * boxes, 4);
                 cp_async_arrive(&full[stage]);
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        };
-        // The activations of the same k.
-        auto load_tokens = [&](bool first, int ch, int at) {
-            const int lw = first ? p.lw1 : p.lw2, kc = (kBoxes >> lw) * Cfg::kBoxK, k0 = ch * kc, k = min(kc, (first ? p.H : p.I) - k0);
-            if (lane < count)
-                bulk_load(ring + at * p.stage_bytes + Cfg::kActOffset + lane * Cfg::act_stride(lw, first),
-                          token + k0 * (first ? Cfg::kXBytes : Cfg::kHBytes), act_bytes(first, k), &full[at]);
-        };
-        auto next = [&] {
             if (++stage == p.stages) stage = 0, phase ^= 1u;
         };
         for (int u = blockIdx.x; ok && u < units1; u += grid) {
             begin_unit(true, first_unit(r, u, rg1, rows1, nch1));
-            for (int ch = 0; ch < nch1; ++ch) {
-                load_weights(true, ch);
-                if (!ok) break;
-                load_tokens(true, ch, stage);
-                next();
-            }
+            for (int ch = 0; ok && ch < nch1; ++ch) load_stage(true, ch);
         }
-        // Down projection: fill the ring with weights, wait for every CTA's h,
-        // then hand the h rows of those stages in and go on.
-        const int stage0 = stage;
-        int ahead = 0;
-        for (int u = shift; ok && u < units2 && ahead < p.stages; u += grid) {
+        for (int u = shift; ok && u < units2; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
             begin_unit(false, n);
-            for (int ch = n.ch0; ok && ch < n.ch1 && ahead < p.stages; ++ch) {
-                load_weights(false, ch);
-                if (ok) next(), ++ahead;
-            }
+            for (int ch = n.ch0; ok && ch < n.ch1; ++ch) load_stage(false, ch);
         }
-        if (ok && ahead > 0) {
+        __syncwarp();
+        // No copy may be in flight when the CTA ends.  After a time-out a stage
+        // may lack its tokens and never complete; its weights get 10 ms.
+        if (lane == 0)
+            for (int s = 0; s < p.stages; ++s)
+                if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u, abort_flag ? 10000000ull : kWaitLimitNs)) give_up();
+        __syncwarp();
+    } else if (warp > kWarps) {
+        // ------------------------------------------------ tokens
+        const int first_token = (warp - kWarps - 1) * (8 * NT / kTokenWarps);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        auto load_unit = [&](bool first, const Unit &n) {
+            const int width = first ? p.H : p.I, lw = first ? p.lw1 : p.lw2, kc = (kBoxes >> lw) * Cfg::kBoxK;
+            const int count = max(0, min(n.count - first_token, 8 * NT / kTokenWarps));  // of this warp
+            const int offset = Cfg::kActOffset + (first_token + lane) * Cfg::act_stride(lw, first);
+            const uint8_t *token = nullptr;
+            if (lane < count) {
+                const int slot = r.order[n.start + first_token + lane], t = slot / p.top_k;
+                if (first)
+                    token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
+                                          : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
+                else
+                    token = Cfg::kTwoParts ? reinterpret_cast<const uint8_t *>(p.hidden) + slot * parts_bytes(p.I)
+                                           : reinterpret_cast<const uint8_t *>(p.hidden16 + static_cast<long long>(slot) * p.I);
+            }
+            for (int ch = n.ch0; ok && ch < n.ch1; ++ch) {
+                if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u))) {
+                    if (lane == 0) give_up();
+                    ok = false;
+                    break;
+                }
+                // Bytes of a token's k's (two parts come in whole runs of 64).
+                const int k0 = ch * kc, k = min(kc, width - k0);
+                const int bytes = first ? k * Cfg::kXBytes : Cfg::kTwoParts ? (k + 63) / 64 * 256 : k * Cfg::kHBytes;
+                if (lane == 0) mbar_arrive_expect_tx(&full[stage], count * bytes);
+                __syncwarp();
+                if (lane < count)
+                    bulk_load(ring + stage * p.stage_bytes + offset, token + k0 * (first ? Cfg::kXBytes : Cfg::kHBytes), bytes, &full[stage]);
+                if (++stage == p.stages) stage = 0, phase ^= 1u;
+            }
+        };
+        for (int u = blockIdx.x; ok && u < units1; u += grid) load_unit(true, first_unit(r, u, rg1, rows1, nch1));
+        // h of every CTA has to be there (and fitted, if need be).
+        if (ok && shift < units2) {
             ok = __all_sync(0xffffffffu, wait_count(&p.counters[1], grid));
             if (ok && !Cfg::kTwoParts && !slots_fit(p)) ok = __all_sync(0xffffffffu, wait_count(&p.counters[2], grid));
             if (!ok && lane == 0) give_up();
             fence_proxy_async_all();
         }
-        int i = 0;
-        for (int u = shift; ok && u < units2; u += grid) {
-            const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
-            begin_unit(false, n);
-            for (int ch = n.ch0; ok && ch < n.ch1; ++ch, ++i) {
-                if (i < ahead) {
-                    load_tokens(false, ch, (stage0 + i) % p.stages);
-                } else {
-                    load_weights(false, ch);
-                    if (!ok) break;
-                    load_tokens(false, ch, stage);
-                    next();
-                }
-            }
-        }
-        __syncwarp();
-        // A stage whose h rows were never asked for cannot complete; its weight
-        // copies are in flight all the same: give them the time of a bounded wait.
-        if (lane == 0)
-            for (int s = 0; s < p.stages; ++s)
-                if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u, ok ? kWaitLimitNs : 10000000ull)) give_up();
-        __syncwarp();
+        for (int u = shift; ok && u < units2; u += grid) load_unit(false, down_unit(r, u, rows2, nch2, p.k_splits));
     } else {
         // ------------------------------------------------ arithmetic
         int stage = 0, buf = 0;
@@ -985,7 +1040,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.lw1, true), Cfg::act_stride(a.lw2, false));
     a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
     constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * moe_warps(NT) * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
-    static_assert(kRing >= 1024 + kChoiceKeys * 4 && kChoiceKeys >= kMoeMaxExperts, "the ring holds the keys of the choice");
+    static_assert(kRing >= 1024 + kTokensOfTheirOwn * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
     a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);  // two at least: 2 x (32 + 32) KB and paddings
     const int wb = Cfg::kWBytes;
     const auto dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
@@ -1006,7 +1061,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     attr.val.cooperative = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(device_sm_count());
-    cfg.blockDim = dim3(32 * (moe_warps(NT) + 1));
+    cfg.blockDim = dim3(moe_threads(NT));
     cfg.dynamicSmemBytes = kRing;
     cfg.stream = stream;
     cfg.attrs = &attr;
@@ -1059,7 +1114,7 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     const size_t n_h16 = up64(n_slots * m.I / 2), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
     Scratch s;
     const cudaError_t e =
-        acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);
+        acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + 3 * n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
     a.hidden = a.logits + n_logits;
@@ -1067,7 +1122,9 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     a.x16 = reinterpret_cast<__half *>(a.hidden + n_hidden + n_h16);
     a.h_max = reinterpret_cast<unsigned *>(a.hidden + n_hidden + n_h16 + n_x16);
     a.x_scale = a.hidden + n_hidden + n_h16 + n_x16 + n_max;
-    a.part = a.x_scale + up64(m.T);
+    a.chosen_weight = a.x_scale + up64(m.T);
+    a.chosen = reinterpret_cast<uint16_t *>(a.chosen_weight + n_max);
+    a.part = a.chosen_weight + 2 * n_max;
     a.counters = s.counters;
     info->launches = 1;
     info->plan = "moe_few_tokens";
