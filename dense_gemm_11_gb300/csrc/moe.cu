@@ -110,6 +110,9 @@ struct Routing {
     uint8_t pair_groups[kMoeMaxSlots], pair_count[kMoeMaxSlots];
     int offset[kMoeMaxExperts + 1];
     int pairs;
+    uint32_t per_token;  // 65536 / top_k, rounded up
+    // Token of a slot: slot / top_k, exact for slots < 1024 and top_k <= 16.
+    __device__ __forceinline__ int token(int slot) const { return static_cast<int>(slot * per_token >> 16); }
 };
 
 template <int XT>
@@ -656,6 +659,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         }
         consumer_sync<kWarps>();
         group_slots<kWarps>(p, r, keys, 8 * NT);
+        if (threadIdx.x == 0) r.per_token = (65536u + p.top_k - 1) / p.top_k;
         if (threadIdx.x == 0 && abort_flag) r.pairs = 0;
         for (int t = threadIdx.x; t < p.T; t += 32 * kWarps) r.x_scale[t] = Cfg::kScaledX ? __ldcg(p.x_scale + t) : 1.f;
     }
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
             const int offset = Cfg::kActOffset + (first_token + lane) * Cfg::act_stride(lw, first);
             const uint8_t *token = nullptr;
             if (lane < count) {
-                const int slot = r.order[n.start + first_token + lane], t = slot / p.top_k;
+                const int slot = r.order[n.start + first_token + lane], t = r.token(slot);
                 if (first)
                     token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
                                           : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
@@ -854,40 +858,50 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[i][j] = kMine == 2 ? part[0][i][j] + part[kMine - 1][i][j] : part[0][i][j];
-            // Warps of the same rows: the first one adds the others' sums.
-            if (sharers > 1) {
-                if (my_box > 0) {
+            // Warps of the same rows add their sums, in the order of their
+            // boxes: the first one for the even tokens, the second for the odd.
+            if (sharers == 1) return 3;
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
+                if (i * 8 < n.count)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) red[buf][warp][i][j][lane] = acc[i][j];
+                    for (int j = 0; j < 4; ++j) red[buf][warp][i][j][lane] = acc[i][j];
+            consumer_sync<kWarps>();
+            if (my_box < 2) {
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    if (i * 8 >= n.count) break;
+                    float lo = 0.f, hi = 0.f;
+                    for (int b = 0; b < sharers; ++b) {
+                        lo += red[buf][(b << lw) + my_row][i][my_box][lane];
+                        hi += red[buf][(b << lw) + my_row][i][my_box + 2][lane];
+                    }
+                    if (my_box == 0)
+                        acc[i][0] = lo, acc[i][2] = hi;
+                    else
+                        acc[i][1] = lo, acc[i][3] = hi;
                 }
-                consumer_sync<kWarps>();
-                if (my_box == 0) {
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            for (int b = 1; b < sharers; ++b) acc[i][j] += red[buf][(b << lw) + my_row][i][j][lane];
-                }
-                buf ^= 1;
             }
-            return my_box == 0;
+            buf ^= 1;
+            return my_box == 0 ? 1 : my_box == 1 ? 2 : 0;
         };
-        // Element i of a fragment: row g + 8 (i / 2), token 2 (lane % 4) + i % 2.
+        // Element i of a fragment: row g + 8 (i / 2), token 2 (lane % 4) + i % 2;
+        // bit j of what unit_sums returns says that this warp has tokens of
+        // i % 2 == j.
         float acc[NT][4];
         for (int u = blockIdx.x; u < units1; u += grid) {
             const Unit n = first_unit(r, u, rg1, rows1, nch1);
-            if (!unit_sums(std::true_type{}, n, acc)) continue;
+            const int mine = unit_sums(std::true_type{}, n, acc);
             const int row = n.row + (warp & ((1 << p.lw1) - 1)) * (gated ? 8 : 16) + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
+                    if (!(mine & (1 << j)) || nt * 8 + j >= n.count) continue;
                     const int tok = nt * 8 + 2 * (lane & 3) + j;
                     const bool in = tok < n.count;
-                    const int slot = in ? r.order[n.start + tok] : 0;
-                    const float xs = Cfg::kScaledX ? r.x_scale[slot / p.top_k] : 1.f;
+                    const int slot = r.order[n.start + min(tok, n.count - 1)];
+                    const float xs = Cfg::kScaledX ? r.x_scale[r.token(slot)] : 1.f;
                     float largest = 0.f;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
@@ -945,14 +959,14 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         const long long slots = static_cast<long long>(p.T) * p.top_k;
         for (int u = shift; u < units2; u += grid) {
             const Unit n = down_unit(r, u, rows2, nch2, p.k_splits);
-            if (!unit_sums(std::false_type{}, n, acc)) continue;
+            const int mine = unit_sums(std::false_type{}, n, acc);
             const int row = n.row + (warp & ((1 << p.lw2) - 1)) * 16 + g;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = nt * 8 + 2 * (lane & 3) + (i & 1), at = row + 8 * (i >> 1);
-                    if (tok < n.count && at < p.H) p.part[(n.split * slots + r.order[n.start + tok]) * p.H + at] = acc[nt][i];
+                    if ((mine & (1 << (i & 1))) && tok < n.count && at < p.H) p.part[(n.split * slots + r.order[n.start + tok]) * p.H + at] = acc[nt][i];
                 }
         }
         // ------------------------------------------------ sum over a token's experts
