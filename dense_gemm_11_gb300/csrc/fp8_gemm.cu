@@ -11,10 +11,14 @@
 // accumulators in tensor memory alternate: while the warps take one block's
 // sums out, the tensor core forms the next.
 //
-// Tiles are computed transposed, C^T = op(B)^T A^T: 128 columns n of C on the
-// MMA's row side (tensor-memory lanes), BN rows m on its column side, so that
-// a few rows of A cost no more than BN >= M columns of accumulator and a warp
-// stores 32 consecutive elements of a row of C.
+// Two kernels:
+//   fp8_tile_kernel   one CTA a tile, computed transposed, C^T = op(B)^T A^T:
+//                     128 columns n of C on the MMA's row side (tensor-memory
+//                     lanes), BN rows m on its column side, so that a few rows
+//                     of A cost no more than BN >= M columns of accumulator and
+//                     a warp stores 32 consecutive elements of a row of C;
+//   fp8_pair_kernel   two CTAs (tcgen05 cta_group::2) a tile of 256 x 256,
+//                     persistent, for many rows.
 //
 // Roles of a CTA: warp 0 issues the TMA loads (operand tiles with the 128-byte
 // swizzle, and the BN scales of A for the block), warp 1 the MMAs, the others
@@ -329,6 +333,347 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
     cluster_sync();  // a CTA's partial stays until every CTA has read it
 }
 
+// ------------------------------------------------------------------ CTA pairs
+// A cluster of two CTAs computes 256 x 256 tiles of C: CTA r stages rows
+// [m0 + 128 r, + 128) of A and columns [n0 + 128 r, + 128) of op(B), 32 KB for a
+// k block; the even CTA's MMA thread multiplies the pair, and each CTA's own
+// tensor memory receives the block's sums of its 128 rows x 256 columns, twice
+// buffered (all 512 columns).  Sixteen epilogue warps hold the running sums, 64
+// a thread: warp w has lane quarter w % 4 and 64 columns, in one scale block of
+// B.  Eight warps with 128 columns each could not hide the latency of their
+// tensor-memory reads (340 us against ??? at 4096 x 11008 x 4096).
+// Bound: what the TMA unit brings in.  It delivers 43.6 bytes a clock to an SM,
+// so a k block takes 750 clocks to stage and 512 to multiply; a 256 x 256 tile
+// is the most that the accumulators leave room for.
+constexpr int kPairStages = 4;
+constexpr int kPairEpi = 16;
+constexpr int kPairN = 256;
+constexpr int kPairCols = kPairN * 4 / kPairEpi;  // of an epilogue warp
+
+template <bool B_ROWS>
+struct Fp8PairCfg {
+    static constexpr int kThreads = 64 + 32 * kPairEpi;
+    static constexpr int kHalfBytes = 128 * kScaleBlock;  // this CTA's rows of A, and columns of op(B)
+    static constexpr int kStageBytes = 2 * kHalfBytes;
+    static constexpr int kSlots = kPairStages + 2;  // as in Fp8Cfg
+    static constexpr int kSlotFloats = 128 + (B_ROWS ? kPairN : 0);
+    static constexpr int kCStage = kPairEpi * 4096;  // staging of C, 4 KB a warp
+    static constexpr int kSmemBytes =
+        1024 + kPairStages * kStageBytes + kCStage + kSlots * kSlotFloats * 4 + (2 * kPairStages + 5) * 8 + 16;
+};
+
+struct Fp8PairArgs {
+    Fp8Args a;
+    int tiles_m, tiles_n, c_tma;
+};
+
+// Tile t: groups of 8 pair rows, so that a wave of tiles shares its rows of A
+// and columns of op(B) in L2.
+__device__ __forceinline__ void fp8_pair_origin(const Fp8PairArgs &p, int t, int &m0, int &n0) {
+    const int group = 8 * p.tiles_n;
+    const int first = t / group * 8, rows = min(p.tiles_m - first, 8);
+    m0 = (first + t % group % rows) * 256;
+    n0 = t % group / rows * kPairN;
+}
+
+// act(alpha * v + beta * C + bias) of columns n .. n + 31 of row m; the whole
+// warp together.  The GELU forms run as a rolled loop that rotates v by 8 a
+// trip: a quarter of the code beside the main loop.
+__device__ __forceinline__ void epilogue32(const Fp8Args &p, float (&v)[32], int m, int n, int lane) {
+    const float bias = p.bias && n + lane < p.N ? __ldg(p.bias + n + lane) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] *= p.alpha;
+    if (p.beta != 0.f && m < p.M) {
+        const size_t ci = static_cast<size_t>(m) * static_cast<size_t>(p.ldc) + n;
+        if (p.c_type == kOutF32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j < p.N) v[j] = fmaf(p.beta, static_cast<const float *>(p.C)[ci + j], v[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (n + j < p.N) v[j] = fmaf(p.beta, load_out(p.C, ci + j, p.c_type), v[j]);
+        }
+    }
+    if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, bias, j);
+    }
+    if (p.act == 2) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = fmaxf(v[j], 0.f);
+    } else if (p.act != 0) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = p.act == 1 ? gelu_erf(v[i]) : gelu_tanh(v[i]);
+#pragma unroll
+            for (int i = 0; i < 24; ++i) v[i] = v[i + 8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[24 + i] = t[i];
+        }
+    }
+}
+
+// 32 columns of this lane's row through the warp's staging buffer (128-byte
+// rows, 128-byte swizzle) to a TMA store: 32 columns of FP32, or 64 of a 16-bit
+// type, of which `second` is the upper half.
+__device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], const CUtensorMap *tm_c, uint8_t *staged, int lane,
+                                        int row, int n, int second) {
+    const bool wide = p.c_type == kOutF32;
+    if (wide || !second) {  // the buffer's last store has read it
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+    }
+    uint8_t *mine = staged + lane * 128;
+    if (wide) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4 *>(mine + ((c ^ (lane & 7)) << 4)) = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4 *>(mine + (((c + 4 * second) ^ (lane & 7)) << 4)) =
+                make_uint4(pack2_out16(v[8 * c], v[8 * c + 1], p.c_type), pack2_out16(v[8 * c + 2], v[8 * c + 3], p.c_type),
+                           pack2_out16(v[8 * c + 4], v[8 * c + 5], p.c_type), pack2_out16(v[8 * c + 6], v[8 * c + 7], p.c_type));
+    }
+    if (wide || second) {
+        const int first = wide ? n : n - 32;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            if (first < p.N) tma_store_2d(tm_c, staged, first, row);
+            bulk_commit();
+        }
+    }
+}
+
+// The same straight from registers, for a C without aligned rows.
+__device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], int m, int n) {
+    const size_t ci = static_cast<size_t>(m) * static_cast<size_t>(p.ldc) + n;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
+}
+
+template <bool B_ROWS>
+__global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                    const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                    const __grid_constant__ CUtensorMap tm_c, const Fp8PairArgs pp) {
+    using Cfg = Fp8PairCfg<B_ROWS>;
+    const Fp8Args &p = pp.a;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sA = smem, *sB = smem + kPairStages * Cfg::kHalfBytes, *sC = sB + kPairStages * Cfg::kHalfBytes;
+    float *sS = reinterpret_cast<float *>(sC + Cfg::kCStage);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sS + Cfg::kSlots * Cfg::kSlotFloats);
+    uint64_t *empty = full + kPairStages;
+    uint64_t *tfull = empty + kPairStages;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1, tiles = pp.tiles_m * pp.tiles_n;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 2 * kPairEpi);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tm_a);
+        tma_prefetch_desc(&tm_b);
+        tma_prefetch_desc(&tm_sa);
+        tma_prefetch_desc(&tm_c);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_holder, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_holder;
+    pdl_wait();
+    pdl_launch_dependents();
+    uint32_t armed = 0, armed_parity = 0;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------ TMA producer (both CTAs)
+        const uint32_t tx = Cfg::kStageBytes + 512 + (B_ROWS ? kPairN * 4 : 0);
+        int stage = 0, slot = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
+            int m0, n0;
+            fp8_pair_origin(pp, t, m0, n0);
+            const int my_m = m0 + static_cast<int>(rank) * 128, my_n = n0 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                if (!mbar_wait_patient(&empty[stage], phase ^ 1u, p.wait_ns)) {
+                    fp8_timeout(abort_flag, p.err);
+                    ok = false;
+                    break;
+                }
+                if (leader) mbar_arrive_expect_tx(&full[stage], 2 * tx);
+                const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+                const int k0 = kb * kScaleBlock;
+                float *sc = sS + slot * Cfg::kSlotFloats;
+                tma_load_2d_pair(&tm_a, bar, sA + stage * Cfg::kHalfBytes, k0, my_m);
+                if (p.p_mn)
+                    tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, my_n, k0);
+                else
+                    tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, k0, my_n);
+                tma_load_2d_pair(&tm_sa, bar, sc, my_m, kb);
+                if (B_ROWS) tma_load_2d_pair(&tm_sb, bar, sc + 128, n0, kb);
+                armed |= 1u << stage;
+                armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+                if (kDebugBuild && !mbar_wait(&empty[stage], phase, p.wait_ns)) {  // one stage in flight
+                    fp8_timeout(abort_flag, p.err);
+                    ok = false;
+                    break;
+                }
+                if (++stage == kPairStages) stage = 0, phase ^= 1u;
+                if (++slot == Cfg::kSlots) slot = 0;
+            }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------ MMA issuer (even CTA)
+        const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), 16, 1024);
+        const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), 16, 1024);
+        const uint32_t b_step = p.p_mn ? 4096u >> 4 : 32u >> 4;
+        int stage = 0, i = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
+            for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
+                const int buf = i & 1;
+                if (!mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) ||
+                    !mbar_wait_patient(&full[stage], phase, p.wait_ns)) {
+                    fp8_timeout(abort_flag, p.err);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage * (Cfg::kHalfBytes >> 4));
+                const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage * (Cfg::kHalfBytes >> 4));
+#pragma unroll
+                for (int kk = 0; kk < kScaleBlock / 32; ++kk)
+                    umma_f8_pair(tmem_base + buf * kPairN, ad + 2u * kk, bd + b_step * kk, p.idesc, kk > 0 ? 1u : 0u);
+                umma_commit_pair_mc(&empty[stage], 0x3);
+                umma_commit_pair_mc(&tfull[buf], 0x3);
+                if (++stage == kPairStages) stage = 0, phase ^= 1u;
+            }
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------ epilogue (both CTAs)
+        const int q = warp & 3, part = (warp - 2) >> 2;
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kPairCols;
+        const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+        uint8_t *const staged = sC + (warp - 2) * 4096;
+        int i = 0, slot = 0;
+        bool ok = true;
+        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
+            int m0, n0;
+            fp8_pair_origin(pp, t, m0, n0);
+            const int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * kPairCols;
+            float2 acc[kPairCols / 2];
+#pragma unroll
+            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            // B's scale of this warp's columns, one k block ahead
+            const float *sb = p.SB + min(col, p.N - 1) / kScaleBlock * p.sb_n;
+            float s_next = B_ROWS ? 1.f : __ldg(sb);
+            for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
+                const int buf = i & 1;
+                float s = s_next;
+                if (!B_ROWS && kb + 1 < p.kb_total) s_next = __ldg(sb + (kb + 1) * p.sb_kb);
+                if (!mbar_wait_patient(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
+                    fp8_timeout(abort_flag, p.err);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const float *sc = sS + slot * Cfg::kSlotFloats;
+                s *= sc[q * 32 + lane];
+                const float2 ss = make_float2(s, s);
+                const float4 *sbv = reinterpret_cast<const float4 *>(sc + 128 + part * kPairCols);
+                constexpr int kAtOnce = B_ROWS ? 1 : 2;  // reads of 16 columns in flight (registers)
+#pragma unroll
+                for (int c = 0; c < kPairCols / 16; c += kAtOnce) {
+                    uint32_t r[kAtOnce][16];
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u) tmem_ld_32x32b_x16(t_row + buf * kPairN + (c + u) * 16, r[u]);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < kAtOnce; ++u)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float2 f0 = ss, f1 = ss;
+                            if (B_ROWS) {
+                                const float4 b = sbv[(c + u) * 4 + j];
+                                f0 = __fmul2_rn(ss, make_float2(b.x, b.y));
+                                f1 = __fmul2_rn(ss, make_float2(b.z, b.w));
+                            }
+                            float2 &lo = acc[(c + u) * 8 + 2 * j], &hi = acc[(c + u) * 8 + 2 * j + 1];
+                            lo = __ffma2_rn(f0, make_float2(__uint_as_float(r[u][4 * j]), __uint_as_float(r[u][4 * j + 1])), lo);
+                            hi = __ffma2_rn(f1, make_float2(__uint_as_float(r[u][4 * j + 2]), __uint_as_float(r[u][4 * j + 3])), hi);
+                        }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(release[buf]);
+                if (++slot == Cfg::kSlots) slot = 0;
+            }
+            if (!ok || row >= p.M) continue;
+            // The tile is done: 32 columns at a time to the epilogue and out.
+            const int m = row + lane;
+#pragma unroll
+            for (int gr = 0; gr < kPairCols / 32; ++gr) {
+                const int n = col + gr * 32;
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[2 * j] = acc[gr * 16 + j].x, v[2 * j + 1] = acc[gr * 16 + j].y;
+                epilogue32(p, v, m, n, lane);
+                if (pp.c_tma)
+                    stage32(p, v, &tm_c, staged, lane, row, n, gr & 1);
+                else if (m < p.M)
+                    store32(p, v, m, n);
+            }
+        }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
+    }
+
+    // ---------------------------------------------------- drain and unwind
+    if (warp == 0 && lane == 0 && leader) {
+        // the even CTA's full barriers count the copies of both CTAs
+        for (int s = 0; s < kPairStages; ++s)
+            if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u)) fp8_timeout(abort_flag, p.err);
+    }
+    if (warp == 1 && lane == 0 && leader) {
+        umma_commit_pair_mc(mma_done, 0x1);
+        if (!mbar_wait(mma_done, 0)) fp8_timeout(abort_flag, p.err);
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
 // C = act(beta * C + bias), where there is no product.
 __global__ void __launch_bounds__(256) fp8_scale_c_kernel(const Fp8Args p) {
     pdl_wait();
@@ -416,6 +761,62 @@ cudaError_t launch_fp8_tile(const Fp8Gemm &g, Fp8Args a, cudaStream_t stream) {
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
+template <bool B_ROWS>
+cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, cudaStream_t stream) {
+    using Cfg = Fp8PairCfg<B_ROWS>;
+    auto kern = fp8_pair_kernel<B_ROWS>;
+    static int max_clusters = -1;  // one device type per process; atomic accesses
+    static unsigned long long smem_set = 0;
+    cudaError_t e = ensure_dynamic_smem(kern, Cfg::kSmemBytes, smem_set);
+    if (e != cudaSuccess) return e;
+    Fp8PairArgs args = {};
+    args.a = a;
+    args.tiles_m = (g.M + 255) / 256;
+    args.tiles_n = (g.N + kPairN - 1) / kPairN;
+    const int cb = g.c_type == kOutF32 ? 4 : 2;
+    // TMA stores of C need aligned rows; any other C is stored element by element.
+    args.c_tma = reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && g.ldc * cb % 16 == 0;
+    args.a.idesc = umma_idesc_f8(256, kPairN, g.a_type == kTypeE5M2, g.b_type == kTypeE5M2, 0, a.p_mn);
+    CUtensorMap ta, tb, tsa, tsb, tc;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const auto ct = g.c_type == kOutF32 ? f32 : g.c_type == kOutF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    bool ok = encode_matrix_map(&ta, u8, g.A, g.K, g.M, g.lda, kScaleBlock, 128, sw) &&
+              (g.b_trans ? encode_matrix_map(&tb, u8, g.B, g.K, g.N, g.ldb, kScaleBlock, 128, sw)
+                         : encode_matrix_map(&tb, u8, g.B, g.N, g.K, g.ldb, 128, kScaleBlock, sw)) &&
+              encode_matrix_map(&tsa, f32, g.SA, g.M, a.kb_total, g.ldsa * 4, 128, 1, none);
+    tsb = tsa;
+    tc = ta;  // not used without TMA stores
+    if (ok && B_ROWS) ok = encode_matrix_map(&tsb, f32, g.SB, g.N, a.kb_total, g.ldsb * 4, kPairN, 1, none);
+    if (ok && args.c_tma) ok = encode_matrix_map(&tc, ct, g.C, g.N, g.M, g.ldc * cb, 128 / cb, 32, sw);
+    if (!ok) return cudaErrorNotSupported;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(Cfg::kThreads);
+    cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = __atomic_load_n(&max_clusters, __ATOMIC_ACQUIRE);
+    if (clusters < 0) {
+        cfg.gridDim = dim3(2 * device_sm_count());
+        e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+        if (e != cudaSuccess) return e;
+        __atomic_store_n(&max_clusters, clusters, __ATOMIC_RELEASE);
+    }
+    if (clusters < 1) return cudaErrorNotSupported;
+    cfg.gridDim = dim3(2 * std::min(clusters, args.tiles_m * args.tiles_n));
+    cfg.numAttrs = 2;
+    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, tc, args);
+    return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
 }  // namespace
 
 bool encode_matrix_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
@@ -450,6 +851,10 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) 
     const int sms = device_sm_count();
     if (tiles * 2 <= sms) a.splits = static_cast<int>(std::min<long long>({8, sms / tiles, std::max(1, a.kb_total / 2)}));
     info->launches = 1;
+    if (g.M > 128) {
+        info->plan = "fp8_pair_256x256";
+        return g.b_rows ? launch_fp8_pair<true>(g, a, stream) : launch_fp8_pair<false>(g, a, stream);
+    }
     switch (bn) {
         case 16: info->plan = "fp8_tile_n16"; return launch_fp8_tile<16, 10>(g, a, stream);
         case 32: info->plan = "fp8_tile_n32"; return launch_fp8_tile<32, 9>(g, a, stream);
