@@ -15,6 +15,14 @@ __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity
     return mbar_wait(bar, parity, limit_ns);
 }
 
+// Arrive on an mbarrier of another CTA of the cluster, releasing at CTA scope:
+// for a consumer's "I have read it" whose reads have completed (their values
+// were used).  The cluster-scope release of mbar_arrive_cluster waits for every
+// earlier memory operation of the thread: 1,500 cycles in the product's loop.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // D(tmem) (+)= A(smem desc) x B(smem desc), 8-bit operands, K = 32 per
 // instruction (32 bytes of each K-major row).
 __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,

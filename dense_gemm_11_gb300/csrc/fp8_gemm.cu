@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(release[buf]);
+                if (lane == 0) mbar_arrive_remote(release[buf]);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             if (!ok || row >= p.M) continue;
