@@ -15,6 +15,23 @@ __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity
     return mbar_wait(bar, parity, limit_ns);
 }
 
+// True in one lane of a warp that runs together.  A warp whose loop is uniform
+// and only guards its tcgen05 and TMA instructions with this keeps their
+// operands (descriptors, addresses) in uniform registers; a loop inside a
+// one-lane branch moves them there for every instruction, which took 125
+// cycles an MMA, as long as the MMA itself.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " elect.sync _|p, 0xffffffff;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Arrive on an mbarrier of another CTA of the cluster, releasing at CTA scope:
 // for a consumer's "I have read it" whose reads have completed (their values
 // were used).  The cluster-scope release of mbar_arrive_cluster waits for every

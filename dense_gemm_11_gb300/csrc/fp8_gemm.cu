@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1, tiles = pp.tiles_m * pp.tiles_n;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     pdl_launch_dependents();
     uint32_t armed = 0, armed_parity = 0;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
         const uint32_t tx = Cfg::kStageBytes + 512 + (B_ROWS ? kPairN * 4 : 0);
         int stage = 0, slot = 0;
@@ -520,34 +520,39 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             fp8_pair_origin(pp, t, m0, n0);
             const int my_m = m0 + static_cast<int>(rank) * 128, my_n = n0 + static_cast<int>(rank) * 128;
             for (int kb = 0; kb < p.kb_total; ++kb) {
-                if (!mbar_wait_patient(&empty[stage], phase ^ 1u, p.wait_ns)) {
+                ok = __all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u, p.wait_ns));
+                if (!ok) {
                     fp8_timeout(abort_flag, p.err);
-                    ok = false;
                     break;
                 }
-                if (leader) mbar_arrive_expect_tx(&full[stage], 2 * tx);
                 const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
                 const int k0 = kb * kScaleBlock;
-                float *sc = sS + slot * Cfg::kSlotFloats;
-                tma_load_2d_pair(&tm_a, bar, sA + stage * Cfg::kHalfBytes, k0, my_m);
-                if (p.p_mn)
-                    tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, my_n, k0);
-                else
-                    tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, k0, my_n);
-                tma_load_2d_pair(&tm_sa, bar, sc, my_m, kb);
-                if (B_ROWS) tma_load_2d_pair(&tm_sb, bar, sc + 128, n0, kb);
+                if (elect_one()) {
+                    float *sc = sS + slot * Cfg::kSlotFloats;
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * tx);
+                    tma_load_2d_pair(&tm_a, bar, sA + stage * Cfg::kHalfBytes, k0, my_m);
+                    if (p.p_mn)
+                        tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, my_n, k0);
+                    else
+                        tma_load_2d_pair(&tm_b, bar, sB + stage * Cfg::kHalfBytes, k0, my_n);
+                    tma_load_2d_pair(&tm_sa, bar, sc, my_m, kb);
+                    if (B_ROWS) tma_load_2d_pair(&tm_sb, bar, sc + 128, n0, kb);
+                }
+                __syncwarp();
                 armed |= 1u << stage;
                 armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-                if (kDebugBuild && !mbar_wait(&empty[stage], phase, p.wait_ns)) {  // one stage in flight
-                    fp8_timeout(abort_flag, p.err);
-                    ok = false;
-                    break;
+                if (kDebugBuild) {  // one stage in flight
+                    ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, p.wait_ns));
+                    if (!ok) {
+                        fp8_timeout(abort_flag, p.err);
+                        break;
+                    }
                 }
                 if (++stage == kPairStages) stage = 0, phase ^= 1u;
                 if (++slot == Cfg::kSlots) slot = 0;
             }
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------ MMA issuer (even CTA)
         const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), 16, 1024);
         const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), 16, 1024);
@@ -558,20 +563,23 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
-                if (!mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) ||
-                    !mbar_wait_patient(&full[stage], phase, p.wait_ns)) {
+                ok = __all_sync(0xffffffffu, mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) &&
+                                                 mbar_wait_patient(&full[stage], phase, p.wait_ns));
+                if (!ok) {
                     fp8_timeout(abort_flag, p.err);
-                    ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage * (Cfg::kHalfBytes >> 4));
                 const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage * (Cfg::kHalfBytes >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kScaleBlock / 32; ++kk)
-                    umma_f8_pair(tmem_base + buf * kPairN, ad + 2u * kk, bd + b_step * kk, p.idesc, kk > 0 ? 1u : 0u);
-                umma_commit_pair_mc(&empty[stage], 0x3);
-                umma_commit_pair_mc(&tfull[buf], 0x3);
+                    for (int kk = 0; kk < kScaleBlock / 32; ++kk)
+                        umma_f8_pair(tmem_base + buf * kPairN, ad + 2u * kk, bd + b_step * kk, p.idesc, kk > 0 ? 1u : 0u);
+                    umma_commit_pair_mc(&empty[stage], 0x3);
+                    umma_commit_pair_mc(&tfull[buf], 0x3);
+                }
+                __syncwarp();
                 if (++stage == kPairStages) stage = 0, phase ^= 1u;
             }
         }
