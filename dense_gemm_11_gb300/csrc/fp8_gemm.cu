@@ -355,7 +355,7 @@ struct Fp8PairCfg {
     static constexpr int kThreads = 64 + 32 * kPairEpi;
     static constexpr int kHalfBytes = 128 * kScaleBlock;  // this CTA's rows of A, and columns of op(B)
     static constexpr int kStageBytes = 2 * kHalfBytes;
-    static constexpr int kSlots = kPairStages + 2;  // as in Fp8Cfg
+    static constexpr int kSlots = kPairStages + 3;  // as in Fp8Cfg, and one for reads after a block's release
     static constexpr int kSlotFloats = 128 + (B_ROWS ? kPairN : 0);
     static constexpr int kCStage = kPairEpi * 4096;  // staging of C, 4 KB a warp
     static constexpr int kSmemBytes =
@@ -455,6 +455,24 @@ __device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], 
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
+}
+
+// acc[COL ..] += s * (B's scale of the column, with B_ROWS) * r, 16 columns.
+template <bool B_ROWS, int COL>
+__device__ __forceinline__ void add_scaled(float2 (&acc)[kPairCols / 2], const uint32_t (&r)[16], float s, const float4 *sb) {
+    const float2 ss = make_float2(s, s);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float2 f0 = ss, f1 = ss;
+        if (B_ROWS) {
+            const float4 b = sb[COL / 4 + j];
+            f0 = __fmul2_rn(ss, make_float2(b.x, b.y));
+            f1 = __fmul2_rn(ss, make_float2(b.z, b.w));
+        }
+        float2 &lo = acc[COL / 2 + 2 * j], &hi = acc[COL / 2 + 2 * j + 1];
+        lo = __ffma2_rn(f0, make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), lo);
+        hi = __ffma2_rn(f1, make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), hi);
+    }
 }
 
 template <bool B_ROWS>
@@ -599,7 +617,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
             // B's scale of this warp's columns, one k block ahead
-            const float *sb = p.SB + min(col, p.N - 1) / kScaleBlock * p.sb_n;
+            const float *sb = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
             float s_next = B_ROWS ? 1.f : __ldg(sb);
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
@@ -611,35 +629,26 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                     break;
                 }
                 tc_fence_after();
+                // Two reads of 16 columns in flight; the accumulator goes back
+                // as soon as the last read is in, before its sums are added.
+                const uint32_t from = t_row + buf * kPairN;
+                uint32_t r0[16], r1[16];
+                tmem_ld_32x32b_x16(from, r0);
+                tmem_ld_32x32b_x16(from + 16, r1);
                 const float *sc = sS + slot * Cfg::kSlotFloats;
                 s *= sc[q * 32 + lane];
-                const float2 ss = make_float2(s, s);
                 const float4 *sbv = reinterpret_cast<const float4 *>(sc + 128 + part * kPairCols);
-                constexpr int kAtOnce = B_ROWS ? 1 : 2;  // reads of 16 columns in flight (registers)
-#pragma unroll
-                for (int c = 0; c < kPairCols / 16; c += kAtOnce) {
-                    uint32_t r[kAtOnce][16];
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u) tmem_ld_32x32b_x16(t_row + buf * kPairN + (c + u) * 16, r[u]);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < kAtOnce; ++u)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            float2 f0 = ss, f1 = ss;
-                            if (B_ROWS) {
-                                const float4 b = sbv[(c + u) * 4 + j];
-                                f0 = __fmul2_rn(ss, make_float2(b.x, b.y));
-                                f1 = __fmul2_rn(ss, make_float2(b.z, b.w));
-                            }
-                            float2 &lo = acc[(c + u) * 8 + 2 * j], &hi = acc[(c + u) * 8 + 2 * j + 1];
-                            lo = __ffma2_rn(f0, make_float2(__uint_as_float(r[u][4 * j]), __uint_as_float(r[u][4 * j + 1])), lo);
-                            hi = __ffma2_rn(f1, make_float2(__uint_as_float(r[u][4 * j + 2]), __uint_as_float(r[u][4 * j + 3])), hi);
-                        }
-                }
+                tmem_wait_ld();
+                add_scaled<B_ROWS, 0>(acc, r0, s, sbv);
+                tmem_ld_32x32b_x16(from + 32, r0);
+                add_scaled<B_ROWS, 16>(acc, r1, s, sbv);
+                tmem_ld_32x32b_x16(from + 48, r1);
+                tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(release[buf]);
+                add_scaled<B_ROWS, 32>(acc, r0, s, sbv);
+                add_scaled<B_ROWS, 48>(acc, r1, s, sbv);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             if (!ok || row >= p.M) continue;
