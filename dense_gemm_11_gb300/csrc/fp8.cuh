@@ -15,6 +15,31 @@ __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity
     return mbar_wait(bar, parity, limit_ns);
 }
 
+// Two FP32 values in one 64-bit register, and acc = a * b + acc, a * b on both
+// (PTX f32x2; one rounding each, as fmaf).  Held as 64-bit values so that the
+// pairs stay in place.
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+    return v;
+}
+__device__ __forceinline__ uint64_t pack_b32x2(uint32_t lo, uint32_t hi) {
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma_f32x2(uint64_t &acc, uint64_t a, uint64_t b) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+    uint64_t v;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+    return v;
+}
+
 // True in one lane of a warp that runs together.  A warp whose loop is uniform
 // and only guards its tcgen05 and TMA instructions with this keeps their
 // operands (descriptors, addresses) in uniform registers; a loop inside a

@@ -345,14 +345,18 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
 // Bound: what the TMA unit brings in.  It delivers 43.6 bytes a clock to an SM,
 // so a k block takes 750 clocks to stage and 512 to multiply; a 256 x 256 tile
 // is the most that the accumulators leave room for.
-constexpr int kPairStages = 4;
-constexpr int kPairEpi = 16;
+constexpr int kPairStages = 5;
+constexpr int kPairEpi = 8;
 constexpr int kPairN = 256;
 constexpr int kPairCols = kPairN * 4 / kPairEpi;  // of an epilogue warp
+// Registers: the launch gives each of the 384 threads 168, 64,512 in all; the
+// first warpgroup (TMA, MMA) keeps 56 and the epilogue takes 224 each:
+// 128 * 56 + 256 * 224 = 64,512.
+constexpr int kPairRegsFew = 56, kPairRegsMany = 224;
 
 template <bool B_ROWS>
 struct Fp8PairCfg {
-    static constexpr int kThreads = 64 + 32 * kPairEpi;
+    static constexpr int kThreads = 128 + 32 * kPairEpi;
     static constexpr int kHalfBytes = 128 * kScaleBlock;  // this CTA's rows of A, and columns of op(B)
     static constexpr int kStageBytes = 2 * kHalfBytes;
     static constexpr int kSlots = kPairStages + 3;  // as in Fp8Cfg, and one for reads after a block's release
@@ -457,21 +461,20 @@ __device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], 
         if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
 }
 
-// acc[COL ..] += s * (B's scale of the column, with B_ROWS) * r, 16 columns.
-template <bool B_ROWS, int COL>
-__device__ __forceinline__ void add_scaled(float2 (&acc)[kPairCols / 2], const uint32_t (&r)[16], float s, const float4 *sb) {
-    const float2 ss = make_float2(s, s);
+// acc[col ..] += s * (B's scale of the column, with B_ROWS) * r, 16 columns.
+template <bool B_ROWS>
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[16], uint64_t ss, uint32_t sb) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        float2 f0 = ss, f1 = ss;
+        uint64_t f0 = ss, f1 = ss;
         if (B_ROWS) {
-            const float4 b = sb[COL / 4 + j];
-            f0 = __fmul2_rn(ss, make_float2(b.x, b.y));
-            f1 = __fmul2_rn(ss, make_float2(b.z, b.w));
+            uint64_t b0, b1;  // volatile: read here, not all at once ahead of the sums
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(b0), "=l"(b1) : "r"(sb + (col + 4 * j) * 4));
+            f0 = mul_f32x2(ss, b0);
+            f1 = mul_f32x2(ss, b1);
         }
-        float2 &lo = acc[COL / 2 + 2 * j], &hi = acc[COL / 2 + 2 * j + 1];
-        lo = __ffma2_rn(f0, make_float2(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), lo);
-        hi = __ffma2_rn(f1, make_float2(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])), hi);
+        fma_f32x2(acc[col / 2 + 2 * j], f0, pack_b32x2(r[4 * j], r[4 * j + 1]));
+        fma_f32x2(acc[col / 2 + 2 * j + 1], f1, pack_b32x2(r[4 * j + 2], r[4 * j + 3]));
     }
 }
 
@@ -526,8 +529,9 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
     uint32_t armed = 0, armed_parity = 0;
-
-    if (warp == 0) {
+    if (warp < 4) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPairRegsFew));
+      if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
         const uint32_t tx = Cfg::kStageBytes + 512 + (B_ROWS ? kPairN * 4 : 0);
         int stage = 0, slot = 0;
@@ -570,7 +574,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if (++slot == Cfg::kSlots) slot = 0;
             }
         }
-    } else if (warp == 1 && leader) {
+      } else if (warp == 1 && leader) {
         // ------------------------------------------------ MMA issuer (even CTA)
         const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), 16, 1024);
         const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), 16, 1024);
@@ -601,21 +605,23 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if (++stage == kPairStages) stage = 0, phase ^= 1u;
             }
         }
-    } else if (warp >= 2) {
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPairRegsMany));
         // ------------------------------------------------ epilogue (both CTAs)
-        const int q = warp & 3, part = (warp - 2) >> 2;
+        const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kPairCols;
         const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
-        uint8_t *const staged = sC + (warp - 2) * 4096;
+        uint8_t *const staged = sC + (warp - 4) * 4096;
         int i = 0, slot = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
             int m0, n0;
             fp8_pair_origin(pp, t, m0, n0);
             const int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * kPairCols;
-            float2 acc[kPairCols / 2];
+            uint64_t acc[kPairCols / 2];  // pairs of columns
 #pragma unroll
-            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = make_float2(0.f, 0.f);
+            for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
             // B's scale of this warp's columns, one k block ahead
             const float *sb = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
             float s_next = B_ROWS ? 1.f : __ldg(sb);
@@ -637,18 +643,25 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 tmem_ld_32x32b_x16(from + 16, r1);
                 const float *sc = sS + slot * Cfg::kSlotFloats;
                 s *= sc[q * 32 + lane];
-                const float4 *sbv = reinterpret_cast<const float4 *>(sc + 128 + part * kPairCols);
+                const uint64_t ss = pack_f32x2(s, s);
+                const uint32_t sbv = smem_u32(sc + 128 + part * kPairCols);
                 tmem_wait_ld();
-                add_scaled<B_ROWS, 0>(acc, r0, s, sbv);
-                tmem_ld_32x32b_x16(from + 32, r0);
-                add_scaled<B_ROWS, 16>(acc, r1, s, sbv);
-                tmem_ld_32x32b_x16(from + 48, r1);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(release[buf]);
-                add_scaled<B_ROWS, 32>(acc, r0, s, sbv);
-                add_scaled<B_ROWS, 48>(acc, r1, s, sbv);
+#pragma unroll
+                for (int c = 0; c < kPairCols; c += 32) {
+                    const bool more = c + 32 < kPairCols;
+                    if (!more) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(release[buf]);
+                    }
+                    add_scaled<B_ROWS>(acc, c, r0, ss, sbv);
+                    if (more) tmem_ld_32x32b_x16(from + c + 32, r0);
+                    add_scaled<B_ROWS>(acc, c + 16, r1, ss, sbv);
+                    if (more) {
+                        tmem_ld_32x32b_x16(from + c + 48, r1);
+                        tmem_wait_ld();
+                    }
+                }
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             if (!ok || row >= p.M) continue;
@@ -659,7 +672,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 const int n = col + gr * 32;
                 float v[32];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[2 * j] = acc[gr * 16 + j].x, v[2 * j + 1] = acc[gr * 16 + j].y;
+                for (int j = 0; j < 16; ++j) unpack_f32x2(acc[gr * 16 + j], v[2 * j], v[2 * j + 1]);
                 epilogue32(p, v, m, n, lane);
                 if (pp.c_tma)
                     stage32(p, v, &tm_c, staged, lane, row, n, gr & 1);
