@@ -6,13 +6,33 @@
 
 namespace gemm11 {
 
-// mbar_wait that reads the clock only once a wait has lasted: the try itself
-// suspends for a while, so that most waits end within the first few.
+// mbar_wait whose tries may suspend the warp for up to a millisecond (the
+// barrier wakes it), and which reads the clock only where the first tries
+// fail.  A warp that polls takes issue slots from the others of its scheduler:
+// beside the MMA warp's polling two of the product's eight epilogue warps ran
+// 400 cycles a block late.
+__device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar_addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar_addr), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity, unsigned long long limit_ns = kWaitLimitNs) {
     const uint32_t a = smem_u32(bar);
-    for (int i = 0; i < 16; ++i)
-        if (mbar_try_wait(a, parity)) return true;
-    return mbar_wait(bar, parity, limit_ns);
+    for (int i = 0; i < 4; ++i)
+        if (mbar_try_wait_long(a, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_try_wait_long(a, parity)) return true;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
 }
 
 // Two FP32 values in one 64-bit register, and acc = a * b + acc, a * b on both

@@ -461,11 +461,11 @@ __device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], 
         if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
 }
 
-// acc[col ..] += s * (B's scale of the column, with B_ROWS) * r, 16 columns.
+// acc[col ..] += s * (B's scale of the column, with B_ROWS) * r, 32 columns.
 template <bool B_ROWS>
-__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[16], uint64_t ss, uint32_t sb) {
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss, uint32_t sb) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 8; ++j) {
         uint64_t f0 = ss, f1 = ss;
         if (B_ROWS) {
             uint64_t b0, b1;  // volatile: read here, not all at once ahead of the sums
@@ -585,8 +585,8 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) &&
-                                                 mbar_wait_patient(&full[stage], phase, p.wait_ns));
+                ok = __all_sync(0xffffffffu, mbar_wait_patient(&full[stage], phase, p.wait_ns) &&
+                                                 mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns));
                 if (!ok) {
                     fp8_timeout(abort_flag, p.err);
                     break;
@@ -622,46 +622,44 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             uint64_t acc[kPairCols / 2];  // pairs of columns
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
-            // B's scale of this warp's columns, one k block ahead
+            // B's scales of this warp's columns: lane l has those of k blocks
+            // l, l + 32, .., and the next 32 are on their way.
             const float *sb = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
-            float s_next = B_ROWS ? 1.f : __ldg(sb);
+            float s_lane = !B_ROWS && lane < p.kb_total ? __ldg(sb + lane * p.sb_kb) : 1.f, s_next = 1.f;
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
-                float s = s_next;
-                if (!B_ROWS && kb + 1 < p.kb_total) s_next = __ldg(sb + (kb + 1) * p.sb_kb);
+                if (!B_ROWS && (kb & 31) == 0) {
+                    if (kb > 0) s_lane = s_next;
+                    if (kb + 32 + lane < p.kb_total) s_next = __ldg(sb + (kb + 32 + lane) * p.sb_kb);
+                }
+                float s = B_ROWS ? 1.f : __shfl_sync(0xffffffffu, s_lane, kb & 31);
                 if (!mbar_wait_patient(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
                     fp8_timeout(abort_flag, p.err);
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                // Two reads of 16 columns in flight; the accumulator goes back
+                // Two reads of 32 columns in flight; the accumulator goes back
                 // as soon as the last read is in, before its sums are added.
                 const uint32_t from = t_row + buf * kPairN;
-                uint32_t r0[16], r1[16];
-                tmem_ld_32x32b_x16(from, r0);
-                tmem_ld_32x32b_x16(from + 16, r1);
+                uint32_t r0[32], r1[32];
+                tmem_ld_32x32b_x32(from, r0);
+                tmem_ld_32x32b_x32(from + 32, r1);
                 const float *sc = sS + slot * Cfg::kSlotFloats;
                 s *= sc[q * 32 + lane];
                 const uint64_t ss = pack_f32x2(s, s);
                 const uint32_t sbv = smem_u32(sc + 128 + part * kPairCols);
                 tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < kPairCols; c += 32) {
-                    const bool more = c + 32 < kPairCols;
-                    if (!more) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(release[buf]);
-                    }
-                    add_scaled<B_ROWS>(acc, c, r0, ss, sbv);
-                    if (more) tmem_ld_32x32b_x16(from + c + 32, r0);
-                    add_scaled<B_ROWS>(acc, c + 16, r1, ss, sbv);
-                    if (more) {
-                        tmem_ld_32x32b_x16(from + c + 48, r1);
-                        tmem_wait_ld();
-                    }
-                }
+                add_scaled<B_ROWS>(acc, 0, r0, ss, sbv);
+                tmem_ld_32x32b_x32(from + 64, r0);
+                add_scaled<B_ROWS>(acc, 32, r1, ss, sbv);
+                tmem_ld_32x32b_x32(from + 96, r1);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(release[buf]);
+                add_scaled<B_ROWS>(acc, 64, r0, ss, sbv);
+                add_scaled<B_ROWS>(acc, 96, r1, ss, sbv);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             if (!ok || row >= p.M) continue;
