@@ -24,8 +24,22 @@ __device__ __forceinline__ bool mbar_try_wait_long(uint32_t bar_addr, uint32_t p
         : "memory");
     return ok != 0;
 }
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar_addr, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n"
+        " .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(ok)
+        : "r"(bar_addr), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity, unsigned long long limit_ns = kWaitLimitNs) {
     const uint32_t a = smem_u32(bar);
+    if (mbar_test_wait(a, parity)) return true;
     for (int i = 0; i < 4; ++i)
         if (mbar_try_wait_long(a, parity)) return true;
     const unsigned long long t0 = globaltimer_ns();

@@ -338,17 +338,24 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
 // [m0 + 128 r, + 128) of A and columns [n0 + 128 r, + 128) of op(B), 32 KB for a
 // k block; the even CTA's MMA thread multiplies the pair, and each CTA's own
 // tensor memory receives the block's sums of its 128 rows x 256 columns, twice
-// buffered (all 512 columns).  Sixteen epilogue warps hold the running sums, 64
-// a thread: warp w has lane quarter w % 4 and 64 columns, in one scale block of
-// B.  Eight warps with 128 columns each could not hide the latency of their
-// tensor-memory reads (340 us against ??? at 4096 x 11008 x 4096).
-// Bound: what the TMA unit brings in.  It delivers 43.6 bytes a clock to an SM,
-// so a k block takes 750 clocks to stage and 512 to multiply; a 256 x 256 tile
-// is the most that the accumulators leave room for.
+// buffered (all 512 columns).  Eight epilogue warps hold the running sums, 128
+// a thread: warp w has lane quarter w % 4 and one half of the columns.
+//
+// A block's columns are two MMA groups, each handed over by barriers of its
+// own: group h multiplies columns [64 h, + 64) of both CTAs' parts of op(B), so
+// its columns of C are n0 + 64 h + j and n0 + 128 + 64 h + j, j < 64.  From the
+// last MMA of a group to the first of the same group two blocks later pass the
+// commit (290 clocks), the epilogue's reads (300 - 400) and its answer (360);
+// two groups in turn keep the tensor core busy meanwhile.
+//
+// Bound: what the TMA unit brings in and the tensor core reads from shared
+// memory.  TMA delivers 43.6 bytes a clock to an SM, 750 clocks for a block; the
+// groups read 64 KB and TMA writes 32 KB, 750 clocks at 128 bytes each; the
+// multiplication itself takes 512 and the scaling 300.
 constexpr int kPairStages = 5;
 constexpr int kPairEpi = 8;
 constexpr int kPairN = 256;
-constexpr int kPairCols = kPairN * 4 / kPairEpi;  // of an epilogue warp
+constexpr int kPairCols = kPairN * 4 / kPairEpi;  // of an epilogue warp, and of an MMA group
 // Registers: the launch gives each of the 384 threads 168, 64,512 in all; the
 // first warpgroup (TMA, MMA) keeps 56 and the epilogue takes 224 each:
 // 128 * 56 + 256 * 224 = 64,512.
@@ -363,7 +370,7 @@ struct Fp8PairCfg {
     static constexpr int kSlotFloats = 128 + (B_ROWS ? kPairN : 0);
     static constexpr int kCStage = kPairEpi * 4096;  // staging of C, 4 KB a warp
     static constexpr int kSmemBytes =
-        1024 + kPairStages * kStageBytes + kCStage + kSlots * kSlotFloats * 4 + (2 * kPairStages + 5) * 8 + 16;
+        1024 + kPairStages * kStageBytes + kCStage + kSlots * kSlotFloats * 4 + (2 * kPairStages + 9) * 8 + 16;
 };
 
 struct Fp8PairArgs {
@@ -461,7 +468,8 @@ __device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], 
         if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
 }
 
-// acc[col ..] += s * (B's scale of the column, with B_ROWS) * r, 32 columns.
+// acc[col ..] += s * (B's scale of the column, with B_ROWS: at sb on) * r, 32
+// columns.
 template <bool B_ROWS>
 __device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss, uint32_t sb) {
 #pragma unroll
@@ -469,7 +477,7 @@ __device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int c
         uint64_t f0 = ss, f1 = ss;
         if (B_ROWS) {
             uint64_t b0, b1;  // volatile: read here, not all at once ahead of the sums
-            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(b0), "=l"(b1) : "r"(sb + (col + 4 * j) * 4));
+            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(b0), "=l"(b1) : "r"(sb + 16 * j));
             f0 = mul_f32x2(ss, b0);
             f1 = mul_f32x2(ss, b1);
         }
@@ -492,8 +500,8 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(sS + Cfg::kSlots * Cfg::kSlotFloats);
     uint64_t *empty = full + kPairStages;
     uint64_t *tfull = empty + kPairStages;
-    uint64_t *tempty = tfull + 2;
-    uint64_t *mma_done = tempty + 2;
+    uint64_t *tempty = tfull + 4;  // [buffer][group], as tfull
+    uint64_t *mma_done = tempty + 4;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
@@ -504,13 +512,13 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);  // both MMA warps
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 2 * kPairEpi);
+            mbar_init(&tempty[b], kPairEpi);  // half the warps of both CTAs
         }
-        mbar_init(mma_done, 1);
+        mbar_init(mma_done, 2);
         *abort_flag = 0;
         fence_mbarrier_init();
         tma_prefetch_desc(&tm_a);
@@ -574,11 +582,17 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if (++slot == Cfg::kSlots) slot = 0;
             }
         }
-      } else if (warp == 1 && leader) {
-        // ------------------------------------------------ MMA issuer (even CTA)
-        const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), 16, 1024);
-        const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), 16, 1024);
+      } else if (warp < 3 && leader) {
+        // ------------------------------------------------ MMA issuers (even CTA), one for each group
+        // A warp's waits and instructions for a group take 500 - 600 clocks a
+        // block beside the epilogue's arithmetic, so one warp for both groups
+        // would set the pace (920 clocks a block).
+        const int h = warp - 1;
         const uint32_t b_step = p.p_mn ? 4096u >> 4 : 32u >> 4;
+        const uint32_t b_group = h * (p.p_mn ? 64 : 64 * 128);  // bytes to the group's columns
+        const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), 16, 1024);
+        const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB) + b_group, 16, 1024);
+        const uint32_t d0 = tmem_base + h * kPairCols;
         int stage = 0, i = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -586,7 +600,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_patient(&full[stage], phase, p.wait_ns) &&
-                                                 mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns));
+                                                 mbar_wait_patient(&tempty[buf * 2 + h], ((i >> 1) & 1) ^ 1u, p.wait_ns));
                 if (!ok) {
                     fp8_timeout(abort_flag, p.err);
                     break;
@@ -597,9 +611,9 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < kScaleBlock / 32; ++kk)
-                        umma_f8_pair(tmem_base + buf * kPairN, ad + 2u * kk, bd + b_step * kk, p.idesc, kk > 0 ? 1u : 0u);
+                        umma_f8_pair(d0 + buf * kPairN, ad + 2u * kk, bd + b_step * kk, p.idesc, kk > 0 ? 1u : 0u);
+                    umma_commit_pair_mc(&tfull[buf * 2 + h], 0x3);
                     umma_commit_pair_mc(&empty[stage], 0x3);
-                    umma_commit_pair_mc(&tfull[buf], 0x3);
                 }
                 __syncwarp();
                 if (++stage == kPairStages) stage = 0, phase ^= 1u;
@@ -611,29 +625,36 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         // ------------------------------------------------ epilogue (both CTAs)
         const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * kPairCols;
-        const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+        const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[part]), 0), mapa_shared(smem_u32(&tempty[2 + part]), 0)};
         uint8_t *const staged = sC + (warp - 4) * 4096;
         int i = 0, slot = 0;
         bool ok = true;
         for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
             int m0, n0;
             fp8_pair_origin(pp, t, m0, n0);
-            const int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * kPairCols;
+            // Columns col + j and col + 128 + j, j < 64.
+            const int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * 64;
             uint64_t acc[kPairCols / 2];  // pairs of columns
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
-            // B's scales of this warp's columns: lane l has those of k blocks
-            // l, l + 32, .., and the next 32 are on their way.
-            const float *sb = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
-            float s_lane = !B_ROWS && lane < p.kb_total ? __ldg(sb + lane * p.sb_kb) : 1.f, s_next = 1.f;
+            // B's scales of the two 128-column blocks: lane l has those of k
+            // blocks l, l + 32, .., and the next 32 are on their way.
+            const float *sb0 = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
+            const float *sb1 = p.SB + (B_ROWS ? 0 : min(col + 128, p.N - 1) / kScaleBlock * p.sb_n);
+            float lane0 = 1.f, lane1 = 1.f, next0 = 1.f, next1 = 1.f;
+            if (!B_ROWS && lane < p.kb_total) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
             for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
                 const int buf = i & 1;
-                if (!B_ROWS && (kb & 31) == 0) {
-                    if (kb > 0) s_lane = s_next;
-                    if (kb + 32 + lane < p.kb_total) s_next = __ldg(sb + (kb + 32 + lane) * p.sb_kb);
+                float s0 = 1.f, s1 = 1.f;
+                if (!B_ROWS) {
+                    if ((kb & 31) == 0) {
+                        lane0 = next0, lane1 = next1;
+                        if (kb + 32 + lane < p.kb_total)
+                            next0 = __ldg(sb0 + (kb + 32 + lane) * p.sb_kb), next1 = __ldg(sb1 + (kb + 32 + lane) * p.sb_kb);
+                    }
+                    s0 = __shfl_sync(0xffffffffu, lane0, kb & 31), s1 = __shfl_sync(0xffffffffu, lane1, kb & 31);
                 }
-                float s = B_ROWS ? 1.f : __shfl_sync(0xffffffffu, s_lane, kb & 31);
-                if (!mbar_wait_patient(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
+                if (!mbar_wait_patient(&tfull[buf * 2 + part], (i >> 1) & 1, p.wait_ns)) {
                     fp8_timeout(abort_flag, p.err);
                     ok = false;
                     break;
@@ -646,20 +667,20 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 tmem_ld_32x32b_x32(from, r0);
                 tmem_ld_32x32b_x32(from + 32, r1);
                 const float *sc = sS + slot * Cfg::kSlotFloats;
-                s *= sc[q * 32 + lane];
-                const uint64_t ss = pack_f32x2(s, s);
-                const uint32_t sbv = smem_u32(sc + 128 + part * kPairCols);
+                s0 *= sc[q * 32 + lane], s1 *= sc[q * 32 + lane];
+                const uint64_t ss0 = pack_f32x2(s0, s0), ss1 = pack_f32x2(s1, s1);
+                const uint32_t sbv = smem_u32(sc + 128 + part * 64);
                 tmem_wait_ld();
-                add_scaled<B_ROWS>(acc, 0, r0, ss, sbv);
+                add_scaled<B_ROWS>(acc, 0, r0, ss0, sbv);
                 tmem_ld_32x32b_x32(from + 64, r0);
-                add_scaled<B_ROWS>(acc, 32, r1, ss, sbv);
+                add_scaled<B_ROWS>(acc, 32, r1, ss0, sbv + 32 * 4);
                 tmem_ld_32x32b_x32(from + 96, r1);
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(release[buf]);
-                add_scaled<B_ROWS>(acc, 64, r0, ss, sbv);
-                add_scaled<B_ROWS>(acc, 96, r1, ss, sbv);
+                add_scaled<B_ROWS>(acc, 64, r0, ss1, sbv + 128 * 4);
+                add_scaled<B_ROWS>(acc, 96, r1, ss1, sbv + 160 * 4);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             if (!ok || row >= p.M) continue;
@@ -667,7 +688,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             const int m = row + lane;
 #pragma unroll
             for (int gr = 0; gr < kPairCols / 32; ++gr) {
-                const int n = col + gr * 32;
+                const int n = col + (gr & 1) * 32 + (gr >> 1) * 128;
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) unpack_f32x2(acc[gr * 16 + j], v[2 * j], v[2 * j + 1]);
@@ -688,8 +709,10 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         for (int s = 0; s < kPairStages; ++s)
             if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u)) fp8_timeout(abort_flag, p.err);
     }
-    if (warp == 1 && lane == 0 && leader) {
-        umma_commit_pair_mc(mma_done, 0x1);
+    if ((warp == 1 || warp == 2) && leader) {
+        // the electing lane issued the MMAs that the commit waits for
+        if (elect_one()) umma_commit_pair_mc(mma_done, 0x1);
+        __syncwarp();
         if (!mbar_wait(mma_done, 0)) fp8_timeout(abort_flag, p.err);
     }
     tc_fence_before();
@@ -804,7 +827,7 @@ cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, cudaStream_t str
     const int cb = g.c_type == kOutF32 ? 4 : 2;
     // TMA stores of C need aligned rows; any other C is stored element by element.
     args.c_tma = reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && g.ldc * cb % 16 == 0;
-    args.a.idesc = umma_idesc_f8(256, kPairN, g.a_type == kTypeE5M2, g.b_type == kTypeE5M2, 0, a.p_mn);
+    args.a.idesc = umma_idesc_f8(256, kPairCols, g.a_type == kTypeE5M2, g.b_type == kTypeE5M2, 0, a.p_mn);
     CUtensorMap ta, tb, tsa, tsb, tc;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, none = CU_TENSOR_MAP_SWIZZLE_NONE;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8, f32 = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
