@@ -473,16 +473,18 @@ __device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], 
 template <bool B_ROWS>
 __device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss, uint32_t sb) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint64_t f0 = ss, f1 = ss;
-        if (B_ROWS) {
-            uint64_t b0, b1;  // volatile: read here, not all at once ahead of the sums
-            asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(b0), "=l"(b1) : "r"(sb + 16 * j));
-            f0 = mul_f32x2(ss, b0);
-            f1 = mul_f32x2(ss, b1);
+    for (int j = 0; j < 8; j += 4) {
+        uint64_t f[8];
+        if (B_ROWS) {  // volatile: 16 columns' scales at a time, not all ahead of the sums
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(sb + 16 * (j + u)));
         }
-        fma_f32x2(acc[col / 2 + 2 * j], f0, pack_b32x2(r[4 * j], r[4 * j + 1]));
-        fma_f32x2(acc[col / 2 + 2 * j + 1], f1, pack_b32x2(r[4 * j + 2], r[4 * j + 3]));
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            f[u] = B_ROWS ? mul_f32x2(ss, f[u]) : ss;
+            fma_f32x2(acc[col / 2 + 2 * j + u], f[u], pack_b32x2(r[4 * j + 2 * u], r[4 * j + 2 * u + 1]));
+        }
     }
 }
 
@@ -643,8 +645,20 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             const float *sb1 = p.SB + (B_ROWS ? 0 : min(col + 128, p.N - 1) / kScaleBlock * p.sb_n);
             float lane0 = 1.f, lane1 = 1.f, next0 = 1.f, next1 = 1.f;
             if (!B_ROWS && lane < p.kb_total) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
-            for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
-                const int buf = i & 1;
+            // Two reads of 32 columns in flight: while 32 columns' sums are
+            // added the next are read, over the end of a block too.  The
+            // accumulator goes back as soon as the block's last read is in.
+            uint32_t r0[32], r1[32];
+            auto take = [&] {  // the next block's accumulator
+                ok = mbar_wait_patient(&tfull[(i & 1) * 2 + part], (i >> 1) & 1, p.wait_ns);
+                if (!ok) fp8_timeout(abort_flag, p.err);
+                tc_fence_after();
+            };
+            take();
+            tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN, r0);
+            tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN + 32, r1);
+            for (int kb = 0; kb < p.kb_total; ++kb) {
+                const uint32_t from = t_row + (i & 1) * kPairN, answer = release[i & 1];
                 float s0 = 1.f, s1 = 1.f;
                 if (!B_ROWS) {
                     if ((kb & 31) == 0) {
@@ -654,18 +668,6 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                     }
                     s0 = __shfl_sync(0xffffffffu, lane0, kb & 31), s1 = __shfl_sync(0xffffffffu, lane1, kb & 31);
                 }
-                if (!mbar_wait_patient(&tfull[buf * 2 + part], (i >> 1) & 1, p.wait_ns)) {
-                    fp8_timeout(abort_flag, p.err);
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                // Two reads of 32 columns in flight; the accumulator goes back
-                // as soon as the last read is in, before its sums are added.
-                const uint32_t from = t_row + buf * kPairN;
-                uint32_t r0[32], r1[32];
-                tmem_ld_32x32b_x32(from, r0);
-                tmem_ld_32x32b_x32(from + 32, r1);
                 const float *sc = sS + slot * Cfg::kSlotFloats;
                 s0 *= sc[q * 32 + lane], s1 *= sc[q * 32 + lane];
                 const uint64_t ss0 = pack_f32x2(s0, s0), ss1 = pack_f32x2(s1, s1);
@@ -678,11 +680,20 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote(release[buf]);
+                if (lane == 0) mbar_arrive_remote(answer);
+                ++i;
                 add_scaled<B_ROWS>(acc, 64, r0, ss1, sbv + 128 * 4);
+                const bool more = kb + 1 < p.kb_total;
+                if (more) {
+                    take();
+                    if (!ok) break;
+                    tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN, r0);
+                }
                 add_scaled<B_ROWS>(acc, 96, r1, ss1, sbv + 160 * 4);
+                if (more) tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN + 32, r1);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
+            tmem_wait_ld();
             if (!ok || row >= p.M) continue;
             // The tile is done: 32 columns at a time to the epilogue and out.
             const int m = row + lane;
