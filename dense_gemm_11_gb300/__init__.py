@@ -412,31 +412,47 @@ def gemm_tc_batched(A, B, C, alpha: float = 1.0, beta: float = 0.0, bias=None, a
 
 
 _FP8_LAYOUTS = {"rows": GEMM_FP8_ROWS, "cols": GEMM_FP8_COLS, "blocks": GEMM_FP8_BLOCKS}
-_types_cache = None
-
-
-def _type_codes():
-    """torch dtype -> gemm_dtype code."""
-    global _types_cache
-    if _types_cache is None:
-        import torch
-        _types_cache = {torch.float32: GEMM_DTYPE_F32, torch.float16: GEMM_DTYPE_F16, torch.bfloat16: GEMM_DTYPE_BF16,
-                        torch.float8_e4m3fn: GEMM_DTYPE_E4M3, torch.float8_e5m2: GEMM_DTYPE_E5M2}
-    return _types_cache
-
-
-def _typed_mat(t, name, codes):
-    """(pointer, row stride, type code) of a 2-D CUDA tensor of one of the types `codes`."""
-    code = _type_codes().get(getattr(t, "dtype", None), -1)
-    if code not in codes:
-        raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in codes)}")
-    ptr, ld = _mat(t, name, t.dtype)
-    return ptr, ld, code
-
-
 _TYPE_NAMES = ("float32", "float16", "bfloat16", "float8_e4m3fn", "float8_e5m2")
+_F32 = (GEMM_DTYPE_F32,)
+_HALFS = (GEMM_DTYPE_F16, GEMM_DTYPE_BF16)
 _FLOATS = (GEMM_DTYPE_F32, GEMM_DTYPE_F16, GEMM_DTYPE_BF16)
 _FP8S = (GEMM_DTYPE_E4M3, GEMM_DTYPE_E5M2)
+_codes = {}  # torch dtype -> gemm_dtype code
+_raw_stream = None
+
+
+def _load_codes():
+    """Fill the type table and look up how to get the current stream; torch is imported on first use."""
+    global _raw_stream
+    import torch
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _codes.update({getattr(torch, name): code for code, name in enumerate(_TYPE_NAMES)})
+
+
+def _typed_mat(t, name, allowed):
+    """(pointer, row stride, rows, cols, type code) of a 2-D CUDA tensor with unit
+    column stride and one of the types `allowed`.  The calls below are short on
+    the GPU: the checks take one pass over the tensor's properties."""
+    if not _codes:
+        _load_codes()
+    code = _codes.get(getattr(t, "dtype", None), -1)
+    if code not in allowed or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in allowed)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    ld, step = stride
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} needs unit column stride")
+    if ld < cols and rows <= 1:  # a single row has no row stride of its own
+        ld = cols
+    return t.data_ptr(), ld or 1, rows, cols, code
+
+
+def _stream_ptr(stream, t):
+    """The raw handle of `stream`, or of the current stream of t's device."""
+    return stream.cuda_stream if stream is not None else _raw_stream(t.get_device())
 
 
 def _fp8_shapes(rows, cols, layout):
@@ -469,15 +485,13 @@ def fp8_quantize(X, Q, S, layout: str = "rows", *, stream=None) -> None:
     layout "blocks": blocks of 128 x 128; Q is rows x cols, S is (ceil(rows/128), ceil(cols/128)).
     Q is float8_e4m3fn or float8_e5m2.  fp8_empty() makes a fitting pair.
     """
-    x_ptr, ldx, x_type = _typed_mat(X, "X", _FLOATS)
-    q_ptr, ldq, q_type = _typed_mat(Q, "Q", _FP8S)
-    s_ptr, lds, _ = _typed_mat(S, "S", (GEMM_DTYPE_F32,))
-    rows, cols = X.shape
-    q_shape, s_shape = _fp8_shapes(rows, cols, layout)
-    if Q.shape != q_shape or S.shape != s_shape:
+    x_ptr, ldx, rows, cols, x_type = _typed_mat(X, "X", _FLOATS)
+    q_ptr, ldq, q_rows, q_cols, q_type = _typed_mat(Q, "Q", _FP8S)
+    s_ptr, lds, s_rows, s_cols, _ = _typed_mat(S, "S", _F32)
+    if ((q_rows, q_cols), (s_rows, s_cols)) != _fp8_shapes(rows, cols, layout):
         raise ValueError(f"shape mismatch X{tuple(X.shape)} Q{tuple(Q.shape)} S{tuple(S.shape)} for layout {layout!r}")
     st = lib().gemm_fp8_quantize_block128(rows, cols, x_ptr, x_type, ldx, q_ptr, q_type, ldq, s_ptr, lds,
-                                          _FP8_LAYOUTS[layout], _stream_handle(stream))
+                                          _FP8_LAYOUTS[layout], _stream_ptr(stream, X))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_quantize_block128")
 
@@ -492,25 +506,20 @@ def gemm_fp8(A, SA, B, SB, C, alpha: float = 1.0, beta: float = 0.0, bias=None, 
     So y = x W^T takes x in "rows" and W in "blocks"; dx = dy W takes dy in "rows" and the same
     W with b_trans=False; dW = dy^T x takes both quantized with layout "cols" and b_scales="rows".
     """
-    a_ptr, lda, a_type = _typed_mat(A, "A", _FP8S)
-    b_ptr, ldb, b_type = _typed_mat(B, "B", _FP8S)
-    c_ptr, ldc, c_type = _typed_mat(C, "C", _FLOATS)
-    sa_ptr, ldsa, _ = _typed_mat(SA, "SA", (GEMM_DTYPE_F32,))
-    sb_ptr, ldsb, _ = _typed_mat(SB, "SB", (GEMM_DTYPE_F32,))
-    M, K = A.shape
-    N, K2 = B.shape if b_trans else B.shape[::-1]
-    if K2 != K or C.shape != (M, N):
+    a_ptr, lda, M, K, a_type = _typed_mat(A, "A", _FP8S)
+    b_ptr, ldb, b_rows, b_cols, b_type = _typed_mat(B, "B", _FP8S)
+    c_ptr, ldc, c_rows, N, c_type = _typed_mat(C, "C", _FLOATS)
+    sa_ptr, ldsa, sa_rows, sa_cols, _ = _typed_mat(SA, "SA", _F32)
+    sb_ptr, ldsb, sb_rows, sb_cols, _ = _typed_mat(SB, "SB", _F32)
+    if c_rows != M or (b_rows, b_cols) != ((N, K) if b_trans else (K, N)):
         raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
     if b_scales != "blocks" and (b_scales != "rows" or not b_trans):
         raise ValueError(f"b_scales must be 'blocks', or 'rows' with b_trans=True, got {b_scales!r}")
-    if SA.shape != _fp8_shapes(M, K, "rows")[1] or SB.shape != _fp8_shapes(*B.shape, b_scales)[1]:
+    if sa_rows != -(-K // 128) or sa_cols != M or (sb_rows, sb_cols) != _fp8_shapes(b_rows, b_cols, b_scales)[1]:
         raise ValueError(f"scales do not fit: SA{tuple(SA.shape)} SB{tuple(SB.shape)} for A{tuple(A.shape)} B{tuple(B.shape)}")
-    bias_ptr = None
-    if bias is not None:
-        bias_ptr = _vector(bias, "bias", N)
     st = lib().gemm_fp8_block128(M, N, K, alpha, a_ptr, a_type, lda, sa_ptr, ldsa, b_ptr, b_type, ldb, sb_ptr, ldsb,
-                                 1 if b_trans else 0, _FP8_LAYOUTS[b_scales], beta, c_ptr, c_type, ldc, bias_ptr, act,
-                                 _stream_handle(stream))
+                                 1 if b_trans else 0, _FP8_LAYOUTS[b_scales], beta, c_ptr, c_type, ldc,
+                                 None if bias is None else _vector(bias, "bias", N), act, _stream_ptr(stream, A))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_block128")
 
@@ -527,54 +536,53 @@ def moe_few_tokens(X, router, gate, up, down, Y, top_k: int, *, scales=None, act
     divided by their sum with renormalize=True.  ids (int32) and weights (fp32), both (T, top_k) and contiguous,
     receive them if given.  Limits: T <= 128, E <= 512, top_k <= 16, T * top_k <= 1024, H and I multiples of 16.
     """
-    import torch
-    codes = _type_codes()
-    x_ptr, ldx, x_type = _typed_mat(X, "X", (GEMM_DTYPE_F16, GEMM_DTYPE_BF16))
-    y_ptr, ldy, y_type = _typed_mat(Y, "Y", _FLOATS)
-    r_ptr, ldr, r_type = _typed_mat(router, "router", _FLOATS)
-    T, H = X.shape
-    E = router.shape[0]
-    w_type = codes.get(getattr(gate, "dtype", None), -1)
-    if w_type != x_type and w_type != GEMM_DTYPE_E4M3:
-        raise TypeError("gate, up and down must have X's type or be float8_e4m3fn")
-    if r_type not in (x_type, GEMM_DTYPE_F32):
+    x_ptr, ldx, T, H, x_type = _typed_mat(X, "X", _HALFS)
+    y_ptr, ldy, y_rows, y_cols, y_type = _typed_mat(Y, "Y", _FLOATS)
+    r_ptr, ldr, E, r_cols, r_type = _typed_mat(router, "router", _FLOATS)
+    if y_rows != T or y_cols != H or r_cols != H or (E > 1 and ldr != H):
+        raise ValueError(f"shape mismatch X{tuple(X.shape)} router{tuple(router.shape)} Y{tuple(Y.shape)} (router contiguous)")
+    if r_type != x_type and r_type != GEMM_DTYPE_F32:
         raise TypeError("router must have X's type or be float32")
     I = gate.shape[1] if gate.dim() == 3 else -1
-    for t, name, shape in ((gate, "gate", (E, I, H)), (up, "up", (E, I, H)), (down, "down", (E, H, I))):
-        if t is None and name == "up":
-            continue
-        if not t.is_cuda or t.dtype != gate.dtype:
-            raise TypeError(f"{name} must be a CUDA {gate.dtype} tensor")
-        if t.shape != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous and {shape}, got {tuple(t.shape)}")
-    if Y.shape != X.shape or router.shape[1] != H or (E > 1 and ldr != H):
-        raise ValueError(f"shape mismatch X{tuple(X.shape)} router{tuple(router.shape)} Y{tuple(Y.shape)} (router contiguous)")
-    s_ptr = [None, None, None]
+    w_type = _codes.get(gate.dtype, -1)
+    if w_type != x_type and w_type != GEMM_DTYPE_E4M3:
+        raise TypeError("gate, up and down must have X's type or be float8_e4m3fn")
+    g_ptr = _expert_tensor(gate, "gate", gate.dtype, E, I, H)
+    u_ptr = None if up is None else _expert_tensor(up, "up", gate.dtype, E, I, H)
+    d_ptr = _expert_tensor(down, "down", gate.dtype, E, H, I)
+    sg_ptr = su_ptr = sd_ptr = None
     if w_type == GEMM_DTYPE_E4M3:
         if scales is None or len(scales) != 3:
             raise ValueError("8-bit weights need scales = (s_gate, s_up, s_down)")
-        hb, ib = (H + 127) // 128, (I + 127) // 128
-        for i, (t, shape) in enumerate(zip(scales, ((E, ib, hb), (E, ib, hb), (E, hb, ib)))):
-            if i == 1 and up is None:
-                continue
-            if not t.is_cuda or t.dtype != torch.float32:
-                raise TypeError("scales must be CUDA float32 tensors")
-            if t.shape != shape or not t.is_contiguous():
-                raise ValueError(f"scales[{i}] must be contiguous and {shape}, got {tuple(t.shape)}")
-            s_ptr[i] = t.data_ptr()
+        import torch
+        hb, ib = -(-H // 128), -(-I // 128)
+        sg_ptr = _expert_tensor(scales[0], "scales[0]", torch.float32, E, ib, hb)
+        su_ptr = None if up is None else _expert_tensor(scales[1], "scales[1]", torch.float32, E, ib, hb)
+        sd_ptr = _expert_tensor(scales[2], "scales[2]", torch.float32, E, hb, ib)
     elif scales is not None:
         raise ValueError("scales are for 8-bit weights only")
-    out = [None, None]
-    for i, (t, name, dt) in enumerate(((ids, "ids", torch.int32), (weights, "weights", torch.float32))):
-        if t is not None:
-            if not t.is_cuda or t.dtype != dt or t.shape != (T, top_k) or not t.is_contiguous():
-                raise TypeError(f"{name} must be a contiguous CUDA {dt} tensor of shape {(T, top_k)}")
-            out[i] = t.data_ptr()
-    st = lib().gemm_moe_few_tokens(T, E, top_k, H, I, x_ptr, x_type, ldx, r_ptr, r_type, gate.data_ptr(),
-                                   None if up is None else up.data_ptr(), down.data_ptr(), w_type, *s_ptr, act,
-                                   1 if renormalize else 0, y_ptr, y_type, ldy, *out, _stream_handle(stream))
+    st = lib().gemm_moe_few_tokens(T, E, top_k, H, I, x_ptr, x_type, ldx, r_ptr, r_type, g_ptr, u_ptr, d_ptr, w_type, sg_ptr,
+                                   su_ptr, sd_ptr, act, 1 if renormalize else 0, y_ptr, y_type, ldy,
+                                   None if ids is None else _choice(ids, "ids", "int32", T, top_k),
+                                   None if weights is None else _choice(weights, "weights", "float32", T, top_k),
+                                   _stream_ptr(stream, X))
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_few_tokens")
+
+
+def _expert_tensor(t, name, dtype, E, rows, cols):
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if t.shape != (E, rows, cols) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {(E, rows, cols)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _choice(t, name, dtype, T, k):
+    import torch
+    if not t.is_cuda or t.dtype != getattr(torch, dtype) or t.shape != (T, k) or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {(T, k)}")
+    return t.data_ptr()
 
 
 def _vector(t, name, n):
