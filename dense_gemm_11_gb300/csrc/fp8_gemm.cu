@@ -64,7 +64,8 @@ constexpr int tmem_cols_fp8(int n) { return n <= 32 ? 32 : n <= 64 ? 64 : n <= 1
 
 template <int BN, int STAGES>
 struct Fp8Cfg {
-    static constexpr int kEpi = BN <= 64 ? 4 : 8;  // epilogue warps
+    static constexpr int kEpi = BN < 64 ? 4 : 8;  // epilogue warps
+    static constexpr int kPerSm = BN <= 64 ? 2 : 1;  // CTAs that an SM holds
     static constexpr int kThreads = 64 + 32 * kEpi;
     static constexpr int kCols = BN / (kEpi / 4);  // accumulator columns of a warp
     static constexpr int kQBytes = BN * kScaleBlock;
@@ -112,7 +113,7 @@ __device__ __forceinline__ void store4(const Fp8Args &p, int m, int n, float (&v
 }
 
 template <int BN, int STAGES>
-__global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
+__global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGES>::kPerSm)
     fp8_tile_kernel(const __grid_constant__ CUtensorMap tm_p, const __grid_constant__ CUtensorMap tm_q,
                     const __grid_constant__ CUtensorMap tm_sq, const Fp8Args p) {
     using Cfg = Fp8Cfg<BN, STAGES>;
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(mma_done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], 1);
@@ -168,36 +169,36 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
     float acc[Cfg::kCols];
     uint32_t armed = 0, armed_parity = 0;
 
-    if (warp == 0 && lane == 0) {
+    if (warp == 0) {
         // ------------------------------------------------ TMA producer
         int stage = 0, slot = 0;
         uint32_t phase = 0;
         for (int kb = kb0; kb < kb1 && !*abort_flag; ++kb) {
-            if (!mbar_wait(&empty[stage], phase ^ 1u, p.wait_ns)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u, p.wait_ns))) {
                 fp8_timeout(abort_flag, p.err);
                 break;
             }
-            mbar_arrive_expect_tx(&full[stage], Cfg::kStageBytes + BN * 4);
             const int k0 = kb * kScaleBlock;
-            if (p.p_mn)
-                tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, n0, k0);
-            else
-                tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, k0, n0);
-            tma_load_2d(&tm_q, &full[stage], sQ + stage * Cfg::kQBytes, k0, m0);
-            tma_load_2d(&tm_sq, &full[stage], sS + slot * Cfg::kSlotFloats, m0, kb);
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[stage], Cfg::kStageBytes + BN * 4);
+                if (p.p_mn)
+                    tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, n0, k0);
+                else
+                    tma_load_2d(&tm_p, &full[stage], sP + stage * kPBytes, k0, n0);
+                tma_load_2d(&tm_q, &full[stage], sQ + stage * Cfg::kQBytes, k0, m0);
+                tma_load_2d(&tm_sq, &full[stage], sS + slot * Cfg::kSlotFloats, m0, kb);
+            }
+            __syncwarp();
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-            if (kDebugBuild && !mbar_wait(&empty[stage], phase, p.wait_ns)) {  // one stage in flight
+            if (kDebugBuild && !__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase, p.wait_ns))) {  // one stage in flight
                 fp8_timeout(abort_flag, p.err);
                 break;
             }
-            if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1u;
-            }
+            if (++stage == STAGES) stage = 0, phase ^= 1u;
             if (++slot == Cfg::kSlots) slot = 0;
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer
         // K-major: 128-byte rows, 8-row groups 1024 bytes apart, 32 k = 32
         // bytes along the row.  MN-major: 128 n bytes for each k, 8-k groups
@@ -209,36 +210,48 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
         uint32_t phase = 0;
         for (int i = 0; i < kb1 - kb0; ++i) {
             const int buf = i & 1;
-            if (!mbar_wait(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns) || !mbar_wait(&full[stage], phase, p.wait_ns)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_patient(&full[stage], phase, p.wait_ns) &&
+                                             mbar_wait_patient(&tempty[buf], ((i >> 1) & 1) ^ 1u, p.wait_ns))) {
                 fp8_timeout(abort_flag, p.err);
                 break;
             }
             tc_fence_after();
             const uint64_t pd = p_desc0 + static_cast<uint64_t>(stage * (kPBytes >> 4));
             const uint64_t qd = q_desc0 + static_cast<uint64_t>(stage * (Cfg::kQBytes >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kScaleBlock / 32; ++kk)
-                umma_f8(tmem_base + buf * BN, pd + p_step * kk, qd + 2u * kk, p.idesc, kk > 0 ? 1u : 0u);
-            umma_commit(&empty[stage]);
-            umma_commit(&tfull[buf]);
-            if (++stage == STAGES) {
-                stage = 0;
-                phase ^= 1u;
+                for (int kk = 0; kk < kScaleBlock / 32; ++kk)
+                    umma_f8(tmem_base + buf * BN, pd + p_step * kk, qd + 2u * kk, p.idesc, kk > 0 ? 1u : 0u);
+                umma_commit(&tfull[buf]);
+                umma_commit(&empty[stage]);
             }
+            __syncwarp();
+            if (++stage == STAGES) stage = 0, phase ^= 1u;
         }
     } else if (warp >= 2) {
         // ------------------------------------------------ epilogue: scale and add
 #pragma unroll
         for (int j = 0; j < Cfg::kCols; ++j) acc[j] = 0.f;
-        const int nn = p.b_rows ? min(n, p.N - 1) : n0 / kScaleBlock;
-        const float *sb = p.SB + nn * p.sb_n;
-        float s_next = kb0 < kb1 ? __ldg(sb + kb0 * p.sb_kb) : 0.f;
+        // B's scale: of this lane's column, one block ahead; or, one for the
+        // whole tile, of 32 blocks at once (lane l has block kb0 + l, + 32, ..).
+        const float *sb = p.SB + (p.b_rows ? min(n, p.N - 1) : n0 / kScaleBlock) * p.sb_n + kb0 * p.sb_kb;
+        const int blocks = kb1 - kb0;
+        float s_next = p.b_rows ? (blocks > 0 ? __ldg(sb) : 0.f) : (lane < blocks ? __ldg(sb + lane * p.sb_kb) : 0.f), s_lane = 0.f;
         int slot = 0;
         for (int kb = kb0; kb < kb1; ++kb) {
             const int i = kb - kb0, buf = i & 1;
-            const float s = s_next;
-            if (kb + 1 < kb1) s_next = __ldg(sb + (kb + 1) * p.sb_kb);
-            if (!mbar_wait(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
+            float s;
+            if (p.b_rows) {
+                s = s_next;
+                if (i + 1 < blocks) s_next = __ldg(sb + (i + 1) * p.sb_kb);
+            } else {
+                if ((i & 31) == 0) {
+                    s_lane = s_next;
+                    if (i + 32 + lane < blocks) s_next = __ldg(sb + (i + 32 + lane) * p.sb_kb);
+                }
+                s = __shfl_sync(0xffffffffu, s_lane, i & 31);
+            }
+            if (!mbar_wait_patient(&tfull[buf], (i >> 1) & 1, p.wait_ns)) {
                 fp8_timeout(abort_flag, p.err);
                 break;
             }
@@ -293,9 +306,10 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, 1)
         for (int s = 0; s < STAGES; ++s)
             if ((armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u)) fp8_timeout(abort_flag, p.err);
     }
-    if (warp == 1 && lane == 0) {
-        umma_commit(mma_done);
-        if (!mbar_wait(mma_done, 0)) fp8_timeout(abort_flag, p.err);
+    if (warp == 1) {
+        if (elect_one()) umma_commit(mma_done);  // by the lane that issued the MMAs
+        __syncwarp();
+        if (!mbar_wait_patient(mma_done, 0)) fp8_timeout(abort_flag, p.err);
     }
     tc_fence_before();
     __syncthreads();
@@ -911,16 +925,17 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) 
     a.tiles_m = (g.M + bn - 1) / bn;
     const long long tiles = static_cast<long long>((g.N + kPR - 1) / kPR) * a.tiles_m;
     const int sms = device_sm_count();
-    if (tiles * 2 <= sms) a.splits = static_cast<int>(std::min<long long>({8, sms / tiles, std::max(1, a.kb_total / 2)}));
+    const int room = sms * (bn <= 64 ? 2 : 1);  // CTAs at a time
+    if (tiles * 2 <= room) a.splits = static_cast<int>(std::min<long long>({8, room / tiles, std::max(1, a.kb_total / 2)}));
     info->launches = 1;
     if (g.M > 128) {
         info->plan = "fp8_pair_256x256";
         return g.b_rows ? launch_fp8_pair<true>(g, a, stream) : launch_fp8_pair<false>(g, a, stream);
     }
     switch (bn) {
-        case 16: info->plan = "fp8_tile_n16"; return launch_fp8_tile<16, 10>(g, a, stream);
-        case 32: info->plan = "fp8_tile_n32"; return launch_fp8_tile<32, 9>(g, a, stream);
-        case 64: info->plan = "fp8_tile_n64"; return launch_fp8_tile<64, 8>(g, a, stream);
+        case 16: info->plan = "fp8_tile_n16"; return launch_fp8_tile<16, 5>(g, a, stream);
+        case 32: info->plan = "fp8_tile_n32"; return launch_fp8_tile<32, 5>(g, a, stream);
+        case 64: info->plan = "fp8_tile_n64"; return launch_fp8_tile<64, 4>(g, a, stream);
         default: info->plan = "fp8_tile_n128"; return launch_fp8_tile<128, 6>(g, a, stream);
     }
 }
