@@ -61,27 +61,46 @@ struct XElem<kOutBF16> {
     using T = __nv_bfloat16;
 };
 
-// Elements [c, c + 8) of a row, zeros from `cols` on.  VEC: rows start on
-// 16-byte boundaries and c is a multiple of 8.
-template <int XT, bool VEC>
-__device__ __forceinline__ void load8(const QuantArgs &p, long long row, int c, float (&v)[8]) {
-    const typename XElem<XT>::T *x = static_cast<const typename XElem<XT>::T *>(p.X) + row * p.ldx + c;
-    if (VEC && c + 8 <= p.cols) {
-        if constexpr (XT == kOutF32) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(x));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(x) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-            unpack8_out16(__ldg(reinterpret_cast<const uint4 *>(x)), XT, v);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < p.cols ? load_out(x, i, XT) : 0.f;
+// Eight elements of a row as they are in memory: 16-bit types take half the
+// registers that their FP32 values would.
+template <int XT>
+struct Eight {
+    uint4 w[XT == kOutF32 ? 2 : 1];
+    __device__ __forceinline__ void clear() {
+        w[0] = make_uint4(0, 0, 0, 0);
+        if (XT == kOutF32) w[XT == kOutF32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
     }
-}
+    __device__ __forceinline__ void widen(float (&v)[8]) const {
+        if constexpr (XT == kOutF32) {
+            v[0] = __uint_as_float(w[0].x), v[1] = __uint_as_float(w[0].y), v[2] = __uint_as_float(w[0].z), v[3] = __uint_as_float(w[0].w);
+            v[4] = __uint_as_float(w[1].x), v[5] = __uint_as_float(w[1].y), v[6] = __uint_as_float(w[1].z), v[7] = __uint_as_float(w[1].w);
+        } else {
+            unpack8_out16(w[0], XT, v);
+        }
+    }
+    // Elements [c, c + 8) of row `row`, zeros from `cols` on.  VEC: rows start
+    // on 16-byte boundaries and c is a multiple of 8.
+    template <bool VEC>
+    __device__ __forceinline__ void load(const QuantArgs &p, long long row, int c) {
+        using T = typename XElem<XT>::T;
+        const T *x = static_cast<const T *>(p.X) + row * p.ldx + c;
+        if (VEC && c + 8 <= p.cols) {
+            w[0] = __ldg(reinterpret_cast<const uint4 *>(x));
+            if constexpr (XT == kOutF32) w[1] = __ldg(reinterpret_cast<const uint4 *>(x) + 1);
+        } else {
+            clear();
+            T *e = reinterpret_cast<T *>(w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < p.cols) e[i] = x[i];
+        }
+    }
+};
 
-__device__ __forceinline__ float max8(const float (&v)[8]) {
-    float m = 0.f;
+template <int XT>
+__device__ __forceinline__ float max8(const Eight<XT> &x) {
+    float v[8], m = 0.f;
+    x.widen(v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
     return m;
@@ -97,7 +116,10 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, in
     return lo | (hi << 16);
 }
 
-__device__ __forceinline__ void store8(const QuantArgs &p, long long row, int c, const float (&v)[8], float inv) {
+template <int XT>
+__device__ __forceinline__ void store8(const QuantArgs &p, long long row, int c, const Eight<XT> &x, float inv) {
+    float v[8];
+    x.widen(v);
     uint2 w;
     w.x = pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, p.e5m2);
     w.y = pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv, p.e5m2);
@@ -125,15 +147,13 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
     const bool live = row < p.rows;
     constexpr int kDeep = 4;  // blocks in flight
     for (int b = b0; b < b1; b += kDeep) {
-        float v[kDeep][8];
+        Eight<XT> v[kDeep];
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
-            if (live && b + u < b1) {
-                load8<XT, VEC>(p, row, (b + u) * kScaleBlock + sub * 8, v[u]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-            }
+            if (live && b + u < b1)
+                v[u].template load<VEC>(p, row, (b + u) * kScaleBlock + sub * 8);
+            else
+                v[u].clear();
         }
 #pragma unroll
         for (int u = 0; u < kDeep; ++u) {
@@ -153,23 +173,21 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
 // 128 x 128 blocks, one for each CTA: 16 lanes x 8 elements along a row, 16
 // rows at a time.
 template <int XT, bool VEC>
-__global__ void __launch_bounds__(256) quant_blocks_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(256, XT == kOutF32 ? 2 : 4) quant_blocks_kernel(const QuantArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     __shared__ float warp_max[8];
     const int bx = blockIdx.x % p.nx, by = blockIdx.x / p.nx;
     const int c = bx * kScaleBlock + (threadIdx.x & 15) * 8;
     const long long r0 = static_cast<long long>(by) * kScaleBlock + (threadIdx.x >> 4);
-    float v[8][8];
+    Eight<XT> v[8];
     float m = 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-        if (r0 + 16 * u < p.rows) {
-            load8<XT, VEC>(p, r0 + 16 * u, c, v[u]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[u][i] = 0.f;
-        }
+        if (r0 + 16 * u < p.rows)
+            v[u].template load<VEC>(p, r0 + 16 * u, c);
+        else
+            v[u].clear();
     }
 #pragma unroll
     for (int u = 0; u < 8; ++u) m = fmaxf(m, max8(v[u]));
@@ -191,7 +209,7 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const QuantArgs p) {
 // X and columns [64 bx, +64); thread t has 8 columns (t % 8) and
 // the 4 rows 4 (t / 8) + i, whose bytes become one word of the turned tile.
 template <int XT, bool VEC>
-__global__ void __launch_bounds__(256) quant_cols_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(256, 6) quant_cols_kernel(const QuantArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     __shared__ float part[8][64];
@@ -200,20 +218,21 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const QuantArgs p) {
     const int bx = blockIdx.x % p.nx, by = blockIdx.x / p.nx;
     const int c0 = bx * 64;
     const long long r0 = static_cast<long long>(by) * kScaleBlock;
-    float v[4][8], m[8];
+    Eight<XT> v[4];
+    float m[8], f[4][8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const long long r = r0 + rg * 4 + i;
-        if (r < p.rows) {
-            load8<XT, VEC>(p, r, c0 + cg * 8, v[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
-        }
+        if (r < p.rows)
+            v[i].template load<VEC>(p, r, c0 + cg * 8);
+        else
+            v[i].clear();
     }
 #pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].widen(f[i]);
+#pragma unroll
     for (int j = 0; j < 8; ++j) {
-        m[j] = fmaxf(fmaxf(fabsf(v[0][j]), fabsf(v[1][j])), fmaxf(fabsf(v[2][j]), fabsf(v[3][j])));
+        m[j] = fmaxf(fmaxf(fabsf(f[0][j]), fabsf(f[1][j])), fmaxf(fabsf(f[2][j]), fabsf(f[3][j])));
         m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 8));
         m[j] = fmaxf(m[j], __shfl_xor_sync(0xffffffffu, m[j], 16));
     }
@@ -233,9 +252,11 @@ __global__ void __launch_bounds__(256) quant_cols_kernel(const QuantArgs p) {
     }
     __syncthreads();
 #pragma unroll
+    for (int i = 0; i < 4; ++i) v[i].widen(f[i]);
+#pragma unroll
     for (int j = 0; j < 8; ++j) {
         const float inv = part[0][cg * 8 + j];
-        turned[cg * 8 + j][rg] = pack4(v[0][j] * inv, v[1][j] * inv, v[2][j] * inv, v[3][j] * inv, p.e5m2);
+        turned[cg * 8 + j][rg] = pack4(f[0][j] * inv, f[1][j] * inv, f[2][j] * inv, f[3][j] * inv, p.e5m2);
     }
     __syncthreads();
     const long long left = p.rows - r0;  // bytes of a turned row that exist
