@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
 // 128 x 128 blocks, one for each CTA: 16 lanes x 8 elements along a row, 16
 // rows at a time.
 template <int XT, bool VEC>
-__global__ void __launch_bounds__(256, XT == kOutF32 ? 2 : 4) quant_blocks_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(256, 3) quant_blocks_kernel(const QuantArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     __shared__ float warp_max[8];
