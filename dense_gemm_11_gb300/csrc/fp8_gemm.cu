@@ -27,6 +27,7 @@
 // order through distributed shared memory.  Every wait is bounded.
 #include <algorithm>
 #include <cstdint>
+#include <cmath>
 #include <mutex>
 
 #include <cudaTypedefs.h>
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
     const int q = warp & 3;                               // tensor-memory lane quarter
     const int col0 = ((warp - 2) >> 2) * Cfg::kCols;      // first accumulator column (epilogue warps)
     const int n = n0 + q * 32 + lane;
-    float acc[Cfg::kCols];
+    uint64_t acc[Cfg::kCols / 2];  // pairs of accumulator columns (rows m of C)
     uint32_t armed = 0, armed_parity = 0;
 
     if (warp == 0) {
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
     } else if (warp >= 2) {
         // ------------------------------------------------ epilogue: scale and add
 #pragma unroll
-        for (int j = 0; j < Cfg::kCols; ++j) acc[j] = 0.f;
+        for (int j = 0; j < Cfg::kCols / 2; ++j) acc[j] = 0;
         // B's scale: of this lane's column, one block ahead; or, one for the
         // whole tile, of 32 blocks at once (lane l has block kb0 + l, + 32, ..).
         const float *sb = p.SB + (p.b_rows ? min(n, p.N - 1) : n0 / kScaleBlock) * p.sb_n + kb0 * p.sb_kb;
@@ -257,19 +258,24 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
             }
             tc_fence_after();
             const uint32_t t = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + buf * BN + col0;
-            const float4 *sa = reinterpret_cast<const float4 *>(sS + slot * Cfg::kSlotFloats + col0);
+            const uint32_t sa = smem_u32(sS + slot * Cfg::kSlotFloats + col0);
+            const uint64_t ss = pack_f32x2(s, s);
+            constexpr int kDeep = Cfg::kCols >= 32 ? 2 : 1;  // reads of 16 columns in flight
 #pragma unroll
-            for (int c = 0; c < Cfg::kCols / 16; ++c) {
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(t + c * 16, r);
+            for (int c = 0; c < Cfg::kCols / 16; c += kDeep) {
+                uint32_t r[kDeep][16];
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u) tmem_ld_32x32b_x16(t + (c + u) * 16, r[u]);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float4 f = sa[c * 4 + j];
-                    acc[c * 16 + 4 * j] = fmaf(s * f.x, __uint_as_float(r[4 * j]), acc[c * 16 + 4 * j]);
-                    acc[c * 16 + 4 * j + 1] = fmaf(s * f.y, __uint_as_float(r[4 * j + 1]), acc[c * 16 + 4 * j + 1]);
-                    acc[c * 16 + 4 * j + 2] = fmaf(s * f.z, __uint_as_float(r[4 * j + 2]), acc[c * 16 + 4 * j + 2]);
-                    acc[c * 16 + 4 * j + 3] = fmaf(s * f.w, __uint_as_float(r[4 * j + 3]), acc[c * 16 + 4 * j + 3]);
+                for (int u = 0; u < kDeep; ++u) {
+                    uint64_t f[8];  // volatile: 16 columns' scales at a time
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * j]), "=l"(f[2 * j + 1]) : "r"(sa + ((c + u) * 16 + 4 * j) * 4));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        fma_f32x2(acc[(c + u) * 8 + j], mul_f32x2(ss, f[j]), pack_b32x2(r[u][2 * j], r[u][2 * j + 1]));
                 }
             }
             tc_fence_before();
@@ -284,10 +290,11 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
             for (int j = 0; j < Cfg::kCols; j += 4) {
                 if (m0 + col0 + j >= p.M) break;
                 float w[4], cold[4];
+                unpack_f32x2(acc[j / 2], w[0], w[1]);
+                unpack_f32x2(acc[j / 2 + 1], w[2], w[3]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int m = m0 + col0 + j + k;
-                    w[k] = acc[j + k];
                     cold[k] = (p.beta != 0.f && m < p.M) ? load_out(p.C, static_cast<size_t>(m) * p.ldc + n, p.c_type) : 0.f;
                 }
                 epilogue4(w, p.alpha, p.beta, cold, b4, p.act);
@@ -327,8 +334,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
     const int rows = min(BN, p.M - m0);
     if (warp >= 2) {
 #pragma unroll
-        for (int j = 0; j < Cfg::kCols; ++j)
-            if (col0 + j < rows) part[(col0 + j) * kPR + q * 32 + lane] = acc[j];
+        for (int j = 0; j < Cfg::kCols; j += 2) {
+            float lo, hi;
+            unpack_f32x2(acc[j / 2], lo, hi);
+            if (col0 + j < rows) part[(col0 + j) * kPR + q * 32 + lane] = lo;
+            if (col0 + j + 1 < rows) part[(col0 + j + 1) * kPR + q * 32 + lane] = hi;
+        }
     }
     cluster_sync();
     const uint32_t part_addr = smem_u32(part);
@@ -442,10 +453,12 @@ __device__ __forceinline__ void epilogue32(const Fp8Args &p, float (&v)[32], int
 }
 
 // 32 columns of this lane's row through the warp's staging buffer (128-byte
-// rows, 128-byte swizzle) to a TMA store: 32 columns of FP32, or 64 of a 16-bit
-// type, of which `second` is the upper half.
-__device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], const CUtensorMap *tm_c, uint8_t *staged, int lane,
-                                        int row, int n, int second) {
+// rows, 128-byte swizzle): 32 columns of FP32, or 64 of a 16-bit type, of which
+// `second` is the upper half.  A full buffer goes out by a TMA store, or, where
+// the rows of C are not aligned for one, row by row with neighbouring lanes on
+// neighbouring elements.
+__device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], const CUtensorMap *tm_c, bool by_tma, uint8_t *staged,
+                                        int lane, int row, int n, int second) {
     const bool wide = p.c_type == kOutF32;
     if (wide || !second) {  // the buffer's last store has read it
         if (lane == 0) bulk_wait_read_all();
@@ -463,23 +476,33 @@ __device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], 
                 make_uint4(pack2_out16(v[8 * c], v[8 * c + 1], p.c_type), pack2_out16(v[8 * c + 2], v[8 * c + 3], p.c_type),
                            pack2_out16(v[8 * c + 4], v[8 * c + 5], p.c_type), pack2_out16(v[8 * c + 6], v[8 * c + 7], p.c_type));
     }
-    if (wide || second) {
-        const int first = wide ? n : n - 32;
+    if (!wide && !second) return;
+    const int first = wide ? n : n - 32, esize = wide ? 4 : 2;
+    if (by_tma) {
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
             if (first < p.N) tma_store_2d(tm_c, staged, first, row);
             bulk_commit();
         }
+        return;
     }
-}
-
-// The same straight from registers, for a C without aligned rows.
-__device__ __forceinline__ void store32(const Fp8Args &p, const float (&v)[32], int m, int n) {
-    const size_t ci = static_cast<size_t>(m) * static_cast<size_t>(p.ldc) + n;
+    __syncwarp();
+    for (int r = 0; r < 32 && row + r < p.M; ++r) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (n + j < p.N && debug_in_bounds(p.c_extent == 0 || ci + j < p.c_extent, p.err)) store_out(p.C, ci + j, p.c_type, v[j]);
+        for (int u = 0; u < 2; ++u) {
+            const int j = u * 32 + lane;
+            if (j * esize >= 128 || first + j >= p.N) continue;
+            const size_t ci = static_cast<size_t>(row + r) * static_cast<size_t>(p.ldc) + first + j;
+            const uint8_t *at = staged + r * 128 + ((((j * esize) >> 4) ^ (r & 7)) << 4) + (j * esize & 15);
+            if (!debug_in_bounds(p.c_extent == 0 || ci < p.c_extent, p.err)) continue;
+            if (wide)
+                static_cast<float *>(p.C)[ci] = *reinterpret_cast<const float *>(at);
+            else
+                static_cast<uint16_t *>(p.C)[ci] = *reinterpret_cast<const uint16_t *>(at);
+        }
+    }
+    __syncwarp();
 }
 
 // acc[col ..] += s * (B's scale of the column, with B_ROWS: at sb on) * r, 32
@@ -718,10 +741,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 16; ++j) unpack_f32x2(acc[gr * 16 + j], v[2 * j], v[2 * j + 1]);
                 epilogue32(p, v, m, n, lane);
-                if (pp.c_tma)
-                    stage32(p, v, &tm_c, staged, lane, row, n, gr & 1);
-                else if (m < p.M)
-                    store32(p, v, m, n);
+                stage32(p, v, &tm_c, pp.c_tma, staged, lane, row, n, gr & 1);
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -837,6 +857,61 @@ cudaError_t launch_fp8_tile(const Fp8Gemm &g, Fp8Args a, cudaStream_t stream) {
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
+// Clusters of `splits` CTAs of fp8_tile_kernel<BN, STAGES> that the GPU holds
+// at once (cached; one device type per process).
+template <int BN, int STAGES>
+int tile_clusters(int splits) {
+    static int cap[9] = {-1, -1, -1, -1, -1, -1, -1, -1, -1};  // atomic accesses: planners may run concurrently
+    const int known = __atomic_load_n(&cap[splits], __ATOMIC_ACQUIRE);
+    if (known >= 0) return known;
+    using Cfg = Fp8Cfg<BN, STAGES>;
+    auto kern = fp8_tile_kernel<BN, STAGES>;
+    static unsigned long long smem_set = 0;
+    int n = 0;
+    if (ensure_dynamic_smem(kern, Cfg::kSmemBytes, smem_set) == cudaSuccess) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(splits);
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(splits * 2 * device_sm_count());
+        cfg.blockDim = dim3(Cfg::kThreads);
+        cfg.dynamicSmemBytes = Cfg::kSmemBytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) {
+            (void)cudaGetLastError();
+            n = 0;
+        }
+    }
+    __atomic_store_n(&cap[splits], n, __ATOMIC_RELEASE);
+    return n;
+}
+
+// K splits of single-CTA tiles.  A model of measured times, in us: 4.5 for the
+// call, a block in every wave of CTAs (0.47 with 128 columns of accumulator,
+// where its scaling counts; 0.25 with up to 64, two CTAs an SM), and for a split
+// 1.5 and the partial tile's bytes from the other CTAs at 32 GB/s.  Measured /
+// modelled: 128 x 4096 x 4096 in 4 splits 9.9 / 10.3, 256 x 4096 x 4096 in 2
+// 14.0 / 14.5, 128 x 19456 x 11008 whole 44.7 / 44.9.  With 128 columns all
+// clusters have to fit at once: 512 x 512 x 11008 in 16 clusters of 8 CTAs, of
+// which some had to wait, took 20.4 us, as long as two waves (12.8 in fewer
+// splits).  Smaller tiles are bound by memory and do not mind: 16 x 11008 x 4096
+// takes 8.3 us in 3 splits, not all of them at once, and 10.7 in 2.
+int pick_splits(int bn, int tiles, int blocks, int rows, int sms, double *time_us) {
+    const int room = sms * (bn <= 64 ? 2 : 1);  // CTAs at a time
+    const double block_us = bn <= 64 ? 0.25 : 0.47;
+    int best = 1;
+    double best_t = 4.5 + std::ceil(static_cast<double>(tiles) / room) * blocks * block_us;
+    for (int s = 2; s <= 8 && s <= blocks; ++s) {
+        if (static_cast<long long>(tiles) * s > room || (bn > 64 && tiles > tile_clusters<128, 6>(s))) break;
+        const double t = 4.5 + (blocks + s - 1) / s * block_us + 1.5 + rows * kPR * 4.0 * (s - 1) / s / 32e3;
+        if (t < best_t) best_t = t, best = s;
+    }
+    *time_us = best_t;
+    return best;
+}
+
 template <bool B_ROWS>
 cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, cudaStream_t stream) {
     using Cfg = Fp8PairCfg<B_ROWS>;
@@ -925,11 +1000,16 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) 
     a.tiles_m = (g.M + bn - 1) / bn;
     const long long tiles = static_cast<long long>((g.N + kPR - 1) / kPR) * a.tiles_m;
     const int sms = device_sm_count();
-    const int room = sms * (bn <= 64 ? 2 : 1);  // CTAs at a time
-    if (tiles * 2 <= room) a.splits = static_cast<int>(std::min<long long>({8, room / tiles, std::max(1, a.kb_total / 2)}));
+    double t_tile = 0.0;
+    a.splits = pick_splits(bn, static_cast<int>(std::min<long long>(tiles, 1 << 30)), a.kb_total, std::min(bn, g.M), sms, &t_tile);
     info->launches = 1;
-    if (g.M > 128) {
+    // Pairs: 0.45 us a block and wave of tiles (0.76 with a scale for each
+    // column), against single tiles and their splits (pick_splits).
+    const double pair_tiles = static_cast<double>((g.M + 255) / 256) * ((g.N + kPairN - 1) / kPairN);
+    const double t_pair = 4.5 + std::ceil(pair_tiles / (sms / 2)) * a.kb_total * (g.b_rows ? 0.76 : 0.45);
+    if (g.M > 128 && t_pair <= t_tile) {
         info->plan = "fp8_pair_256x256";
+        a.splits = 1;
         return g.b_rows ? launch_fp8_pair<true>(g, a, stream) : launch_fp8_pair<false>(g, a, stream);
     }
     switch (bn) {
