@@ -36,21 +36,23 @@
 // do not depend on timing.  Every wait is bounded.
 //
 // Numbers.  Every product is a 16-bit x 16-bit mma.sync with FP32 sums; what
-// the activations are held in depends on the weights:
+// the activations are held in depends on the types:
 //   BF16 weights   X as it is; h as the sum of two BF16 numbers (16 significant
 //                  bits, FP32's range), two products each;
-//   FP16 weights   X as it is; h in FP16 after scaling a token's h by the power
-//                  of two that brings its largest element to [2^14, 2^15): 11
-//                  bits down to 2^-28 of the largest, nothing overflows.  h is
-//                  written in FP32 and in FP16 as it is; where some slot's
-//                  maximum turns out to be outside [2^-4, 65504] (as it is, h
-//                  keeps 2^-21 of the maximum or better inside) all are fitted
-//                  between two grid barriers (3 us), else nothing is;
+//   FP16 weights   X as it is; h as the sum of two FP16 numbers (21 bits);
 //   e4m3 weights   widened to FP16 (exact), one conversion for two elements
 //                  (TF32 products took two more each, and twice the matrix
-//                  instructions: 3.2 TB/s against 4.x); h as for FP16, and a
-//                  BF16 X too (8 bits: exact down to 2^-31 of the largest).
-// The e4m3 scale of a 128 x 128 block multiplies that block's FP32 sum.
+//                  instructions: 165 us against 149 at 16 tokens, 32 experts).
+//                  An FP16 X as it is with h in two parts; a BF16 X in FP16
+//                  after scaling a token by the power of two that brings its
+//                  largest element to [2^14, 2^15) (its 8 bits are exact down to
+//                  2^-31 of that), and h in one FP16 number: 11 bits, under a
+//                  result that is usually rounded to BF16's 8.
+// Where h is held in FP16 it is written in FP32 too.  If some slot's largest
+// |h| turns out to be outside [2^-4, 65504] (inside, what FP16 drops is 2^-20 of
+// the largest at most), all are fitted as a BF16 X is, between two grid barriers
+// (3 us), else nothing is.  The e4m3 scale of a 128 x 128 block multiplies that
+// block's FP32 sum.
 #include <algorithm>
 #include <cstdint>
 
@@ -83,11 +85,12 @@ struct MoeArgs {
     int y_type, act, renorm;
     int *ids;
     float *weights;
-    // Scratch: T x E logits; h in FP32 (slots x I), or two BF16 parts in
-    // alternate runs of 64; h and X in FP16, scaled; the largest |h| of a slot,
-    // and the scale of a token; k_splits x slots x H partial results.
+    // Scratch: T x E logits; h in FP32 (slots x I) and in 16 bits, one number or
+    // two, these in alternate runs of 64; X in FP16, scaled; the largest |h| of
+    // a slot, and the scale of a token; k_splits x slots x H partial results.
     float *logits, *hidden, *part;
-    __half *hidden16, *x16;  // hidden16: h as it is, or fitted
+    uint8_t *hidden16;
+    __half *x16;
     unsigned *h_max;
     float *x_scale;
     uint16_t *chosen;  // T x top_k, and their weights
@@ -183,6 +186,19 @@ __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(addr)
                  : "memory");
+}
+// h as hi + lo, each of 16 bits.  An infinity has no remainder.
+template <int TYPE>
+__device__ __forceinline__ void two_parts(float h, uint16_t &hi, uint16_t &lo) {
+    if constexpr (TYPE == kOutF16) {
+        const __half a = __float2half_rn(h);
+        hi = __half_as_ushort(a);
+        lo = __half_as_ushort(__float2half_rn(fabsf(h) < INFINITY ? h - __half2float(a) : 0.f));
+    } else {
+        const __nv_bfloat16 a = __float2bfloat16_rn(h);
+        hi = __bfloat16_as_ushort(a);
+        lo = __bfloat16_as_ushort(__float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(a) : 0.f));
+    }
 }
 // 2^e that brings a largest magnitude into [2^14, 2^15), and 2^-e.  Normal
 // numbers both (a maximum below 2^-112 stays smaller); 1 for zero.
@@ -464,7 +480,7 @@ __device__ __forceinline__ bool slots_fit(const MoeArgs &p) {
 }
 
 // ---------------------------------------------------------------- units
-// Bytes of a slot's h as two BF16 parts.
+// Bytes of a slot's h as two 16-bit parts.
 __host__ __device__ constexpr long long parts_bytes(int I) { return (I + 63ll) / 64 * 256; }
 
 struct Unit {
@@ -506,7 +522,8 @@ template <int XT, bool FP8>
 struct MoeCfg {
     static constexpr int kWBytes = FP8 ? 1 : 2;
     static constexpr int kBoxK = 128 / kWBytes;  // k of a box: 128 (one scale block) or 64
-    static constexpr bool kTwoParts = !FP8 && XT == kOutBF16;  // h as two BF16 numbers
+    static constexpr bool kFit = FP8 || XT == kOutF16;         // h in FP16
+    static constexpr bool kTwoParts = !FP8 || XT == kOutF16;   // h as two numbers
     static constexpr bool kScaledX = FP8 && XT == kOutBF16;    // X as scaled FP16
     static constexpr int kMma = FP8 ? kOutF16 : XT;
     static constexpr int kXBytes = 2, kHBytes = kTwoParts ? 4 : 2;
@@ -524,8 +541,8 @@ struct MoeCfg {
 // (g, t) holds rows g and g + 8, token 8 n + g and the same k's of both; w0 and
 // w1 are the first of each 8 rows (16-byte chunk c of row g at c ^ g, by the
 // copy's swizzle), act[n] its token's k's of this box; USED of the NT groups of
-// 8 tokens exist.  PARTS: the second BF16
-// parts follow the first after 128 bytes.  TAIL: only `valid` k's exist; the
+// 8 tokens exist.  PARTS: activations are sums of
+// two numbers, 64 k's of the second 128 bytes after the first's.  TAIL: only `valid` k's exist; the
 // weights past them are zeros, the activations are left over from other stages.
 template <int XT, bool FP8, int NT, int USED, bool PARTS, bool TAIL>
 __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *const (&act)[NT], int valid,
@@ -545,12 +562,15 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
                 widen_e4m3(w[2 * h], a0, a2);
                 widen_e4m3(w[2 * h + 1], a1, a3);
                 const int k = (ch + h) * 16 + t * 4;
+                const int at = PARTS ? (ch / 4) * 256 + ((ch + h) % 4 * 16 + t * 4) * 2 : k * 2;
 #pragma unroll
-                for (int n = 0; n < USED; ++n) {
-                    uint2 x = *reinterpret_cast<const uint2 *>(act[n] + k * 2);
-                    if (TAIL && k >= valid) x = make_uint2(0, 0);
-                    mma_16bit<Cfg::kMma>(c[n], a0, a1, a2, a3, x.x, x.y);
-                }
+                for (int part = 0; part < (PARTS ? 2 : 1); ++part)
+#pragma unroll
+                    for (int n = 0; n < USED; ++n) {
+                        uint2 x = *reinterpret_cast<const uint2 *>(act[n] + at + part * 128);
+                        if (TAIL && k >= valid) x = make_uint2(0, 0);
+                        mma_16bit<Cfg::kMma>(c[n], a0, a1, a2, a3, x.x, x.y);
+                    }
             }
         }
     } else {
@@ -765,8 +785,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                     token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
                                           : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
                 else
-                    token = Cfg::kTwoParts ? reinterpret_cast<const uint8_t *>(p.hidden) + slot * parts_bytes(p.I)
-                                           : reinterpret_cast<const uint8_t *>(p.hidden16 + static_cast<long long>(slot) * p.I);
+                    token = p.hidden16 + slot * (Cfg::kTwoParts ? parts_bytes(p.I) : 2ll * p.I);
             }
             for (int ch = n.ch0; ok && ch < n.ch1; ++ch) {
                 if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u))) {
@@ -788,7 +807,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         // h of every CTA has to be there (and fitted, if need be).
         if (ok && shift < units2) {
             ok = __all_sync(0xffffffffu, wait_count(&p.counters[1], grid));
-            if (ok && !Cfg::kTwoParts && !slots_fit(p)) ok = __all_sync(0xffffffffu, wait_count(&p.counters[2], grid));
+            if (ok && Cfg::kFit && !slots_fit(p)) ok = __all_sync(0xffffffffu, wait_count(&p.counters[2], grid));
             if (!ok && lane == 0) give_up();
             fence_proxy_async_all();
         }
@@ -911,20 +930,20 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                         if (gated) h *= acc[nt][j + 2] * xs;
                         if (!in || at >= p.I) continue;
                         if constexpr (Cfg::kTwoParts) {
-                            __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(reinterpret_cast<uint8_t *>(p.hidden) + slot * parts_bytes(p.I)) +
-                                                at / 64 * 128 + at % 64;
-                            const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                            const float rest = h - __bfloat162float(hi);
+                            uint16_t *to = reinterpret_cast<uint16_t *>(p.hidden16 + slot * parts_bytes(p.I)) + at / 64 * 128 + at % 64;
+                            uint16_t hi, lo;
+                            two_parts<Cfg::kMma>(h, hi, lo);
                             to[0] = hi;
-                            to[64] = __float2bfloat16_rn(fabsf(h) < INFINITY ? rest : 0.f);  // inf - inf is no remainder
+                            to[64] = lo;
                         } else {
-                            const long long to = static_cast<long long>(slot) * p.I + at;
-                            p.hidden[to] = h;
-                            p.hidden16[to] = __float2half_rn(h);
+                            reinterpret_cast<__half *>(p.hidden16)[static_cast<long long>(slot) * p.I + at] = __float2half_rn(h);
+                        }
+                        if constexpr (Cfg::kFit) {
+                            p.hidden[static_cast<long long>(slot) * p.I + at] = h;
                             if (fabsf(h) < INFINITY) largest = fmaxf(largest, fabsf(h));
                         }
                     }
-                    if constexpr (!Cfg::kTwoParts) {
+                    if constexpr (Cfg::kFit) {
 #pragma unroll
                         for (int d = 16; d >= 4; d >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, d));
                         if (in && lane < 4) atomicMax(p.h_max + slot, __float_as_uint(largest));
@@ -935,7 +954,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         __threadfence();
         consumer_sync<kWarps>();
         if (threadIdx.x == 0) atomicAdd(&p.counters[1], 1u);
-        if constexpr (!Cfg::kTwoParts) {
+        if constexpr (Cfg::kFit) {
             // h to FP16, now that every slot's largest element is known
             if (threadIdx.x == 0 && !wait_count(&p.counters[1], grid)) give_up();
             consumer_sync<kWarps>();
@@ -947,9 +966,20 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                 const float f = pow2(fit_exponent(__uint_as_float(__ldcg(p.h_max + x / per))));
                 const float4 *h = reinterpret_cast<const float4 *>(p.hidden) + 2ll * x;
                 const float4 a = __ldcg(h), b = __ldcg(h + 1);
-                reinterpret_cast<uint4 *>(p.hidden16)[x] =
-                    make_uint4(pack2_out16(a.x * f, a.y * f, kOutF16), pack2_out16(a.z * f, a.w * f, kOutF16),
-                               pack2_out16(b.x * f, b.y * f, kOutF16), pack2_out16(b.z * f, b.w * f, kOutF16));
+                const float v[8] = {a.x * f, a.y * f, a.z * f, a.w * f, b.x * f, b.y * f, b.z * f, b.w * f};
+                if constexpr (Cfg::kTwoParts) {
+                    const int at = x % per * 8;
+                    uint16_t hi[8], lo[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) two_parts<Cfg::kMma>(v[i], hi[i], lo[i]);
+                    uint8_t *to = p.hidden16 + x / per * parts_bytes(p.I) + at / 64 * 256 + at % 64 * 2;
+                    auto two = [](const uint16_t *u) { return u[0] | static_cast<uint32_t>(u[1]) << 16; };
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(two(hi), two(hi + 2), two(hi + 4), two(hi + 6));
+                    *reinterpret_cast<uint4 *>(to + 128) = make_uint4(two(lo), two(lo + 2), two(lo + 4), two(lo + 6));
+                } else {
+                    reinterpret_cast<uint4 *>(p.hidden16)[x] = make_uint4(pack2_out16(v[0], v[1], kOutF16), pack2_out16(v[2], v[3], kOutF16),
+                                                                          pack2_out16(v[4], v[5], kOutF16), pack2_out16(v[6], v[7], kOutF16));
+                }
             }
             fence_proxy_async_all();  // read by bulk copies
             __threadfence();
@@ -1124,15 +1154,15 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     // Scratch, in floats, each part on 256 bytes.
     auto up64 = [](size_t n) { return (n + 63) / 64 * 64; };
     const size_t n_slots = static_cast<size_t>(m.T) * m.top_k;
-    const size_t n_logits = up64(static_cast<size_t>(m.T) * m.E), n_hidden = up64(n_slots * parts_bytes(m.I) / 4);
-    const size_t n_h16 = up64(n_slots * m.I / 2), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
+    const size_t n_logits = up64(static_cast<size_t>(m.T) * m.E), n_hidden = up64(n_slots * m.I);
+    const size_t n_h16 = up64(n_slots * parts_bytes(m.I) / 4), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
     Scratch s;
     const cudaError_t e =
         acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + 3 * n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
     a.hidden = a.logits + n_logits;
-    a.hidden16 = reinterpret_cast<__half *>(a.hidden + n_hidden);
+    a.hidden16 = reinterpret_cast<uint8_t *>(a.hidden + n_hidden);
     a.x16 = reinterpret_cast<__half *>(a.hidden + n_hidden + n_h16);
     a.h_max = reinterpret_cast<unsigned *>(a.hidden + n_hidden + n_h16 + n_x16);
     a.x_scale = a.hidden + n_hidden + n_h16 + n_x16 + n_max;

@@ -349,7 +349,7 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  *   ids     T x top_k int, weights T x top_k float: the choice and the w_j in
  *           the order of the logits; either may be NULL.
  * Sums, the softmax and the logits are FP32; h is rounded once, to 16 (BF16
- * weights) or 11 significant bits.  A
+ * weights), 21 (FP16 X) or 11 significant bits (BF16 X, 8-bit weights).  A
  * token with a NaN logit gets NaN weights, and so a NaN row.
  * Limits: 1 <= top_k <= min(E, 16), E <= 512, T <= 128, T * top_k <= 1024;
  * H and I multiples of 16, E * max(H, I) < 2^31; X, router, gate, up and down 16-byte aligned and

@@ -4,15 +4,15 @@ Inputs are made so that every partial sum of a logit is exact in FP32 (tokens
 in steps of 1/32, router weights in steps of 2^-13), so the chosen experts are
 compared exactly, ties included.
 
-Bound of y.  Rounding h to TF32 errs by at most 2^-11 of |h| (half an ulp of
-11 significant bits is 2^-12, and the conversion's ties and the sums before it
-stay inside the other half): 2^-11 of S = sum_j w_j |Wdown| |h_j|.  h itself
-errs by the FP32 sums of its two factors, 1e-5 of sum |W||x| each, which for
-normal data of width H <= 4096 is at most 1e-5 * 0.8 sqrt(H) / 0.8 of its size
-where that is typical (64e-5 relative, averaged over the sum by the signs);
-activations in __expf and rcp.approx add 2^-20.  With FP32 sums of the down
-projection at 1e-5 S: 2^-11 S + 7e-4 S, rounded up to 1.5e-3 S, plus one
-rounding of the output.
+Bound of y.  h is held in 11 bits or more: rounding errs by at most 2^-12 of
+|h| where an FP16 number holds it (2^-17 and 2^-22 with two numbers), plus
+2^-20 of the slot's largest |h|; together under 2^-11 of S = sum_j w_j |Wdown|
+|h_j| for the data here.  h itself errs by the FP32 sums of its two factors,
+1e-5 of sum |W||x| each, which for normal data of width H <= 4096 is at most
+1e-5 * 0.8 sqrt(H) / 0.8 of its size where that is typical (64e-5 relative,
+averaged over the sum by the signs); activations in __expf and rcp.approx add
+2^-20.  With FP32 sums of the down projection at 1e-5 S: 2^-11 S + 7e-4 S,
+rounded up to 1.5e-3 S, plus one rounding of the output.
 """
 import numpy as np
 import pytest
@@ -111,6 +111,34 @@ def test_extreme_logits():
     X[2] *= 64
     check_layer(X, router * 64, mats, None, 3)
     check_layer(X, router * 64, mats, None, 3, renorm=False)
+
+
+@pytest.mark.parametrize("power", [15, -12])
+@pytest.mark.parametrize("xt,fp8", [(torch.float16, False), (torch.float16, True), (torch.bfloat16, True), (torch.bfloat16, False)])
+@pytest.mark.parametrize("T", [2, 40])
+def test_hidden_values_outside_fp16(xt, fp8, power, T):
+    """|h| above FP16's largest number, or so small that FP16 would lose bits."""
+    X, router, mats, scales = layer(T, 6, 256, 208, xt, fp8)
+    if fp8:
+        scales[1].mul_(2.0 ** power)
+    else:
+        mats[1].mul_(2.0 ** power)
+    Y = torch.empty(T, 256, device="cuda")
+    g.moe_few_tokens(X, router, *mats, Y, 2, scales=scales)
+    y, _, _, S = ref.moe(X, router, *mats, 2, scales)
+    # (the absolute floor of the comparison, 1e-6, is scaled away)
+    assert_within((Y.double() * 2.0 ** -power).cpu().numpy(), y.numpy() * 2.0 ** -power, S.numpy() * 2.0 ** -power, TOL)
+
+
+def test_infinite_weight_reaches_its_tokens_only():
+    X, router, mats, _ = layer(12, 6, 128, 128, torch.float16)
+    ids = torch.empty(12, 2, dtype=torch.int32, device="cuda")
+    Y = torch.empty_like(X)
+    g.moe_few_tokens(X, router, *mats, Y, 2, ids=ids)
+    clean, hit = Y.clone(), (ids == int(ids[0, 0])).any(dim=1)
+    mats[1][int(ids[0, 0])] = float("inf")
+    g.moe_few_tokens(X, router, *mats, Y, 2)
+    assert torch.equal(Y[~hit], clean[~hit]) and not torch.isfinite(Y[hit].float()).all(dim=1).any()
 
 
 def test_nan_token_stays_alone():
