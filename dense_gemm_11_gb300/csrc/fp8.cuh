@@ -68,6 +68,19 @@ __device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi) {
 __device__ __forceinline__ void fma_f32x2(uint64_t &acc, uint64_t a, uint64_t b) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
 }
+// acc = (a * f) * (lo, hi) + acc, in order (volatile), so that the products do
+// not pile up in registers.
+__device__ __forceinline__ void fma_scaled_f32x2(uint64_t &acc, uint64_t a, uint64_t f, uint32_t lo, uint32_t hi) {
+    asm volatile(
+        "{\n"
+        " .reg .b64 d, t;\n"
+        " mov.b64 d, {%3, %4};\n"
+        " mul.rn.f32x2 t, %1, %2;\n"
+        " fma.rn.f32x2 %0, t, d, %0;\n"
+        "}\n"
+        : "+l"(acc)
+        : "l"(a), "l"(f), "r"(lo), "r"(hi));
+}
 __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
     uint64_t v;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));

@@ -509,18 +509,21 @@ __device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], 
 // columns.
 template <bool B_ROWS>
 __device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss, uint32_t sb) {
+    constexpr int kAtOnce = 4;  // pairs whose scales are read together
 #pragma unroll
-    for (int j = 0; j < 8; j += 4) {
-        uint64_t f[8];
-        if (B_ROWS) {  // volatile: 16 columns' scales at a time, not all ahead of the sums
+    for (int j = 0; j < 16; j += kAtOnce) {
+        uint64_t f[kAtOnce];
+        if (B_ROWS) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(sb + 16 * (j + u)));
+            for (int u = 0; u < kAtOnce / 2; ++u)
+                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(sb + 8 * j + 16 * u));
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            f[u] = B_ROWS ? mul_f32x2(ss, f[u]) : ss;
-            fma_f32x2(acc[col / 2 + 2 * j + u], f[u], pack_b32x2(r[4 * j + 2 * u], r[4 * j + 2 * u + 1]));
+        for (int u = 0; u < kAtOnce; ++u) {
+            if (B_ROWS)
+                fma_scaled_f32x2(acc[col / 2 + j + u], ss, f[u], r[2 * (j + u)], r[2 * (j + u) + 1]);
+            else
+                fma_f32x2(acc[col / 2 + j + u], ss, pack_b32x2(r[2 * (j + u)], r[2 * (j + u) + 1]));
         }
     }
 }
