@@ -49,6 +49,16 @@ __device__ __forceinline__ bool mbar_wait_patient(uint64_t *bar, uint32_t parity
     }
 }
 
+// 16 or 32 columns of a warp's 32 tensor-memory lanes.
+template <int COLS>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[COLS]) {
+    static_assert(COLS == 16 || COLS == 32, "columns");
+    if constexpr (COLS == 32)
+        tmem_ld_32x32b_x32(taddr, r);
+    else
+        tmem_ld_32x32b_x16(taddr, r);
+}
+
 // Two FP32 values in one 64-bit register, and acc = a * b + acc, a * b on both
 // (PTX f32x2; one rounding each, as fmaf).  Held as 64-bit values so that the
 // pairs stay in place.

@@ -505,27 +505,22 @@ __device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], 
     __syncwarp();
 }
 
-// acc[col ..] += s * (B's scale of the column, with B_ROWS: at sb on) * r, 32
-// columns.
-template <bool B_ROWS>
-__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss, uint32_t sb) {
-    constexpr int kAtOnce = 4;  // pairs whose scales are read together
+// acc[col ..] += s * r, 32 columns.
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[32], uint64_t ss) {
 #pragma unroll
-    for (int j = 0; j < 16; j += kAtOnce) {
-        uint64_t f[kAtOnce];
-        if (B_ROWS) {
+    for (int u = 0; u < 16; ++u) fma_f32x2(acc[col / 2 + u], ss, pack_b32x2(r[2 * u], r[2 * u + 1]));
+}
+// acc[col ..] += s * f * r, 16 columns, f their scales.
+__device__ __forceinline__ void add_scaled(uint64_t (&acc)[kPairCols / 2], int col, const uint32_t (&r)[16], uint64_t ss,
+                                           const uint64_t (&f)[8]) {
 #pragma unroll
-            for (int u = 0; u < kAtOnce / 2; ++u)
-                asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(sb + 8 * j + 16 * u));
-        }
+    for (int u = 0; u < 8; ++u) fma_scaled_f32x2(acc[col / 2 + u], ss, f[u], r[2 * u], r[2 * u + 1]);
+}
+// The scales of 16 columns (volatile: in order with the sums).
+__device__ __forceinline__ void load_col_scales(uint64_t (&f)[8], uint32_t at) {
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-            if (B_ROWS)
-                fma_scaled_f32x2(acc[col / 2 + j + u], ss, f[u], r[2 * (j + u)], r[2 * (j + u) + 1]);
-            else
-                fma_f32x2(acc[col / 2 + j + u], ss, pack_b32x2(r[2 * (j + u)], r[2 * (j + u) + 1]));
-        }
-    }
+    for (int u = 0; u < 4; ++u)
+        asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(at + 16 * u));
 }
 
 template <bool B_ROWS>
@@ -685,18 +680,21 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             const float *sb1 = p.SB + (B_ROWS ? 0 : min(col + 128, p.N - 1) / kScaleBlock * p.sb_n);
             float lane0 = 1.f, lane1 = 1.f, next0 = 1.f, next1 = 1.f;
             if (!B_ROWS && lane < p.kb_total) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
-            // Two reads of 32 columns in flight: while 32 columns' sums are
-            // added the next are read, over the end of a block too.  The
-            // accumulator goes back as soon as the block's last read is in.
-            uint32_t r0[32], r1[32];
+            // Two reads in flight (32 columns each, 16 with a scale for each
+            // column): while the sums of one are added the next is read, over
+            // the end of a block too.  The accumulator goes back as soon as the
+            // block's last read is in.
+            constexpr int kStep = B_ROWS ? 16 : 32;
+            uint32_t r0[kStep], r1[kStep];
+            uint64_t fa[8], fb[8];
             auto take = [&] {  // the next block's accumulator
                 ok = mbar_wait_patient(&tfull[(i & 1) * 2 + part], (i >> 1) & 1, p.wait_ns);
                 if (!ok) fp8_timeout(abort_flag, p.err);
                 tc_fence_after();
             };
             take();
-            tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN, r0);
-            tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN + 32, r1);
+            tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
+            tmem_ld<kStep>(t_row + (i & 1) * kPairN + kStep, r1);
             for (int kb = 0; kb < p.kb_total; ++kb) {
                 const uint32_t from = t_row + (i & 1) * kPairN, answer = release[i & 1];
                 float s0 = 1.f, s1 = 1.f;
@@ -711,26 +709,61 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 const float *sc = sS + slot * Cfg::kSlotFloats;
                 s0 *= sc[q * 32 + lane], s1 *= sc[q * 32 + lane];
                 const uint64_t ss0 = pack_f32x2(s0, s0), ss1 = pack_f32x2(s1, s1);
-                const uint32_t sbv = smem_u32(sc + 128 + part * 64);
-                tmem_wait_ld();
-                add_scaled<B_ROWS>(acc, 0, r0, ss0, sbv);
-                tmem_ld_32x32b_x32(from + 64, r0);
-                add_scaled<B_ROWS>(acc, 32, r1, ss0, sbv + 32 * 4);
-                tmem_ld_32x32b_x32(from + 96, r1);
+                // columns from 64 on are 64 further in C's tile
+                const uint32_t sbv = smem_u32(sc + 128 + part * 64), sbw = sbv + 64 * 4;
+                if constexpr (B_ROWS) {
+                    // each step's scales are read during the step before
+                    load_col_scales(fa, sbv);
+                    tmem_wait_ld();
+                    load_col_scales(fb, sbv + 16 * 4);
+                    add_scaled(acc, 0, r0, ss0, fa);
+                    tmem_ld<kStep>(from + 32, r0);
+                    load_col_scales(fa, sbv + 32 * 4);
+                    add_scaled(acc, 16, r1, ss0, fb);
+                    tmem_ld<kStep>(from + 48, r1);
+                    tmem_wait_ld();
+                    load_col_scales(fb, sbv + 48 * 4);
+                    add_scaled(acc, 32, r0, ss0, fa);
+                    tmem_ld<kStep>(from + 64, r0);
+                    load_col_scales(fa, sbw + 64 * 4);
+                    add_scaled(acc, 48, r1, ss0, fb);
+                    tmem_ld<kStep>(from + 80, r1);
+                    tmem_wait_ld();
+                    load_col_scales(fb, sbw + 80 * 4);
+                    add_scaled(acc, 64, r0, ss0, fa);
+                    tmem_ld<kStep>(from + 96, r0);
+                    load_col_scales(fa, sbw + 96 * 4);
+                    add_scaled(acc, 80, r1, ss0, fb);
+                    tmem_ld<kStep>(from + 112, r1);
+                } else {
+                    tmem_wait_ld();
+                    add_scaled(acc, 0, r0, ss0);
+                    tmem_ld<kStep>(from + 64, r0);
+                    add_scaled(acc, 32, r1, ss0);
+                    tmem_ld<kStep>(from + 96, r1);
+                }
                 tmem_wait_ld();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(answer);
                 ++i;
-                add_scaled<B_ROWS>(acc, 64, r0, ss1, sbv + 128 * 4);
+                if constexpr (B_ROWS) {
+                    load_col_scales(fb, sbw + 112 * 4);
+                    add_scaled(acc, 96, r0, ss0, fa);
+                } else {
+                    add_scaled(acc, 64, r0, ss1);
+                }
                 const bool more = kb + 1 < p.kb_total;
                 if (more) {
                     take();
                     if (!ok) break;
-                    tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN, r0);
+                    tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
                 }
-                add_scaled<B_ROWS>(acc, 96, r1, ss1, sbv + 160 * 4);
-                if (more) tmem_ld_32x32b_x32(t_row + (i & 1) * kPairN + 32, r1);
+                if constexpr (B_ROWS)
+                    add_scaled(acc, 112, r1, ss0, fb);
+                else
+                    add_scaled(acc, 96, r1, ss1);
+                if (more) tmem_ld<kStep>(t_row + (i & 1) * kPairN + kStep, r1);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             tmem_wait_ld();
