@@ -712,7 +712,7 @@ int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, in
     if (fp8 && (!s_gate || !s_down || (up && !s_up))) return GEMM_ERR_INVALID_ARG;
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool ok = top_k <= kMoeMaxTopK && E <= kMoeMaxExperts && T <= kMoeMaxTokens && T * top_k <= kMoeMaxSlots &&
-                    H % 16 == 0 && I % 16 == 0 && al16(X) && al16(router) && al16(gate) && al16(up) && al16(down) &&
+                    H <= kMoeMaxWidth && H % 16 == 0 && I % 16 == 0 && al16(X) && al16(router) && al16(gate) && al16(up) && al16(down) &&
                     (T == 1 || ldx % 8 == 0) && static_cast<long long>(E) * std::max(H, I) < (1LL << 31);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();

@@ -73,7 +73,7 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
 cudaError_t run_fp8_scale_c(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info);
 
 // ---- mixture of experts for a few tokens (moe.cu) ----
-constexpr int kMoeMaxTokens = 128, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxSlots = 1024;
+constexpr int kMoeMaxTokens = 128, kMoeMaxExperts = 512, kMoeMaxTopK = 16, kMoeMaxSlots = 1024, kMoeMaxWidth = 32768;
 constexpr int kActSilu = 4;  // the C ABI's GEMM_ACT_SILU
 struct Moe {
     int T = 0, E = 0, top_k = 0, H = 0, I = 0;

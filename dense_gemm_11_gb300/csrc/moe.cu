@@ -99,6 +99,7 @@ struct MoeArgs {
     unsigned *err;
     int lw1, lw2;    // log2 of WR, the row groups (of 16 rows) of a unit, in the first half and in the down projection
     int k_splits;    // units of the down projection that share a row group's k
+    int by_token;    // the routing takes a CTA for each token
     int flat_h, flat_i;  // rows of H (I) elements are whole 128-byte boxes: one copy takes a stage's boxes
     int stages, stage_bytes;
 };
@@ -301,40 +302,55 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
 __device__ __forceinline__ float key_logit(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k); }
 
 // The keys of one token's logits, by a whole CTA: a warp takes 4 experts at a
-// time.
+// time, with the token in shared memory (xs) and the experts' rows of 4 steps
+// (2 of FP32) in flight.
 template <int XT, int kWarps>
-__device__ void router_token(const MoeArgs &p, int t, uint32_t *keys) {
+__device__ void router_token(const MoeArgs &p, int t, uint32_t *keys, uint4 *xs) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint16_t *x = static_cast<const uint16_t *>(p.X) + t * p.ldx;
-    const int esize = p.router_f32 ? 4 : 2;
+    const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.X) + t * p.ldx);
+    for (int k = threadIdx.x; k < p.H / 8; k += 32 * kWarps) xs[k] = __ldg(x + k);
+    consumer_sync<kWarps>();
     for (int e0 = warp * 4; e0 < p.E; e0 += kWarps * 4) {
         float acc[4] = {};
-#pragma unroll 2
-        for (int k = lane * 8; k < p.H; k += 256) {
-            float f[8];
-            widen8(__ldg(reinterpret_cast<const uint4 *>(x + k)), XT, f);
-            uint4 w[4][2];
+        auto rows = [&](auto wide) {  // wide: an FP32 router, 16 bytes are 4 elements
+            constexpr bool kWide = decltype(wide)::value;
+            constexpr int kDeep = kWide ? 2 : 4, kParts = kWide ? 2 : 1;
+            for (int k0 = lane; k0 < p.H / 8; k0 += 32 * kDeep) {
+                uint4 w[kDeep][4][kParts];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int e = min(e0 + i, p.E - 1);
-                const uint4 *r = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.router) + (static_cast<long long>(e) * p.H + k) * esize);
-                w[i][0] = __ldg(r);
-                if (p.router_f32) w[i][1] = __ldg(r + 1);
-            }
+                for (int u = 0; u < kDeep; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[8];
-                if (p.router_f32) {
-                    v[0] = __uint_as_float(w[i][0].x), v[1] = __uint_as_float(w[i][0].y), v[2] = __uint_as_float(w[i][0].z);
-                    v[3] = __uint_as_float(w[i][0].w), v[4] = __uint_as_float(w[i][1].x), v[5] = __uint_as_float(w[i][1].y);
-                    v[6] = __uint_as_float(w[i][1].z), v[7] = __uint_as_float(w[i][1].w);
-                } else {
-                    widen8(w[i][0], XT, v);
+                    for (int i = 0; i < 4; ++i) {
+                        const int k = min(k0 + 32 * u, p.H / 8 - 1), e = min(e0 + i, p.E - 1);
+                        const uint4 *r = static_cast<const uint4 *>(p.router) + (static_cast<long long>(e) * (p.H / 8) + k) * kParts;
+#pragma unroll
+                        for (int h = 0; h < kParts; ++h) w[u][i][h] = __ldg(r + h);
+                    }
+#pragma unroll
+                for (int u = 0; u < kDeep; ++u) {
+                    if (k0 + 32 * u >= p.H / 8) break;
+                    float f[8];
+                    widen8(xs[k0 + 32 * u], XT, f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float v[8];
+                        if constexpr (kWide) {
+                            const uint4 a = w[u][i][0], b = w[u][i][kParts - 1];
+                            v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+                            v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+                        } else {
+                            widen8(w[u][i][0], XT, v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) acc[i] = fmaf(v[j], f[j], acc[i]);
+                    }
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[i] = fmaf(v[j], f[j], acc[i]);
             }
-        }
+        };
+        if (p.router_f32)
+            rows(std::true_type{});
+        else
+            rows(std::false_type{});
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -647,11 +663,11 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         // barrier every CTA makes the same choice.  Many: a CTA takes a token,
         // logits and choice, and the barrier is for the choices.
         uint32_t *keys = reinterpret_cast<uint32_t *>(ring);
-        const bool by_token = p.T >= kTokensOfTheirOwn;
+        const bool by_token = p.by_token;
         const int slots = p.T * p.top_k;
         if (by_token) {
             for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-                router_token<XT, kWarps>(p, t, keys);
+                router_token<XT, kWarps>(p, t, keys, reinterpret_cast<uint4 *>(ring + 4096));
                 consumer_sync<kWarps>();
                 if (warp == 0) choose_experts(p, keys, p.chosen + t * p.top_k, p.chosen_weight + t * p.top_k);
                 consumer_sync<kWarps>();
@@ -1084,10 +1100,12 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     const int act_bytes = std::min(m.T, 8 * NT) * std::max(Cfg::act_stride(a.lw1, true), Cfg::act_stride(a.lw2, false));
     a.stage_bytes = (Cfg::kActOffset + act_bytes + 1023) / 1024 * 1024;
     constexpr int kRing = 226 * 1024 - static_cast<int>(sizeof(Routing) + 2 * moe_warps(NT) * NT * 4 * 32 * 4 + 16 * kMaxStages + 128);
-    static_assert(kRing >= 1024 + kTokensOfTheirOwn * kMoeMaxExperts * 4, "the ring holds the keys of the choice");
+    static_assert(kRing >= 1024 + kTokensOfTheirOwn * kMoeMaxExperts * 4 && kRing >= 1024 + 4096 + kMoeMaxWidth * 2,
+                  "the ring holds the keys of the choice, or one token and its keys");
     a.stages = std::min(kMaxStages, (kRing - 1024) / a.stage_bytes);  // two at least: 2 x (32 + 32) KB and paddings
     const int wb = Cfg::kWBytes;
     const auto dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
+    a.by_token = m.T >= kTokensOfTheirOwn;
     a.flat_h = m.H * wb % 128 == 0;
     a.flat_i = m.I * wb % 128 == 0;
     CUtensorMap tg, tu, td;

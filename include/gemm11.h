@@ -352,7 +352,7 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  * weights), 21 (FP16 X) or 11 significant bits (BF16 X, 8-bit weights).  A
  * token with a NaN logit gets NaN weights, and so a NaN row.
  * Limits: 1 <= top_k <= min(E, 16), E <= 512, T <= 128, T * top_k <= 1024;
- * H and I multiples of 16, E * max(H, I) < 2^31; X, router, gate, up and down 16-byte aligned and
+ * H and I multiples of 16, H <= 32768, E * max(H, I) < 2^31; X, router, gate, up and down 16-byte aligned and
  * ldx a multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
  * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
  * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive

@@ -82,7 +82,7 @@ def test_moe_rejects(L, change):
 
 
 @pytest.mark.parametrize("change", [
-    dict(T=129), dict(E=513), dict(E=32, top_k=17), dict(T=128, top_k=16, E=64), dict(H=264, ldx=264, ldy=264), dict(I=120),
+    dict(T=129), dict(E=513), dict(E=32, top_k=17), dict(T=128, top_k=16, E=64), dict(H=264, ldx=264, ldy=264), dict(I=120), dict(H=32784, ldx=32784, ldy=32784),
     dict(X=FAKE + 2), dict(router=FAKE + 2), dict(gate=FAKE + 1), dict(up=FAKE + 1), dict(down=FAKE + 8), dict(ldx=257),
 ])
 def test_moe_does_not_support(L, change):
