@@ -1134,7 +1134,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
 
 template <int XT, bool FP8>
 cudaError_t launch_moe_tokens(const Moe &m, const MoeArgs &a, double active, double tokens, cudaStream_t stream) {
-    if (tokens <= 6.0) return launch_moe<XT, FP8, 1>(m, a, active, stream);
+    if (tokens <= 6.5) return launch_moe<XT, FP8, 1>(m, a, active, stream);
     if (tokens <= 12.0) return launch_moe<XT, FP8, 2>(m, a, active, stream);
     return launch_moe<XT, FP8, 4>(m, a, active, stream);
 }
