@@ -488,18 +488,28 @@ __device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], 
         return;
     }
     __syncwarp();
-    for (int r = 0; r < 32 && row + r < p.M; ++r) {
+    constexpr int kRowsAtOnce = 8;  // reads of so many rows before their stores
+    for (int r0 = 0; r0 < 32 && row + r0 < p.M; r0 += kRowsAtOnce) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int j = u * 32 + lane;
             if (j * esize >= 128 || first + j >= p.N) continue;
-            const size_t ci = static_cast<size_t>(row + r) * static_cast<size_t>(p.ldc) + first + j;
-            const uint8_t *at = staged + r * 128 + ((((j * esize) >> 4) ^ (r & 7)) << 4) + (j * esize & 15);
-            if (!debug_in_bounds(p.c_extent == 0 || ci < p.c_extent, p.err)) continue;
-            if (wide)
-                static_cast<float *>(p.C)[ci] = *reinterpret_cast<const float *>(at);
-            else
-                static_cast<uint16_t *>(p.C)[ci] = *reinterpret_cast<const uint16_t *>(at);
+            float w[kRowsAtOnce];
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) {
+                const uint8_t *at = staged + (r0 + k) * 128 + ((((j * esize) >> 4) ^ k) << 4) + (j * esize & 15);
+                w[k] = wide ? *reinterpret_cast<const float *>(at) : __uint_as_float(*reinterpret_cast<const uint16_t *>(at));
+            }
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) {
+                if (row + r0 + k >= p.M) break;
+                const size_t ci = static_cast<size_t>(row + r0 + k) * static_cast<size_t>(p.ldc) + first + j;
+                if (!debug_in_bounds(p.c_extent == 0 || ci < p.c_extent, p.err)) continue;
+                if (wide)
+                    static_cast<float *>(p.C)[ci] = w[k];
+                else
+                    static_cast<uint16_t *>(p.C)[ci] = static_cast<uint16_t>(__float_as_uint(w[k]));
+            }
         }
     }
     __syncwarp();

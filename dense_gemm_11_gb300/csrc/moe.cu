@@ -100,7 +100,7 @@ struct MoeArgs {
     int lw1, lw2;    // log2 of WR, the row groups (of 16 rows) of a unit, in the first half and in the down projection
     int k_splits;    // units of the down projection that share a row group's k
     int by_token;    // the routing takes a CTA for each token
-    int flat_h, flat_i;  // rows of H (I) elements are whole 128-byte boxes: one copy takes a stage's boxes
+    int flat_h, flat_i;  // elements of a row up to which one copy takes a stage's boxes (whole 128-byte ones)
     int stages, stage_bytes;
 };
 
@@ -608,6 +608,11 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
     }
 }
 
+// Of each matrix: boxes by the stage, and single boxes for a ragged end.
+struct MoeMaps {
+    CUtensorMap gate, up, down, gate1, up1, down1;
+};
+
 // Consumer warps: sixteen with one box each while their registers last (16
 // tokens), else eight with two boxes.
 constexpr int moe_warps(int nt) { return nt <= 2 ? 16 : 8; }
@@ -616,8 +621,7 @@ constexpr int moe_threads(int nt) { return 32 * (moe_warps(nt) + 1 + moe_token_w
 
 template <int XT, bool FP8, int NT>
 __global__ void __launch_bounds__(moe_threads(NT), 1)
-    moe_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
-               const __grid_constant__ CUtensorMap tm_down, const MoeArgs p) {
+    moe_kernel(const __grid_constant__ MoeMaps maps, const MoeArgs p) {
     using Cfg = MoeCfg<XT, FP8>;
     constexpr int kWarps = moe_warps(NT), kMine = kBoxes / kWarps;  // boxes of a warp in a stage
     constexpr int kTokenWarps = moe_token_warps(NT), kThreads = moe_threads(NT);
@@ -645,9 +649,9 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         }
         abort_flag = 0;
         fence_mbarrier_init();
-        tma_prefetch_desc(&tm_gate);
-        tma_prefetch_desc(&tm_up);
-        tma_prefetch_desc(&tm_down);
+        tma_prefetch_desc(&maps.gate);
+        tma_prefetch_desc(&maps.up);
+        tma_prefetch_desc(&maps.down);
     }
     __syncthreads();
 
@@ -739,24 +743,20 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
             uint8_t *dst = ring + stage * p.stage_bytes;
             const int lw = first ? p.lw1 : p.lw2, boxes = kBoxes >> lw, width = first ? p.H : p.I, k0 = ch * boxes * Cfg::kBoxK;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], kStageWeights);
-                if (first) {
-                    const int half = gated ? kStageWeights / 2 : 0;  // gate rows, then up rows
-                    if (p.flat_h) {
-                        tma_load_3d(&tm_gate, &full[stage], dst, 0, y, ch * boxes);
-                        if (half) tma_load_3d(&tm_up, &full[stage], dst + half, 0, y, ch * boxes);
-                    } else {
-                        for (int b = 0; b < boxes; ++b) {
-                            const int at = b * ((half ? 1024 : 2048) << lw);
-                            tma_load_3d(&tm_gate, &full[stage], dst + at, k0 + b * Cfg::kBoxK, y, 0);
-                            if (half) tma_load_3d(&tm_up, &full[stage], dst + half + at, k0 + b * Cfg::kBoxK, y, 0);
-                        }
-                    }
-                } else if (p.flat_i) {
-                    tma_load_3d(&tm_down, &full[stage], dst, 0, y, ch * boxes);
+                // Gate rows in the first half of the stage, up rows in the second.
+                const int half = first && gated ? kStageWeights / 2 : 0, box_bytes = (half ? 1024 : 2048) << lw;
+                if (k0 + boxes * Cfg::kBoxK <= (first ? p.flat_h : p.flat_i)) {
+                    mbar_arrive_expect_tx(&full[stage], kStageWeights);
+                    tma_load_3d(first ? &maps.gate : &maps.down, &full[stage], dst, 0, y, ch * boxes);
+                    if (half) tma_load_3d(&maps.up, &full[stage], dst + half, 0, y, ch * boxes);
                 } else {
-                    for (int b = 0; b < boxes; ++b)
-                        tma_load_3d(&tm_down, &full[stage], dst + b * (2048 << lw), k0 + b * Cfg::kBoxK, y, 0);
+                    // the row's end: the boxes that have any of it, one by one
+                    const int some = min(boxes, (width - k0 + Cfg::kBoxK - 1) / Cfg::kBoxK);
+                    mbar_arrive_expect_tx(&full[stage], some * box_bytes * (half ? 2 : 1));
+                    for (int b = 0; b < some; ++b) {
+                        tma_load_3d(first ? &maps.gate1 : &maps.down1, &full[stage], dst + b * box_bytes, k0 + b * Cfg::kBoxK, y, 0);
+                        if (half) tma_load_3d(&maps.up1, &full[stage], dst + half + b * box_bytes, k0 + b * Cfg::kBoxK, y, 0);
+                    }
                 }
             }
             __syncwarp();
@@ -1050,14 +1050,22 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
         p.counters[0] = p.counters[1] = p.counters[2] = p.counters[3] = p.counters[4] = 0u;
 }
 
-// Tensor map of E matrices of `rows` rows of `width` elements.  flat: a box is
-// `boxes` 128-byte pieces of `box_rows` rows (dimensions: piece, row, piece
-// number); else one piece, and the row's ragged end reads as zeros.
-bool encode_expert_map(CUtensorMap *map, const void *base, int elem_bytes, CUtensorMapDataType dt, uint64_t all_rows,
-                       uint64_t width, bool flat, uint32_t box_rows, uint32_t boxes) {
-    const uint64_t piece = 128 / elem_bytes;
-    return flat ? encode_box_map(map, dt, base, piece, all_rows, width / piece, width * elem_bytes, 128, piece, box_rows, boxes)
-                : encode_box_map(map, dt, base, width, all_rows, 1, width * elem_bytes, width * elem_bytes, piece, box_rows, 1);
+// Tensor maps of all experts' `rows` rows of `width` elements: `many` with boxes
+// of `boxes` 128-byte pieces of `box_rows` rows (dimensions: piece, row, number
+// of the whole piece), `one` with single pieces, where the row's ragged end reads
+// as zeros.  *flat: elements of a row that `many` reaches.  A map that no stage
+// takes is the other one again.
+bool encode_expert_maps(CUtensorMap *many, CUtensorMap *one, int *flat, const void *base, int elem_bytes, CUtensorMapDataType dt,
+                        uint64_t rows, uint64_t width, uint32_t box_rows, uint32_t boxes) {
+    const uint64_t piece = 128 / elem_bytes, whole = width / piece, stage = boxes * piece;
+    const bool use_many = whole >= boxes, use_one = !use_many || width % stage != 0;
+    *flat = use_many ? static_cast<int>(whole * piece) : 0;
+    bool ok = true;
+    if (use_many) ok = encode_box_map(many, dt, base, piece, rows, whole, width * elem_bytes, 128, piece, box_rows, boxes);
+    if (ok && use_one) ok = encode_box_map(one, dt, base, width, rows, 1, width * elem_bytes, width * elem_bytes, piece, box_rows, 1);
+    if (!use_many) *many = *one;
+    if (!use_one) *one = *many;
+    return ok;
 }
 
 // How a phase is cut into units: log2 of WR, and of the down projection also
@@ -1106,15 +1114,16 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     const int wb = Cfg::kWBytes;
     const auto dt = FP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16;
     a.by_token = m.T >= kTokensOfTheirOwn;
-    a.flat_h = m.H * wb % 128 == 0;
-    a.flat_i = m.I * wb % 128 == 0;
-    CUtensorMap tg, tu, td;
+    MoeMaps maps;
     const uint64_t rows_i = static_cast<uint64_t>(m.E) * m.I, rows_h = static_cast<uint64_t>(m.E) * m.H;
     const uint32_t rows1 = (m.up ? 8 : 16) << a.lw1, boxes1 = kBoxes >> a.lw1, rows2 = 16 << a.lw2, boxes2 = kBoxes >> a.lw2;
-    if (!encode_expert_map(&tg, m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
-        !encode_expert_map(&tu, m.up ? m.up : m.gate, wb, dt, rows_i, m.H, a.flat_h, rows1, boxes1) ||
-        !encode_expert_map(&td, m.down, wb, dt, rows_h, m.I, a.flat_i, rows2, boxes2))
-        return cudaErrorNotSupported;
+    bool ok = encode_expert_maps(&maps.gate, &maps.gate1, &a.flat_h, m.gate, wb, dt, rows_i, m.H, rows1, boxes1) &&
+              encode_expert_maps(&maps.down, &maps.down1, &a.flat_i, m.down, wb, dt, rows_h, m.I, rows2, boxes2);
+    if (ok && m.up)
+        ok = encode_expert_maps(&maps.up, &maps.up1, &a.flat_h, m.up, wb, dt, rows_i, m.H, rows1, boxes1);
+    else
+        maps.up = maps.up1 = maps.gate;  // not used
+    if (!ok) return cudaErrorNotSupported;
     static unsigned long long smem_set = 0;
     cudaError_t e = ensure_dynamic_smem(kern, kRing, smem_set);
     if (e != cudaSuccess) return e;
@@ -1128,7 +1137,7 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, tg, tu, td, a);
+    e = cudaLaunchKernelEx(&cfg, kern, maps, a);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
