@@ -706,7 +706,6 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             };
             take();
             tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
-            if (B_ROWS) tmem_ld<kStep>(t_row + (i & 1) * kPairN + kStep, r1);
             for (int kb = 0; kb < p.kb_total; ++kb) {
                 const uint32_t from = t_row + (i & 1) * kPairN, answer = release[i & 1];
                 float s0 = 1.f, s1 = 1.f;
@@ -727,26 +726,33 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                     // each step's scales are read during the step before
                     load_col_scales(fa, sbv);
                     tmem_wait_ld();
+                    tmem_ld<kStep>(from + 16, r1);
                     load_col_scales(fb, sbv + 16 * 4);
                     add_scaled(acc, 0, r0, ss0, fa);
+                    tmem_wait_ld();
                     tmem_ld<kStep>(from + 32, r0);
                     load_col_scales(fa, sbv + 32 * 4);
                     add_scaled(acc, 16, r1, ss0, fb);
-                    tmem_ld<kStep>(from + 48, r1);
                     tmem_wait_ld();
+                    tmem_ld<kStep>(from + 48, r1);
                     load_col_scales(fb, sbv + 48 * 4);
                     add_scaled(acc, 32, r0, ss0, fa);
+                    tmem_wait_ld();
                     tmem_ld<kStep>(from + 64, r0);
                     load_col_scales(fa, sbw + 64 * 4);
                     add_scaled(acc, 48, r1, ss0, fb);
-                    tmem_ld<kStep>(from + 80, r1);
                     tmem_wait_ld();
+                    tmem_ld<kStep>(from + 80, r1);
                     load_col_scales(fb, sbw + 80 * 4);
                     add_scaled(acc, 64, r0, ss0, fa);
+                    tmem_wait_ld();
                     tmem_ld<kStep>(from + 96, r0);
                     load_col_scales(fa, sbw + 96 * 4);
                     add_scaled(acc, 80, r1, ss0, fb);
+                    tmem_wait_ld();
                     tmem_ld<kStep>(from + 112, r1);
+                    load_col_scales(fb, sbw + 112 * 4);
+                    add_scaled(acc, 96, r0, ss0, fa);
                 } else {
                     tmem_wait_ld();
                     tmem_ld<kStep>(from + 32, r1);
@@ -763,10 +769,6 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(answer);
                 ++i;
-                if constexpr (B_ROWS) {
-                    load_col_scales(fb, sbw + 112 * 4);
-                    add_scaled(acc, 96, r0, ss0, fa);
-                }
                 const bool more = kb + 1 < p.kb_total;
                 if (more) {
                     take();
@@ -777,7 +779,6 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                     add_scaled(acc, 112, r1, ss0, fb);
                 else
                     add_scaled(acc, 96, r1, ss1);
-                if (B_ROWS && more) tmem_ld<kStep>(t_row + (i & 1) * kPairN + kStep, r1);
                 if (++slot == Cfg::kSlots) slot = 0;
             }
             tmem_wait_ld();
