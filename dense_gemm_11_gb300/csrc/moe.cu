@@ -14,12 +14,13 @@
 //     of its tokens.  A unit goes through its k in stages of 32 KB of weights:
 //     16 WR rows x 16 / WR boxes of 128 bytes, one TMA copy (two with a gate).
 //     Issuing a copy costs the producer about 100 cycles, so stages are large:
-//     with 16 KB it, not memory, set the pace (130 us against ??? at 1 token)
+//     with 16 KB it, not memory, set the pace (130 us against 116 at 1 token, 8
+//     experts of 4096 x 11008, 2 each)
 //   * one warp fills a ring of stages with weights.  It runs ahead of the
 //     arithmetic across units, and into the down projection while other CTAs
 //     still finish the first half.  One or two more bring the tokens' rows of
 //     the same k, a copy each (by the weights' warp, 6 of them a stage held the
-//     weights back: 136 us against ?? at 64 tokens, 64 experts);
+//     weights back: 138 us against 134 at 64 tokens, 64 experts);
 //   * sixteen warps take a stage's WR row groups x 16 / WR boxes, one each, and
 //     multiply their 16 rows x 128 bytes by the tokens with mma.sync; warps that
 //     share rows add their sums in warp order in shared memory at the unit's
