@@ -409,7 +409,26 @@ struct Fp8PairCfg {
 struct Fp8PairArgs {
     Fp8Args a;
     int tiles_m, tiles_n, c_tma;
+    // Units of work: `whole` tiles, then the k blocks of each remaining tile in
+    // `parts` units, whose sums fp8_join_kernel adds.
+    int units, whole, parts;
+    int part_blocks;     // of a unit but the tile's last
+    uint32_t per_tile;   // 65536 / parts, rounded up
+    float *partials;  // 256 x 256 sums of each such unit
 };
+
+// Unit t: its tile and its blocks of k (v is below 256, so that the product
+// divides it exactly).
+struct Fp8PairUnit {
+    int tile, kb0, blocks;
+};
+template <bool PARTS>
+__device__ __forceinline__ Fp8PairUnit fp8_pair_unit(const Fp8PairArgs &p, int t) {
+    if (!PARTS || t < p.whole) return {t, 0, p.a.kb_total};
+    const int v = t - p.whole, tile = static_cast<int>(static_cast<uint32_t>(v) * p.per_tile >> 16);
+    const int kb0 = (v - tile * p.parts) * p.part_blocks;
+    return {p.whole + tile, kb0, min(p.part_blocks, p.a.kb_total - kb0)};
+}
 
 // Tile t: groups of 8 pair rows, so that a wave of tiles shares its rows of A
 // and columns of op(B) in L2.
@@ -465,9 +484,8 @@ __device__ __forceinline__ void epilogue32(const Fp8Args &p, float (&v)[32], int
 // `second` is the upper half.  A full buffer goes out by a TMA store, or, where
 // the rows of C are not aligned for one, row by row with neighbouring lanes on
 // neighbouring elements.
-__device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], const CUtensorMap *tm_c, bool by_tma, uint8_t *staged,
-                                        int lane, int row, int n, int second) {
-    const bool wide = p.c_type == kOutF32;
+__device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], const CUtensorMap *tm_c, bool wide, bool by_tma, uint8_t *staged,
+                                        int lane, int row, int n, int n_end, int second) {
     if (wide || !second) {  // the buffer's last store has read it
         if (lane == 0) bulk_wait_read_all();
         __syncwarp();
@@ -490,7 +508,7 @@ __device__ __forceinline__ void stage32(const Fp8Args &p, const float (&v)[32], 
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-            if (first < p.N) tma_store_2d(tm_c, staged, first, row);
+            if (first < n_end) tma_store_2d(tm_c, staged, first, row);
             bulk_commit();
         }
         return;
@@ -541,11 +559,12 @@ __device__ __forceinline__ void load_col_scales(uint64_t (&f)[8], uint32_t at) {
         asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(f[2 * u]), "=l"(f[2 * u + 1]) : "r"(at + 16 * u));
 }
 
-template <bool B_ROWS>
+template <bool B_ROWS, bool PARTS>
 __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                     const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
-                    const __grid_constant__ CUtensorMap tm_c, const Fp8PairArgs pp) {
+                    const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_parts,
+                    const Fp8PairArgs pp) {
     using Cfg = Fp8PairCfg<B_ROWS>;
     const Fp8Args &p = pp.a;
     extern __shared__ uint8_t smem_raw[];
@@ -563,7 +582,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
     const bool leader = rank == 0;
-    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1, tiles = pp.tiles_m * pp.tiles_n;
+    const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(&full[s], 1);
@@ -600,11 +619,12 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         int stage = 0, slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
+        for (int t = cid; ok && t < pp.units && !*abort_flag; t += ncl) {
+            const Fp8PairUnit unit = fp8_pair_unit<PARTS>(pp, t);
             int m0, n0;
-            fp8_pair_origin(pp, t, m0, n0);
+            fp8_pair_origin(pp, unit.tile, m0, n0);
             const int my_m = m0 + static_cast<int>(rank) * 128, my_n = n0 + static_cast<int>(rank) * 128;
-            for (int kb = 0; kb < p.kb_total; ++kb) {
+            for (int kb = unit.kb0; kb < unit.kb0 + unit.blocks; ++kb) {
                 ok = __all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u, p.wait_ns));
                 if (!ok) {
                     fp8_timeout(abort_flag, p.err);
@@ -651,8 +671,9 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         int stage = 0, i = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
-            for (int kb = 0; kb < p.kb_total; ++kb, ++i) {
+        for (int t = cid; ok && t < pp.units && !*abort_flag; t += ncl) {
+            const int blocks = fp8_pair_unit<PARTS>(pp, t).blocks;
+            for (int kb = 0; kb < blocks; ++kb, ++i) {
                 const int buf = i & 1;
                 ok = __all_sync(0xffffffffu, mbar_wait_patient(&full[stage], phase, p.wait_ns) &&
                                                  mbar_wait_patient(&tempty[buf * 2 + h], ((i >> 1) & 1) ^ 1u, p.wait_ns));
@@ -684,20 +705,25 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         uint8_t *const staged = sC + (warp - 4) * 4096;
         int i = 0, slot = 0;
         bool ok = true;
-        for (int t = cid; ok && t < tiles && !*abort_flag; t += ncl) {
+        for (int t = cid; ok && t < pp.units && !*abort_flag; t += ncl) {
+            const Fp8PairUnit unit = fp8_pair_unit<PARTS>(pp, t);
+            // The shuffle keeps the compiler from carrying the unit's choice into
+            // the loop below (1,000 clocks a block without it, 815 with).
+            const int blocks = PARTS ? __shfl_sync(0xffffffffu, unit.blocks, 0) : p.kb_total;
             int m0, n0;
-            fp8_pair_origin(pp, t, m0, n0);
+            fp8_pair_origin(pp, unit.tile, m0, n0);
             // Columns col + j and col + 128 + j, j < 64.
-            const int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * 64;
+            int row = m0 + static_cast<int>(rank) * 128 + q * 32, col = n0 + part * 64;
             uint64_t acc[kPairCols / 2];  // pairs of columns
 #pragma unroll
             for (int j = 0; j < kPairCols / 2; ++j) acc[j] = 0;
             // B's scales of the two 128-column blocks: lane l has those of k
             // blocks l, l + 32, .., and the next 32 are on their way.
-            const float *sb0 = p.SB + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
-            const float *sb1 = p.SB + (B_ROWS ? 0 : min(col + 128, p.N - 1) / kScaleBlock * p.sb_n);
+            const float *sb = p.SB + unit.kb0 * p.sb_kb;
+            const float *sb0 = sb + (B_ROWS ? 0 : min(col, p.N - 1) / kScaleBlock * p.sb_n);
+            const float *sb1 = sb + (B_ROWS ? 0 : min(col + 128, p.N - 1) / kScaleBlock * p.sb_n);
             float lane0 = 1.f, lane1 = 1.f, next0 = 1.f, next1 = 1.f;
-            if (!B_ROWS && lane < p.kb_total) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
+            if (!B_ROWS && lane < blocks) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
             // While the sums of one read (32 columns, 16 with a scale for each
             // column) are added the next is on its way, over the end of a block
             // too.  A wait is for every read, so only one is in flight: with two
@@ -714,13 +740,13 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             };
             take();
             tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
-            for (int kb = 0; kb < p.kb_total; ++kb) {
+            for (int kb = 0; kb < blocks; ++kb) {
                 const uint32_t from = t_row + (i & 1) * kPairN, answer = release[i & 1];
                 float s0 = 1.f, s1 = 1.f;
                 if (!B_ROWS) {
                     if ((kb & 31) == 0) {
                         lane0 = next0, lane1 = next1;
-                        if (kb + 32 + lane < p.kb_total)
+                        if (kb + 32 + lane < blocks)
                             next0 = __ldg(sb0 + (kb + 32 + lane) * p.sb_kb), next1 = __ldg(sb1 + (kb + 32 + lane) * p.sb_kb);
                     }
                     s0 = __shfl_sync(0xffffffffu, lane0, kb & 31), s1 = __shfl_sync(0xffffffffu, lane1, kb & 31);
@@ -777,7 +803,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(answer);
                 ++i;
-                const bool more = kb + 1 < p.kb_total;
+                const bool more = kb + 1 < blocks;
                 if (more) {
                     take();
                     if (!ok) break;
@@ -791,7 +817,10 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             }
             tmem_wait_ld();
             if (!ok || row >= p.M) continue;
-            // The tile is done: 32 columns at a time to the epilogue and out.
+            // The unit is done: 32 columns at a time to the epilogue and out, or
+            // as they are to the partial sums.
+            const bool some = PARTS && t >= pp.whole;
+            if (some) row = (t - pp.whole) * 256 + static_cast<int>(rank) * 128 + q * 32, col = part * 64;
             const int m = row + lane;
 #pragma unroll
             for (int gr = 0; gr < kPairCols / 32; ++gr) {
@@ -799,8 +828,9 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) unpack_f32x2(acc[gr * 16 + j], v[2 * j], v[2 * j + 1]);
-                epilogue32(p, v, m, n, lane);
-                stage32(p, v, &tm_c, pp.c_tma, staged, lane, row, n, gr & 1);
+                if (!some) epilogue32(p, v, m, n, lane);
+                stage32(p, v, some ? &tm_parts : &tm_c, some || p.c_type == kOutF32, some || pp.c_tma, staged, lane, row, n,
+                        some ? kPairN : p.N, gr & 1);
             }
         }
         if (lane == 0) bulk_wait_all();
@@ -827,6 +857,27 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
     }
+}
+
+// The tiles whose k the pair kernel's units shared: the parts' sums added in the
+// order of k, and the epilogue.  Four columns a thread.
+__global__ void __launch_bounds__(256) fp8_join_kernel(const Fp8PairArgs pp) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int kPieces = 256 * kPairN / 4;  // of a tile
+    const int left = blockIdx.x / (kPieces / 256), at = blockIdx.x % (kPieces / 256) * 256 + threadIdx.x;
+    int m, n;
+    fp8_pair_origin(pp, pp.whole + left, m, n);
+    m += at / (kPairN / 4), n += at % (kPairN / 4) * 4;
+    if (m >= pp.a.M || n >= pp.a.N) return;
+    const float4 *from = reinterpret_cast<const float4 *>(pp.partials) + static_cast<size_t>(left) * pp.parts * kPieces + at;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int part = 0; part < pp.parts; ++part) {
+        const float4 w = __ldcg(from + static_cast<size_t>(part) * kPieces);
+        v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+    }
+    store4(pp.a, m, n, v);
 }
 
 // C = act(beta * C + bias), where there is no product.
@@ -971,10 +1022,37 @@ int pick_splits(int bn, int tiles, int blocks, int rows, int sms, double *time_u
     return best;
 }
 
-template <bool B_ROWS>
-cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, cudaStream_t stream) {
+// Pair tiles on `clusters`: whole waves, and what they leave over, whose tiles may
+// be cut into units along k (a second kernel adds them).  A block of k takes 0.44
+// us, 0.70 with a scale for each column; a cut the second launch and the way
+// through memory, 4.5 us where it is all there is, 12 after a wave (whose last
+// tiles run faster than a full wave, and whose end the next launch fills in
+// part), and 0.16 for each part.  Measured, whole tiles / cut: 2560 x 2048 x 8192
+// (80 tiles) 53.2 / 41.3 us, with a scale for each column 84.0 / 58.3; 1024 x
+// 1024 x 8192 (16) 20.4 in single-CTA tiles / 16.9, and 22.9 / 20.6; left whole
+// 4096 x 11008 x 4096 (688) 141.8 / 144.3, 4096 x 4096 x 4096 (256) 60.5 / 63.0,
+// and in single-CTA tiles 512 x 512 x 11008 (4) 13.2 / 14.3.
+struct PairPlan {
+    int left, parts;  // tiles to cut, units of each
+    double time_us;
+};
+PairPlan pair_plan(double tiles, int clusters, int blocks, bool b_rows) {
+    const double block_us = b_rows ? 0.70 : 0.44, waves = std::floor(tiles / clusters);
+    const int left = static_cast<int>(tiles - waves * clusters);
+    PairPlan best = {0, 1, left ? blocks * block_us : 0.0};
+    for (int s = 2; left && s <= blocks && s * left <= clusters; ++s) {
+        const int each = (blocks + s - 1) / s;
+        const double t = each * block_us + (waves > 0 ? 12.0 : 4.5) + 0.16 * s;
+        if (t < best.time_us) best = {left, (blocks + each - 1) / each, t};
+    }
+    best.time_us += 4.5 + waves * blocks * block_us;
+    return best;
+}
+
+template <bool B_ROWS, bool PARTS>
+cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, const PairPlan &plan, cudaStream_t stream, CallInfo *info) {
     using Cfg = Fp8PairCfg<B_ROWS>;
-    auto kern = fp8_pair_kernel<B_ROWS>;
+    auto kern = fp8_pair_kernel<B_ROWS, PARTS>;
     static int max_clusters = -1;  // one device type per process; atomic accesses
     static unsigned long long smem_set = 0;
     cudaError_t e = ensure_dynamic_smem(kern, Cfg::kSmemBytes, smem_set);
@@ -1021,9 +1099,32 @@ cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, cudaStream_t str
         __atomic_store_n(&max_clusters, clusters, __ATOMIC_RELEASE);
     }
     if (clusters < 1) return cudaErrorNotSupported;
-    cfg.gridDim = dim3(2 * std::min(clusters, args.tiles_m * args.tiles_n));
+    args.parts = plan.parts;
+    args.whole = args.tiles_m * args.tiles_n - plan.left;
+    args.part_blocks = (a.kb_total + args.parts - 1) / args.parts;
+    args.per_tile = (65536 + args.parts - 1) / args.parts;
+    args.units = args.whole + plan.left * args.parts;
+    CUtensorMap tp = ta;  // not used without parts
+    if (PARTS) {
+        const int rows = plan.left * args.parts * 256;
+        Scratch sc;
+        e = acquire_scratch(stream, static_cast<size_t>(rows) * kPairN, 0, &sc);
+        if (e != cudaSuccess) return e;
+        args.partials = sc.partials;
+        if (!encode_matrix_map(&tp, f32, sc.partials, kPairN, rows, kPairN * 4, 32, 32, sw)) return cudaErrorNotSupported;
+    }
+    cfg.gridDim = dim3(2 * std::min(clusters, args.units));
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, tc, args);
+    e = cudaLaunchKernelEx(&cfg, kern, ta, tb, tsa, tsb, tc, tp, args);
+    if (e == cudaSuccess) e = cudaPeekAtLastError();
+    if (e != cudaSuccess || !PARTS) return e;
+    info->launches = 2;
+    cfg.gridDim = dim3(plan.left * 64);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, fp8_join_kernel, args);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
@@ -1062,14 +1163,14 @@ cudaError_t run_fp8_gemm(const Fp8Gemm &g, cudaStream_t stream, CallInfo *info) 
     double t_tile = 0.0;
     a.splits = pick_splits(bn, static_cast<int>(std::min<long long>(tiles, 1 << 30)), a.kb_total, std::min(bn, g.M), sms, &t_tile);
     info->launches = 1;
-    // Pairs: 0.44 us a block and wave of tiles (0.70 with a scale for each
-    // column), against single tiles and their splits (pick_splits).
     const double pair_tiles = static_cast<double>((g.M + 255) / 256) * ((g.N + kPairN - 1) / kPairN);
-    const double t_pair = 4.5 + std::ceil(pair_tiles / (sms / 2)) * a.kb_total * (g.b_rows ? 0.70 : 0.44);
-    if (g.M > 128 && t_pair <= t_tile) {
-        info->plan = "fp8_pair_256x256";
-        a.splits = 1;
-        return g.b_rows ? launch_fp8_pair<true>(g, a, stream) : launch_fp8_pair<false>(g, a, stream);
+    const PairPlan pairs = pair_plan(pair_tiles, sms / 2, a.kb_total, g.b_rows);
+    if (g.M > 128 && pairs.time_us <= t_tile) {
+        info->plan = pairs.left ? "fp8_pair_256x256_splitk" : "fp8_pair_256x256";
+        a.splits = pairs.parts;
+        if (pairs.left)
+            return g.b_rows ? launch_fp8_pair<true, true>(g, a, pairs, stream, info) : launch_fp8_pair<false, true>(g, a, pairs, stream, info);
+        return g.b_rows ? launch_fp8_pair<true, false>(g, a, pairs, stream, info) : launch_fp8_pair<false, false>(g, a, pairs, stream, info);
     }
     switch (bn) {
         case 16: info->plan = "fp8_tile_n16"; return launch_fp8_tile<16, 5>(g, a, stream);

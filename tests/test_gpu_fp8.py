@@ -308,3 +308,41 @@ def test_refusals():
     with pytest.raises(g.GemmError) as e:
         g.gemm_fp8(odd, SA, B, SB, C)
     assert e.value.status == g.GEMM_ERR_UNSUPPORTED
+
+
+SPLIT = [(1024, 1024, 8192), (1000, 1010, 8100), (2560, 2040, 6100)]  # few tiles, with ragged ends, and a few after a whole wave
+
+
+@pytest.mark.parametrize("way", ["forward", "dgrad", "wgrad"])
+@pytest.mark.parametrize("M,N,K", SPLIT)
+def test_product_of_tiles_cut_along_k(way, M, N, K):
+    check_product(M, N, K, way, seed=M + N + K)
+    assert g.last_plan() == "fp8_pair_256x256_splitk" and g.last_launch_count() == 2
+
+
+@pytest.mark.parametrize("ct", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("act", [0, 1, 2, 3])
+def test_epilogue_of_tiles_cut_along_k(ct, act):
+    check_product(1000, 1010, 8100, "forward", ct, seed=act, alpha=0.7, beta=-0.5, bias=True, act=act, ld_pad=3)
+    assert g.last_plan() == "fp8_pair_256x256_splitk"
+
+
+@pytest.mark.parametrize("way", ["forward", "wgrad"])
+def test_tiles_cut_along_k_repeat_bitwise_and_in_a_graph(way):
+    M, N, K = 1024, 1024, 8192
+    A, SA, B, SB, kw = operands(M, N, K, way, seed=5)
+    C = [torch.empty(M, N, device="cuda") for _ in range(4)]
+    g.gemm_fp8(A, SA, B, SB, C[0], **kw)
+    g.gemm_fp8(A, SA, B, SB, C[1], **kw)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            g.gemm_fp8(A, SA, B, SB, C[2], **kw)
+            g.gemm_fp8(A, SA, B, SB, C[3], **kw)
+        for _ in range(2):
+            graph.replay()
+    torch.cuda.synchronize()
+    assert g.check() == g.GEMM_OK
+    assert all(torch.equal(C[0], c) for c in C[1:])
