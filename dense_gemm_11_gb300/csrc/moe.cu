@@ -30,8 +30,9 @@
 //     be any permutation that both operands share, so that a thread's k's are
 //     neighbours, one 16-byte load).
 // Few row groups (WR = 1) make many small units, which spread evenly over the
-// SMs; many (WR = 8) read a token's activations once for 128 rows and leave no
-// sums to add.  The host takes the largest WR whose units still spread well.
+// SMs; many (WR = 16) read a token's activations once for 256 rows and leave no
+// sums to add and no warp to wait for.  The host takes the largest WR whose
+// units still spread well.
 // Between the phases (router, first half, down projection, sum over a token's
 // experts) CTAs meet at grid barriers; every sum has a fixed order, so results
 // do not depend on timing.  Every wait is bounded.
@@ -1058,24 +1059,29 @@ bool encode_expert_maps(CUtensorMap *many, CUtensorMap *one, int *flat, const vo
 // how many units share a row group's k.  `groups` row groups of 16 (one of each
 // expert that is used), `k` long; `act_bytes` of activations in a stage with
 // WR = 1.  Preferred is the largest WR, then the fewest splits, whose units
-// fill whole rounds over the SMs to 90 %; failing that, what fills them best.
+// fill whole rounds over the SMs to 80 %; failing that, what fills them best.
+// (64 tokens, 64 experts of 2048 x 1024, 6 each: 111.7 us with WR = 16 at 84 %,
+// 117.9 with the best 90 % filling; 52 tokens, 23 experts of 352 x 880, 7 each:
+// 43.6 against 50.5; at 70 % one token over 8 experts took 122 us, 117 at 80 %.)
 // WR is at least what keeps a stage's activations within its weights (the ring
-// would hold too few stages) and a stage's k below the whole length.
+// would hold too few stages) and a stage's k below the whole length; 16 only
+// where a unit of 8 would have fewer than 12 stages, over which to hide its end.
 struct Cut {
     int lw = 0, splits = 1;
 };
 Cut pick_cut(double groups, int k, int box_k, int act_bytes, int max_splits, int sms) {
     int least = 0;
-    while (least < 3 && ((act_bytes >> least) > kStageWeights || (kBoxes >> least) * box_k >= 2 * k)) ++least;
+    while (least < 4 && ((act_bytes >> least) > kStageWeights || (kBoxes >> least) * box_k >= 2 * k)) ++least;
     Cut best;
     double best_fill = -1.0;
-    for (int lw = 3; lw >= least; --lw)
+    const int most = k < 12 * (kBoxes >> 3) * box_k ? 4 : 3;
+    for (int lw = std::max(most, least); lw >= least; --lw)
         for (int splits = 1; splits <= max_splits; splits *= 2) {
             if (splits > 1 && (kBoxes >> lw) * box_k * splits * 2 > k) break;  // two stages at least
             const double units = std::max(1.0, groups / (1 << lw) * splits);
             const double fill = units / (std::ceil(units / sms - 1e-9) * sms);
             if (fill > best_fill + 1e-9) best_fill = fill, best.lw = lw, best.splits = splits;
-            if (fill >= 0.9) return best;
+            if (fill >= 0.8) return best;
         }
     return best;
 }
