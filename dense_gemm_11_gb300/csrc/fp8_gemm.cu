@@ -11,7 +11,7 @@
 // accumulators in tensor memory alternate: while the warps take one block's
 // sums out, the tensor core forms the next.
 //
-// Two kernels:
+// Two kernels, and a small one after the second:
 //   fp8_tile_kernel   one CTA a tile, computed transposed, C^T = op(B)^T A^T:
 //                     128 columns n of C on the MMA's row side (tensor-memory
 //                     lanes), BN rows m on its column side, so that a few rows
@@ -22,7 +22,8 @@
 //                     16 x 11008 x 4096 11.2 us, 4.1 TB/s, 64 rows 13.5 us;
 //   fp8_pair_kernel   two CTAs (tcgen05 cta_group::2) a tile of 256 x 256,
 //                     persistent, for many rows: 4096 x 11008 x 4096 142 us,
-//                     2.6 PFLOP/s, its figures at the kernel.
+//                     2.6 PFLOP/s, its figures at the kernel.  Tiles that would
+//                     leave most SMs idle are cut along k; fp8_join_kernel adds.
 //
 // Roles of a CTA: warp 0 issues the TMA loads (operand tiles with the 128-byte
 // swizzle, and the BN scales of A for the block), warp 1 the MMAs, the others

@@ -323,6 +323,8 @@ GEMM11_API int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int
  * multiples of 16 (bytes), ldsa a multiple of 4, and for GEMM_FP8_ROWS of B
  * the same of SB and ldsb (leading dimensions of a single row excepted);
  * anything else returns GEMM_ERR_UNSUPPORTED.  M, N and K are unrestricted.
+ * Scratch: for few tiles of 256 x 256 and a long K up to 20 MB (plan
+ * "fp8_pair_256x256_splitk"), under stream capture as in gemm_moe_few_tokens.
  */
 GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_type, long long lda,
                                  const float *SA, long long ldsa, const void *B, int b_type, long long ldb,
