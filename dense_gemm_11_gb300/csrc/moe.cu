@@ -39,20 +39,21 @@
 //
 // Numbers.  Every product is a 16-bit x 16-bit mma.sync with FP32 sums; what
 // the activations are held in depends on the types:
-//   BF16 weights   X as it is; h as the sum of two BF16 numbers (16 significant
-//                  bits, FP32's range), two products each;
-//   FP16 weights   X as it is; h as the sum of two FP16 numbers (21 bits);
+//   BF16 weights   X as it is; h as the sum of three BF16 numbers, all of its
+//                  FP32 bits, three products each;
+//   FP16 weights   X as it is; h as the sum of two FP16 numbers (22 bits);
 //   e4m3 weights   widened to FP16 (exact), one conversion for two elements
 //                  (TF32 products took two more each, and twice the matrix
 //                  instructions: 165 us against 149 at 16 tokens, 32 experts).
-//                  An FP16 X as it is with h in two parts; a BF16 X in FP16
+//                  h as with FP16 weights.  An FP16 X as it is; a BF16 X in FP16
 //                  after scaling a token by the power of two that brings its
 //                  largest element to [2^14, 2^15) (its 8 bits are exact down to
-//                  2^-31 of that), and h in one FP16 number: 11 bits, under a
-//                  result that is usually rounded to BF16's 8.
+//                  2^-31 of that).
+// h in one 16-bit number would leave an FP32 Y with 11 or 8 bits, and a BF16 Y
+// with last bits that differ from those of FP32 sums in a tenth of its elements.
 // Where h is held in FP16 it is written in FP32 too.  If some slot's largest
-// |h| turns out to be outside [2^-4, 65504] (inside, what FP16 drops is 2^-20 of
-// the largest at most), all are fitted as a BF16 X is, between two grid barriers
+// |h| turns out to be outside [2^-4, 65504] (inside, what two numbers drop is
+// 2^-21 of the largest at most), all are fitted as a BF16 X is, between two grid barriers
 // (3 us), else nothing is.  The e4m3 scale of a 128 x 128 block multiplies that
 // block's FP32 sum.
 #include <algorithm>
@@ -88,8 +89,8 @@ struct MoeArgs {
     int y_type, act, renorm;
     int *ids;
     float *weights;
-    // Scratch: T x E logits; h in FP32 (slots x I) and in 16 bits, one number or
-    // two, these in alternate runs of 64; X in FP16, scaled; the largest |h| of
+    // Scratch: T x E logits; h in FP32 (slots x I) and as 16-bit numbers, two or
+    // three, these in runs of 64 by turns; X in FP16, scaled; the largest |h| of
     // a slot, and the scale of a token; k_splits x slots x H partial results.
     float *logits, *hidden, *part;
     uint8_t *hidden16;
@@ -167,6 +168,9 @@ __device__ __forceinline__ bool wait_count(const unsigned *c, unsigned want) {
     }
 }
 
+// SiLU by the approximate exponential and reciprocal: each is within 2^-22 of
+// its value, and v log2(e) is rounded to FP32 before, so the result is within
+// (4 + |v| / 2) 2^-23 of its value, below what the FP32 sums v comes from err by.
 __device__ __forceinline__ float moe_act(int act, float v) {
     return act == kActSilu ? v * rcp_approx(1.f + __expf(-v)) : apply_activation(act, v);
 }
@@ -188,17 +192,23 @@ __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
                  : "r"(addr)
                  : "memory");
 }
-// h as hi + lo, each of 16 bits.  An infinity has no remainder.
-template <int TYPE>
-__device__ __forceinline__ void two_parts(float h, uint16_t &hi, uint16_t &lo) {
-    if constexpr (TYPE == kOutF16) {
-        const __half a = __float2half_rn(h);
-        hi = __half_as_ushort(a);
-        lo = __half_as_ushort(__float2half_rn(fabsf(h) < INFINITY ? h - __half2float(a) : 0.f));
-    } else {
-        const __nv_bfloat16 a = __float2bfloat16_rn(h);
-        hi = __bfloat16_as_ushort(a);
-        lo = __bfloat16_as_ushort(__float2bfloat16_rn(fabsf(h) < INFINITY ? h - __bfloat162float(a) : 0.f));
+// h as a sum of N 16-bit numbers, each the rest of the one before it.  One that
+// overflows to infinity leaves no rest.
+template <int TYPE, int N>
+__device__ __forceinline__ void split_parts(float h, uint16_t (&part)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        float back;
+        if constexpr (TYPE == kOutF16) {
+            const __half a = __float2half_rn(h);
+            part[i] = __half_as_ushort(a);
+            back = __half2float(a);
+        } else {
+            const __nv_bfloat16 a = __float2bfloat16_rn(h);
+            part[i] = __bfloat16_as_ushort(a);
+            back = __bfloat162float(a);
+        }
+        h = fabsf(back) < INFINITY ? h - back : 0.f;
     }
 }
 // 2^e that brings a largest magnitude into [2^14, 2^15), and 2^-e.  Normal
@@ -495,8 +505,8 @@ __device__ __forceinline__ bool slots_fit(const MoeArgs &p) {
 }
 
 // ---------------------------------------------------------------- units
-// Bytes of a slot's h as two 16-bit parts.
-__host__ __device__ constexpr long long parts_bytes(int I) { return (I + 63ll) / 64 * 256; }
+// Bytes of a slot's h as `parts` 16-bit numbers an element.
+__host__ __device__ constexpr long long parts_bytes(int I, int parts) { return (I + 63ll) / 64 * 128 * parts; }
 
 struct Unit {
     int expert, row, start, count;  // first matrix row (of the expert), first slot in `order`, tokens
@@ -538,10 +548,10 @@ struct MoeCfg {
     static constexpr int kWBytes = FP8 ? 1 : 2;
     static constexpr int kBoxK = 128 / kWBytes;  // k of a box: 128 (one scale block) or 64
     static constexpr bool kFit = FP8 || XT == kOutF16;         // h in FP16
-    static constexpr bool kTwoParts = !FP8 || XT == kOutF16;   // h as two numbers
+    static constexpr int kParts = kFit ? 2 : 3;                // numbers that h is the sum of
     static constexpr bool kScaledX = FP8 && XT == kOutBF16;    // X as scaled FP16
     static constexpr int kMma = FP8 ? kOutF16 : XT;
-    static constexpr int kXBytes = 2, kHBytes = kTwoParts ? 4 : 2;
+    static constexpr int kXBytes = 2, kHBytes = 2 * kParts;
     static constexpr int kScaleBytes = FP8 ? kBoxes * 2 * 4 : 0;
     static constexpr int kActOffset = kStageWeights + kScaleBytes;
     // Row strides of the activations: the 8 threads of a quarter warp (16 of
@@ -556,10 +566,10 @@ struct MoeCfg {
 // (g, t) holds rows g and g + 8, token 8 n + g and the same k's of both; w0 and
 // w1 are the first of each 8 rows (16-byte chunk c of row g at c ^ g, by the
 // copy's swizzle), act[n] its token's k's of this box; USED of the NT groups of
-// 8 tokens exist.  PARTS: activations are sums of
-// two numbers, 64 k's of the second 128 bytes after the first's.  TAIL: only `valid` k's exist; the
+// 8 tokens exist.  PARTS: activations are sums of so many numbers, 64 k's of
+// the next one 128 bytes after those of the one before.  TAIL: only `valid` k's exist; the
 // weights past them are zeros, the activations are left over from other stages.
-template <int XT, bool FP8, int NT, int USED, bool PARTS, bool TAIL>
+template <int XT, bool FP8, int NT, int USED, int PARTS, bool TAIL>
 __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w1, const uint8_t *const (&act)[NT], int valid,
                                              float (&c)[NT][4]) {
     using Cfg = MoeCfg<XT, FP8>;
@@ -577,9 +587,9 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
                 widen_e4m3(w[2 * h], a0, a2);
                 widen_e4m3(w[2 * h + 1], a1, a3);
                 const int k = (ch + h) * 16 + t * 4;
-                const int at = PARTS ? (ch / 4) * 256 + ((ch + h) % 4 * 16 + t * 4) * 2 : k * 2;
+                const int at = (ch / 4) * (128 * PARTS) + ((ch + h) % 4 * 16 + t * 4) * 2;
 #pragma unroll
-                for (int part = 0; part < (PARTS ? 2 : 1); ++part)
+                for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                     for (int n = 0; n < USED; ++n) {
                         uint2 x = *reinterpret_cast<const uint2 *>(act[n] + at + part * 128);
@@ -595,7 +605,7 @@ __device__ __forceinline__ void multiply_box(const uint8_t *w0, const uint8_t *w
             const uint4 a = *reinterpret_cast<const uint4 *>(w0 + g * 128 + ((chunk ^ g) << 4));
             const uint4 b = *reinterpret_cast<const uint4 *>(w1 + g * 128 + ((chunk ^ g) << 4));
 #pragma unroll
-            for (int part = 0; part < (PARTS ? 2 : 1); ++part)
+            for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                 for (int n = 0; n < USED; ++n) {
                     uint4 x = *reinterpret_cast<const uint4 *>(act[n] + part * 128 + chunk * 16);
@@ -799,7 +809,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                     token = Cfg::kScaledX ? reinterpret_cast<const uint8_t *>(p.x16 + static_cast<long long>(t) * p.H)
                                           : static_cast<const uint8_t *>(p.X) + 2 * (t * p.ldx);
                 else
-                    token = p.hidden16 + slot * (Cfg::kTwoParts ? parts_bytes(p.I) : 2ll * p.I);
+                    token = p.hidden16 + slot * parts_bytes(p.I, Cfg::kParts);
             }
             for (int ch = n.ch0; ok && ch < n.ch1; ++ch) {
                 if (!__all_sync(0xffffffffu, mbar_wait_patient(&empty[stage], phase ^ 1u))) {
@@ -807,9 +817,9 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                     ok = false;
                     break;
                 }
-                // Bytes of a token's k's (two parts come in whole runs of 64).
+                // Bytes of a token's k's (those of h come in whole runs of 64).
                 const int k0 = ch * kc, k = min(kc, width - k0);
-                const int bytes = first ? k * Cfg::kXBytes : Cfg::kTwoParts ? (k + 63) / 64 * 256 : k * Cfg::kHBytes;
+                const int bytes = first ? k * Cfg::kXBytes : static_cast<int>(parts_bytes(k, Cfg::kParts));
                 if (lane == 0) mbar_arrive_expect_tx(&full[stage], count * bytes);
                 __syncwarp();
                 if (lane < count)
@@ -838,7 +848,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
             const bool halves = kFirst && gated;
             const int w_box = halves ? 1024 : 2048, row8 = halves ? kStageWeights / 2 : 1024;
             const int width = kFirst ? p.H : p.I;
-            constexpr bool kParts = !kFirst && Cfg::kTwoParts;
+            constexpr int kParts = kFirst ? 1 : Cfg::kParts;
             constexpr int kBoxBytes = Cfg::kBoxK * (kFirst ? Cfg::kXBytes : Cfg::kHBytes);  // of a token's k's of a box
             // Token of this thread in each group of 8 (past the last: the last one, whose sums nobody takes).
             int token_at[NT];
@@ -932,15 +942,11 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                         float h = moe_act(p.act, acc[nt][j + 2 * half] * xs);
                         if (gated) h *= acc[nt][j + 2] * xs;
                         if (!in || at >= p.I) continue;
-                        if constexpr (Cfg::kTwoParts) {
-                            uint16_t *to = reinterpret_cast<uint16_t *>(p.hidden16 + slot * parts_bytes(p.I)) + at / 64 * 128 + at % 64;
-                            uint16_t hi, lo;
-                            two_parts<Cfg::kMma>(h, hi, lo);
-                            to[0] = hi;
-                            to[64] = lo;
-                        } else {
-                            reinterpret_cast<__half *>(p.hidden16)[static_cast<long long>(slot) * p.I + at] = __float2half_rn(h);
-                        }
+                        uint16_t part[Cfg::kParts];
+                        split_parts<Cfg::kMma>(h, part);
+                        uint16_t *to = reinterpret_cast<uint16_t *>(p.hidden16 + slot * parts_bytes(p.I, Cfg::kParts)) + at / 64 * (64 * Cfg::kParts) + at % 64;
+#pragma unroll
+                        for (int i = 0; i < Cfg::kParts; ++i) to[64 * i] = part[i];
                         if constexpr (Cfg::kFit) {
                             p.hidden[static_cast<long long>(slot) * p.I + at] = h;
                             if (fabsf(h) < INFINITY) largest = fmaxf(largest, fabsf(h));
@@ -970,18 +976,15 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                 const float4 *h = reinterpret_cast<const float4 *>(p.hidden) + 2ll * x;
                 const float4 a = __ldcg(h), b = __ldcg(h + 1);
                 const float v[8] = {a.x * f, a.y * f, a.z * f, a.w * f, b.x * f, b.y * f, b.z * f, b.w * f};
-                if constexpr (Cfg::kTwoParts) {
-                    const int at = x % per * 8;
-                    uint16_t hi[8], lo[8];
+                const int at = x % per * 8;
+                uint16_t part[8][Cfg::kParts];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) two_parts<Cfg::kMma>(v[i], hi[i], lo[i]);
-                    uint8_t *to = p.hidden16 + x / per * parts_bytes(p.I) + at / 64 * 256 + at % 64 * 2;
-                    auto two = [](const uint16_t *u) { return u[0] | static_cast<uint32_t>(u[1]) << 16; };
-                    *reinterpret_cast<uint4 *>(to) = make_uint4(two(hi), two(hi + 2), two(hi + 4), two(hi + 6));
-                    *reinterpret_cast<uint4 *>(to + 128) = make_uint4(two(lo), two(lo + 2), two(lo + 4), two(lo + 6));
-                } else {
-                    reinterpret_cast<uint4 *>(p.hidden16)[x] = make_uint4(pack2_out16(v[0], v[1], kOutF16), pack2_out16(v[2], v[3], kOutF16),
-                                                                          pack2_out16(v[4], v[5], kOutF16), pack2_out16(v[6], v[7], kOutF16));
+                for (int i = 0; i < 8; ++i) split_parts<Cfg::kMma>(v[i], part[i]);
+                uint8_t *to = p.hidden16 + x / per * parts_bytes(p.I, Cfg::kParts) + at / 64 * (128 * Cfg::kParts) + at % 64 * 2;
+#pragma unroll
+                for (int j = 0; j < Cfg::kParts; ++j) {
+                    auto two = [&](int i) { return part[i][j] | static_cast<uint32_t>(part[i + 1][j]) << 16; };
+                    *reinterpret_cast<uint4 *>(to + 128 * j) = make_uint4(two(0), two(2), two(4), two(6));
                 }
             }
             fence_proxy_async_all();  // read by bulk copies
@@ -1175,7 +1178,7 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     auto up64 = [](size_t n) { return (n + 63) / 64 * 64; };
     const size_t n_slots = static_cast<size_t>(m.T) * m.top_k;
     const size_t n_logits = up64(static_cast<size_t>(m.T) * m.E), n_hidden = up64(n_slots * m.I);
-    const size_t n_h16 = up64(n_slots * parts_bytes(m.I) / 4), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
+    const size_t n_h16 = up64(n_slots * parts_bytes(m.I, 3) / 4), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
     Scratch s;
     const cudaError_t e =
         acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + 3 * n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);

@@ -350,15 +350,15 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  *   act     any gemm_act.
  *   ids     T x top_k int, weights T x top_k float: the choice and the w_j in
  *           the order of the logits; either may be NULL.
- * Sums, the softmax and the logits are FP32; h is rounded once, to 16 (BF16
- * weights), 21 (FP16 X) or 11 significant bits (BF16 X, 8-bit weights).  A
- * token with a NaN logit gets NaN weights, and so a NaN row.
+ * Sums, the softmax and the logits are FP32; h keeps all 24 bits of its FP32
+ * value with BF16 weights and 22 with FP16 or 8-bit weights.  A token with a
+ * NaN logit gets NaN weights, and so a NaN row.
  * Limits: 1 <= top_k <= min(E, 16), E <= 512, T <= 128, T * top_k <= 1024;
  * H and I multiples of 16, H <= 32768, E * max(H, I) < 2^31; X, router, gate, up and down 16-byte aligned and
  * ldx a multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
  * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
  * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive
- * otherwise.  Scratch: about T E + T H / 2 + T top_k (4 H + 2 I) floats of library-owned device
+ * otherwise.  Scratch: about T E + T H / 2 + T top_k (4 H + 5 I / 2) floats of library-owned device
  * memory per stream.  A call under stream capture may allocate it, and a graph
  * keeps the scratch it was captured with: replays of it must not overlap on
  * the GPU with each other or with calls on the stream that it was captured on.
