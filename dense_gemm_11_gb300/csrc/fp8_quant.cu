@@ -1,12 +1,13 @@
 // fp8_quant.cu -- FP32 / FP16 / BF16 matrices to 8-bit floating point with one
 // FP32 scale for each block of 128.
 //
-// A block's scale is s = a / F with a = max(max |x|, 2^-117) and F the 8-bit
+// A block's scale is s = a / F with a = max(max |x|, floor) and F the 8-bit
 // type's largest value (448 for e4m3, 57344 for e5m2); an element becomes
 // q = round8(x * (F / a)), one IEEE division for the block and one FP32
-// multiplication for the element, to nearest even.  The floor 2^-117 keeps
-// both quotients normal numbers (s >= 2^-126, F / a < 2^117 * 2^16), so that a
-// block of zeros needs no case of its own.  |x| (F / a) exceeds F by at most
+// multiplication for the element, to nearest even.  The floor, F 2^-126 rounded
+// up to a power of two (2^-117 and 2^-110), keeps both quotients normal numbers
+// (s = 2^-126 / 0.875 and F / a = 1.75 * 2^125 at the floor), so that a block of
+// zeros needs no case of its own.  |x| (F / a) exceeds F by at most
 // an ulp, which rounds to F.  A NaN becomes the NaN code and leaves the rest
 // of its block alone (fmaxf skips it); an infinity makes its block's scale
 // infinite and with it every product of the block NaN or infinite.
@@ -34,7 +35,6 @@
 namespace gemm11 {
 namespace {
 
-constexpr float kTinyMax = 6.018531076210112e-36f;  // 2^-117
 
 struct QuantArgs {
     const void *X;
@@ -111,6 +111,7 @@ __device__ __forceinline__ float max8(const Eight<XT> &x) {
 }
 
 __device__ __forceinline__ float type_max(int e5m2) { return e5m2 ? 57344.f : 448.f; }
+__device__ __forceinline__ float type_floor(int e5m2) { return e5m2 ? 0x1p-110f : 0x1p-117f; }
 
 // Four values, scaled and rounded, as packed bytes (the first lowest).
 __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d, int e5m2) {
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
             float m = max8(v[u]);
 #pragma unroll
             for (int d = 8; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            m = fmaxf(m, kTinyMax);
+            m = fmaxf(m, type_floor(p.e5m2));
             const float top = type_max(p.e5m2);
             if (live && b + u < b1) {
                 store8(p, row, (b + u) * kScaleBlock + sub * 8, v[u], top / m);
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(256, 3) quant_blocks_kernel(const QuantArgs p)
     for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
     __syncthreads();
-    m = kTinyMax;
+    m = type_floor(p.e5m2);
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
     const float top = type_max(p.e5m2), inv = top / m;
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(256, 6) quant_cols_kernel(const QuantArgs p) {
     __syncthreads();
     const float top = type_max(p.e5m2);
     if (threadIdx.x < 64) {
-        float a = kTinyMax;
+        float a = type_floor(p.e5m2);
 #pragma unroll
         for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w][threadIdx.x]);
         part[0][threadIdx.x] = top / a;

@@ -287,9 +287,11 @@ typedef enum {
  * gemm_fp8_quantize_block128 -- X (rows x cols, row-major, ldx elements a row,
  * FP32, FP16 or BF16) to 8 bits (q_type GEMM_DTYPE_E4M3 or GEMM_DTYPE_E5M2)
  * with scales, in one of the layouts above.  For each block, with
- * F = 448 (e4m3) or 57344 (e5m2):
- *   a = max(max |x|, 2^-117),   s = a / F,   q = round8(x * (F / a)),
- * every operation in FP32 rounded to nearest, round8 to nearest even.  A NaN
+ * F = 448 and f = 2^-117 (e4m3) or F = 57344 and f = 2^-110 (e5m2):
+ *   a = max(max |x|, f),   s = a / F,   q = round8(x * (F / a)),
+ * every operation in FP32 rounded to nearest, round8 to nearest even.  Below f
+ * the scale stays (s and F / a remain normal numbers), and a block of zeros has
+ * q = 0.  A NaN
  * becomes a NaN code and does not count in the maximum; an infinity makes the
  * scale of its block infinite, so every value of the block reads back as NaN
  * or infinity.
