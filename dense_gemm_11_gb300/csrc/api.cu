@@ -7,8 +7,10 @@
 #include <cstdio>
 #include <cstdlib>
 #include <map>
+#include <memory>
 #include <mutex>
 #include <utility>
+#include <vector>
 
 #include "../../include/gemm11.h"
 #include "fp8.h"
@@ -77,17 +79,30 @@ struct DeviceState {
 };
 DeviceState g_dev[kMaxDevices];
 
+// The buffers of one stream.
+struct ScratchBuffer {
+    void *at = nullptr;
+    size_t bytes = 0;
+};
 struct ScratchEntry {
-    float *partials = nullptr;
-    size_t partial_floats = 0;
-    unsigned *counters = nullptr;
-    size_t ncounters = 0;
-    float *operands = nullptr;
-    size_t operand_floats = 0;
-    bool captured = false;  // a CUDA graph holds the addresses of partials and counters
+    ScratchBuffer partials, counters, operands;
+};
+// The buffers of one stream capture.  The graph that it makes holds their
+// addresses, so they belong to that graph: no call outside the capture and no
+// other graph gets them, and they live until the graph and its instances are
+// destroyed, which `gone` says (set by the graph's user object; the memory is
+// freed at a later call, since a destructor of one may not call CUDA).
+struct CaptureScratch {
+    int dev = 0;
+    std::map<uintptr_t, ScratchEntry> streams;             // of each stream that takes part: its branches may overlap
+    std::vector<std::pair<ScratchBuffer, bool>> buffers;   // all, outgrown ones too; whether counters
+    std::atomic<bool> gone{false};
 };
 std::mutex g_scratch_mu;
 std::map<std::pair<int, uintptr_t>, ScratchEntry> g_scratch;
+// By capture id.  Never destroyed: a graph may outlive the library's statics.
+std::map<unsigned long long, std::unique_ptr<CaptureScratch>> &g_captures = *new std::map<unsigned long long, std::unique_ptr<CaptureScratch>>;
+std::atomic<int> g_captures_gone{0};
 
 // Library scratch allocation: plain cudaMalloc in release builds; debug
 // builds put a filled guard band of kCanaryBytes on both sides and hand out
@@ -159,97 +174,161 @@ unsigned *watchdog_word() {
 
 namespace {
 
-// While `stream` is being captured nothing may wait for it, and allocations
-// need the relaxed capture mode; the new buffer is cleared (bytes > 0) on a
-// stream of its own, outside the graph.
-cudaError_t scratch_alloc_capturing(void **user, size_t bytes, size_t clear) {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    cudaError_t e = cudaThreadExchangeStreamCaptureMode(&mode);
-    if (e != cudaSuccess) return e;
-    cudaStream_t side = nullptr;
-    e = scratch_alloc(user, bytes);
-    if (e == cudaSuccess && clear) {
-        e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
-        if (e == cudaSuccess) e = cudaMemsetAsync(*user, 0, clear, side);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(side);
-        if (side) cudaStreamDestroy(side);
+// While a stream is being captured allocations need the relaxed capture mode.
+class RelaxedCapture {
+  public:
+    RelaxedCapture() { error_ = cudaThreadExchangeStreamCaptureMode(&mode_); }
+    ~RelaxedCapture() {
+        if (error_ == cudaSuccess) (void)cudaThreadExchangeStreamCaptureMode(&mode_);
     }
-    (void)cudaThreadExchangeStreamCaptureMode(&mode);
-    return e;
+    cudaError_t error() const { return error_; }
+
+  private:
+    cudaStreamCaptureMode mode_ = cudaStreamCaptureModeRelaxed;
+    cudaError_t error_;
+};
+
+struct Capture {
+    bool active = false;
+    unsigned long long id = 0;
+    cudaGraph_t graph = nullptr;
+};
+Capture capture_of(cudaStream_t stream) {
+    Capture c;
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    if (cudaStreamGetCaptureInfo(stream, &st, &c.id, &c.graph) != cudaSuccess)
+        (void)cudaGetLastError();  // the legacy stream while another one is captured
+    else
+        c.active = st == cudaStreamCaptureStatusActive;
+    return c;
 }
 
-bool is_capturing(cudaStream_t stream) {
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &st) != cudaSuccess) {
-        (void)cudaGetLastError();  // the legacy stream while another one is captured
-        return false;
+void CUDART_CB graph_gone(void *scratch) {
+    static_cast<CaptureScratch *>(scratch)->gone.store(true);
+    g_captures_gone.fetch_add(1);
+}
+
+// Free what belonged to graphs that are gone.
+void collect_gone() {
+    if (g_captures_gone.load() == 0) return;
+    RelaxedCapture relaxed;
+    if (relaxed.error() != cudaSuccess) return;
+    for (auto it = g_captures.begin(); it != g_captures.end();) {
+        if (!it->second->gone.load()) {
+            ++it;
+            continue;
+        }
+        for (auto &b : it->second->buffers) scratch_free(b.first.at);
+        it = g_captures.erase(it);
+        g_captures_gone.fetch_sub(1);
     }
-    return st == cudaStreamCaptureStatusActive;
+}
+
+// The buffers of the capture, which its graph keeps from the first call on.
+cudaError_t capture_scratch(const Capture &c, int dev, CaptureScratch **out) {
+    auto it = g_captures.find(c.id);
+    if (it == g_captures.end()) {
+        it = g_captures.emplace(c.id, std::make_unique<CaptureScratch>()).first;
+        it->second->dev = dev;
+        cudaUserObject_t object = nullptr;
+        cudaError_t e = cudaUserObjectCreate(&object, it->second.get(), graph_gone, 1, cudaUserObjectNoDestructorSync);
+        if (e != cudaSuccess) {
+            g_captures.erase(it);
+            return e;
+        }
+        e = cudaGraphRetainUserObject(c.graph, object, 1, cudaGraphUserObjectMove);
+        if (e != cudaSuccess) {
+            (void)cudaUserObjectRelease(object, 1);  // says that it is gone
+            return e;
+        }
+    }
+    *out = it->second.get();
+    return cudaSuccess;
+}
+
+enum class ScratchKind { partials, counters, operands };
+
+// At least `bytes` bytes of one kind for work on `stream`; new counters are zero.
+cudaError_t acquire_buffer(cudaStream_t stream, int dev, const Capture &c, ScratchKind kind, size_t bytes, size_t preferred, void **out) {
+    CaptureScratch *cs = nullptr;
+    if (c.active) {
+        const cudaError_t e = capture_scratch(c, dev, &cs);
+        if (e != cudaSuccess) return e;
+    }
+    const uintptr_t key = reinterpret_cast<uintptr_t>(stream);
+    ScratchEntry &entry = cs ? cs->streams[key] : g_scratch[{dev, key}];
+    ScratchBuffer &b = kind == ScratchKind::partials ? entry.partials : kind == ScratchKind::counters ? entry.counters : entry.operands;
+    const bool zero = kind == ScratchKind::counters;
+    if (b.bytes < bytes && cs) {
+        // Nothing may wait for a stream that is captured; new counters are
+        // cleared on a stream of their own, outside the graph.  An outgrown
+        // buffer stays with the graph, whose earlier work uses it.
+        RelaxedCapture relaxed;
+        cudaError_t e = relaxed.error();
+        if (e != cudaSuccess) return e;
+        cs->buffers.reserve(cs->buffers.size() + 1);
+        ScratchBuffer fresh;
+        e = scratch_alloc(&fresh.at, bytes);
+        if (e != cudaSuccess) return e;
+        fresh.bytes = bytes;
+        cs->buffers.emplace_back(fresh, zero);
+        if (zero) {
+            cudaStream_t side = nullptr;
+            e = cudaStreamCreateWithFlags(&side, cudaStreamNonBlocking);
+            if (e == cudaSuccess) e = cudaMemsetAsync(fresh.at, 0, bytes, side);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(side);
+            if (side) cudaStreamDestroy(side);
+            if (e != cudaSuccess) return e;
+        }
+        b = fresh;
+    } else if (b.bytes < bytes) {
+        cudaError_t e = cudaStreamSynchronize(stream);  // work already queued may still use the old buffer
+        if (e != cudaSuccess) return e;
+        scratch_free(b.at);
+        b = ScratchBuffer();
+        const size_t want = std::max(bytes, preferred);
+        e = scratch_alloc(&b.at, want);
+        if (e == cudaSuccess && zero) e = cudaMemset(b.at, 0, want);
+        if (e != cudaSuccess) return e;
+        b.bytes = want;
+    }
+    *out = b.at;
+    return cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out) {
+cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out) try {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
-    const bool capturing = is_capturing(stream);
+    const Capture c = capture_of(stream);
     std::lock_guard<std::mutex> lock(g_scratch_mu);
-    ScratchEntry &e = g_scratch[{dev, reinterpret_cast<uintptr_t>(stream)}];
-    // A buffer whose address a graph has keeps living: growing leaves it.
-    const bool keep_old = e.captured || capturing;
-    if (e.partial_floats < partial_floats) {
-        // Work already queued on this stream may still use the old buffer.
-        cudaError_t r = keep_old ? cudaSuccess : cudaStreamSynchronize(stream);
-        if (r != cudaSuccess) return r;
-        if (!keep_old) scratch_free(e.partials);
-        e.partials = nullptr;
-        e.partial_floats = 0;
-        size_t want = partial_floats + partial_floats / 4;
-        void **at = reinterpret_cast<void **>(&e.partials);
-        r = capturing ? scratch_alloc_capturing(at, want * sizeof(float), 0) : scratch_alloc(at, want * sizeof(float));
-        if (r != cudaSuccess) return r;
-        e.partial_floats = want;
-    }
-    if (e.ncounters < ncounters) {
-        cudaError_t r = keep_old ? cudaSuccess : cudaStreamSynchronize(stream);
-        if (r != cudaSuccess) return r;
-        if (!keep_old) scratch_free(e.counters);
-        e.counters = nullptr;
-        e.ncounters = 0;
-        size_t want = ncounters < 1024 ? 1024 : ncounters + ncounters / 4;
-        void **at = reinterpret_cast<void **>(&e.counters);
-        if (capturing) {
-            r = scratch_alloc_capturing(at, want * sizeof(unsigned), want * sizeof(unsigned));
-        } else {
-            r = scratch_alloc(at, want * sizeof(unsigned));
-            if (r == cudaSuccess) r = cudaMemset(e.counters, 0, want * sizeof(unsigned));
-        }
-        if (r != cudaSuccess) return r;
-        e.ncounters = want;
-    }
-    e.captured = e.captured || capturing;
-    out->partials = e.partials;
-    out->counters = e.counters;
-    return cudaSuccess;
+    collect_gone();
+    void *partials = nullptr, *counters = nullptr;
+    cudaError_t e = acquire_buffer(stream, dev, c, ScratchKind::partials, partial_floats * sizeof(float),
+                                   (partial_floats + partial_floats / 4) * sizeof(float), &partials);
+    if (e == cudaSuccess)
+        e = acquire_buffer(stream, dev, c, ScratchKind::counters, ncounters * sizeof(unsigned),
+                           (ncounters < 1024 ? 1024 : ncounters + ncounters / 4) * sizeof(unsigned), &counters);
+    out->partials = static_cast<float *>(partials);
+    out->counters = static_cast<unsigned *>(counters);
+    return e;
+} catch (...) {
+    return cudaErrorMemoryAllocation;  // of the tables
 }
 
-cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, float **out) {
+cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, float **out) try {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
+    const Capture c = capture_of(stream);
     std::lock_guard<std::mutex> lock(g_scratch_mu);
-    ScratchEntry &e = g_scratch[{dev, reinterpret_cast<uintptr_t>(stream)}];
-    if (e.operand_floats < floats) {
-        cudaError_t r = cudaStreamSynchronize(stream);  // queued work may still read the old buffer
-        if (r != cudaSuccess) return r;
-        scratch_free(e.operands);
-        e.operands = nullptr;
-        e.operand_floats = 0;
-        r = scratch_alloc(reinterpret_cast<void **>(&e.operands), floats * sizeof(float));
-        if (r != cudaSuccess) return r;
-        e.operand_floats = floats;
-    }
-    *out = e.operands;
-    return cudaSuccess;
+    collect_gone();
+    void *at = nullptr;
+    const cudaError_t e = acquire_buffer(stream, dev, c, ScratchKind::operands, floats * sizeof(float), 0, &at);
+    *out = static_cast<float *>(at);
+    return e;
+} catch (...) {
+    return cudaErrorMemoryAllocation;
 }
 
 size_t debug_shrink_c() {
@@ -274,10 +353,16 @@ int read_status_word(DeviceState *ds, cudaStream_t stream) {
     {
         std::lock_guard<std::mutex> lock(g_scratch_mu);
         for (auto &kv : g_scratch)
-            if (kv.first.first == dev && kv.second.counters) {
-                e = cudaMemset(kv.second.counters, 0, kv.second.ncounters * sizeof(unsigned));
+            if (kv.first.first == dev && kv.second.counters.at) {
+                e = cudaMemset(kv.second.counters.at, 0, kv.second.counters.bytes);
                 if (e != cudaSuccess) return fail_cuda(e);
             }
+        for (auto &kv : g_captures)
+            for (auto &b : kv.second->buffers)
+                if (kv.second->dev == dev && b.second) {
+                    e = cudaMemset(b.first.at, 0, b.first.bytes);
+                    if (e != cudaSuccess) return fail_cuda(e);
+                }
     }
     const unsigned zero = 0;
     e = cudaMemcpy(ds->watchdog, &zero, sizeof(zero), cudaMemcpyHostToDevice);
@@ -301,13 +386,13 @@ int finish_call(const CallInfo &info, cudaStream_t stream) {
         if (it != g_scratch.end()) {
             ScratchEntry &se = it->second;
             const char *poke = std::getenv("GEMM11_DEBUG_POKE_CANARY");
-            if (poke && poke[0] == '1' && se.partials) {
-                canary_poke_kernel<<<1, 1, 0, stream>>>(reinterpret_cast<unsigned *>(se.partials + se.partial_floats));
+            if (poke && poke[0] == '1' && se.partials.at) {
+                canary_poke_kernel<<<1, 1, 0, stream>>>(
+                    reinterpret_cast<unsigned *>(static_cast<unsigned char *>(se.partials.at) + se.partials.bytes));
             }
-            cudaError_t e = check_bands(se.partials, se.partial_floats * sizeof(float), ds->watchdog, stream);
-            if (e == cudaSuccess) e = check_bands(se.counters, se.ncounters * sizeof(unsigned), ds->watchdog, stream);
-            if (e == cudaSuccess)
-                e = check_bands(se.operands, se.operand_floats * sizeof(float), ds->watchdog, stream);
+            cudaError_t e = cudaSuccess;
+            for (const ScratchBuffer *b : {&se.partials, &se.counters, &se.operands})
+                if (e == cudaSuccess) e = check_bands(b->at, b->bytes, ds->watchdog, stream);
             if (e != cudaSuccess) return fail_cuda(e);
         }
     }

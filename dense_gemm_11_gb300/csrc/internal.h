@@ -9,8 +9,9 @@
 namespace gemm11 {
 
 // Scratch for split-K partial tiles and their arrival counters, owned by the
-// library, one per (device, stream), grown on demand.  Counters are zero
-// between calls: every kernel that increments one resets it.
+// library, one per (device, stream), grown on demand; under stream capture one
+// per capture and stream, which the graph keeps.  Counters are zero between
+// calls: every kernel that increments one resets it.
 struct Scratch {
     float *partials = nullptr;
     unsigned *counters = nullptr;
@@ -19,8 +20,8 @@ struct Scratch {
 // `ncounters` zeroed counters usable on `stream` (current device).
 cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out);
 
-// A second per-(device, stream) buffer for repacked operands (used together
-// with the partials above), grown on demand.
+// A second buffer of the same kind for repacked operands (used together with
+// the partials above).
 cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, float **out);
 
 // Device address of the current device's watchdog word.

@@ -34,7 +34,12 @@
  *     word and returns early; gemm_check() reports it as GEMM_ERR_TIMEOUT.
  *   - Split-K shapes use a library-owned workspace, allocated lazily once per
  *     (device, stream) and reused; calls on one stream are serialised by the
- *     stream, calls on different streams use different workspaces.
+ *     stream, calls on different streams use different workspaces.  While a
+ *     stream is being captured the call allocates a workspace that belongs to
+ *     the graph and is freed by a later call once the graph and its instances
+ *     are destroyed.  So replays of different graphs may overlap, with each
+ *     other and with calls; two instances of one graph, which share its
+ *     workspace, may not.
  *   - Debug build.  The same sources compiled with GEMM11_DEBUG=1 give
  *     libgemm11_debug.so (the Python binding loads it when the environment
  *     variable GEMM11_DEBUG is 1).  The DeepGEMM essay "企业官网建设流程全解析"
@@ -326,7 +331,7 @@ GEMM11_API int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int
  * the same of SB and ldsb (leading dimensions of a single row excepted);
  * anything else returns GEMM_ERR_UNSUPPORTED.  M, N and K are unrestricted.
  * Scratch: for few tiles of 256 x 256 and a long K up to 20 MB (plan
- * "fp8_pair_256x256_splitk"), under stream capture as in gemm_moe_few_tokens.
+ * "fp8_pair_256x256_splitk").
  */
 GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_type, long long lda,
                                  const float *SA, long long ldsa, const void *B, int b_type, long long ldb,
@@ -361,9 +366,7 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
  * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive
  * otherwise.  Scratch: about T E + T H / 2 + T top_k (4 H + 5 I / 2) floats of library-owned device
- * memory per stream.  A call under stream capture may allocate it, and a graph
- * keeps the scratch it was captured with: replays of it must not overlap on
- * the GPU with each other or with calls on the stream that it was captured on.
+ * memory per stream, or per graph under stream capture (see above).
  */
 GEMM11_API int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, int x_type, long long ldx,
                                    const void *router, int router_type, const void *gate, const void *up,
