@@ -114,6 +114,7 @@ cudaError_t scratch_alloc(void **user, size_t bytes) {
     if (e != cudaSuccess) return e;
     e = cudaMemset(raw, kCanaryByte, kCanaryBytes);
     if (e == cudaSuccess) e = cudaMemset(raw + kCanaryBytes + bytes, kCanaryByte, kCanaryBytes);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the check runs on the call's stream
     if (e != cudaSuccess) {
         cudaFree(raw);
         return e;
@@ -288,7 +289,9 @@ cudaError_t acquire_buffer(cudaStream_t stream, int dev, const Capture &c, Scrat
         b = ScratchBuffer();
         const size_t want = std::max(bytes, preferred);
         e = scratch_alloc(&b.at, want);
-        if (e == cudaSuccess && zero) e = cudaMemset(b.at, 0, want);
+        // On the call's stream: the default stream's work is not ordered with
+        // that of a non-blocking stream.
+        if (e == cudaSuccess && zero) e = cudaMemsetAsync(b.at, 0, want, stream);
         if (e != cudaSuccess) return e;
         b.bytes = want;
     }
@@ -366,6 +369,7 @@ int read_status_word(DeviceState *ds, cudaStream_t stream) {
     }
     const unsigned zero = 0;
     e = cudaMemcpy(ds->watchdog, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // the next call may be on any stream
     if (e != cudaSuccess) return fail_cuda(e);
     return (word & (kDebugBoundsFault | kDebugCanaryFault)) ? GEMM_ERR_DEBUG_CHECK : GEMM_ERR_TIMEOUT;
 }
