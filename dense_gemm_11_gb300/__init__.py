@@ -199,8 +199,15 @@ def _mat(t, name, dtype):
     # a single row has no row stride of its own: report the tensor's when it is
     # a valid one (a view keeps its parent's, which may be 16-byte aligned)
     if t.shape[0] > 1 or t.stride(0) >= t.shape[1]:
+        _check_rows(name, *t.shape, t.stride(0))
         return t.data_ptr(), max(t.stride(0), 1)
     return t.data_ptr(), max(t.shape[1], 1)
+
+
+def _check_rows(name, rows, cols, ld):
+    """Rows that share memory (an expanded tensor) have no leading dimension."""
+    if rows > 1 and 0 < cols > ld:
+        raise ValueError(f"{name} needs a row stride of at least its width, got {ld} for {rows} x {cols} (an expanded tensor?)")
 
 
 def gemm_f32_raw(M, N, K, alpha, A_ptr, lda, B_ptr, ldb, beta, C_ptr, ldc, stream_ptr=0) -> int:
@@ -445,7 +452,8 @@ def _typed_mat(t, name, allowed):
     ld, step = stride
     if step != 1 and cols > 1:
         raise ValueError(f"{name} needs unit column stride")
-    if ld < cols and rows <= 1:  # a single row has no row stride of its own
+    if ld < cols:  # a single row has no row stride of its own
+        _check_rows(name, rows, cols, ld)
         ld = cols
     return t.data_ptr(), ld or 1, rows, cols, code
 
