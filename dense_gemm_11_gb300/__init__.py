@@ -542,7 +542,8 @@ def moe_few_tokens(X, router, gate, up, down, Y, top_k: int, *, scales=None, act
     expert).  up=None: no gating, h = act(gate @ x).  Y: (T, H) fp32, fp16 or bf16.
     The e_j are the top_k largest logits of router @ x (ties: the lower index); w_j their softmax probabilities,
     divided by their sum with renormalize=True.  ids (int32) and weights (fp32), both (T, top_k) and contiguous,
-    receive them if given.  Limits: T <= 128, E <= 512, top_k <= 16, T * top_k <= 1024, H and I multiples of 16, H <= 32768.
+    receive them if given.  Limits: T <= 128, E <= 512, top_k <= 16, T * top_k <= 1024, H and I multiples of 16, H <= 32768,
+    T * top_k * I < 2^31.
     """
     x_ptr, ldx, T, H, x_type = _typed_mat(X, "X", _HALFS)
     y_ptr, ldy, y_rows, y_cols, y_type = _typed_mat(Y, "Y", _FLOATS)

@@ -549,6 +549,10 @@ namespace {
 bool valid_act(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_GELU_TANH; }
 bool valid_fp8(int type) { return type == GEMM_DTYPE_E4M3 || type == GEMM_DTYPE_E5M2; }
 
+// The largest extent of a matrix held in 8 bits: the kernels' indices run over
+// the end of one by less than two tiles.
+constexpr int kMaxExtent = 0x7FFFFFFF - 511;
+
 // A call with an empty result.
 int noop() {
     t_last_plan = "noop_empty";
@@ -702,6 +706,7 @@ int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int x_type, lo
     if (ldx < std::max(1, cols) || ldq < std::max(1LL, q_cols) || lds < std::max(1LL, s_cols)) return GEMM_ERR_INVALID_ARG;
     if (rows == 0 || cols == 0) return noop();
     if (!X || !Q || !S) return GEMM_ERR_INVALID_ARG;
+    if (rows > kMaxExtent || cols > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
     if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
@@ -739,6 +744,7 @@ int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A, int a_typ
         return GEMM_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return noop();
     if (!C) return GEMM_ERR_INVALID_ARG;
+    if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     const bool product = K > 0 && alpha != 0.f;
     if (product) {
         if (!A || !SA || !B || !SB) return GEMM_ERR_INVALID_ARG;
@@ -802,7 +808,8 @@ int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, in
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     const bool ok = top_k <= kMoeMaxTopK && E <= kMoeMaxExperts && T <= kMoeMaxTokens && T * top_k <= kMoeMaxSlots &&
                     H <= kMoeMaxWidth && H % 16 == 0 && I % 16 == 0 && al16(X) && al16(router) && al16(gate) && al16(up) && al16(down) &&
-                    (T == 1 || ldx % 8 == 0) && static_cast<long long>(E) * std::max(H, I) < (1LL << 31);
+                    (T == 1 || ldx % 8 == 0) && static_cast<long long>(E) * std::max(H, I) < (1LL << 31) &&
+                    static_cast<long long>(T) * top_k * I < (1LL << 31);
     if (!ok) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);

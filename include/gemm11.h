@@ -303,7 +303,8 @@ typedef enum {
  * Any alignment and leading dimensions are accepted (16-byte aligned rows of X
  * and 8-byte aligned rows of Q take wider loads and stores).  Returns
  * GEMM_ERR_INVALID_ARG for a negative size, a short leading dimension, an
- * unknown type or layout, or a NULL pointer with a non-empty extent.
+ * unknown type or layout, or a NULL pointer with a non-empty extent, and
+ * GEMM_ERR_UNSUPPORTED for rows or cols above 2^31 - 512.
  */
 GEMM11_API int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int x_type, long long ldx, void *Q,
                                           int q_type, long long ldq, float *S, long long lds, int layout,
@@ -329,7 +330,8 @@ GEMM11_API int gemm_fp8_quantize_block128(int rows, int cols, const void *X, int
  * The tensor-memory-access path needs A, B and SA 16-byte aligned, lda and ldb
  * multiples of 16 (bytes), ldsa a multiple of 4, and for GEMM_FP8_ROWS of B
  * the same of SB and ldsb (leading dimensions of a single row excepted);
- * anything else returns GEMM_ERR_UNSUPPORTED.  M, N and K are unrestricted.
+ * anything else returns GEMM_ERR_UNSUPPORTED.  M, N and K are unrestricted up
+ * to 2^31 - 512.
  * Scratch: for few tiles of 256 x 256 and a long K up to 20 MB (plan
  * "fp8_pair_256x256_splitk").
  */
@@ -361,8 +363,9 @@ GEMM11_API int gemm_fp8_block128(int M, int N, int K, float alpha, const void *A
  * value with BF16 weights and 22 with FP16 or 8-bit weights.  A token with a
  * NaN logit gets NaN weights, and so a NaN row.
  * Limits: 1 <= top_k <= min(E, 16), E <= 512, T <= 128, T * top_k <= 1024;
- * H and I multiples of 16, H <= 32768, E * max(H, I) < 2^31; X, router, gate, up and down 16-byte aligned and
- * ldx a multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
+ * H and I multiples of 16, H <= 32768, E * max(H, I) < 2^31,
+ * T * top_k * I < 2^31; X, router, gate, up and down 16-byte aligned and ldx a
+ * multiple of 8 (T > 1); otherwise GEMM_ERR_UNSUPPORTED.  Sizes below 0,
  * top_k < 1 or > E, ldx or ldy < H, unknown types and NULL pointers return
  * GEMM_ERR_INVALID_ARG.  T == 0 or H == 0 is a no-op; E and I must be positive
  * otherwise.  Scratch: about T E + T H / 2 + T top_k (4 H + 5 I / 2) floats of library-owned device
