@@ -59,6 +59,41 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[COLS]) {
         tmem_ld_32x32b_x16(taddr, r);
 }
 
+// A read that is in flight where a loop comes round.  The compiler may copy a
+// variable there, which would read it before it has landed; registers that only
+// PTX knows it cannot.  A kernel declares them once, before their first use.
+#define GEMM11_TMEM_AHEAD_REGISTERS() asm volatile(".reg .b32 ahead<32>;")
+template <int COLS>
+__device__ __forceinline__ void tmem_ld_ahead(uint32_t taddr) {
+    static_assert(COLS == 16 || COLS == 32, "columns");
+    if constexpr (COLS == 32)
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {ahead0, ahead1, ahead2, ahead3, ahead4, ahead5, ahead6, ahead7, ahead8, ahead9, ahead10, ahead11, ahead12, ahead13, ahead14, ahead15, "
+                     "ahead16, ahead17, ahead18, ahead19, ahead20, ahead21, ahead22, ahead23, ahead24, ahead25, ahead26, ahead27, ahead28, ahead29, ahead30, ahead31}, [%0];" ::"r"(taddr) : "memory");
+    else
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {ahead0, ahead1, ahead2, ahead3, ahead4, ahead5, ahead6, ahead7, ahead8, ahead9, ahead10, ahead11, ahead12, ahead13, ahead14, ahead15}, [%0];" ::"r"(taddr) : "memory");
+}
+// Wait for it, and for this thread's other reads.
+template <int COLS>
+__device__ __forceinline__ void tmem_wait_ahead(uint32_t (&r)[COLS]) {
+    tmem_wait_ld();
+    if constexpr (COLS == 32)
+        asm volatile(
+            "mov.b32 %0, ahead0; mov.b32 %1, ahead1; mov.b32 %2, ahead2; mov.b32 %3, ahead3; mov.b32 %4, ahead4; mov.b32 %5, ahead5; mov.b32 %6, ahead6; mov.b32 %7, ahead7;"
+            "mov.b32 %8, ahead8; mov.b32 %9, ahead9; mov.b32 %10, ahead10; mov.b32 %11, ahead11; mov.b32 %12, ahead12; mov.b32 %13, ahead13; mov.b32 %14, ahead14; mov.b32 %15, ahead15;"
+            "mov.b32 %16, ahead16; mov.b32 %17, ahead17; mov.b32 %18, ahead18; mov.b32 %19, ahead19; mov.b32 %20, ahead20; mov.b32 %21, ahead21; mov.b32 %22, ahead22; mov.b32 %23, ahead23;"
+            "mov.b32 %24, ahead24; mov.b32 %25, ahead25; mov.b32 %26, ahead26; mov.b32 %27, ahead27; mov.b32 %28, ahead28; mov.b32 %29, ahead29; mov.b32 %30, ahead30; mov.b32 %31, ahead31;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+              "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+              "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]));
+    else
+        asm volatile(
+            "mov.b32 %0, ahead0; mov.b32 %1, ahead1; mov.b32 %2, ahead2; mov.b32 %3, ahead3; mov.b32 %4, ahead4; mov.b32 %5, ahead5; mov.b32 %6, ahead6; mov.b32 %7, ahead7;"
+            "mov.b32 %8, ahead8; mov.b32 %9, ahead9; mov.b32 %10, ahead10; mov.b32 %11, ahead11; mov.b32 %12, ahead12; mov.b32 %13, ahead13; mov.b32 %14, ahead14; mov.b32 %15, ahead15;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+              "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]));
+}
+
 // Two FP32 values in one 64-bit register, and acc = a * b + acc, a * b on both
 // (PTX f32x2; one rounding each, as fmaf).  Held as 64-bit values so that the
 // pairs stay in place.

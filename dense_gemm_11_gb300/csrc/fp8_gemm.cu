@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
                 tmem_wait_ld();
 #pragma unroll
                 for (int u = 0; u < kDeep; ++u) {
+                    tmem_landed(r[u]);
                     uint64_t f[8];  // volatile: 16 columns' scales at a time
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -706,6 +707,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         uint8_t *const staged = sC + (warp - 4) * 4096;
         int i = 0, slot = 0;
         bool ok = true;
+        GEMM11_TMEM_AHEAD_REGISTERS();
         for (int t = cid; ok && t < pp.units && !*abort_flag; t += ncl) {
             const Fp8PairUnit unit = fp8_pair_unit<PARTS>(pp, t);
             // The shuffle keeps the compiler from carrying the unit's choice into
@@ -727,7 +729,8 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             if (!B_ROWS && lane < blocks) next0 = __ldg(sb0 + lane * p.sb_kb), next1 = __ldg(sb1 + lane * p.sb_kb);
             // While the sums of one read (32 columns, 16 with a scale for each
             // column) are added the next is on its way, over the end of a block
-            // too.  A wait is for every read, so only one is in flight: with two
+            // too, there in registers of its own (GEMM11_TMEM_AHEAD_REGISTERS).
+            // A wait is for every read, so only one is in flight: with two
             // each wait paid for the later one (146 us against 142 for 4096 x
             // 11008 x 4096).  The accumulator goes back as soon as the block's
             // last read is in.
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 tc_fence_after();
             };
             take();
-            tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
+            tmem_ld_ahead<kStep>(t_row + (i & 1) * kPairN);
             for (int kb = 0; kb < blocks; ++kb) {
                 const uint32_t from = t_row + (i & 1) * kPairN, answer = release[i & 1];
                 float s0 = 1.f, s1 = 1.f;
@@ -760,46 +763,46 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if constexpr (B_ROWS) {
                     // each step's scales are read during the step before
                     load_col_scales(fa, sbv);
-                    tmem_wait_ld();
+                    tmem_wait_ahead(r0);
                     tmem_ld<kStep>(from + 16, r1);
                     load_col_scales(fb, sbv + 16 * 4);
                     add_scaled(acc, 0, r0, ss0, fa);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r1);
                     tmem_ld<kStep>(from + 32, r0);
                     load_col_scales(fa, sbv + 32 * 4);
                     add_scaled(acc, 16, r1, ss0, fb);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r0);
                     tmem_ld<kStep>(from + 48, r1);
                     load_col_scales(fb, sbv + 48 * 4);
                     add_scaled(acc, 32, r0, ss0, fa);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r1);
                     tmem_ld<kStep>(from + 64, r0);
                     load_col_scales(fa, sbw + 64 * 4);
                     add_scaled(acc, 48, r1, ss0, fb);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r0);
                     tmem_ld<kStep>(from + 80, r1);
                     load_col_scales(fb, sbw + 80 * 4);
                     add_scaled(acc, 64, r0, ss0, fa);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r1);
                     tmem_ld<kStep>(from + 96, r0);
                     load_col_scales(fa, sbw + 96 * 4);
                     add_scaled(acc, 80, r1, ss0, fb);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r0);
                     tmem_ld<kStep>(from + 112, r1);
                     load_col_scales(fb, sbw + 112 * 4);
                     add_scaled(acc, 96, r0, ss0, fa);
                 } else {
-                    tmem_wait_ld();
+                    tmem_wait_ahead(r0);
                     tmem_ld<kStep>(from + 32, r1);
                     add_scaled(acc, 0, r0, ss0);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r1);
                     tmem_ld<kStep>(from + 64, r0);
                     add_scaled(acc, 32, r1, ss0);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r0);
                     tmem_ld<kStep>(from + 96, r1);
                     add_scaled(acc, 64, r0, ss1);
                 }
-                tmem_wait_ld();
+                tmem_wait_ld(r1);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(answer);
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
                 if (more) {
                     take();
                     if (!ok) break;
-                    tmem_ld<kStep>(t_row + (i & 1) * kPairN, r0);
+                    tmem_ld_ahead<kStep>(t_row + (i & 1) * kPairN);
                 }
                 if constexpr (B_ROWS)
                     add_scaled(acc, 112, r1, ss0, fb);

@@ -337,6 +337,19 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for this thread's reads of tensor memory, the one into r among them.
+// What uses r comes after: the wait names no registers, and without the empty
+// statements, through which r passes, the compiler could move uses before it.
+template <int COLS>
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[COLS]) {
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) asm volatile("" : "+r"(r[i]));
+}
+template <int COLS>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[COLS]) {
+    tmem_wait_ld();
+    tmem_landed(r);
+}
 
 // ---------------------------------------------------------------- CTA pairs (clusters of 2)
 __device__ __forceinline__ uint32_t cluster_ctarank() {
