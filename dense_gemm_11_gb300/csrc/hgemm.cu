@@ -799,15 +799,15 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                 {
                     uint32_t ra[32], rb[32];
                     tmem_ld_32x32b_x32(t_row, ra);
-                    tmem_wait_ld();
+                    tmem_wait_ld(ra);
 #pragma unroll
                     for (int ch = 0; ch < BN / 32; ch += 2) {
                         tmem_ld_32x32b_x32(t_row + (ch + 1) * 32, rb);
                         put(ra, ch);
-                        tmem_wait_ld();
+                        tmem_wait_ld(rb);
                         if (ch + 2 < BN / 32) tmem_ld_32x32b_x32(t_row + (ch + 2) * 32, ra);
                         put(rb, ch + 1);
-                        tmem_wait_ld();
+                        tmem_wait_ld(ra);
                     }
                 }
                 tc_fence_before();
@@ -844,7 +844,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                 for (int ch = 0; ch < BN / 32 && ch * 32 < p.M; ++ch) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(t_row + ch * 32, r);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r);
                     // columns at or past M (the MMA's padding) are never read
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
@@ -882,7 +882,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
             for (int ch = ch_first; ch < BN / 32; ch += ch_step) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_row + ch * 32, r);
-                tmem_wait_ld();
+                tmem_wait_ld(r);
                 if (partial) {
                     if (!part_ok) continue;
                     // scratch layout per unit: [chunk][column j][row 0..127] -> coalesced
@@ -1283,7 +1283,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                     if (g0 + gi >= kGroups) continue;
                     uint32_t r[16];
                     tmem_ld_32x32b_x16(t_row + (g0 + gi) * 32 + j0, r);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r);
                     if (c == 0) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) tot[gi][j0 + j] = __uint_as_float(r[j]);
@@ -1362,7 +1362,8 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                     uint32_t r2[2][32];
                     tmem_ld_32x32b_x32(t_row + (2 * u) * 32, r2[0]);
                     tmem_ld_32x32b_x32(t_row + (2 * u + 1) * 32, r2[1]);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r2[0]);
+                    tmem_landed(r2[1]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float v[32];
@@ -1386,7 +1387,7 @@ __global__ void __launch_bounds__(64 + 32 * EPI, 1)
                 for (int ch = ch_first; ch < BN / 32; ch += ch_step) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(t_row + ch * 32, r);
-                    tmem_wait_ld();
+                    tmem_wait_ld(r);
                     const int col0 = n0 + ch * 32;
                     float v[32];
 #pragma unroll
