@@ -417,6 +417,7 @@ struct Fp8PairArgs {
     int part_blocks;     // of a unit but the tile's last
     uint32_t per_tile;   // 65536 / parts, rounded up
     float *partials;  // 256 x 256 sums of each such unit
+    size_t partial_floats;  // of them all, checked by GEMM11_DEBUG builds
 };
 
 // Unit t: its tile and its blocks of k (v is below 256, so that the product
@@ -825,6 +826,7 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             // as they are to the partial sums.
             const bool some = PARTS && t >= pp.whole;
             if (some) row = (t - pp.whole) * 256 + static_cast<int>(rank) * 128 + q * 32, col = part * 64;
+            if (some && !debug_in_bounds((row + 32u) * static_cast<size_t>(kPairN) <= pp.partial_floats, p.err)) continue;
             const int m = row + lane;
 #pragma unroll
             for (int gr = 0; gr < kPairCols / 32; ++gr) {
@@ -875,6 +877,7 @@ __global__ void __launch_bounds__(256) fp8_join_kernel(const Fp8PairArgs pp) {
     m += at / (kPairN / 4), n += at % (kPairN / 4) * 4;
     if (m >= pp.a.M || n >= pp.a.N) return;
     const float4 *from = reinterpret_cast<const float4 *>(pp.partials) + static_cast<size_t>(left) * pp.parts * kPieces + at;
+    if (!debug_in_bounds((static_cast<size_t>(left + 1) * pp.parts - 1) * kPieces + at < pp.partial_floats / 4, pp.a.err)) return;
     float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int part = 0; part < pp.parts; ++part) {
@@ -931,7 +934,10 @@ Fp8Args fp8_args(const Fp8Gemm &g) {
     a.err = watchdog_word();
     a.wait_ns = kWaitLimitNs;
     a.splits = 1;
-    if (kDebugBuild) a.c_extent = static_cast<size_t>(g.M - 1) * static_cast<size_t>(g.ldc) + g.N;
+    if (kDebugBuild) {
+        a.c_extent = static_cast<size_t>(g.M - 1) * static_cast<size_t>(g.ldc) + g.N;
+        a.c_extent -= std::min(a.c_extent - 1, debug_shrink_c());
+    }
     return a;
 }
 
@@ -1115,6 +1121,7 @@ cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, const PairPlan &
         e = acquire_scratch(stream, static_cast<size_t>(rows) * kPairN, 0, &sc);
         if (e != cudaSuccess) return e;
         args.partials = sc.partials;
+        args.partial_floats = static_cast<size_t>(rows) * kPairN;
         if (!encode_matrix_map(&tp, f32, sc.partials, kPairN, rows, kPairN * 4, 32, 32, sw)) return cudaErrorNotSupported;
     }
     cfg.gridDim = dim3(2 * std::min(clusters, args.units));

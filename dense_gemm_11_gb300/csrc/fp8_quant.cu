@@ -48,7 +48,13 @@ struct QuantArgs {
     int per_cta;  // rows kernel: column blocks of a CTA
     int nx;       // CTAs along the columns (the grid is one-dimensional: rows may be many)
     int q_vec;    // Q rows take aligned 8-byte (rows, blocks) or 4-byte (cols) stores
+    unsigned *err;
+    size_t q_extent, s_extent;  // checked by GEMM11_DEBUG builds
 };
+
+__device__ __forceinline__ bool scale_inside(const QuantArgs &p, long long at) {
+    return debug_in_bounds(static_cast<size_t>(at) < p.s_extent, p.err);
+}
 
 template <int XT>
 struct XElem;
@@ -129,6 +135,7 @@ __device__ __forceinline__ void store8(const QuantArgs &p, long long row, int c,
     w.x = pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv, p.e5m2);
     w.y = pack4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv, p.e5m2);
     uint8_t *q = p.Q + row * p.ldq + c;
+    if (!debug_in_bounds(c >= p.cols || static_cast<size_t>(q - p.Q) + min(8, p.cols - c) <= p.q_extent, p.err)) return;
     if (p.q_vec && c + 8 <= p.cols) {
         *reinterpret_cast<uint2 *>(q) = w;
     } else {
@@ -169,7 +176,7 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const QuantArgs p) {
             const float top = type_max(p.e5m2);
             if (live && b + u < b1) {
                 store8(p, row, (b + u) * kScaleBlock + sub * 8, v[u], top / m);
-                if (sub == 0) p.S[static_cast<long long>(b + u) * p.lds + row] = m / top;
+                if (sub == 0 && scale_inside(p, static_cast<long long>(b + u) * p.lds + row)) p.S[static_cast<long long>(b + u) * p.lds + row] = m / top;
             }
         }
     }
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(256, 3) quant_blocks_kernel(const QuantArgs p)
 #pragma unroll
     for (int w = 0; w < 8; ++w) m = fmaxf(m, warp_max[w]);
     const float top = type_max(p.e5m2), inv = top / m;
-    if (threadIdx.x == 0) p.S[static_cast<long long>(by) * p.lds + bx] = m / top;
+    if (threadIdx.x == 0 && scale_inside(p, static_cast<long long>(by) * p.lds + bx)) p.S[static_cast<long long>(by) * p.lds + bx] = m / top;
 #pragma unroll
     for (int u = 0; u < 8; ++u)
         if (r0 + 16 * u < p.rows) store8(p, r0 + 16 * u, c, v[u], inv);
@@ -252,7 +259,7 @@ __global__ void __launch_bounds__(256, 6) quant_cols_kernel(const QuantArgs p) {
 #pragma unroll
         for (int w = 0; w < 8; ++w) a = fmaxf(a, part[w][threadIdx.x]);
         part[0][threadIdx.x] = top / a;
-        if (c0 + static_cast<int>(threadIdx.x) < p.cols)
+        if (c0 + static_cast<int>(threadIdx.x) < p.cols && scale_inside(p, static_cast<long long>(by) * p.lds + c0 + threadIdx.x))
             p.S[static_cast<long long>(by) * p.lds + c0 + threadIdx.x] = a / top;
     }
     __syncthreads();
@@ -268,6 +275,7 @@ __global__ void __launch_bounds__(256, 6) quant_cols_kernel(const QuantArgs p) {
     for (int c = warp; c < 64 && c0 + c < p.cols; c += 8) {
         uint8_t *q = p.Q + static_cast<long long>(c0 + c) * p.ldq + r0 + lane * 4;
         const uint32_t w = turned[c][lane];
+        if (!debug_in_bounds(lane * 4 >= left || static_cast<size_t>(q - p.Q) + min(4LL, left - lane * 4) <= p.q_extent, p.err)) continue;
         if (p.q_vec && lane * 4 + 4 <= left) {
             *reinterpret_cast<uint32_t *>(q) = w;
         } else {
@@ -331,6 +339,13 @@ cudaError_t run_fp8_quantize(const Fp8Quant &q, cudaStream_t stream, CallInfo *i
     const bool vec = (reinterpret_cast<uintptr_t>(q.X) & 15u) == 0 && (q.rows == 1 || (q.ldx * xb) % 16 == 0);
     const uintptr_t qa = q.layout == 1 ? 3u : 7u;
     const int q_rows = q.layout == 1 ? q.cols : q.rows;
+    a.err = watchdog_word();
+    if (kDebugBuild) {
+        const long long q_cols = q.layout == 1 ? q.rows : q.cols, kb = (q_cols + kScaleBlock - 1) / kScaleBlock;
+        a.q_extent = static_cast<size_t>((q_rows - 1LL) * q.ldq + q_cols);
+        a.s_extent = static_cast<size_t>(q.layout == 2 ? ((q_rows + kScaleBlock - 1LL) / kScaleBlock - 1) * q.lds + kb : (kb - 1) * q.lds + q_rows);
+        a.q_extent -= std::min(a.q_extent, debug_shrink_c());
+    }
     a.q_vec = (reinterpret_cast<uintptr_t>(q.Q) & qa) == 0 && (q_rows == 1 || (q.ldq & static_cast<long long>(qa)) == 0);
     switch (q.x_type * 2 + (vec ? 1 : 0)) {
         case 0: return launch_quant<kOutF32, false>(a, q.layout, stream, info);

@@ -106,7 +106,14 @@ struct MoeArgs {
     int by_token;    // the routing takes a CTA for each token
     int flat_h, flat_i;  // elements of a row up to which one copy takes a stage's boxes (whole 128-byte ones)
     int stages, stage_bytes;
+    // Elements (hidden16: bytes) of each part of the scratch, and of Y, checked by GEMM11_DEBUG builds.
+    size_t n_logits, n_hidden, n_hidden16, n_x16, n_part, n_y;
 };
+
+// Whether element `at` of a buffer of n may be accessed.
+__device__ __forceinline__ bool inside(long long at, size_t n, const MoeArgs &p) {
+    return debug_in_bounds(at >= 0 && static_cast<size_t>(at) < n, p.err);
+}
 
 // Shared-memory tables of the routing, the same in every CTA.
 struct Routing {
@@ -283,7 +290,7 @@ __device__ void router_logits(const MoeArgs &p, float *red) {
             router_dot<XT>(p, e, t0, lane, 32, acc);
 #pragma unroll
             for (int i = 0; i < kRouterTokens; ++i)
-                if (lane == i && t0 + i < p.T) p.logits[(t0 + i) * p.E + e] = acc[i];
+                if (lane == i && t0 + i < p.T && inside((t0 + i) * p.E + e, p.n_logits, p)) p.logits[(t0 + i) * p.E + e] = acc[i];
         }
     } else if (static_cast<int>(blockIdx.x) < units) {
         const int e = blockIdx.x / groups, t0 = (blockIdx.x % groups) * kRouterTokens;
@@ -296,7 +303,7 @@ __device__ void router_logits(const MoeArgs &p, float *red) {
             float v = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) v += red[w * kRouterTokens + threadIdx.x];
-            p.logits[(t0 + threadIdx.x) * p.E + e] = v;
+            if (inside((t0 + threadIdx.x) * p.E + e, p.n_logits, p)) p.logits[(t0 + threadIdx.x) * p.E + e] = v;
         }
     }
 }
@@ -394,6 +401,7 @@ __device__ void scale_token(const MoeArgs &p, int t, float *red) {
     for (int k = threadIdx.x * 8; k < p.H; k += 32 * kWarps * 8) {
         float v[8];
         widen8(__ldg(reinterpret_cast<const uint4 *>(x + k)), XT, v);
+        if (!inside(static_cast<long long>(t) * p.H + k + 7, p.n_x16, p)) continue;
         *reinterpret_cast<uint4 *>(p.x16 + static_cast<long long>(t) * p.H + k) =
             make_uint4(pack2_out16(v[0] * f, v[1] * f, kOutF16), pack2_out16(v[2] * f, v[3] * f, kOutF16),
                        pack2_out16(v[4] * f, v[5] * f, kOutF16), pack2_out16(v[6] * f, v[7] * f, kOutF16));
@@ -774,6 +782,11 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
             }
             armed |= 1u << stage;
             armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+            if (kDebugBuild && !__all_sync(0xffffffffu, mbar_wait(&empty[stage], phase))) {  // one stage in flight
+                if (lane == 0) give_up();
+                ok = false;
+                return;
+            }
             if (++stage == p.stages) stage = 0, phase ^= 1u;
         };
         for (int u = blockIdx.x; ok && u < units1; u += grid) {
@@ -945,9 +958,11 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                         uint16_t part[Cfg::kParts];
                         split_parts<Cfg::kMma>(h, part);
                         uint16_t *to = reinterpret_cast<uint16_t *>(p.hidden16 + slot * parts_bytes(p.I, Cfg::kParts)) + at / 64 * (64 * Cfg::kParts) + at % 64;
+                        if (!inside(reinterpret_cast<uint8_t *>(to + 64 * (Cfg::kParts - 1)) + 1 - p.hidden16, p.n_hidden16, p)) continue;
 #pragma unroll
                         for (int i = 0; i < Cfg::kParts; ++i) to[64 * i] = part[i];
                         if constexpr (Cfg::kFit) {
+                            if (!inside(static_cast<long long>(slot) * p.I + at, p.n_hidden, p)) continue;
                             p.hidden[static_cast<long long>(slot) * p.I + at] = h;
                             if (fabsf(h) < INFINITY) largest = fmaxf(largest, fabsf(h));
                         }
@@ -981,6 +996,7 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) split_parts<Cfg::kMma>(v[i], part[i]);
                 uint8_t *to = p.hidden16 + x / per * parts_bytes(p.I, Cfg::kParts) + at / 64 * (128 * Cfg::kParts) + at % 64 * 2;
+                if (!inside(to + 128 * (Cfg::kParts - 1) + 15 - p.hidden16, p.n_hidden16, p)) continue;
 #pragma unroll
                 for (int j = 0; j < Cfg::kParts; ++j) {
                     auto two = [&](int i) { return part[i][j] | static_cast<uint32_t>(part[i + 1][j]) << 16; };
@@ -1002,7 +1018,9 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int tok = nt * 8 + 2 * (lane & 3) + (i & 1), at = row + 8 * (i >> 1);
-                    if ((mine & (1 << (i & 1))) && tok < n.count && at < p.H) p.part[(n.split * slots + r.order[n.start + tok]) * p.H + at] = acc[nt][i];
+                    if (!(mine & (1 << (i & 1))) || tok >= n.count || at >= p.H) continue;
+                    const long long to = (n.split * slots + r.order[n.start + tok]) * p.H + at;
+                    if (inside(to, p.n_part, p)) p.part[to] = acc[nt][i];
                 }
         }
         // ------------------------------------------------ sum over a token's experts
@@ -1030,7 +1048,8 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
                     y[0] = fmaf(f, v.x, y[0]), y[1] = fmaf(f, v.y, y[1]), y[2] = fmaf(f, v.z, y[2]), y[3] = fmaf(f, v.w, y[3]);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) store_out(p.Y, static_cast<size_t>(t) * p.ldy + c + i, p.y_type, y[i]);
+                for (int i = 0; i < 4; ++i)
+                    if (inside(static_cast<long long>(t) * p.ldy + c + i, p.n_y, p)) store_out(p.Y, static_cast<size_t>(t) * p.ldy + c + i, p.y_type, y[i]);
             }
         }
     }
@@ -1193,6 +1212,15 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     a.chosen = reinterpret_cast<uint16_t *>(a.chosen_weight + n_max);
     a.part = a.chosen_weight + 2 * n_max;
     a.counters = s.counters;
+    if (kDebugBuild) {
+        a.n_logits = n_logits;
+        a.n_hidden = n_hidden;
+        a.n_hidden16 = n_h16 * 4;
+        a.n_x16 = n_x16 * 2;
+        a.n_part = n_slots * m.H * kMaxSplits;
+        a.n_y = static_cast<size_t>(m.T - 1) * static_cast<size_t>(m.ldy) + m.H;
+        a.n_y -= std::min(a.n_y, debug_shrink_c());
+    }
     info->launches = 1;
     info->plan = "moe_few_tokens";
     const bool fp8 = m.w_type == kTypeE4M3;

@@ -47,9 +47,10 @@
  *     this build is the synchronous end of that:
  *       - the pipelines keep one operand stage in flight (the FP32 path
  *         waits for every outstanding copy before it reads a stage; the
- *         tensor-core producers wait for the MMA to consume each stage);
- *       - stores to C and accesses to library scratch check their index
- *         against the extent; a failing check records a fault bit in the
+ *         tensor-core producers, and the mixture of experts' weight loads,
+ *         wait until each stage is consumed);
+ *       - stores to the result (TMA stores excepted, which clip) and accesses
+ *         to library scratch check their index against the extent; a failing check records a fault bit in the
  *         device status word and the access is skipped (nothing traps);
  *       - library scratch is allocated with guard bands of 4 KiB on both
  *         sides, filled with 0xA5 and checked after every call;
