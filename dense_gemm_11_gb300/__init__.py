@@ -552,8 +552,9 @@ def moe_few_tokens(X, router, gate, up, down, Y, top_k: int, *, scales=None, act
         raise ValueError(f"shape mismatch X{tuple(X.shape)} router{tuple(router.shape)} Y{tuple(Y.shape)} (router contiguous)")
     if r_type != x_type and r_type != GEMM_DTYPE_F32:
         raise TypeError("router must have X's type or be float32")
-    I = gate.shape[1] if gate.dim() == 3 else -1
-    w_type = _codes.get(gate.dtype, -1)
+    shape = getattr(gate, "shape", ())
+    I = shape[1] if len(shape) == 3 else -1
+    w_type = _codes.get(getattr(gate, "dtype", None), -1)
     if w_type != x_type and w_type != GEMM_DTYPE_E4M3:
         raise TypeError("gate, up and down must have X's type or be float8_e4m3fn")
     g_ptr = _expert_tensor(gate, "gate", gate.dtype, E, I, H)
@@ -580,7 +581,7 @@ def moe_few_tokens(X, router, gate, up, down, Y, top_k: int, *, scales=None, act
 
 
 def _expert_tensor(t, name, dtype, E, rows, cols):
-    if not t.is_cuda or t.dtype != dtype:
+    if getattr(t, "dtype", None) != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     if t.shape != (E, rows, cols) or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous and {(E, rows, cols)}, got {tuple(t.shape)}")
@@ -589,7 +590,7 @@ def _expert_tensor(t, name, dtype, E, rows, cols):
 
 def _choice(t, name, dtype, T, k):
     import torch
-    if not t.is_cuda or t.dtype != getattr(torch, dtype) or t.shape != (T, k) or not t.is_contiguous():
+    if getattr(t, "dtype", None) != getattr(torch, dtype) or not t.is_cuda or t.shape != (T, k) or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {(T, k)}")
     return t.data_ptr()
 
