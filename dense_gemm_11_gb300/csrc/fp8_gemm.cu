@@ -18,11 +18,11 @@
 //                     of A cost no more than BN >= M columns of accumulator and
 //                     a warp stores 32 consecutive elements of a row of C.
 //                     Bound by op(B)'s bytes and, with the matrices in the L2
-//                     or the product short, by the call: 1 x 4096 x 4096 6.8 us,
-//                     16 x 11008 x 4096 11.2 us, 4.1 TB/s, 64 rows 13.5 us;
+//                     or the product short, by the call: 1 x 4096 x 4096 6.9 us,
+//                     16 x 11008 x 4096 11.6 us, 4.0 TB/s, 64 rows 13.8 us;
 //   fp8_pair_kernel   two CTAs (tcgen05 cta_group::2) a tile of 256 x 256,
-//                     persistent, for many rows: 4096 x 11008 x 4096 142 us,
-//                     2.6 PFLOP/s, its figures at the kernel.  Tiles that would
+//                     persistent, for many rows: 4096 x 11008 x 4096 148 us,
+//                     2.5 PFLOP/s, its figures at the kernel.  Tiles that would
 //                     leave most SMs idle are cut along k; fp8_join_kernel adds.
 //
 // Roles of a CTA: warp 0 issues the TMA loads (operand tiles with the 128-byte
@@ -382,11 +382,12 @@ __global__ void __launch_bounds__(Fp8Cfg<BN, STAGES>::kThreads, Fp8Cfg<BN, STAGE
 // Bound: what the TMA unit brings in and the tensor core reads from shared
 // memory.  TMA delivers 43.6 bytes a clock to an SM, 750 clocks for a block; the
 // groups read 64 KB and TMA writes 32 KB, 750 clocks at 128 bytes each; the
-// multiplication itself takes 512 and the scaling 300.  Measured a block: 815
-// clocks (4096 x 11008 x 4096, 142 us), 770 with B stored K x N (1000 x 4096 x
-// 11008, 35 us).  With a scale for each column 1,340 (4096 x 4096 x 4095, 89 us),
-// and the epilogue is the bound: without the second multiplication it takes 1,190,
-// without reading the columns' scales 1,050, without both 920.
+// multiplication itself takes 512 and the scaling 300.  Measured a block, from
+// a tile's first to its last: 789 clocks (4096 x 11008 x 4096, 148 us), 776 with
+// B stored K x N (1000 x 4096 x 11008, 40.5 us).  With a scale for each column
+// 1,161 (4096 x 4096 x 4095, 91 us), and the epilogue is the bound: of 1,340
+// clocks, counted with the tiles' ends, the second multiplication costs 150,
+// reading the columns' scales 290, both 420.
 constexpr int kPairStages = 5;
 constexpr int kPairEpi = 8;
 constexpr int kPairN = 256;
@@ -712,7 +713,8 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
         for (int t = cid; ok && t < pp.units && !*abort_flag; t += ncl) {
             const Fp8PairUnit unit = fp8_pair_unit<PARTS>(pp, t);
             // The shuffle keeps the compiler from carrying the unit's choice into
-            // the loop below (1,000 clocks a block without it, 815 with).
+            // the loop below (1,000 clocks a block without it, 815 with, counted
+            // with the tiles' ends).
             const int blocks = PARTS ? __shfl_sync(0xffffffffu, unit.blocks, 0) : p.kb_total;
             int m0, n0;
             fp8_pair_origin(pp, unit.tile, m0, n0);
@@ -732,9 +734,11 @@ __global__ void __launch_bounds__(Fp8PairCfg<B_ROWS>::kThreads, 1)
             // column) are added the next is on its way, over the end of a block
             // too, there in registers of its own (GEMM11_TMEM_AHEAD_REGISTERS).
             // A wait is for every read, so only one is in flight: with two
-            // each wait paid for the later one (146 us against 142 for 4096 x
-            // 11008 x 4096).  The accumulator goes back as soon as the block's
-            // last read is in.
+            // each wait paid for the later one (3 % for 4096 x 11008 x 4096).
+            // The accumulator goes back as soon as the block's last read is in.
+            // The registers of its own cost 3.5 % there (148 us against 143 with
+            // a variable), turning the loop so that none is in flight where it
+            // comes round 20 %.
             constexpr int kStep = B_ROWS ? 16 : 32;
             uint32_t r0[kStep], r1[kStep];
             uint64_t fa[8], fb[8];
@@ -1038,10 +1042,12 @@ int pick_splits(int bn, int tiles, int blocks, int rows, int sms, double *time_u
 // through memory, 4.5 us where it is all there is, 12 after a wave (whose last
 // tiles run faster than a full wave, and whose end the next launch fills in
 // part), and 0.16 for each part.  Measured, whole tiles / cut: 2560 x 2048 x 8192
-// (80 tiles) 53.2 / 41.3 us, with a scale for each column 84.0 / 58.3; 1024 x
-// 1024 x 8192 (16) 20.4 in single-CTA tiles / 16.9, and 22.9 / 20.6; left whole
-// 4096 x 11008 x 4096 (688) 141.8 / 144.3, 4096 x 4096 x 4096 (256) 60.5 / 63.0,
-// and in single-CTA tiles 512 x 512 x 11008 (4) 13.2 / 14.3.
+// (80 tiles) 56.3 / 42.9 us, with a scale for each column 84.4 / 60.6; 1024 x
+// 1024 x 8192 (16) 20.3 in single-CTA tiles / 17.6, and 22.9 / 21.4; left whole
+// 4096 x 11008 x 4096 (688) 148.0 / 149.5, 4096 x 4096 x 4096 (256) 62.1 / 64.6.
+// The two models are off by a microsecond or so: 512 x 512 x 11008 (4) takes 13.1
+// in single-CTA tiles and 14.7 cut, which is taken where clusters of 7 CTAs do
+// not all fit at once.
 struct PairPlan {
     int left, parts;  // tiles to cut, units of each
     double time_us;

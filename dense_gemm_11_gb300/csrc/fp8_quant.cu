@@ -22,8 +22,8 @@
 //           of 33 words: neither side has bank conflicts);
 //   blocks  a CTA holds one 128 x 128 block.
 // Measured on BF16 of 4096 x 11008 (135 MB read and written, several such
-// matrices in turn): rows 28.0 us, cols 29.5, blocks 27.8, 4.6 to 4.9 TB/s; on
-// FP32 of 11008 x 4096, 225 MB, blocks takes 35.9 us, 6.3 TB/s; rows of 16 x
+// matrices in turn): rows 28.7 us, cols 30.1, blocks 28.5, 4.5 to 4.7 TB/s; on
+// FP32 of 11008 x 4096, 225 MB, blocks takes 36.6 us, 6.2 TB/s; rows of 16 x
 // 4096, one wave of small CTAs, 1.5 us.
 #include <algorithm>
 

@@ -1082,9 +1082,9 @@ bool encode_expert_maps(CUtensorMap *many, CUtensorMap *one, int *flat, const vo
 // expert that is used), `k` long; `act_bytes` of activations in a stage with
 // WR = 1.  Preferred is the largest WR, then the fewest splits, whose units
 // fill whole rounds over the SMs to 80 %; failing that, what fills them best.
-// (64 tokens, 64 experts of 2048 x 1024, 6 each: 111.7 us with WR = 16 at 84 %,
-// 117.9 with the best 90 % filling; 52 tokens, 23 experts of 352 x 880, 7 each:
-// 43.6 against 50.5; at 70 % one token over 8 experts took 122 us, 117 at 80 %.)
+// (64 tokens, 64 experts of 2048 x 1024, 6 each: 104 us with WR = 16 at 84 %, 110
+// with WR = 8 at 96 %; 52 tokens, 23 experts of 352 x 880, 7 each: 41 at 83 %, 56
+// with WR = 1 at 95 %; one token over 8 experts: 104 us at 75 %, 98 at 91 %.)
 // WR is at least what keeps a stage's activations within its weights (the ring
 // would hold too few stages) and a stage's k below the whole length; 16 only
 // where a unit of 8 would have fewer than 12 stages, over which to hide its end.
@@ -1157,7 +1157,9 @@ cudaError_t launch_moe(const Moe &m, MoeArgs a, double active, cudaStream_t stre
 
 // 8 tokens a unit up to 6.5 tokens an expert, where a second unit for an expert
 // with more costs less than accumulators that mostly stay empty (64 tokens over
-// 64 experts, 6 each: 103 us against 108 with 16 a unit), else 16.
+// 64 experts, 6 each: 104 us against 114 with 16 a unit), else 16 (52 tokens over
+// 23 experts, 7 each, 15.8 an expert: 41.0 us against 42.6 with 8, and with BF16
+// weights 40.3 against 47.0).
 template <int XT, bool FP8>
 cudaError_t launch_moe_tokens(const Moe &m, const MoeArgs &a, double active, double tokens, cudaStream_t stream) {
     return tokens <= 6.5 ? launch_moe<XT, FP8, 1>(m, a, active, stream) : launch_moe<XT, FP8, 2>(m, a, active, stream);
