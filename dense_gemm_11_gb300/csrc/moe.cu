@@ -570,7 +570,9 @@ struct MoeCfg {
     }
 };
 
-// This warp's 16 rows x one box of k times the tokens, added to c.  Thread
+// This warp's 16 rows x one box of k times the tokens, added to c (a box's own
+// sums: the matrix instruction's additions truncate, and 11008 k in one chain
+// of them left 7e-6 of the result, boxes added to nearest 4e-7).  Thread
 // (g, t) holds rows g and g + 8, token 8 n + g and the same k's of both; w0 and
 // w1 are the first of each 8 rows (16-byte chunk c of row g at c ^ g, by the
 // copy's swizzle), act[n] its token's k's of this box; USED of the NT groups of
@@ -880,23 +882,24 @@ __global__ void __launch_bounds__(moe_threads(NT), 1)
 #pragma unroll
                     for (int i = 0; i < NT; ++i) act[i] = st + token_at[i];
                     float sum[NT][4] = {};
-                    float(&to)[NT][4] = FP8 ? sum : acc;
                     if (valid < Cfg::kBoxK)
-                        multiply_box<XT, FP8, NT, NT, kParts, true>(w, w + row8, act, valid, to);
+                        multiply_box<XT, FP8, NT, NT, kParts, true>(w, w + row8, act, valid, sum);
                     else if (NT > 1 && n.count <= 8)
-                        multiply_box<XT, FP8, NT, 1, kParts, false>(w, w + row8, act, valid, to);
+                        multiply_box<XT, FP8, NT, 1, kParts, false>(w, w + row8, act, valid, sum);
                     else
-                        multiply_box<XT, FP8, NT, NT, kParts, false>(w, w + row8, act, valid, to);
+                        multiply_box<XT, FP8, NT, NT, kParts, false>(w, w + row8, act, valid, sum);
+                    // the scales of a box's rows
+                    float s0 = 1.f, s1 = 1.f;
                     if constexpr (FP8) {
                         const float *sc = reinterpret_cast<const float *>(st + kStageWeights) + warp;
-                        const float s0 = sc[0], s1 = sc[kBoxes];
+                        s0 = sc[0], s1 = sc[kBoxes];
+                    }
 #pragma unroll
-                        for (int i = 0; i < NT; ++i) {
-                            acc[i][0] = fmaf(s0, sum[i][0], acc[i][0]);
-                            acc[i][1] = fmaf(s0, sum[i][1], acc[i][1]);
-                            acc[i][2] = fmaf(s1, sum[i][2], acc[i][2]);
-                            acc[i][3] = fmaf(s1, sum[i][3], acc[i][3]);
-                        }
+                    for (int i = 0; i < NT; ++i) {
+                        acc[i][0] = fmaf(s0, sum[i][0], acc[i][0]);
+                        acc[i][1] = fmaf(s0, sum[i][1], acc[i][1]);
+                        acc[i][2] = fmaf(s1, sum[i][2], acc[i][2]);
+                        acc[i][3] = fmaf(s1, sum[i][3], acc[i][3]);
                     }
                 }
                 __syncwarp();
