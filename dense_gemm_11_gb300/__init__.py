@@ -14,6 +14,13 @@ fallback: if the shared library is missing, every call raises.
     fp8_quantize(X, Q, S, layout="rows")              X held in 8 bits with an FP32 scale for each block of 128
     gemm_fp8(A, SA, B, SB, C, ..., b_trans=True)      the product of two matrices held that way
     moe_few_tokens(X, router, gate, up, down, Y, k)   a mixture-of-experts layer for a few tokens, one launch
+    moe_dispatch(ids, X, Xs, offsets, rows)           the tokens' rows of such a layer, sorted by expert
+    moe_combine(Ys, rows, Y, weights=None)            the experts' rows back to their tokens
+    moe_combine_grad(dY, Ys, rows, weights, dYs, dw)  and the gradient of that
+    gemm_grouped(A, B, C, offsets, ...)               every expert's rows times its matrix
+    gemm_grouped_wgrad(A, B, C, offsets, ...)         the gradient of every expert's matrix
+    fp8_gated_act(G, U, H, GQ, GS, UQ, US)            act(g) u, and g and u kept in 8 bits
+    fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU)    its backward pass from these
 
 Tensors are torch CUDA tensors on the current device; A and B may be 2-D
 views with a leading dimension larger than their width (unit column stride).
@@ -62,6 +69,8 @@ class TuneEntry(ctypes.Structure):
 EXPORTED_SYMBOLS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_f16_f32acc_epilogue", "gemm_bf16_f32acc_epilogue",
                     "gemm_tc_f32acc_epilogue", "gemm_tc_strided_batched", "gemm_f16_f32acc_epilogue_noalloc",
                     "gemm_fp8_quantize_block128", "gemm_fp8_block128", "gemm_moe_few_tokens",
+                    "gemm_moe_dispatch", "gemm_moe_combine", "gemm_moe_combine_grad", "gemm_grouped_f32acc",
+                    "gemm_grouped_wgrad_f32acc", "gemm_fp8_gated_act", "gemm_fp8_gated_act_grad",
                     "gemm_tune_set", "gemm_tune_get",
                     "gemm_status_string", "gemm_last_cuda_error", "gemm_check", "gemm_watchdog_selftest",
                     "gemm_last_plan", "gemm_last_launch_count", "gemm_tc_rate_probe",
@@ -130,6 +139,28 @@ def lib():
             L.gemm_moe_few_tokens.argtypes = [c_int, c_int, c_int, c_int, c_int, c_void_p, c_int, c_ll, c_void_p, c_int,
                                               c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int,
                                               c_int, c_void_p, c_int, c_ll, c_void_p, c_void_p, c_void_p]
+            L.gemm_moe_dispatch.restype = c_int
+            L.gemm_moe_dispatch.argtypes = [c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_ll, c_void_p, c_ll, c_void_p,
+                                            c_void_p, c_void_p]
+            L.gemm_moe_combine.restype = c_int
+            L.gemm_moe_combine.argtypes = [c_int, c_int, c_int, c_int, c_void_p, c_int, c_ll, c_void_p, c_void_p, c_void_p, c_ll,
+                                           c_void_p]
+            L.gemm_moe_combine_grad.restype = c_int
+            L.gemm_moe_combine_grad.argtypes = [c_int, c_int, c_int, c_int, c_void_p, c_int, c_ll, c_void_p, c_ll, c_void_p,
+                                                c_void_p, c_void_p, c_ll, c_void_p, c_void_p]
+            L.gemm_grouped_f32acc.restype = c_int
+            L.gemm_grouped_f32acc.argtypes = [c_int, c_int, c_int, c_int, c_float, c_void_p, c_ll, c_void_p, c_ll, c_ll, c_int,
+                                              c_int, c_float, c_void_p, c_int, c_ll, c_void_p, c_void_p]
+            L.gemm_grouped_wgrad_f32acc.restype = c_int
+            L.gemm_grouped_wgrad_f32acc.argtypes = [c_int, c_int, c_int, c_int, c_float, c_void_p, c_ll, c_void_p, c_ll, c_int,
+                                                    c_float, c_void_p, c_int, c_ll, c_ll, c_void_p, c_void_p]
+            L.gemm_fp8_gated_act.restype = c_int
+            L.gemm_fp8_gated_act.argtypes = [c_int, c_int, c_void_p, c_ll, c_void_p, c_ll, c_int, c_void_p, c_ll, c_void_p, c_ll,
+                                             c_void_p, c_ll, c_void_p, c_ll, c_void_p, c_ll, c_int, c_int, c_void_p]
+            L.gemm_fp8_gated_act_grad.restype = c_int
+            L.gemm_fp8_gated_act_grad.argtypes = [c_int, c_int, c_void_p, c_ll, c_int, c_void_p, c_ll, c_void_p, c_ll, c_void_p,
+                                                  c_ll, c_void_p, c_ll, c_int, c_void_p, c_ll, c_void_p, c_ll, c_void_p, c_ll,
+                                                  c_int, c_void_p]
             L.gemm_tune_set.restype = c_int
             L.gemm_tune_set.argtypes = [ctypes.POINTER(TuneEntry), c_int]
             L.gemm_tune_get.restype = c_int
@@ -600,6 +631,259 @@ def _vector(t, name, n):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous CUDA float32 tensor of length {n}")
     return t.data_ptr()
+
+
+def _one_device(*tensors):
+    """All on the current device, whose kernels and streams the library uses."""
+    import torch
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"every tensor must be on the current device, cuda:{here}; got one on {t.device}")
+
+
+def _int32(t, name, shape):
+    """Pointer of a contiguous int32 tensor of this shape."""
+    if not _codes:
+        _load_codes()
+    import torch
+    if getattr(t, "dtype", None) != torch.int32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA int32 tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _slots(t, name):
+    """(pointer, T, top_k) of a contiguous (T, top_k) int32 tensor."""
+    shape = getattr(t, "shape", ())
+    ptr = _int32(t, name, shape)
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be (T, top_k) with top_k >= 1, got {tuple(shape)}")
+    return ptr, shape[0], shape[1]
+
+
+def _offsets(t):
+    """(pointer, E) of the offsets of E experts' rows."""
+    shape = getattr(t, "shape", ())
+    ptr = _int32(t, "offsets", shape)
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError(f"offsets must be (E + 1,), got {tuple(shape)}")
+    return ptr, shape[0] - 1
+
+
+def _slot_weights(t, name, T, k):
+    import torch
+    if getattr(t, "dtype", None) != torch.float32 or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA float32 tensor")
+    if t.shape != (T, k) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {(T, k)}, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _expert_mats(t, name, allowed):
+    """(pointer, row stride, matrix stride, E, rows, cols, type code) of a 3-D CUDA tensor of row-major matrices."""
+    if not _codes:
+        _load_codes()
+    code = _codes.get(getattr(t, "dtype", None), -1)
+    if code not in allowed or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in allowed)}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be 3-D")
+    E, rows, cols = shape
+    step, ld, one = stride
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} needs unit column stride")
+    if ld < cols:
+        _check_rows(name, rows, cols, ld)
+        ld = cols
+    size = (rows - 1) * ld + cols
+    if E > 1 and rows > 0 and cols > 0 and step < size:
+        raise ValueError(f"{name} needs matrices that share no memory, got stride {step} for {rows} x {cols} (an expanded tensor?)")
+    return t.data_ptr(), ld or 1, max(step, 1), E, rows, cols, code
+
+
+def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
+    """The choice of a router sorted by expert, and the tokens' rows copied into that order.
+
+    ids: (T, top_k) int32, the experts of every token (moe_few_tokens writes them, any router may); an id outside
+    0 .. E - 1 chooses none.  offsets: (E + 1,) int32, receives where each expert's rows start.  rows: (T, top_k) int32,
+    receives the row of every slot (-1: none); slots of one expert keep their order.
+    X: (T, H) fp32, fp16 or bf16; Xs: the same type and width, at least T * top_k rows, receives Xs[rows[t, j]] = X[t]
+    (rows from offsets[E] on stay as they are).  X=None and Xs=None: the order alone.
+    Limits: E <= 4096, top_k <= 128.
+    """
+    ids_ptr, T, k = _slots(ids, "ids")
+    off_ptr, E = _offsets(offsets)
+    rows_ptr = _int32(rows, "rows", (T, k))
+    x_ptr = xs_ptr = None
+    H, x_type, ldx, ldxs = 0, GEMM_DTYPE_F32, 1, 1
+    if X is not None or Xs is not None:
+        x_ptr, ldx, x_rows, H, x_type = _typed_mat(X, "X", _FLOATS)
+        xs_ptr, ldxs, xs_rows, xs_cols, xs_type = _typed_mat(Xs, "Xs", _FLOATS)
+        if xs_type != x_type:
+            raise TypeError("X and Xs must have one type")
+        if x_rows != T or xs_cols != H or xs_rows < T * k:
+            raise ValueError(f"shape mismatch ids{(T, k)} X{tuple(X.shape)} Xs{tuple(Xs.shape)} (at least T * top_k rows)")
+    _one_device(ids, X, Xs, offsets, rows)
+    st = lib().gemm_moe_dispatch(T, E, k, H, ids_ptr, x_ptr, x_type, ldx, xs_ptr, ldxs, off_ptr, rows_ptr, _stream_ptr(stream, ids))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_moe_dispatch")
+
+
+def moe_combine(Ys, rows, Y, weights=None, *, stream=None) -> None:
+    """Y[t] = sum_j weights[t, j] * Ys[rows[t, j]], added in fp32 in the order of the slots.
+
+    Ys: (R, H), Y: (T, H), both fp32, fp16 or bf16.  rows: (T, top_k) int32 (moe_dispatch); a slot without a row adds
+    nothing.  weights: (T, top_k) fp32, or None: ones, which also makes this the gradient of moe_dispatch's copy.
+    """
+    ys_ptr, ldys, R, H, y_type = _typed_mat(Ys, "Ys", _FLOATS)
+    y_ptr, ldy, T, y_cols, code = _typed_mat(Y, "Y", _FLOATS)
+    rows_ptr, r_T, k = _slots(rows, "rows")
+    if code != y_type:
+        raise TypeError("Ys and Y must have one type")
+    if r_T != T or y_cols != H:
+        raise ValueError(f"shape mismatch Ys{tuple(Ys.shape)} rows{tuple(rows.shape)} Y{tuple(Y.shape)}")
+    w_ptr = None if weights is None else _slot_weights(weights, "weights", T, k)
+    _one_device(Ys, rows, Y, weights)
+    st = lib().gemm_moe_combine(T, k, H, R, ys_ptr, y_type, ldys, rows_ptr, w_ptr, y_ptr, ldy, _stream_ptr(stream, Y))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_moe_combine")
+
+
+def moe_combine_grad(dY, Ys, rows, weights, dYs, dweights, *, stream=None) -> None:
+    """The gradient of moe_combine: dYs[rows[t, j]] = weights[t, j] * dY[t], dweights[t, j] = <dY[t], Ys[rows[t, j]]>.
+
+    dY: (T, H), Ys and dYs: (R, H), one type; rows: (T, top_k) int32; weights and dweights: (T, top_k) fp32.  A slot
+    without a row gets dweights 0; rows of dYs that no slot names stay as they are.
+    """
+    dy_ptr, lddy, T, H, code = _typed_mat(dY, "dY", _FLOATS)
+    ys_ptr, ldys, R, ys_cols, ys_type = _typed_mat(Ys, "Ys", _FLOATS)
+    dys_ptr, lddys, dys_rows, dys_cols, dys_type = _typed_mat(dYs, "dYs", _FLOATS)
+    rows_ptr, r_T, k = _slots(rows, "rows")
+    if ys_type != code or dys_type != code:
+        raise TypeError("dY, Ys and dYs must have one type")
+    if r_T != T or ys_cols != H or (dys_rows, dys_cols) != (R, H):
+        raise ValueError(f"shape mismatch dY{tuple(dY.shape)} Ys{tuple(Ys.shape)} rows{tuple(rows.shape)} dYs{tuple(dYs.shape)}")
+    w_ptr, dw_ptr = _slot_weights(weights, "weights", T, k), _slot_weights(dweights, "dweights", T, k)
+    _one_device(dY, Ys, rows, weights, dYs, dweights)
+    st = lib().gemm_moe_combine_grad(T, k, H, R, dy_ptr, code, lddy, ys_ptr, ldys, rows_ptr, w_ptr, dys_ptr, lddys, dw_ptr,
+                                     _stream_ptr(stream, dY))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_moe_combine_grad")
+
+
+def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, *, b_trans: bool = True, stream=None) -> None:
+    """C[r] = alpha * A[r] @ op(B[e]) + beta * C[r] for the rows offsets[e] <= r < offsets[e + 1] of every expert e.
+
+    A: (R, K), C: (R, N).  B: (E, N, K), op(B) = B^T, or (E, K, N) with b_trans=False.  A and B both fp16 or both bf16,
+    C fp32, fp16 or bf16.  offsets: (E + 1,) int32 on the device, not descending, from 0 to R (moe_dispatch); rows of C
+    that no expert has stay as they are.  A's and B's rows start on 16-byte boundaries (row strides multiples of 8).
+    So y = x W^T of every expert takes W as it is, and dx = dy W the same W with b_trans=False.
+    """
+    a_ptr, lda, R, K, a_type = _typed_mat(A, "A", _HALFS)
+    b_ptr, ldb, stride_b, E, b_rows, b_cols, b_type = _expert_mats(B, "B", _HALFS)
+    c_ptr, ldc, c_rows, N, c_type = _typed_mat(C, "C", _FLOATS)
+    off_ptr, off_E = _offsets(offsets)
+    if a_type != b_type:
+        raise TypeError("A and B must both be float16 or both bfloat16")
+    if c_rows != R or off_E != E or (b_rows, b_cols) != ((N, K) if b_trans else (K, N)):
+        raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
+    _one_device(A, B, C, offsets)
+    st = lib().gemm_grouped_f32acc(E, R, N, K, alpha, a_ptr, lda, b_ptr, ldb, stride_b, a_type, 1 if b_trans else 0, beta, c_ptr,
+                                   c_type, ldc, off_ptr, _stream_ptr(stream, A))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped_f32acc")
+
+
+def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, *, stream=None) -> None:
+    """C[e] = alpha * A[rows of e]^T @ B[rows of e] + beta * C[e] for every expert e (rows offsets[e] .. offsets[e + 1] - 1).
+
+    A: (R, M), B: (R, N), both fp16 or both bf16; C: (E, M, N) fp32, fp16 or bf16.  An expert without rows gets
+    beta * C[e].  So dW = dy^T x of every expert takes dy as A and x as B.  offsets and alignment as for gemm_grouped.
+    """
+    a_ptr, lda, R, M, a_type = _typed_mat(A, "A", _HALFS)
+    b_ptr, ldb, b_rows, N, b_type = _typed_mat(B, "B", _HALFS)
+    c_ptr, ldc, stride_c, E, c_rows, c_cols, c_type = _expert_mats(C, "C", _FLOATS)
+    off_ptr, off_E = _offsets(offsets)
+    if a_type != b_type:
+        raise TypeError("A and B must both be float16 or both bfloat16")
+    if b_rows != R or off_E != E or (c_rows, c_cols) != (M, N):
+        raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
+    _one_device(A, B, C, offsets)
+    st = lib().gemm_grouped_wgrad_f32acc(E, R, M, N, alpha, a_ptr, lda, b_ptr, ldb, a_type, beta, c_ptr, c_type, ldc, stride_c,
+                                         off_ptr, _stream_ptr(stream, A))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_grouped_wgrad_f32acc")
+
+
+def _kept(Q, S, names, rows, cols, q_type=None):
+    """(pointer, row stride, type) of Q and (pointer, row stride) of S, a rows x cols matrix in 8 bits (layout "rows")."""
+    q_ptr, ldq, q_rows, q_cols, code = _typed_mat(Q, names[0], _FP8S)
+    s_ptr, lds, s_rows, s_cols, _ = _typed_mat(S, names[1], _F32)
+    if ((q_rows, q_cols), (s_rows, s_cols)) != _fp8_shapes(rows, cols, "rows"):
+        raise ValueError(f"{names[0]}{tuple(Q.shape)} and {names[1]}{tuple(S.shape)} do not hold {rows} x {cols} in layout 'rows'")
+    if q_type is not None and code != q_type:
+        raise TypeError("GQ and UQ must have one type")
+    return q_ptr, ldq, code, s_ptr, lds
+
+
+def _same(t, name, rows, cols, code):
+    """(pointer, row stride) of a rows x cols matrix of type `code`."""
+    ptr, ld, r, c, _ = _typed_mat(t, name, (code,))
+    if (r, c) != (rows, cols):
+        raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
+    return ptr, ld
+
+
+def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *, stream=None) -> None:
+    """H = act(G) * U, and G and U kept in 8 bits for fp8_gated_act_grad.
+
+    G, U, H: (rows, cols), one type, fp32, fp16 or bf16.  GQ, GS and UQ, US receive what fp8_quantize makes of G and U
+    with layout "rows" (fp8_empty() makes fitting pairs).  U=None (and UQ=US=None): H = act(G).  act: any GEMM_ACT_*.
+    """
+    g_ptr, ldg, rows, cols, code = _typed_mat(G, "G", _FLOATS)
+    h_ptr, ldh = _same(H, "H", rows, cols, code)
+    gq_ptr, ldgq, q_type, gs_ptr, ldgs = _kept(GQ, GS, ("GQ", "GS"), rows, cols)
+    u_ptr = uq_ptr = us_ptr = None
+    ldu = lduq = ldus = 1
+    if U is not None:
+        u_ptr, ldu = _same(U, "U", rows, cols, code)
+        uq_ptr, lduq, _, us_ptr, ldus = _kept(UQ, US, ("UQ", "US"), rows, cols, q_type)
+    elif UQ is not None or US is not None:
+        raise ValueError("UQ and US are for a gate: without U they must be None")
+    _one_device(G, U, H, GQ, GS, UQ, US)
+    st = lib().gemm_fp8_gated_act(rows, cols, g_ptr, ldg, u_ptr, ldu, code, h_ptr, ldh, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq,
+                                  us_ptr, ldus, q_type, act, _stream_ptr(stream, G))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp8_gated_act")
+
+
+def fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU, H=None, act: int = GEMM_ACT_SILU, *, stream=None) -> None:
+    """The backward pass of fp8_gated_act from its 8-bit copies g' = GQ * GS and u' = UQ * US.
+
+    dG = dH * u' * act'(g'), dU = dH * act(g'), and, with H given, H = act(g') * u' again (for the gradient of the
+    weights that H is multiplied by).  dH, dG, dU, H: (rows, cols), one type, fp32, fp16 or bf16.
+    Without a gate UQ, US and dU are None, and u' is 1.
+    """
+    dh_ptr, lddh, rows, cols, code = _typed_mat(dH, "dH", _FLOATS)
+    gq_ptr, ldgq, q_type, gs_ptr, ldgs = _kept(GQ, GS, ("GQ", "GS"), rows, cols)
+    dg_ptr, lddg = _same(dG, "dG", rows, cols, code)
+    uq_ptr = us_ptr = du_ptr = h_ptr = None
+    lduq = ldus = lddu = ldh = 1
+    if UQ is not None:
+        uq_ptr, lduq, _, us_ptr, ldus = _kept(UQ, US, ("UQ", "US"), rows, cols, q_type)
+        du_ptr, lddu = _same(dU, "dU", rows, cols, code)
+    elif US is not None or dU is not None:
+        raise ValueError("US and dU are for a gate: without UQ they must be None")
+    if H is not None:
+        h_ptr, ldh = _same(H, "H", rows, cols, code)
+    _one_device(dH, GQ, GS, UQ, US, dG, dU, H)
+    st = lib().gemm_fp8_gated_act_grad(rows, cols, dh_ptr, lddh, code, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq, us_ptr, ldus,
+                                       q_type, dg_ptr, lddg, du_ptr, lddu, h_ptr, ldh, act, _stream_ptr(stream, dH))
+    if st != GEMM_OK:
+        raise GemmError(st, "gemm_fp8_gated_act_grad")
 
 
 def tune_set(entries) -> None:

@@ -13,6 +13,7 @@
 #include <vector>
 
 #include "../../include/gemm11.h"
+#include "experts.h"
 #include "fp8.h"
 #include "internal.h"
 #include "ptx.cuh"
@@ -548,10 +549,33 @@ namespace {
 
 bool valid_act(int act) { return act >= GEMM_ACT_NONE && act <= GEMM_ACT_GELU_TANH; }
 bool valid_fp8(int type) { return type == GEMM_DTYPE_E4M3 || type == GEMM_DTYPE_E5M2; }
+bool valid_float(int type) { return type == GEMM_DTYPE_F32 || type == GEMM_DTYPE_F16 || type == GEMM_DTYPE_BF16; }
 
 // The largest extent of a matrix held in 8 bits: the kernels' indices run over
 // the end of one by less than two tiles.
 constexpr int kMaxExtent = 0x7FFFFFFF - 511;
+
+// Slots of a token that the mixture-of-experts operators for many tokens take.
+constexpr int kRowsMaxTopK = 128;
+
+// Row strides of the tensor-memory-access path end at 2^40 bytes.
+constexpr long long kMaxStride = 1LL << 38;
+
+// Products over sorted rows: no extent, and no number of tiles, beyond 32 bits
+// (a and b are those of a result; every expert may have a tile that is not full).
+bool grouped_fits(int E, int a, int b, int k) {
+    if (E > kMaxExtent || a > kMaxExtent || b > kMaxExtent || k > kMaxExtent) return false;
+    const double tiles = static_cast<double>(E) * (a / 256 + 1) * (b / 256 + 1);
+    return tiles < 2147483647.0;
+}
+
+bool gated_args_valid(int rows, int cols, int type, int q_type, int act) {
+    return rows >= 0 && cols >= 0 && valid_float(type) && valid_fp8(q_type) && (valid_act(act) || act == GEMM_ACT_SILU);
+}
+// The grid has one dimension: blocks of 16 rows x 128 columns.
+bool gated_fits(int rows, int cols) {
+    return rows <= kMaxExtent && cols <= kMaxExtent && ((rows + 15LL) / 16) * ((cols + 127LL) / 128) <= kMaxExtent;
+}
 
 // A call with an empty result.
 int noop() {
@@ -843,6 +867,270 @@ int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const void *X, in
     CallInfo info;
     const cudaError_t e = run_moe(m, s, &info);
     if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids, const void *X, int x_type, long long ldx, void *Xs,
+                      long long ldxs, int *offsets, int *rows, void *stream) {
+    if (T < 0 || E < 0 || H < 0 || top_k < 1 || !valid_float(x_type)) return GEMM_ERR_INVALID_ARG;
+    const bool copy = H > 0 && (X || Xs);
+    if (copy && (ldx < H || ldxs < H)) return GEMM_ERR_INVALID_ARG;
+    if (!offsets || (T > 0 && (!ids || !rows || (copy && (!X || !Xs))))) return GEMM_ERR_INVALID_ARG;
+    if (T > kMaxExtent || H > kMaxExtent / 4 || E > kDispatchMaxExperts || top_k > kRowsMaxTopK ||
+        static_cast<long long>(T) * top_k > kMaxExtent)
+        return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    MoeDispatch d;
+    d.T = T;
+    d.E = E;
+    d.top_k = top_k;
+    d.H = copy && T > 0 ? H : 0;
+    d.ids = ids;
+    d.X = X;
+    d.x_type = x_type;
+    d.ldx = ldx;
+    d.Xs = Xs;
+    d.ldxs = ldxs;
+    d.offsets = offsets;
+    d.rows = rows;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_moe_dispatch(d, s, &info);
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, long long ldys, const int *rows,
+                     const float *weights, void *Y, long long ldy, void *stream) {
+    if (T < 0 || H < 0 || R < 0 || top_k < 1 || !valid_float(type)) return GEMM_ERR_INVALID_ARG;
+    if (ldys < std::max(1, H) || ldy < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
+    if (T == 0 || H == 0) return noop();
+    if (!rows || !Y || (R > 0 && !Ys)) return GEMM_ERR_INVALID_ARG;
+    if (T > kMaxExtent || H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK) return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    MoeCombine c;
+    c.T = T;
+    c.top_k = top_k;
+    c.H = H;
+    c.R = R;
+    c.Ys = Ys;
+    c.type = type;
+    c.ldys = ldys;
+    c.rows = rows;
+    c.weights = weights;
+    c.Y = Y;
+    c.ldy = ldy;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_moe_combine(c, s, &info);
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void *dY, int type, long long lddy, const void *Ys,
+                          long long ldys, const int *rows, const float *weights, void *dYs, long long lddys,
+                          float *dweights, void *stream) {
+    if (T < 0 || H < 0 || R < 0 || top_k < 1 || !valid_float(type)) return GEMM_ERR_INVALID_ARG;
+    if (lddy < std::max(1, H) || ldys < std::max(1, H) || lddys < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
+    if (T == 0) return noop();
+    if (!rows || !weights || !dweights || (H > 0 && (!dY || (R > 0 && (!Ys || !dYs))))) return GEMM_ERR_INVALID_ARG;
+    if (T > kMaxExtent || H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK) return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    MoeCombine c;
+    c.T = T;
+    c.top_k = top_k;
+    c.H = H;
+    c.R = R;
+    c.Ys = Ys;
+    c.type = type;
+    c.ldys = ldys;
+    c.rows = rows;
+    c.weights = weights;
+    c.Y = const_cast<void *>(dY);
+    c.ldy = lddy;
+    c.dYs = dYs;
+    c.lddys = lddys;
+    c.dweights = dweights;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_moe_combine_grad(c, s, &info);
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, const void *A, long long lda, const void *B,
+                        long long ldb, long long stride_b, int ab_type, int b_trans, float beta, void *C, int c_type,
+                        long long ldc, const int *offsets, void *stream) {
+    if (E < 0 || R < 0 || N < 0 || K < 0 || (b_trans != 0 && b_trans != 1)) return GEMM_ERR_INVALID_ARG;
+    if ((ab_type != GEMM_DTYPE_F16 && ab_type != GEMM_DTYPE_BF16) || !valid_float(c_type)) return GEMM_ERR_INVALID_ARG;
+    const int b_rows = b_trans ? N : K, b_cols = b_trans ? K : N;
+    if (lda < std::max(1, K) || ldb < std::max(1, b_cols) || ldc < std::max(1, N)) return GEMM_ERR_INVALID_ARG;
+    if (E > 1 && b_rows > 0 && b_cols > 0 && stride_b < (b_rows - 1LL) * ldb + b_cols) return GEMM_ERR_INVALID_ARG;
+    if (E == 0 || R == 0 || N == 0) return noop();
+    const bool product = K > 0 && alpha != 0.f;
+    if (!C || !offsets || (product && (!A || !B))) return GEMM_ERR_INVALID_ARG;
+    if (!grouped_fits(E, R, N, K)) return GEMM_ERR_UNSUPPORTED;
+    auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+    if (product && !(al16(A) && al16(B) && (R == 1 || lda % 8 == 0) && (b_rows == 1 || ldb % 8 == 0) && (E == 1 || stride_b % 8 == 0) &&
+                     lda < kMaxStride && ldb < kMaxStride && (E == 1 || stride_b < kMaxStride)))
+        return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    Grouped g;
+    g.E = E;
+    g.R = R;
+    g.N = N;
+    g.K = K;
+    g.alpha = alpha;
+    g.A = A;
+    g.lda = R == 1 ? K : lda;
+    g.B = B;
+    g.ldb = b_rows == 1 ? b_cols : ldb;
+    g.stride_b = E == 1 ? g.ldb * b_rows : stride_b;
+    g.bf16 = ab_type == GEMM_DTYPE_BF16;
+    g.b_trans = b_trans;
+    g.beta = beta;
+    g.C = C;
+    g.c_type = c_type;
+    g.ldc = ldc;
+    g.offsets = offsets;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_grouped(g, s, &info);
+    if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha, const void *A, long long lda, const void *B,
+                              long long ldb, int ab_type, float beta, void *C, int c_type, long long ldc,
+                              long long stride_c, const int *offsets, void *stream) {
+    if (E < 0 || R < 0 || M < 0 || N < 0) return GEMM_ERR_INVALID_ARG;
+    if ((ab_type != GEMM_DTYPE_F16 && ab_type != GEMM_DTYPE_BF16) || !valid_float(c_type)) return GEMM_ERR_INVALID_ARG;
+    if (lda < std::max(1, M) || ldb < std::max(1, N) || ldc < std::max(1, N)) return GEMM_ERR_INVALID_ARG;
+    if (E > 1 && M > 0 && N > 0 && stride_c < (M - 1LL) * ldc + N) return GEMM_ERR_INVALID_ARG;
+    if (E == 0 || M == 0 || N == 0) return noop();
+    const bool product = R > 0 && alpha != 0.f;
+    if (!C || !offsets || (product && (!A || !B))) return GEMM_ERR_INVALID_ARG;
+    if (!grouped_fits(E, M, N, R)) return GEMM_ERR_UNSUPPORTED;
+    auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
+    if (product && !(al16(A) && al16(B) && (R == 1 || (lda % 8 == 0 && ldb % 8 == 0)) && lda < kMaxStride && ldb < kMaxStride))
+        return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    Grouped g;
+    g.wgrad = 1;
+    g.E = E;
+    g.R = R;
+    g.M = M;
+    g.N = N;
+    g.alpha = alpha;
+    g.A = A;
+    g.lda = R == 1 ? M : lda;
+    g.B = B;
+    g.ldb = R == 1 ? N : ldb;
+    g.bf16 = ab_type == GEMM_DTYPE_BF16;
+    g.beta = beta;
+    g.C = C;
+    g.c_type = c_type;
+    g.ldc = ldc;
+    g.stride_c = E == 1 ? ldc * M : stride_c;
+    g.offsets = offsets;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_grouped(g, s, &info);
+    if (e == cudaErrorNotSupported) return GEMM_ERR_UNSUPPORTED;
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_fp8_gated_act(int rows, int cols, const void *G, long long ldg, const void *U, long long ldu, int type, void *H,
+                       long long ldh, void *GQ, long long ldgq, float *GS, long long ldgs, void *UQ, long long lduq,
+                       float *US, long long ldus, int q_type, int act, void *stream) {
+    if (!gated_args_valid(rows, cols, type, q_type, act)) return GEMM_ERR_INVALID_ARG;
+    const int c = std::max(1, cols), r = std::max(1, rows);
+    if (ldg < c || ldh < c || ldgq < c || ldgs < r || (U && (ldu < c || lduq < c || ldus < r))) return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return noop();
+    if (!G || !H || !GQ || !GS || (U && (!UQ || !US)) || (!U && (UQ || US))) return GEMM_ERR_INVALID_ARG;
+    if (!gated_fits(rows, cols)) return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    GatedAct a;
+    a.rows = rows;
+    a.cols = cols;
+    a.G = G;
+    a.ldg = ldg;
+    a.U = U;
+    a.ldu = ldu;
+    a.type = type;
+    a.H = H;
+    a.ldh = ldh;
+    a.GQ = GQ;
+    a.ldgq = ldgq;
+    a.GS = GS;
+    a.ldgs = ldgs;
+    a.UQ = UQ;
+    a.lduq = lduq;
+    a.US = US;
+    a.ldus = ldus;
+    a.q_type = q_type;
+    a.act = act;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_gated_act(a, s, &info);
+    if (e != cudaSuccess) return fail_cuda(e);
+    return finish_call(info, s);
+}
+
+int gemm_fp8_gated_act_grad(int rows, int cols, const void *dH, long long lddh, int type, const void *GQ, long long ldgq,
+                            const float *GS, long long ldgs, const void *UQ, long long lduq, const float *US,
+                            long long ldus, int q_type, void *dG, long long lddg, void *dU, long long lddu, void *H,
+                            long long ldh, int act, void *stream) {
+    if (!gated_args_valid(rows, cols, type, q_type, act)) return GEMM_ERR_INVALID_ARG;
+    const int c = std::max(1, cols), r = std::max(1, rows);
+    if (lddh < c || lddg < c || ldgq < c || ldgs < r || (UQ && (lddu < c || lduq < c || ldus < r)) || (H && ldh < c))
+        return GEMM_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return noop();
+    if (!dH || !GQ || !GS || !dG || (UQ && (!US || !dU)) || (!UQ && (US || dU))) return GEMM_ERR_INVALID_ARG;
+    if (!gated_fits(rows, cols)) return GEMM_ERR_UNSUPPORTED;
+    DeviceState *ds = device_state();
+    if (!ds) return fail_cuda(cudaErrorInvalidDevice);
+    if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
+    GatedAct a;
+    a.rows = rows;
+    a.cols = cols;
+    a.type = type;
+    a.dH = dH;
+    a.lddh = lddh;
+    a.GQ = const_cast<void *>(GQ);
+    a.ldgq = ldgq;
+    a.GS = const_cast<float *>(GS);
+    a.ldgs = ldgs;
+    a.UQ = const_cast<void *>(UQ);
+    a.lduq = lduq;
+    a.US = const_cast<float *>(US);
+    a.ldus = ldus;
+    a.q_type = q_type;
+    a.dG = dG;
+    a.lddg = lddg;
+    a.dU = dU;
+    a.lddu = lddu;
+    a.H = H;
+    a.ldh = ldh;
+    a.act = act;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    CallInfo info;
+    const cudaError_t e = run_gated_act_grad(a, s, &info);
     if (e != cudaSuccess) return fail_cuda(e);
     return finish_call(info, s);
 }

@@ -89,7 +89,7 @@ typedef enum {
     GEMM_ACT_GELU = 1,      /* exact GELU: x * Phi(x) = 0.5 * x * (1 + erf(x / sqrt(2))) */
     GEMM_ACT_RELU = 2,      /* max(x, 0) */
     GEMM_ACT_GELU_TANH = 3, /* 0.5 * x * (1 + tanh(sqrt(2/pi) * (x + 0.044715 * x^3))) */
-    GEMM_ACT_SILU = 4       /* x / (1 + exp(-x)) (gemm_moe_few_tokens only) */
+    GEMM_ACT_SILU = 4       /* x / (1 + exp(-x)) (gemm_moe_few_tokens and gemm_fp8_gated_act only) */
 } gemm_act;
 
 /* Element types of the tensor-core entry point gemm_tc_f32acc_epilogue. */
@@ -377,6 +377,120 @@ GEMM11_API int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const 
                                    const void *down, int w_type, const float *s_gate, const float *s_up,
                                    const float *s_down, int act, int renormalize, void *Y, int y_type, long long ldy,
                                    int *ids, float *weights, void *stream);
+
+/*
+ * A mixture-of-experts layer for many tokens (a prefill, a training step) is a
+ * run of the calls below.  Forward: gemm_moe_dispatch sorts the router's choice
+ * by expert and copies the tokens' rows into that order, gemm_grouped_f32acc
+ * multiplies every expert's rows by its matrices, gemm_fp8_gated_act is the
+ * activation between them, gemm_moe_combine brings the rows back to their
+ * tokens.  Backward: gemm_moe_combine_grad, gemm_grouped_f32acc with the same
+ * weights and b_trans turned, gemm_grouped_wgrad_f32acc for every weight,
+ * gemm_fp8_gated_act_grad, and gemm_moe_combine without weights, which is the
+ * gradient of the copy.
+ *
+ * gemm_moe_dispatch -- for each slot (t, j), expert e = ids[t * top_k + j]:
+ *   offsets[e] = number of slots whose expert is below e (offsets[E]: of all
+ *   that have one), rows[t * top_k + j] = offsets[e] + number of earlier slots
+ *   of expert e, and Xs[rows[t * top_k + j]] = X[t].
+ *   ids      T x top_k int, as gemm_moe_few_tokens writes them.  An id outside
+ *            0 .. E - 1 chooses no expert: its slot gets row -1.
+ *   X        T x H, FP32, FP16 or BF16 (x_type); Xs of the same type, at least
+ *            T * top_k rows, of which those from offsets[E] on stay as they are.
+ *            X and Xs both NULL: the order alone.
+ *   offsets  E + 1 int;  rows  T x top_k int.
+ * Any alignment is accepted (16-byte aligned rows take wide copies).  T == 0
+ * writes the offsets (zeros).  GEMM_ERR_UNSUPPORTED for E > 4096, top_k > 128 or
+ * T * top_k above 2^31 - 512.
+ */
+GEMM11_API int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids, const void *X, int x_type,
+                                 long long ldx, void *Xs, long long ldxs, int *offsets, int *rows, void *stream);
+
+/*
+ * gemm_moe_combine -- Y[t] = round( sum_j w[t, j] Ys[rows[t, j]] ), the slots of
+ * a token added in their order in FP32.
+ *   Ys  R x H, Y  T x H, both of one type (FP32, FP16, BF16).
+ *   rows     T x top_k int (gemm_moe_dispatch); a slot whose row is outside
+ *            0 .. R - 1 adds nothing, a token without any gets zeros.
+ *   weights  T x top_k float, or NULL: ones.  With ones it is also the gradient
+ *            of gemm_moe_dispatch's copy.
+ * Any alignment.  T == 0 or H == 0 is a no-op.
+ */
+GEMM11_API int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, long long ldys,
+                                const int *rows, const float *weights, void *Y, long long ldy, void *stream);
+
+/*
+ * gemm_moe_combine_grad -- the gradient of gemm_moe_combine with weights:
+ *   dYs[rows[t, j]] = round( w[t, j] dY[t] ),  dweights[t, j] = sum_h dY[t, h]
+ *   Ys[rows[t, j], h] in FP32, 0 for a slot without a row.
+ * dY T x H, Ys and dYs R x H, all of one type; rows of dYs that no slot names
+ * stay as they are.  Any alignment.  T == 0 is a no-op.
+ */
+GEMM11_API int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void *dY, int type, long long lddy,
+                                     const void *Ys, long long ldys, const int *rows, const float *weights, void *dYs,
+                                     long long lddys, float *dweights, void *stream);
+
+/*
+ * gemm_grouped_f32acc -- the experts' products over rows sorted by expert:
+ *   C[r] = round_c( alpha A[r] op(B[e]) + beta C[r] )  for offsets[e] <= r < offsets[e + 1].
+ *   A        R x K, FP16 or BF16 (ab_type), lda elements a row.
+ *   B        E matrices stride_b elements apart, of ab_type: b_trans = 1 each
+ *            N x K, op(B) = B^T (the forward product of weights stored out x
+ *            in); b_trans = 0 each K x N, op(B) = B (the gradient of the rows).
+ *   C        R x N, FP32, FP16 or BF16 (c_type); rows from offsets[E] on, and
+ *            rows before offsets[0], stay as they are.
+ *   offsets  E + 1 int on the device, not descending, from 0 to R
+ *            (gemm_moe_dispatch); values outside 0 .. R are taken as the nearer
+ *            of the two.  The host does not read them.
+ * FP32 accumulation: the tensor cores add 512 of the contraction, the rest is
+ * added in FP32 to nearest.  alpha, beta and the degenerate shapes are those of
+ * gemm_tc_f32acc_epilogue.  A and B 16-byte aligned, lda, ldb and stride_b
+ * multiples of 8 (those of a single row, or expert, excepted), otherwise
+ * GEMM_ERR_UNSUPPORTED; C any alignment and any ldc >= N.
+ */
+GEMM11_API int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, const void *A, long long lda, const void *B,
+                                   long long ldb, long long stride_b, int ab_type, int b_trans, float beta, void *C,
+                                   int c_type, long long ldc, const int *offsets, void *stream);
+
+/*
+ * gemm_grouped_wgrad_f32acc -- the gradient of the experts' weights:
+ *   C[e] = round_c( alpha sum_r A[r]^T B[r] + beta C[e] ) over offsets[e] <= r < offsets[e + 1],
+ * A R x M and B R x N of ab_type, C E matrices M x N stride_c elements apart
+ * (FP32, FP16 or BF16).  An expert without rows gets beta C[e].  offsets, the
+ * accumulation and the alignment are those of gemm_grouped_f32acc.
+ */
+GEMM11_API int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha, const void *A, long long lda,
+                                         const void *B, long long ldb, int ab_type, float beta, void *C, int c_type,
+                                         long long ldc, long long stride_c, const int *offsets, void *stream);
+
+/*
+ * gemm_fp8_gated_act -- h = act(g) u of a feed-forward layer, and g and u kept
+ * for the backward pass in 8 bits: GQ, GS and UQ, US are what
+ * gemm_fp8_quantize_block128 makes of G and U with GEMM_FP8_ROWS.
+ *   G, U, H  rows x cols, all of `type` (FP32, FP16 or BF16).  U (with UQ and US)
+ *            may be NULL: h = act(g).
+ *   GQ, UQ   rows x cols, e4m3 or e5m2 (q_type); GS, US ceil(cols / 128) x rows.
+ *   act      any gemm_act.
+ * Any alignment.  rows == 0 or cols == 0 is a no-op.
+ */
+GEMM11_API int gemm_fp8_gated_act(int rows, int cols, const void *G, long long ldg, const void *U, long long ldu,
+                                  int type, void *H, long long ldh, void *GQ, long long ldgq, float *GS,
+                                  long long ldgs, void *UQ, long long lduq, float *US, long long ldus, int q_type,
+                                  int act, void *stream);
+
+/*
+ * gemm_fp8_gated_act_grad -- its backward pass from the 8-bit copies: with
+ * g' = GQ GS and u' = UQ US (1 without UQ)
+ *   dG = round( dH u' act'(g') ),  dU = round( dH act(g') ) (with UQ),
+ *   H  = round( act(g') u' ) where H is not NULL (the rows that the gradient of
+ *   the next weights needs, so that h itself need not be kept).
+ * dH, dG, dU and H of `type`.  The derivative of ReLU at 0 is 0.  Any alignment.
+ */
+GEMM11_API int gemm_fp8_gated_act_grad(int rows, int cols, const void *dH, long long lddh, int type, const void *GQ,
+                                       long long ldgq, const float *GS, long long ldgs, const void *UQ,
+                                       long long lduq, const float *US, long long ldus, int q_type, void *dG,
+                                       long long lddg, void *dU, long long lddu, void *H, long long ldh, int act,
+                                       void *stream);
 
 /*
  * Tuned plans.  The planners pick a kernel family, tile width and split-K

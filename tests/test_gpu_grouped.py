@@ -1,0 +1,173 @@
+"""Products over rows sorted by expert, against FP64 (GB300)."""
+import pytest
+import torch
+
+import dense_gemm_11_gb300 as g
+from experts_ref import PRODUCT, close, grouped, rounded, wgrad
+
+pytestmark = pytest.mark.gpu
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+
+
+def padded(*shape, dtype, fill=None, scale=1.0, pad=None):
+    """A tensor whose rows start on 16-byte boundaries (or have `pad` elements between them)."""
+    cols = shape[-1]
+    ld = -(-cols // 8) * 8 if pad is None else cols + pad
+    full = torch.randn(*shape[:-1], ld, device="cuda") * scale if fill is None else torch.full((*shape[:-1], ld), fill, device="cuda")
+    return full.to(dtype)[..., :cols]
+
+
+def offsets_of(sizes):
+    return torch.tensor([0] + list(sizes), device="cuda").cumsum(0).int()
+
+
+# rows of each expert, N, K
+SIZES = [
+    ([1], 1, 1), ([1, 0, 2], 8, 16), ([0, 0, 5, 0], 24, 72), ([3, 130, 257, 1, 0, 64], 264, 200), ([128, 128], 256, 64), ([300], 520, 1100),
+    ([0, 700, 33], 129, 65), ([5] * 40, 136, 128), ([31, 32, 33, 255, 256], 40, 513), ([2, 1, 0, 4], 1000, 1024),
+]
+
+
+@pytest.mark.parametrize("c", [F32, BF16])
+@pytest.mark.parametrize("b_trans", [True, False])
+@pytest.mark.parametrize("sizes,N,K", SIZES)
+def test_rows(sizes, N, K, b_trans, c):
+    t = F16 if N % 16 == 8 else BF16
+    torch.manual_seed(N + K)
+    R, E = sum(sizes) + 3, len(sizes)
+    A, B = padded(R, K, dtype=t), padded(E, *((N, K) if b_trans else (K, N)), dtype=t)
+    C = padded(R, N, dtype=c, fill=-7.0)
+    g.gemm_grouped(A, B, C, offsets_of(sizes), b_trans=b_trans)
+    assert g.check() == g.GEMM_OK
+    want, mag = grouped(A, B, offsets_of(sizes), b_trans)
+    n = sum(sizes)
+    close(C[:n], want[:n], rounded(PRODUCT * mag[:n], want[:n], c))
+    assert (C[n:] == -7.0).all()  # rows behind the last expert's
+
+
+@pytest.mark.parametrize("c", [F32, F16, BF16])
+@pytest.mark.parametrize("sizes,M,N", [(s, n, k) for s, n, k in SIZES] + [([65, 63, 0, 1], 264, 264), ([64, 128, 192], 256, 8), ([513, 511], 136, 300)])
+def test_weights(sizes, M, N, c):
+    t = F16 if M % 16 == 8 else BF16
+    torch.manual_seed(M + N)
+    R, E = sum(sizes) + 5, len(sizes)
+    A, B = padded(R, M, dtype=t), padded(R, N, dtype=t)
+    C = padded(E, M, N, dtype=c, fill=-7.0)
+    g.gemm_grouped_wgrad(A, B, C, offsets_of(sizes))
+    assert g.check() == g.GEMM_OK
+    want, mag = wgrad(A, B, offsets_of(sizes))
+    close(C, want, rounded(PRODUCT * mag, want, c))
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+def test_neighbours_do_not_leak(t):
+    """NaN and infinity in another expert's rows, in its weights and behind the last row reach nobody else."""
+    sizes, N, K = [70, 1, 100, 0, 29], 72, 136
+    off = offsets_of(sizes)
+    A, X = padded(240, K, dtype=t), padded(240, N, dtype=t)
+    for m in (A, X):
+        m[70] = float("nan")
+        m[200:] = float("inf")
+    B = padded(5, N, K, dtype=t)
+    B[1], B[3] = float("nan"), float("inf")
+    for bt in (True, False):
+        b = B if bt else B.transpose(1, 2).contiguous()
+        C = padded(240, N, dtype=F32, fill=0.0)
+        g.gemm_grouped(A, b, C, off, b_trans=bt)
+        assert C[70].isnan().all() and not C[:70].isnan().any() and torch.isfinite(C[71:200]).all() and (C[200:] == 0).all()
+    dW = padded(5, K, N, dtype=F32, fill=float("nan"))
+    g.gemm_grouped_wgrad(A, X, dW, off)
+    assert g.check() == g.GEMM_OK
+    assert dW[1].isnan().all() and torch.isfinite(dW[[0, 2, 3, 4]]).all() and (dW[3] == 0).all()
+
+
+@pytest.mark.parametrize("alpha,beta", [(0.5, 2.0), (0.0, 0.5), (-1.0, 0.0), (0.0, 0.0)])
+def test_alpha_beta(alpha, beta):
+    sizes, N, K = [40, 0, 200], 80, 600
+    off = offsets_of(sizes)
+    A, B, C0 = padded(243, K, dtype=BF16), padded(3, N, K, dtype=BF16), padded(243, N, dtype=F16)
+    C = padded(243, N, dtype=F16)
+    C.copy_(C0)
+    if beta == 0.0:
+        C[:240] = float("nan")
+    g.gemm_grouped(A, B, C, off, alpha, beta)
+    want, mag = grouped(A, B, off, True, alpha, beta, C0)
+    close(C[:240], want[:240], rounded(PRODUCT * mag[:240], want[:240], F16))
+    assert torch.equal(C[240:], C0[240:])
+    A2, D0 = padded(243, N, dtype=BF16), padded(3, N, K, dtype=F32)
+    D = D0.clone()
+    if beta == 0.0:
+        D[:] = float("nan")
+    g.gemm_grouped_wgrad(A2, A, D, off, alpha, beta)
+    want, mag = wgrad(A2, A, off, alpha, beta, D0)
+    close(D, want, rounded(PRODUCT * mag, want, F32))
+
+
+def test_alpha_zero_reads_nothing():
+    off = offsets_of([10, 6])
+    A, B, C = padded(16, 32, dtype=F16, fill=float("nan")), padded(2, 8, 32, dtype=F16, fill=float("nan")), padded(16, 8, dtype=F32, fill=3.0)
+    g.gemm_grouped(A, B, C, off, 0.0, 2.0)
+    assert (C == 6.0).all()
+
+
+@pytest.mark.parametrize("pad", [0, 1, 3])
+@pytest.mark.parametrize("c", [F32, BF16])
+def test_any_rows_of_c(c, pad):
+    """C whose rows are not aligned for wide stores, and what lies between its rows."""
+    sizes, N, K = [150, 300], 129, 96
+    off = offsets_of(sizes)
+    A, B = padded(450, K, dtype=BF16), padded(2, N, K, dtype=BF16)
+    full = torch.full((450 * (N + pad) + 1,), -7.0, device="cuda", dtype=c)
+    C = full[1:].as_strided((450, N), (N + pad, 1))
+    g.gemm_grouped(A, B, C, off)
+    want, mag = grouped(A, B, off, True)
+    close(C, want, rounded(PRODUCT * mag, want, c))
+    if pad:
+        assert (full[1:].as_strided((450, pad), (N + pad, 1), storage_offset=1 + N) == -7.0).all()
+    D = torch.full((2 * (K * (N + pad) + 5),), -7.0, device="cuda", dtype=c)
+    dW = D.as_strided((2, K, N), (K * (N + pad) + 5, N + pad, 1))
+    X = padded(450, N, dtype=BF16)
+    g.gemm_grouped_wgrad(A, X, dW, off)
+    want, mag = wgrad(A, X, off)
+    close(dW, want, rounded(PRODUCT * mag, want, c))
+    assert (D[-5:] == -7.0).all()
+
+
+def test_offsets_outside_are_taken_as_the_nearer_end():
+    A, B, C = padded(20, 16, dtype=F16), padded(3, 8, 16, dtype=F16), padded(20, 8, dtype=F32, fill=-7.0)
+    g.gemm_grouped(A, B, C, torch.tensor([-5, 4, 12, 1000], dtype=torch.int32, device="cuda"))
+    want, mag = grouped(A, B, torch.tensor([0, 4, 12, 20]), True)
+    close(C, want, rounded(PRODUCT * mag, want, F32))
+    C.fill_(-7.0)
+    g.gemm_grouped(A, B, C, torch.tensor([3, 4, 4, 9], dtype=torch.int32, device="cuda"))
+    want, mag = grouped(A, B, torch.tensor([3, 4, 4, 9]), True)
+    close(C[3:9], want[3:9], rounded(PRODUCT * mag[3:9], want[3:9], F32))
+    assert (C[:3] == -7.0).all() and (C[9:] == -7.0).all()
+
+
+def test_many_experts_and_tiles():
+    """More experts than a warp has lanes, most without rows; more tiles than CTA pairs."""
+    torch.manual_seed(1)
+    sizes = [(i * 37) % 11 if i % 3 == 0 else 0 for i in range(300)] + [900]
+    off = offsets_of(sizes)
+    R = sum(sizes)
+    A, B, C = padded(R, 64, dtype=BF16), padded(301, 520, 64, dtype=BF16), padded(R, 520, dtype=F32, fill=-7.0)
+    g.gemm_grouped(A, B, C, off)
+    want, mag = grouped(A, B, off, True)
+    close(C, want, rounded(PRODUCT * mag, want, F32))
+    X, dW = padded(R, 264, dtype=BF16), padded(301, 264, 64, dtype=F32, fill=-7.0)
+    g.gemm_grouped_wgrad(X, A, dW, off)
+    assert g.check() == g.GEMM_OK
+    want, mag = wgrad(X, A, off)
+    close(dW, want, rounded(PRODUCT * mag, want, F32))
+
+
+def test_sums_to_nearest():
+    """Equal signs: the tensor core's truncation would show over a long contraction without the chunks."""
+    K = 8192
+    A, B = padded(256, K, dtype=BF16).abs(), padded(1, 256, K, dtype=BF16).abs()
+    C = padded(256, 256, dtype=F32)
+    g.gemm_grouped(A, B, C, offsets_of([256]))
+    want, mag = grouped(A, B, offsets_of([256]), True)
+    err = ((C.double() - want) / mag).abs()
+    assert float(err.max()) <= 3e-6 and float(((C.double() - want) / mag).mean().abs()) <= 3e-6
