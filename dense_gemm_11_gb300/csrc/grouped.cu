@@ -32,7 +32,7 @@ constexpr int kChunk = 8;
 // Registers: 384 threads of 168 at launch, 64,512; 128 x 56 + 256 x 224 = 64,512.
 constexpr int kRegsFew = 56, kRegsMany = 224;
 constexpr int kThreads = 128 + 32 * kEpi;
-constexpr int kBars = 2 * kStages + 4 + 3;
+constexpr int kBars = 3 * kStages + 4 + 1;
 constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Rows of A that one copy brings in, for CTAs with up to kFewRows rows, up to
@@ -164,9 +164,10 @@ __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&a
 // registers.
 //
 // wgrad: the contraction ends at any row of A and B, and behind it are the next
-// expert's.  Both CTAs take the last block of 64 rows to a barrier of their own,
-// zero what is behind the end in shared memory (a row is 128 bytes there, the
-// swizzle moves bytes within it) and hand the block on.
+// expert's.  The copies of the last block of 64 rows signal barriers of the CTA's
+// own; warp 2 then zeroes what is behind the end in shared memory (a row is 128
+// bytes there, the swizzle moves bytes within it) and hands the block on, while
+// warp 0 is already at the next tile's.
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_some,
@@ -179,8 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tfull = empty + kStages;
     uint64_t *tempty = tfull + 2;
     uint64_t *mma_done = tempty + 2;
-    uint64_t *tail = mma_done + 1, *tail_peer = tail + 1;
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tail_peer + 1);
+    uint64_t *landed = mma_done + 1;  // last blocks of a contraction that ends in them
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(landed + kStages);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -189,16 +190,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int cid = blockIdx.x >> 1, ncl = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], MODE == kWgrad ? 2 : 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&landed[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 2 * kEpi);  // the warps of both CTAs
         }
         mbar_init(mma_done, 1);
-        mbar_init(tail, 1);
-        mbar_init(tail_peer, 1);
         *abort_flag = 0;
         fence_mbarrier_init();
         if (p.product) {
@@ -220,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem_base = *tmem_holder;
     pdl_wait();
     pdl_launch_dependents();
-    uint32_t armed = 0, armed_parity = 0, tails = 0;
+    uint32_t armed = 0, armed_parity = 0;
+    uint32_t ends = 0, ends_parity = 0;  // stages that had such a block, and the parity of the last
     TileList<MODE == kWgrad> list;
     Tile tile;
     if (warp < 4) {
@@ -250,43 +251,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int valid = tile.k1 - k0;
                     if (MODE == kWgrad && valid < kKB) {
                         if (elect_one()) {
-                            mbar_arrive_expect_tx(tail, tx);
-                            tma_load_2d(&tm_b, tail, b, my_n, k0);
-                            tma_load_2d(&tm_b, tail, b + kBox, my_n + 64, k0);
-                            for (int i = 0; i < boxes; ++i) tma_load_2d(&tm_a, tail, a + i * kBox, my_m + i * 64, k0);
+                            mbar_arrive_expect_tx(&landed[stage], tx);
+                            tma_load_2d(&tm_b, &landed[stage], b, my_n, k0);
+                            tma_load_2d(&tm_b, &landed[stage], b + kBox, my_n + 64, k0);
+                            for (int i = 0; i < boxes; ++i) tma_load_2d(&tm_a, &landed[stage], a + i * kBox, my_m + i * 64, k0);
                         }
                         __syncwarp();
-                        ++tails;
-                        ok = __all_sync(0xffffffffu, mbar_wait_patient(tail, (tails - 1) & 1u, p.wait_ns));
-                        if (!ok) {
-                            grouped_timeout(abort_flag, p.err);
-                            break;
-                        }
-                        const uint4 zero = make_uint4(0, 0, 0, 0);
-                        for (int i = valid * 8 + lane; i < kKB * 8; i += 32) {
-                            reinterpret_cast<uint4 *>(b)[i] = zero;
-                            reinterpret_cast<uint4 *>(b + kBox)[i] = zero;
-                            reinterpret_cast<uint4 *>(a)[i] = zero;
-                            reinterpret_cast<uint4 *>(a + kBox)[i] = zero;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (leader) {
-                            ok = __all_sync(0xffffffffu, mbar_wait_cluster(tail_peer, (tails - 1) & 1u, p.wait_ns));
-                            if (!ok) {
-                                grouped_timeout(abort_flag, p.err);
-                                break;
-                            }
-                            if (elect_one()) mbar_arrive(&full[stage]);
-                        } else if (elect_one()) {
-                            mbar_arrive_cluster(mapa_shared(smem_u32(tail_peer), 0));
-                        }
-                        __syncwarp();
+                        if (ends & (1u << stage)) ends_parity ^= 1u << stage;
+                        ends |= 1u << stage;
                     } else {
                         const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
                         if (elect_one()) {
                             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * tx);
                             if (MODE == kWgrad) {
+                                if (leader) mbar_arrive(&full[stage]);
                                 tma_load_2d_pair(&tm_b, bar, b, my_n, k0);
                                 tma_load_2d_pair(&tm_b, bar, b + kBox, my_n + 64, k0);
                             } else if (MODE == kDgrad) {
@@ -316,6 +294,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (++stage == kStages) stage = 0, phase ^= 1u;
                 }
             }
+        } else if (MODE == kWgrad && warp == 2) {
+            // ------------------------------------------------ ends of contractions (both CTAs)
+            list.window(p, lane);
+            int stage = 0;
+            bool ok = true;
+            for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
+                const int blocks = tile_blocks(tile), valid = tile.k1 - tile.k0 - (blocks - 1) * kKB;
+                if (blocks == 0) continue;
+                stage = (stage + blocks - 1) % kStages;
+                if (valid < kKB) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_patient(&landed[stage], ends_parity >> stage & 1u, p.wait_ns));
+                    if (!ok) {
+                        grouped_timeout(abort_flag, p.err);
+                        break;
+                    }
+                    ends_parity ^= 1u << stage;
+                    uint8_t *b = sB + stage * kHalf, *a = sA + stage * kHalf;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    for (int i = valid * 8 + lane; i < kKB * 8; i += 32) {
+                        reinterpret_cast<uint4 *>(b)[i] = zero;
+                        reinterpret_cast<uint4 *>(b + kBox)[i] = zero;
+                        reinterpret_cast<uint4 *>(a)[i] = zero;
+                        reinterpret_cast<uint4 *>(a + kBox)[i] = zero;
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (elect_one()) mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));
+                    __syncwarp();
+                }
+                stage = stage + 1 == kStages ? 0 : stage + 1;
+            }
         } else if (warp == 1 && leader) {
             // ------------------------------------------------ MMA issuer (even CTA)
             // K-major: 128-byte rows, 8-row groups 1024 bytes apart, 16 k = 32
@@ -341,7 +350,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc_fence_after();
                     for (int kb = 0; kb < some; ++kb) {
-                        ok = __all_sync(0xffffffffu, mbar_wait_patient(&full[stage], phase, p.wait_ns));
+                        const int left = tile.k1 - tile.k0 - (kb0 + kb) * kKB;
+                        // the end of a contraction comes from both CTAs' threads
+                        ok = __all_sync(0xffffffffu, MODE == kWgrad && left < kKB ? mbar_wait_cluster(&full[stage], phase, p.wait_ns)
+                                                                                  : mbar_wait_patient(&full[stage], phase, p.wait_ns));
                         if (!ok) {
                             grouped_timeout(abort_flag, p.err);
                             break;
@@ -350,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t bd = b_desc0 + static_cast<uint64_t>(stage * (kHalf >> 4));
                         const uint64_t ad = a_desc0 + static_cast<uint64_t>(stage * (kHalf >> 4));
                         // of the last block only the 16 k that it reaches into
-                        const int steps = (min(kKB, tile.k1 - tile.k0 - (kb0 + kb) * kKB) + 15) / 16;
+                        const int steps = (min(kKB, left) + 15) / 16;
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < kKB / 16; ++kk)
@@ -430,10 +442,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // ---------------------------------------------------- drain and unwind
     if (warp == 0 && lane == 0) {
-        if (MODE == kWgrad && tails > 0 && !mbar_wait(tail, (tails - 1) & 1u)) grouped_timeout(abort_flag, p.err);
-        // the even CTA's full barriers count the copies of both CTAs
-        for (int s = 0; s < kStages; ++s)
+        // the even CTA's full barriers count the copies of both CTAs, except of the ends
+        for (int s = 0; s < kStages; ++s) {
+            if ((ends & (1u << s)) && !mbar_wait(&landed[s], (ends_parity >> s) & 1u)) grouped_timeout(abort_flag, p.err);
             if (leader && (armed & (1u << s)) && !mbar_wait(&full[s], (armed_parity >> s) & 1u)) grouped_timeout(abort_flag, p.err);
+        }
     }
     if (warp == 1 && leader) {
         // the electing lane issued the MMAs that the commit waits for
