@@ -35,6 +35,7 @@ struct DispatchArgs {
     int row_bytes, esize;
     int *offsets, *rows;
     int per_cta;  // tokens
+    int copies;   // of the counters, a power of two
     unsigned *err;
     size_t xs_extent;  // bytes, checked by GEMM11_DEBUG builds
 };
@@ -83,27 +84,56 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     extern __shared__ int counts[];  // of each expert: slots before this CTA's, then the others
     __shared__ int warp_sum[32];
     __shared__ int pos[kSortBatch];
-    int *before = counts, *rest = counts + p.E;
+    const int copies = p.copies;  // neighbouring lanes count in counters of their own: fewer of a warp's additions meet
+    int *before = counts, *rest = counts + p.E * copies;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.per_cta, t1 = min(p.T, t0 + p.per_cta);
+    for (int e = threadIdx.x; e < 2 * p.E * copies; e += kSortThreads) counts[e] = 0;
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    for (int e = threadIdx.x; e < 2 * p.E; e += kSortThreads) counts[e] = 0;
-    __syncthreads();
-    const int mine = t0 * p.k;
-    for (int i = threadIdx.x; i < p.n; i += kSortThreads) {
-        const int e = __ldg(p.ids + i);
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(p.E)) atomicAdd((i < mine ? before : rest) + e, 1);
+    const int mine = t0 * p.k, my_copy = lane & (copies - 1);
+    auto count = [&](int e, int i) {
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(p.E)) atomicAdd((i < mine ? before : rest) + e * copies + my_copy, 1);
+    };
+    int done = 0;
+    if (reinterpret_cast<uintptr_t>(p.ids) % 16 == 0) {
+        const int4 *ids4 = reinterpret_cast<const int4 *>(p.ids);
+        const int quads = p.n >> 2;
+        constexpr int kAhead = 4;
+        for (int q0 = threadIdx.x; q0 < quads; q0 += kAhead * kSortThreads) {
+            int4 e[kAhead];
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u)
+                e[u] = q0 + u * kSortThreads < quads ? __ldg(ids4 + q0 + u * kSortThreads) : make_int4(-1, -1, -1, -1);
+#pragma unroll
+            for (int u = 0; u < kAhead; ++u) {
+                const int i = (q0 + u * kSortThreads) * 4;
+                count(e[u].x, i);
+                count(e[u].y, i + 1);
+                count(e[u].z, i + 2);
+                count(e[u].w, i + 3);
+            }
+        }
+        done = quads * 4;
     }
+    for (int i = done + threadIdx.x; i < p.n; i += kSortThreads) count(__ldg(p.ids + i), i);
     __syncthreads();
 
     // before[e] becomes the row of this CTA's first slot of expert e.
     constexpr int kPer = kDispatchMaxExperts / kSortThreads;
-    int total[kPer], sum = 0;
+    int total[kPer], ahead[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
-        total[i] = e < p.E ? before[e] + rest[e] : 0;
+        total[i] = ahead[i] = 0;
+        if (e < p.E) {
+            for (int c = 0; c < copies; ++c) {
+                ahead[i] += before[e * copies + c];
+                total[i] += rest[e * copies + c];
+            }
+            total[i] += ahead[i];
+        }
         sum += total[i];
     }
     int incl = sum;
@@ -129,7 +159,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;
         if (e < p.E) {
-            before[e] += start;
+            before[e] = ahead[i] + start;
             if (blockIdx.x == 0) p.offsets[e] = start;
         }
         start += total[i];
@@ -197,8 +227,8 @@ struct CombineArgs {
     void *dYs;
     long long lddys;
     float *dweights;
-    int lanes;  // threads of a token, 8 columns each (a power of two, 256 at most)
-    int tokens; // of a CTA: kCombineThreads / lanes
+    int lanes;   // threads of a token (gradient: of a slot), a power of two, 256 at most
+    int tokens;  // or slots, of a CTA: kCombineThreads / lanes
     unsigned *err;
     size_t y_extent;  // elements of what is written, checked by GEMM11_DEBUG builds
 };
@@ -210,110 +240,113 @@ __device__ __forceinline__ int slot_row(const CombineArgs &p, long long i) {
     return static_cast<unsigned>(r) < static_cast<unsigned>(p.R) ? r : -1;
 }
 
-// A thread has eight columns of a token and reads the KU rows of a step before
-// it adds them, in the order of the slots.
-template <int XT, bool VEC, int KU>
+// A thread has U times eight columns of a token and reads the KU rows of a step
+// before it adds them, in the order of the slots.
+template <int XT, bool VEC, int KU, int U>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     const long long t = static_cast<long long>(blockIdx.x) * p.tokens + threadIdx.x / p.lanes;
     if (t >= p.T) return;
-    for (int c = static_cast<int>(threadIdx.x % p.lanes) * 8; c < p.H; c += p.lanes * 8) {
-        float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int step = p.lanes * 8;
+    for (int c = static_cast<int>(threadIdx.x % p.lanes) * 8; c < p.H; c += U * step) {
+        float sum[U][8];
+#pragma unroll
+        for (int v = 0; v < U; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[v][i] = 0.f;
         for (int j0 = 0; j0 < p.k; j0 += KU) {
-            Row8<XT> y[KU];
+            Row8<XT> y[KU][U];
             float w[KU];
             int r[KU];
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
                 r[u] = j0 + u < p.k ? slot_row(p, t * p.k + j0 + u) : -1;
-                w[u] = p.weights && r[u] >= 0 ? __ldg(p.weights + t * p.k + j0 + u) : 1.f;
-                if (r[u] >= 0) y[u].template load<VEC>(p.Ys, r[u] * p.ldys + c, p.H - c);
+                w[u] = p.weights && j0 + u < p.k ? __ldg(p.weights + t * p.k + j0 + u) : 1.f;
             }
+#pragma unroll
+            for (int u = 0; u < KU; ++u)
+#pragma unroll
+                for (int v = 0; v < U; ++v)
+                    if (r[u] >= 0 && c + v * step < p.H) y[u][v].template load<VEC>(p.Ys, r[u] * p.ldys + c + v * step, p.H - c - v * step);
 #pragma unroll
             for (int u = 0; u < KU; ++u) {
                 if (r[u] < 0) continue;
-                float v[8];
-                y[u].widen(v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[i] = fmaf(w[u], v[i], sum[i]);
-            }
-        }
-        Row8<XT> out;
-        out.round(sum);
-        if (debug_in_bounds(static_cast<size_t>(t * p.ldy + min(c + 8, p.H)) <= p.y_extent, p.err)) out.template store<VEC>(p.Y, t * p.ldy + c, p.H - c);
-    }
-}
-
-// The gradient: KU slots at a time, whose dot products stay in registers while
-// the columns pass and are then added over the token's threads.
-template <int XT, bool VEC, int KU>
-__global__ void __launch_bounds__(kCombineThreads) combine_grad_kernel(const CombineArgs p) {
-    __shared__ float part[kCombineThreads / 32][KU];
-    pdl_wait();
-    pdl_launch_dependents();
-    const int mine = threadIdx.x / p.lanes, at = threadIdx.x % p.lanes;
-    const long long t = static_cast<long long>(blockIdx.x) * p.tokens + mine;
-    const bool live = t < p.T;
-    for (int j0 = 0; j0 < p.k; j0 += KU) {
-        float w[KU], dot[KU];
-        int r[KU];
+                for (int v = 0; v < U; ++v) {
+                    float f[8];
+                    y[u][v].widen(f);
 #pragma unroll
-        for (int u = 0; u < KU; ++u) {
-            r[u] = live && j0 + u < p.k ? slot_row(p, t * p.k + j0 + u) : -1;
-            w[u] = r[u] >= 0 ? __ldg(p.weights + t * p.k + j0 + u) : 0.f;
-            dot[u] = 0.f;
-        }
-        if (live) {
-            for (int c = at * 8; c < p.H; c += p.lanes * 8) {
-                Row8<XT> dy, y[KU];
-                dy.template load<VEC>(p.Y, t * p.ldy + c, p.H - c);
-#pragma unroll
-                for (int u = 0; u < KU; ++u)
-                    if (r[u] >= 0) y[u].template load<VEC>(p.Ys, r[u] * p.ldys + c, p.H - c);
-                float d[8];
-                dy.widen(d);
-#pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    if (r[u] < 0) continue;
-                    float v[8];
-                    y[u].widen(v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        dot[u] = fmaf(d[i], v[i], dot[u]);
-                        v[i] = w[u] * d[i];
-                    }
-                    Row8<XT> out;
-                    out.round(v);
-                    if (debug_in_bounds(static_cast<size_t>(r[u] * p.lddys + min(c + 8, p.H)) <= p.y_extent, p.err))
-                        out.template store<VEC>(p.dYs, r[u] * p.lddys + c, p.H - c);
+                    for (int i = 0; i < 8; ++i) sum[v][i] = fmaf(w[u], f[i], sum[v][i]);
                 }
             }
         }
-        const int within = min(p.lanes, 32);
 #pragma unroll
-        for (int u = 0; u < KU; ++u)
-            for (int d = within >> 1; d >= 1; d >>= 1) dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], d);
-        if (p.lanes <= 32) {
-            if (at == 0 && live) {
+        for (int v = 0; v < U; ++v) {
+            const int cv = c + v * step;
+            if (cv >= p.H) break;
+            Row8<XT> out;
+            out.round(sum[v]);
+            if (debug_in_bounds(static_cast<size_t>(t * p.ldy + min(cv + 8, p.H)) <= p.y_extent, p.err)) out.template store<VEC>(p.Y, t * p.ldy + cv, p.H - cv);
+        }
+    }
+}
+
+// The gradient: `lanes` threads a slot, which read the token's row (again for each
+// of its slots, from the caches) and the slot's, U times eight columns at a time.
+// A slot's sum stays within its threads: most often one warp.
+template <int XT, bool VEC, int U>
+__global__ void __launch_bounds__(kCombineThreads) combine_grad_kernel(const CombineArgs p) {
+    __shared__ float part[kCombineThreads / 32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int at = threadIdx.x % p.lanes, step = p.lanes * 8;
+    const long long slot = static_cast<long long>(blockIdx.x) * p.tokens + threadIdx.x / p.lanes;
+    const bool live = slot < static_cast<long long>(p.T) * p.k;
+    float dot = 0.f;
+    if (live) {
+        const long long t = slot / p.k;
+        const int r = slot_row(p, slot);
+        const float w = __ldg(p.weights + slot);
+        for (int c = at * 8; r >= 0 && c < p.H; c += U * step) {
+            Row8<XT> dy[U], y[U];
 #pragma unroll
-                for (int u = 0; u < KU; ++u)
-                    if (j0 + u < p.k) p.dweights[t * p.k + j0 + u] = dot[u];
+            for (int v = 0; v < U; ++v) {
+                const int cv = c + v * step;
+                if (cv < p.H) {
+                    dy[v].template load<VEC>(p.Y, t * p.ldy + cv, p.H - cv);
+                    y[v].template load<VEC>(p.Ys, r * p.ldys + cv, p.H - cv);
+                }
             }
-        } else {
-            __syncthreads();  // the last step's sums are read
-            if ((threadIdx.x & 31) == 0) {
 #pragma unroll
-                for (int u = 0; u < KU; ++u) part[threadIdx.x >> 5][u] = dot[u];
-            }
-            __syncthreads();
-            if (live && at < KU && j0 + at < p.k) {
-                float s = 0.f;
-                for (int i = 0; i < p.lanes / 32; ++i) s += part[mine * (p.lanes / 32) + i][at];
-                p.dweights[t * p.k + j0 + at] = s;
+            for (int v = 0; v < U; ++v) {
+                const int cv = c + v * step;
+                if (cv < p.H) {
+                    float d[8], f[8];
+                    dy[v].widen(d);
+                    y[v].widen(f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        dot = fmaf(d[i], f[i], dot);
+                        d[i] *= w;
+                    }
+                    Row8<XT> out;
+                    out.round(d);
+                    if (debug_in_bounds(static_cast<size_t>(r * p.lddys + min(cv + 8, p.H)) <= p.y_extent, p.err))
+                        out.template store<VEC>(p.dYs, r * p.lddys + cv, p.H - cv);
+                }
             }
         }
     }
+    for (int d = min(p.lanes, 32) >> 1; d >= 1; d >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, d);
+    if (p.lanes > 32) {
+        if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = dot;
+        __syncthreads();
+        dot = 0.f;
+        if (at == 0)
+            for (int i = 0; i < p.lanes / 32; ++i) dot += part[threadIdx.x / 32 + i];
+    }
+    if (at == 0 && live) p.dweights[slot] = dot;
 }
 
 template <typename Args>
@@ -335,16 +368,20 @@ cudaError_t launch_pdl(void (*kern)(const Args), unsigned grid, unsigned threads
 int type_bytes(int type) { return type == kOutF32 ? 4 : 2; }
 
 template <int XT, bool VEC>
-cudaError_t launch_combine(const CombineArgs &a, bool grad, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
-    if (grad) {
-        if (a.k <= 2) return launch_pdl(combine_grad_kernel<XT, VEC, 2>, grid, kCombineThreads, 0, stream, a);
-        if (a.k <= 4) return launch_pdl(combine_grad_kernel<XT, VEC, 4>, grid, kCombineThreads, 0, stream, a);
-        return launch_pdl(combine_grad_kernel<XT, VEC, 8>, grid, kCombineThreads, 0, stream, a);
-    }
-    if (a.k <= 2) return launch_pdl(combine_kernel<XT, VEC, 2>, grid, kCombineThreads, 0, stream, a);
-    if (a.k <= 4) return launch_pdl(combine_kernel<XT, VEC, 4>, grid, kCombineThreads, 0, stream, a);
-    return launch_pdl(combine_kernel<XT, VEC, 8>, grid, kCombineThreads, 0, stream, a);
+cudaError_t launch_combine(CombineArgs a, bool grad, cudaStream_t stream) {
+    // Columns of a thread: as many as keep four to eight loads of 16 bytes in flight.
+    const int u = grad ? 4 : a.k <= 2 ? 2 : 1;
+    const long long units = grad ? static_cast<long long>(a.T) * a.k : a.T;
+    a.lanes = 1;
+    while (a.lanes < kCombineThreads && a.lanes * 8 * u < a.H) a.lanes *= 2;
+    // Many slots: a warp each.
+    if (grad && units >= 16LL * device_sm_count()) a.lanes = std::min(a.lanes, 32);
+    a.tokens = kCombineThreads / a.lanes;
+    const unsigned grid = static_cast<unsigned>((units + a.tokens - 1) / a.tokens);
+    if (grad) return launch_pdl(combine_grad_kernel<XT, VEC, 4>, grid, kCombineThreads, 0, stream, a);
+    if (a.k <= 2) return launch_pdl(combine_kernel<XT, VEC, 2, 2>, grid, kCombineThreads, 0, stream, a);
+    if (a.k <= 4) return launch_pdl(combine_kernel<XT, VEC, 4, 1>, grid, kCombineThreads, 0, stream, a);
+    return launch_pdl(combine_kernel<XT, VEC, 8, 1>, grid, kCombineThreads, 0, stream, a);
 }
 
 cudaError_t combine(const MoeCombine &c, bool grad, cudaStream_t stream) {
@@ -362,9 +399,6 @@ cudaError_t combine(const MoeCombine &c, bool grad, cudaStream_t stream) {
     a.dYs = c.dYs;
     a.lddys = c.lddys;
     a.dweights = c.dweights;
-    a.lanes = 1;
-    while (a.lanes < 256 && a.lanes * 8 < c.H) a.lanes *= 2;
-    a.tokens = kCombineThreads / a.lanes;
     a.err = watchdog_word();
     if (kDebugBuild) {
         a.y_extent = grad ? static_cast<size_t>((c.R - 1LL) * c.lddys + c.H) : static_cast<size_t>((c.T - 1LL) * c.ldy + c.H);
@@ -409,7 +443,9 @@ cudaError_t run_moe_dispatch(const MoeDispatch &d, cudaStream_t stream, CallInfo
     a.per_cta = (d.T + grid - 1) / grid;
     const unsigned ctas = static_cast<unsigned>(std::max(1, a.per_cta ? (d.T + a.per_cta - 1) / a.per_cta : 1));
     const bool vec = rows_aligned(d.X, d.ldx, b, d.T) && rows_aligned(d.Xs, d.ldxs, b, a.n);
-    const size_t smem = 2u * sizeof(int) * d.E;
+    a.copies = 8;
+    while (a.copies > 1 && 2u * sizeof(int) * d.E * a.copies > 32768u) a.copies /= 2;
+    const size_t smem = 2u * sizeof(int) * d.E * a.copies;
     info->plan = vec ? "moe_dispatch" : "moe_dispatch_unaligned";
     info->launches = 1;
     return vec ? launch_pdl(dispatch_kernel<true>, ctas, kSortThreads, smem, stream, a) : launch_pdl(dispatch_kernel<false>, ctas, kSortThreads, smem, stream, a);
