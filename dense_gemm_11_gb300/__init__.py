@@ -456,13 +456,16 @@ _HALFS = (GEMM_DTYPE_F16, GEMM_DTYPE_BF16)
 _FLOATS = (GEMM_DTYPE_F32, GEMM_DTYPE_F16, GEMM_DTYPE_BF16)
 _FP8S = (GEMM_DTYPE_E4M3, GEMM_DTYPE_E5M2)
 _codes = {}  # torch dtype -> gemm_dtype code
-_raw_stream = None
+_plain_types = {}  # name -> torch dtype
+_raw_stream = _device_now = None
 
 
 def _load_codes():
-    """Fill the type table and look up how to get the current stream; torch is imported on first use."""
-    global _raw_stream
+    """Fill the type tables and look up how to get the current stream and device; torch is imported on first use."""
+    global _raw_stream, _device_now
     import torch
+    _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+    _plain_types.update(int32=torch.int32, float32=torch.float32)
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
     _codes.update({getattr(torch, name): code for code, name in enumerate(_TYPE_NAMES)})
 
@@ -633,60 +636,61 @@ def _vector(t, name, n):
     return t.data_ptr()
 
 
-def _one_device(*tensors):
-    """All on the current device, whose kernels and streams the library uses."""
-    import torch
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"every tensor must be on the current device, cuda:{here}; got one on {t.device}")
-
-
-def _int32(t, name, shape):
-    """Pointer of a contiguous int32 tensor of this shape."""
-    if not _codes:
-        _load_codes()
-    import torch
-    if getattr(t, "dtype", None) != torch.int32 or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA int32 tensor")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _slots(t, name):
-    """(pointer, T, top_k) of a contiguous (T, top_k) int32 tensor."""
-    shape = getattr(t, "shape", ())
-    ptr = _int32(t, name, shape)
-    if len(shape) != 2 or shape[1] < 1:
-        raise ValueError(f"{name} must be (T, top_k) with top_k >= 1, got {tuple(shape)}")
-    return ptr, shape[0], shape[1]
-
-
-def _offsets(t):
-    """(pointer, E) of the offsets of E experts' rows."""
-    shape = getattr(t, "shape", ())
-    ptr = _int32(t, "offsets", shape)
-    if len(shape) != 1 or shape[0] < 1:
-        raise ValueError(f"offsets must be (E + 1,), got {tuple(shape)}")
-    return ptr, shape[0] - 1
-
-
-def _slot_weights(t, name, T, k):
-    import torch
-    if getattr(t, "dtype", None) != torch.float32 or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA float32 tensor")
-    if t.shape != (T, k) or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and {(T, k)}, got {tuple(t.shape)}")
-    return t.data_ptr()
-
-
-def _expert_mats(t, name, allowed):
-    """(pointer, row stride, matrix stride, E, rows, cols, type code) of a 3-D CUDA tensor of row-major matrices."""
+def _placed(t, name, allowed):
+    """(pointer, row stride, rows, cols, type code, device) of a 2-D CUDA tensor, as _typed_mat takes it."""
     if not _codes:
         _load_codes()
     code = _codes.get(getattr(t, "dtype", None), -1)
-    if code not in allowed or not t.is_cuda:
+    if code not in allowed or (device := t.get_device()) < 0:
+        raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in allowed)}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = shape
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} needs unit column stride")
+    if ld < cols:  # a single row has no row stride of its own
+        _check_rows(name, rows, cols, ld)
+        ld = cols
+    return t.data_ptr(), ld or 1, rows, cols, code, device
+
+
+def _packed(t, name, dtype_name, shape):
+    """(pointer, device) of a contiguous CUDA tensor of this type and shape."""
+    if not _codes:
+        _load_codes()
+    if getattr(t, "dtype", None) is not _plain_types[dtype_name] or (device := t.get_device()) < 0:
+        raise TypeError(f"{name} must be a CUDA {dtype_name} tensor")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr(), device
+
+
+def _slots(t, name):
+    """(pointer, T, top_k, device) of a contiguous (T, top_k) int32 tensor."""
+    shape = getattr(t, "shape", ())
+    ptr, device = _packed(t, name, "int32", shape)
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"{name} must be (T, top_k) with top_k >= 1, got {tuple(shape)}")
+    return ptr, shape[0], shape[1], device
+
+
+def _offsets(t):
+    """(pointer, E, device) of the offsets of E experts' rows."""
+    shape = getattr(t, "shape", ())
+    ptr, device = _packed(t, "offsets", "int32", shape)
+    if len(shape) != 1 or shape[0] < 1:
+        raise ValueError(f"offsets must be (E + 1,), got {tuple(shape)}")
+    return ptr, shape[0] - 1, device
+
+
+def _expert_mats(t, name, allowed):
+    """(pointer, row stride, matrix stride, E, rows, cols, type code, device) of a 3-D CUDA tensor of row-major matrices."""
+    if not _codes:
+        _load_codes()
+    code = _codes.get(getattr(t, "dtype", None), -1)
+    if code not in allowed or (device := t.get_device()) < 0:
         raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in allowed)}")
     shape, stride = t.shape, t.stride()
     if len(shape) != 3:
@@ -701,7 +705,11 @@ def _expert_mats(t, name, allowed):
     size = (rows - 1) * ld + cols
     if E > 1 and rows > 0 and cols > 0 and step < size:
         raise ValueError(f"{name} needs matrices that share no memory, got stride {step} for {rows} x {cols} (an expanded tensor?)")
-    return t.data_ptr(), ld or 1, max(step, 1), E, rows, cols, code
+    return t.data_ptr(), ld or 1, max(step, 1), E, rows, cols, code, device
+
+
+def _elsewhere(*devices):
+    raise ValueError(f"every tensor must be on the current device, cuda:{_device_now()}; got them on {devices}")
 
 
 def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
@@ -714,20 +722,23 @@ def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
     (rows from offsets[E] on stay as they are).  X=None and Xs=None: the order alone.
     Limits: E <= 4096, top_k <= 128.
     """
-    ids_ptr, T, k = _slots(ids, "ids")
-    off_ptr, E = _offsets(offsets)
-    rows_ptr = _int32(rows, "rows", (T, k))
+    ids_ptr, T, k, here = _slots(ids, "ids")
+    off_ptr, E, off_on = _offsets(offsets)
+    rows_ptr, rows_on = _packed(rows, "rows", "int32", (T, k))
+    x_on = xs_on = here
     x_ptr = xs_ptr = None
     H, x_type, ldx, ldxs = 0, GEMM_DTYPE_F32, 1, 1
     if X is not None or Xs is not None:
-        x_ptr, ldx, x_rows, H, x_type = _typed_mat(X, "X", _FLOATS)
-        xs_ptr, ldxs, xs_rows, xs_cols, xs_type = _typed_mat(Xs, "Xs", _FLOATS)
+        x_ptr, ldx, x_rows, H, x_type, x_on = _placed(X, "X", _FLOATS)
+        xs_ptr, ldxs, xs_rows, xs_cols, xs_type, xs_on = _placed(Xs, "Xs", _FLOATS)
         if xs_type != x_type:
             raise TypeError("X and Xs must have one type")
         if x_rows != T or xs_cols != H or xs_rows < T * k:
             raise ValueError(f"shape mismatch ids{(T, k)} X{tuple(X.shape)} Xs{tuple(Xs.shape)} (at least T * top_k rows)")
-    _one_device(ids, X, Xs, offsets, rows)
-    st = lib().gemm_moe_dispatch(T, E, k, H, ids_ptr, x_ptr, x_type, ldx, xs_ptr, ldxs, off_ptr, rows_ptr, _stream_ptr(stream, ids))
+    if not here == off_on == rows_on == x_on == xs_on == _device_now():
+        _elsewhere(here, off_on, rows_on, x_on, xs_on)
+    st = lib().gemm_moe_dispatch(T, E, k, H, ids_ptr, x_ptr, x_type, ldx, xs_ptr, ldxs, off_ptr, rows_ptr,
+                                 _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_dispatch")
 
@@ -738,16 +749,18 @@ def moe_combine(Ys, rows, Y, weights=None, *, stream=None) -> None:
     Ys: (R, H), Y: (T, H), both fp32, fp16 or bf16.  rows: (T, top_k) int32 (moe_dispatch); a slot without a row adds
     nothing.  weights: (T, top_k) fp32, or None: ones, which also makes this the gradient of moe_dispatch's copy.
     """
-    ys_ptr, ldys, R, H, y_type = _typed_mat(Ys, "Ys", _FLOATS)
-    y_ptr, ldy, T, y_cols, code = _typed_mat(Y, "Y", _FLOATS)
-    rows_ptr, r_T, k = _slots(rows, "rows")
+    ys_ptr, ldys, R, H, y_type, ys_on = _placed(Ys, "Ys", _FLOATS)
+    y_ptr, ldy, T, y_cols, code, here = _placed(Y, "Y", _FLOATS)
+    rows_ptr, r_T, k, rows_on = _slots(rows, "rows")
     if code != y_type:
         raise TypeError("Ys and Y must have one type")
     if r_T != T or y_cols != H:
         raise ValueError(f"shape mismatch Ys{tuple(Ys.shape)} rows{tuple(rows.shape)} Y{tuple(Y.shape)}")
-    w_ptr = None if weights is None else _slot_weights(weights, "weights", T, k)
-    _one_device(Ys, rows, Y, weights)
-    st = lib().gemm_moe_combine(T, k, H, R, ys_ptr, y_type, ldys, rows_ptr, w_ptr, y_ptr, ldy, _stream_ptr(stream, Y))
+    w_ptr, w_on = (None, here) if weights is None else _packed(weights, "weights", "float32", (T, k))
+    if not here == ys_on == rows_on == w_on == _device_now():
+        _elsewhere(here, ys_on, rows_on, w_on)
+    st = lib().gemm_moe_combine(T, k, H, R, ys_ptr, y_type, ldys, rows_ptr, w_ptr, y_ptr, ldy,
+                                _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_combine")
 
@@ -758,18 +771,20 @@ def moe_combine_grad(dY, Ys, rows, weights, dYs, dweights, *, stream=None) -> No
     dY: (T, H), Ys and dYs: (R, H), one type; rows: (T, top_k) int32; weights and dweights: (T, top_k) fp32.  A slot
     without a row gets dweights 0; rows of dYs that no slot names stay as they are.
     """
-    dy_ptr, lddy, T, H, code = _typed_mat(dY, "dY", _FLOATS)
-    ys_ptr, ldys, R, ys_cols, ys_type = _typed_mat(Ys, "Ys", _FLOATS)
-    dys_ptr, lddys, dys_rows, dys_cols, dys_type = _typed_mat(dYs, "dYs", _FLOATS)
-    rows_ptr, r_T, k = _slots(rows, "rows")
+    dy_ptr, lddy, T, H, code, here = _placed(dY, "dY", _FLOATS)
+    ys_ptr, ldys, R, ys_cols, ys_type, ys_on = _placed(Ys, "Ys", _FLOATS)
+    dys_ptr, lddys, dys_rows, dys_cols, dys_type, dys_on = _placed(dYs, "dYs", _FLOATS)
+    rows_ptr, r_T, k, rows_on = _slots(rows, "rows")
     if ys_type != code or dys_type != code:
         raise TypeError("dY, Ys and dYs must have one type")
     if r_T != T or ys_cols != H or (dys_rows, dys_cols) != (R, H):
         raise ValueError(f"shape mismatch dY{tuple(dY.shape)} Ys{tuple(Ys.shape)} rows{tuple(rows.shape)} dYs{tuple(dYs.shape)}")
-    w_ptr, dw_ptr = _slot_weights(weights, "weights", T, k), _slot_weights(dweights, "dweights", T, k)
-    _one_device(dY, Ys, rows, weights, dYs, dweights)
+    w_ptr, w_on = _packed(weights, "weights", "float32", (T, k))
+    dw_ptr, dw_on = _packed(dweights, "dweights", "float32", (T, k))
+    if not here == ys_on == dys_on == rows_on == w_on == dw_on == _device_now():
+        _elsewhere(here, ys_on, dys_on, rows_on, w_on, dw_on)
     st = lib().gemm_moe_combine_grad(T, k, H, R, dy_ptr, code, lddy, ys_ptr, ldys, rows_ptr, w_ptr, dys_ptr, lddys, dw_ptr,
-                                     _stream_ptr(stream, dY))
+                                     _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_combine_grad")
 
@@ -782,17 +797,18 @@ def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, *, b_t
     that no expert has stay as they are.  A's and B's rows start on 16-byte boundaries (row strides multiples of 8).
     So y = x W^T of every expert takes W as it is, and dx = dy W the same W with b_trans=False.
     """
-    a_ptr, lda, R, K, a_type = _typed_mat(A, "A", _HALFS)
-    b_ptr, ldb, stride_b, E, b_rows, b_cols, b_type = _expert_mats(B, "B", _HALFS)
-    c_ptr, ldc, c_rows, N, c_type = _typed_mat(C, "C", _FLOATS)
-    off_ptr, off_E = _offsets(offsets)
+    a_ptr, lda, R, K, a_type, here = _placed(A, "A", _HALFS)
+    b_ptr, ldb, stride_b, E, b_rows, b_cols, b_type, b_on = _expert_mats(B, "B", _HALFS)
+    c_ptr, ldc, c_rows, N, c_type, c_on = _placed(C, "C", _FLOATS)
+    off_ptr, off_E, off_on = _offsets(offsets)
     if a_type != b_type:
         raise TypeError("A and B must both be float16 or both bfloat16")
     if c_rows != R or off_E != E or (b_rows, b_cols) != ((N, K) if b_trans else (K, N)):
         raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
-    _one_device(A, B, C, offsets)
+    if not here == b_on == c_on == off_on == _device_now():
+        _elsewhere(here, b_on, c_on, off_on)
     st = lib().gemm_grouped_f32acc(E, R, N, K, alpha, a_ptr, lda, b_ptr, ldb, stride_b, a_type, 1 if b_trans else 0, beta, c_ptr,
-                                   c_type, ldc, off_ptr, _stream_ptr(stream, A))
+                                   c_type, ldc, off_ptr, _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_grouped_f32acc")
 
@@ -803,38 +819,37 @@ def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, 
     A: (R, M), B: (R, N), both fp16 or both bf16; C: (E, M, N) fp32, fp16 or bf16.  An expert without rows gets
     beta * C[e].  So dW = dy^T x of every expert takes dy as A and x as B.  offsets and alignment as for gemm_grouped.
     """
-    a_ptr, lda, R, M, a_type = _typed_mat(A, "A", _HALFS)
-    b_ptr, ldb, b_rows, N, b_type = _typed_mat(B, "B", _HALFS)
-    c_ptr, ldc, stride_c, E, c_rows, c_cols, c_type = _expert_mats(C, "C", _FLOATS)
-    off_ptr, off_E = _offsets(offsets)
+    a_ptr, lda, R, M, a_type, here = _placed(A, "A", _HALFS)
+    b_ptr, ldb, b_rows, N, b_type, b_on = _placed(B, "B", _HALFS)
+    c_ptr, ldc, stride_c, E, c_rows, c_cols, c_type, c_on = _expert_mats(C, "C", _FLOATS)
+    off_ptr, off_E, off_on = _offsets(offsets)
     if a_type != b_type:
         raise TypeError("A and B must both be float16 or both bfloat16")
     if b_rows != R or off_E != E or (c_rows, c_cols) != (M, N):
         raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
-    _one_device(A, B, C, offsets)
+    if not here == b_on == c_on == off_on == _device_now():
+        _elsewhere(here, b_on, c_on, off_on)
     st = lib().gemm_grouped_wgrad_f32acc(E, R, M, N, alpha, a_ptr, lda, b_ptr, ldb, a_type, beta, c_ptr, c_type, ldc, stride_c,
-                                         off_ptr, _stream_ptr(stream, A))
+                                         off_ptr, _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_grouped_wgrad_f32acc")
 
 
-def _kept(Q, S, names, rows, cols, q_type=None):
-    """(pointer, row stride, type) of Q and (pointer, row stride) of S, a rows x cols matrix in 8 bits (layout "rows")."""
-    q_ptr, ldq, q_rows, q_cols, code = _typed_mat(Q, names[0], _FP8S)
-    s_ptr, lds, s_rows, s_cols, _ = _typed_mat(S, names[1], _F32)
-    if ((q_rows, q_cols), (s_rows, s_cols)) != _fp8_shapes(rows, cols, "rows"):
-        raise ValueError(f"{names[0]}{tuple(Q.shape)} and {names[1]}{tuple(S.shape)} do not hold {rows} x {cols} in layout 'rows'")
-    if q_type is not None and code != q_type:
-        raise TypeError("GQ and UQ must have one type")
-    return q_ptr, ldq, code, s_ptr, lds
+def _kept(Q, S, q_name, s_name, rows, cols):
+    """(pointer, row stride, type, device) of Q and (pointer, row stride, device) of S, a rows x cols matrix in 8 bits (layout "rows")."""
+    q_ptr, ldq, q_rows, q_cols, code, q_on = _placed(Q, q_name, _FP8S)
+    s_ptr, lds, s_rows, s_cols, _, s_on = _placed(S, s_name, _F32)
+    if q_rows != rows or q_cols != cols or s_rows != (cols + 127) // 128 or s_cols != rows:
+        raise ValueError(f"{q_name}{tuple(Q.shape)} and {s_name}{tuple(S.shape)} do not hold {rows} x {cols} in layout 'rows'")
+    return q_ptr, ldq, code, q_on, s_ptr, lds, s_on
 
 
 def _same(t, name, rows, cols, code):
-    """(pointer, row stride) of a rows x cols matrix of type `code`."""
-    ptr, ld, r, c, _ = _typed_mat(t, name, (code,))
-    if (r, c) != (rows, cols):
+    """(pointer, row stride, device) of a rows x cols matrix of type `code`."""
+    ptr, ld, r, c, _, device = _placed(t, name, (code,))
+    if r != rows or c != cols:
         raise ValueError(f"{name} must be {(rows, cols)}, got {tuple(t.shape)}")
-    return ptr, ld
+    return ptr, ld, device
 
 
 def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *, stream=None) -> None:
@@ -843,19 +858,23 @@ def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *
     G, U, H: (rows, cols), one type, fp32, fp16 or bf16.  GQ, GS and UQ, US receive what fp8_quantize makes of G and U
     with layout "rows" (fp8_empty() makes fitting pairs).  U=None (and UQ=US=None): H = act(G).  act: any GEMM_ACT_*.
     """
-    g_ptr, ldg, rows, cols, code = _typed_mat(G, "G", _FLOATS)
-    h_ptr, ldh = _same(H, "H", rows, cols, code)
-    gq_ptr, ldgq, q_type, gs_ptr, ldgs = _kept(GQ, GS, ("GQ", "GS"), rows, cols)
+    g_ptr, ldg, rows, cols, code, here = _placed(G, "G", _FLOATS)
+    h_ptr, ldh, h_on = _same(H, "H", rows, cols, code)
+    gq_ptr, ldgq, q_type, gq_on, gs_ptr, ldgs, gs_on = _kept(GQ, GS, "GQ", "GS", rows, cols)
     u_ptr = uq_ptr = us_ptr = None
     ldu = lduq = ldus = 1
+    u_on = uq_on = us_on = here
     if U is not None:
-        u_ptr, ldu = _same(U, "U", rows, cols, code)
-        uq_ptr, lduq, _, us_ptr, ldus = _kept(UQ, US, ("UQ", "US"), rows, cols, q_type)
+        u_ptr, ldu, u_on = _same(U, "U", rows, cols, code)
+        uq_ptr, lduq, uq_type, uq_on, us_ptr, ldus, us_on = _kept(UQ, US, "UQ", "US", rows, cols)
+        if uq_type != q_type:
+            raise TypeError("GQ and UQ must have one type")
     elif UQ is not None or US is not None:
         raise ValueError("UQ and US are for a gate: without U they must be None")
-    _one_device(G, U, H, GQ, GS, UQ, US)
+    if not here == h_on == gq_on == gs_on == u_on == uq_on == us_on == _device_now():
+        _elsewhere(here, h_on, gq_on, gs_on, u_on, uq_on, us_on)
     st = lib().gemm_fp8_gated_act(rows, cols, g_ptr, ldg, u_ptr, ldu, code, h_ptr, ldh, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq,
-                                  us_ptr, ldus, q_type, act, _stream_ptr(stream, G))
+                                  us_ptr, ldus, q_type, act, _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_gated_act")
 
@@ -867,21 +886,25 @@ def fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU, H=None, act: int = GEMM_ACT_S
     weights that H is multiplied by).  dH, dG, dU, H: (rows, cols), one type, fp32, fp16 or bf16.
     Without a gate UQ, US and dU are None, and u' is 1.
     """
-    dh_ptr, lddh, rows, cols, code = _typed_mat(dH, "dH", _FLOATS)
-    gq_ptr, ldgq, q_type, gs_ptr, ldgs = _kept(GQ, GS, ("GQ", "GS"), rows, cols)
-    dg_ptr, lddg = _same(dG, "dG", rows, cols, code)
+    dh_ptr, lddh, rows, cols, code, here = _placed(dH, "dH", _FLOATS)
+    gq_ptr, ldgq, q_type, gq_on, gs_ptr, ldgs, gs_on = _kept(GQ, GS, "GQ", "GS", rows, cols)
+    dg_ptr, lddg, dg_on = _same(dG, "dG", rows, cols, code)
     uq_ptr = us_ptr = du_ptr = h_ptr = None
     lduq = ldus = lddu = ldh = 1
+    uq_on = us_on = du_on = h_on = here
     if UQ is not None:
-        uq_ptr, lduq, _, us_ptr, ldus = _kept(UQ, US, ("UQ", "US"), rows, cols, q_type)
-        du_ptr, lddu = _same(dU, "dU", rows, cols, code)
+        uq_ptr, lduq, uq_type, uq_on, us_ptr, ldus, us_on = _kept(UQ, US, "UQ", "US", rows, cols)
+        if uq_type != q_type:
+            raise TypeError("GQ and UQ must have one type")
+        du_ptr, lddu, du_on = _same(dU, "dU", rows, cols, code)
     elif US is not None or dU is not None:
         raise ValueError("US and dU are for a gate: without UQ they must be None")
     if H is not None:
-        h_ptr, ldh = _same(H, "H", rows, cols, code)
-    _one_device(dH, GQ, GS, UQ, US, dG, dU, H)
+        h_ptr, ldh, h_on = _same(H, "H", rows, cols, code)
+    if not here == gq_on == gs_on == dg_on == uq_on == us_on == du_on == h_on == _device_now():
+        _elsewhere(here, gq_on, gs_on, dg_on, uq_on, us_on, du_on, h_on)
     st = lib().gemm_fp8_gated_act_grad(rows, cols, dh_ptr, lddh, code, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq, us_ptr, ldus,
-                                       q_type, dg_ptr, lddg, du_ptr, lddu, h_ptr, ldh, act, _stream_ptr(stream, dH))
+                                       q_type, dg_ptr, lddg, du_ptr, lddu, h_ptr, ldh, act, _raw_stream(here) if stream is None else stream.cuda_stream)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_gated_act_grad")
 

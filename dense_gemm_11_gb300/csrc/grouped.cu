@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ends_parity ^= 1u << stage;
                     uint8_t *b = sB + stage * kHalf, *a = sA + stage * kHalf;
                     const uint4 zero = make_uint4(0, 0, 0, 0);
-                    for (int i = valid * 8 + lane; i < kKB * 8; i += 32) {
+                    const int reached = (valid + 15) / 16 * 16;  // by the MMAs
+                    for (int i = valid * 8 + lane; i < reached * 8; i += 32) {
                         reinterpret_cast<uint4 *>(b)[i] = zero;
                         reinterpret_cast<uint4 *>(b + kBox)[i] = zero;
                         reinterpret_cast<uint4 *>(a)[i] = zero;

@@ -6,7 +6,6 @@ import torch
 
 import dense_gemm_11_gb300 as g
 from conftest import gpu_available
-from test_row_strides import OnCuda
 
 FAKE = 0x10000
 F32, F16, BF16, E4 = g.GEMM_DTYPE_F32, g.GEMM_DTYPE_F16, g.GEMM_DTYPE_BF16, g.GEMM_DTYPE_E4M3
@@ -99,6 +98,14 @@ B16, I32, F = torch.bfloat16, torch.int32, torch.float32
 E4T = torch.float8_e4m3fn
 
 
+class OnCuda(torch.Tensor):
+    """A CPU tensor that says it is a CUDA tensor: only its properties are looked at here."""
+    is_cuda = True
+
+    def get_device(self):
+        return 0
+
+
 def on(*shape, dtype=B16):
     return torch.zeros(shape).to(dtype).as_subclass(OnCuda)
 
@@ -167,6 +174,7 @@ def test_what_does_not_fit(function, change):
 @host_only
 @pytest.mark.parametrize("function", list(arguments()))
 def test_other_device(function, monkeypatch):
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    g._load_codes()
+    monkeypatch.setattr(g, "_device_now", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         getattr(g, function)(**arguments()[function])
