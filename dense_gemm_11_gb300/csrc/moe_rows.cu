@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortBatch = 1024;  // slots that are ranked and then copied together
+static_assert(kDispatchMaxExperts <= 8192, "an expert and its slots among 32 in one word");
 
 struct DispatchArgs {
     int T, E, k, n;  // n = T k
@@ -40,28 +41,36 @@ struct DispatchArgs {
     size_t xs_extent;  // bytes, checked by GEMM11_DEBUG builds
 };
 
-// One segment of a row to its k copies: U times 16 bytes a lane.
+// A segment of a row: U times 16 bytes a lane.
 template <int U>
-__device__ __forceinline__ void copy_vec(const DispatchArgs &p, const uint8_t *from, const int *pos, int c0, int lane) {
-    const int full = p.row_bytes >> 4;
+struct Segment {
     uint4 v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int c = c0 + u * 32 + lane;
-        if (c < full) v[u] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
-    }
-    for (int j = 0; j < p.k; ++j) {
-        const int r = pos[j];
-        if (r < 0) continue;
-        uint8_t *to = p.Xs + r * p.xs_bytes;
-        if (!debug_in_bounds(static_cast<size_t>(r * p.xs_bytes + p.row_bytes) <= p.xs_extent, p.err)) continue;
+    __device__ __forceinline__ void load(const DispatchArgs &p, const uint8_t *from, int c0, int lane) {
+        const int full = p.row_bytes >> 4;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * 32 + lane;
-            if (c < full) reinterpret_cast<uint4 *>(to)[c] = v[u];
+            if (c < full) v[u] = __ldg(reinterpret_cast<const uint4 *>(from) + c);
         }
     }
-}
+    __device__ __forceinline__ void store(const DispatchArgs &p, const int *pos, int c0, int lane) const {
+        const int full = p.row_bytes >> 4;
+        for (int j = 0; j < p.k; ++j) {
+            const int r = pos[j];
+            if (r < 0) continue;
+            uint8_t *to = p.Xs + r * p.xs_bytes;
+            if (!debug_in_bounds(static_cast<size_t>(r * p.xs_bytes + p.row_bytes) <= p.xs_extent, p.err)) continue;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int c = c0 + u * 32 + lane;
+                if (c < full) reinterpret_cast<uint4 *>(to)[c] = v[u];
+            }
+        }
+    }
+};
+constexpr int kSegment = 2;                        // 16-byte pieces of a lane
+constexpr int kSegmentPieces = 32 * kSegment;      // of a warp
+constexpr int kSegmentElements = 128;              // of a warp, where rows are not aligned
 
 // Elements [first, last) of a row to its copies, one a lane.
 template <typename T>
@@ -78,23 +87,25 @@ __device__ __forceinline__ void copy_elements(const DispatchArgs &p, const uint8
 }
 
 // Every CTA counts all the slots itself, those before its own tokens apart, so
-// that it knows where its slots go without waiting for another CTA.
+// that it knows where its slots go without waiting for another CTA: 49,152 slots
+// over 64 experts take 3.5 us.  (Clusters of eight that share the counting save 1
+// us of that and lose it again: of the 152 SMs they fill 128.)
 template <bool VEC>
 __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchArgs p) {
     extern __shared__ int counts[];  // of each expert: slots before this CTA's, then the others
     __shared__ int warp_sum[32];
     __shared__ int pos[kSortBatch];
-    const int copies = p.copies;  // neighbouring lanes count in counters of their own: fewer of a warp's additions meet
-    int *before = counts, *rest = counts + p.E * copies;
+    const int copies = p.copies, E = p.E;  // neighbouring lanes count in counters of their own: fewer of a warp's additions meet
+    int *const before = counts, *const rest = counts + E * copies;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.per_cta, t1 = min(p.T, t0 + p.per_cta);
-    for (int e = threadIdx.x; e < 2 * p.E * copies; e += kSortThreads) counts[e] = 0;
+    for (int e = threadIdx.x; e < 2 * E * copies; e += kSortThreads) counts[e] = 0;
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     const int mine = t0 * p.k, my_copy = lane & (copies - 1);
     auto count = [&](int e, int i) {
-        if (static_cast<unsigned>(e) < static_cast<unsigned>(p.E)) atomicAdd((i < mine ? before : rest) + e * copies + my_copy, 1);
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd((i < mine ? before : rest) + e * copies + my_copy, 1);
     };
     int done = 0;
     if (reinterpret_cast<uintptr_t>(p.ids) % 16 == 0) {
@@ -120,14 +131,16 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     for (int i = done + threadIdx.x; i < p.n; i += kSortThreads) count(__ldg(p.ids + i), i);
     __syncthreads();
 
-    // before[e] becomes the row of this CTA's first slot of expert e.
+    // before[e] becomes next[e], the row of this CTA's first slot of expert e.
+    int *const next = before;
     constexpr int kPer = kDispatchMaxExperts / kSortThreads;
+    const int per = (E + kSortThreads - 1) / kSortThreads;  // experts of a thread
     int total[kPer], ahead[kPer], sum = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
+        const int e = threadIdx.x * per + i;
         total[i] = ahead[i] = 0;
-        if (e < p.E) {
+        if (i < per && e < E) {
             for (int c = 0; c < copies; ++c) {
                 ahead[i] += before[e * copies + c];
                 total[i] += rest[e * copies + c];
@@ -157,61 +170,77 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     int start = incl - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * kPer + i;
-        if (e < p.E) {
-            before[e] = ahead[i] + start;
+        const int e = threadIdx.x * per + i;
+        if (i < per && e < E) {
+            next[e] = ahead[i] + start;
             if (blockIdx.x == 0) p.offsets[e] = start;
         }
         start += total[i];
     }
-    if (blockIdx.x == 0 && threadIdx.x == kSortThreads - 1) p.offsets[p.E] = start;
-    __syncthreads();
+    if (blockIdx.x == 0 && threadIdx.x == kSortThreads - 1) p.offsets[E] = start;
 
     const int batch = kSortBatch / p.k;  // tokens
-    const int segments = VEC ? (p.row_bytes + 2047) / 2048 : (p.row_bytes / p.esize + 127) / 128;
+    const int segments = VEC ? ((p.row_bytes >> 4) + kSegmentPieces - 1) / kSegmentPieces : (p.row_bytes / p.esize + kSegmentElements - 1) / kSegmentElements;
+    const int elements = p.row_bytes / p.esize, whole = (p.row_bytes >> 4) * (16 / p.esize);
     for (int t = t0; t < t1; t += batch) {
-        const int tokens = min(batch, t1 - t), slots = tokens * p.k;
+        const int tokens = min(batch, t1 - t), slots = tokens * p.k, units = tokens * segments;
+        auto source = [&](int u) { return p.X + static_cast<long long>(t + u / segments) * p.x_bytes; };
+        Segment<kSegment> now;
+        if (VEC && warp < units) now.load(p, source(warp), warp % segments * kSegmentPieces, lane);
+        // Slots of one expert among the 32 of a warp (a match takes 400 clocks: all
+        // warps at once), then, 32 after 32, where the expert's rows have come to.
+        __syncthreads();  // the last batch's rows are written, and the first's counts
+        static_assert(kSortBatch <= kSortThreads, "a slot a thread");
+        if (warp * 32 < slots) {
+            const int i = threadIdx.x;
+            int e = i < slots ? __ldg(p.ids + t * p.k + i) : -1;
+            if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) e = -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int rank = __popc(same & ((1u << lane) - 1u)), alike = lane == __ffs(same) - 1 ? __popc(same) : 0;
+            if (i < slots) pos[i] = e < 0 ? -1 : e | rank << 13 | alike << 18;
+        }
+        __syncthreads();
         if (warp == 0) {
             for (int i0 = 0; i0 < slots; i0 += 32) {
-                const int i = i0 + lane;
-                int e = i < slots ? __ldg(p.ids + t * p.k + i) : -1;
-                if (static_cast<unsigned>(e) >= static_cast<unsigned>(p.E)) e = -1;
-                const unsigned same = __match_any_sync(0xffffffffu, e);
-                const int r = e >= 0 ? before[e] + __popc(same & ((1u << lane) - 1u)) : -1;
+                const int i = i0 + lane, packed = i < slots ? pos[i] : -1, e = packed & 0x1FFF;
+                const int r = packed >= 0 ? next[e] : 0;
                 __syncwarp();
-                if (e >= 0 && lane == __ffs(same) - 1) before[e] += __popc(same);
-                __syncwarp();
-                if (i < slots) {
-                    pos[i] = r;
-                    p.rows[t * p.k + i] = r;
+                if (packed >= 0) {
+                    pos[i] = r + (packed >> 13 & 31);
+                    if (packed >> 18) next[e] = r + (packed >> 18);
                 }
+                __syncwarp();
             }
         }
         __syncthreads();
-        if (p.row_bytes > 0) {
-            for (int u = warp; u < tokens * segments; u += kSortThreads / 32) {
-                const int i = u / segments, s = u % segments;
-                const uint8_t *from = p.X + static_cast<long long>(t + i) * p.x_bytes;
-                const int *to = pos + i * p.k;
-                if (VEC) {
-                    copy_vec<4>(p, from, to, s * 128, lane);
-                    const int elements = p.row_bytes / p.esize, whole = (p.row_bytes >> 4) * (16 / p.esize);
-                    if (s == segments - 1 && whole < elements) {
-                        if (p.esize == 2)
-                            copy_elements<uint16_t>(p, from, to, whole, elements, lane);
-                        else
-                            copy_elements<uint32_t>(p, from, to, whole, elements, lane);
-                    }
-                } else {
-                    const int first = s * 128, last = min(first + 128, p.row_bytes / p.esize);
+        for (int i = threadIdx.x; i < slots; i += kSortThreads) p.rows[t * p.k + i] = pos[i];
+        if (VEC) {
+            // the next unit is read before this one is written
+            for (int u = warp; u < units; u += kSortThreads / 32) {
+                const int ahead_u = u + kSortThreads / 32;
+                Segment<kSegment> then;
+                if (ahead_u < units) then.load(p, source(ahead_u), ahead_u % segments * kSegmentPieces, lane);
+                now.store(p, pos + u / segments * p.k, u % segments * kSegmentPieces, lane);
+                now = then;
+            }
+            if (whole < elements) {
+                for (int i = warp; i < tokens; i += kSortThreads / 32) {
+                    const uint8_t *from = p.X + static_cast<long long>(t + i) * p.x_bytes;
                     if (p.esize == 2)
-                        copy_elements<uint16_t>(p, from, to, first, last, lane);
+                        copy_elements<uint16_t>(p, from, pos + i * p.k, whole, elements, lane);
                     else
-                        copy_elements<uint32_t>(p, from, to, first, last, lane);
+                        copy_elements<uint32_t>(p, from, pos + i * p.k, whole, elements, lane);
                 }
             }
+        } else {
+            for (int u = warp; u < units; u += kSortThreads / 32) {
+                const int begin = u % segments * kSegmentElements, end = min(begin + kSegmentElements, elements);
+                if (p.esize == 2)
+                    copy_elements<uint16_t>(p, source(u), pos + u / segments * p.k, begin, end, lane);
+                else
+                    copy_elements<uint32_t>(p, source(u), pos + u / segments * p.k, begin, end, lane);
+            }
         }
-        __syncthreads();
     }
 }
 
@@ -439,11 +468,11 @@ cudaError_t run_moe_dispatch(const MoeDispatch &d, cudaStream_t stream, CallInfo
         a.xs_extent = static_cast<size_t>((a.n - 1LL) * a.xs_bytes + a.row_bytes);
         a.xs_extent -= std::min(a.xs_extent, debug_shrink_c() * b);
     }
-    const int grid = std::max(1, std::min(d.T, device_sm_count()));
-    a.per_cta = (d.T + grid - 1) / grid;
-    const unsigned ctas = static_cast<unsigned>(std::max(1, a.per_cta ? (d.T + a.per_cta - 1) / a.per_cta : 1));
     const bool vec = rows_aligned(d.X, d.ldx, b, d.T) && rows_aligned(d.Xs, d.ldxs, b, a.n);
-    a.copies = 8;
+    const int grid = std::max(1, std::min(d.T, device_sm_count()));
+    a.per_cta = std::max(1, (d.T + grid - 1) / grid);
+    const unsigned ctas = static_cast<unsigned>(std::max(1, (d.T + a.per_cta - 1) / a.per_cta));
+    a.copies = a.n >= 4096 ? 8 : 1;
     while (a.copies > 1 && 2u * sizeof(int) * d.E * a.copies > 32768u) a.copies /= 2;
     const size_t smem = 2u * sizeof(int) * d.E * a.copies;
     info->plan = vec ? "moe_dispatch" : "moe_dispatch_unaligned";
