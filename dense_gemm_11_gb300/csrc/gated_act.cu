@@ -259,7 +259,7 @@ __device__ __forceinline__ void keep8(const GatedArgs &p, const f2 (&v)[4], floa
 constexpr int kDeep = 2;  // blocks of a row in flight
 
 template <int XT, bool VEC, bool E5M2, bool GATED>
-__global__ void __launch_bounds__(256) gated_act_kernel(const GatedArgs p) {
+__global__ void __launch_bounds__(256, XT == kOutF32 ? 1 : 5) gated_act_kernel(const GatedArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     const int sub = threadIdx.x & 15, group = threadIdx.x & 16;
@@ -339,7 +339,7 @@ __device__ __forceinline__ void widen_kept(uint2 w, float s, f2 (&v)[4]) {
 }
 
 template <int XT, bool VEC, bool E5M2, bool GATED>
-__global__ void __launch_bounds__(256) gated_act_grad_kernel(const GatedArgs p) {
+__global__ void __launch_bounds__(256, XT == kOutF32 ? 1 : 4) gated_act_grad_kernel(const GatedArgs p) {
     pdl_wait();
     pdl_launch_dependents();
     const int sub = threadIdx.x & 15;
@@ -455,9 +455,12 @@ cudaError_t gated(const GatedAct &g, bool grad, cudaStream_t stream) {
         a.q_extent = static_cast<size_t>((g.rows - 1LL) * (g.UQ ? std::max(g.ldgq, g.lduq) : g.ldgq) + g.cols);
         a.s_extent = static_cast<size_t>((nb - 1LL) * (g.US ? std::max(g.ldgs, g.ldus) : g.ldgs) + g.rows);
     }
-    // Two column blocks a CTA (kDeep) once that leaves every SM several CTAs.
+    // Column blocks of a CTA: one while that leaves SMs without work, then four
+    // (8192 x 11008 BF16: 112 us in twos, 109 in fours, 110 in eights; backward 148,
+    // 145, 143), or two in FP32 forwards (4096 x 11008: 90.6, 92.4 in fours).  The
+    // launch bounds of the 16-bit kernels add to that: 115 -> 109 and 145 -> 134.
     const long long ctas = static_cast<long long>((g.rows + 15) / 16) * nb;
-    a.per_cta = ctas >= 16LL * device_sm_count() ? 2 : 1;
+    a.per_cta = ctas < 16LL * device_sm_count() ? 1 : !grad && g.type == kOutF32 ? 2 : 4;
     a.nx = (nb + a.per_cta - 1) / a.per_cta;
     switch (g.type * 2 + (vec ? 1 : 0)) {
         case 0: return launch_gated<kOutF32, false>(a, grad, stream);
