@@ -37,7 +37,7 @@ constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Rows of A that one copy brings in, for CTAs with up to kFewRows rows, up to
 // kSomeRows, and more.
-constexpr int kBoxFew = 8, kBoxSome = 32, kBoxMany = 128, kFewRows = 24, kSomeRows = 96;
+constexpr int kBoxFew = 8, kBoxSome = 32, kBoxMany = 128, kFewRows = 3 * kBoxFew, kSomeRows = 3 * kBoxSome;
 
 // forward: C[r] = A[r] B[e]^T, dgrad: C[r] = A[r] B[e], wgrad: C[e] = A^T B.
 enum Mode { kForward, kDgrad, kWgrad };
@@ -119,6 +119,15 @@ struct TileList {
         tile.k0 = WGRAD ? s : 0, tile.k1 = WGRAD ? e : p.k;
         tile.n0 *= kTile;
         if (!p.product) tile.k1 = tile.k0;
+        // The same in every lane: told so, the compiler keeps what depends on these
+        // in uniform registers, which the copies and MMAs take.
+        tile.e = __shfl_sync(0xffffffffu, tile.e, 0);
+        tile.m0 = __shfl_sync(0xffffffffu, tile.m0, 0);
+        tile.n0 = __shfl_sync(0xffffffffu, tile.n0, 0);
+        tile.row_end = __shfl_sync(0xffffffffu, tile.row_end, 0);
+        tile.span = __shfl_sync(0xffffffffu, tile.span, 0);
+        tile.k0 = __shfl_sync(0xffffffffu, tile.k0, 0);
+        tile.k1 = __shfl_sync(0xffffffffu, tile.k1, 0);
         return true;
     }
 };
@@ -232,11 +241,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
+            const uint32_t full_even = mapa_shared(smem_u32(full), 0), at_b = smem_u32(sB), at_a = smem_u32(sA);
             for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
                 const int half = tile.span >> 1, my_m = tile.m0 + rank * half, my_n = tile.n0 + rank * 128;
                 // rows of A (wgrad: columns) come in boxes
                 const int box = MODE == kWgrad ? 64 : half <= kFewRows ? kBoxFew : half <= kSomeRows ? kBoxSome : kBoxMany;
-                const CUtensorMap *const map = box == kBoxFew ? &tm_a_few : box == kBoxSome ? &tm_a_some : &tm_a;
                 const int boxes = (half + box - 1) / box, box_bytes = box * kKB * 2;
                 const uint32_t tx = kHalf + boxes * box_bytes;
                 const int blocks = tile_blocks(tile);
@@ -260,24 +269,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (ends & (1u << stage)) ends_parity ^= 1u << stage;
                         ends |= 1u << stage;
                     } else {
-                        const uint32_t bar = mapa_shared(smem_u32(&full[stage]), 0);
+                        const uint32_t bar = full_even + stage * 8, b0 = at_b + stage * kHalf, a0 = at_a + stage * kHalf;
                         if (elect_one()) {
                             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * tx);
                             if (MODE == kWgrad) {
                                 if (leader) mbar_arrive(&full[stage]);
-                                tma_load_2d_pair(&tm_b, bar, b, my_n, k0);
-                                tma_load_2d_pair(&tm_b, bar, b + kBox, my_n + 64, k0);
-                            } else if (MODE == kDgrad) {
-                                tma_load_3d_pair(&tm_b, bar, b, my_n, k0, tile.e);
-                                tma_load_3d_pair(&tm_b, bar, b + kBox, my_n + 64, k0, tile.e);
+                                tma_load_2d_pair_at(&tm_b, bar, b0, my_n, k0);
+                                tma_load_2d_pair_at(&tm_b, bar, b0 + kBox, my_n + 64, k0);
+                                tma_load_2d_pair_at(&tm_a, bar, a0, my_m, k0);
+                                if (half > 64) tma_load_2d_pair_at(&tm_a, bar, a0 + kBox, my_m + 64, k0);
                             } else {
-                                tma_load_3d_pair(&tm_b, bar, b, k0, my_n, tile.e);
-                            }
-                            for (int i = 0; i < boxes; ++i) {
-                                if (MODE == kWgrad)
-                                    tma_load_2d_pair(&tm_a, bar, a + i * kBox, my_m + i * 64, k0);
-                                else
-                                    tma_load_2d_pair(map, bar, a + i * box_bytes, k0, my_m + i * box);
+                                if (MODE == kDgrad) {
+                                    tma_load_3d_pair_at(&tm_b, bar, b0, my_n, k0, tile.e);
+                                    tma_load_3d_pair_at(&tm_b, bar, b0 + kBox, my_n + 64, k0, tile.e);
+                                } else {
+                                    tma_load_3d_pair_at(&tm_b, bar, b0, k0, my_n, tile.e);
+                                }
+                                if (half > kSomeRows) {
+                                    tma_load_2d_pair_at(&tm_a, bar, a0, k0, my_m);
+                                } else if (half > kFewRows) {
+                                    tma_load_2d_pair_at(&tm_a_some, bar, a0, k0, my_m);
+                                    if (half > 32) tma_load_2d_pair_at(&tm_a_some, bar, a0 + 4096, k0, my_m + 32);
+                                    if (half > 64) tma_load_2d_pair_at(&tm_a_some, bar, a0 + 8192, k0, my_m + 64);
+                                } else {
+                                    tma_load_2d_pair_at(&tm_a_few, bar, a0, k0, my_m);
+                                    if (half > 8) tma_load_2d_pair_at(&tm_a_few, bar, a0 + 1024, k0, my_m + 8);
+                                    if (half > 16) tma_load_2d_pair_at(&tm_a_few, bar, a0 + 2048, k0, my_m + 16);
+                                }
                             }
                         }
                         __syncwarp();

@@ -63,12 +63,12 @@ struct Segment {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int c = c0 + u * 32 + lane;
-                if (c < full) reinterpret_cast<uint4 *>(to)[c] = v[u];
+                if (c < full) __stcs(reinterpret_cast<uint4 *>(to) + c, v[u]);
             }
         }
     }
 };
-constexpr int kSegment = 2;                        // 16-byte pieces of a lane
+constexpr int kSegment = 4;                        // 16-byte pieces of a lane
 constexpr int kSegmentPieces = 32 * kSegment;      // of a warp
 constexpr int kSegmentElements = 128;              // of a warp, where rows are not aligned
 

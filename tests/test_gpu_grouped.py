@@ -60,6 +60,29 @@ def test_weights(sizes, M, N, c):
 
 
 @pytest.mark.parametrize("t", [F16, BF16])
+def test_many_rows(t):
+    """More than one tile an expert and a CTA pair, ragged in every direction, empty experts among them."""
+    torch.manual_seed(7)
+    for sizes, N, K in (([400, 0, 513, 96, 1, 300], 777, 520), ([256] * 3, 512, 64), ([1000, 24], 260, 8), ([200] * 20, 2300, 136), ([999], 1024, 4160)):
+        off, R = offsets_of(sizes), sum(sizes) + 2
+        A = padded(R, K, dtype=t)
+        for bt in (True, False):
+            B, C = padded(len(sizes), *((N, K) if bt else (K, N)), dtype=t), padded(R, N, dtype=t, fill=-7.0)
+            g.gemm_grouped(A, B, C, off, 0.5, b_trans=bt)
+            assert g.check() == g.GEMM_OK
+            want, mag = grouped(A, B, off, bt, 0.5)
+            n = sum(sizes)
+            close(C[:n], want[:n], rounded(PRODUCT * mag[:n], want[:n], t))
+            assert (C[n:] == -7.0).all()
+        X, dW = padded(R, N, dtype=t), padded(len(sizes), max(K, 136), N, dtype=t, fill=-7.0)
+        A = padded(R, max(K, 136), dtype=t)
+        g.gemm_grouped_wgrad(A, X, dW, off, 0.5)
+        assert g.check() == g.GEMM_OK
+        want, mag = wgrad(A, X, off, 0.5)
+        close(dW, want, rounded(PRODUCT * mag, want, t))
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
 def test_neighbours_do_not_leak(t):
     """NaN and infinity in another expert's rows, in its weights and behind the last row reach nobody else."""
     sizes, N, K = [70, 1, 100, 0, 29], 72, 136
