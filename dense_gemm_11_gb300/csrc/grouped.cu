@@ -52,6 +52,12 @@ struct GroupedArgs {
     int c_type;
     int tiles_m, tiles_n;  // tiles_m: of every expert (wgrad)
     int product;           // 0: C = beta C
+    // A tile is `split` units, which share the blocks of its contraction; unit u
+    // leaves its sums at partials + u * part_stride, laid out as C without gaps, and
+    // grouped_join_kernel adds them in the order of the contraction.
+    int split;
+    float *partials;
+    size_t part_stride;
     uint32_t idesc;
     unsigned *err;
     unsigned long long wait_ns;
@@ -63,6 +69,7 @@ struct GroupedArgs {
 struct Tile {
     int e, m0, n0, row_end, span;
     int k0, k1;
+    int unit;  // of the tile (SPLIT)
 };
 
 // Tile i of tiles_m x tiles_n: groups of 8 tile rows, so that a wave of tiles
@@ -75,7 +82,7 @@ __device__ __forceinline__ void tile_place(int i, int tiles_m, int tiles_n, int 
 }
 
 // The list of tiles, walked forwards by a whole warp: lane l has expert e0 + l.
-template <bool WGRAD>
+template <bool WGRAD, bool SPLIT>
 struct TileList {
     int e0 = 0, base = 0;  // tiles before expert e0
     int start = 0, end = 0, tiles = 0, incl = 0;
@@ -86,6 +93,7 @@ struct TileList {
             start = min(max(__ldg(p.offsets + e0 + lane), 0), p.R);
             end = min(max(__ldg(p.offsets + e0 + lane + 1), start), p.R);
             tiles = WGRAD ? p.tiles_m * p.tiles_n : ((end - start + kTile - 1) / kTile) * p.tiles_n;
+            if (SPLIT) tiles *= p.split;
         }
         incl = tiles;
 #pragma unroll
@@ -112,11 +120,20 @@ struct TileList {
         // the last is not nearly empty.
         const int first = WGRAD ? 0 : s, rows = WGRAD ? p.m : e - s;
         const int tiles_m = (rows + kTile - 1) / kTile, each = ((rows + tiles_m - 1) / tiles_m + 15) & ~15;
-        tile_place(t - base - before, tiles_m, p.tiles_n, tile.m0, tile.n0);
+        int i = t - base - before;
+        tile.unit = 0;
+        if (SPLIT) tile.unit = i % p.split, i /= p.split;
+        tile_place(i, tiles_m, p.tiles_n, tile.m0, tile.n0);
         tile.m0 = first + tile.m0 * each;
         tile.row_end = min(first + rows, tile.m0 + each);
         tile.span = (tile.row_end - tile.m0 + 15) & ~15;
         tile.k0 = WGRAD ? s : 0, tile.k1 = WGRAD ? e : p.k;
+        if (SPLIT) {
+            const long long blocks = (tile.k1 - tile.k0 + kKB - 1) / kKB;
+            const int from = static_cast<int>(blocks * tile.unit / p.split), to = static_cast<int>(blocks * (tile.unit + 1) / p.split);
+            tile.k1 = min(tile.k1, tile.k0 + to * kKB);
+            tile.k0 = min(tile.k1, tile.k0 + from * kKB);
+        }
         tile.n0 *= kTile;
         if (!p.product) tile.k1 = tile.k0;
         // The same in every lane: told so, the compiler keeps what depends on these
@@ -158,6 +175,15 @@ __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&a
     }
 }
 
+// The same of a unit's sums, to memory as they are.
+__device__ __forceinline__ void store_sums(float *at, const float (&acc)[kCols], int ld, int rows) {
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) {
+        if (j < rows) *at = acc[j];
+        at += ld;
+    }
+}
+
 // CTA pairs (clusters of two), computed transposed: C^T = op(B)^T A^T, 256 columns
 // n of C on the MMA's row side (128 of each CTA: tensor-memory lanes) and up to
 // 256 rows on its column side, of which an MMA takes any multiple of 16.  So an
@@ -177,7 +203,7 @@ __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&a
 // own; warp 2 then zeroes what is behind the end in shared memory (a row is 128
 // bytes there, the swizzle moves bytes within it) and hands the block on, while
 // warp 0 is already at the next tile's.
-template <int MODE>
+template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_some,
                    const __grid_constant__ CUtensorMap tm_a_few, const GroupedArgs p) {
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     uint32_t armed = 0, armed_parity = 0;
     uint32_t ends = 0, ends_parity = 0;  // stages that had such a block, and the parity of the last
-    TileList<MODE == kWgrad> list;
+    TileList<MODE == kWgrad, SPLIT> list;
     Tile tile;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
@@ -441,6 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) continue;
             const int n = tile.n0 + rank * 128 + q * 32 + lane, row = tile.m0 + part * half;
             const int rows = n < p.n ? min(half, tile.row_end - row) : 0;
+            if constexpr (SPLIT) {
+                const size_t first = (MODE == kWgrad ? static_cast<size_t>(tile.e) * p.m : 0) + row;
+                if (first + max(rows, 0) <= p.part_stride / p.n) store_sums(p.partials + tile.unit * p.part_stride + first * p.n + n, acc, p.n, rows);
+                continue;
+            }
             const size_t at = (MODE == kWgrad ? static_cast<size_t>(tile.e * p.stride_c) : 0) + static_cast<size_t>(row) * static_cast<size_t>(p.ldc) + n;
             if (p.beta != 0.f) {
                 if (p.c_type == kOutF32)
@@ -483,12 +514,72 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// C = alpha times the units' sums + beta C, for the rows that an expert has (wgrad:
+// all): four columns a thread, whose sums of four units are in flight together.
+__global__ void __launch_bounds__(256) grouped_join_kernel(const GroupedArgs p, int wgrad) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int quads = (p.n + 3) / 4;
+    const long long r0 = wgrad ? 0 : min(max(__ldg(p.offsets), 0), p.R), r1 = wgrad ? static_cast<long long>(p.E) * p.m : min(max(__ldg(p.offsets + p.E), 0), p.R);
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < (r1 - r0) * quads; i += gridDim.x * 256LL) {
+        const long long row = r0 + i / quads;
+        const int n = static_cast<int>(i % quads) * 4, left = min(4, p.n - n);
+        const float *from = p.partials + row * p.n + n;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int u = 0; u < p.split; u += 4) {
+            float v[4][4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[k][j] = u + k < p.split && j < left ? __ldcg(from + (u + k) * p.part_stride + j) : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] += v[k][j];
+        }
+        const size_t at = wgrad ? static_cast<size_t>(row / p.m * p.stride_c + row % p.m * p.ldc) + n : static_cast<size_t>(row * p.ldc) + n;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j >= left) break;
+            float v = p.alpha * sum[j];
+            if (p.beta != 0.f) v = fmaf(p.beta, load_out(p.C, at + j, p.c_type), v);
+            if (debug_in_bounds(p.c_extent == 0 || at + j < p.c_extent, p.err)) store_out(p.C, at + j, p.c_type, v);
+        }
+    }
+}
+
+// Tiles that there are at most.
+long long most_tiles(const Grouped &g) {
+    const long long tiles_n = (g.N + kTile - 1) / kTile;
+    return g.wgrad ? static_cast<long long>(g.E) * ((g.M + kTile - 1) / kTile) * tiles_n : (g.R / kTile + static_cast<long long>(std::min(g.E, g.R))) * tiles_n;
+}
+
+// Units of a tile where the tiles would leave pairs without work: a model, in us.
+// A block of 64 takes a pair 0.37 (its 32 KB of weights at a 76th of the memory's
+// rate), 0.2 at least where few pairs are at work; each unit 0.5 beside its
+// blocks, and the sums' way through memory 3 and their bytes.
+int pick_split(const Grouped &g, int pairs) {
+    const double tiles = static_cast<double>(most_tiles(g)), cells = g.wgrad ? static_cast<double>(g.E) * g.M * g.N : static_cast<double>(g.R) * g.N;
+    const double blocks = std::floor(g.wgrad ? static_cast<double>(g.R) / g.E / kKB : (g.K + kKB - 1) / kKB);
+    auto time = [&](int s) {
+        const double units = tiles * s, each = std::ceil(blocks / s), waves = std::floor(units / pairs), left = units - waves * pairs, more = s > 1 ? 0.5 : 0.0;
+        return waves * (each * 0.37 + more) + (left > 0 ? each * std::max(0.2, 0.37 * left / pairs) + more : 0.0) + (s > 1 ? 3.0 + cells * (8 * s + 4) / 6e6 : 0.0);
+    };
+    int best = 1;
+    double t = time(1);
+    for (int s = 2; s <= 16 && 2 * s <= blocks && cells * s <= 16e6; ++s) {  // 64 MB of sums
+        const double with = time(s);
+        if (with < t) t = with, best = s;
+    }
+    return best;
+}
+
 // Strides that nothing has (of a single row, of a single expert) may be any.
 uint64_t map_stride(long long elements) { return static_cast<uint64_t>((elements * 2 + 15) / 16 * 16); }
 
-template <int MODE>
-cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream) {
-    auto kern = grouped_kernel<MODE>;
+template <int MODE, bool SPLIT>
+cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream, CallInfo *info) {
+    auto kern = grouped_kernel<MODE, SPLIT>;
     static int max_clusters = -1;  // one device type per process; atomic accesses
     static unsigned long long smem_set = 0;
     cudaError_t e = ensure_dynamic_smem(kern, kSmemBytes, smem_set);
@@ -532,10 +623,27 @@ cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream)
         __atomic_store_n(&max_clusters, clusters, __ATOMIC_RELEASE);
     }
     if (clusters < 1) return cudaErrorNotSupported;
-    const long long most = MODE == kWgrad ? static_cast<long long>(g.E) * a.tiles_m * a.tiles_n : (g.R / kTile + static_cast<long long>(std::min(g.E, g.R))) * a.tiles_n;
+    const long long most = most_tiles(g) * a.split;
+    if (SPLIT) {
+        Scratch sc;
+        a.part_stride = g.wgrad ? static_cast<size_t>(g.E) * g.M * g.N : static_cast<size_t>(g.R) * g.N;
+        e = acquire_scratch(stream, a.part_stride * a.split, 0, &sc);
+        if (e != cudaSuccess) return e;
+        a.partials = sc.partials;
+    }
     cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(clusters, most)));
     cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, kern, tb, ta, some, few, a);
+    if (e == cudaSuccess) e = cudaPeekAtLastError();
+    if (e != cudaSuccess || !SPLIT) return e;
+    info->launches = 2;
+    const long long quads = static_cast<long long>(a.part_stride / g.N) * ((g.N + 3) / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((quads + 255) / 256, 8LL * device_sm_count())));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = attr + 1;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, grouped_join_kernel, a, g.wgrad);
     return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
@@ -563,12 +671,12 @@ cudaError_t run_grouped(const Grouped &g, cudaStream_t stream, CallInfo *info) {
         a.c_extent -= std::min(a.c_extent - 1, debug_shrink_c());
     }
     info->launches = 1;
-    if (g.wgrad) {
-        info->plan = "grouped_wgrad_pair_256x256";
-        return launch_grouped<kWgrad>(g, a, stream);
-    }
-    info->plan = "grouped_pair_256x256";
-    return g.b_trans ? launch_grouped<kForward>(g, a, stream) : launch_grouped<kDgrad>(g, a, stream);
+    a.split = a.product ? pick_split(g, std::max(1, device_sm_count() / 2)) : 1;
+    const bool split = a.split > 1;
+    info->plan = g.wgrad ? (split ? "grouped_wgrad_pair_splitk" : "grouped_wgrad_pair") : split ? "grouped_pair_splitk" : "grouped_pair";
+    if (g.wgrad) return split ? launch_grouped<kWgrad, true>(g, a, stream, info) : launch_grouped<kWgrad, false>(g, a, stream, info);
+    if (g.b_trans) return split ? launch_grouped<kForward, true>(g, a, stream, info) : launch_grouped<kForward, false>(g, a, stream, info);
+    return split ? launch_grouped<kDgrad, true>(g, a, stream, info) : launch_grouped<kDgrad, false>(g, a, stream, info);
 }
 
 }  // namespace gemm11

@@ -194,3 +194,56 @@ def test_sums_to_nearest():
     want, mag = grouped(A, B, offsets_of([256]), True)
     err = ((C.double() - want) / mag).abs()
     assert float(err.max()) <= 3e-6 and float(((C.double() - want) / mag).mean().abs()) <= 3e-6
+
+
+SPLIT = [([3, 0, 16, 1], 200, 4100), ([64, 60], 256, 8192), ([1, 1], 1000, 4096), ([130, 0, 5], 24, 2056), ([256], 300, 11008)]
+
+
+@pytest.mark.parametrize("t,c", [(BF16, BF16), (F16, F32)])
+@pytest.mark.parametrize("sizes,N,K", SPLIT)
+def test_units_share_a_contraction(sizes, N, K, t, c):
+    """Few tiles, a long contraction: its parts' sums are added in one order, whichever CTA comes last."""
+    torch.manual_seed(K)
+    off, R = offsets_of(sizes), sum(sizes) + 1
+    A, C0 = padded(R, K, dtype=t), padded(R, N, dtype=c)
+    for bt in (True, False):
+        B = padded(len(sizes), *((N, K) if bt else (K, N)), dtype=t)
+        results = []
+        for beta in (0.0, 0.0, 0.5):
+            C = padded(R, N, dtype=c)
+            C.copy_(C0)
+            g.gemm_grouped(A, B, C, off, 1.0, beta, b_trans=bt)
+            assert "splitk" in g.last_plan() and g.check() == g.GEMM_OK
+            want, mag = grouped(A, B, off, bt, 1.0, beta, C0)
+            close(C[:R - 1], want[:R - 1], rounded(PRODUCT * mag[:R - 1], want[:R - 1], c))
+            assert torch.equal(C[R - 1], C0[R - 1])
+            results.append(C)
+        assert torch.equal(results[0], results[1])
+
+
+@pytest.mark.parametrize("sizes,M,N", [([2000, 0, 777], 100, 130), ([8000], 256, 512), ([3, 900, 64, 1300], 16, 40), ([20000, 0, 9001], 100, 130), ([7, 33000], 264, 256)])
+def test_units_share_rows(sizes, M, N):
+    off, R = offsets_of(sizes), sum(sizes) + 9
+    A, B = padded(R, M, dtype=BF16), padded(R, N, dtype=BF16)
+    A[R - 9:] = float("nan")
+    for beta in (0.0, 2.0):
+        C0 = padded(len(sizes), M, N, dtype=F32)
+        C, D = C0.clone(), C0.clone()
+        g.gemm_grouped_wgrad(A, B, C, off, 0.25, beta)
+        assert ("splitk" in g.last_plan() or R < 20000) and g.check() == g.GEMM_OK
+        g.gemm_grouped_wgrad(A, B, D, off, 0.25, beta)
+        assert torch.equal(C, D)
+        want, mag = wgrad(A, B, off, 0.25, beta, C0)
+        close(C, want, rounded(PRODUCT * mag, want, F32))
+
+
+def test_descending_offsets_stay_inside():
+    """What they give is not defined, but nothing is written outside C, and the next call is right."""
+    full = torch.full((130, 64), -7.0, device="cuda")
+    C, A, B = full[1:129], padded(128, 4096, dtype=BF16), padded(6, 64, 4096, dtype=BF16)
+    g.gemm_grouped(A, B, C, torch.tensor([0, 128, 0, 128, 0, 128, 0], dtype=torch.int32, device="cuda"))
+    assert g.check() == g.GEMM_OK and (full[0] == -7.0).all() and (full[129] == -7.0).all()
+    off = offsets_of([20, 0, 30, 40, 8, 30])
+    g.gemm_grouped(A, B, C, off)
+    want, mag = grouped(A, B, off, True)
+    close(C, want, rounded(PRODUCT * mag, want, F32))
