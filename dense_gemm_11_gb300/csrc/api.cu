@@ -877,8 +877,7 @@ int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids, const void
     const bool copy = H > 0 && (X || Xs);
     if (copy && (ldx < H || ldxs < H)) return GEMM_ERR_INVALID_ARG;
     if (!offsets || (T > 0 && (!ids || !rows || (copy && (!X || !Xs))))) return GEMM_ERR_INVALID_ARG;
-    if (T > kMaxExtent || H > kMaxExtent / 4 || E > kDispatchMaxExperts || top_k > kRowsMaxTopK ||
-        static_cast<long long>(T) * top_k > kMaxExtent)
+    if (H > kMaxExtent / 4 || E > kDispatchMaxExperts || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent)
         return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
@@ -909,7 +908,7 @@ int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, l
     if (ldys < std::max(1, H) || ldy < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
     if (T == 0 || H == 0) return noop();
     if (!rows || !Y || (R > 0 && !Ys)) return GEMM_ERR_INVALID_ARG;
-    if (T > kMaxExtent || H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK) return GEMM_ERR_UNSUPPORTED;
+    if (H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
     if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
@@ -939,7 +938,7 @@ int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void *dY, int ty
     if (lddy < std::max(1, H) || ldys < std::max(1, H) || lddys < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
     if (T == 0) return noop();
     if (!rows || !weights || !dweights || (H > 0 && (!dY || (R > 0 && (!Ys || !dYs))))) return GEMM_ERR_INVALID_ARG;
-    if (T > kMaxExtent || H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK) return GEMM_ERR_UNSUPPORTED;
+    if (H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
     if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);

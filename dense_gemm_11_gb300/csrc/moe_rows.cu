@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     const int copies = p.copies, E = p.E;  // neighbouring lanes count in counters of their own: fewer of a warp's additions meet
     int *const before = counts, *const rest = counts + E * copies;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * p.per_cta, t1 = min(p.T, t0 + p.per_cta);
+    const int t0 = blockIdx.x * p.per_cta, t1 = t0 + min(p.T - t0, p.per_cta);
     for (int e = threadIdx.x; e < 2 * E * copies; e += kSortThreads) counts[e] = 0;
     __syncthreads();
     pdl_wait();

@@ -387,7 +387,7 @@ GEMM11_API int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const 
  * tokens.  Backward: gemm_moe_combine_grad, gemm_grouped_f32acc with the same
  * weights and b_trans turned, gemm_grouped_wgrad_f32acc for every weight,
  * gemm_fp8_gated_act_grad, and gemm_moe_combine without weights, which is the
- * gradient of the copy.
+ * gradient of the copy.  No result of these calls may overlap an input.
  *
  * gemm_moe_dispatch -- for each slot (t, j), expert e = ids[t * top_k + j]:
  *   offsets[e] = number of slots whose expert is below e (offsets[E]: of all
@@ -414,7 +414,8 @@ GEMM11_API int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids,
  *            0 .. R - 1 adds nothing, a token without any gets zeros.
  *   weights  T x top_k float, or NULL: ones.  With ones it is also the gradient
  *            of gemm_moe_dispatch's copy.
- * Any alignment.  T == 0 or H == 0 is a no-op.
+ * Any alignment.  T == 0 or H == 0 is a no-op.  GEMM_ERR_UNSUPPORTED for top_k >
+ * 128 or T * top_k above 2^31 - 512.
  */
 GEMM11_API int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, long long ldys,
                                 const int *rows, const float *weights, void *Y, long long ldy, void *stream);
@@ -423,8 +424,9 @@ GEMM11_API int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, 
  * gemm_moe_combine_grad -- the gradient of gemm_moe_combine with weights:
  *   dYs[rows[t, j]] = round( w[t, j] dY[t] ),  dweights[t, j] = sum_h dY[t, h]
  *   Ys[rows[t, j], h] in FP32, 0 for a slot without a row.
- * dY T x H, Ys and dYs R x H, all of one type; rows of dYs that no slot names
- * stay as they are.  Any alignment.  T == 0 is a no-op.
+ * dY T x H, Ys and dYs R x H, all of one type; no two slots may name one row;
+ * rows of dYs that no slot names stay as they are.  Any alignment.  T == 0 is a
+ * no-op.  Limits as for gemm_moe_combine.
  */
 GEMM11_API int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void *dY, int type, long long lddy,
                                      const void *Ys, long long ldys, const int *rows, const float *weights, void *dYs,
@@ -446,7 +448,10 @@ GEMM11_API int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void 
  * added in FP32 to nearest.  alpha, beta and the degenerate shapes are those of
  * gemm_tc_f32acc_epilogue.  A and B 16-byte aligned, lda, ldb and stride_b
  * multiples of 8 (those of a single row, or expert, excepted), otherwise
- * GEMM_ERR_UNSUPPORTED; C any alignment and any ldc >= N.
+ * GEMM_ERR_UNSUPPORTED; C any alignment and any ldc >= N.  GEMM_ERR_UNSUPPORTED
+ * too for extents above 2^31 - 512 and for E (R / 256 + 1) (N / 256 + 1) from 2^31.
+ * Scratch: where few tiles leave SMs without work, tiles share their contraction
+ * and up to 64 MB hold their parts' sums (plan "grouped_pair_splitk").
  */
 GEMM11_API int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, const void *A, long long lda, const void *B,
                                    long long ldb, long long stride_b, int ab_type, int b_trans, float beta, void *C,
@@ -457,7 +462,8 @@ GEMM11_API int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, cons
  *   C[e] = round_c( alpha sum_r A[r]^T B[r] + beta C[e] ) over offsets[e] <= r < offsets[e + 1],
  * A R x M and B R x N of ab_type, C E matrices M x N stride_c elements apart
  * (FP32, FP16 or BF16).  An expert without rows gets beta C[e].  offsets, the
- * accumulation and the alignment are those of gemm_grouped_f32acc.
+ * accumulation, the alignment, the limits (M for R) and the scratch are those of
+ * gemm_grouped_f32acc.
  */
 GEMM11_API int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha, const void *A, long long lda,
                                          const void *B, long long ldb, int ab_type, float beta, void *C, int c_type,

@@ -63,8 +63,8 @@ def test_invalid(L, name, change):
 
 UNSUPPORTED = [
     ("gemm_moe_dispatch", [dict(E=4097), dict(top_k=129), dict(T=BIG), dict(T=2 ** 28, top_k=8), dict(H=2 ** 30, ldx=2 ** 30, ldxs=2 ** 30)]),
-    ("gemm_moe_combine", [dict(top_k=129), dict(T=BIG), dict(R=BIG), dict(H=BIG, ldys=BIG, ldy=BIG)]),
-    ("gemm_moe_combine_grad", [dict(top_k=129), dict(T=BIG), dict(R=BIG), dict(H=BIG, lddy=BIG, ldys=BIG, lddys=BIG)]),
+    ("gemm_moe_combine", [dict(top_k=129), dict(T=BIG), dict(T=2 ** 28, top_k=8), dict(R=BIG), dict(H=BIG, ldys=BIG, ldy=BIG)]),
+    ("gemm_moe_combine_grad", [dict(top_k=129), dict(T=BIG), dict(T=2 ** 28, top_k=8), dict(R=BIG), dict(H=BIG, lddy=BIG, ldys=BIG, lddys=BIG)]),
     ("gemm_grouped_f32acc", [dict(A=FAKE + 8), dict(B=FAKE + 2), dict(lda=68), dict(ldb=68, stride_b=8000), dict(stride_b=4100), dict(R=BIG), dict(E=BIG),
                              dict(N=BIG, ldc=BIG, stride_b=2 ** 50), dict(K=BIG, lda=2 ** 31, ldb=2 ** 31, stride_b=2 ** 50), dict(lda=2 ** 38),
                              dict(E=2 ** 20, R=2 ** 20, N=2 ** 12, ldc=2 ** 12, stride_b=2 ** 18)]),
