@@ -30,6 +30,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 from .build import DEBUG_LIB_PATH, LIB_PATH, build  # noqa: F401  (build() is part of the public API)
@@ -70,7 +71,7 @@ EXPORTED_SYMBOLS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_f16_f32acc_epilogue", "
                     "gemm_tc_f32acc_epilogue", "gemm_tc_strided_batched", "gemm_f16_f32acc_epilogue_noalloc",
                     "gemm_fp8_quantize_block128", "gemm_fp8_block128", "gemm_moe_few_tokens",
                     "gemm_moe_dispatch", "gemm_moe_combine", "gemm_moe_combine_grad", "gemm_grouped_f32acc",
-                    "gemm_grouped_wgrad_f32acc", "gemm_fp8_gated_act", "gemm_fp8_gated_act_grad",
+                    "gemm_grouped_wgrad_f32acc", "gemm_fp8_gated_act", "gemm_fp8_gated_act_grad", "gemm_call_words",
                     "gemm_tune_set", "gemm_tune_get",
                     "gemm_status_string", "gemm_last_cuda_error", "gemm_check", "gemm_watchdog_selftest",
                     "gemm_last_plan", "gemm_last_launch_count", "gemm_tc_rate_probe",
@@ -161,6 +162,8 @@ def lib():
             L.gemm_fp8_gated_act_grad.argtypes = [c_int, c_int, c_void_p, c_ll, c_int, c_void_p, c_ll, c_void_p, c_ll, c_void_p,
                                                   c_ll, c_void_p, c_ll, c_int, c_void_p, c_ll, c_void_p, c_ll, c_void_p, c_ll,
                                                   c_int, c_void_p]
+            L.gemm_call_words.restype = c_int
+            L.gemm_call_words.argtypes = [c_int, ctypes.c_char_p, c_int]
             L.gemm_tune_set.restype = c_int
             L.gemm_tune_set.argtypes = [ctypes.POINTER(TuneEntry), c_int]
             L.gemm_tune_get.restype = c_int
@@ -636,17 +639,30 @@ def _vector(t, name, n):
     return t.data_ptr()
 
 
+# The calls below are short on the GPU, and most of a call is what the host does:
+# each tensor is looked at once, and the arguments go over as an array of words.
+_pack13, _pack12, _pack15, _pack20, _pack22 = (struct.Struct(f"={n}q").pack for n in (13, 12, 15, 20, 22))
+_pack_grouped, _pack_wgrad = struct.Struct("=4qd7qd5q").pack, struct.Struct("=4qd5qd6q").pack
+
+
 def _placed(t, name, allowed):
     """(pointer, row stride, rows, cols, type code, device) of a 2-D CUDA tensor, as _typed_mat takes it."""
+    try:
+        code, device = _codes[t.dtype], t.get_device()
+        rows, cols = t.shape
+        ld, step = t.stride()
+        if code in allowed and step == 1 and ld >= cols > 0 <= device:
+            return t.data_ptr(), ld, rows, cols, code, device
+    except Exception:  # noqa: S110 (no tensor, another type or shape: named below)
+        pass
     if not _codes:
         _load_codes()
     code = _codes.get(getattr(t, "dtype", None), -1)
     if code not in allowed or (device := t.get_device()) < 0:
         raise TypeError(f"{name} must be a CUDA tensor of type {'/'.join(_TYPE_NAMES[c] for c in allowed)}")
-    shape = t.shape
-    if len(shape) != 2:
+    if len(t.shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    rows, cols = shape
+    rows, cols = t.shape
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} needs unit column stride")
@@ -726,7 +742,7 @@ def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
     off_ptr, E, off_on = _offsets(offsets)
     rows_ptr, rows_on = _packed(rows, "rows", "int32", (T, k))
     x_on = xs_on = here
-    x_ptr = xs_ptr = None
+    x_ptr = xs_ptr = 0
     H, x_type, ldx, ldxs = 0, GEMM_DTYPE_F32, 1, 1
     if X is not None or Xs is not None:
         x_ptr, ldx, x_rows, H, x_type, x_on = _placed(X, "X", _FLOATS)
@@ -737,8 +753,9 @@ def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
             raise ValueError(f"shape mismatch ids{(T, k)} X{tuple(X.shape)} Xs{tuple(Xs.shape)} (at least T * top_k rows)")
     if not here == off_on == rows_on == x_on == xs_on == _device_now():
         _elsewhere(here, off_on, rows_on, x_on, xs_on)
-    st = lib().gemm_moe_dispatch(T, E, k, H, ids_ptr, x_ptr, x_type, ldx, xs_ptr, ldxs, off_ptr, rows_ptr,
-                                 _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack13(T, E, k, H, ids_ptr, x_ptr, x_type, ldx, xs_ptr, ldxs, off_ptr, rows_ptr, on)
+    st = (_lib or lib()).gemm_call_words(0, words, 13)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_dispatch")
 
@@ -756,11 +773,12 @@ def moe_combine(Ys, rows, Y, weights=None, *, stream=None) -> None:
         raise TypeError("Ys and Y must have one type")
     if r_T != T or y_cols != H:
         raise ValueError(f"shape mismatch Ys{tuple(Ys.shape)} rows{tuple(rows.shape)} Y{tuple(Y.shape)}")
-    w_ptr, w_on = (None, here) if weights is None else _packed(weights, "weights", "float32", (T, k))
+    w_ptr, w_on = (0, here) if weights is None else _packed(weights, "weights", "float32", (T, k))
     if not here == ys_on == rows_on == w_on == _device_now():
         _elsewhere(here, ys_on, rows_on, w_on)
-    st = lib().gemm_moe_combine(T, k, H, R, ys_ptr, y_type, ldys, rows_ptr, w_ptr, y_ptr, ldy,
-                                _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack12(T, k, H, R, ys_ptr, y_type, ldys, rows_ptr, w_ptr, y_ptr, ldy, on)
+    st = (_lib or lib()).gemm_call_words(1, words, 12)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_combine")
 
@@ -783,8 +801,9 @@ def moe_combine_grad(dY, Ys, rows, weights, dYs, dweights, *, stream=None) -> No
     dw_ptr, dw_on = _packed(dweights, "dweights", "float32", (T, k))
     if not here == ys_on == dys_on == rows_on == w_on == dw_on == _device_now():
         _elsewhere(here, ys_on, dys_on, rows_on, w_on, dw_on)
-    st = lib().gemm_moe_combine_grad(T, k, H, R, dy_ptr, code, lddy, ys_ptr, ldys, rows_ptr, w_ptr, dys_ptr, lddys, dw_ptr,
-                                     _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack15(T, k, H, R, dy_ptr, code, lddy, ys_ptr, ldys, rows_ptr, w_ptr, dys_ptr, lddys, dw_ptr, on)
+    st = (_lib or lib()).gemm_call_words(2, words, 15)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_moe_combine_grad")
 
@@ -807,8 +826,10 @@ def gemm_grouped(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, *, b_t
         raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
     if not here == b_on == c_on == off_on == _device_now():
         _elsewhere(here, b_on, c_on, off_on)
-    st = lib().gemm_grouped_f32acc(E, R, N, K, alpha, a_ptr, lda, b_ptr, ldb, stride_b, a_type, 1 if b_trans else 0, beta, c_ptr,
-                                   c_type, ldc, off_ptr, _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack_grouped(E, R, N, K, alpha, a_ptr, lda, b_ptr, ldb, stride_b, a_type, 1 if b_trans else 0, beta, c_ptr, c_type,
+                          ldc, off_ptr, on)
+    st = (_lib or lib()).gemm_call_words(3, words, 18)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_grouped_f32acc")
 
@@ -829,8 +850,9 @@ def gemm_grouped_wgrad(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, 
         raise ValueError(f"shape mismatch A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)} offsets{tuple(offsets.shape)}")
     if not here == b_on == c_on == off_on == _device_now():
         _elsewhere(here, b_on, c_on, off_on)
-    st = lib().gemm_grouped_wgrad_f32acc(E, R, M, N, alpha, a_ptr, lda, b_ptr, ldb, a_type, beta, c_ptr, c_type, ldc, stride_c,
-                                         off_ptr, _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack_wgrad(E, R, M, N, alpha, a_ptr, lda, b_ptr, ldb, a_type, beta, c_ptr, c_type, ldc, stride_c, off_ptr, on)
+    st = (_lib or lib()).gemm_call_words(4, words, 17)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_grouped_wgrad_f32acc")
 
@@ -861,7 +883,7 @@ def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *
     g_ptr, ldg, rows, cols, code, here = _placed(G, "G", _FLOATS)
     h_ptr, ldh, h_on = _same(H, "H", rows, cols, code)
     gq_ptr, ldgq, q_type, gq_on, gs_ptr, ldgs, gs_on = _kept(GQ, GS, "GQ", "GS", rows, cols)
-    u_ptr = uq_ptr = us_ptr = None
+    u_ptr = uq_ptr = us_ptr = 0
     ldu = lduq = ldus = 1
     u_on = uq_on = us_on = here
     if U is not None:
@@ -873,8 +895,10 @@ def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *
         raise ValueError("UQ and US are for a gate: without U they must be None")
     if not here == h_on == gq_on == gs_on == u_on == uq_on == us_on == _device_now():
         _elsewhere(here, h_on, gq_on, gs_on, u_on, uq_on, us_on)
-    st = lib().gemm_fp8_gated_act(rows, cols, g_ptr, ldg, u_ptr, ldu, code, h_ptr, ldh, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq,
-                                  us_ptr, ldus, q_type, act, _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack20(rows, cols, g_ptr, ldg, u_ptr, ldu, code, h_ptr, ldh, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq, us_ptr, ldus,
+                    q_type, act, on)
+    st = (_lib or lib()).gemm_call_words(5, words, 20)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_gated_act")
 
@@ -889,7 +913,7 @@ def fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU, H=None, act: int = GEMM_ACT_S
     dh_ptr, lddh, rows, cols, code, here = _placed(dH, "dH", _FLOATS)
     gq_ptr, ldgq, q_type, gq_on, gs_ptr, ldgs, gs_on = _kept(GQ, GS, "GQ", "GS", rows, cols)
     dg_ptr, lddg, dg_on = _same(dG, "dG", rows, cols, code)
-    uq_ptr = us_ptr = du_ptr = h_ptr = None
+    uq_ptr = us_ptr = du_ptr = h_ptr = 0
     lduq = ldus = lddu = ldh = 1
     uq_on = us_on = du_on = h_on = here
     if UQ is not None:
@@ -903,8 +927,10 @@ def fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU, H=None, act: int = GEMM_ACT_S
         h_ptr, ldh, h_on = _same(H, "H", rows, cols, code)
     if not here == gq_on == gs_on == dg_on == uq_on == us_on == du_on == h_on == _device_now():
         _elsewhere(here, gq_on, gs_on, dg_on, uq_on, us_on, du_on, h_on)
-    st = lib().gemm_fp8_gated_act_grad(rows, cols, dh_ptr, lddh, code, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq, us_ptr, ldus,
-                                       q_type, dg_ptr, lddg, du_ptr, lddu, h_ptr, ldh, act, _raw_stream(here) if stream is None else stream.cuda_stream)
+    on = _raw_stream(here) if stream is None else stream.cuda_stream
+    words = _pack22(rows, cols, dh_ptr, lddh, code, gq_ptr, ldgq, gs_ptr, ldgs, uq_ptr, lduq, us_ptr, ldus, q_type, dg_ptr, lddg,
+                    du_ptr, lddu, h_ptr, ldh, act, on)
+    st = (_lib or lib()).gemm_call_words(6, words, 22)
     if st != GEMM_OK:
         raise GemmError(st, "gemm_fp8_gated_act_grad")
 

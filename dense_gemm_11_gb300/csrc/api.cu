@@ -3,12 +3,16 @@
 // split-K scratch and the device watchdog word.
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <map>
 #include <memory>
 #include <mutex>
+#include <tuple>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -577,6 +581,41 @@ bool gated_fits(int rows, int cols) {
     return rows <= kMaxExtent && cols <= kMaxExtent && ((rows + 15LL) / 16) * ((cols + 127LL) / 128) <= kMaxExtent;
 }
 
+// Arguments of a call as words (see gemm_call_words).
+class Words {
+  public:
+    Words(const void *words, int count) : at_(static_cast<const unsigned char *>(words)), count_(count) {}
+    template <typename... Args>
+    int call(int (*f)(Args...)) {
+        if (!at_ || count_ != static_cast<int>(sizeof...(Args))) return GEMM_ERR_INVALID_ARG;
+        return spread(f, std::index_sequence_for<Args...>());
+    }
+
+  private:
+    template <typename... Args, size_t... I>
+    int spread(int (*f)(Args...), std::index_sequence<I...>) {
+        bool ok = true;
+        const std::tuple<Args...> args{get<Args>(I, &ok)...};
+        return ok ? f(std::get<I>(args)...) : GEMM_ERR_INVALID_ARG;
+    }
+    template <typename T>
+    T get(size_t i, bool *ok) const {
+        if constexpr (std::is_same_v<T, float>) {
+            double v;
+            std::memcpy(&v, at_ + 8 * i, 8);
+            return static_cast<float>(v);
+        } else {
+            long long v;
+            std::memcpy(&v, at_ + 8 * i, 8);
+            if constexpr (std::is_pointer_v<T>) return reinterpret_cast<T>(static_cast<uintptr_t>(v));
+            if constexpr (std::is_same_v<T, int>) *ok = *ok && v >= INT_MIN && v <= INT_MAX;
+            return (T)v;
+        }
+    }
+    const unsigned char *at_;
+    int count_;
+};
+
 // A call with an empty result.
 int noop() {
     t_last_plan = "noop_empty";
@@ -1132,6 +1171,21 @@ int gemm_fp8_gated_act_grad(int rows, int cols, const void *dH, long long lddh, 
     const cudaError_t e = run_gated_act_grad(a, s, &info);
     if (e != cudaSuccess) return fail_cuda(e);
     return finish_call(info, s);
+}
+
+int gemm_call_words(int function, const void *words, int count) {
+    static_assert(sizeof(void *) == sizeof(long long), "a pointer is a word");
+    Words w(words, count);
+    switch (function) {
+        case GEMM_CALL_MOE_DISPATCH: return w.call(gemm_moe_dispatch);
+        case GEMM_CALL_MOE_COMBINE: return w.call(gemm_moe_combine);
+        case GEMM_CALL_MOE_COMBINE_GRAD: return w.call(gemm_moe_combine_grad);
+        case GEMM_CALL_GROUPED: return w.call(gemm_grouped_f32acc);
+        case GEMM_CALL_GROUPED_WGRAD: return w.call(gemm_grouped_wgrad_f32acc);
+        case GEMM_CALL_GATED_ACT: return w.call(gemm_fp8_gated_act);
+        case GEMM_CALL_GATED_ACT_GRAD: return w.call(gemm_fp8_gated_act_grad);
+        default: return GEMM_ERR_INVALID_ARG;
+    }
 }
 
 const char *gemm_status_string(int status) {

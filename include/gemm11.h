@@ -499,6 +499,27 @@ GEMM11_API int gemm_fp8_gated_act_grad(int rows, int cols, const void *dH, long 
                                        void *stream);
 
 /*
+ * gemm_call_words -- the calls of this section with their arguments in an array,
+ * one 64-bit word each, in the order of the declarations (pointers and integers
+ * as they are, alpha and beta as doubles, `stream` last): for bindings that pay
+ * for every argument of a call (20 of them cost 1.8 us through Python's ctypes on
+ * the Arm host of a GB300, an array 0.5 us).
+ *   function  a gemm_word_call;  count  the number of its arguments.
+ * Returns what the call returns, GEMM_ERR_INVALID_ARG for an unknown function, a
+ * wrong count or a word that does not fit its argument.
+ */
+typedef enum {
+    GEMM_CALL_MOE_DISPATCH = 0,     /* 13 words */
+    GEMM_CALL_MOE_COMBINE = 1,      /* 12 */
+    GEMM_CALL_MOE_COMBINE_GRAD = 2, /* 15 */
+    GEMM_CALL_GROUPED = 3,          /* 18 */
+    GEMM_CALL_GROUPED_WGRAD = 4,    /* 17 */
+    GEMM_CALL_GATED_ACT = 5,        /* 20 */
+    GEMM_CALL_GATED_ACT_GRAD = 6    /* 22 */
+} gemm_word_call;
+GEMM11_API int gemm_call_words(int function, const void *words, int count);
+
+/*
  * Tuned plans.  The planners pick a kernel family, tile width and split-K
  * factor from the shape by fixed rules; a tuning table replaces those rules
  * for exact shapes.  The pages tune the same parameters per shape and per GPU

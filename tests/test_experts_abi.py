@@ -1,5 +1,6 @@
 """Refusals of the mixture-of-experts operators for many tokens (no GPU: every case ends on the host)."""
 import os
+import struct
 
 import pytest
 import torch
@@ -79,6 +80,33 @@ UNSUPPORTED = [
 @pytest.mark.parametrize("name,change", [(n, c) for n, cs in UNSUPPORTED for c in cs])
 def test_unsupported(L, name, change):
     assert call(L, name, **change) == g.GEMM_ERR_UNSUPPORTED
+
+
+WORD_CALLS = list(CALLS)  # in the order of gemm_word_call
+
+
+def words(name, **change):
+    args = {**CALLS[name], **change}
+    fmt = "".join("d" if n in ("alpha", "beta") else "q" for n in args)
+    return struct.pack("=" + fmt, *(0 if v is None else v for v in args.values())), len(args)
+
+
+@pytest.mark.parametrize("name,change", [(n, c) for n, cs in INVALID + UNSUPPORTED for c in cs])
+def test_the_same_as_words(L, name, change):
+    packed, n = words(name, **change)
+    assert L.gemm_call_words(WORD_CALLS.index(name), packed, n) == call(L, name, **change) != g.GEMM_OK
+
+
+def test_words_that_do_not_fit(L):
+    for i, name in enumerate(WORD_CALLS):
+        packed, n = words(name)
+        for bad in (n - 1, n + 1, 0, -1):
+            assert L.gemm_call_words(i, packed, bad) == g.GEMM_ERR_INVALID_ARG
+        assert L.gemm_call_words(i, None, n) == g.GEMM_ERR_INVALID_ARG
+        for first in (2 ** 31, -2 ** 31 - 1, 2 ** 40):  # an int that is none: not cut to one that would pass
+            assert L.gemm_call_words(i, struct.pack("=q", first) + packed[8:], n) == g.GEMM_ERR_INVALID_ARG
+    for i in (-1, len(WORD_CALLS)):
+        assert L.gemm_call_words(i, words("gemm_moe_dispatch")[0], 13) == g.GEMM_ERR_INVALID_ARG
 
 
 @pytest.mark.parametrize("name,change", [
