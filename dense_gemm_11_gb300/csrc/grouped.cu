@@ -46,6 +46,8 @@ constexpr int kChunk = 8;
 constexpr int kRegsFew = 56, kRegsMany = 224;
 constexpr int kThreads = 128 + 32 * kEpi;
 constexpr int kBars = 3 * kStages + 4 + 1;
+constexpr int kOutRows = 64, kOut = kOutRows * 32 * 2;  // results that a warp turns in shared memory at a time
+static_assert(4 * kOut <= kHalf, "four warps turn theirs in one operand's part of a stage");
 constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Rows of A that one copy brings in: 32, once or twice, for a CTA's half of a tile
@@ -64,6 +66,8 @@ struct GroupedArgs {
     void *C;
     long long ldc, stride_c;
     int c_type;
+    int turn;    // C by store_turned, which has the memory of the last stage
+    int stages;  // in the ring: without that one
     int tiles_m, tiles_n;  // tiles_m: of every expert (wgrad)
     int product;           // 0: C = beta C
     // A tile is `split` units, which share the blocks of its contraction; unit u
@@ -179,22 +183,87 @@ __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&a
     const long long ld = p.ldc;
     const float alpha = p.alpha, beta = p.beta;
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        if (j < rows) {
-            float v = alpha * acc[j];
-            if (BETA) v = fmaf(beta, load_out(c, 0, CT), v);
-            if (debug_in_bounds(p.c_extent == 0 || at + static_cast<size_t>(j) * static_cast<size_t>(ld) < p.c_extent, p.err)) store_out(c, 0, CT, v);
+    for (int j0 = 0; j0 < kCols; j0 += 16) {
+        if (j0 >= rows) break;
+#pragma unroll
+        for (int j = j0; j < j0 + 16; ++j) {
+            if (j < rows) {
+                float v = alpha * acc[j];
+                if (BETA) v = fmaf(beta, load_out(c, 0, CT), v);
+                if (debug_in_bounds(p.c_extent == 0 || at + static_cast<size_t>(j) * static_cast<size_t>(ld) < p.c_extent, p.err)) store_out(c, 0, CT, v);
+            }
+            c += ld;
         }
-        c += ld;
+    }
+}
+
+// The same for 16 bits through shared memory, 16 bytes a lane.  A lane puts 8 rows of
+// its column there as 16 bytes, and takes eight columns of a row: 8 x 8 matrices, of
+// which it gets two neighbouring elements of the transpose, four of them for columns
+// 2 i, 2 i + 1 of each eight.  Column c of eight rows is at 16 bytes c, the eight that
+// it is in turned by 2 (c / 8), so that none of the accesses meets a bank twice.
+//
+// For contractions of one chunk, where a tile's time is its stores': BF16 results of
+// 4096 x 6 rows over 64 experts of 2048 x 128 49.0 -> 45.3 us, of 64 x 6 rows 21.6 ->
+// 14.2, the weights' gradient of 128 x 2 rows over 16 experts of 2048 x 4096 101 -> 88.
+// At 512 either takes 55 us, and behind that the ring's last stage, whose memory
+// this has, is worth more (weights' gradient of 1024 rows an expert 187 us, turned 190).
+// A copy of 256 bytes for each row out of shared memory instead took twice as long as
+// single stores (434 us against 219 for 79 x 8 rows, 23 experts of 5120 x 2560, in this
+// form 192), full lines by four warps together 282.
+// at: of the warp's first column; cols: that it has.
+template <int CT>
+__device__ __forceinline__ void store_turned(const GroupedArgs &p, const float (&acc)[kCols], size_t at, int rows, int cols, uint32_t smem, int lane) {
+    const float alpha = p.alpha;
+    const uint32_t put = smem + ((lane ^ (lane >> 3 << 1)) << 4);
+    const int m = lane & 7, c = (m >> 1) * 8 + (lane >> 3) * 2 + (m & 1);  // of this lane's row of a matrix
+    const uint32_t take = smem + ((c ^ (c >> 3 << 1)) << 4);
+    const int col = (lane & 3) * 8, left = cols - col;
+    uint16_t *to = static_cast<uint16_t *>(p.C) + at + static_cast<size_t>(lane >> 2) * static_cast<size_t>(p.ldc) + col;
+    const long long step = 8 * p.ldc;
+#pragma unroll
+    for (int j0 = 0; j0 < kCols; j0 += kOutRows) {
+        if (j0 < rows) {
+#pragma unroll
+            for (int j = j0; j < j0 + kOutRows; j += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = pack2_out16(alpha * acc[j + 2 * k], alpha * acc[j + 2 * k + 1], CT);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(put + (j - j0) * 64), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = j0; j < j0 + kOutRows; j += 8) {
+                uint4 w;
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(take + (j - j0) * 64) : "memory");
+                const int r = j + (lane >> 2);
+                if (r < rows && left > 0 && debug_in_bounds(p.c_extent == 0 || at + static_cast<size_t>(r) * static_cast<size_t>(p.ldc) + min(cols, col + 8) <= p.c_extent, p.err)) {
+                    if (left >= 8) {
+                        *reinterpret_cast<uint4 *>(to) = w;
+                    } else {
+                        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int k = 0; k < 7; ++k)
+                            if (k < left) to[k] = static_cast<uint16_t>(e[k >> 1] >> (k & 1) * 16);
+                    }
+                }
+                to += step;
+            }
+            __syncwarp();
+        }
     }
 }
 
 // The same of a unit's sums, to memory as they are.
 __device__ __forceinline__ void store_sums(float *at, const float (&acc)[kCols], int ld, int rows) {
 #pragma unroll
-    for (int j = 0; j < kCols; ++j) {
-        if (j < rows) *at = acc[j];
-        at += ld;
+    for (int j0 = 0; j0 < kCols; j0 += 16) {
+        if (j0 >= rows) break;
+#pragma unroll
+        for (int j = j0; j < j0 + 16; ++j) {
+            if (j < rows) *at = acc[j];
+            at += ld;
+        }
     }
 }
 
@@ -347,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                     }
-                    if (++stage == kStages) stage = 0, phase ^= 1u;
+                    if (++stage == p.stages) stage = 0, phase ^= 1u;
                 }
             }
         } else if (MODE == kWgrad && warp == 2) {
@@ -358,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
                 const int blocks = tile_blocks(tile), valid = tile.k1 - tile.k0 - (blocks - 1) * kKB;
                 if (blocks == 0) continue;
-                stage = (stage + blocks - 1) % kStages;
+                stage = (stage + blocks - 1) % p.stages;
                 if (valid < kKB) {
                     ok = __all_sync(0xffffffffu, mbar_wait_patient(&landed[stage], ends_parity >> stage & 1u, p.wait_ns));
                     if (!ok) {
@@ -380,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) mbar_arrive_cluster(mapa_shared(smem_u32(&full[stage]), 0));
                     __syncwarp();
                 }
-                stage = stage + 1 == kStages ? 0 : stage + 1;
+                stage = stage + 1 == p.stages ? 0 : stage + 1;
             }
         } else if (warp == 1 && leader) {
             // ------------------------------------------------ MMA issuer (even CTA)
@@ -429,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (kb == some - 1) umma_commit_pair_mc(&tfull[buf], 0x3);
                         }
                         __syncwarp();
-                        if (++stage == kStages) stage = 0, phase ^= 1u;
+                        if (++stage == p.stages) stage = 0, phase ^= 1u;
                     }
                 }
             }
@@ -442,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int q = warp & 3, part = (warp - 4) >> 2;
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
+        const uint32_t turned = smem_u32((part ? sA : sB) + (kStages - 1) * kHalf) + q * kOut;
         list.window(p, lane);
         int i = 0;
         bool ok = true;
@@ -485,7 +555,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const size_t at = (MODE == kWgrad ? static_cast<size_t>(tile.e * p.stride_c) : 0) + static_cast<size_t>(row) * static_cast<size_t>(p.ldc) + n;
-            if (p.beta != 0.f) {
+            if (p.turn) {
+                const int first = n - lane, cols = min(p.n - first, 32), all = min(half, tile.row_end - row);
+                if (cols > 0) {
+                    if (p.c_type == kOutF16)
+                        store_turned<kOutF16>(p, acc, at - lane, all, cols, turned, lane);
+                    else
+                        store_turned<kOutBF16>(p, acc, at - lane, all, cols, turned, lane);
+                }
+            } else if (p.beta != 0.f) {
                 if (p.c_type == kOutF32)
                     store_rows<kOutF32, true>(p, acc, at, rows);
                 else if (p.c_type == kOutF16)
@@ -688,6 +766,10 @@ cudaError_t run_grouped(const Grouped &g, cudaStream_t stream, CallInfo *info) {
     }
     info->launches = 1;
     a.split = a.product ? pick_split(g, std::max(1, device_sm_count() / 2)) : 1;
+    // of a contraction; the weights' gradient's are known as a mean
+    const double blocks = (g.wgrad ? static_cast<double>(g.R) / g.E : g.K) / kKB;
+    a.turn = a.split == 1 && g.c_type != kOutF32 && g.beta == 0.f && blocks <= kChunk && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && g.ldc % 8 == 0 && (!g.wgrad || g.stride_c % 8 == 0);
+    a.stages = kStages - a.turn;
     const bool split = a.split > 1;
     info->plan = g.wgrad ? (split ? "grouped_wgrad_pair_splitk" : "grouped_wgrad_pair") : split ? "grouped_pair_splitk" : "grouped_pair";
     if (g.wgrad) return split ? launch_grouped<kWgrad, true>(g, a, stream, info) : launch_grouped<kWgrad, false>(g, a, stream, info);

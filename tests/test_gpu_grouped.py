@@ -247,3 +247,32 @@ def test_descending_offsets_stay_inside():
     g.gemm_grouped(A, B, C, off)
     want, mag = grouped(A, B, off, True)
     close(C, want, rounded(PRODUCT * mag, want, F32))
+
+
+@pytest.mark.parametrize("c", [F16, BF16])
+@pytest.mark.parametrize("N", [1, 7, 31, 33, 250, 513, 1021])
+def test_short_contractions_into_16_bits(N, c):
+    """Rows of C on 16 bytes and not, any last column, more tiles than CTA pairs: what lies between the rows stays."""
+    torch.manual_seed(N)
+    sizes = [1, 8, 9, 0, 127, 129, 250, 255, 257, 300, 64] * 8
+    off, n, K = offsets_of(sizes), sum(sizes), 40
+    A, B = padded(n, K, dtype=c), padded(len(sizes), N, K, dtype=c)
+    want, mag = grouped(A, B, off, True)
+    for pad, start in ((-N % 8 + 8, 0), (-N % 8, 8), (-N % 8 + 8, 4), (-N % 2 + 2, 0)):
+        full = torch.full((n + 2, N + pad), -7.0, device="cuda", dtype=c).reshape(-1)
+        C = full[start:start + n * (N + pad)].reshape(n, N + pad)[:, :N]
+        g.gemm_grouped(A, B, C, off, b_trans=True)
+        assert g.check() == g.GEMM_OK
+        close(C, want, rounded(PRODUCT * mag, want, c))
+        C.fill_(-7.0)
+        assert (full == -7.0).all()
+    M, few = 130, offsets_of([3, 64, 0, 65, 200])
+    X, Y = padded(340, M, dtype=c), padded(340, N, dtype=c)
+    want, mag = wgrad(X, Y, few)
+    full = torch.full((5, M + 3, -(-N // 8) * 8 + 8), -7.0, device="cuda", dtype=c)
+    C = full[:, :M, :N]
+    g.gemm_grouped_wgrad(X, Y, C, few)
+    assert g.check() == g.GEMM_OK
+    close(C, want, rounded(PRODUCT * mag, want, c))
+    C.fill_(-7.0)
+    assert (full == -7.0).all()
