@@ -6,8 +6,8 @@
 //   weights  C[e] = alpha A[rows of e]^T B[rows of e] + beta C[e].
 //
 // FP16 or BF16 operands, FP32 sums.  The offsets are on the device and the host
-// does not know them: a CTA pair takes every ncl-th tile of a list that each warp
-// works out for itself, 32 experts at a time, one a lane.
+// does not know them: a CTA pair takes every ncl-th tile of a list that one warp of
+// each CTA works out, 32 experts at a time, one a lane, ahead of the others.
 //
 // Bound: the tensor core at the clock that the power limit leaves, for long
 // contractions (8192 rows over 8 experts of 4096 x 4096 160 us, 1.72 PFLOP/s; the
@@ -45,10 +45,13 @@ constexpr int kChunk = 8;
 // Registers: 384 threads of 168 at launch, 64,512; 128 x 56 + 256 x 224 = 64,512.
 constexpr int kRegsFew = 56, kRegsMany = 224;
 constexpr int kThreads = 128 + 32 * kEpi;
-constexpr int kBars = 3 * kStages + 4 + 1;
+constexpr int kTiles = 4;                 // found ahead
+constexpr int kBars = 3 * kStages + 4 + 1 + 2 * kTiles;
+static_assert(kBars % 2 == 0, "the tiles behind them start on 16 bytes");
+constexpr int kTurnRows = 192;            // of a contraction, on average
 constexpr int kOutRows = 64, kOut = kOutRows * 32 * 2;  // results that a warp turns in shared memory at a time
 static_assert(4 * kOut <= kHalf, "four warps turn theirs in one operand's part of a stage");
-constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16;
+constexpr int kSmemBytes = 1024 + kStages * 2 * kHalf + kBars * 8 + 16 + kTiles * 32;
 static_assert(kSmemBytes <= 232448, "shared memory of a CTA");
 // Rows of A that one copy brings in: 32, once or twice, for a CTA's half of a tile
 // of up to 128 rows, otherwise 128.  With 128 always, 2 rows of 2 experts of 11008 x
@@ -84,11 +87,12 @@ struct GroupedArgs {
 
 // A tile of C: rows [m0, row_end) of expert e, `span` of them when rounded up to
 // 16, from column n0; and its contraction k0 .. k1 (wgrad: rows of A and B).
-struct Tile {
+struct alignas(16) Tile {
     int e, m0, n0, row_end, span;
     int k0, k1;
     int unit;  // of the tile (SPLIT)
 };
+static_assert(sizeof(Tile) == 32, "two words of 16 bytes");
 
 // Tile i of tiles_m x tiles_n: groups of 8 tile rows, so that a wave of tiles
 // shares its rows and columns in L2.
@@ -154,6 +158,33 @@ struct TileList {
         }
         tile.n0 *= kTile;
         if (!p.product) tile.k1 = tile.k0;
+        return true;
+    }
+};
+
+// The tiles that one warp of a CTA finds, kTiles ahead, for the others: some 700
+// clocks of dependent shuffles and divisions each, which every warp spent by itself
+// before (24,576 rows over 64 experts of 2048 x 256 47.9 -> 42.8 us, of 2048 x 1024
+// 83.7 -> 81.6; the weights' gradient of 16,384 over 16 of 2048 x 4096 184 -> 179).
+struct TileRing {
+    uint64_t *found, *taken;
+    Tile *tiles;
+    int slot = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ void step() {
+        if (++slot == kTiles) slot = 0, phase ^= 1u;
+    }
+    // A whole warp's; 0: behind the last tile, -1: the wait ran out.
+    __device__ __forceinline__ int take(Tile &tile, int lane, unsigned long long wait_ns) {
+        if (!__all_sync(0xffffffffu, mbar_wait_patient(&found[slot], phase, wait_ns))) return -1;
+        const int4 *from = reinterpret_cast<const int4 *>(tiles + slot);
+        const int4 a = from[0], b = from[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[slot]);
+        step();
+        tile.e = a.x, tile.m0 = a.y, tile.n0 = a.z, tile.row_end = a.w;
+        tile.span = b.x, tile.k0 = b.y, tile.k1 = b.z, tile.unit = b.w;
         // The same in every lane: told so, the compiler keeps what depends on these
         // in uniform registers, which the copies and MMAs take.
         tile.e = __shfl_sync(0xffffffffu, tile.e, 0);
@@ -163,7 +194,7 @@ struct TileList {
         tile.span = __shfl_sync(0xffffffffu, tile.span, 0);
         tile.k0 = __shfl_sync(0xffffffffu, tile.k0, 0);
         tile.k1 = __shfl_sync(0xffffffffu, tile.k1, 0);
-        return true;
+        return tile.e >= 0;
     }
 };
 
@@ -175,7 +206,8 @@ __device__ __forceinline__ void grouped_timeout(volatile int *abort_flag, unsign
 }
 
 // A lane's column of C down the rows of the tile that the warp has, from its sums.
-// BETA = false: C is not read.
+// BETA = false: C is not read.  What the tile does not have is passed over by 16 rows
+// (384 rows over 64 experts of 2048 x 128 21 -> 14 us).
 template <int CT, bool BETA>
 __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&acc)[kCols], size_t at, int rows) {
     using T = typename Elem8<CT>::T;
@@ -203,14 +235,13 @@ __device__ __forceinline__ void store_rows(const GroupedArgs &p, const float (&a
 // 2 i, 2 i + 1 of each eight.  Column c of eight rows is at 16 bytes c, the eight that
 // it is in turned by 2 (c / 8), so that none of the accesses meets a bank twice.
 //
-// For contractions of one chunk, where a tile's time is its stores': BF16 results of
-// 4096 x 6 rows over 64 experts of 2048 x 128 49.0 -> 45.3 us, of 64 x 6 rows 21.6 ->
-// 14.2, the weights' gradient of 128 x 2 rows over 16 experts of 2048 x 4096 101 -> 88.
-// At 512 either takes 55 us, and behind that the ring's last stage, whose memory
-// this has, is worth more (weights' gradient of 1024 rows an expert 187 us, turned 190).
-// A copy of 256 bytes for each row out of shared memory instead took twice as long as
-// single stores (434 us against 219 for 79 x 8 rows, 23 experts of 5120 x 2560, in this
-// form 192), full lines by four warps together 282.
+// For the weights' gradient from few rows, whose time is its stores: 256 rows over 16
+// experts of 2048 x 4096 92 -> 79.5 us, 632 over 23 of 5120 x 2560 201 -> 169.  At 256
+// rows an expert either takes 90, and behind that the ring's last stage, whose memory
+// this has, is worth more.  Rows (of which a tile seldom has 256) gained nothing: 24,576
+// over 64 experts of 2048 x 256 42.1 us, 42.8 stored singly, of 2048 x 512 52.6, 51.3.
+// A copy of 256 bytes for each row out of shared memory took twice as long as single
+// stores, full lines by four warps together a quarter longer.
 // at: of the warp's first column; cols: that it has.
 template <int CT>
 __device__ __forceinline__ void store_turned(const GroupedArgs &p, const float (&acc)[kCols], size_t at, int rows, int cols, uint32_t smem, int lane) {
@@ -226,6 +257,7 @@ __device__ __forceinline__ void store_turned(const GroupedArgs &p, const float (
         if (j0 < rows) {
 #pragma unroll
             for (int j = j0; j < j0 + kOutRows; j += 8) {
+                if (j >= rows) break;
                 uint32_t w[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) w[k] = pack2_out16(alpha * acc[j + 2 * k], alpha * acc[j + 2 * k + 1], CT);
@@ -233,21 +265,26 @@ __device__ __forceinline__ void store_turned(const GroupedArgs &p, const float (
             }
             __syncwarp();
 #pragma unroll
-            for (int j = j0; j < j0 + kOutRows; j += 8) {
-                uint4 w;
-                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(take + (j - j0) * 64) : "memory");
-                const int r = j + (lane >> 2);
-                if (r < rows && left > 0 && debug_in_bounds(p.c_extent == 0 || at + static_cast<size_t>(r) * static_cast<size_t>(p.ldc) + min(cols, col + 8) <= p.c_extent, p.err)) {
-                    if (left >= 8) {
-                        *reinterpret_cast<uint4 *>(to) = w;
-                    } else {
-                        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+            for (int j4 = j0; j4 < j0 + kOutRows; j4 += 32) {
+                if (j4 >= rows) break;
+                uint32_t w[4][4];
 #pragma unroll
-                        for (int k = 0; k < 7; ++k)
-                            if (k < left) to[k] = static_cast<uint16_t>(e[k >> 1] >> (k & 1) * 16);
+                for (int k = 0; k < 4; ++k)
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];" : "=r"(w[k][0]), "=r"(w[k][1]), "=r"(w[k][2]), "=r"(w[k][3]) : "r"(take + (j4 - j0 + 8 * k) * 64) : "memory");
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int r = j4 + 8 * k + (lane >> 2);
+                    if (r < rows && left > 0 && debug_in_bounds(p.c_extent == 0 || at + static_cast<size_t>(r) * static_cast<size_t>(p.ldc) + min(cols, col + 8) <= p.c_extent, p.err)) {
+                        if (left >= 8) {
+                            *reinterpret_cast<uint4 *>(to) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 7; ++i)
+                                if (i < left) to[i] = static_cast<uint16_t>(w[k][i >> 1] >> (i & 1) * 16);
+                        }
                     }
+                    to += step;
                 }
-                to += step;
             }
             __syncwarp();
         }
@@ -305,7 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *tempty = tfull + 2;
     uint64_t *mma_done = tempty + 2;
     uint64_t *landed = mma_done + 1;  // last blocks of a contraction that ends in them
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(landed + kStages);
+    uint64_t *found = landed + kStages;
+    Tile *tiles = reinterpret_cast<Tile *>(found + 2 * kTiles);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tiles + kTiles);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -321,6 +360,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 2 * kEpi);  // the warps of both CTAs
+        }
+        for (int b = 0; b < kTiles; ++b) {
+            mbar_init(&found[b], 1);
+            mbar_init(&found[kTiles + b], 1 + (leader ? 1 : 0) + (MODE == kWgrad ? 1 : 0) + kEpi);  // warps 0, 1, 2 and the epilogue
         }
         mbar_init(mma_done, 1);
         *abort_flag = 0;
@@ -343,18 +386,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     uint32_t armed = 0, armed_parity = 0;
     uint32_t ends = 0, ends_parity = 0;  // stages that had such a block, and the parity of the last
-    TileList<MODE == kWgrad, SPLIT> list;
+    TileRing ring = {found, found + kTiles, tiles};
     Tile tile;
+    auto next = [&] {
+        const int got = ring.take(tile, lane, p.wait_ns);
+        if (got < 0) grouped_timeout(abort_flag, p.err);
+        return got > 0;
+    };
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
-            list.window(p, lane);
-            int stage = 0;
+                int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             const uint32_t full_even = mapa_shared(smem_u32(full), 0), at_b = smem_u32(sB), at_a = smem_u32(sA);
-            for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
+            while (ok && !*abort_flag && next()) {
                 const int half = tile.span >> 1, my_m = tile.m0 + rank * half, my_n = tile.n0 + rank * 128;
                 // rows of A (wgrad: columns) come in boxes
                 const int box = MODE == kWgrad ? 64 : half <= 2 * kBoxSome ? kBoxSome : kBoxMany;
@@ -421,10 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (MODE == kWgrad && warp == 2) {
             // ------------------------------------------------ ends of contractions (both CTAs)
-            list.window(p, lane);
-            int stage = 0;
+                int stage = 0;
             bool ok = true;
-            for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
+            while (ok && !*abort_flag && next()) {
                 const int blocks = tile_blocks(tile), valid = tile.k1 - tile.k0 - (blocks - 1) * kKB;
                 if (blocks == 0) continue;
                 stage = (stage + blocks - 1) % p.stages;
@@ -451,6 +497,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 stage = stage + 1 == p.stages ? 0 : stage + 1;
             }
+        } else if (warp == 3) {
+            // ------------------------------------------------ tiles (both CTAs)
+            TileList<MODE == kWgrad, SPLIT> list;
+            list.window(p, lane);
+            for (int t = cid; !*abort_flag; t += ncl) {
+                const bool more = list.find(p, t, lane, tile);
+                if (!more) tile.e = -1;
+                if (!__all_sync(0xffffffffu, mbar_wait_patient(&ring.taken[ring.slot], ring.phase ^ 1u, p.wait_ns))) {
+                    grouped_timeout(abort_flag, p.err);
+                    break;
+                }
+                if (lane == 0) {
+                    int4 *to = reinterpret_cast<int4 *>(tiles + ring.slot);
+                    to[0] = make_int4(tile.e, tile.m0, tile.n0, tile.row_end);
+                    to[1] = make_int4(tile.span, tile.k0, tile.k1, tile.unit);
+                    mbar_arrive(&found[ring.slot]);
+                }
+                __syncwarp();
+                if (!more) break;
+                ring.step();
+            }
         } else if (warp == 1 && leader) {
             // ------------------------------------------------ MMA issuer (even CTA)
             // K-major: 128-byte rows, 8-row groups 1024 bytes apart, 16 k = 32
@@ -460,11 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), MODE != kForward ? kBox : 16, 1024);
             const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), MODE == kWgrad ? kBox : 16, 1024);
             constexpr uint32_t kBstep = MODE != kForward ? 2048 >> 4 : 32 >> 4, kAstep = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
-            list.window(p, lane);
-            int stage = 0, i = 0;  // i: chunk
+                int stage = 0, i = 0;  // i: chunk
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
+            while (ok && !*abort_flag && next()) {
                 const int blocks = tile_blocks(tile);
                 const uint32_t idesc = p.idesc | static_cast<uint32_t>(tile.span >> 3) << 17;
                 for (int kb0 = 0; ok && kb0 < blocks; kb0 += kChunk, ++i) {
@@ -512,10 +578,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
         const uint32_t release[2] = {mapa_shared(smem_u32(&tempty[0]), 0), mapa_shared(smem_u32(&tempty[1]), 0)};
         const uint32_t turned = smem_u32((part ? sA : sB) + (kStages - 1) * kHalf) + q * kOut;
-        list.window(p, lane);
         int i = 0;
         bool ok = true;
-        for (int t = cid; ok && !*abort_flag && list.find(p, t, lane, tile); t += ncl) {
+        while (ok && !*abort_flag && next()) {
             const int chunks = (tile_blocks(tile) + kChunk - 1) / kChunk;
             const int half = tile.span >> 1;
             float acc[kCols];
@@ -555,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             const size_t at = (MODE == kWgrad ? static_cast<size_t>(tile.e * p.stride_c) : 0) + static_cast<size_t>(row) * static_cast<size_t>(p.ldc) + n;
-            if (p.turn) {
+            if (MODE == kWgrad && p.turn) {
                 const int first = n - lane, cols = min(p.n - first, 32), all = min(half, tile.row_end - row);
                 if (cols > 0) {
                     if (p.c_type == kOutF16)
@@ -766,9 +831,8 @@ cudaError_t run_grouped(const Grouped &g, cudaStream_t stream, CallInfo *info) {
     }
     info->launches = 1;
     a.split = a.product ? pick_split(g, std::max(1, device_sm_count() / 2)) : 1;
-    // of a contraction; the weights' gradient's are known as a mean
-    const double blocks = (g.wgrad ? static_cast<double>(g.R) / g.E : g.K) / kKB;
-    a.turn = a.split == 1 && g.c_type != kOutF32 && g.beta == 0.f && blocks <= kChunk && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 && g.ldc % 8 == 0 && (!g.wgrad || g.stride_c % 8 == 0);
+    a.turn = g.wgrad && a.split == 1 && g.c_type != kOutF32 && g.beta == 0.f && g.R <= static_cast<long long>(kTurnRows) * g.E && reinterpret_cast<uintptr_t>(g.C) % 16 == 0 &&
+             g.ldc % 8 == 0 && g.stride_c % 8 == 0;
     a.stages = kStages - a.turn;
     const bool split = a.split > 1;
     info->plan = g.wgrad ? (split ? "grouped_wgrad_pair_splitk" : "grouped_wgrad_pair") : split ? "grouped_pair_splitk" : "grouped_pair";

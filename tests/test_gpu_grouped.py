@@ -266,13 +266,15 @@ def test_short_contractions_into_16_bits(N, c):
         close(C, want, rounded(PRODUCT * mag, want, c))
         C.fill_(-7.0)
         assert (full == -7.0).all()
-    M, few = 130, offsets_of([3, 64, 0, 65, 200])
-    X, Y = padded(340, M, dtype=c), padded(340, N, dtype=c)
-    want, mag = wgrad(X, Y, few)
-    full = torch.full((5, M + 3, -(-N // 8) * 8 + 8), -7.0, device="cuda", dtype=c)
-    C = full[:, :M, :N]
-    g.gemm_grouped_wgrad(X, Y, C, few)
-    assert g.check() == g.GEMM_OK
-    close(C, want, rounded(PRODUCT * mag, want, c))
-    C.fill_(-7.0)
-    assert (full == -7.0).all()
+    for M, few in ((130, [3, 64, 0, 65, 200]), (515, [3, 64, 0, 65, 20] * 9), (77, [300, 350])):
+        R = sum(few) + 8
+        X, Y = padded(R, M, dtype=c), padded(R, N, dtype=c)
+        want, mag = wgrad(X, Y, offsets_of(few))
+        for pad, start in ((-N % 8 + 8, 0), (-N % 8, 8), (-N % 8 + 8, 4), (-N % 2 + 2, 0)):
+            full = torch.full((len(few) + 1, M + 3, N + pad), -7.0, device="cuda", dtype=c).reshape(-1)
+            C = full[start:start + len(few) * (M + 3) * (N + pad)].reshape(len(few), M + 3, N + pad)[:, :M, :N]
+            g.gemm_grouped_wgrad(X, Y, C, offsets_of(few))
+            assert g.check() == g.GEMM_OK
+            close(C, want, rounded(PRODUCT * mag, want, c))
+            C.fill_(-7.0)
+            assert (full == -7.0).all()
