@@ -10,13 +10,13 @@
 // each CTA works out, 32 experts at a time, one a lane, ahead of the others.
 //
 // Bound: the tensor core at the clock that the power limit leaves, for long
-// contractions (8192 rows over 8 experts of 4096 x 4096 160 us, 1.72 PFLOP/s; the
-// weights' gradient with 4096 rows an expert 599 us for 32768 rows, 1.83); the
-// weights' bytes for few rows (2400 rows over 64 experts of 2048 x 2048 88.7 us,
-// 6.3 TB/s); both at once between (24,570 rows over 64 experts of 2048 x 1024 85
+// contractions (8192 rows over 8 experts of 4096 x 4096 158 us, 1.74 PFLOP/s; the
+// weights' gradient with 4096 rows an expert 590 us for 32768 rows, 1.86); the
+// weights' bytes for few rows (2400 rows over 64 experts of 2048 x 2048 88.3 us,
+// 6.3 TB/s); both at once between (24,570 rows over 64 experts of 2048 x 1024 82
 // us: 54 of multiplication, 62 of memory).  Results in FP32 beside a contraction of
-// 1000 rows are bound by neither: 8 experts of 4096 x 4096 with 8192 rows take 206
-// us, in BF16 181, without stores as long as their multiplication; the MMAs wait
+// 1000 rows are bound by neither: 8 experts of 4096 x 4096 with 8192 rows take 202
+// us, in BF16 175, without stores as long as their multiplication; the MMAs wait
 // for operands, whose copies wait while the results are on their way to memory.
 #include <algorithm>
 #include <cstdint>
