@@ -278,3 +278,37 @@ def test_short_contractions_into_16_bits(N, c):
             close(C, want, rounded(PRODUCT * mag, want, c))
             C.fill_(-7.0)
             assert (full == -7.0).all()
+
+
+def test_weights_into_16_bits_repeat():
+    """Twice, on two streams at once and from a graph: the same bits; NaN of one expert stays there; no rows at all give zeros."""
+    torch.manual_seed(5)
+    sizes, M, N = [3, 70, 0, 129, 64] * 6, 300, 520
+    off, R = offsets_of(sizes), sum(sizes)
+    X, Y = padded(R, M, dtype=BF16), padded(R, N, dtype=BF16)
+    X[73 + 64] = float("nan")  # of expert 3
+    outs = [padded(len(sizes), M, N, dtype=BF16, fill=-7.0) for _ in range(4)]
+    g.gemm_grouped_wgrad(X, Y, outs[0], off)
+    side = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s, C in zip(side, outs[1:3]):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            g.gemm_grouped_wgrad(X, Y, C, off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.gemm_grouped_wgrad(X, Y, outs[3], off)
+    outs[3].fill_(-7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert g.check() == g.GEMM_OK
+    for C in outs[1:]:
+        assert torch.equal(C.view(torch.int16), outs[0].view(torch.int16))
+    others = [e for e in range(len(sizes)) if e != 3]
+    assert outs[0][3].isnan().all() and torch.isfinite(outs[0][others]).all() and (outs[0][2] == 0).all()
+    want, mag = wgrad(X, Y, off)
+    close(outs[0][others], want[others], rounded(PRODUCT * mag[others], want[others], BF16))
+    g.gemm_grouped_wgrad(X, Y, outs[0], torch.zeros_like(off))
+    g.gemm_grouped_wgrad(X, Y, outs[1], off, 0.0)
+    g.gemm_grouped_wgrad(X[:0], Y[:0], outs[2], torch.zeros_like(off))
+    assert all((C == 0).all() for C in outs[:3])
