@@ -280,7 +280,7 @@ def test_short_contractions_into_16_bits(N, c):
             assert (full == -7.0).all()
 
 
-def test_weights_into_16_bits_repeat():
+def test_weights_into_16_bits_streams_and_graphs():
     """Twice, on two streams at once and from a graph: the same bits; NaN of one expert stays there; no rows at all give zeros."""
     torch.manual_seed(5)
     sizes, M, N = [3, 70, 0, 129, 64] * 6, 300, 520
