@@ -14,9 +14,9 @@
 // are summed, so no inverse of the order is stored.  No sum of floating-point
 // numbers is made with atomics, so the results do not depend on the order in which
 // CTAs run.  Measured on BF16, 8192 tokens, 6 slots of 64 experts, 2048 columns:
-// dispatch 46.4 us, 7.3 of them for the order (235 MB, 5.1 TB/s, 6.0 while it
-// copies), combine 40.6 (5.8 TB/s), its gradient 68.6 (437 MB, 6.4 TB/s).  For few
-// tokens a launch: 16 tokens, 2 slots, 4096 columns 3.8 us in a graph.
+// dispatch 42.1 us, 7.1 of them for the order (235 MB, 5.6 TB/s), combine 40.6 (5.8
+// TB/s), its gradient 68.6 (437 MB, 6.4 TB/s).  For few tokens a launch: 16 tokens, 2
+// slots, 4096 columns 3.5 us in a graph.
 #include <algorithm>
 #include <cstdint>
 
@@ -27,6 +27,13 @@ namespace gemm11 {
 namespace {
 
 constexpr int kSortThreads = 1024;
+// Rows that go through shared memory: they are on their way while the slots are
+// counted, and a copy of one is an instruction.  8192 tokens, 6 slots, in registers /
+// so: rows of 1 KB 14.2 / 15.7 us, 2 KB 23.5 / 24.5, 4 KB 46.7 / 42.1; 2000 tokens with
+// rows of 16 KB 43.3 / 38.9, of 32 KB 83.0 / 77.5, of 64 KB, of which 3 fit, 158.4 / 158.7.
+constexpr int kBulkBytes = 4096;          // of a row, at least
+constexpr int kMinBuffers = 4, kMaxBuffers = 64;
+constexpr int kBulkSmem = 232448 - 5120;  // 5120: the kernel's own
 constexpr int kSortBatch = 1024;  // slots that are ranked and then copied together
 static_assert(kDispatchMaxExperts <= 8192, "an expert and its slots among 32 in one word");
 
@@ -41,6 +48,8 @@ struct DispatchArgs {
     int *offsets, *rows;
     int per_cta;  // tokens
     int copies;   // of the counters, a power of two
+    int warps, depth;  // that copy rows through shared memory (kBulk), and the buffers of each
+    int pitch;         // bytes from one buffer to the next
     unsigned *err;
     size_t xs_extent;  // bytes, checked by GEMM11_DEBUG builds
 };
@@ -72,7 +81,7 @@ struct Segment {
         }
     }
 };
-constexpr int kSegment = 4;                        // 16-byte pieces of a lane: 46.7 us, 2: 47.4, 1: 49.4 (8192 tokens, 6 slots, 2048 columns)
+constexpr int kSegment = 4;                        // 16-byte pieces of a lane: 46.7 us, 2: 47.4, 1: 49.4 (8192 tokens, 6 slots, 2048 columns, without kBulk)
 constexpr int kSegmentPieces = 32 * kSegment;      // of a warp
 constexpr int kSegmentElements = 128;              // of a warp, where rows are not aligned
 
@@ -94,19 +103,42 @@ __device__ __forceinline__ void copy_elements(const DispatchArgs &p, const uint8
 // that it knows where its slots go without waiting for another CTA: 49,152 slots
 // over 64 experts take 3.5 us.  (Clusters of eight that share the counting save 1
 // us of that and lose it again: of the 152 SMs they fill 128.)
-template <bool VEC>
+enum Rows { kElements, kVectors, kBulk };  // in pieces of one element, 16 bytes, a row through shared memory
+template <Rows ROWS>
 __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchArgs p) {
-    extern __shared__ int counts[];  // of each expert: slots before this CTA's, then the others
+    constexpr bool VEC = ROWS == kVectors;
+    extern __shared__ __align__(128) int counts[];  // of each expert: slots before this CTA's, then the others
     __shared__ int warp_sum[32];
     __shared__ int pos[kSortBatch];
+    __shared__ uint64_t full[ROWS == kBulk ? kMaxBuffers : 1];
     const int copies = p.copies, E = p.E;  // neighbouring lanes count in counters of their own: fewer of a warp's additions meet
     int *const before = counts, *const rest = counts + E * copies;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t0 = blockIdx.x * p.per_cta, t1 = t0 + min(p.T - t0, p.per_cta);
     for (int e = threadIdx.x; e < 2 * E * copies; e += kSortThreads) counts[e] = 0;
+    const uint32_t rows_at = smem_u32(counts) + ((2 * E * copies * 4 + 127) & ~127);
+    if (ROWS == kBulk && threadIdx.x == 0) {
+        for (int b = 0; b < p.warps * p.depth; ++b) mbar_init(&full[b], 1);
+        fence_mbarrier_init();
+    }
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
+    // Warp 31 - w takes the CTA's tokens w, w + warps, ..; the m-th of them is in its
+    // buffer m % depth.  (Few slots are counted by the lowest warps, which copy last.)
+    const int worker = kSortThreads / 32 - 1 - warp;
+    int next_row = worker, fetched = 0;
+    auto fetch = [&] {
+        if (next_row < t1 - t0 && lane == 0) {
+            const int b = worker * p.depth + fetched % p.depth;
+            mbar_arrive_expect_tx(&full[b], p.row_bytes);
+            bulk_load(rows_at + b * p.pitch, p.X + static_cast<long long>(t0 + next_row) * p.x_bytes, p.row_bytes, &full[b]);
+        }
+        if (next_row < t1 - t0) ++fetched;
+        next_row += p.warps;
+    };
+    if (ROWS == kBulk && worker < p.warps)
+        for (int m = 0; m < p.depth; ++m) fetch();
     const int mine = t0 * p.k, my_copy = lane & (copies - 1);
     auto count = [&](int e, int i) {
         if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd((i < mine ? before : rest) + e * copies + my_copy, 1);
@@ -184,6 +216,8 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
     if (blockIdx.x == 0 && threadIdx.x == kSortThreads - 1) p.offsets[E] = start;
 
     const int batch = kSortBatch / p.k;  // tokens
+    int my_row = worker, read = 0;
+    bool late = false;
     const int segments = VEC ? ((p.row_bytes >> 4) + kSegmentPieces - 1) / kSegmentPieces : (p.row_bytes / p.esize + kSegmentElements - 1) / kSegmentElements;
     const int elements = p.row_bytes / p.esize, whole = (p.row_bytes >> 4) * (16 / p.esize);
     for (int t = t0; t < t1; t += batch) {
@@ -218,7 +252,32 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
         }
         __syncthreads();
         for (int i = threadIdx.x; i < slots; i += kSortThreads) p.rows[t * p.k + i] = pos[i];
-        if (VEC) {
+        if (ROWS == kBulk) {
+            // read = tokens of this warp so far, the next of them `my_row`
+            for (; worker < p.warps && my_row < t - t0 + tokens && read < fetched; my_row += p.warps, ++read) {
+                const int b = worker * p.depth + read % p.depth;
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[b], (read / p.depth) & 1))) {
+                    if (lane == 0) atomicOr(p.err, kWatchdogTimeout);
+                    late = true;
+                }
+                if (late) continue;  // what was fetched is waited for
+                for (int j = lane; j < p.k; j += 32) {
+                    const int r = pos[(my_row - (t - t0)) * p.k + j];
+                    if (r >= 0 && debug_in_bounds(static_cast<size_t>(r * p.xs_bytes + p.row_bytes) <= p.xs_extent, p.err))
+                        bulk_store(p.Xs + r * p.xs_bytes, rows_at + b * p.pitch, p.row_bytes);
+                }
+                bulk_commit();
+                // the buffer of the token before is refilled, with one alone this token's
+                if (next_row < t1 - t0 && (read > 0 || p.depth == 1)) {
+                    if (p.depth > 1)
+                        bulk_wait_read_all_but_one();
+                    else
+                        bulk_wait_read_all();
+                    __syncwarp();
+                    fetch();
+                }
+            }
+        } else if (VEC) {
             // the next unit is read before this one is written
             for (int u = warp; u < units; u += kSortThreads / 32) {
                 const int ahead_u = u + kSortThreads / 32;
@@ -246,6 +305,7 @@ __global__ void __launch_bounds__(kSortThreads) dispatch_kernel(const DispatchAr
             }
         }
     }
+    if (ROWS == kBulk) bulk_wait_all();
 }
 
 // ------------------------------------------------------------------ back to the tokens
@@ -484,7 +544,20 @@ cudaError_t run_moe_dispatch(const MoeDispatch &d, cudaStream_t stream, CallInfo
     const size_t smem = 2u * sizeof(int) * d.E * a.copies;
     info->plan = vec ? "moe_dispatch" : "moe_dispatch_unaligned";
     info->launches = 1;
-    return vec ? launch_pdl(dispatch_kernel<true>, ctas, kSortThreads, smem, stream, a) : launch_pdl(dispatch_kernel<false>, ctas, kSortThreads, smem, stream, a);
+    if (vec && a.row_bytes % 16 == 0 && a.row_bytes >= kBulkBytes && a.row_bytes <= kBulkSmem) {
+        a.pitch = (a.row_bytes + 127) & ~127;
+        const size_t first = (smem + 127) & ~size_t(127);
+        const int buffers = static_cast<int>(std::min<size_t>({(kBulkSmem - first) / a.pitch, static_cast<size_t>(a.per_cta), static_cast<size_t>(kMaxBuffers)}));
+        if (buffers >= std::min(a.per_cta, kMinBuffers)) {
+            a.depth = (buffers + kSortThreads / 32 - 1) / (kSortThreads / 32);
+            a.warps = buffers / a.depth;
+            static unsigned long long smem_set = 0;
+            const cudaError_t e = ensure_dynamic_smem(dispatch_kernel<kBulk>, kBulkSmem, smem_set);
+            if (e != cudaSuccess) return e;
+            return launch_pdl(dispatch_kernel<kBulk>, ctas, kSortThreads, first + static_cast<size_t>(a.warps) * a.depth * a.pitch, stream, a);
+        }
+    }
+    return vec ? launch_pdl(dispatch_kernel<kVectors>, ctas, kSortThreads, smem, stream, a) : launch_pdl(dispatch_kernel<kElements>, ctas, kSortThreads, smem, stream, a);
 }
 
 cudaError_t run_moe_combine(const MoeCombine &c, cudaStream_t stream, CallInfo *info) {

@@ -91,6 +91,34 @@ def test_dispatch_many_slots_and_one_expert():
     assert torch.equal(Xs[rows.reshape(-1).long(), 0], X[:, 0].repeat_interleave(4))
 
 
+# Rows of 4 KB and more go through shared memory: all of a CTA's at once, more of them than it holds, several batches of 1024 slots,
+# more slots of a token than lanes, sizes that are not multiples of 128 bytes, rows of which few or none fit.
+@pytest.mark.parametrize("T,k,E,H,dtype,pad", [
+    (2100, 3, 9, 2048, BF16, 0), (9001, 2, 4, 2048, F32, 8), (1201, 2, 5, 8192, F32, 0), (1500, 1, 5, 16384, BF16, 0), (700, 2, 3, 30000, F16, 8), (400, 2, 3, 60000, F16, 0),
+    (3100, 40, 64, 2056, BF16, 16), (30001, 6, 64, 2048, BF16, 0), (153, 2, 8, 2048, F16, 0), (151, 6, 300, 12296, F32, 4),
+])
+def test_dispatch_long_rows(T, k, E, H, dtype, pad):
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    ids = torch.randint(-1, E + 1, (T, k), generator=gen, device="cuda", dtype=torch.int32)
+    X = strided(T, H, dtype, pad)
+    X.copy_(torch.randn(T, H, generator=gen, device="cuda"))
+    Xs = strided(T * k, H, dtype, pad, fill=-7.0)
+    offsets, rows = torch.full((E + 1,), -9, dtype=torch.int32, device="cuda"), torch.full((T, k), -9, dtype=torch.int32, device="cuda")
+    want_offsets, want_rows = sort(ids.cpu(), E)
+    for _ in range(2):
+        g.moe_dispatch(ids, X, Xs, offsets, rows)
+        assert g.check() == g.GEMM_OK
+        assert torch.equal(offsets.cpu().long(), want_offsets) and torch.equal(rows.cpu().long(), want_rows)
+        flat = rows.reshape(-1).long()
+        taken = (flat >= 0).nonzero()[:, 0]
+        for part in taken.split(4096):
+            assert torch.equal(Xs[flat[part]], X[part // k])
+        assert (Xs[int(offsets[-1]):] == -7.0).all()
+        if pad:
+            assert (Xs.as_strided((T * k, pad), (H + pad, 1), storage_offset=H) == -7.0).all()
+        X.neg_()
+
+
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("T,k,E,H,dtype,pad,shift", SHAPES)
 def test_combine(T, k, E, H, dtype, pad, shift, weighted):
