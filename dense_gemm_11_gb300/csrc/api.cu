@@ -561,6 +561,9 @@ constexpr int kMaxExtent = 0x7FFFFFFF - 511;
 
 // Slots of a token that the mixture-of-experts operators for many tokens take.
 constexpr int kRowsMaxTopK = 128;
+// Slots of one dispatch: its CTAs' 32-bit indices run over the last one by up to
+// 12,287 (three times four slots for each of 1024 threads).
+constexpr int kDispatchMaxSlots = 0x7FFFFFFF - 32767;
 
 // Row strides of the tensor-memory-access path end at 2^40 bytes.
 constexpr long long kMaxStride = 1LL << 38;
@@ -916,7 +919,7 @@ int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids, const void
     const bool copy = H > 0 && (X || Xs);
     if (copy && (ldx < H || ldxs < H)) return GEMM_ERR_INVALID_ARG;
     if (!offsets || (T > 0 && (!ids || !rows || (copy && (!X || !Xs))))) return GEMM_ERR_INVALID_ARG;
-    if (H > kMaxExtent / 4 || E > kDispatchMaxExperts || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent)
+    if (H > kMaxExtent / 4 || E > kDispatchMaxExperts || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kDispatchMaxSlots)
         return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);

@@ -400,8 +400,8 @@ GEMM11_API int gemm_moe_few_tokens(int T, int E, int top_k, int H, int I, const 
  *            X and Xs both NULL: the order alone.
  *   offsets  E + 1 int;  rows  T x top_k int.
  * Any alignment is accepted (16-byte aligned rows take wide copies).  T == 0
- * writes the offsets (zeros).  GEMM_ERR_UNSUPPORTED for E > 4096, top_k > 128 or
- * T * top_k above 2^31 - 512.
+ * writes the offsets (zeros).  GEMM_ERR_UNSUPPORTED for E > 4096, top_k > 128,
+ * H above 2^29 - 128 or T * top_k above 2^31 - 32768.
  */
 GEMM11_API int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids, const void *X, int x_type,
                                  long long ldx, void *Xs, long long ldxs, int *offsets, int *rows, void *stream);

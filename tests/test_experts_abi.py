@@ -82,6 +82,15 @@ def test_unsupported(L, name, change):
     assert call(L, name, **change) == g.GEMM_ERR_UNSUPPORTED
 
 
+# The kernels' 32-bit indices run over the last slot, of 2^31 - 32,768 at most, by less than 2^15.
+BEYOND = [("gemm_moe_dispatch", [dict(T=2 ** 31 - 32767, top_k=1), dict(T=2 ** 31 - 512, top_k=1, X=None, Xs=None), dict(T=2 ** 24 - 255, top_k=128, X=None, Xs=None)])]
+
+
+@pytest.mark.parametrize("name,change", [(n, c) for n, cs in BEYOND for c in cs])
+def test_indices_that_would_pass_32_bits(L, name, change):
+    assert call(L, name, **change) == g.GEMM_ERR_UNSUPPORTED
+
+
 WORD_CALLS = list(CALLS)  # in the order of gemm_word_call
 
 
