@@ -564,6 +564,9 @@ constexpr int kRowsMaxTopK = 128;
 // Slots of one dispatch: its CTAs' 32-bit indices run over the last one by up to
 // 12,287 (three times four slots for each of 1024 threads).
 constexpr int kDispatchMaxSlots = 0x7FFFFFFF - 32767;
+// Columns that the way back takes: its 32-bit index of a column goes on by up to
+// 4096 (128 threads with four times eight columns each) from the last one.
+constexpr int kCombineMaxColumns = 0x7FFFFFFF - 4095;
 
 // Row strides of the tensor-memory-access path end at 2^40 bytes.
 constexpr long long kMaxStride = 1LL << 38;
@@ -950,7 +953,7 @@ int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, l
     if (ldys < std::max(1, H) || ldy < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
     if (T == 0 || H == 0) return noop();
     if (!rows || !Y || (R > 0 && !Ys)) return GEMM_ERR_INVALID_ARG;
-    if (H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
+    if (H > kCombineMaxColumns || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
     if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);
@@ -980,7 +983,7 @@ int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void *dY, int ty
     if (lddy < std::max(1, H) || ldys < std::max(1, H) || lddys < std::max(1, H)) return GEMM_ERR_INVALID_ARG;
     if (T == 0) return noop();
     if (!rows || !weights || !dweights || (H > 0 && (!dY || (R > 0 && (!Ys || !dYs))))) return GEMM_ERR_INVALID_ARG;
-    if (H > kMaxExtent || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
+    if (H > kCombineMaxColumns || R > kMaxExtent || top_k > kRowsMaxTopK || static_cast<long long>(T) * top_k > kMaxExtent) return GEMM_ERR_UNSUPPORTED;
     DeviceState *ds = device_state();
     if (!ds) return fail_cuda(cudaErrorInvalidDevice);
     if (ds->init_error != cudaSuccess) return fail_cuda(ds->init_error);

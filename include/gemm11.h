@@ -415,7 +415,7 @@ GEMM11_API int gemm_moe_dispatch(int T, int E, int top_k, int H, const int *ids,
  *   weights  T x top_k float, or NULL: ones.  With ones it is also the gradient
  *            of gemm_moe_dispatch's copy.
  * Any alignment.  T == 0 or H == 0 is a no-op.  GEMM_ERR_UNSUPPORTED for top_k >
- * 128 or T * top_k above 2^31 - 512.
+ * 128, H above 2^31 - 4096, and R or T * top_k above 2^31 - 512.
  */
 GEMM11_API int gemm_moe_combine(int T, int top_k, int H, int R, const void *Ys, int type, long long ldys,
                                 const int *rows, const float *weights, void *Y, long long ldy, void *stream);

@@ -82,8 +82,13 @@ def test_unsupported(L, name, change):
     assert call(L, name, **change) == g.GEMM_ERR_UNSUPPORTED
 
 
-# The kernels' 32-bit indices run over the last slot, of 2^31 - 32,768 at most, by less than 2^15.
-BEYOND = [("gemm_moe_dispatch", [dict(T=2 ** 31 - 32767, top_k=1), dict(T=2 ** 31 - 512, top_k=1, X=None, Xs=None), dict(T=2 ** 24 - 255, top_k=128, X=None, Xs=None)])]
+# The kernels' 32-bit indices run over the last slot, of 2^31 - 32,768 at most, by less than 2^15, and over the last column, of
+# 2^31 - 4096 at most, by 4096.
+BEYOND = [
+    ("gemm_moe_dispatch", [dict(T=2 ** 31 - 32767, top_k=1), dict(T=2 ** 31 - 512, top_k=1, X=None, Xs=None), dict(T=2 ** 24 - 255, top_k=128, X=None, Xs=None)]),
+    ("gemm_moe_combine", [dict(H=h, ldys=2 ** 31, ldy=2 ** 31) for h in (2 ** 31 - 4095, 2 ** 31 - 2048, 2 ** 31 - 512)]),
+    ("gemm_moe_combine_grad", [dict(H=h, lddy=2 ** 31, ldys=2 ** 31, lddys=2 ** 31) for h in (2 ** 31 - 4095, 2 ** 31 - 2048, 2 ** 31 - 512)]),
+]
 
 
 @pytest.mark.parametrize("name,change", [(n, c) for n, cs in BEYOND for c in cs])
