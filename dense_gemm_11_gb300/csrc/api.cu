@@ -16,6 +16,8 @@
 #include <utility>
 #include <vector>
 
+#include <cudaTypedefs.h>
+
 #include "../../include/gemm11.h"
 #include "experts.h"
 #include "fp8.h"
@@ -147,9 +149,25 @@ int current_device() {
     return d;
 }
 
+// Makes the current device's context current on this host thread, which has none
+// before its first runtime call that needs one: cudaGetDevice does not, and the
+// driver's tensor-map encoder fails without.  A context that the caller made current
+// stays.
+bool bind_context(int d) {
+    static thread_local bool bound = false;
+    if (bound) return true;
+    void *fn = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &fn, 4000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess) return false;
+    CUcontext c = nullptr;
+    if (reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(fn)(&c) != CUDA_SUCCESS) return false;
+    bound = c || cudaSetDevice(d) == cudaSuccess;
+    return bound;
+}
+
 DeviceState *device_state() {
     const int d = current_device();
-    if (d < 0 || d >= kMaxDevices) return nullptr;
+    if (d < 0 || d >= kMaxDevices || !bind_context(d)) return nullptr;
     DeviceState &s = g_dev[d];
     std::call_once(s.once, [&s, d] {
         cudaError_t e = cudaDeviceGetAttribute(&s.sm_count, cudaDevAttrMultiProcessorCount, d);
