@@ -94,6 +94,12 @@ struct ScratchBuffer {
 struct ScratchEntry {
     ScratchBuffer partials, counters, operands;
 };
+// Of one (device, stream), for good: its scratch outside captures, and the lock that
+// a call on the stream holds (ScratchHold), captured or not.  It is taken before
+// g_scratch_mu, never after.
+struct StreamScratch : ScratchEntry {
+    std::mutex in_use;
+};
 // The buffers of one stream capture.  The graph that it makes holds their
 // addresses, so they belong to that graph: no call outside the capture and no
 // other graph gets them, and they live until the graph and its instances are
@@ -106,8 +112,9 @@ struct CaptureScratch {
     std::atomic<bool> gone{false};
 };
 std::mutex g_scratch_mu;
-std::map<std::pair<int, uintptr_t>, ScratchEntry> g_scratch;
-// By capture id.  Never destroyed: a graph may outlive the library's statics.
+// Neither table is destroyed: a call may hold a lock of this one while the process ends ...
+std::map<std::pair<int, uintptr_t>, StreamScratch> &g_scratch = *new std::map<std::pair<int, uintptr_t>, StreamScratch>;
+// ... and a graph may outlive the library's statics.  By capture id.
 std::map<unsigned long long, std::unique_ptr<CaptureScratch>> &g_captures = *new std::map<unsigned long long, std::unique_ptr<CaptureScratch>>;
 std::atomic<int> g_captures_gone{0};
 
@@ -280,7 +287,7 @@ cudaError_t acquire_buffer(cudaStream_t stream, int dev, const Capture &c, Scrat
         if (e != cudaSuccess) return e;
     }
     const uintptr_t key = reinterpret_cast<uintptr_t>(stream);
-    ScratchEntry &entry = cs ? cs->streams[key] : g_scratch[{dev, key}];
+    ScratchEntry &entry = cs ? cs->streams[key] : static_cast<ScratchEntry &>(g_scratch[{dev, key}]);
     ScratchBuffer &b = kind == ScratchKind::partials ? entry.partials : kind == ScratchKind::counters ? entry.counters : entry.operands;
     const bool zero = kind == ScratchKind::counters;
     if (b.bytes < bytes && cs) {
@@ -322,11 +329,22 @@ cudaError_t acquire_buffer(cudaStream_t stream, int dev, const Capture &c, Scrat
     return cudaSuccess;
 }
 
+// The lock of the call's stream, for the rest of the call.
+void hold_scratch(cudaStream_t stream, int dev, CallInfo *info) {
+    std::mutex *in_use;
+    {
+        std::lock_guard<std::mutex> lock(g_scratch_mu);
+        in_use = &g_scratch[{dev, reinterpret_cast<uintptr_t>(stream)}].in_use;  // stays where it is
+    }
+    info->scratch.take(*in_use);
+}
+
 }  // namespace
 
-cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out) try {
+cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, CallInfo *info, Scratch *out) try {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
+    hold_scratch(stream, dev, info);
     const Capture c = capture_of(stream);
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     collect_gone();
@@ -343,9 +361,10 @@ cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t n
     return cudaErrorMemoryAllocation;  // of the tables
 }
 
-cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, float **out) try {
+cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, CallInfo *info, float **out) try {
     const int dev = current_device();
     if (dev < 0) return cudaErrorInvalidDevice;
+    hold_scratch(stream, dev, info);
     const Capture c = capture_of(stream);
     std::lock_guard<std::mutex> lock(g_scratch_mu);
     collect_gone();

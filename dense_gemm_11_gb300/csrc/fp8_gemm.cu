@@ -1124,7 +1124,7 @@ cudaError_t launch_fp8_pair(const Fp8Gemm &g, const Fp8Args &a, const PairPlan &
     if (PARTS) {
         const int rows = plan.left * args.parts * 256;
         Scratch sc;
-        e = acquire_scratch(stream, static_cast<size_t>(rows) * kPairN, 0, &sc);
+        e = acquire_scratch(stream, static_cast<size_t>(rows) * kPairN, 0, info, &sc);
         if (e != cudaSuccess) return e;
         args.partials = sc.partials;
         args.partial_floats = static_cast<size_t>(rows) * kPairN;

@@ -786,7 +786,7 @@ cudaError_t launch_grouped(const Grouped &g, GroupedArgs a, cudaStream_t stream,
     if (SPLIT) {
         Scratch sc;
         a.part_stride = g.wgrad ? static_cast<size_t>(g.E) * g.M * g.N : static_cast<size_t>(g.R) * g.N;
-        e = acquire_scratch(stream, a.part_stride * a.split, 0, &sc);
+        e = acquire_scratch(stream, a.part_stride * a.split, 0, info, &sc);
         if (e != cudaSuccess) return e;
         a.partials = sc.partials;
     }

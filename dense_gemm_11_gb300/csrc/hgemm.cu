@@ -1850,7 +1850,7 @@ cudaError_t run_gemm_f16(const TcGemm &g, cudaStream_t stream, CallInfo *info) {
     if (splits > 1) {
         Scratch sc;
         cudaError_t e =
-            acquire_scratch(stream, static_cast<size_t>(tiles) * splits * kBM * bn, static_cast<size_t>(tiles) * 4, &sc);
+            acquire_scratch(stream, static_cast<size_t>(tiles) * splits * kBM * bn, static_cast<size_t>(tiles) * 4, info, &sc);
         if (e != cudaSuccess) return e;
         a.ws = sc.partials;
         a.counters = sc.counters;
@@ -1961,7 +1961,7 @@ cudaError_t run_gemm_f32_3xtf32(int M, int N, int K, float alpha, const float *A
     const int Kp = (K + 3) & ~3;
     const size_t a_elems = static_cast<size_t>(M) * Kp, b_elems = static_cast<size_t>(N) * Kp;
     float *ws = nullptr;
-    cudaError_t e = acquire_operand_scratch(stream, 2 * a_elems + 2 * b_elems, &ws);
+    cudaError_t e = acquire_operand_scratch(stream, 2 * a_elems + 2 * b_elems, info, &ws);
     if (e != cudaSuccess) return e;
     float *a_hi = ws, *a_lo = ws + a_elems, *bt_hi = a_lo + a_elems, *bt_lo = bt_hi + b_elems;
     e = launch_kernel(split_rows_tf32_kernel, dim3(std::min(M, 8 * sms)), dim3(256), 0, stream, A, lda, M, K, Kp, a_hi,

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 
 namespace gemm11 {
 
@@ -16,13 +17,38 @@ struct Scratch {
     float *partials = nullptr;
     unsigned *counters = nullptr;
 };
+
+// What one call holds of its stream's scratch, from the first acquire_...scratch
+// to its end, with all of its launches enqueued.  Another host thread's call on
+// the stream waits for that: it would otherwise put its own launches between
+// these, over the sums that the first leaves for the second, or free the buffer
+// for a larger one before the launch that uses it is on the stream.
+class ScratchHold {
+  public:
+    void take(std::mutex &m) {
+        if (!lock_.owns_lock()) lock_ = std::unique_lock<std::mutex>(m);
+    }
+
+  private:
+    std::unique_lock<std::mutex> lock_;
+};
+
+// One call: what it reports, and what it holds until it returns.
+struct CallInfo {
+    const char *plan = "none";
+    int launches = 0;
+    bool tuned = false;  // the plan came from the tuning table
+    ScratchHold scratch;
+};
+
 // Returns cudaSuccess and fills `out` with at least `partial_floats` floats and
-// `ncounters` zeroed counters usable on `stream` (current device).
-cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, Scratch *out);
+// `ncounters` zeroed counters usable on `stream` (current device) until the end
+// of the call `info`.
+cudaError_t acquire_scratch(cudaStream_t stream, size_t partial_floats, size_t ncounters, CallInfo *info, Scratch *out);
 
 // A second buffer of the same kind for repacked operands (used together with
 // the partials above).
-cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, float **out);
+cudaError_t acquire_operand_scratch(cudaStream_t stream, size_t floats, CallInfo *info, float **out);
 
 // Device address of the current device's watchdog word.
 unsigned *watchdog_word();
@@ -75,12 +101,6 @@ cudaError_t ensure_dynamic_smem(Kernel kern, int bytes, unsigned long long &done
     if (e == cudaSuccess && bit) __atomic_fetch_or(&done_mask, bit, __ATOMIC_RELEASE);
     return e;
 }
-
-struct CallInfo {
-    const char *plan = "none";
-    int launches = 0;
-    bool tuned = false;  // the plan came from the tuning table
-};
 
 // ---- FP32 path (sgemm.cu) ----
 cudaError_t run_gemm_f32(int M, int N, int K, float alpha, const float *A, int lda, const float *B, int ldb,

@@ -1205,7 +1205,7 @@ cudaError_t run_moe(const Moe &m, cudaStream_t stream, CallInfo *info) {
     const size_t n_h16 = up64(n_slots * parts_bytes(m.I, 3) / 4), n_x16 = up64(static_cast<size_t>(m.T) * m.H / 2), n_max = up64(n_slots);
     Scratch s;
     const cudaError_t e =
-        acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + 3 * n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, &s);
+        acquire_scratch(stream, n_logits + n_hidden + n_h16 + n_x16 + 3 * n_max + up64(m.T) + n_slots * m.H * kMaxSplits, 5, info, &s);
     if (e != cudaSuccess) return e;
     a.logits = s.partials;
     a.hidden = a.logits + n_logits;

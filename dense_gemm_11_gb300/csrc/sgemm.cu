@@ -1058,7 +1058,7 @@ cudaError_t run_gemm_f32(int M, int N, int K, float alpha, const float *A, int l
         }
         Scratch sc;
         if (splits > 1) {
-            cudaError_t e = acquire_scratch(stream, static_cast<size_t>(col_blocks) * splits * 128, col_blocks, &sc);
+            cudaError_t e = acquire_scratch(stream, static_cast<size_t>(col_blocks) * splits * 128, col_blocks, info, &sc);
             if (e != cudaSuccess) return e;
         }
         info->plan = splits > 1 ? "sgemv_cols_splitk" : "sgemv_cols";
@@ -1097,7 +1097,7 @@ cudaError_t run_gemm_f32(int M, int N, int K, float alpha, const float *A, int l
         const size_t a_floats = a_ok ? 0 : ((static_cast<size_t>(M) * lda2 + 63) & ~size_t(63));
         const size_t b_floats = b_ok ? 0 : static_cast<size_t>(K) * ldb2;
         float *ops = nullptr;
-        cudaError_t e = acquire_operand_scratch(stream, a_floats + b_floats + 64, &ops);
+        cudaError_t e = acquire_operand_scratch(stream, a_floats + b_floats + 64, info, &ops);
         if (e != cudaSuccess) return e;
         const int blocks = 8 * sms;
         if (!a_ok) {
@@ -1184,7 +1184,7 @@ cudaError_t run_gemm_f32(int M, int N, int K, float alpha, const float *A, int l
         const size_t strip_floats = (strip > 1 && s2.splits > 1) ? static_cast<size_t>(s2.tiles_m) * s2.splits * 64 * 64 : 0;
         if (main_floats + strip_floats > 0) {
             Scratch sc;
-            e = acquire_scratch(stream, main_floats + strip_floats, strip_floats > 0 ? s2.tiles_m : 0, &sc);
+            e = acquire_scratch(stream, main_floats + strip_floats, strip_floats > 0 ? s2.tiles_m : 0, info, &sc);
             if (e != cudaSuccess) return e;
             a.ws = sc.partials;
             a.counters = sc.counters;
@@ -1255,7 +1255,7 @@ cudaError_t run_gemm_f32(int M, int N, int K, float alpha, const float *A, int l
         a.splits = splits;
         if (splits > 1) {
             Scratch sc;
-            e = acquire_scratch(stream, static_cast<size_t>(tiles) * splits * 64 * 64, tiles, &sc);
+            e = acquire_scratch(stream, static_cast<size_t>(tiles) * splits * 64 * 64, tiles, info, &sc);
             if (e != cudaSuccess) return e;
             a.ws = sc.partials;
             a.counters = sc.counters;

@@ -34,7 +34,9 @@
  *     word and returns early; gemm_check() reports it as GEMM_ERR_TIMEOUT.
  *   - Split-K shapes use a library-owned workspace, allocated lazily once per
  *     (device, stream) and reused; calls on one stream are serialised by the
- *     stream, calls on different streams use different workspaces.  While a
+ *     stream (a call that uses the workspace enqueues all of its launches before
+ *     another host thread's enqueues any), calls on different streams use
+ *     different workspaces.  While a
  *     stream is being captured the call allocates a workspace that belongs to
  *     the graph and is freed by a later call once the graph and its instances
  *     are destroyed.  So replays of different graphs may overlap, with each
