@@ -312,3 +312,21 @@ def test_weights_into_16_bits_streams_and_graphs():
     g.gemm_grouped_wgrad(X, Y, outs[1], off, 0.0)
     g.gemm_grouped_wgrad(X[:0], Y[:0], outs[2], torch.zeros_like(off))
     assert all((C == 0).all() for C in outs[:3])
+
+
+@pytest.mark.parametrize("b_trans", [True, False])
+def test_as_many_experts_as_there_may_be(b_trans):
+    """All without rows but the last, whose rows are found within the limit of a wait."""
+    E = 2 ** 24
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = 3
+    A, B, C = padded(5, 8, dtype=BF16), torch.zeros(E, 1, 8, dtype=BF16, device="cuda"), torch.full((5, 1), -7.0, device="cuda")
+    B[E - 1] = torch.randn(1, 8)
+    W = B if b_trans else torch.zeros(E, 8, 8, dtype=BF16, device="cuda")[:, :, :1]
+    if not b_trans:
+        W[E - 1, :, 0] = B[E - 1, 0]
+    g.gemm_grouped(A, W, C, off, b_trans=b_trans)
+    assert g.check() == g.GEMM_OK
+    want, mag = grouped(A[:3], B[E - 1:], torch.tensor([0, 3]), True)
+    close(C[:3], want, rounded(PRODUCT * mag, want, F32))
+    assert (C[3:] == -7.0).all()
