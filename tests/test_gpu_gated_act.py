@@ -111,3 +111,16 @@ def test_what_the_copies_lose():
     a, s, _, _ = act(G.double(), 4)
     for got, want in ((dG, dH.double() * U.double() * s), (dU, dH.double() * a)):
         assert float((got.double() - want).norm() / want.norm()) <= 1 / 16 + 1 / 16
+
+
+# 2432 blocks of 16 rows x 128 columns and more: a CTA takes four column blocks of its rows, two at a time (FP32 forwards: two in all), and
+# the last CTA of a row one, two or three; ragged last rows and columns.
+MANY = [(2500, 2100, BF16, 0, 0), (4001, 1290, F16, 0, 0), (2500, 2100, F32, 0, 0), (3100, 1800, BF16, 3, 1), (40000, 129, F16, 0, 0)]
+
+
+@pytest.mark.parametrize("code", [1, 2, 4])
+@pytest.mark.parametrize("gated", [True, False])
+@pytest.mark.parametrize("rows,cols,t,pad,shift", MANY)
+def test_many_blocks(rows, cols, t, pad, shift, gated, code):
+    assert -(-rows // 16) * -(-cols // 128) >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
+    test_forward_and_backward(rows, cols, t, pad, shift, gated, code)
