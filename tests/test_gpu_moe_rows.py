@@ -197,3 +197,43 @@ def test_tokens_without_a_row():
 def test_unit_roundoffs():
     for t, u in UNIT.items():
         assert u == torch.finfo(t).eps / 2
+
+
+@pytest.mark.parametrize("T,k,E,H,dtype,pad", [(900, 3, 13, 2056, BF16, 0), (1300, 2, 7, 3001, F16, 5), (1250, 2, 9, 4104, F32, 0), (40, 2, 8, 9000, F32, 0), (6, 5, 8, 8200, BF16, 0)])
+def test_combine_grad_in_several_steps(T, k, E, H, dtype, pad):
+    """Slots with more columns than their threads take at once: 32 threads where there are 16 slots an SM and more, else 128."""
+    lanes = 1
+    while lanes < 128 and lanes * 32 < H:
+        lanes *= 2
+    if T * k >= 16 * torch.cuda.get_device_properties(0).multi_processor_count:
+        lanes = min(lanes, 32)
+    assert H > 32 * lanes
+    torch.manual_seed(H)
+    _, rows = sort(choice(T, k, E, seed=T, drop=0.2).cpu(), E)
+    R = T * k
+    dY, Ys, dYs = strided(T, H, dtype, pad), strided(R, H, dtype, pad), strided(R, H, dtype, pad, fill=-7.0)
+    dY.copy_(torch.randn(T, H, device="cuda"))
+    Ys.copy_(torch.randn(R, H, device="cuda"))
+    w, dw = torch.rand(T, k, device="cuda"), torch.full((T, k), -7.0, device="cuda")
+    g.moe_combine_grad(dY, Ys, rows.int().cuda(), w, dYs, dw)
+    assert g.check() == g.GEMM_OK
+    on = rows >= 0
+    t = torch.arange(T)[:, None].expand(T, k)[on]
+    dy, ys, wt = dY.double().cpu()[t], Ys.double().cpu()[rows[on]], w.double().cpu()[on]
+    want = torch.full((R, H), -7.0, dtype=torch.float64)
+    want[rows[on]] = dy * wt[:, None]
+    bound = rounded(2.0 ** -24 * want.abs(), want, dtype)
+    bound[(want == -7.0).all(1)] = 0
+    close(dYs.cpu(), want, bound, "dYs")
+    want_w, mag = torch.zeros(T, k, dtype=torch.float64), torch.zeros(T, k, dtype=torch.float64)
+    want_w[on], mag[on] = (dy * ys).sum(1), (dy * ys).abs().sum(1)
+    # roundings that one product passes through: a thread's fused additions, eight for each 8 x lanes columns, five of the
+    # shuffles and four of the warps'; (1 + 2^-24)^n - 1 is below 1.001 n 2^-24 for these n
+    n = 8 * -(-H // (8 * lanes)) + 5 + 4
+    close(dw.cpu(), want_w, 1.001 * n * 2.0 ** -24 * mag, "dweights")
+
+
+@pytest.mark.parametrize("T,k,E,H,dtype,pad", [(3000, 2, 4096, 2048, BF16, 0), (700, 3, 4000, 16384, BF16, 8)])
+def test_dispatch_long_rows_many_experts(T, k, E, H, dtype, pad):
+    """The experts' counters take 32 KB of the shared memory that the rows go through."""
+    test_dispatch_long_rows(T, k, E, H, dtype, pad)
