@@ -124,3 +124,55 @@ MANY = [(2500, 2100, BF16, 0, 0), (4001, 1290, F16, 0, 0), (2500, 2100, F32, 0, 
 def test_many_blocks(rows, cols, t, pad, shift, gated, code):
     assert -(-rows // 16) * -(-cols // 128) >= 16 * torch.cuda.get_device_properties(0).multi_processor_count
     test_forward_and_backward(rows, cols, t, pad, shift, gated, code)
+
+
+# largest value, half a step relative to a value, half of the smallest step
+FORMATS = {E4: (448.0, 2.0 ** -4, 2.0 ** -10), E5: (57344.0, 2.0 ** -3, 2.0 ** -17)}
+
+
+@pytest.mark.parametrize("q", [E4, E5])
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+def test_what_the_copies_lose_beside_a_large_value(t, q):
+    """A copy is off by half a step of its type at most: relative to the value, or, below the type's normal numbers, to its block's scale.
+
+    Beside a value of 2^12 those below 2^-14.8 of it (e4m3) are that small, and those below half of a step are zeros.
+    """
+    torch.manual_seed(4)
+    G, U = torch.randn(20, 700, device="cuda").to(t), (torch.randn(20, 700, device="cuda") * 0.1).to(t)
+    G[:, ::128], U[::2, 5] = 2.0 ** 12, -(2.0 ** 12)
+    G[:, 1::7] *= 2.0 ** -10
+    (GQ, GS), (UQ, US) = pair(20, 700, q, 0), pair(20, 700, q, 0)
+    H = torch.empty_like(G)
+    g.fp8_gated_act(G, U, H, GQ, GS, UQ, US)
+    assert g.check() == g.GEMM_OK
+    top, relative, smallest = FORMATS[q]
+    for X, Q, S in ((G, GQ, GS), (U, UQ, US)):
+        x = X.double()
+        padded = torch.nn.functional.pad(x.abs(), (0, 768 - 700)).reshape(20, 6, 128)
+        scale = (padded.amax(2) / top).repeat_interleave(128, 1)[:, :700]
+        # the scale, its reciprocal and the product with it are FP32: 2^-24 each, which may move a value over the middle of a step
+        bound = torch.maximum(relative * x.abs(), smallest * scale) * (1 + 2.0 ** -3 * 2.0 ** -18) + 4 * 2.0 ** -24 * x.abs()
+        close(kept(Q, S), x, bound)
+        small = x.abs() < 0.99 * smallest * scale
+        assert (kept(Q, S)[small] == 0).all()
+    if q == E4:
+        assert bool((kept(GQ, GS) == 0).any()) and bool(((kept(GQ, GS) - G.double()).abs() > 0.0625 * G.double().abs()).any())  # more than 2^-4 of a value
+
+
+@pytest.mark.parametrize("t", [F32, F16, BF16])
+def test_an_infinity_takes_its_block(t):
+    """h has it where it belongs; the copies' scale is infinite, and the gradients are NaN in the 128 columns of that block of the row."""
+    torch.manual_seed(5)
+    G, U, dH = (torch.randn(5, 400, device="cuda").to(t) for _ in range(3))
+    G[2, 200] = float("inf")
+    clean = torch.ones(5, 400, dtype=torch.bool, device="cuda")
+    clean[2, 128:256] = False
+    (GQ, GS), (UQ, US) = pair(5, 400, E4, 0), pair(5, 400, E4, 0)
+    H, dG, dU, back = (torch.empty_like(G) for _ in range(4))
+    g.fp8_gated_act(G, U, H, GQ, GS, UQ, US)
+    g.fp8_gated_act_grad(dH, GQ, GS, UQ, US, dG, dU, back)
+    assert g.check() == g.GEMM_OK
+    assert H[2, 200].abs() == float("inf") and int(torch.isfinite(H.float()).sum()) == 5 * 400 - 1
+    assert GS[1, 2] == float("inf") and int(torch.isfinite(GS).sum()) == GS.numel() - 1
+    for out in (dG, dU, back):
+        assert torch.isfinite(out[clean].float()).all() and out[~clean].isnan().all()
