@@ -538,7 +538,7 @@ cudaError_t run_moe_dispatch(const MoeDispatch &d, cudaStream_t stream, CallInfo
     const bool vec = rows_aligned(d.X, d.ldx, b, d.T) && rows_aligned(d.Xs, d.ldxs, b, a.n);
     const int grid = std::max(1, std::min(d.T, device_sm_count()));
     a.per_cta = std::max(1, (d.T + grid - 1) / grid);
-    const unsigned ctas = static_cast<unsigned>(std::max(1, (d.T + a.per_cta - 1) / a.per_cta));
+    const unsigned ctas = static_cast<unsigned>(std::max(1LL, (static_cast<long long>(d.T) + a.per_cta - 1) / a.per_cta));
     a.copies = a.n >= 4096 ? 8 : 1;
     while (a.copies > 1 && 2u * sizeof(int) * d.E * a.copies > 32768u) a.copies /= 2;
     const size_t smem = 2u * sizeof(int) * d.E * a.copies;

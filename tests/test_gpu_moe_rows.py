@@ -237,3 +237,23 @@ def test_combine_grad_in_several_steps(T, k, E, H, dtype, pad):
 def test_dispatch_long_rows_many_experts(T, k, E, H, dtype, pad):
     """The experts' counters take 32 KB of the shared memory that the rows go through."""
     test_dispatch_long_rows(T, k, E, H, dtype, pad)
+
+
+def test_as_many_slots_as_there_may_be():
+    """2^31 - 32,768 slots, one a token: every one gets its row (the order alone; 17 GB)."""
+    n, E, part = 2 ** 31 - 32768, 8, 1 << 27
+
+    def pieces():
+        for i in range(0, n, part):
+            j = torch.arange(i, min(i + part, n), device="cuda")
+            yield i, j, j * 5 % E  # of eight neighbouring slots one for each expert
+
+    ids, rows = torch.empty(n, 1, dtype=torch.int32, device="cuda"), torch.full((n, 1), -9, dtype=torch.int32, device="cuda")
+    for i, j, e in pieces():
+        ids[i:i + len(j), 0] = e.int()
+    offsets = torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    g.moe_dispatch(ids, None, None, offsets, rows)
+    assert g.check() == g.GEMM_OK
+    assert offsets.tolist() == [e * (n // E) for e in range(E + 1)]
+    for i, j, e in pieces():
+        assert torch.equal(rows[i:i + len(j), 0].long(), e * (n // E) + j // E)
