@@ -608,11 +608,6 @@ constexpr int kCombineMaxColumns = 0x7FFFFFFF - 4095;
 // Row strides of the tensor-memory-access path end at 2^40 bytes.
 constexpr long long kMaxStride = 1LL << 38;
 
-// Experts of the products of rows: one warp of each CTA walks their offsets, 32 at a
-// time, while the others wait for the next tile, for two seconds at most
-// (kWaitLimitNs).  2^24 experts of which the last alone has rows take 0.2 s.
-constexpr int kGroupedMaxExperts = 1 << 24;
-
 // Products over sorted rows: no extent, and no number of tiles, beyond 32 bits
 // (a and b are those of a result; every expert may have a tile that is not full).
 bool grouped_fits(int E, int a, int b, int k) {
@@ -1062,7 +1057,7 @@ int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, const void *A, 
     if (E == 0 || R == 0 || N == 0) return noop();
     const bool product = K > 0 && alpha != 0.f;
     if (!C || !offsets || (product && (!A || !B))) return GEMM_ERR_INVALID_ARG;
-    if (E > kGroupedMaxExperts || !grouped_fits(E, R, N, K)) return GEMM_ERR_UNSUPPORTED;
+    if (!grouped_fits(E, R, N, K)) return GEMM_ERR_UNSUPPORTED;
     auto al16 = [](const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; };
     if (product && !(al16(A) && al16(B) && (R == 1 || lda % 8 == 0) && (b_rows == 1 || ldb % 8 == 0) && (E == 1 || stride_b % 8 == 0) &&
                      lda < kMaxStride && ldb < kMaxStride && (E == 1 || stride_b < kMaxStride)))

@@ -824,7 +824,11 @@ cudaError_t run_grouped(const Grouped &g, cudaStream_t stream, CallInfo *info) {
     a.c_type = g.c_type;
     a.product = g.alpha != 0.f && (g.wgrad ? g.R > 0 : g.K > 0);
     a.err = watchdog_word();
-    a.wait_ns = kWaitLimitNs;
+    // A warp may have to wait while another walks the offsets of experts without rows
+    // (32 in 0.6 us: 2^28 experts of which the last alone has rows take 4 to 5 s), and for
+    // all of a tile's contraction (a block in 0.2 to 0.8 us: 3.0 s for a pair alone with
+    // 3 * 2^28 rows of an expert), which the host knows no better than as R.
+    a.wait_ns = kWaitLimitNs + 2000ull * static_cast<unsigned long long>(g.E / 32) + 4000ull * static_cast<unsigned long long>((g.wgrad ? g.R : g.K) / kKB);
     if (kDebugBuild) {
         a.c_extent = g.wgrad ? static_cast<size_t>((g.E - 1LL) * g.stride_c + (g.M - 1LL) * g.ldc + g.N) : static_cast<size_t>((g.R - 1LL) * g.ldc + g.N);
         a.c_extent -= std::min(a.c_extent - 1, debug_shrink_c());

@@ -451,8 +451,7 @@ GEMM11_API int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void 
  * gemm_tc_f32acc_epilogue.  A and B 16-byte aligned, lda, ldb and stride_b
  * multiples of 8 (those of a single row, or expert, excepted), otherwise
  * GEMM_ERR_UNSUPPORTED; C any alignment and any ldc >= N.  GEMM_ERR_UNSUPPORTED
- * too for extents above 2^31 - 512, for E above 2^24 and for E (R / 256 + 1)
- * (N / 256 + 1) from 2^31.
+ * too for extents above 2^31 - 512 and for E (R / 256 + 1) (N / 256 + 1) from 2^31.
  * Scratch: where few tiles leave SMs without work, tiles share their contraction
  * and up to 64 MB hold their parts' sums (plan "grouped_pair_splitk").
  */
@@ -465,8 +464,8 @@ GEMM11_API int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, cons
  *   C[e] = round_c( alpha sum_r A[r]^T B[r] + beta C[e] ) over offsets[e] <= r < offsets[e + 1],
  * A R x M and B R x N of ab_type, C E matrices M x N stride_c elements apart
  * (FP32, FP16 or BF16).  An expert without rows gets beta C[e].  offsets, the
- * accumulation, the alignment, the limits (M for R, and E up to 2^31 - 512) and the
- * scratch are those of gemm_grouped_f32acc.
+ * accumulation, the alignment, the limits (M for R) and the scratch are those of
+ * gemm_grouped_f32acc.
  */
 GEMM11_API int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha, const void *A, long long lda,
                                          const void *B, long long ldb, int ab_type, float beta, void *C, int c_type,

@@ -91,12 +91,6 @@ BEYOND = [
 ]
 
 
-def test_more_experts_than_a_walk_of_their_offsets_ends_in_time(L):
-    one = dict(R=1, N=1, K=8, lda=8, ldb=8, ldc=1, stride_b=64)
-    for E in (2 ** 24 + 1, 2 ** 27, 2 ** 30):
-        assert call(L, "gemm_grouped_f32acc", E=E, **one) == call(L, "gemm_grouped_f32acc", E=E, b_trans=0, **one) == g.GEMM_ERR_UNSUPPORTED
-
-
 @pytest.mark.parametrize("name,change", [(n, c) for n, cs in BEYOND for c in cs])
 def test_indices_that_would_pass_32_bits(L, name, change):
     assert call(L, name, **change) == g.GEMM_ERR_UNSUPPORTED

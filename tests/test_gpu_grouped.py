@@ -314,19 +314,30 @@ def test_weights_into_16_bits_streams_and_graphs():
     assert all((C == 0).all() for C in outs[:3])
 
 
-@pytest.mark.parametrize("b_trans", [True, False])
-def test_as_many_experts_as_there_may_be(b_trans):
-    """All without rows but the last, whose rows are found within the limit of a wait."""
-    E = 2 ** 24
+def test_many_experts_without_rows():
+    """The walk of their offsets to the last one, which has rows, outlasts the two seconds that a wait has otherwise."""
+    E = 2 ** 28
     off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
     off[E] = 3
     A, B, C = padded(5, 8, dtype=BF16), torch.zeros(E, 1, 8, dtype=BF16, device="cuda"), torch.full((5, 1), -7.0, device="cuda")
     B[E - 1] = torch.randn(1, 8)
-    W = B if b_trans else torch.zeros(E, 8, 8, dtype=BF16, device="cuda")[:, :, :1]
-    if not b_trans:
-        W[E - 1, :, 0] = B[E - 1, 0]
-    g.gemm_grouped(A, W, C, off, b_trans=b_trans)
+    g.gemm_grouped(A, B, C, off)
     assert g.check() == g.GEMM_OK
     want, mag = grouped(A[:3], B[E - 1:], torch.tensor([0, 3]), True)
     close(C[:3], want, rounded(PRODUCT * mag, want, F32))
     assert (C[3:] == -7.0).all()
+
+
+def test_all_rows_of_one_expert():
+    """A contraction of 3 * 2^28 rows, which one CTA pair walks alone: so does that."""
+    E, e, R = 5000, 3211, 3 * 2 ** 28
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[e + 1:] = R
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    A, B = (torch.randint(-1, 2, (R, 8), generator=gen, device="cuda", dtype=torch.int8).to(BF16) for _ in range(2))
+    C = torch.full((E, 8, 8), -7.0, device="cuda")
+    g.gemm_grouped_wgrad(A, B, C, off)
+    assert g.check() == g.GEMM_OK and g.last_plan() == "grouped_wgrad_pair"
+    want = sum(a.double().t() @ b.double() for a, b in zip(A.split(2 ** 24), B.split(2 ** 24)))
+    assert float(want.abs().max()) < 2 ** 22  # of -1, 0 and 1: every partial sum is far from 2^24, so exact
+    assert torch.equal(C[e].double(), want) and int((C != 0).sum()) == int((want != 0).sum())
