@@ -141,7 +141,9 @@ struct TileList {
         // The rows in as few tiles as hold them, all alike (to 16 rows), so that
         // the last is not nearly empty.
         const int first = WGRAD ? 0 : s, rows = WGRAD ? p.m : e - s;
-        const int tiles_m = (rows + kTile - 1) / kTile, each = ((rows + tiles_m - 1) / tiles_m + 15) & ~15;
+        const int tiles_m = (rows + kTile - 1) / kTile;
+        const unsigned even = (static_cast<unsigned>(rows) + static_cast<unsigned>(tiles_m) - 1) / static_cast<unsigned>(tiles_m);  // the sum may pass 2^31
+        const int each = static_cast<int>(even + 15) & ~15;
         int i = t - base - before;
         tile.unit = 0;
         if (SPLIT) tile.unit = i % p.split, i /= p.split;

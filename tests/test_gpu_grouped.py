@@ -341,3 +341,33 @@ def test_all_rows_of_one_expert():
     want = sum(a.double().t() @ b.double() for a, b in zip(A.split(2 ** 24), B.split(2 ** 24)))
     assert float(want.abs().max()) < 2 ** 22  # of -1, 0 and 1: every partial sum is far from 2^24, so exact
     assert torch.equal(C[e].double(), want) and int((C != 0).sum()) == int((want != 0).sum())
+
+
+LARGEST = 2 ** 31 - 512
+
+
+def parts(n, size=2 ** 27):
+    return [slice(i, min(i + size, n)) for i in range(0, n, size)]
+
+
+def test_as_many_rows_as_there_may_be():
+    """2^31 - 512 rows of one expert (39 GB)."""
+    A, C = torch.empty(LARGEST, 8, dtype=BF16, device="cuda"), torch.full((LARGEST, 1), -7.0, dtype=BF16, device="cuda")
+    for s in parts(LARGEST):
+        A[s] = (torch.arange(s.start, s.stop, device="cuda") % 5 - 2).to(BF16)[:, None]
+    B = torch.tensor([1.0, 2, 3, -4, 5, 6, 7, 8], device="cuda").to(BF16).reshape(1, 1, 8)  # 28 together
+    g.gemm_grouped(A, B, C, torch.tensor([0, LARGEST], dtype=torch.int32, device="cuda"))
+    assert g.check() == g.GEMM_OK
+    for s in parts(LARGEST):
+        assert torch.equal(C[s, 0], A[s, 0] * 28)
+
+
+def test_as_many_columns_as_there_may_be():
+    """A matrix gradient of 2^31 - 512 rows (9 GB)."""
+    A, B, C = torch.empty(1, LARGEST, dtype=BF16, device="cuda"), torch.full((1, 1), 2.0, dtype=BF16, device="cuda"), torch.full((1, LARGEST, 1), -7.0, dtype=BF16, device="cuda")
+    for s in parts(LARGEST):
+        A[0, s] = (torch.arange(s.start, s.stop, device="cuda") % 5 - 2).to(BF16)
+    g.gemm_grouped_wgrad(A, B, C, torch.tensor([0, 1], dtype=torch.int32, device="cuda"))
+    assert g.check() == g.GEMM_OK
+    for s in parts(LARGEST):
+        assert torch.equal(C[0, s, 0], A[0, s] * 2)
