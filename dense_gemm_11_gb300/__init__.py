@@ -736,7 +736,7 @@ def moe_dispatch(ids, X, Xs, offsets, rows, *, stream=None) -> None:
     receives the row of every slot (-1: none); slots of one expert keep their order.
     X: (T, H) fp32, fp16 or bf16; Xs: the same type and width, at least T * top_k rows, receives Xs[rows[t, j]] = X[t]
     (rows from offsets[E] on stay as they are).  X=None and Xs=None: the order alone.
-    Limits: E <= 4096, top_k <= 128.
+    Limits: E <= 4096, top_k <= 128, T * top_k <= 2^31 - 32768.
     """
     ids_ptr, T, k, here = _slots(ids, "ids")
     off_ptr, E, off_on = _offsets(offsets)
@@ -879,6 +879,7 @@ def fp8_gated_act(G, U, H, GQ, GS, UQ=None, US=None, act: int = GEMM_ACT_SILU, *
 
     G, U, H: (rows, cols), one type, fp32, fp16 or bf16.  GQ, GS and UQ, US receive what fp8_quantize makes of G and U
     with layout "rows" (fp8_empty() makes fitting pairs).  U=None (and UQ=US=None): H = act(G).  act: any GEMM_ACT_*.
+    An infinity makes the scale of its block of 128 infinite; what the backward pass computes from that block is NaN.
     """
     g_ptr, ldg, rows, cols, code, here = _placed(G, "G", _FLOATS)
     h_ptr, ldh, h_on = _same(H, "H", rows, cols, code)

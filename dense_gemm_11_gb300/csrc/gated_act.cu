@@ -10,7 +10,9 @@
 //
 // Kept in 16 bits, g, u and h of a row of I columns are 6 I bytes; the 8-bit
 // copies are 2.06 I.  The derivative is that of act at g', which the backward
-// pass knows exactly: the copies' rounding is the only thing that is lost.
+// pass knows exactly: the copies' rounding is the only thing that is lost.  As in the
+// quantizer, a NaN leaves the rest of its block alone and an infinity makes its
+// block's scale infinite: what the backward pass computes from those 128 columns is NaN.
 //
 // Bound: memory.  One pass: 16 lanes hold 128 columns of a row, eight each, so
 // that the maximum is four shuffles; everything is computed in FP32 and rounded

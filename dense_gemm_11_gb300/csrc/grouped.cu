@@ -37,10 +37,10 @@ constexpr int kTile = 256;
 constexpr int kEpi = 8;                   // epilogue warps
 constexpr int kCols = kTile * 4 / kEpi;   // accumulator columns of one
 // The tensor core's sums truncate; so many blocks (512 of the contraction) are
-// summed there, and these sums are added to nearest in FP32 registers.  That takes
-// 8192 rows over 8 experts of 11008 x 4096 from 482 us, with all of a contraction
-// summed there, to 491, and the error of an FP32 result over 11008 from 1.2e-5 of its
-// norm to 4.8e-7 (4 blocks: 515 us, 2.6e-7).
+// summed there, and these sums are added to nearest in FP32 registers.  In a row of
+// calls that takes 8192 rows over 8 experts of 11008 x 4096 from 444 us, with all of a
+// contraction summed there, to 448 (weights of some 2^-6), and the error of an FP32
+// result over 11008 from 1.2e-5 of its norm to 4.8e-7 (4 blocks: 478 us, 2.5e-7).
 constexpr int kChunk = 8;
 // Registers: 384 threads of 168 at launch, 64,512; 128 x 56 + 256 x 224 = 64,512.
 constexpr int kRegsFew = 56, kRegsMany = 224;
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
         if (warp == 0) {
             // ------------------------------------------------ TMA producer (both CTAs)
-                int stage = 0;
+            int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             const uint32_t full_even = mapa_shared(smem_u32(full), 0), at_b = smem_u32(sB), at_a = smem_u32(sA);
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         } else if (MODE == kWgrad && warp == 2) {
             // ------------------------------------------------ ends of contractions (both CTAs)
-                int stage = 0;
+            int stage = 0;
             bool ok = true;
             while (ok && !*abort_flag && next()) {
                 const int blocks = tile_blocks(tile), valid = tile.k1 - tile.k0 - (blocks - 1) * kKB;
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t b_desc0 = umma_desc_sw128(smem_u32(sB), MODE != kForward ? kBox : 16, 1024);
             const uint64_t a_desc0 = umma_desc_sw128(smem_u32(sA), MODE == kWgrad ? kBox : 16, 1024);
             constexpr uint32_t kBstep = MODE != kForward ? 2048 >> 4 : 32 >> 4, kAstep = MODE == kWgrad ? 2048 >> 4 : 32 >> 4;
-                int stage = 0, i = 0;  // i: chunk
+            int stage = 0, i = 0;  // i: chunk
             uint32_t phase = 0;
             bool ok = true;
             while (ok && !*abort_flag && next()) {

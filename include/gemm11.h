@@ -36,7 +36,9 @@
  *     (device, stream) and reused; calls on one stream are serialised by the
  *     stream (a call that uses the workspace enqueues all of its launches before
  *     another host thread's enqueues any), calls on different streams use
- *     different workspaces.  While a
+ *     different workspaces.  cudaStreamPerThread counts as one stream here,
+ *     although each host thread has its own: calls on it that use the workspace
+ *     must come from one thread, or be ordered by the caller.  While a
  *     stream is being captured the call allocates a workspace that belongs to
  *     the graph and is freed by a later call once the graph and its instances
  *     are destroyed.  So replays of different graphs may overlap, with each
@@ -453,7 +455,8 @@ GEMM11_API int gemm_moe_combine_grad(int T, int top_k, int H, int R, const void 
  * GEMM_ERR_UNSUPPORTED; C any alignment and any ldc >= N.  GEMM_ERR_UNSUPPORTED
  * too for extents above 2^31 - 512 and for E (R / 256 + 1) (N / 256 + 1) from 2^31.
  * Scratch: where few tiles leave SMs without work, tiles share their contraction
- * and up to 64 MB hold their parts' sums (plan "grouped_pair_splitk").
+ * and up to 64 MB hold their parts' sums (plan "grouped_pair_splitk"); the workspace
+ * that grows for them is allocated with a quarter more, up to 80 MB.
  */
 GEMM11_API int gemm_grouped_f32acc(int E, int R, int N, int K, float alpha, const void *A, long long lda, const void *B,
                                    long long ldb, long long stride_b, int ab_type, int b_trans, float beta, void *C,
@@ -479,6 +482,8 @@ GEMM11_API int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha
  *            may be NULL: h = act(g).
  *   GQ, UQ   rows x cols, e4m3 or e5m2 (q_type); GS, US ceil(cols / 128) x rows.
  *   act      any gemm_act.
+ * An infinity in G or U makes the scale of its block of 128 infinite (H has it where
+ * it belongs): what gemm_fp8_gated_act_grad computes from that block's copies is NaN.
  * Any alignment.  rows == 0 or cols == 0 is a no-op.
  */
 GEMM11_API int gemm_fp8_gated_act(int rows, int cols, const void *G, long long ldg, const void *U, long long ldu,
