@@ -484,7 +484,8 @@ GEMM11_API int gemm_grouped_wgrad_f32acc(int E, int R, int M, int N, float alpha
  *   act      any gemm_act.
  * An infinity in G or U makes the scale of its block of 128 infinite (H has it where
  * it belongs): what gemm_fp8_gated_act_grad computes from that block's copies is NaN.
- * Any alignment.  rows == 0 or cols == 0 is a no-op.
+ * Any alignment.  rows == 0 or cols == 0 is a no-op.  GEMM_ERR_UNSUPPORTED for rows,
+ * cols or ceil(rows / 16) ceil(cols / 128) above 2^31 - 512.
  */
 GEMM11_API int gemm_fp8_gated_act(int rows, int cols, const void *G, long long ldg, const void *U, long long ldu,
                                   int type, void *H, long long ldh, void *GQ, long long ldgq, float *GS,
@@ -497,7 +498,8 @@ GEMM11_API int gemm_fp8_gated_act(int rows, int cols, const void *G, long long l
  *   dG = round( dH u' act'(g') ),  dU = round( dH act(g') ) (with UQ),
  *   H  = round( act(g') u' ) where H is not NULL (the rows that the gradient of
  *   the next weights needs, so that h itself need not be kept).
- * dH, dG, dU and H of `type`.  The derivative of ReLU at 0 is 0.  Any alignment.
+ * dH, dG, dU and H of `type`.  The derivative of ReLU at 0 is 0.  Any alignment;
+ * limits as for gemm_fp8_gated_act.
  */
 GEMM11_API int gemm_fp8_gated_act_grad(int rows, int cols, const void *dH, long long lddh, int type, const void *GQ,
                                        long long ldgq, const float *GS, long long ldgs, const void *UQ,
